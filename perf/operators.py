@@ -226,8 +226,8 @@ def _attn(s):
     if own:
         import block_diffusion_speculative_ctx_gb300 as dfl
         out, lse = dfl.shared_prefix_attention(s["q"], s["k"], s["v"], s["prefix_pages"], s["prefix"], s["table"],
-                                               s["kv"], s["q_start"], causal=s["causal"], max_q=s["max_q"],
-                                               out=s["out"], lse=s["lse"])
+                                               s["kv"], s["q_start"], causal=s["causal"], out=s["out"],
+                                               lse=s["lse"])
         return [out, lse]
     q, start, kv = s["q"].float(), s["q_start"].long(), s["kv"].long()
     rows, h, hd = q.shape
