@@ -13,7 +13,9 @@ The functions carry the C names:
     dflash_draft_block_sampled, dflash_verify_sampled, dflash_train_forward,
     dflash_generate, dflash_inspect, dflash_destroy, dflash_last_error
 
-``Session`` wraps them for tests and the benchmark.
+``Session`` wraps them for tests and the benchmark.  ``kv_tables``,
+``shared_prefix_attention`` and ``process_logits`` (ops.py) are the stateless
+serving operators over torch tensors.
 """
 from __future__ import annotations
 
@@ -83,7 +85,9 @@ class dflash_profile_entry(ctypes.Structure):
 
 EXPORTS = ("dflash_init", "dflash_prefill", "dflash_set_block_size", "dflash_block_size", "dflash_draft_block", "dflash_verify", "dflash_draft_block_sampled",
            "dflash_verify_sampled", "dflash_set_sampling_filter", "dflash_train_forward", "dflash_generate",
-           "dflash_inspect", "dflash_set_profiling", "dflash_destroy", "dflash_last_error")
+           "dflash_inspect", "dflash_set_profiling", "dflash_destroy", "dflash_last_error",
+           "dflash_kv_tables", "dflash_shared_prefix_attention", "dflash_shared_prefix_workspace",
+           "dflash_process_logits")
 
 _lib = None
 
@@ -126,6 +130,11 @@ def load(build_if_missing: bool = False):
               "dflash_inspect", "dflash_set_profiling", "dflash_set_block_size"):
         getattr(lib, f).restype = ctypes.c_int
     lib.dflash_destroy.restype = None
+    for f in ("dflash_kv_tables", "dflash_shared_prefix_attention", "dflash_process_logits"):
+        getattr(lib, f).argtypes = [P, P]
+        getattr(lib, f).restype = ctypes.c_int
+    lib.dflash_shared_prefix_workspace.argtypes = [I32] * 6
+    lib.dflash_shared_prefix_workspace.restype = SZ
     _lib = lib
     return lib
 
@@ -205,3 +214,12 @@ def dflash_destroy(ctx):
 
 
 from .session import Session, config_from_workload  # noqa: E402,F401
+
+
+def __getattr__(name):
+    # the serving operators (ops.py) need torch, which this module itself does not import
+    if name in ("kv_tables", "shared_prefix_attention", "process_logits", "KVTables"):
+        from . import ops
+        globals()[name] = getattr(ops, name)
+        return globals()[name]
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

@@ -1,0 +1,210 @@
+// Page tables and slot maps of a batch from its request lengths
+// (dflash_kv_tables in include/dflash.h).
+//
+// Request s takes a_s = ceil((kv + new) / 64) - ceil(kv / 64) pages.  With A and
+// Q the exclusive prefix sums of a and of the new lengths, its j-th new page is
+// free_pages[used + A_s + j] and its rows start at Q_s.  Bytes: the table read and
+// written, 16 B a row; at the largest session (1024 requests) that is 1.6 MB, far
+// below a launch's latency, so the kernel is bound by its chain of dependent
+// steps: lengths -> scan -> entries.  Hence one launch: one cluster of 1..8 CTAs,
+// every CTA scans the whole batch itself (at most 4096 lengths, from L2) and then
+// writes its share of the table and the rows; a second launch or a grid-wide
+// exchange of the scan would each cost more than the repeated scan.  The cluster's
+// only exchange is a barrier before `used` is overwritten (it may be in place).
+#include "ops.h"
+#include "tcgen05.cuh"
+
+namespace dfl {
+
+namespace {
+
+constexpr int NT = 512;
+constexpr int PER = DFLASH_OPS_MAX_BATCH / NT;  // requests per thread of the scan
+constexpr int MAXC = 8;                         // portable cluster size
+
+__global__ void __launch_bounds__(NT) kv_tables_kernel(dflash_kv_tables_args a, int ctas) {
+    pdl_wait();
+    pdl_trigger();
+    __shared__ int qs[DFLASH_OPS_MAX_BATCH + 1];  // first row of each request
+    __shared__ int pa[DFLASH_OPS_MAX_BATCH];      // pages taken before each request
+    __shared__ int2 wsum[NT / 32];
+    __shared__ int bad_s;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int rank = blockIdx.x;
+    if (tid == 0) bad_s = 0;
+    __syncthreads();
+
+    // thread t owns the `per` consecutive requests from per * t (per as small as the batch allows)
+    const int per = (a.batch + NT - 1) / NT, s0 = per * tid;
+    int bad = 0;
+    long long rows = 0, pages = 0;  // sums in 64 bits: lengths are the caller's
+    int nw[PER], ad[PER];
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+        nw[i] = ad[i] = 0;
+        if (i < per && s0 + i < a.batch) {
+            const int kv = a.kv_lens[s0 + i], n = a.new_lens[s0 + i];
+            if (kv < 0 || n < 0) {
+                bad |= 8;
+            } else {
+                const long long need = ((long long)kv + n + 63) >> 6;
+                nw[i] = n;
+                ad[i] = (int)(need - (((long long)kv + 63) >> 6));
+                if (need > a.width) bad |= 2;
+            }
+        }
+        rows += nw[i];
+        pages += ad[i];
+    }
+    const int used = a.free_pages ? *a.used : 0;
+    if (used < 0) bad |= 8;
+    // the sums saturate: past 2^30 the call fails its row or page check anyway
+    constexpr long long SAT = 1ll << 30;
+    int2 mine = make_int2((int)min(rows, SAT), (int)min(pages, SAT));
+    int2 inc = mine;
+    auto add = [](int x, int y) { return (int)min((long long)x + y, 1ll << 30); };
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int x = __shfl_up_sync(0xffffffffu, inc.x, o), y = __shfl_up_sync(0xffffffffu, inc.y, o);
+        if (lane >= o) inc = make_int2(add(inc.x, x), add(inc.y, y));
+    }
+    if (lane == 31) wsum[warp] = inc;
+    if (bad) atomicOr(&bad_s, bad);
+    __syncthreads();
+    int2 before = make_int2(0, 0), total = make_int2(0, 0);
+#pragma unroll
+    for (int w = 0; w < NT / 32; ++w) {
+        if (w == warp) before = total;
+        total = make_int2(add(total.x, wsum[w].x), add(total.y, wsum[w].y));
+    }
+    // exclusive: the inclusive warp scan of the lane before, plus the warps before
+    int2 ex = make_int2(__shfl_up_sync(0xffffffffu, inc.x, 1), __shfl_up_sync(0xffffffffu, inc.y, 1));
+    if (lane == 0) ex = make_int2(0, 0);
+    ex = make_int2(add(ex.x, before.x), add(ex.y, before.y));
+#pragma unroll
+    for (int i = 0; i < PER; ++i)
+        if (i < per && s0 + i < a.batch) {
+            qs[s0 + i] = ex.x;
+            pa[s0 + i] = ex.y;
+            ex = make_int2(add(ex.x, nw[i]), add(ex.y, ad[i]));
+        }
+    if (tid == 0) qs[a.batch] = total.x;
+    int status = bad_s;
+    if (a.free_pages && (long long)max(used, 0) + total.y > a.n_free) status |= 1;
+    if (total.x > a.rows) status |= 4;
+    __syncthreads();
+    const bool ok = status == 0;
+
+    const int gt = rank * NT + tid, gn = ctas * NT;
+    // table: old entries copied (unless in place), the request's new pages, then scratch
+    if (ok && a.table_out) {
+        const long long cells = (long long)a.batch * a.width;
+        for (long long i = gt; i < cells; i += gn) {
+            const int s = (int)(i / a.width), j = (int)(i - (long long)s * a.width);
+            const int kv = a.kv_lens[s];
+            const int old = (int)(((long long)kv + 63) >> 6);
+            const int need = (int)(((long long)kv + a.new_lens[s] + 63) >> 6);
+            int page = a.scratch_page;
+            if (j < old || (!a.free_pages && j < need)) page = a.table[(long long)s * a.ld_table + j];
+            else if (j < need) page = a.free_pages[used + pa[s] + j - old];
+            a.table_out[(long long)s * a.ld_out + j] = page;
+        }
+    }
+    // rows: the request of row r is the last s with qs[s] <= r (requests without rows share
+    // their start with the next one)
+    for (int r = gt; r < a.rows; r += gn) {
+        int seq = -1, pos = -1;
+        long long slot = -1;
+        if (ok && r < total.x) {
+            int lo = 0, hi = a.batch;  // qs[lo] <= r < qs[hi]
+            while (hi - lo > 1) {
+                const int mid = (lo + hi) >> 1;
+                if (qs[mid] <= r) lo = mid;
+                else hi = mid;
+            }
+            seq = lo;
+            const int kv = a.kv_lens[seq], i = kv + r - qs[seq];
+            pos = a.base_pos + i;
+            const int j = i >> 6, old = (int)(((long long)kv + 63) >> 6);
+            const int page = (j < old || !a.free_pages) ? a.table[(long long)seq * a.ld_table + j]
+                                                        : a.free_pages[used + pa[seq] + j - old];
+            slot = (long long)page * 64 + (i & 63);
+        }
+        if (a.row_seq) a.row_seq[r] = seq;
+        if (a.row_pos) a.row_pos[r] = pos;
+        if (a.slots) a.slots[r] = slot;
+    }
+    for (int s = gt; s <= a.batch; s += gn) a.q_start[s] = ok ? qs[s] : 0;
+    if (ctas > 1) tc::cluster_sync();  // every CTA has read `used`
+    else __syncthreads();
+    if (rank == 0 && tid == 0) {
+        *a.status = status;
+        if (a.used_out) *a.used_out = ok ? used + (a.free_pages ? total.y : 0) : used;
+    }
+}
+
+dflash_status fail(const char* msg) {
+    set_global_error(msg);
+    return DFLASH_E_INVAL;
+}
+
+}  // namespace
+
+void kv_tables(const Launch& L, const dflash_kv_tables_args& a) {
+    // One CTA per 4096 table entries and rows, 1..8 in one cluster
+    const long long work = (long long)a.batch * a.width + a.rows;
+    int c = 1;
+    while (c < MAXC && work > (long long)c * 4096) c *= 2;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(c);
+    cfg.blockDim = dim3(NT);
+    cfg.stream = L.stream;
+    cudaLaunchAttribute attr[2];
+    int n = 0;
+    if (L.pdl) {
+        attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[n++].val.programmaticStreamSerializationAllowed = 1;
+    }
+    if (c > 1) {
+        attr[n].id = cudaLaunchAttributeClusterDimension;
+        attr[n].val.clusterDim.x = c;
+        attr[n].val.clusterDim.y = attr[n].val.clusterDim.z = 1;
+        ++n;
+    }
+    cfg.attrs = attr;
+    cfg.numAttrs = n;
+    if (cudaLaunchKernelEx(&cfg, kv_tables_kernel, a, c) != cudaSuccess) L.fail();
+    L.bump();
+}
+
+}  // namespace dfl
+
+using namespace dfl;
+
+extern "C" dflash_status dflash_kv_tables(const dflash_kv_tables_args* p, void* cuda_stream) {
+    if (!p) return fail("kv_tables: args is NULL");
+    const dflash_kv_tables_args& a = *p;
+    if (a.batch < 1 || a.batch > DFLASH_OPS_MAX_BATCH) return fail("kv_tables: batch outside [1, 4096]");
+    if (a.width < 0 || a.rows < 0 || a.rows >= (1 << 30) || a.n_free < 0)
+        return fail("kv_tables: width, rows and n_free must not be negative (rows below 2^30)");
+    if (a.width > (1 << 24) || a.base_pos < 0 || a.base_pos > (1 << 30))
+        return fail("kv_tables: width above 2^24 or base_pos outside [0, 2^30]");
+    if (!a.kv_lens || !a.new_lens || !a.q_start || !a.status) return fail("kv_tables: NULL argument");
+    if (a.width > 0 && !a.table) return fail("kv_tables: table is NULL");
+    if (a.ld_table < a.width || (a.table_out && a.ld_out < a.width))
+        return fail("kv_tables: a table row stride is smaller than width");
+    if (a.free_pages && (!a.used || !a.used_out || (a.width > 0 && !a.table_out)))
+        return fail("kv_tables: taking pages needs used, used_out and table_out");
+    if (a.table_out == a.table && a.table && a.ld_out != a.ld_table)
+        return fail("kv_tables: in place needs one row stride");
+    bool failed = false;
+    Launch L{(cudaStream_t)cuda_stream, nullptr};
+    L.failed = &failed;
+    kv_tables(L, a);
+    const cudaError_t e = cudaGetLastError();
+    if (failed || e != cudaSuccess) {
+        set_global_error(e != cudaSuccess ? cudaGetErrorString(e) : "kv_tables: launch failed");
+        return DFLASH_E_CUDA;
+    }
+    return DFLASH_OK;
+}

@@ -414,6 +414,170 @@ dflash_status dflash_head_argmax_noalloc(int32_t dtype, const float* x, const fl
                                          const void* head, int32_t rows, int32_t d_model, int32_t vocab,
                                          int32_t* out, void* cuda_stream);
 
+/* ======================================================= serving operators
+ * Stateless operators next to the round, on the caller's device memory.  They
+ * allocate nothing, keep nothing between calls and never synchronise: each is
+ * queued on cuda_stream (NULL = legacy default stream; the stream's device
+ * must be current) and may be captured into a CUDA graph.  Argument errors are
+ * E_INVAL before anything is queued, with the text in dflash_last_error(NULL);
+ * what only the device can see is reported in an output, as each call says.
+ * KV pages hold 64 tokens: a cache is [pages][H_kv][64][hd] (one layer), page
+ * p token t of KV head h at ((p * H_kv + h) * 64 + t) * hd.  Sequences per
+ * call: at most DFLASH_OPS_MAX_BATCH. */
+enum { DFLASH_OPS_MAX_BATCH = 4096 };
+
+/* Page tables and slot maps of a batch from its request lengths.  Request s
+ * has kv_lens[s] tokens cached and appends new_lens[s].  With
+ * old = ceil(kv / 64) and need = ceil((kv + new) / 64):
+ *   table_out[s][j]  = table[s][j] for j < old; the next page of free_pages
+ *                      (requests in order, free_pages[*used] first) for
+ *                      old <= j < need; scratch_page for need <= j < width
+ *   q_start[s]       = sum of new_lens before s; q_start[batch] = the total T
+ *   row r < T (token j of request s): row_seq = s, row_pos = base_pos + kv + j,
+ *                      slot = 64 * page + token, page = table_out[s][(kv+j)/64]
+ *   rows T <= r < rows: row_seq = row_pos = -1, slot = -1
+ *   used_out         = *used + pages taken
+ * free_pages NULL: the caller's table already holds every page; nothing is
+ * taken and table_out may be NULL.
+ * status (device): 0, or a sum of 1 (the pool has too few pages), 2 (a request
+ * needs more than width pages), 4 (T > rows), 8 (a negative length or *used).  When it is
+ * not 0 nothing is taken: table_out is not written, used_out = *used, q_start
+ * is all 0 and every row is -1.
+ * table_out may be table and used_out may be used (in place); no other overlap.
+ * Rows of table and table_out are ld_table / ld_out entries apart.
+ * Errors: E_INVAL (sizes, NULL), E_CUDA. */
+typedef struct {
+    int32_t batch;             /* 1 .. DFLASH_OPS_MAX_BATCH */
+    int32_t width;             /* table entries per request */
+    int32_t rows;              /* entries of row_seq, row_pos and slots */
+    int32_t n_free;            /* entries of free_pages */
+    int32_t base_pos;          /* position of a request's token 0 (a shared prefix before it) */
+    int32_t scratch_page;
+    int64_t ld_table;
+    int64_t ld_out;
+    const int32_t* kv_lens;    /* [batch] */
+    const int32_t* new_lens;   /* [batch] */
+    const int32_t* table;      /* [batch][width] */
+    const int32_t* free_pages; /* [n_free] or NULL */
+    const int32_t* used;       /* [1]: pages of free_pages taken before; NULL when free_pages is */
+    int32_t* table_out;        /* [batch][width] */
+    int32_t* used_out;         /* [1] */
+    int32_t* q_start;          /* [batch + 1] */
+    int32_t* row_seq;          /* [rows] or NULL */
+    int32_t* row_pos;          /* [rows] or NULL */
+    int64_t* slots;            /* [rows] or NULL */
+    int32_t* status;           /* [1] */
+} dflash_kv_tables_args;
+dflash_status dflash_kv_tables(const dflash_kv_tables_args* args, void* cuda_stream);
+
+/* Attention of a batch whose sequences begin with the same prefix.  The
+ * prefix's keys and values (prefix_len tokens in prefix_pages, any length) are
+ * read once for the whole batch; each sequence's own keys (kv_lens[s] tokens
+ * in table[s], the rows of this call included) follow it.  Rows
+ * q_start[s] .. q_start[s+1]-1 of q belong to sequence s; row j of its m rows
+ * sees the whole prefix and its own keys i < kv_lens[s] - m + j + 1 (causal)
+ * or i < kv_lens[s].  out = softmax(scale q.k) v per query head h over KV head
+ * h / (H / H_kv); lse (optional) = natural log of the sum of exp(scale q.k).
+ * A row that sees no key gets out = 0 and lse = -inf.  Rows outside
+ * [q_start[0], q_start[batch]) are left as they were.  The slots of a page
+ * past the last valid token may hold anything; keys and values of valid
+ * tokens must be finite.
+ * Device-side checks: a sequence with a page outside [0, n_pages) among its
+ * keys, kv_lens[s] outside [0, 64 * width], or q_start decreasing or leaving
+ * [0, rows] gets NaN in its rows' out and lse (every row, for a bad prefix
+ * page or a bounded device wait that ran out); nothing is read or written out
+ * of range.
+ * dtype F32 or BF16 (q, caches and out); head_dim 64 or 128; H / H_kv at most
+ * 64; q, k_cache and v_cache 16-byte aligned, ld_q a multiple of 16 bytes.
+ * The scores, the softmax and the accumulation are fp32; in BF16 each softmax
+ * weight is rounded to bf16 for the product with v.
+ * workspace: 16-byte aligned device memory of at least
+ * dflash_shared_prefix_workspace() bytes, used by this call only until it has
+ * finished: calls that may overlap need workspaces of their own.
+ * Errors: E_INVAL, E_CUDA. */
+typedef struct {
+    int32_t dtype;
+    int32_t n_heads;
+    int32_t n_kv_heads;
+    int32_t head_dim;
+    int32_t batch;             /* 1 .. DFLASH_OPS_MAX_BATCH */
+    int32_t rows;              /* rows of q, out and lse */
+    int32_t n_pages;           /* pages of each cache */
+    int32_t prefix_len;        /* tokens; prefix_pages holds ceil(prefix_len / 64) entries */
+    int32_t width;             /* table entries per sequence */
+    int32_t causal;
+    float scale;               /* > 0 */
+    int32_t reserved;          /* 0 */
+    int64_t ld_q;              /* elements between rows of q (H * hd when contiguous) */
+    int64_t ld_out;            /* elements between rows of out */
+    int64_t ld_table;
+    const void* q;             /* [rows][H][hd] */
+    const void* k_cache;       /* [n_pages][H_kv][64][hd] */
+    const void* v_cache;
+    const int32_t* prefix_pages;
+    const int32_t* table;      /* [batch][width]: sequence s's own keys 64 j .. 64 j + 63 */
+    const int32_t* kv_lens;    /* [batch] */
+    const int32_t* q_start;    /* [batch + 1] */
+    void* out;                 /* [rows][H][hd] */
+    float* lse;                /* [rows][H] or NULL */
+    void* workspace;
+    size_t workspace_bytes;
+} dflash_shared_prefix_args;
+dflash_status dflash_shared_prefix_attention(const dflash_shared_prefix_args* args, void* cuda_stream);
+/* Bytes of workspace for a call with these sizes (any lengths within them);
+ * 0 for sizes that the call refuses. */
+size_t dflash_shared_prefix_workspace(int32_t dtype, int32_t n_heads, int32_t n_kv_heads, int32_t head_dim,
+                                      int32_t batch, int32_t rows);
+
+/* Penalties for repeated tokens, biases and grammar masks on logits.  Rows are
+ * sequence-major, rows_per_seq of them each; row j of sequence s continues
+ * history[s][0 .. hist_lens[s]) and the first j of its drafts.  For token v
+ * with c = its count among the tokens after the prompt (drafts included), in
+ * this order:
+ *   x = logits[v]
+ *   seen in the prompt or after it:  x = x > 0 ? x / repetition : x * repetition
+ *   x = x - frequency * c;   c > 0:  x = x - presence
+ *   x = x + bias_values of the last entry of bias_ids[s] that is v
+ *   bit v of the row's mask is 0:    x = -inf
+ * in fp32, rounded once to the logits' type.  A mask that allows no token
+ * leaves a row of -inf.  Ids outside [0, vocab) in history, drafts and
+ * bias_ids are skipped (padding); a mask_index outside [0, n_masks) means no
+ * mask; hist_lens is clamped to [0, hist_width], prompt_lens to [0, hist_lens].
+ * Each of the three groups may be left out: history NULL (no penalties),
+ * bias_ids NULL, masks NULL; repetition / presence / frequency NULL are 1 / 0
+ * / 0.  out may be logits (in place: only the tokens that change are touched),
+ * with no other overlap; rows are ld_logits / ld_out elements apart and what
+ * lies behind vocab in a row is not touched.
+ * Errors: E_INVAL, E_CUDA. */
+typedef struct {
+    int32_t dtype;             /* of logits and out: F32 or BF16 */
+    int32_t batch;
+    int32_t rows_per_seq;      /* 1 .. 32 */
+    int32_t vocab;
+    int32_t hist_width;        /* columns of history */
+    int32_t bias_width;        /* columns of bias_ids and bias_values */
+    int32_t n_masks;
+    int32_t reserved;          /* 0 */
+    int64_t ld_logits;
+    int64_t ld_out;
+    int64_t ld_hist;           /* elements between rows of history */
+    int64_t ld_mask;           /* words between masks: at least ceil(vocab / 32) */
+    const void* logits;        /* [batch * rows_per_seq][vocab] */
+    void* out;
+    const int32_t* history;    /* [batch][hist_width] or NULL */
+    const int32_t* hist_lens;  /* [batch] */
+    const int32_t* prompt_lens; /* [batch]: the first prompt_lens[s] history tokens are the prompt */
+    const int32_t* drafts;     /* [batch][rows_per_seq - 1] or NULL (no drafts between the rows) */
+    const float* repetition;   /* [batch] or NULL */
+    const float* presence;     /* [batch] or NULL */
+    const float* frequency;    /* [batch] or NULL */
+    const int32_t* bias_ids;   /* [batch][bias_width] or NULL */
+    const float* bias_values;  /* [batch][bias_width] */
+    const uint32_t* masks;     /* [n_masks][ld_mask] or NULL: bit v % 32 of word v / 32 is 1 when v is allowed */
+    const int32_t* mask_index; /* [batch * rows_per_seq] */
+} dflash_logits_args;
+dflash_status dflash_process_logits(const dflash_logits_args* args, void* cuda_stream);
+
 /* Release every library-owned buffer.  NULL is a no-op. */
 void dflash_destroy(dflash_ctx* ctx);
 

@@ -1,0 +1,116 @@
+"""Refusals of the serving operators, host side (no GPU): every bad argument is E_INVAL with a reason,
+and the ctypes mirrors of the argument structs have the header's layout."""
+import ctypes
+import os
+import subprocess
+
+import pytest
+
+import block_diffusion_speculative_ctx_gb300 as dfl
+from block_diffusion_speculative_ctx_gb300 import build as dbuild
+
+ops = pytest.importorskip("block_diffusion_speculative_ctx_gb300.ops")
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+
+
+@pytest.fixture(scope="module")
+def lib():
+    dbuild.build()
+    return dfl.load()
+
+
+def test_struct_layouts_match_the_header(tmp_path):
+    prog = tmp_path / "sz.c"
+    structs = (ops.dflash_kv_tables_args, ops.dflash_shared_prefix_args, ops.dflash_logits_args)
+    names = [f"sizeof({s.__name__})" for s in structs]
+    names += [f"offsetof({s.__name__}, {f[0]})" for s in structs for f in s._fields_]
+    prog.write_text("#include <stdio.h>\n#include <stddef.h>\n#include \"dflash.h\"\nint main(void) {\n"
+                    + "".join(f'  printf("%zu\\n", (size_t){n});\n' for n in names) + "  return 0;\n}\n")
+    exe = tmp_path / "sz"
+    subprocess.run(["gcc", "-I", os.path.join(ROOT, "include"), str(prog), "-o", str(exe)], check=True)
+    got = [int(x) for x in subprocess.run([str(exe)], capture_output=True, text=True, check=True).stdout.split()]
+    want = [ctypes.sizeof(s) for s in structs] + [getattr(s, f[0]).offset for s in structs for f in s._fields_]
+    assert got == want
+
+
+P = 4096  # stands for a device pointer (never read: every call here is refused)
+
+
+def tables(**kw):
+    d = dict(batch=2, width=4, rows=8, n_free=4, base_pos=0, scratch_page=0, ld_table=4, ld_out=4, kv_lens=P, new_lens=P,
+             table=P, free_pages=P, used=P, table_out=2 * P, used_out=P, q_start=P, row_seq=P, row_pos=P, slots=P, status=P)
+    d.update(kw)
+    return ops.dflash_kv_tables_args(**d)
+
+
+def attn(**kw):
+    d = dict(dtype=1, n_heads=8, n_kv_heads=2, head_dim=128, batch=2, rows=4, n_pages=16, prefix_len=100, width=2, causal=1,
+             scale=0.1, reserved=0, ld_q=1024, ld_out=1024, ld_table=2, q=P, k_cache=P, v_cache=P, prefix_pages=P, table=P,
+             kv_lens=P, q_start=P, out=P, lse=P, workspace=P, workspace_bytes=1 << 40)
+    d.update(kw)
+    return ops.dflash_shared_prefix_args(**d)
+
+
+def rules(**kw):
+    d = dict(dtype=0, batch=2, rows_per_seq=4, vocab=1000, hist_width=8, bias_width=3, n_masks=2, reserved=0, ld_logits=1000,
+             ld_out=1000, ld_hist=8, ld_mask=32, logits=P, out=P, history=P, hist_lens=P, prompt_lens=P, drafts=P,
+             repetition=P, presence=P, frequency=P, bias_ids=P, bias_values=P, masks=P, mask_index=P)
+    d.update(kw)
+    return ops.dflash_logits_args(**d)
+
+
+@pytest.mark.parametrize("kw", [
+    dict(batch=0), dict(batch=4097), dict(width=-1), dict(rows=-1), dict(rows=1 << 30), dict(n_free=-1), dict(width=1 << 25),
+    dict(base_pos=-1), dict(kv_lens=None), dict(new_lens=None), dict(q_start=None), dict(status=None), dict(table=None),
+    dict(ld_table=3), dict(ld_out=3), dict(used=None), dict(used_out=None), dict(table_out=None),
+    dict(table_out=P, ld_out=5)])
+def test_kv_tables_refuses(lib, kw):
+    assert lib.dflash_kv_tables(ctypes.byref(tables(**kw)), None) == dfl.DFLASH_E_INVAL
+    assert "kv_tables" in dfl.dflash_last_error(None)
+
+
+@pytest.mark.parametrize("kw", [
+    dict(dtype=2), dict(head_dim=96), dict(n_heads=9), dict(n_kv_heads=0), dict(n_heads=130, ld_q=130 * 128, ld_out=130 * 128),
+    dict(n_heads=2048, n_kv_heads=2048, ld_q=1 << 18, ld_out=1 << 18), dict(batch=0), dict(batch=4097), dict(rows=-1),
+    dict(rows=(1 << 20) + 1), dict(n_pages=0), dict(n_pages=1 << 24), dict(prefix_len=-1), dict(width=-1), dict(scale=0.0),
+    dict(scale=-1.0), dict(scale=float("nan")), dict(scale=float("inf")), dict(q=None), dict(k_cache=None), dict(v_cache=None),
+    dict(kv_lens=None), dict(q_start=None), dict(table=None), dict(prefix_pages=None), dict(out=None), dict(workspace=None),
+    dict(q=P + 8), dict(k_cache=P + 2), dict(v_cache=P + 4), dict(out=P + 8), dict(workspace=P + 1), dict(ld_q=1016),
+    dict(ld_q=1028), dict(ld_out=1000), dict(ld_table=1), dict(workspace_bytes=0)])
+def test_shared_prefix_attention_refuses(lib, kw):
+    assert lib.dflash_shared_prefix_attention(ctypes.byref(attn(**kw)), None) == dfl.DFLASH_E_INVAL
+    assert "shared_prefix_attention" in dfl.dflash_last_error(None)
+
+
+def test_shared_prefix_workspace_sizes(lib):
+    f = lib.dflash_shared_prefix_workspace
+    assert f(1, 32, 8, 128, 32, 512) > 0
+    assert f(1, 32, 8, 128, 32, 513) >= f(1, 32, 8, 128, 32, 512)
+
+
+@pytest.mark.parametrize("kw", [
+    dict(dtype=2), dict(batch=0), dict(batch=4097), dict(rows_per_seq=0), dict(rows_per_seq=33), dict(vocab=0),
+    dict(logits=None), dict(out=None), dict(logits=P + 2), dict(ld_logits=999), dict(ld_out=999), dict(ld_out=1004),
+    dict(hist_lens=None), dict(prompt_lens=None), dict(ld_hist=7), dict(history=None), dict(bias_values=None),
+    dict(mask_index=None), dict(ld_mask=31)])
+def test_process_logits_refuses(lib, kw):
+    assert lib.dflash_process_logits(ctypes.byref(rules(**kw)), None) == dfl.DFLASH_E_INVAL
+    assert "process_logits" in dfl.dflash_last_error(None)
+
+
+def test_null_args(lib):
+    assert lib.dflash_kv_tables(None, None) == dfl.DFLASH_E_INVAL
+    assert lib.dflash_shared_prefix_attention(None, None) == dfl.DFLASH_E_INVAL
+    assert lib.dflash_process_logits(None, None) == dfl.DFLASH_E_INVAL
+
+
+def test_the_bindings_refuse_cpu_tensors():
+    import torch
+    i = torch.zeros(2, dtype=torch.int32)
+    with pytest.raises(ValueError, match="CUDA"):
+        dfl.kv_tables(i, i, i[:, None], rows=4)
+    with pytest.raises(ValueError, match="CUDA"):
+        dfl.process_logits(torch.zeros(2, 8))
+    c = torch.zeros(1, 1, 64, 64)
+    with pytest.raises(ValueError, match="CUDA"):
+        dfl.shared_prefix_attention(torch.zeros(1, 1, 64), c, c, None, 0, i[:1, None], i[:1], i)
