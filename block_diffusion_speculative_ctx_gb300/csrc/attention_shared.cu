@@ -80,17 +80,20 @@ __global__ void __launch_bounds__(128) shared_simple_kernel(dflash_shared_prefix
 
 // Merge of the partial results: out = sum_i 2^(m_i - M) o_i / sum_i 2^(m_i - M) l_i over the segments that
 // hold the row's query vectors, prefix and own, in plan order (one fixed order: the same bits every run).
-// A CTA takes one row and `kper` KV heads; a thread takes 8 head dimensions of one query vector, so each
-// partial is read in whole 32-byte sectors.  Bytes: 4 hd + 8 per vector and segment (in L2), out written
-// once.
+// A CTA takes one row and one KV head, so its chain of dependent loads is: lengths -> (max, sum) of every
+// segment, one a thread -> outputs, read by groups of threads that take every G-th segment, a thread 8 head
+// dimensions of one query vector (whole 32-byte sectors).  Bytes: 4 hd + 8 per vector and segment, from L2.
 struct MergeArgs {
     sp::Shape P;
     sp::Work W;
     void* out;
     float* lse;
     long long ld_out;
-    int kper;
 };
+
+constexpr int MNT = 256;
+constexpr int MSEG = 3 * 160;  // segments of one row: at most one per worker of line 0 and of line 1
+constexpr int MHEADS = 8;      // query heads at a time
 
 template <typename T>
 __device__ __forceinline__ void store8(T* d, const float (&x)[8]);
@@ -106,11 +109,16 @@ __device__ __forceinline__ void store8<bf16>(bf16* d, const float (&x)[8]) {
 }
 
 template <typename T>
-__global__ void __launch_bounds__(256) merge_kernel(MergeArgs a) {
+__global__ void __launch_bounds__(MNT) merge_kernel(MergeArgs a) {
     using namespace sp;
-    __shared__ int seq_s, bad_s;
+    __shared__ int seq_s, bad_s, n_s;
+    __shared__ uint32_t blk_s[MSEG];               // block and stream of each segment
+    __shared__ float wgt_s[MHEADS][MSEG];          // its weight 2^(m - M) for each query head
+    __shared__ float inv_s[MHEADS];
+    __shared__ float acc_s[MNT][8];
     const Shape& P = a.P;
-    const int tid = threadIdx.x, r = blockIdx.x;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int r = blockIdx.x, kvh = blockIdx.y;
     if (tid == 0) {
         seq_s = -1;
         bad_s = 0;
@@ -119,76 +127,127 @@ __global__ void __launch_bounds__(256) merge_kernel(MergeArgs a) {
     pdl_wait();
     pdl_trigger();
     const Head h = *a.W.head;
-    for (int c = tid; c < P.n_cta; c += blockDim.x)
+    for (int c = tid; c < P.n_cta; c += MNT)
         if (a.W.err[c]) bad_s = 1;
-    for (int s = tid; s < P.batch; s += blockDim.x)
+    for (int s = tid; s < P.batch; s += MNT)
         if (P.q_start[s] <= r && r < P.q_start[s + 1]) seq_s = s;
     __syncthreads();
     bool bad = h.bad || bad_s;
     const int seq = seq_s;
     if (!bad && seq < 0) return;  // a row of no sequence
-    Seq q = {};
-    int j = 0, start = 0;
+    // the row's items: [0] prefix, [1] own
+    int line[2] = {0, 0}, n[2] = {0, 0}, n_eff[2] = {0, 0}, id[2] = {0, 0}, c0[2] = {0, 0}, nc[2] = {0, 0}, rl[2] = {0, 0};
+    uint32_t at[2] = {0u, 0u};
     if (!bad) {
-        start = P.q_start[seq];
-        q = seq_of(P, start, P.q_start[seq + 1], P.kv_lens[seq]);
-        j = r - start;
+        const int start = P.q_start[seq];
+        const Seq q = seq_of(P, start, P.q_start[seq + 1], P.kv_lens[seq]);
         if (q.kv < 0 || q.kv > (long long)64 * P.width) bad = true;
-    }
-    const int chunks = P.hd / 8;
-    for (int i = tid; i < a.kper * P.g * chunks; i += blockDim.x) {
-        const int c8 = i % chunks, hh = i / chunks % P.g, kvh = blockIdx.y * a.kper + i / (chunks * P.g);
-        if (kvh >= P.Hkv) break;
-        float M = -INFINITY, l = 0.f, o[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-        uint32_t slot_bad = 0;
-        // the segments of the item whose line starts at b: n tiles of weight w, of which the first n_eff count
-        auto item = [&](uint32_t b, uint32_t w, int n, int n_eff, int id, int nrows, int rl) {
-            const bool pair = nrows > P.RH;
-            const int x0 = pair ? rl / P.RH : 0, x1 = pair ? x0 : 1;
-            const int v = (pair ? rl % P.RH : rl) * P.g + hh;
-            const int c1 = owner(h.W, b + (uint32_t)(n - 1) * w, P.n_cta);
-            for (int c = owner(h.W, b, P.n_cta); c <= c1; ++c) {
-                const uint32_t lo = max(b, part_begin(h.W, c, P.n_cta)), hi = part_begin(h.W, c + 1, P.n_cta);
-                const int t0 = (int)((lo - b + w - 1) / w);
-                const int t1 = min((int)min((uint32_t)n, (hi - b + w - 1) / w), n_eff);
-                if (t0 >= t1) continue;
-                slot_bad |= a.W.slot_bad[id + c];
-                for (int x = x0; x <= x1; ++x) {
-                    if (x == 1 && !pair && t1 - t0 < 2) break;  // stream B had no tile
-                    const size_t slot = (size_t)(id + c) * 2 + x;
-                    const float2 ml = a.W.ml[slot * P.VT + v];
-                    const float* src = a.W.o + slot * P.VT * P.hd + ((size_t)c8 * P.VT + v) * 8;
-                    const float4 s0 = *reinterpret_cast<const float4*>(src), s1 = *reinterpret_cast<const float4*>(src + 4);
-                    const float mn = fmaxf(M, ml.x);
-                    const float e0 = M == -INFINITY ? 0.f : exp2f(M - mn), e1 = ml.x == -INFINITY ? 0.f : exp2f(ml.x - mn);
-                    M = mn;
-                    l = l * e0 + ml.y * e1;
-                    const float y[8] = {s0.x, s0.y, s0.z, s0.w, s1.x, s1.y, s1.z, s1.w};
+        if (P.npt) {
+            const int RT = P.row_tile(h.pl), rt = (r - h.r_begin) / RT;
+            line[0] = h.pl;
+            n[0] = n_eff[0] = P.npt;
+            id[0] = kvh * h.nqt + rt;
+            at[0] = (uint32_t)id[0] * (P.lead[h.pl] + (uint32_t)P.npt * P.w);
+            rl[0] = (r - h.r_begin) - rt * RT;
+        }
+        if (q.tiles && !bad) {
+            const int RT = P.row_tile(q.line), j = r - start, gi = j / RT, k = kvh * q.groups + gi;
+            line[1] = q.line;
+            n[1] = q.tiles;
+            n_eff[1] = seen_tiles(P, q, min(q.m, (gi + 1) * RT));
+            id[1] = (h.pl == q.line ? h.n_prefix : 0) + (int)a.W.ibase[seq] + k;
+            at[1] = a.W.base[seq] + (uint32_t)k * (P.lead[q.line] + (uint32_t)q.tiles * P.w);
+            rl[1] = j - gi * RT;
+        }
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) o[e] = o[e] * e0 + (e1 == 0.f ? 0.f : y[e] * e1);
+        for (int i = 0; i < 2; ++i)
+            if (n_eff[i]) {
+                const uint32_t W = h.W[line[i]], t0 = at[i] + P.lead[line[i]];
+                c0[i] = owner(W, t0, P.workers(line[i]));
+                nc[i] = owner(W, t0 + (uint32_t)(n_eff[i] - 1) * P.w, P.workers(line[i])) - c0[i] + 1;
+            }
+    }
+    const int cand = nc[0] + nc[1];  // workers that may hold a segment, in plan order
+    auto vec = [&](int i) { return rl[i] % P.RH * P.g; };  // first of the row's vectors in its stream
+    if (tid == 0) n_s = cand;
+    for (int k = tid; k < cand; k += MNT) {
+        const int i = k < nc[0] ? 0 : 1, c = i ? c0[1] + k - nc[0] : c0[0] + k;
+        const uint32_t W = h.W[line[i]];
+        int t0, t1;
+        cut(max(at[i], part_begin(W, c, P.workers(line[i]))), part_begin(W, c + 1, P.workers(line[i])), at[i],
+            P.lead[line[i]], P.w, n[i], t0, t1);
+        uint32_t blk = 0xFFFFFFFFu;  // no tile of the item in this worker's part
+        if (t0 < min(t1, n_eff[i])) {
+            blk = block_of(P, h, line[i], id[i], c) + (uint32_t)(rl[i] / P.RH);
+            if (a.W.block_bad[blk]) bad_s = 1;
+        }
+        blk_s[k] = blk;
+    }
+    __syncthreads();
+    bad = bad || bad_s;
+
+    const int chunks = P.hd / 8;
+    for (int h0 = 0; h0 < P.g; h0 += MHEADS) {
+        const int nh = min(MHEADS, P.g - h0);
+        // weights: a warp takes a head
+        for (int hh = warp; hh < nh; hh += MNT / 32) {
+            float M = -INFINITY;
+            for (int k = lane; k < cand; k += 32) {
+                float m = -INFINITY;
+                if (blk_s[k] != 0xFFFFFFFFu) m = a.W.ml[(size_t)blk_s[k] * P.VT + vec(k < nc[0] ? 0 : 1) + h0 + hh].x;
+                wgt_s[hh][k] = m;
+                M = fmaxf(M, m);
+            }
+            M = warp_max(M);
+            float l = 0.f;
+            for (int k = lane; k < cand; k += 32) {
+                const float m = wgt_s[hh][k], w = m == -INFINITY ? 0.f : exp2f(m - M);
+                if (w != 0.f) l += w * a.W.ml[(size_t)blk_s[k] * P.VT + vec(k < nc[0] ? 0 : 1) + h0 + hh].y;
+                wgt_s[hh][k] = w;
+            }
+            l = warp_sum(l);
+            if (lane == 0) {
+                inv_s[hh] = bad ? NAN : l > 0.f ? 1.f / l : 0.f;
+                if (a.lse)
+                    a.lse[(long long)r * P.H + kvh * P.g + h0 + hh] =
+                        bad ? NAN : l > 0.f ? (M + log2f(l)) * 0.6931471805599453f : -INFINITY;
+            }
+        }
+        __syncthreads();
+        const int part = nh * chunks, G = MNT / part, grp = tid / part, e = tid - grp * part;
+        const int hh = e / chunks, c8 = e - hh * chunks;
+        float o[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+        if (grp < G) {
+#pragma unroll 4
+            for (int k = grp; k < cand; k += G) {
+                const float w = wgt_s[hh][k];
+                if (w != 0.f) {
+                    const float* src = a.W.o + (size_t)blk_s[k] * P.VT * P.hd +
+                                       ((size_t)c8 * P.VT + vec(k < nc[0] ? 0 : 1) + h0 + hh) * 8;
+                    const float4 x = *reinterpret_cast<const float4*>(src), y = *reinterpret_cast<const float4*>(src + 4);
+                    o[0] += w * x.x;
+                    o[1] += w * x.y;
+                    o[2] += w * x.z;
+                    o[3] += w * x.w;
+                    o[4] += w * y.x;
+                    o[5] += w * y.y;
+                    o[6] += w * y.z;
+                    o[7] += w * y.w;
                 }
             }
-        };
-        if (!bad && P.npt) {
-            const int rt = (r - h.r_begin) / P.RT, id = kvh * h.nqt + rt;
-            item((uint32_t)id * P.npt * h.wp, h.wp, P.npt, P.npt, id, min(P.RT, h.r_end - h.r_begin - rt * P.RT),
-                 (r - h.r_begin) % P.RT);
-        }
-        if (!bad && q.tiles) {
-            const int gi = j / P.RT, k = kvh * q.groups + gi, nrows = min(P.RT, q.m - gi * P.RT);
-            const int n_eff = P.causal ? min(q.tiles, cdiv(max(q.kv - q.m + gi * P.RT + nrows, 0), P.KT)) : q.tiles;
-            item(a.W.base[seq] + (uint32_t)k * q.tiles * q.w, q.w, q.tiles, n_eff, (int)(h.n_prefix + a.W.ibase[seq]) + k, nrows,
-                 j % P.RT);
-        }
-        const bool nan = bad || slot_bad;
-        const float inv = l > 0.f ? 1.f / l : 0.f;
-        float y[8];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) y[e] = nan ? NAN : o[e] * inv;
-        const int head = kvh * P.g + hh;
-        store8<T>(reinterpret_cast<T*>(a.out) + (long long)r * a.ld_out + (long long)head * P.hd + c8 * 8, y);
-        if (a.lse && c8 == 0)
-            a.lse[(long long)r * P.H + head] = nan ? NAN : l > 0.f ? (M + log2f(l)) * 0.6931471805599453f : -INFINITY;
+            for (int i = 0; i < 8; ++i) acc_s[tid][i] = o[i];
+        }
+        __syncthreads();
+        if (grp == 0) {
+            for (int q = 1; q < G; ++q)
+#pragma unroll
+                for (int i = 0; i < 8; ++i) o[i] += acc_s[tid + q * part][i];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) o[i] = bad ? NAN : o[i] * inv_s[hh];
+            store8<T>(reinterpret_cast<T*>(a.out) + (long long)r * a.ld_out + (long long)(kvh * P.g + h0 + hh) * P.hd + c8 * 8, o);
+        }
+        __syncthreads();
     }
 }
 
@@ -200,29 +259,23 @@ namespace {
 
 constexpr int CTAS = 152;  // one per SM
 
-sp::Shape shape_of(const dflash_shared_prefix_args& a) {
+// The sizes alone (what the workspace depends on).
+sp::Shape sizes_of(int H, int Hkv, int hd, int batch, int rows) {
     sp::Shape P = {};
-    P.H = a.n_heads;
-    P.Hkv = a.n_kv_heads;
-    P.g = a.n_heads / a.n_kv_heads;
-    P.hd = a.head_dim;
+    P.H = H;
+    P.Hkv = Hkv;
+    P.g = H / Hkv;
+    P.hd = hd;
     P.VT = 128;
     P.RH = P.VT / P.g;
-    P.RT = 2 * P.RH;
-    P.KT = 128;
-    P.batch = a.batch;
-    P.rows = a.rows;
-    P.width = a.width;
-    P.prefix_len = a.prefix_len;
-    P.causal = a.causal != 0;
-    P.n_pages = a.n_pages;
-    P.npt = (a.prefix_len + P.KT - 1) / P.KT;
+    P.KT = 64;
+    P.batch = batch;
+    P.rows = rows;
     P.n_cta = CTAS;
-    P.ld_table = a.ld_table;
-    P.prefix_pages = a.prefix_pages;
-    P.table = a.table;
-    P.kv_lens = a.kv_lens;
-    P.q_start = a.q_start;
+    // an item's fixed cost: two tiles on line 0, three on line 1
+    P.w = 1;
+    P.lead[0] = 2;
+    P.lead[1] = 3;
     return P;
 }
 
@@ -236,19 +289,27 @@ bool shared_prefix_attention(const Launch& L, const dflash_shared_prefix_args& a
         return true;
     }
     MergeArgs m;
-    m.P = shape_of(a);
-    sp::layout((char*)a.workspace, a.head_dim, m.P.VT, a.batch, m.P.n_cta,
-               sp::max_slots(a.n_kv_heads, m.P.RT, a.batch, a.rows, m.P.n_cta), &m.W);
+    sp::Shape& P = m.P;
+    P = sizes_of(a.n_heads, a.n_kv_heads, a.head_dim, a.batch, a.rows);
+    P.width = a.width;
+    P.prefix_len = a.prefix_len;
+    P.causal = a.causal != 0;
+    P.n_pages = a.n_pages;
+    P.npt = (a.prefix_len + P.KT - 1) / P.KT;
+    P.ld_table = a.ld_table;
+    P.prefix_pages = a.prefix_pages;
+    P.table = a.table;
+    P.kv_lens = a.kv_lens;
+    P.q_start = a.q_start;
+    sp::layout((char*)a.workspace, P, &m.W);
     m.out = a.out;
     m.lse = a.lse;
     m.ld_out = a.ld_out;
-    if (!shared_attention_tc(L, m.P, m.W, a)) return false;
+    if (!shared_attention_tc(L, P, m.W, a)) return false;
     // the merge starts as the main kernel's CTAs leave
     Launch after = L;
     after.pdl = true;
-    const int per = m.P.g * a.head_dim / 8;
-    m.kper = std::max(1, 256 / per);
-    launch_k(after, merge_kernel<bf16>, dim3(a.rows, (a.n_kv_heads + m.kper - 1) / m.kper), dim3(256), 0, 1, m);
+    launch_k(after, merge_kernel<bf16>, dim3(a.rows, a.n_kv_heads), dim3(MNT), 0, 1, m);
     return true;
 }
 
@@ -263,7 +324,7 @@ dflash_status check_shared_prefix(const dflash_shared_prefix_args& a, const char
     if (a.n_heads < 1 || a.n_kv_heads < 1 || a.n_heads % a.n_kv_heads || a.n_heads / a.n_kv_heads > 64)
         return bad("shared_prefix_attention: n_heads must be a multiple of n_kv_heads, at most 64 times it");
     if (a.n_heads > 1024) return bad("shared_prefix_attention: more than 1024 heads");
-    if (a.batch < 1 || a.batch > DFLASH_OPS_MAX_BATCH) return bad("shared_prefix_attention: batch outside [1, 4096]");
+    if (a.batch < 1 || a.batch > DFLASH_OPS_MAX_BATCH) return bad("shared_prefix_attention: batch outside [1, 2048]");
     if (a.rows < 0 || a.rows > (1 << 20)) return bad("shared_prefix_attention: rows outside [0, 2^20]");
     // rows of the caches as one matrix [pages * H_kv * 64, hd]: TMA coordinates are 32-bit
     if (a.n_pages < 1 || (long long)a.n_pages * a.n_kv_heads * 64 >= (1ll << 31))
@@ -297,8 +358,7 @@ extern "C" size_t dflash_shared_prefix_workspace(int32_t dtype, int32_t n_heads,
         batch > DFLASH_OPS_MAX_BATCH || rows < 0 || rows > (1 << 20) || (head_dim != 64 && head_dim != 128) ||
         (dtype != DFLASH_DTYPE_F32 && dtype != DFLASH_DTYPE_BF16))
         return 0;
-    const int RT = 2 * (128 / (n_heads / n_kv_heads));
-    return sp::layout(nullptr, head_dim, 128, batch, CTAS, sp::max_slots(n_kv_heads, RT, batch, rows, CTAS), nullptr);
+    return sp::layout(nullptr, sizes_of(n_heads, n_kv_heads, head_dim, batch, rows), nullptr);
 }
 
 extern "C" dflash_status dflash_shared_prefix_attention(const dflash_shared_prefix_args* p, void* cuda_stream) {

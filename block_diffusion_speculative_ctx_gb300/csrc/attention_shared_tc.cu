@@ -8,21 +8,24 @@
 // throughout, the weights rounded once to bf16 for the product with V (the sum
 // takes the unrounded ones).
 //
-// One CTA per SM walks its segments of the plan (shared_plan.cuh).  A segment
-// holds up to two streams A, B of 128 query vectors (TMEM lanes):
-//   pair: A and B hold different rows and share every K/V tile, which halves
-//         the shared-memory fill per product;
-//   one:  A and B hold the same rows, A takes the even tiles and B the odd ones.
+// One CTA per SM holds two streams A, B of 128 query vectors each (TMEM lanes)
+// and walks its part of both lines of the plan (shared_plan.cuh):
+//   line 0: A and B hold different rows of one item and share every K/V tile,
+//           which halves the shared-memory fill per product (tensor-bound);
+//   line 1: A and B walk segments of their own with half of the ring each
+//           (few query vectors, so bound by the K/V bytes).
+// Odd CTAs walk line 1 first, so that the bytes of one line stream while the
+// other line's products run on the neighbours.
 // Roles (warps): 0-3 softmax of A, 4-7 softmax of B (a thread is one query
-// vector), 8 issues every tcgen05.mma, 9 loads.  While the tensor cores work on
-// one stream's P V and next Q K^T, the other stream's softmax runs.
-//   TMEM: S_A, S_B (128 columns each; P overwrites its S as bf16 and is the A
-//   operand of P V from there), O_A, O_B.
-//   Shared memory: Q_A, Q_B, a ring of 128-key K or V tiles (two cache pages),
+// vector), 8 and 9 issue the tcgen05.mma of A and of B, 10 and 11 load.
+//   TMEM: per stream two S buffers of 64 columns (P overwrites its S as bf16 and
+//   is the A operand of P V from there) and O.  S of tile j + 1 is there before
+//   the softmax of tile j ends, so the softmax never waits for a product chain.
+//   Shared memory: Q_A, Q_B, a ring of K or V tiles (64 keys: one cache page),
 //   all 128-byte swizzled by TMA; page numbers come 32 at a time, one a lane.
-// Order of the MMA warp within a step: P V of A, Q K^T of A's next tile, then
-// B's: the tensor cores execute in order, so P V has read P before the next S
-// overwrites it, and a completed S implies that the P V before it has completed.
+// An MMA warp issues S0 S1, then P V of tile j and S of tile j + 2 back to back:
+// the tensor cores execute one thread's products in order, so P V has read P
+// before the next S overwrites it.
 //
 // Every wait is bounded; one that runs out sets the CTA's error word (the merge
 // writes NaN), every role leaves, copies in flight are awaited (bounded).
@@ -39,26 +42,32 @@ namespace {
 using namespace tc;
 using namespace sp;
 
-constexpr int VT = 128, KT = 128;
-constexpr int NTHR = 320;
+constexpr int VT = 128, KT = 64;
+constexpr int NTHR = 384;
 
 template <int HD>
 struct Cfg {
-    static constexpr int HALVES = HD / 64;
-    static constexpr int REG = 128 * 128;             // 128 rows of 64 elements
-    static constexpr int TILE = HALVES * REG;         // Q, K or V tile
-    static constexpr int STAGES = HD == 128 ? 4 : 8;
-    static constexpr int SMEM_TILES = (2 + STAGES) * TILE;
+    static constexpr int HALVES = HD / 64;            // 64-dim halves: one 128-byte swizzled row each
+    static constexpr int Q_REG = VT * 128, Q_TILE = HALVES * Q_REG;
+    static constexpr int KV_REG = KT * 128, TILE = HALVES * KV_REG;
+    static constexpr int STAGES = HD == 128 ? 8 : 16;  // 128 KB
+    static constexpr int RING_AT = 2 * Q_TILE;
+    static constexpr int SMEM_TILES = RING_AT + STAGES * TILE;
 };
 
+struct LineBars {
+    uint64_t kv_full[16], kv_empty[16];
+    uint64_t q_full[2], q_empty[2];
+    uint64_t s_full[2][2], p_full[2][2], o_done[2][2];  // per stream and S buffer
+    uint64_t o_empty[2];
+    uint64_t drain[2];
+};
 struct Bars {
-    uint64_t kv_full[8], kv_empty[8];
-    uint64_t q_full, q_empty;
-    uint64_t s_full[2], p_full[2], o_full[2], o_empty[2];
+    LineBars line[2];
     uint32_t tmem;
     int flag;
     int fail;
-    uint32_t ws[2 * NTHR / 32];
+    uint32_t ws[4 * NTHR / 32];
 };
 
 struct TcArgs {
@@ -120,18 +129,49 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* r) {
         : "memory");
 }
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ uint64_t pack2(float lo, float hi) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ void unpack2(uint64_t v, float& lo, float& hi) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
 __device__ __forceinline__ float ex2(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
 
-// Ring positions of a segment of n tiles, in the order the MMA warp consumes them.
-// pair: K0 V0 K1 V1 ...; one: K0 K1 V0 K2 V1 K3 ...
-__device__ __forceinline__ uint32_t k_seq(bool pair, int j) { return pair ? 2u * j : (uint32_t)(j + max(0, j - 1)); }
-__device__ __forceinline__ uint32_t v_seq(bool pair, int j, int n) {
-    return pair ? 2u * j + 1u : (uint32_t)(j + min(n, j + 2));
-}
+// Ring positions of a segment of n tiles, in the order the MMA warps consume them: K0 K1 V0 K2 V1 K3 ...
+__device__ __forceinline__ uint32_t k_seq(int j) { return (uint32_t)(j + max(0, j - 1)); }
+__device__ __forceinline__ uint32_t v_seq(int j, int n) { return (uint32_t)(j + min(n, j + 2)); }
+
+// The bounded waits of one thread: after one has run out, the later ones return at once.
+struct Waiter {
+    uint32_t* err;
+    int* fail;
+    bool ok = true;
+    __device__ __forceinline__ bool operator()(uint64_t* bar, uint32_t parity) {
+        if (mbar_try_wait(bar, parity)) return ok;
+        if (ok && !mbar_wait(bar, parity, err)) {
+            ok = false;
+            *(volatile int*)fail = 1;
+        }
+        return ok;
+    }
+};
 
 template <int HD>
 __global__ void __launch_bounds__(NTHR, 1)
@@ -142,36 +182,42 @@ __global__ void __launch_bounds__(NTHR, 1)
     const uint32_t raw = smem_u32(smem_raw);
     uint8_t* sm = smem_raw + (((raw + 1023u) & ~1023u) - raw);
     const uint32_t sb = smem_u32(sm);
-    const uint32_t q_at = sb, ring_at = sb + 2 * C::TILE;
-    Bars* B = reinterpret_cast<Bars*>(sm + C::SMEM_TILES);
-    uint32_t* base = reinterpret_cast<uint32_t*>(B + 1);
-    uint32_t* ibase = base + a.P.batch;
+    const uint32_t q_at = sb, ring_at = sb + C::RING_AT;
+    Bars* bars = reinterpret_cast<Bars*>(sm + C::SMEM_TILES);
+    uint32_t* base = reinterpret_cast<uint32_t*>(bars + 1);  // [2][MAX_BATCH]
+    uint32_t* ibase = base + 2 * MAX_BATCH;
 
     const Shape& P = a.P;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int cta = blockIdx.x;
 
     if (warp == 8) {
-        tmem_alloc(&B->tmem, 512);
+        tmem_alloc(&bars->tmem, 512);
         tmem_relinquish();
     }
     if (tid == 0) {
-        for (int i = 0; i < C::STAGES; ++i) {
-            mbar_init(&B->kv_full[i], 1);
-            mbar_init(&B->kv_empty[i], 1);
-        }
-        mbar_init(&B->q_full, 1);
-        mbar_init(&B->q_empty, 1);
-        for (int x = 0; x < 2; ++x) {
-            mbar_init(&B->s_full[x], 1);
-            mbar_init(&B->p_full[x], 4);
-            mbar_init(&B->o_full[x], 1);
-            mbar_init(&B->o_empty[x], 4);
+        for (int line = 0; line < 2; ++line) {
+            LineBars* B = &bars->line[line];
+            for (int i = 0; i < C::STAGES; ++i) {
+                mbar_init(&B->kv_full[i], 1);
+                mbar_init(&B->kv_empty[i], line == 0 ? 2 : 1);  // a line 0 stage is read by both streams
+            }
+            for (int x = 0; x < 2; ++x) {
+                mbar_init(&B->q_full[x], 1);
+                mbar_init(&B->q_empty[x], 1);
+                for (int b = 0; b < 2; ++b) {
+                    mbar_init(&B->s_full[x][b], 1);
+                    mbar_init(&B->p_full[x][b], 4);
+                    mbar_init(&B->o_done[x][b], 1);
+                }
+                mbar_init(&B->o_empty[x], 4);
+                mbar_init(&B->drain[x], 1);
+            }
         }
         mbar_fence_init();
-        B->fail = 0;
+        bars->fail = 0;
     }
-    if (tid == 32 * 9) {
+    if (tid == 32 * 10) {
         prefetch_tmap(&mq);
         prefetch_tmap(&mk);
         prefetch_tmap(&mv);
@@ -181,265 +227,275 @@ __global__ void __launch_bounds__(NTHR, 1)
     if (tid == 0) a.W.err[cta] = 0u;
     Head h;
     fence_before();
-    make_plan<NTHR>(P, base, ibase, B->ws, &B->flag, h);  // (its barriers order the setup above)
+    make_plan<NTHR>(P, base, ibase, bars->ws, &bars->flag, h);  // (its barriers order the setup above)
     fence_after();
-    const uint32_t tmem = B->tmem;
+    const uint32_t tmem = bars->tmem;
     if (cta == 0) {
         if (tid == 0) *a.W.head = h;
         for (int s = tid; s < P.batch; s += NTHR) {
-            a.W.base[s] = base[s];
+            a.W.base[s] = base[(P.q_start[s + 1] - P.q_start[s] > P.RH ? 0 : MAX_BATCH) + s];
             a.W.ibase[s] = ibase[s];
         }
     }
     uint32_t* err = &a.W.err[cta];
-    bool ok = true;
-    auto wait = [&](uint64_t* bar, uint32_t parity) {
-        if (ok && !mbar_wait(bar, parity, err)) {
-            ok = false;
-            *(volatile int*)&B->fail = 1;
-        }
-        return ok;
-    };
-
-    Walk walk(h, cta, P.n_cta);
+    Waiter wait{err, &bars->fail};
     Seg s;
-    uint32_t ring = 0;  // ring position of the segment's first tile
-    uint32_t issued = 0;
-    if (warp == 9) {
-        // ------------------------------------------------------------ loads
-        uint32_t nseg = 0;
-        while (ok && walk.next(P, h, base, ibase, s)) {
-            const int n = s.t1 - s.t0;
-            const int* pages = s.seq < 0 ? P.prefix_pages : P.table + (long long)s.seq * P.ld_table;
-            const int n_pages = (s.keys + 63) >> 6;  // valid entries of `pages`
-            const uint32_t oob = (uint32_t)P.n_pages * P.Hkv * 64;
-            uint32_t bad = 0;
-            // windows of 32 page numbers, one a lane, for the K and the V tiles
-            int kw = -64, vw = -64, kpg = 0, vpg = 0;
-            auto tile = [&](bool is_v, int j) {
-                int& w0 = is_v ? vw : kw;
-                int& pg = is_v ? vpg : kpg;
-                const int first = 2 * (s.t0 + j);
-                if (first >= w0 + 32 || first < w0) {
-                    w0 = first;
-                    pg = first + lane < n_pages ? pages[first + lane] : -2;
-                    // past the list: zeros; outside the cache: zeros, and the segment is bad
-                    if (pg != -2 || first + lane < n_pages) {
-                        if (pg < 0 || pg >= P.n_pages) {
-                            pg = -1;
+
+#pragma unroll 1
+    for (int turn = 0; turn < 2; ++turn) {
+        const int line = (cta + turn) & 1;
+        const bool pair = line == 0;
+        LineBars* B = &bars->line[line];
+        if (turn == 1) __syncthreads();  // every role of the first line has ended: the ring and TMEM are free
+        if (h.W[line] == 0 || bars->fail) continue;
+        // ring of a stream: all stages, in step with the other stream (line 0), or half of them (line 1)
+        const uint32_t depth = pair ? C::STAGES : C::STAGES / 2;
+        auto worker = [&](int x) { return pair ? cta : 2 * cta + x; };
+        auto first_stage = [&](int x) { return pair ? 0u : (uint32_t)x * (C::STAGES / 2); };
+        uint32_t ring = 0;  // ring position of the segment's first tile
+
+        if (warp >= 10) {
+            // ------------------------------------------------------------ loads
+            const int x = warp - 10;
+            if (!pair || x == 0) {
+                Walk walk(P, h, line, worker(x));
+                uint32_t nseg = 0, issued = 0;
+                while (wait.ok && walk.next(P, h, base, ibase, s)) {
+                    const int n = s.t1 - s.t0;
+                    const int* pages = s.seq < 0 ? P.prefix_pages : P.table + (long long)s.seq * P.ld_table;
+                    const int n_pages = (s.keys + 63) >> 6;  // valid entries of `pages`
+                    const int oob = P.n_pages * P.Hkv * 64;  // a row behind the cache: reads as zeros
+                    // page numbers 32 at a time, one a lane (K tiles run up to two ahead of V tiles: a window
+                    // each); past the list and outside the cache: zeros
+                    int bad = 0, w0[2] = {-64, -64}, pg[2] = {0, 0};
+                    auto tile = [&](int kv, int j) {
+                        const int first = s.t0 + j;
+                        if (first >= w0[kv] + 32) {
+                            w0[kv] = first;
+                            pg[kv] = -1;
+                            if (first + lane < n_pages) {
+                                pg[kv] = pages[first + lane];
+                                if (pg[kv] < 0 || pg[kv] >= P.n_pages) {
+                                    pg[kv] = -1;
+                                    bad |= first + lane < s.t1;
+                                }
+                            }
                         }
-                    }
-                }
-                const int p0 = __shfl_sync(0xffffffffu, pg, first - w0), p1 = __shfl_sync(0xffffffffu, pg, first - w0 + 1);
-                if (p0 == -1 || p1 == -1) bad = 1;
-                const uint32_t pos = ring + (is_v ? v_seq(s.pair, j, n) : k_seq(s.pair, j));
-                const int st = pos % C::STAGES;
-                if (lane == 0) {
-                    if (wait(&B->kv_empty[st], ((pos / C::STAGES) & 1) ^ 1)) {
-                        mbar_arrive_expect_tx(&B->kv_full[st], C::TILE);
-                        const uint32_t dst = ring_at + st * C::TILE;
+                        const int p = __shfl_sync(0xffffffffu, pg[kv], first - w0[kv]);
+                        if (lane == 0) {
+                            const int row = p < 0 ? oob : (p * P.Hkv + s.kvh) * 64;
+                            const uint32_t pos = ring + (kv ? v_seq(j, n) : k_seq(j)), st = first_stage(x) + pos % depth;
+                            if (wait(&B->kv_empty[st], ((pos / depth) & 1) ^ 1)) {
+                                mbar_arrive_expect_tx(&B->kv_full[st], C::TILE);
 #pragma unroll
-                        for (int i = 0; i < 2; ++i) {
-                            const int pgi = i ? p1 : p0;
-                            const int row = pgi < 0 ? (int)oob : (pgi * P.Hkv + s.kvh) * 64;
-#pragma unroll
-                            for (int c = 0; c < C::HALVES; ++c)
-                                tma_load_2d_u(dst + c * C::REG + i * 64 * 128, is_v ? &mv : &mk, &B->kv_full[st], 64 * c, row);
+                                for (int c = 0; c < C::HALVES; ++c)
+                                    tma_load_2d_u(ring_at + st * C::TILE + c * C::KV_REG, kv ? &mv : &mk, &B->kv_full[st],
+                                                  64 * c, row);
+                                issued = pos + 1;
+                            }
                         }
-                        issued = pos + 1;
-                    }
-                }
-                ok = __shfl_sync(0xffffffffu, (int)ok, 0);
-            };
-            auto load_q = [&]() {
-                if (lane == 0) {
-                    if (wait(&B->q_empty, (nseg & 1) ^ 1)) {
-                        mbar_arrive_expect_tx(&B->q_full, (s.pair ? 2 : 1) * C::HALVES * 128 * P.g * P.RH);
-                        for (int x = 0; x < (s.pair ? 2 : 1); ++x)
+                    };
+#pragma unroll 1
+                    for (int j = -1; j < n; ++j) {
+                        if (j >= 0) tile(1, j);
+                        if (j < 0 || j + 1 < n) {
+                            if (j < 0) {
+                                tile(0, 0);
+                                // the queries: behind the first tile, whose stage waits for the segment before alone
+                                if (lane == 0)
+                                    for (int y = x; y < (pair ? 2 : x + 1); ++y) {
+                                        if (!wait(&B->q_empty[y], (nseg & 1) ^ 1)) break;
+                                        mbar_arrive_expect_tx(&B->q_full[y], C::HALVES * 128 * P.g * P.RH);
 #pragma unroll
-                            for (int c = 0; c < C::HALVES; ++c)
-                                tma_load_3d(q_at + x * C::TILE + c * C::REG, &mq, &B->q_full, 64 * c, s.kvh * P.g,
-                                            s.row0 + x * P.RH);
-                        ++nseg;
+                                        for (int c = 0; c < C::HALVES; ++c)
+                                            tma_load_3d(q_at + y * C::Q_TILE + c * C::Q_REG, &mq, &B->q_full[y], 64 * c,
+                                                        s.kvh * P.g, s.row0 + (pair ? y * P.RH : 0));
+                                    }
+                            }
+                            if (j + 2 < n) tile(0, j + 2);
+                        }
+                        wait.ok = __shfl_sync(0xffffffffu, (int)wait.ok, 0);
+                        if (!wait.ok) break;
                     }
+                    ++nseg;
+                    bad = __any_sync(0xffffffffu, bad);
+                    if (lane == 0) {
+                        a.W.block_bad[s.block] = bad;
+                        if (pair) a.W.block_bad[s.block + 1] = bad;
+                    }
+                    ring += 2 * n;
                 }
-                ok = __shfl_sync(0xffffffffu, (int)ok, 0);
-            };
-            // the queries after the first two tiles: those wait for stages of the segment before only
-            if (s.pair) {
-                for (int j = 0; j < n && ok; ++j) {
-                    tile(false, j);
-                    tile(true, j);
-                    if (j == 0) load_q();
+                if (lane == 0 && wait.ok) {
+                    // the last releases have arrived: nothing is under way to this line's barriers any more
+                    for (uint32_t pos = issued > depth ? issued - depth : 0; pos < issued; ++pos)
+                        wait(&B->kv_empty[first_stage(x) + pos % depth], (pos / depth) & 1);
+                    for (int y = x; y < (pair ? 2 : x + 1); ++y)
+                        if (nseg) wait(&B->q_empty[y], (nseg - 1) & 1);
                 }
-            } else {
-                tile(false, 0);
-                if (n > 1) tile(false, 1);
-                if (n == 1) tile(true, 0);
-                load_q();
-                for (int j = n == 1 ? 1 : 0; j < n && ok; ++j) {
-                    tile(true, j);
-                    if (j + 2 < n) tile(false, j + 2);
+                // a wait ran out: the copies in flight must land before the CTA leaves its shared memory
+                if (lane == 0 && !wait.ok) {
+                    for (uint32_t pos = issued > depth ? issued - depth : 0; pos < issued; ++pos)
+                        mbar_wait(&B->kv_full[first_stage(x) + pos % depth], (pos / depth) & 1, err);
+                    for (int y = x; y < (pair ? 2 : x + 1); ++y)
+                        if (nseg) mbar_wait(&B->q_full[y], (nseg - 1) & 1, err);
                 }
             }
-            if (lane == 0) a.W.slot_bad[s.slot] = bad;
-            ring += 2 * n;
-        }
-        // a wait ran out: the copies in flight must land before the CTA leaves its shared memory
-        if (lane == 0 && !ok) {
-            const uint32_t lo = issued > C::STAGES ? issued - C::STAGES : 0;
-            for (uint32_t pos = lo; pos < issued; ++pos) mbar_wait(&B->kv_full[pos % C::STAGES], (pos / C::STAGES) & 1, err);
-            if (nseg) mbar_wait(&B->q_full, (nseg - 1) & 1, err);
-        }
-    } else if (warp == 8) {
-        // ------------------------------------------------------------ MMA
-        if (lane == 0) {
-            constexpr uint32_t ID_S = idesc_bf16(VT, KT), ID_O = idesc_bf16(VT, HD, true);
-            uint32_t nseg = 0, np[2] = {0, 0}, no[2] = {0, 0};
-            while (ok && walk.next(P, h, base, ibase, s)) {
-                const int n = s.t1 - s.t0;
-                const int nx[2] = {s.pair ? n : (n + 1) / 2, s.pair ? n : n / 2};
-                int s_left = nx[0] + nx[1];
-                auto issue_s = [&](int x, int k) {
-                    const uint32_t pos = ring + k_seq(s.pair, s.pair ? k : 2 * k + x);
-                    const int st = pos % C::STAGES;
-                    if (!wait(&B->kv_full[st], (pos / C::STAGES) & 1)) return;
-                    fence_after();
-                    const uint32_t qa = q_at + (s.pair ? x : 0) * C::TILE, kb = ring_at + st * C::TILE;
-                    const uint32_t d = tmem + 128 * x;
-#pragma unroll
-                    for (int kk = 0; kk < HD / 16; ++kk)
-                        umma_bf16(d, sw128_desc(qa + (kk >> 2) * C::REG + (kk & 3) * 32),
-                                  sw128_desc(kb + (kk >> 2) * C::REG + (kk & 3) * 32), ID_S, kk > 0 ? 1u : 0u);
-                    umma_commit(&B->s_full[x]);
-                    if (!s.pair || x == 1) umma_commit(&B->kv_empty[st]);
-                    if (--s_left == 0) umma_commit(&B->q_empty);
-                };
-                wait(&B->q_full, nseg & 1);
-                ++nseg;
-                for (int x = 0; x < 2; ++x)
-                    if (ok && nx[x] > 0) issue_s(x, 0);
-                for (int k = 0; k < nx[0] && ok; ++k)
-                    for (int x = 0; x < 2; ++x) {
-                        if (!ok || k >= nx[x]) continue;
-                        if (k == 0) {
-                            wait(&B->o_empty[x], (no[x] & 1) ^ 1);  // the segment before has been read out
-                            ++no[x];
-                        }
-                        wait(&B->p_full[x], np[x] & 1);
-                        ++np[x];
-                        const uint32_t pos = ring + v_seq(s.pair, s.pair ? k : 2 * k + x, n);
-                        const int st = pos % C::STAGES;
-                        wait(&B->kv_full[st], (pos / C::STAGES) & 1);
-                        if (!ok) break;
+        } else if (warp >= 8) {
+            // ------------------------------------------------------------ MMA
+            const int x = warp - 8;
+            if (lane == 0) {
+                constexpr uint32_t ID_S = idesc_bf16(VT, KT), ID_O = idesc_bf16(VT, HD, true);
+                const uint32_t tS = tmem + 128 * x, tO = tmem + 256 + HD * x;
+                const uint64_t q_desc = sw128_desc(q_at + x * C::Q_TILE);
+                const uint64_t k_desc = sw128_desc(ring_at), v_desc = sw128_desc(ring_at, C::KV_REG, 1024);
+                Walk walk(P, h, line, worker(x));
+                uint32_t nseg = 0, nt = 0;  // segments and tiles before this one
+                while (wait.ok && walk.next(P, h, base, ibase, s)) {
+                    const int n = s.t1 - s.t0;
+                    auto issue_s = [&](int j) {
+                        const uint32_t pos = ring + k_seq(j), st = first_stage(x) + pos % depth;
+                        if (!wait(&B->kv_full[st], (pos / depth) & 1)) return;
                         fence_after();
-                        const uint32_t vb = ring_at + st * C::TILE;
-                        const uint32_t d = tmem + 256 + HD * x, pa = tmem + 128 * x;
+                        const uint64_t kd = k_desc + st * (C::TILE >> 4);
+                        const uint32_t buf = (nt + j) & 1;
+#pragma unroll
+                        for (int kk = 0; kk < HD / 16; ++kk)
+                            umma_bf16(tS + 64 * buf, q_desc + (((kk >> 2) * C::Q_REG + (kk & 3) * 32) >> 4),
+                                      kd + (((kk >> 2) * C::KV_REG + (kk & 3) * 32) >> 4), ID_S, kk > 0 ? 1u : 0u);
+                        umma_commit(&B->s_full[x][buf]);
+                        umma_commit(&B->kv_empty[st]);
+                        if (j == n - 1) umma_commit(&B->q_empty[x]);
+                    };
+                    if (!wait(&B->q_full[x], nseg & 1)) break;
+                    issue_s(0);
+                    if (n > 1) issue_s(1);
+                    if (!wait(&B->o_empty[x], (nseg & 1) ^ 1)) break;  // the segment before has been read out
+#pragma unroll 1
+                    for (int j = 0; j < n; ++j) {
+                        const uint32_t pos = ring + v_seq(j, n), st = first_stage(x) + pos % depth;
+                        const uint32_t buf = (nt + j) & 1;
+                        wait(&B->kv_full[st], (pos / depth) & 1);
+                        if (!wait(&B->p_full[x][buf], ((nt + j) >> 1) & 1)) break;
+                        fence_after();
+                        const uint64_t vd = v_desc + st * (C::TILE >> 4);
 #pragma unroll
                         for (int kk = 0; kk < KT / 16; ++kk)
-                            umma_bf16_ts(d, pa + 8 * kk, sw128_desc(vb + kk * 2048, C::REG, 1024), ID_O,
-                                         (k > 0 || kk > 0) ? 1u : 0u);
-                        if (!s.pair || x == 1) umma_commit(&B->kv_empty[st]);
-                        if (k == nx[x] - 1) umma_commit(&B->o_full[x]);
-                        else issue_s(x, k + 1);
+                            umma_bf16_ts(tO, tS + 64 * buf + 8 * kk, vd + ((kk * 2048) >> 4), ID_O, (j > 0 || kk > 0) ? 1u : 0u);
+                        umma_commit(&B->o_done[x][buf]);
+                        umma_commit(&B->kv_empty[st]);
+                        if (j + 2 < n) issue_s(j + 2);
                     }
-                ring += 2 * n;
-            }
-        }
-    } else {
-        // ------------------------------------------------------------ softmax
-        const int x = warp >> 2, v = tid & 127, quad = warp & 3;
-        const uint32_t tl = tmem + ((uint32_t)(32 * quad) << 16);
-        const uint32_t tS = tl + 128 * x, tO = tl + 256 + HD * x;
-        uint32_t ns = 0, no = 0;
-        while (ok && walk.next(P, h, base, ibase, s)) {
-            const int n = s.t1 - s.t0;
-            const int nx = s.pair ? n : (n + 1 - x) / 2;
-            const int r0 = s.pair ? x * P.RH : 0;  // this stream's rows of the item
-            const int nv = min(P.RH, s.nrows - r0) * P.g;
-            int lim = 0;
-            if (v < nv) lim = (s.seq >= 0 && P.causal) ? max(s.lim0 + r0 + v / P.g, 0) : s.keys;
-            const bool live_warp = 32 * quad < nv;
-            float m_run = -INFINITY, l_run = 0.f;
-            for (int k = 0; k < nx; ++k) {
-                const int j = s.pair ? k : 2 * k + x, k0 = (s.t0 + j) * KT;
-                if (!wait(&B->s_full[x], ns & 1)) break;
-                ++ns;
-                fence_after();
-                if (k0 + KT > s.keys && (!s.pair || x == 0)) {
-                    // the list ends inside this tile: zero the rows of V behind it (a page's unused slots
-                    // may hold anything, and 0 * NaN is NaN).  In a pair A's P V comes first.
-                    const uint32_t pos = ring + v_seq(s.pair, j, n);
-                    const int st = pos % C::STAGES;
-                    if (!wait(&B->kv_full[st], (pos / C::STAGES) & 1)) break;
-                    const int first = s.keys - k0;
-                    uint8_t* V = sm + 2 * C::TILE + st * C::TILE;
-                    for (int i = first * 8 + v; i < KT * 8; i += 128)
-#pragma unroll
-                        for (int c = 0; c < C::HALVES; ++c)
-                            *reinterpret_cast<uint4*>(V + c * C::REG + i * 16) = make_uint4(0u, 0u, 0u, 0u);
-                    fence_proxy_async();
+                    ++nseg;
+                    nt += n;
+                    ring += 2 * n;
                 }
-                if (live_warp) {
-                    uint32_t sr[128];
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) tmem_ld32_issue(tS + 32 * c, sr + 32 * c);
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) tmem_ld32_wait(sr + 32 * c);
-                    if (__any_sync(0xffffffffu, k0 + KT > lim)) {
-                        const int left = lim - k0;
-#pragma unroll
-                        for (int c = 0; c < 128; ++c)
-                            if (c >= left) sr[c] = 0xFF800000u;  // -inf
-                    }
-                    float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-                    for (int c = 0; c < 128; ++c) mx4[c & 3] = fmaxf(mx4[c & 3], __uint_as_float(sr[c]));
-                    const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * a.scale_log2;
-                    const float m_new = mx > m_run + 8.f ? mx : m_run;
-                    if (k > 0 && __any_sync(0xffffffffu, m_new != m_run)) {
-                        const float alpha = m_run == -INFINITY ? 0.f : ex2(m_run - m_new);
-                        l_run *= alpha;
+                if (!wait.ok) {  // products that were issued must have ended before their accumulators are freed
+                    umma_commit(&B->drain[x]);
+                    mbar_wait(&B->drain[x], 0, err);
+                }
+            }
+            __syncwarp();
+        } else {
+            // ------------------------------------------------------------ softmax
+            const int x = warp >> 2, v = tid & 127, quad = warp & 3;
+            const uint32_t tl = tmem + ((uint32_t)(32 * quad) << 16);
+            const uint32_t tO = tl + 256 + HD * x;
+            const uint64_t scale2 = pack2(a.scale_log2, a.scale_log2);
+            uint32_t nt = 0;  // tiles before this segment
+            Walk walk(P, h, line, worker(x));
+            while (wait.ok && walk.next(P, h, base, ibase, s)) {
+                const int n = s.t1 - s.t0;
+                const int r0 = pair ? x * P.RH : 0;  // this stream's rows of the item
+                const int nv = min(P.RH, s.nrows - r0) * P.g;
+                int lim = 0;
+                if (v < nv) lim = s.causal ? max(s.lim0 + r0 + v / P.g, 0) : s.keys;
+                const bool live_warp = 32 * quad < nv;
+                float m_run = -INFINITY, l_run = 0.f;
 #pragma unroll 1
-                        for (int c = 0; c < HD; c += 32) {
-                            uint32_t o[32];
-                            tmem_ld32_issue(tO + c, o);
-                            tmem_ld32_wait(o);
+                for (int j = 0; j < n; ++j) {
+                    const int k0 = (s.t0 + j) * KT;
+                    const uint32_t buf = (nt + j) & 1, phase = ((nt + j) >> 1) & 1;
+                    const uint32_t tS = tl + 128 * x + 64 * buf;
+                    if (!wait(&B->s_full[x][buf], phase)) break;
+                    fence_after();
+                    if (k0 + KT > s.keys) {
+                        // the list ends inside this tile: zero the rows of V behind it (a page's unused slots may
+                        // hold anything, and 0 * NaN is NaN); on line 0 both streams do, each before its own P V
+                        const uint32_t pos = ring + v_seq(j, n), st = first_stage(x) + pos % depth;
+                        if (!wait(&B->kv_full[st], (pos / depth) & 1)) break;
+                        uint8_t* V = sm + C::RING_AT + st * C::TILE;
+                        for (int i = (s.keys - k0) * 8 + v; i < KT * 8; i += 128)
 #pragma unroll
-                            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
-                            tmem_st32(tO + c, o);
-                        }
+                            for (int c = 0; c < C::HALVES; ++c)
+                                *reinterpret_cast<uint4*>(V + c * C::KV_REG + i * 16) = make_uint4(0u, 0u, 0u, 0u);
+                        fence_proxy_async();
                     }
-                    m_run = m_new;
-                    const float neg = m_run == -INFINITY ? 0.f : -m_run;
-                    float sum[4] = {0.f, 0.f, 0.f, 0.f};
+                    if (live_warp) {
+                        uint32_t sr[KT];
+                        tmem_ld32_issue(tS, sr);
+                        tmem_ld32_issue(tS + 32, sr + 32);
+                        tmem_ld32_wait(sr);
+                        tmem_ld32_wait(sr + 32);
+                        if (__any_sync(0xffffffffu, k0 + KT > lim)) {
+                            const int left = lim - k0;
 #pragma unroll
-                    for (int c = 0; c < 2; ++c) {
-                        uint32_t pk[32];
-#pragma unroll
-                        for (int e = 0; e < 32; ++e) {
-                            const float p0 = ex2(fmaf(__uint_as_float(sr[64 * c + 2 * e]), a.scale_log2, neg));
-                            const float p1 = ex2(fmaf(__uint_as_float(sr[64 * c + 2 * e + 1]), a.scale_log2, neg));
-                            sum[(2 * e) & 3] += p0;
-                            sum[(2 * e + 1) & 3] += p1;
-                            pk[e] = pack2_bf16(p0, p1);
+                            for (int c = 0; c < KT; ++c)
+                                if (c >= left) sr[c] = 0xFF800000u;  // -inf
                         }
-                        tmem_st32(tS + 32 * c, pk);
+                        float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                        for (int c = 0; c < KT; c += 2)
+                            mx4[(c >> 1) & 3] =
+                                fmaxf(fmaxf(mx4[(c >> 1) & 3], __uint_as_float(sr[c])), __uint_as_float(sr[c + 1]));
+                        const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * a.scale_log2;
+                        const float m_new = mx > m_run + 8.f ? mx : m_run;
+                        if (j > 0 && __any_sync(0xffffffffu, m_new != m_run)) {
+                            // O holds the tiles before this one once the product of the last of them has completed
+                            if (!wait(&B->o_done[x][buf ^ 1], ((nt + j - 1) >> 1) & 1)) break;
+                            fence_after();
+                            const float alpha = m_run == -INFINITY ? 0.f : ex2(m_run - m_new);
+                            l_run *= alpha;
+#pragma unroll 1
+                            for (int c = 0; c < HD; c += 32) {
+                                uint32_t o[32];
+                                tmem_ld32_issue(tO + c, o);
+                                tmem_ld32_wait(o);
+#pragma unroll
+                                for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+                                tmem_st32(tO + c, o);
+                            }
+                        }
+                        m_run = m_new;
+                        const float neg = m_run == -INFINITY ? 0.f : -m_run;
+                        const uint64_t neg2 = pack2(neg, neg);
+                        uint64_t sum2[2] = {0ull, 0ull};
+                        uint32_t pk[KT / 2];
+#pragma unroll
+                        for (int e = 0; e < KT / 2; ++e) {
+                            float x0, x1;
+                            unpack2(fma2(pack2(__uint_as_float(sr[2 * e]), __uint_as_float(sr[2 * e + 1])), scale2, neg2), x0, x1);
+                            x0 = ex2(x0);
+                            x1 = ex2(x1);
+                            sum2[e & 1] = add2(sum2[e & 1], pack2(x0, x1));
+                            pk[e] = pack2_bf16(x0, x1);
+                        }
+                        tmem_st32(tS, pk);
+                        float s0, s1;
+                        unpack2(add2(sum2[0], sum2[1]), s0, s1);
+                        l_run += s0 + s1;
+                        tmem_st_wait();
                     }
-                    l_run += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-                    tmem_st_wait();
+                    fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&B->p_full[x][buf]);
                 }
-                fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&B->p_full[x]);
-            }
-            if (nx > 0 && wait(&B->o_full[x], no & 1)) {
-                ++no;
+                const uint32_t last = nt + n - 1;
+                if (!wait(&B->o_done[x][last & 1], (last >> 1) & 1)) break;
                 fence_after();
                 if (live_warp) {
-                    const size_t slot = (size_t)s.slot * 2 + x;
-                    if (v < nv) a.W.ml[slot * VT + v] = make_float2(m_run, l_run);
-                    float* o = a.W.o + slot * VT * HD + (size_t)v * 8;
+                    const size_t blk = s.block + (pair ? x : 0);
+                    if (v < nv) a.W.ml[blk * VT + v] = make_float2(m_run, l_run);
+                    float* o = a.W.o + blk * VT * HD + (size_t)v * 8;
 #pragma unroll 1
                     for (int c = 0; c < HD; c += 32) {
                         uint32_t r[32];
@@ -458,25 +514,16 @@ __global__ void __launch_bounds__(NTHR, 1)
                 fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&B->o_empty[x]);
+                nt += n;
+                ring += 2 * n;
             }
-            ring += 2 * n;
         }
+        __syncwarp();
     }
-    __syncwarp();
     fence_before();
     __syncthreads();
     if (warp == 8) {
         fence_after();
-        if (B->fail) {
-            // products that were issued must have ended before their accumulators are freed
-            if (lane == 0) {
-                mbar_init(&B->q_full, 1);
-                mbar_fence_init();
-                umma_commit(&B->q_full);
-                mbar_wait(&B->q_full, 0, err);
-            }
-            __syncwarp();
-        }
         tmem_dealloc(tmem, 512);
     }
 }
@@ -526,7 +573,7 @@ bool run(const Launch& L, const Shape& P, const Work& W, const dflash_shared_pre
         const cuuint32_t box[2] = {64, 64};
         if (!encode(&mk, 2, a.k_cache, dims, strides, box) || !encode(&mv, 2, a.v_cache, dims, strides, box)) return false;
     }
-    const size_t smem = C::SMEM_TILES + sizeof(Bars) + (size_t)P.batch * 8 + 1024;
+    const size_t smem = C::SMEM_TILES + sizeof(Bars) + 3 * MAX_BATCH * 4 + 1024;
     if (cudaFuncSetAttribute(shared_tc_kernel<HD>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
         return false;
     launch_k(L, shared_tc_kernel<HD>, dim3(P.n_cta), dim3(NTHR), smem, 1, t, mq, mk, mv);

@@ -7,7 +7,7 @@
 // written, 16 B a row; at the largest session (1024 requests) that is 1.6 MB, far
 // below a launch's latency, so the kernel is bound by its chain of dependent
 // steps: lengths -> scan -> entries.  Hence one launch: one cluster of 1..8 CTAs,
-// every CTA scans the whole batch itself (at most 4096 lengths, from L2) and then
+// every CTA scans the whole batch itself (at most 2048 lengths, from L2) and then
 // writes its share of the table and the rows; a second launch or a grid-wide
 // exchange of the scan would each cost more than the repeated scan.  The cluster's
 // only exchange is a barrier before `used` is overwritten (it may be in place).
@@ -184,7 +184,7 @@ using namespace dfl;
 extern "C" dflash_status dflash_kv_tables(const dflash_kv_tables_args* p, void* cuda_stream) {
     if (!p) return fail("kv_tables: args is NULL");
     const dflash_kv_tables_args& a = *p;
-    if (a.batch < 1 || a.batch > DFLASH_OPS_MAX_BATCH) return fail("kv_tables: batch outside [1, 4096]");
+    if (a.batch < 1 || a.batch > DFLASH_OPS_MAX_BATCH) return fail("kv_tables: batch outside [1, 2048]");
     if (a.width < 0 || a.rows < 0 || a.rows >= (1 << 30) || a.n_free < 0)
         return fail("kv_tables: width, rows and n_free must not be negative (rows below 2^30)");
     if (a.width > (1 << 24) || a.base_pos < 0 || a.base_pos > (1 << 30))

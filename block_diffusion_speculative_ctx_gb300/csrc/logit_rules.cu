@@ -204,7 +204,7 @@ dflash_status check_logits(const dflash_logits_args& a, const char** why) {
         return DFLASH_E_INVAL;
     };
     if (a.dtype != DFLASH_DTYPE_F32 && a.dtype != DFLASH_DTYPE_BF16) return bad("process_logits: dtype must be F32 or BF16");
-    if (a.batch < 1 || a.batch > DFLASH_OPS_MAX_BATCH) return bad("process_logits: batch outside [1, 4096]");
+    if (a.batch < 1 || a.batch > DFLASH_OPS_MAX_BATCH) return bad("process_logits: batch outside [1, 2048]");
     if (a.rows_per_seq < 1 || a.rows_per_seq > 32) return bad("process_logits: rows_per_seq outside [1, 32]");
     if (a.vocab < 1 || a.vocab > (1 << 30)) return bad("process_logits: vocab outside [1, 2^30]");
     if (!a.logits || !a.out) return bad("process_logits: logits or out is NULL");

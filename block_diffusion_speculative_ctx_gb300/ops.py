@@ -18,7 +18,7 @@ import torch
 from . import DFLASH_DTYPE_BF16, DFLASH_DTYPE_F32, DFLASH_OK, DFlashError, dflash_last_error, load
 
 _P, _I32, _I64, _F = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_float
-OPS_MAX_BATCH = 4096
+OPS_MAX_BATCH = 2048
 PAGE_TOKENS = 64
 _DTYPES = {torch.float32: DFLASH_DTYPE_F32, torch.bfloat16: DFLASH_DTYPE_BF16}
 

@@ -424,7 +424,7 @@ dflash_status dflash_head_argmax_noalloc(int32_t dtype, const float* x, const fl
  * KV pages hold 64 tokens: a cache is [pages][H_kv][64][hd] (one layer), page
  * p token t of KV head h at ((p * H_kv + h) * 64 + t) * hd.  Sequences per
  * call: at most DFLASH_OPS_MAX_BATCH. */
-enum { DFLASH_OPS_MAX_BATCH = 4096 };
+enum { DFLASH_OPS_MAX_BATCH = 2048 };
 
 /* Page tables and slot maps of a batch from its request lengths.  Request s
  * has kv_lens[s] tokens cached and appends new_lens[s].  With

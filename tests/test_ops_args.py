@@ -60,7 +60,7 @@ def rules(**kw):
 
 
 @pytest.mark.parametrize("kw", [
-    dict(batch=0), dict(batch=4097), dict(width=-1), dict(rows=-1), dict(rows=1 << 30), dict(n_free=-1), dict(width=1 << 25),
+    dict(batch=0), dict(batch=2049), dict(width=-1), dict(rows=-1), dict(rows=1 << 30), dict(n_free=-1), dict(width=1 << 25),
     dict(base_pos=-1), dict(kv_lens=None), dict(new_lens=None), dict(q_start=None), dict(status=None), dict(table=None),
     dict(ld_table=3), dict(ld_out=3), dict(used=None), dict(used_out=None), dict(table_out=None),
     dict(table_out=P, ld_out=5)])
@@ -71,7 +71,7 @@ def test_kv_tables_refuses(lib, kw):
 
 @pytest.mark.parametrize("kw", [
     dict(dtype=2), dict(head_dim=96), dict(n_heads=9), dict(n_kv_heads=0), dict(n_heads=130, ld_q=130 * 128, ld_out=130 * 128),
-    dict(n_heads=2048, n_kv_heads=2048, ld_q=1 << 18, ld_out=1 << 18), dict(batch=0), dict(batch=4097), dict(rows=-1),
+    dict(n_heads=2048, n_kv_heads=2048, ld_q=1 << 18, ld_out=1 << 18), dict(batch=0), dict(batch=2049), dict(rows=-1),
     dict(rows=(1 << 20) + 1), dict(n_pages=0), dict(n_pages=1 << 24), dict(prefix_len=-1), dict(width=-1), dict(scale=0.0),
     dict(scale=-1.0), dict(scale=float("nan")), dict(scale=float("inf")), dict(q=None), dict(k_cache=None), dict(v_cache=None),
     dict(kv_lens=None), dict(q_start=None), dict(table=None), dict(prefix_pages=None), dict(out=None), dict(workspace=None),
@@ -89,7 +89,7 @@ def test_shared_prefix_workspace_sizes(lib):
 
 
 @pytest.mark.parametrize("kw", [
-    dict(dtype=2), dict(batch=0), dict(batch=4097), dict(rows_per_seq=0), dict(rows_per_seq=33), dict(vocab=0),
+    dict(dtype=2), dict(batch=0), dict(batch=2049), dict(rows_per_seq=0), dict(rows_per_seq=33), dict(vocab=0),
     dict(logits=None), dict(out=None), dict(logits=P + 2), dict(ld_logits=999), dict(ld_out=999), dict(ld_out=1004),
     dict(hist_lens=None), dict(prompt_lens=None), dict(ld_hist=7), dict(history=None), dict(bias_values=None),
     dict(mask_index=None), dict(ld_mask=31)])

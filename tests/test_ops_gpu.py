@@ -69,7 +69,7 @@ def check_tables(got, want, check_table=True):
 @pytest.mark.parametrize("batch,kv_hi,new_hi,width_extra,slack,base,rows_extra", [
     (1, 0, 1, 0, 0, 0, 0), (1, 0, 0, 3, 2, 0, 4), (3, 130, 70, 1, 0, 17, 0), (32, 2303, 1, 4, 9, 8192, 3),
     (33, 64, 64, 0, 1, 0, 1), (511, 90, 3, 2, 0, 0, 0), (513, 300, 40, 1, 7, 64, 100), (1024, 2303, 16, 5, 0, 8192, 0),
-    (4096, 130, 20, 0, 3, 1, 5)])
+    (2048, 130, 20, 0, 3, 1, 5)])
 def test_kv_tables(batch, kv_hi, new_hi, width_extra, slack, base, rows_extra, in_place):
     kv, new, table, free, rows, scratch, base = tables_case(batch, kv_hi, new_hi, width_extra, slack, batch, base, rows_extra)
     if batch == 1 and new_hi:
