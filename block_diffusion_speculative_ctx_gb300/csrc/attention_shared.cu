@@ -80,9 +80,11 @@ __global__ void __launch_bounds__(128) shared_simple_kernel(dflash_shared_prefix
 
 // Merge of the partial results: out = sum_i 2^(m_i - M) o_i / sum_i 2^(m_i - M) l_i over the segments that
 // hold the row's query vectors, prefix and own, in plan order (one fixed order: the same bits every run).
-// A CTA takes one row and one KV head, so its chain of dependent loads is: lengths -> (max, sum) of every
-// segment, one a thread -> outputs, read by groups of threads that take every G-th segment, a thread 8 head
-// dimensions of one query vector (whole 32-byte sectors).  Bytes: 4 hd + 8 per vector and segment, from L2.
+// A warp takes one row and one KV head: lanes find the row's sequence and work out the workers of its items
+// (a segment a lane), then take 8 head dimensions of one query vector each (whole 32-byte sectors) and
+// stream the segments through, four in flight.  NW > 1: the warps of a CTA share one (row, KV head), each
+// taking every NW-th segment, for calls of few rows (whose prefix is split the most).  Bytes: 4 hd + 8 per
+// vector and segment, from L2; a row's chain of dependent loads is what a small call waits for.
 struct MergeArgs {
     sp::Shape P;
     sp::Work W;
@@ -91,9 +93,7 @@ struct MergeArgs {
     long long ld_out;
 };
 
-constexpr int MNT = 256;
-constexpr int MSEG = 3 * 160;  // segments of one row: at most one per worker of line 0 and of line 1
-constexpr int MHEADS = 8;      // query heads at a time
+constexpr int MWARPS = 8;
 
 template <typename T>
 __device__ __forceinline__ void store8(T* d, const float (&x)[8]);
@@ -108,146 +108,128 @@ __device__ __forceinline__ void store8<bf16>(bf16* d, const float (&x)[8]) {
         make_uint4(tc::pack2_bf16(x[0], x[1]), tc::pack2_bf16(x[2], x[3]), tc::pack2_bf16(x[4], x[5]), tc::pack2_bf16(x[6], x[7]));
 }
 
-template <typename T>
-__global__ void __launch_bounds__(MNT) merge_kernel(MergeArgs a) {
-    using namespace sp;
-    __shared__ int seq_s, bad_s, n_s;
-    __shared__ uint32_t blk_s[MSEG];               // block and stream of each segment
-    __shared__ float wgt_s[MHEADS][MSEG];          // its weight 2^(m - M) for each query head
-    __shared__ float inv_s[MHEADS];
-    __shared__ float acc_s[MNT][8];
-    const Shape& P = a.P;
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int r = blockIdx.x, kvh = blockIdx.y;
-    if (tid == 0) {
-        seq_s = -1;
-        bad_s = 0;
+// (M, l, o) of two disjoint sets of keys joined into the first.
+struct Part {
+    float M = -INFINITY, l = 0.f, o[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    __device__ __forceinline__ void join(float m, float s, const float4& x, const float4& y) {
+        const float mn = fmaxf(M, m);
+        const float e0 = M == -INFINITY ? 0.f : exp2f(M - mn), e1 = m == -INFINITY ? 0.f : exp2f(m - mn);
+        M = mn;
+        l = l * e0 + s * e1;
+        const float v[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+#pragma unroll
+        for (int e = 0; e < 8; ++e) o[e] = o[e] * e0 + v[e] * e1;
     }
-    __syncthreads();
+};
+
+// A row's item on its line: the blocks of its segments (first, step, count) and the row's first vector in
+// its stream.
+struct Item {
+    int block = 0, step = 1, count = 0, v = 0;
+};
+__device__ __forceinline__ Item item_of(const sp::Shape& P, const sp::Head& h, int line, uint32_t at, int id, int n_eff, int rl) {
+    Item i;
+    const uint32_t part = h.part[line], t0 = at + (uint32_t)P.lead[line];
+    const int c0 = (int)(t0 / part), x = rl >= P.RH ? 1 : 0;
+    i.count = (int)((t0 + (uint32_t)n_eff - 1u) / part) - c0 + 1;
+    i.step = line == 0 ? 2 : 1;
+    i.block = (int)sp::block_of(P, h, line, id, c0) + x;
+    i.v = (rl - x * P.RH) * P.g;
+    return i;
+}
+
+template <typename T, int NW>
+__global__ void __launch_bounds__(32 * MWARPS, 4) merge_kernel(MergeArgs a) {
+    using namespace sp;
+    const Shape& P = a.P;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int r = NW > 1 ? blockIdx.x : blockIdx.x * MWARPS + warp, kvh = blockIdx.y;
+    __shared__ Part part_s[NW > 1 ? NW : 1][32];
     pdl_wait();
     pdl_trigger();
+    if (r >= P.rows) return;  // (NW > 1: the whole CTA)
     const Head h = *a.W.head;
-    for (int c = tid; c < P.n_cta; c += MNT)
-        if (a.W.err[c]) bad_s = 1;
-    for (int s = tid; s < P.batch; s += MNT)
-        if (P.q_start[s] <= r && r < P.q_start[s + 1]) seq_s = s;
-    __syncthreads();
-    bool bad = h.bad || bad_s;
-    const int seq = seq_s;
-    if (!bad && seq < 0) return;  // a row of no sequence
-    // the row's items: [0] prefix, [1] own
-    int line[2] = {0, 0}, n[2] = {0, 0}, n_eff[2] = {0, 0}, id[2] = {0, 0}, c0[2] = {0, 0}, nc[2] = {0, 0}, rl[2] = {0, 0};
-    uint32_t at[2] = {0u, 0u};
-    if (!bad) {
-        const int start = P.q_start[seq];
-        const Seq q = seq_of(P, start, P.q_start[seq + 1], P.kv_lens[seq]);
-        if (q.kv < 0 || q.kv > (long long)64 * P.width) bad = true;
-        if (P.npt) {
-            const int RT = P.row_tile(h.pl), rt = (r - h.r_begin) / RT;
-            line[0] = h.pl;
-            n[0] = n_eff[0] = P.npt;
-            id[0] = kvh * h.nqt + rt;
-            at[0] = (uint32_t)id[0] * (P.lead[h.pl] + (uint32_t)P.npt * P.w);
-            rl[0] = (r - h.r_begin) - rt * RT;
-        }
-        if (q.tiles && !bad) {
-            const int RT = P.row_tile(q.line), j = r - start, gi = j / RT, k = kvh * q.groups + gi;
-            line[1] = q.line;
-            n[1] = q.tiles;
-            n_eff[1] = seen_tiles(P, q, min(q.m, (gi + 1) * RT));
-            id[1] = (h.pl == q.line ? h.n_prefix : 0) + (int)a.W.ibase[seq] + k;
-            at[1] = a.W.base[seq] + (uint32_t)k * (P.lead[q.line] + (uint32_t)q.tiles * P.w);
-            rl[1] = j - gi * RT;
-        }
+    uint32_t err = 0;
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
-            if (n_eff[i]) {
-                const uint32_t W = h.W[line[i]], t0 = at[i] + P.lead[line[i]];
-                c0[i] = owner(W, t0, P.workers(line[i]));
-                nc[i] = owner(W, t0 + (uint32_t)(n_eff[i] - 1) * P.w, P.workers(line[i])) - c0[i] + 1;
-            }
-    }
-    const int cand = nc[0] + nc[1];  // workers that may hold a segment, in plan order
-    auto vec = [&](int i) { return rl[i] % P.RH * P.g; };  // first of the row's vectors in its stream
-    if (tid == 0) n_s = cand;
-    for (int k = tid; k < cand; k += MNT) {
-        const int i = k < nc[0] ? 0 : 1, c = i ? c0[1] + k - nc[0] : c0[0] + k;
-        const uint32_t W = h.W[line[i]];
-        int t0, t1;
-        cut(max(at[i], part_begin(W, c, P.workers(line[i]))), part_begin(W, c + 1, P.workers(line[i])), at[i],
-            P.lead[line[i]], P.w, n[i], t0, t1);
-        uint32_t blk = 0xFFFFFFFFu;  // no tile of the item in this worker's part
-        if (t0 < min(t1, n_eff[i])) {
-            blk = block_of(P, h, line[i], id[i], c) + (uint32_t)(rl[i] / P.RH);
-            if (a.W.block_bad[blk]) bad_s = 1;
+    for (int i = 0; i < 5; ++i)
+        if (lane + 32 * i < P.n_cta) err |= a.W.err[lane + 32 * i];
+    const bool live = r >= h.r_begin && r < h.r_end;
+    bool bad = __any_sync(0xffffffffu, h.bad || err != 0);
+    if (!bad && !live) return;  // a row of no sequence
+    Item pre, own;
+    if (!bad) {
+        const Rec rec = a.W.rec[a.W.row_seq[r]];
+        const Seq q = seq_of(P, rec.start, rec.start + rec.m, rec.kv);
+        bad = rec.kv < 0 || rec.kv > (long long)64 * P.width;
+        if (P.npt) {
+            const int RT = P.row_tile(h.pl), rt = (r - h.r_begin) / RT, id = kvh * h.nqt + rt;
+            pre = item_of(P, h, h.pl, (uint32_t)id * (uint32_t)(P.lead[h.pl] + P.npt), id, P.npt, r - h.r_begin - rt * RT);
         }
-        blk_s[k] = blk;
-    }
-    __syncthreads();
-    bad = bad || bad_s;
-
-    const int chunks = P.hd / 8;
-    for (int h0 = 0; h0 < P.g; h0 += MHEADS) {
-        const int nh = min(MHEADS, P.g - h0);
-        // weights: a warp takes a head
-        for (int hh = warp; hh < nh; hh += MNT / 32) {
-            float M = -INFINITY;
-            for (int k = lane; k < cand; k += 32) {
-                float m = -INFINITY;
-                if (blk_s[k] != 0xFFFFFFFFu) m = a.W.ml[(size_t)blk_s[k] * P.VT + vec(k < nc[0] ? 0 : 1) + h0 + hh].x;
-                wgt_s[hh][k] = m;
-                M = fmaxf(M, m);
-            }
-            M = warp_max(M);
-            float l = 0.f;
-            for (int k = lane; k < cand; k += 32) {
-                const float m = wgt_s[hh][k], w = m == -INFINITY ? 0.f : exp2f(m - M);
-                if (w != 0.f) l += w * a.W.ml[(size_t)blk_s[k] * P.VT + vec(k < nc[0] ? 0 : 1) + h0 + hh].y;
-                wgt_s[hh][k] = w;
-            }
-            l = warp_sum(l);
-            if (lane == 0) {
-                inv_s[hh] = bad ? NAN : l > 0.f ? 1.f / l : 0.f;
-                if (a.lse)
-                    a.lse[(long long)r * P.H + kvh * P.g + h0 + hh] =
-                        bad ? NAN : l > 0.f ? (M + log2f(l)) * 0.6931471805599453f : -INFINITY;
-            }
+        if (q.tiles) {
+            const int RT = P.row_tile(q.line), j = r - rec.start, gi = j / RT, k = kvh * q.groups + gi;
+            const int n_eff = seen_tiles(P, q, min(q.m, (gi + 1) * RT));
+            if (n_eff)
+                own = item_of(P, h, q.line, rec.base + (uint32_t)k * (uint32_t)(P.lead[q.line] + q.tiles),
+                              (h.pl == q.line ? h.n_prefix : 0) + (int)rec.ibase + k, n_eff, j - gi * RT);
         }
-        __syncthreads();
-        const int part = nh * chunks, G = MNT / part, grp = tid / part, e = tid - grp * part;
-        const int hh = e / chunks, c8 = e - hh * chunks;
-        float o[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-        if (grp < G) {
-#pragma unroll 4
-            for (int k = grp; k < cand; k += G) {
-                const float w = wgt_s[hh][k];
-                if (w != 0.f) {
-                    const float* src = a.W.o + (size_t)blk_s[k] * P.VT * P.hd +
-                                       ((size_t)c8 * P.VT + vec(k < nc[0] ? 0 : 1) + h0 + hh) * 8;
-                    const float4 x = *reinterpret_cast<const float4*>(src), y = *reinterpret_cast<const float4*>(src + 4);
-                    o[0] += w * x.x;
-                    o[1] += w * x.y;
-                    o[2] += w * x.z;
-                    o[3] += w * x.w;
-                    o[4] += w * y.x;
-                    o[5] += w * y.y;
-                    o[6] += w * y.z;
-                    o[7] += w * y.w;
+    }
+    const int count = pre.count + own.count;
+    const int w0 = NW > 1 ? warp : 0;
+    const int chunks = P.hd / 8, elems = P.g * chunks;
+#pragma unroll 1
+    for (int e0 = 0; e0 < elems; e0 += 32) {
+        const int e = min(e0 + lane, elems - 1), hh = e / chunks, c8 = e - hh * chunks;
+        Part acc;
+        uint32_t bb = 0;
+#pragma unroll 1
+        for (int k0 = w0; k0 < count; k0 += 2 * NW) {
+            float2 ml[2];
+            float4 x[2], y[2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int k = k0 + i * NW;
+                ml[i] = make_float2(-INFINITY, 0.f);
+                x[i] = y[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (k < count) {
+                    const bool p = k < pre.count;
+                    const size_t blk = p ? pre.block + k * pre.step : own.block + (k - pre.count) * own.step;
+                    const int v = (p ? pre.v : own.v) + hh;
+                    ml[i] = a.W.ml[blk * P.VT + v];
+                    const float* src = a.W.o + ((blk * chunks + c8) * P.VT + v) * 8;
+                    x[i] = *reinterpret_cast<const float4*>(src);
+                    y[i] = *reinterpret_cast<const float4*>(src + 4);
+                    bb |= a.W.block_bad[blk];
                 }
             }
 #pragma unroll
-            for (int i = 0; i < 8; ++i) acc_s[tid][i] = o[i];
+            for (int i = 0; i < 2; ++i) acc.join(ml[i].x, ml[i].y, x[i], y[i]);
         }
-        __syncthreads();
-        if (grp == 0) {
-            for (int q = 1; q < G; ++q)
-#pragma unroll
-                for (int i = 0; i < 8; ++i) o[i] += acc_s[tid + q * part][i];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) o[i] = bad ? NAN : o[i] * inv_s[hh];
-            store8<T>(reinterpret_cast<T*>(a.out) + (long long)r * a.ld_out + (long long)(kvh * P.g + h0 + hh) * P.hd + c8 * 8, o);
+        if (bb) acc.M = NAN;  // (a NaN maximum makes the whole row NaN below)
+        if (NW > 1) {
+            part_s[w0][lane] = acc;
+            __syncthreads();
+            if (w0 == 0)
+#pragma unroll 1
+                for (int q = 1; q < NW; ++q) {
+                    const Part p = part_s[q][lane];
+                    if (isnan(p.M) || isnan(acc.M)) acc.M = NAN;
+                    else
+                        acc.join(p.M, p.l, make_float4(p.o[0], p.o[1], p.o[2], p.o[3]),
+                                 make_float4(p.o[4], p.o[5], p.o[6], p.o[7]));
+                }
         }
-        __syncthreads();
+        if (w0 == 0 && e0 + lane < elems) {
+            const int head = kvh * P.g + hh;
+            const bool nan = bad || isnan(acc.M);
+            const float inv = acc.l == 0.f ? 0.f : 1.f / acc.l;  // (no key: 0; a NaN sum stays NaN)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) acc.o[i] = nan ? NAN : acc.o[i] * inv;
+            store8<T>(reinterpret_cast<T*>(a.out) + (long long)r * a.ld_out + (long long)head * P.hd + c8 * 8, acc.o);
+            if (a.lse && c8 == 0)
+                a.lse[(long long)r * P.H + head] =
+                    nan ? NAN : acc.l == 0.f ? -INFINITY : (acc.M + log2f(acc.l)) * 0.6931471805599453f;
+        }
+        if (NW > 1) __syncthreads();
     }
 }
 
@@ -273,7 +255,6 @@ sp::Shape sizes_of(int H, int Hkv, int hd, int batch, int rows) {
     P.rows = rows;
     P.n_cta = CTAS;
     // an item's fixed cost: two tiles on line 0, three on line 1
-    P.w = 1;
     P.lead[0] = 2;
     P.lead[1] = 3;
     return P;
@@ -309,7 +290,9 @@ bool shared_prefix_attention(const Launch& L, const dflash_shared_prefix_args& a
     // the merge starts as the main kernel's CTAs leave
     Launch after = L;
     after.pdl = true;
-    launch_k(after, merge_kernel<bf16>, dim3(a.rows, a.n_kv_heads), dim3(MNT), 0, 1, m);
+    // rows of one stream: the prefix is split over nearly every worker of its line, else over a few
+    if (a.rows <= P.RH) launch_k(after, merge_kernel<bf16, MWARPS>, dim3(a.rows, a.n_kv_heads), dim3(32 * MWARPS), 0, 1, m);
+    else launch_k(after, merge_kernel<bf16, 1>, dim3((a.rows + MWARPS - 1) / MWARPS, a.n_kv_heads), dim3(32 * MWARPS), 0, 1, m);
     return true;
 }
 

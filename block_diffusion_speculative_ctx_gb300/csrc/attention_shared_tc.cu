@@ -55,19 +55,21 @@ struct Cfg {
     static constexpr int SMEM_TILES = RING_AT + STAGES * TILE;
 };
 
+constexpr int SEGS = 4;
 struct LineBars {
     uint64_t kv_full[16], kv_empty[16];
     uint64_t q_full[2], q_empty[2];
     uint64_t s_full[2][2], p_full[2][2], o_done[2][2];  // per stream and S buffer
     uint64_t o_empty[2];
     uint64_t drain[2];
+    uint64_t seg_full[2][SEGS], seg_empty[2][SEGS];
 };
 struct Bars {
     LineBars line[2];
+    Seg seg[2][SEGS];  // segments handed from a load warp to the other roles
     uint32_t tmem;
-    int flag;
     int fail;
-    uint32_t ws[4 * NTHR / 32];
+    PlanMem<NTHR> plan;
 };
 
 struct TcArgs {
@@ -212,6 +214,10 @@ __global__ void __launch_bounds__(NTHR, 1)
                 }
                 mbar_init(&B->o_empty[x], 4);
                 mbar_init(&B->drain[x], 1);
+                for (int i = 0; i < SEGS; ++i) {
+                    mbar_init(&B->seg_full[x][i], 1);
+                    mbar_init(&B->seg_empty[x][i], line == 0 ? 10 : 5);  // MMA and softmax warps that read it
+                }
             }
         }
         mbar_fence_init();
@@ -227,19 +233,24 @@ __global__ void __launch_bounds__(NTHR, 1)
     if (tid == 0) a.W.err[cta] = 0u;
     Head h;
     fence_before();
-    make_plan<NTHR>(P, base, ibase, bars->ws, &bars->flag, h);  // (its barriers order the setup above)
+    make_plan<NTHR>(P, base, ibase, &bars->plan, h);  // (its barriers order the setup above)
     fence_after();
     const uint32_t tmem = bars->tmem;
-    if (cta == 0) {
-        if (tid == 0) *a.W.head = h;
-        for (int s = tid; s < P.batch; s += NTHR) {
-            a.W.base[s] = base[(P.q_start[s + 1] - P.q_start[s] > P.RH ? 0 : MAX_BATCH) + s];
-            a.W.ibase[s] = ibase[s];
+    // for the merge kernel: the head, and a warp per sequence its record and its rows' map
+    if (cta == 0 && tid == 0) *a.W.head = h;
+    if (!h.bad)
+#pragma unroll 1
+        for (int q = warp * P.n_cta + cta; q < P.batch; q += P.n_cta * (NTHR / 32)) {
+            const int start = P.q_start[q], m = P.q_start[q + 1] - start;
+            if (lane == 0) {
+                Rec r = {start, m, P.kv_lens[q], base[(m > P.RH ? 0 : MAX_BATCH) + q], ibase[q], {0u, 0u, 0u}};
+                a.W.rec[q] = r;
+            }
+#pragma unroll 1
+            for (int i = lane; i < m; i += 32) a.W.row_seq[start + i] = q;
         }
-    }
     uint32_t* err = &a.W.err[cta];
     Waiter wait{err, &bars->fail};
-    Seg s;
 
 #pragma unroll 1
     for (int turn = 0; turn < 2; ++turn) {
@@ -253,6 +264,16 @@ __global__ void __launch_bounds__(NTHR, 1)
         auto worker = [&](int x) { return pair ? cta : 2 * cta + x; };
         auto first_stage = [&](int x) { return pair ? 0u : (uint32_t)x * (C::STAGES / 2); };
         uint32_t ring = 0;  // ring position of the segment's first tile
+        // the i-th segment, read by a whole warp (or its one issuing lane)
+        auto take = [&](int x, uint32_t i, bool all, Seg& s) {
+            const int rx = pair ? 0 : x, slot = i % SEGS;
+            s.n = 0;
+            if (!wait(&B->seg_full[rx][slot], (i / SEGS) & 1)) return false;
+            s = bars->seg[rx][slot];
+            if (all) __syncwarp();
+            if (!all || lane == 0) mbar_arrive(&B->seg_empty[rx][slot]);
+            return s.n > 0;
+        };
 
         if (warp >= 10) {
             // ------------------------------------------------------------ loads
@@ -260,9 +281,21 @@ __global__ void __launch_bounds__(NTHR, 1)
             if (!pair || x == 0) {
                 Walk walk(P, h, line, worker(x));
                 uint32_t nseg = 0, issued = 0;
-                while (wait.ok && walk.next(P, h, base, ibase, s)) {
-                    const int n = s.t1 - s.t0;
-                    const int* pages = s.seq < 0 ? P.prefix_pages : P.table + (long long)s.seq * P.ld_table;
+                int kvh, row0, seq;
+                Seg s;
+#pragma unroll 1
+                while (wait.ok) {
+                    if (!walk.next(P, h, base, ibase, s, kvh, row0, seq)) s.n = 0;
+                    if (lane == 0) {
+                        const int slot = nseg % SEGS;
+                        if (wait(&B->seg_empty[x][slot], ((nseg / SEGS) & 1) ^ 1)) {
+                            bars->seg[x][slot] = s;
+                            mbar_arrive(&B->seg_full[x][slot]);
+                        }
+                    }
+                    const int n = s.n;
+                    if (n == 0) break;
+                    const int* pages = seq < 0 ? P.prefix_pages : P.table + (long long)seq * P.ld_table;
                     const int n_pages = (s.keys + 63) >> 6;  // valid entries of `pages`
                     const int oob = P.n_pages * P.Hkv * 64;  // a row behind the cache: reads as zeros
                     // page numbers 32 at a time, one a lane (K tiles run up to two ahead of V tiles: a window
@@ -277,13 +310,13 @@ __global__ void __launch_bounds__(NTHR, 1)
                                 pg[kv] = pages[first + lane];
                                 if (pg[kv] < 0 || pg[kv] >= P.n_pages) {
                                     pg[kv] = -1;
-                                    bad |= first + lane < s.t1;
+                                    bad |= first + lane < s.t0 + n;
                                 }
                             }
                         }
                         const int p = __shfl_sync(0xffffffffu, pg[kv], first - w0[kv]);
                         if (lane == 0) {
-                            const int row = p < 0 ? oob : (p * P.Hkv + s.kvh) * 64;
+                            const int row = p < 0 ? oob : (p * P.Hkv + kvh) * 64;
                             const uint32_t pos = ring + (kv ? v_seq(j, n) : k_seq(j)), st = first_stage(x) + pos % depth;
                             if (wait(&B->kv_empty[st], ((pos / depth) & 1) ^ 1)) {
                                 mbar_arrive_expect_tx(&B->kv_full[st], C::TILE);
@@ -309,7 +342,7 @@ __global__ void __launch_bounds__(NTHR, 1)
 #pragma unroll
                                         for (int c = 0; c < C::HALVES; ++c)
                                             tma_load_3d(q_at + y * C::Q_TILE + c * C::Q_REG, &mq, &B->q_full[y], 64 * c,
-                                                        s.kvh * P.g, s.row0 + (pair ? y * P.RH : 0));
+                                                        kvh * P.g, row0 + (pair ? y * P.RH : 0));
                                     }
                             }
                             if (j + 2 < n) tile(0, j + 2);
@@ -348,10 +381,11 @@ __global__ void __launch_bounds__(NTHR, 1)
                 const uint32_t tS = tmem + 128 * x, tO = tmem + 256 + HD * x;
                 const uint64_t q_desc = sw128_desc(q_at + x * C::Q_TILE);
                 const uint64_t k_desc = sw128_desc(ring_at), v_desc = sw128_desc(ring_at, C::KV_REG, 1024);
-                Walk walk(P, h, line, worker(x));
                 uint32_t nseg = 0, nt = 0;  // segments and tiles before this one
-                while (wait.ok && walk.next(P, h, base, ibase, s)) {
-                    const int n = s.t1 - s.t0;
+                Seg s;
+#pragma unroll 1
+                while (take(x, nseg, false, s)) {
+                    const int n = s.n;
                     auto issue_s = [&](int j) {
                         const uint32_t pos = ring + k_seq(j), st = first_stage(x) + pos % depth;
                         if (!wait(&B->kv_full[st], (pos / depth) & 1)) return;
@@ -367,22 +401,23 @@ __global__ void __launch_bounds__(NTHR, 1)
                         if (j == n - 1) umma_commit(&B->q_empty[x]);
                     };
                     if (!wait(&B->q_full[x], nseg & 1)) break;
-                    issue_s(0);
-                    if (n > 1) issue_s(1);
-                    if (!wait(&B->o_empty[x], (nseg & 1) ^ 1)) break;  // the segment before has been read out
 #pragma unroll 1
-                    for (int j = 0; j < n; ++j) {
-                        const uint32_t pos = ring + v_seq(j, n), st = first_stage(x) + pos % depth;
-                        const uint32_t buf = (nt + j) & 1;
-                        wait(&B->kv_full[st], (pos / depth) & 1);
-                        if (!wait(&B->p_full[x][buf], ((nt + j) >> 1) & 1)) break;
-                        fence_after();
-                        const uint64_t vd = v_desc + st * (C::TILE >> 4);
+                    for (int j = -2; j < n && wait.ok; ++j) {
+                        if (j >= 0) {
+                            const uint32_t pos = ring + v_seq(j, n), st = first_stage(x) + pos % depth;
+                            const uint32_t buf = (nt + j) & 1;
+                            wait(&B->kv_full[st], (pos / depth) & 1);
+                            if (j == 0) wait(&B->o_empty[x], (nseg & 1) ^ 1);  // the segment before has been read out
+                            if (!wait(&B->p_full[x][buf], ((nt + j) >> 1) & 1)) break;
+                            fence_after();
+                            const uint64_t vd = v_desc + st * (C::TILE >> 4);
 #pragma unroll
-                        for (int kk = 0; kk < KT / 16; ++kk)
-                            umma_bf16_ts(tO, tS + 64 * buf + 8 * kk, vd + ((kk * 2048) >> 4), ID_O, (j > 0 || kk > 0) ? 1u : 0u);
-                        umma_commit(&B->o_done[x][buf]);
-                        umma_commit(&B->kv_empty[st]);
+                            for (int kk = 0; kk < KT / 16; ++kk)
+                                umma_bf16_ts(tO, tS + 64 * buf + 8 * kk, vd + ((kk * 2048) >> 4), ID_O,
+                                             (j > 0 || kk > 0) ? 1u : 0u);
+                            umma_commit(&B->o_done[x][buf]);
+                            umma_commit(&B->kv_empty[st]);
+                        }
                         if (j + 2 < n) issue_s(j + 2);
                     }
                     ++nseg;
@@ -402,13 +437,16 @@ __global__ void __launch_bounds__(NTHR, 1)
             const uint32_t tO = tl + 256 + HD * x;
             const uint64_t scale2 = pack2(a.scale_log2, a.scale_log2);
             uint32_t nt = 0;  // tiles before this segment
-            Walk walk(P, h, line, worker(x));
-            while (wait.ok && walk.next(P, h, base, ibase, s)) {
-                const int n = s.t1 - s.t0;
+            uint32_t nseg = 0;
+            Seg s;
+#pragma unroll 1
+            while (take(x, nseg, true, s)) {
+                ++nseg;
+                const int n = s.n;
                 const int r0 = pair ? x * P.RH : 0;  // this stream's rows of the item
                 const int nv = min(P.RH, s.nrows - r0) * P.g;
                 int lim = 0;
-                if (v < nv) lim = s.causal ? max(s.lim0 + r0 + v / P.g, 0) : s.keys;
+                if (v < nv) lim = max(s.lim0 + s.step * (r0 + v / P.g), 0);
                 const bool live_warp = 32 * quad < nv;
                 float m_run = -INFINITY, l_run = 0.f;
 #pragma unroll 1

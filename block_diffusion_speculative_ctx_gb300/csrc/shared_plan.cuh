@@ -7,16 +7,15 @@
 // against the sequence's own keys).  A worker has VT vectors per stream; items
 // of more than one stream's rows (RH) go on line 0, whose workers are the CTAs
 // with both streams in step over the same tiles, the others on line 1, whose
-// workers are the single streams.  A line strings its items up, prefix first,
-// each with one weight w per tile of KT keys after a lead weight for its fixed
-// cost (queries in, partial result out).  The line [0, W) is cut into equal
-// parts, one per worker: a tile belongs to the worker in whose part its first
-// unit lies.  So every worker gets the same work whatever the lengths are, and
-// an item is split over no more workers than its weight takes.  A worker's run
-// of tiles inside one item is a segment; its partial result (per vector:
-// maximum, sum, unnormalised output) goes to a block of the workspace numbered
-// by item + worker: along a line neither ever falls and one of them rises at
-// each segment, so blocks are unique.
+// workers are the single streams.  A line strings its items up, prefix first:
+// an item takes a lead (its fixed cost: queries in, partial result out) and one
+// unit per tile of KT keys that it has.  The line is cut into parts of equal
+// length, one per worker, so every worker gets the same work whatever the
+// lengths are, and an item is split over no more workers than its length takes.
+// A worker's run of tiles inside one item is a segment; its partial result (per
+// vector: maximum, sum, unnormalised output) goes to a block of the workspace
+// numbered by item + worker: along a line neither ever falls and one of them
+// rises at each segment, so blocks are unique, and an item's are consecutive.
 #pragma once
 
 #include "ops.h"
@@ -34,7 +33,7 @@ struct Shape {
     int batch, rows, width, prefix_len, causal, n_pages;
     int npt;       // prefix tiles
     int n_cta;
-    int w, lead[2];  // weights of a tile and of an item's fixed cost (per line)
+    int lead[2];   // an item's fixed cost in tiles (per line)
     long long ld_table;
     const int *prefix_pages, *table, *kv_lens, *q_start;
     __host__ __device__ int row_tile(int line) const { return line == 0 ? 2 * RH : RH; }
@@ -43,8 +42,9 @@ struct Shape {
 
 // Cut of the lines, written by CTA 0 for the merge kernel.
 struct Head {
-    uint32_t W[2];     // total weights
-    uint32_t CP;       // weight of the prefix items, at the start of line pl
+    uint32_t W[2];     // length
+    uint32_t part[2];  // length of a worker's part: ceil(W / workers)
+    uint32_t CP;       // length of the prefix items, at the start of line pl
     uint32_t items0;   // items on line 0
     int pl;            // line of the prefix items
     int n_prefix;      // prefix items
@@ -53,11 +53,18 @@ struct Head {
     int bad;           // q_start is not a list of rows, or a line is too long
 };
 
+// A sequence as the merge kernel reads it: its rows, keys, and its own items' first unit and number on
+// their line.
+struct Rec {
+    int start, m, kv;
+    uint32_t base, ibase, pad[3];
+};
+
 struct Work {
     Head* head;
     uint32_t* err;        // [n_cta]: a bounded wait ran out
-    uint32_t* base;       // [batch]: first unit of the sequence's own items on its line
-    uint32_t* ibase;      // [batch]: first of the sequence's own items on its line
+    Rec* rec;             // [batch]
+    int* row_seq;         // [rows]: of the rows in [r_begin, r_end)
     uint32_t* block_bad;  // [blocks]: a page of the segment lies outside the cache
     float2* ml;           // [blocks][VT]
     float* o;             // [blocks][hd / 8][VT][8]
@@ -82,8 +89,8 @@ inline size_t layout(char* p, const Shape& P, Work* w) {
     Work x;
     x.head = (Head*)take(sizeof(Head));
     x.err = (uint32_t*)take((size_t)P.n_cta * 4);
-    x.base = (uint32_t*)take((size_t)P.batch * 4);
-    x.ibase = (uint32_t*)take((size_t)P.batch * 4);
+    x.rec = (Rec*)take((size_t)P.batch * sizeof(Rec));
+    x.row_seq = (int*)take((size_t)P.rows * 4);
     x.block_bad = (uint32_t*)take(blocks * 4);
     x.ml = (float2*)take(blocks * P.VT * 8);
     x.o = (float*)take(blocks * P.VT * P.hd * 4);
@@ -91,20 +98,7 @@ inline size_t layout(char* p, const Shape& P, Work* w) {
     return at;
 }
 
-__device__ __forceinline__ uint32_t part_begin(uint32_t W, int c, int n) {
-    return (uint32_t)((unsigned long long)W * (unsigned)c / (unsigned)n);
-}
-// The worker whose part holds unit x < W: the last c with floor(c W / n) <= x.
-__device__ __forceinline__ int owner(uint32_t W, uint32_t x, int n) {
-    return (int)((((unsigned long long)x + 1) * (unsigned)n + W - 1) / W) - 1;
-}
 __device__ __forceinline__ int cdiv(int a, int b) { return (a + b - 1) / b; }
-// Tiles [t0, t1) of an item of n tiles at unit b that lie in the part [lo, hi), lo >= b.
-__device__ __forceinline__ void cut(uint32_t lo, uint32_t hi, uint32_t b, uint32_t lead, uint32_t w, int n, int& t0, int& t1) {
-    const uint32_t x = lo - b, y = hi > b ? hi - b : 0u;
-    t0 = x <= lead ? 0 : (int)((x - lead + w - 1) / w);
-    t1 = y <= lead ? 0 : (int)min((uint32_t)n, (y - lead + w - 1) / w);
-}
 // First block of worker c's segment of item `id`.
 __device__ __forceinline__ uint32_t block_of(const Shape& P, const Head& h, int line, int id, int c) {
     return line == 0 ? 2u * (uint32_t)(id + c) : 2u * (h.items0 + (uint32_t)P.n_cta) + (uint32_t)(id + c);
@@ -129,14 +123,14 @@ __device__ __forceinline__ int seen_tiles(const Shape& P, const Seq& q, int r1) 
     return P.causal ? min(q.tiles, cdiv(max(q.kv - q.m + r1, 0), P.KT)) : q.tiles;
 }
 
+// What the roles need to know of a segment; n == 0: no more.
 struct Seg {
-    int seq;          // -1: prefix
-    int kvh;
-    int row0, nrows;  // rows of q
-    int t0, t1;       // tiles
+    int n;            // tiles
+    int t0;           // the first of them
     int keys;         // keys of the list (prefix_len or kv)
-    int lim0;         // keys seen by row row0 (causal own keys: one more per row)
-    bool causal;
+    int lim0;         // keys seen by the item's first row
+    int step;         // and by each row more (causal own keys: 1, else 0)
+    int nrows;        // rows of the item
     uint32_t block;
 };
 
@@ -145,28 +139,32 @@ struct Walk {
     uint32_t p, p1;
     int line, c;
     __device__ __forceinline__ Walk(const Shape& P, const Head& h, int ln, int worker)
-        : p(part_begin(h.W[ln], worker, P.workers(ln))), p1(part_begin(h.W[ln], worker + 1, P.workers(ln))), line(ln), c(worker) {}
+        : p(min(h.W[ln], (uint32_t)worker * h.part[ln])), p1(min(h.W[ln], p + h.part[ln])), line(ln), c(worker) {}
 
-    __device__ __forceinline__ bool next(const Shape& P, const Head& h, const uint32_t* base, const uint32_t* ibase, Seg& s) {
-        const uint32_t w = P.w, lead = P.lead[line];
+    // The next segment, its KV head, first row of q and sequence (-1: prefix).
+    __device__ __forceinline__ bool next(const Shape& P, const Head& h, const uint32_t* base, const uint32_t* ibase, Seg& s,
+                                         int& kvh, int& row0, int& seq) {
+        const uint32_t lead = P.lead[line];
         const int RT = P.row_tile(line);
         base += line * MAX_BATCH;
+#pragma unroll 1
         while (p < p1) {
             uint32_t b;
             int n, n_eff, id;
+            s.step = 0;
             if (h.pl == line && p < h.CP) {
-                const uint32_t per = lead + (uint32_t)P.npt * w;
+                const uint32_t per = lead + (uint32_t)P.npt;
                 id = (int)(p / per);
                 b = (uint32_t)id * per;
                 n = n_eff = P.npt;
-                s.seq = -1;
-                s.kvh = id / h.nqt;
-                s.row0 = h.r_begin + id % h.nqt * RT;
-                s.nrows = min(RT, h.r_end - s.row0);
+                seq = -1;
+                kvh = id / h.nqt;
+                row0 = h.r_begin + (id - kvh * h.nqt) * RT;
+                s.nrows = min(RT, h.r_end - row0);
                 s.keys = s.lim0 = P.prefix_len;
-                s.causal = false;
             } else {
                 int lo = 0, hi = P.batch;  // the last sequence with base <= p has items here (base rises over it alone)
+#pragma unroll 1
                 while (hi - lo > 1) {
                     const int mid = (lo + hi) >> 1;
                     if (base[mid] <= p) lo = mid;
@@ -174,42 +172,50 @@ struct Walk {
                 }
                 const int start = P.q_start[lo];
                 const Seq q = seq_of(P, start, P.q_start[lo + 1], P.kv_lens[lo]);
-                const uint32_t per = lead + (uint32_t)q.tiles * w;
+                const uint32_t per = lead + (uint32_t)q.tiles;
                 const int k = (int)((p - base[lo]) / per);
                 b = base[lo] + (uint32_t)k * per;
                 n = q.tiles;
-                const int gi = k % q.groups;
                 id = (h.pl == line ? h.n_prefix : 0) + (int)ibase[lo] + k;
-                s.seq = lo;
-                s.kvh = k / q.groups;
-                s.row0 = start + gi * RT;
-                s.nrows = min(RT, q.m - gi * RT);
-                s.keys = q.kv;
-                s.causal = P.causal != 0;
-                s.lim0 = P.causal ? q.kv - q.m + gi * RT + 1 : q.kv;
-                n_eff = seen_tiles(P, q, gi * RT + s.nrows);
+                seq = lo;
+                kvh = k / q.groups;
+                const int r = (k - kvh * q.groups) * RT;
+                row0 = start + r;
+                s.nrows = min(RT, q.m - r);
+                s.keys = s.lim0 = q.kv;
+                if (P.causal) {
+                    s.lim0 = q.kv - q.m + r + 1;
+                    s.step = 1;
+                }
+                n_eff = seen_tiles(P, q, r + s.nrows);
             }
-            int t1;
-            cut(p, p1, b, lead, w, n, s.t0, t1);
-            s.t1 = min(t1, n_eff);
+            // tile t is unit b + lead + t
+            s.t0 = max((int)(p - b) - (int)lead, 0);
+            s.n = min(n_eff, (int)min(p1 - b, lead + (uint32_t)n) - (int)lead) - s.t0;
             s.block = block_of(P, h, line, id, c);
-            p = min(p1, b + lead + (uint32_t)n * w);
-            if (s.t0 < s.t1) return true;
+            p = min(p1, b + lead + (uint32_t)n);
+            if (s.n > 0) return true;
         }
         return false;
     }
 };
 
 // Scan of the batch by every thread of the CTA (NTHR threads, all call it): fills base ([2][MAX_BATCH]:
-// per line, the exclusive sums of the own items' weights, from the prefix items' end), ibase ([batch]: of
-// the counts on the sequence's line) and the head.  ws: 4 * NTHR / 32 words, flag: one word (shared
-// memory).  Ends with a barrier.
+// per line, the exclusive sums of the own items' lengths, from the prefix items' end), ibase ([batch]: of
+// the counts on the sequence's line) and the head.  Ends with a barrier.
 template <int NTHR>
-__device__ void make_plan(const Shape& P, uint32_t* base, uint32_t* ibase, uint32_t* ws, int* flag, Head& h) {
+struct PlanMem {
+    uint32_t ws[NTHR / 32][4];
+    unsigned long long sum[2];  // in 64 bits: a line of 2^31 units or more is refused
+    int bad;
+};
+template <int NTHR>
+__device__ __forceinline__ void make_plan(const Shape& P, uint32_t* base, uint32_t* ibase, PlanMem<NTHR>* m, Head& h) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    constexpr unsigned long long MOST = 1ull << 31;  // sums saturate here: the call is bad then
-    if (tid == 0) *flag = 0;
-    __syncthreads();
+    if (tid == 0) {
+        m->bad = 0;
+        m->sum[0] = m->sum[1] = 0;
+    }
     h.r_begin = P.q_start[0];
     h.r_end = P.q_start[P.batch];
     int bad = 0;
@@ -221,18 +227,15 @@ __device__ void make_plan(const Shape& P, uint32_t* base, uint32_t* ibase, uint3
     h.pl = live > P.RH ? 0 : 1;
     h.nqt = cdiv(live, P.row_tile(h.pl));
     h.n_prefix = P.npt ? h.nqt * P.Hkv : 0;
-    unsigned long long cp = (unsigned long long)h.n_prefix * (P.lead[h.pl] + (unsigned long long)P.npt * P.w);
-    if (cp >= MOST) {
-        bad = 1;
-        cp = 0;
-    }
+    const unsigned long long cp = (unsigned long long)h.n_prefix * (unsigned)(P.lead[h.pl] + P.npt);
     h.CP = (uint32_t)cp;
-    unsigned long long carry[2] = {h.pl == 0 ? cp : 0ull, h.pl == 1 ? cp : 0ull};
-    uint32_t icarry[2] = {0u, 0u};
+    uint32_t carry[4] = {h.pl == 0 ? h.CP : 0u, h.pl == 1 ? h.CP : 0u, 0u, 0u};  // lengths, item counts
+    __syncthreads();
+    if (tid == 0) atomicAdd(&m->sum[h.pl], cp);
+#pragma unroll 1
     for (int s0 = 0; s0 < P.batch; s0 += NTHR) {
         const int s = s0 + tid;
-        unsigned long long c[2] = {0ull, 0ull};
-        uint32_t it[2] = {0u, 0u};
+        uint32_t v[4] = {0u, 0u, 0u, 0u};
         int line = 0;
         if (s < P.batch) {
             const int a = P.q_start[s], b = P.q_start[s + 1];
@@ -241,62 +244,49 @@ __device__ void make_plan(const Shape& P, uint32_t* base, uint32_t* ibase, uint3
             } else {
                 const Seq q = seq_of(P, a, b, P.kv_lens[s]);
                 line = q.line;
-                const uint32_t items = (uint32_t)(q.groups * P.Hkv);
-                const unsigned long long cost = (unsigned long long)items * (P.lead[line] + (unsigned long long)q.tiles * P.w);
-                if (cost >= MOST) bad = 1;
-                else {
-                    c[line] = cost;
-                    it[line] = items;
-                }
+                const uint32_t items = (uint32_t)(q.groups * P.Hkv), per = (uint32_t)(P.lead[line] + q.tiles);
+                if (items) atomicAdd(&m->sum[line], (unsigned long long)items * per);
+                v[line] = items * per;
+                v[2 + line] = items;
             }
         }
-        unsigned long long ci[2];
-        uint32_t ii[2];
+        uint32_t own[4] = {v[0], v[1], v[2], v[3]};
+#pragma unroll 1
+        for (int o = 1; o < 32; o <<= 1)
 #pragma unroll
-        for (int l = 0; l < 2; ++l) {
-            ci[l] = c[l];
-            ii[l] = it[l];
+            for (int i = 0; i < 4; ++i) {
+                const uint32_t y = __shfl_up_sync(0xffffffffu, v[i], o);
+                if (lane >= o) v[i] += y;
+            }
+        if (lane == 31)
 #pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const unsigned long long x = __shfl_up_sync(0xffffffffu, ci[l], o);
-                const uint32_t y = __shfl_up_sync(0xffffffffu, ii[l], o);
-                if (lane >= o) {
-                    ci[l] = min(ci[l] + x, MOST);
-                    ii[l] += y;
-                }
-            }
-            if (lane == 31) {
-                ws[4 * warp + 2 * l] = (uint32_t)ci[l];
-                ws[4 * warp + 2 * l + 1] = ii[l];
-            }
-        }
+            for (int i = 0; i < 4; ++i) m->ws[warp][i] = v[i];
         __syncthreads();
-        unsigned long long before[2] = {0ull, 0ull};
-        uint32_t ibefore[2] = {0u, 0u};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] -= own[i];
+#pragma unroll 1
         for (int w = 0; w < NTHR / 32; ++w)
 #pragma unroll
-            for (int l = 0; l < 2; ++l) {
-                if (w == warp) {
-                    before[l] = carry[l];
-                    ibefore[l] = icarry[l];
-                }
-                carry[l] = min(carry[l] + ws[4 * w + 2 * l], MOST);
-                icarry[l] += ws[4 * w + 2 * l + 1];
+            for (int i = 0; i < 4; ++i) {
+                if (w == warp) v[i] += carry[i];
+                carry[i] += m->ws[w][i];
             }
         if (s < P.batch) {
-#pragma unroll
-            for (int l = 0; l < 2; ++l) base[l * MAX_BATCH + s] = (uint32_t)min(before[l] + ci[l] - c[l], MOST);
-            ibase[s] = line == 0 ? ibefore[0] + ii[0] - it[0] : ibefore[1] + ii[1] - it[1];
+            base[s] = v[0];
+            base[MAX_BATCH + s] = v[1];
+            ibase[s] = v[2 + line];
         }
         __syncthreads();
     }
-    if (carry[0] >= MOST || carry[1] >= MOST) bad = 1;
-    if (bad) *flag = 1;
+    if (bad) m->bad = 1;
     __syncthreads();
-    h.bad = *flag;
-    h.W[0] = h.bad ? 0u : (uint32_t)carry[0];
-    h.W[1] = h.bad ? 0u : (uint32_t)carry[1];
-    h.items0 = icarry[0] + (h.pl == 0 ? (uint32_t)h.n_prefix : 0u);
+    h.bad = m->bad || m->sum[0] >> 31 || m->sum[1] >> 31;
+#pragma unroll
+    for (int l = 0; l < 2; ++l) {
+        h.W[l] = h.bad ? 0u : carry[l];
+        h.part[l] = max(1u, (h.W[l] + P.workers(l) - 1) / P.workers(l));
+    }
+    h.items0 = carry[2] + (h.pl == 0 ? (uint32_t)h.n_prefix : 0u);
 }
 
 }  // namespace sp

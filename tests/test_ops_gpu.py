@@ -313,9 +313,11 @@ def test_shared_prefix_attention_reports_bad_metadata(dtype, fault):
     if fault == "q_start":
         return  # only that nothing faults: which rows are whose is not defined any more
     assert out[2:4].isnan().all() and lse[2:4].isnan().all()
-    keep = [0, 1, 4, 5]
+    # the other rows as without the fault, within the bounds (not bit for bit: how the keys are split
+    # depends on every sequence's length, and each split adds its partial sums in another order)
     good = dfl().shared_prefix_attention(*attn_inputs(c))
-    assert torch.equal(out[keep], good[0][keep]) and torch.equal(lse[keep], good[1][keep])
+    out[2:4], lse[2:4] = good[0][2:4], good[1][2:4]
+    attn_check(c, (out, lse), True)
 
 
 def test_shared_prefix_attention_past_32_bit_offsets():
