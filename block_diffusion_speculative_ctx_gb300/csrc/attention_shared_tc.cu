@@ -23,9 +23,12 @@
 //   the softmax of tile j ends, so the softmax never waits for a product chain.
 //   Shared memory: Q_A, Q_B, a ring of K or V tiles (64 keys: one cache page),
 //   all 128-byte swizzled by TMA; page numbers come 32 at a time, one a lane.
-// An MMA warp issues S0 S1, then P V of tile j and S of tile j + 2 back to back:
-// the tensor cores execute one thread's products in order, so P V has read P
-// before the next S overwrites it.
+// An MMA warp issues S0, S1, then batches of P V of tile j and S of tile j + 2,
+// back to back: the tensor cores execute one thread's products in order, so P V
+// has read P before the next S overwrites it.  Each batch has one commit (a
+// commit holds the issue up by 100 cycles and more): it tells the softmax that S
+// has come and O is up to date, and the loads that the batch's V and K stages
+// are free.
 //
 // Every wait is bounded; one that runs out sets the CTA's error word (the merge
 // writes NaN), every role leaves, copies in flight are awaited (bounded).
@@ -51,15 +54,21 @@ struct Cfg {
     static constexpr int Q_REG = VT * 128, Q_TILE = HALVES * Q_REG;
     static constexpr int KV_REG = KT * 128, TILE = HALVES * KV_REG;
     static constexpr int STAGES = HD == 128 ? 8 : 16;  // 128 KB
+    static constexpr int LOG_STAGES = HD == 128 ? 3 : 4;
     static constexpr int RING_AT = 2 * Q_TILE;
     static constexpr int SMEM_TILES = RING_AT + STAGES * TILE;
 };
 
 constexpr int SEGS = 4;
+// A wait for batch i must not begin once batch i + DONE can have completed (the barrier's parity would be
+// that of before i).  The load warps wait the latest: a stage comes round after at most 16 ring positions, and
+// the shortest segments (one tile: two positions, three batches) put 24 batches on those.
+constexpr int DONE = 32;
 struct LineBars {
-    uint64_t kv_full[16], kv_empty[16];
+    uint64_t kv_full[16];
     uint64_t q_full[2], q_empty[2];
-    uint64_t s_full[2][2], p_full[2][2], o_done[2][2];  // per stream and S buffer
+    uint64_t p_full[2][2];     // per stream and S buffer
+    uint64_t done[2][DONE];    // per stream: its i-th batch of products, on barrier i % DONE
     uint64_t o_empty[2];
     uint64_t drain[2];
     uint64_t seg_full[2][SEGS], seg_empty[2][SEGS];
@@ -67,6 +76,7 @@ struct LineBars {
 struct Bars {
     LineBars line[2];
     Seg seg[2][SEGS];  // segments handed from a load warp to the other roles
+    uint32_t rel[16];  // batch that frees a stage (the load warps' own)
     uint32_t tmem;
     int fail;
     PlanMem<NTHR> plan;
@@ -166,12 +176,20 @@ struct Waiter {
     int* fail;
     bool ok = true;
     __device__ __forceinline__ bool operator()(uint64_t* bar, uint32_t parity) {
-        if (mbar_try_wait(bar, parity)) return ok;
-        if (ok && !mbar_wait(bar, parity, err)) {
+        if (!mbar_try_wait(bar, parity) && ok && !late(bar, parity)) {
             ok = false;
+            atomicOr(err, ERR_TIMEOUT);
             *(volatile int*)fail = 1;
         }
         return ok;
+    }
+    // about a second
+    static __device__ __noinline__ bool late(uint64_t* bar, uint32_t parity) {
+        for (uint32_t i = 0; i < (1u << 23); ++i) {
+            if (mbar_try_wait(bar, parity)) return true;
+            if (i >= 1024) __nanosleep(128);
+        }
+        return false;
     }
 };
 
@@ -200,18 +218,12 @@ __global__ void __launch_bounds__(NTHR, 1)
     if (tid == 0) {
         for (int line = 0; line < 2; ++line) {
             LineBars* B = &bars->line[line];
-            for (int i = 0; i < C::STAGES; ++i) {
-                mbar_init(&B->kv_full[i], 1);
-                mbar_init(&B->kv_empty[i], line == 0 ? 2 : 1);  // a line 0 stage is read by both streams
-            }
+            for (int i = 0; i < C::STAGES; ++i) mbar_init(&B->kv_full[i], 1);
             for (int x = 0; x < 2; ++x) {
                 mbar_init(&B->q_full[x], 1);
                 mbar_init(&B->q_empty[x], 1);
-                for (int b = 0; b < 2; ++b) {
-                    mbar_init(&B->s_full[x][b], 1);
-                    mbar_init(&B->p_full[x][b], 4);
-                    mbar_init(&B->o_done[x][b], 1);
-                }
+                for (int b = 0; b < 2; ++b) mbar_init(&B->p_full[x][b], 4);
+                for (int b = 0; b < DONE; ++b) mbar_init(&B->done[x][b], 1);
                 mbar_init(&B->o_empty[x], 4);
                 mbar_init(&B->drain[x], 1);
                 for (int i = 0; i < SEGS; ++i) {
@@ -260,7 +272,11 @@ __global__ void __launch_bounds__(NTHR, 1)
         if (turn == 1) __syncthreads();  // every role of the first line has ended: the ring and TMEM are free
         if (h.W[line] == 0 || bars->fail) continue;
         // ring of a stream: all stages, in step with the other stream (line 0), or half of them (line 1)
-        const uint32_t depth = pair ? C::STAGES : C::STAGES / 2;
+        const uint32_t depth = pair ? C::STAGES : C::STAGES / 2, dshift = pair ? C::LOG_STAGES : C::LOG_STAGES - 1;
+        auto stage_of = [&](uint32_t pos) { return pos & (depth - 1); };
+        auto phase_of = [&](uint32_t pos) { return (pos >> dshift) & 1u; };
+        // the i-th batch of stream x has completed (i counts through the line)
+        auto batch_done = [&](int x, uint32_t i) { return wait(&B->done[x][i % DONE], (i / DONE) & 1); };
         auto worker = [&](int x) { return pair ? cta : 2 * cta + x; };
         auto first_stage = [&](int x) { return pair ? 0u : (uint32_t)x * (C::STAGES / 2); };
         uint32_t ring = 0;  // ring position of the segment's first tile
@@ -280,7 +296,7 @@ __global__ void __launch_bounds__(NTHR, 1)
             const int x = warp - 10;
             if (!pair || x == 0) {
                 Walk walk(P, h, line, worker(x));
-                uint32_t nseg = 0, issued = 0;
+                uint32_t nseg = 0, issued = 0, nb = 0;  // nb: batches before this segment
                 int kvh, row0, seq;
                 Seg s;
 #pragma unroll 1
@@ -317,8 +333,9 @@ __global__ void __launch_bounds__(NTHR, 1)
                         const int p = __shfl_sync(0xffffffffu, pg[kv], first - w0[kv]);
                         if (lane == 0) {
                             const int row = p < 0 ? oob : (p * P.Hkv + kvh) * 64;
-                            const uint32_t pos = ring + (kv ? v_seq(j, n) : k_seq(j)), st = first_stage(x) + pos % depth;
-                            if (wait(&B->kv_empty[st], ((pos / depth) & 1) ^ 1)) {
+                            const uint32_t pos = ring + (kv ? v_seq(j, n) : k_seq(j)), st = first_stage(x) + stage_of(pos);
+                            if (pos < depth || (batch_done(x, bars->rel[st]) && (!pair || batch_done(1, bars->rel[st])))) {
+                                bars->rel[st] = nb + j + 2 * kv;
                                 mbar_arrive_expect_tx(&B->kv_full[st], C::TILE);
 #pragma unroll
                                 for (int c = 0; c < C::HALVES; ++c)
@@ -357,20 +374,22 @@ __global__ void __launch_bounds__(NTHR, 1)
                         if (pair) a.W.block_bad[s.block + 1] = bad;
                     }
                     ring += 2 * n;
+                    nb += n + 2;
                 }
                 if (lane == 0 && wait.ok) {
-                    // the last releases have arrived: nothing is under way to this line's barriers any more
-                    for (uint32_t pos = issued > depth ? issued - depth : 0; pos < issued; ++pos)
-                        wait(&B->kv_empty[first_stage(x) + pos % depth], (pos / depth) & 1);
+                    // the last commits have arrived: nothing is under way to this line's barriers any more
                     for (int y = x; y < (pair ? 2 : x + 1); ++y)
-                        if (nseg) wait(&B->q_empty[y], (nseg - 1) & 1);
+                        if (nseg) {
+                            for (uint32_t i = nb > DONE ? nb - DONE : 0; i < nb; ++i) batch_done(y, i);
+                            wait(&B->q_empty[y], (nseg - 1) & 1);
+                        }
                 }
                 // a wait ran out: the copies in flight must land before the CTA leaves its shared memory
                 if (lane == 0 && !wait.ok) {
                     for (uint32_t pos = issued > depth ? issued - depth : 0; pos < issued; ++pos)
-                        mbar_wait(&B->kv_full[first_stage(x) + pos % depth], (pos / depth) & 1, err);
+                        Waiter::late(&B->kv_full[first_stage(x) + stage_of(pos)], phase_of(pos));
                     for (int y = x; y < (pair ? 2 : x + 1); ++y)
-                        if (nseg) mbar_wait(&B->q_full[y], (nseg - 1) & 1, err);
+                        if (nseg) Waiter::late(&B->q_full[y], (nseg - 1) & 1);
                 }
             }
         } else if (warp >= 8) {
@@ -381,52 +400,50 @@ __global__ void __launch_bounds__(NTHR, 1)
                 const uint32_t tS = tmem + 128 * x, tO = tmem + 256 + HD * x;
                 const uint64_t q_desc = sw128_desc(q_at + x * C::Q_TILE);
                 const uint64_t k_desc = sw128_desc(ring_at), v_desc = sw128_desc(ring_at, C::KV_REG, 1024);
-                uint32_t nseg = 0, nt = 0;  // segments and tiles before this one
+                uint32_t nseg = 0, nt = 0, nb = 0;  // segments, tiles and batches before this one
                 Seg s;
 #pragma unroll 1
                 while (take(x, nseg, false, s)) {
                     const int n = s.n;
-                    auto issue_s = [&](int j) {
-                        const uint32_t pos = ring + k_seq(j), st = first_stage(x) + pos % depth;
-                        if (!wait(&B->kv_full[st], (pos / depth) & 1)) return;
-                        fence_after();
-                        const uint64_t kd = k_desc + st * (C::TILE >> 4);
-                        const uint32_t buf = (nt + j) & 1;
-#pragma unroll
-                        for (int kk = 0; kk < HD / 16; ++kk)
-                            umma_bf16(tS + 64 * buf, q_desc + (((kk >> 2) * C::Q_REG + (kk & 3) * 32) >> 4),
-                                      kd + (((kk >> 2) * C::KV_REG + (kk & 3) * 32) >> 4), ID_S, kk > 0 ? 1u : 0u);
-                        umma_commit(&B->s_full[x][buf]);
-                        umma_commit(&B->kv_empty[st]);
-                        if (j == n - 1) umma_commit(&B->q_empty[x]);
-                    };
                     if (!wait(&B->q_full[x], nseg & 1)) break;
 #pragma unroll 1
-                    for (int j = -2; j < n && wait.ok; ++j) {
+                    for (int j = -2; j < n; ++j) {
+                        // batch: P V of tile j, S of tile j + 2
+                        const uint32_t vpos = ring + v_seq(max(j, 0), n), vst = first_stage(x) + stage_of(vpos);
+                        const uint32_t kpos = ring + k_seq(j + 2), kst = first_stage(x) + stage_of(kpos);
+                        const uint32_t d = tS + 64 * ((nt + j) & 1);  // S buffer of both tiles
+                        if (j + 2 < n) wait(&B->kv_full[kst], phase_of(kpos));
                         if (j >= 0) {
-                            const uint32_t pos = ring + v_seq(j, n), st = first_stage(x) + pos % depth;
-                            const uint32_t buf = (nt + j) & 1;
-                            wait(&B->kv_full[st], (pos / depth) & 1);
+                            wait(&B->kv_full[vst], phase_of(vpos));
                             if (j == 0) wait(&B->o_empty[x], (nseg & 1) ^ 1);  // the segment before has been read out
-                            if (!wait(&B->p_full[x][buf], ((nt + j) >> 1) & 1)) break;
-                            fence_after();
-                            const uint64_t vd = v_desc + st * (C::TILE >> 4);
+                            wait(&B->p_full[x][(nt + j) & 1], ((nt + j) >> 1) & 1);
+                        }
+                        if (!wait.ok) break;
+                        fence_after();
+                        if (j >= 0) {
+                            const uint64_t vd = v_desc + vst * (C::TILE >> 4);
 #pragma unroll
                             for (int kk = 0; kk < KT / 16; ++kk)
-                                umma_bf16_ts(tO, tS + 64 * buf + 8 * kk, vd + ((kk * 2048) >> 4), ID_O,
-                                             (j > 0 || kk > 0) ? 1u : 0u);
-                            umma_commit(&B->o_done[x][buf]);
-                            umma_commit(&B->kv_empty[st]);
+                                umma_bf16_ts(tO, d + 8 * kk, vd + ((kk * 2048) >> 4), ID_O, (j > 0 || kk > 0) ? 1u : 0u);
                         }
-                        if (j + 2 < n) issue_s(j + 2);
+                        if (j + 2 < n) {
+                            const uint64_t kd = k_desc + kst * (C::TILE >> 4);
+#pragma unroll
+                            for (int kk = 0; kk < HD / 16; ++kk)
+                                umma_bf16(d, q_desc + (((kk >> 2) * C::Q_REG + (kk & 3) * 32) >> 4),
+                                          kd + (((kk >> 2) * C::KV_REG + (kk & 3) * 32) >> 4), ID_S, kk > 0 ? 1u : 0u);
+                        }
+                        umma_commit(&B->done[x][(nb + j + 2) % DONE]);
+                        if (j + 3 == n) umma_commit(&B->q_empty[x]);
                     }
+                    nb += n + 2;
                     ++nseg;
                     nt += n;
                     ring += 2 * n;
                 }
                 if (!wait.ok) {  // products that were issued must have ended before their accumulators are freed
                     umma_commit(&B->drain[x]);
-                    mbar_wait(&B->drain[x], 0, err);
+                    Waiter::late(&B->drain[x], 0);
                 }
             }
             __syncwarp();
@@ -436,7 +453,7 @@ __global__ void __launch_bounds__(NTHR, 1)
             const uint32_t tl = tmem + ((uint32_t)(32 * quad) << 16);
             const uint32_t tO = tl + 256 + HD * x;
             const uint64_t scale2 = pack2(a.scale_log2, a.scale_log2);
-            uint32_t nt = 0;  // tiles before this segment
+            uint32_t nt = 0, nb = 0;  // tiles and batches before this segment
             uint32_t nseg = 0;
             Seg s;
 #pragma unroll 1
@@ -452,15 +469,15 @@ __global__ void __launch_bounds__(NTHR, 1)
 #pragma unroll 1
                 for (int j = 0; j < n; ++j) {
                     const int k0 = (s.t0 + j) * KT;
-                    const uint32_t buf = (nt + j) & 1, phase = ((nt + j) >> 1) & 1;
+                    const uint32_t buf = (nt + j) & 1;
                     const uint32_t tS = tl + 128 * x + 64 * buf;
-                    if (!wait(&B->s_full[x][buf], phase)) break;
+                    if (!batch_done(x, nb + j)) break;
                     fence_after();
                     if (k0 + KT > s.keys) {
                         // the list ends inside this tile: zero the rows of V behind it (a page's unused slots may
                         // hold anything, and 0 * NaN is NaN); on line 0 both streams do, each before its own P V
-                        const uint32_t pos = ring + v_seq(j, n), st = first_stage(x) + pos % depth;
-                        if (!wait(&B->kv_full[st], (pos / depth) & 1)) break;
+                        const uint32_t pos = ring + v_seq(j, n), st = first_stage(x) + stage_of(pos);
+                        if (!wait(&B->kv_full[st], phase_of(pos))) break;
                         uint8_t* V = sm + C::RING_AT + st * C::TILE;
                         for (int i = (s.keys - k0) * 8 + v; i < KT * 8; i += 128)
 #pragma unroll
@@ -489,7 +506,7 @@ __global__ void __launch_bounds__(NTHR, 1)
                         const float m_new = mx > m_run + 8.f ? mx : m_run;
                         if (j > 0 && __any_sync(0xffffffffu, m_new != m_run)) {
                             // O holds the tiles before this one once the product of the last of them has completed
-                            if (!wait(&B->o_done[x][buf ^ 1], ((nt + j - 1) >> 1) & 1)) break;
+                            if (!batch_done(x, nb + j + 1)) break;
                             fence_after();
                             const float alpha = m_run == -INFINITY ? 0.f : ex2(m_run - m_new);
                             l_run *= alpha;
@@ -527,8 +544,7 @@ __global__ void __launch_bounds__(NTHR, 1)
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&B->p_full[x][buf]);
                 }
-                const uint32_t last = nt + n - 1;
-                if (!wait(&B->o_done[x][last & 1], (last >> 1) & 1)) break;
+                if (!batch_done(x, nb + n + 1)) break;
                 fence_after();
                 if (live_warp) {
                     const size_t blk = s.block + (pair ? x : 0);
@@ -553,6 +569,7 @@ __global__ void __launch_bounds__(NTHR, 1)
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&B->o_empty[x]);
                 nt += n;
+                nb += n + 2;
                 ring += 2 * n;
             }
         }
