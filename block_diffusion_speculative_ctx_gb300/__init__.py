@@ -218,7 +218,7 @@ from .session import Session, config_from_workload  # noqa: E402,F401
 
 def __getattr__(name):
     # the serving operators (ops.py) need torch, which this module itself does not import
-    if name in ("kv_tables", "shared_prefix_attention", "process_logits", "KVTables"):
+    if name in ("kv_tables", "shared_prefix_attention", "shared_prefix_workspace", "process_logits", "KVTables"):
         from . import ops
         globals()[name] = getattr(ops, name)
         return globals()[name]

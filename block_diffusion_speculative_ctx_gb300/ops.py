@@ -11,6 +11,7 @@ refused while autograd is recording."""
 from __future__ import annotations
 
 import ctypes
+import struct
 from typing import NamedTuple, Optional
 
 import torch
@@ -58,50 +59,71 @@ class KVTables(NamedTuple):
     status: torch.Tensor
 
 
-def _ptr(t):
-    return None if t is None else t.data_ptr()
+# Every call packs its argument struct with one of these (a fraction of a ctypes.Structure's cost: the
+# small calls are as long as their host side) and passes the bytes.
+_TABLES, _ATTN, _LOGITS = struct.Struct("6i2q12Q"), struct.Struct("10ifi3q11Q"), struct.Struct("8i4q13Q")
+_I32T, _I64T, _F32T = torch.int32, torch.int64, torch.float32
+_raw_stream = torch._C._cuda_getCurrentRawStream
 
 
-def _need(cond, msg):
-    if not cond:
-        raise ValueError(msg)
+def _bad(msg):
+    raise ValueError(msg)
 
 
-def _same_device(first, tensors):
-    """The one CUDA device of the call; gradients are refused."""
-    dev = first.device
-    _need(dev.type == "cuda", "the operators run on CUDA tensors only")
-    grad = torch.is_grad_enabled()
-    for name, t in tensors:
-        if t is None:
-            continue
-        _need(t.device == dev, f"{name} is on {t.device}, not on {dev}")
-        _need(not (grad and t.requires_grad), f"{name} requires a gradient, which this operator has not")
+def _device(first, *floats):
+    """Index of the one CUDA device of the call; floating tensors that record a gradient are refused."""
+    dev = first.get_device()
+    if dev < 0:
+        _bad("the operators run on CUDA tensors only")
+    if torch.is_grad_enabled():
+        for t in floats:
+            if t is not None and t.requires_grad:
+                _bad("a tensor requires a gradient, which these operators do not have")
     return dev
 
 
-def _vec(name, t, dtype, n):
-    _need(t.dtype == dtype and t.dim() == 1 and t.shape[0] == n and t.is_contiguous(),
-          f"{name} must be a contiguous {dtype} tensor of {n}")
+def _flat(name, t, dtype, n, dev):
+    """Address of a contiguous tensor of n elements on the device."""
+    if t.dtype is not dtype or t.numel() != n or t.get_device() != dev or not t.is_contiguous():
+        _bad(f"{name} must be a contiguous {dtype} tensor of {n} elements on cuda:{dev}, "
+             f"not {t.dtype} {tuple(t.shape)} on {t.device}")
+    return t.data_ptr()
 
 
-def _mat(name, t, dtype, rows, cols=None):
-    """A row-major matrix (any row stride); its row stride in elements."""
-    _need(t.dtype == dtype and t.dim() == 2 and t.shape[0] == rows and (cols is None or t.shape[1] == cols),
-          f"{name} must be a {dtype} matrix of {rows} rows" + ("" if cols is None else f" and {cols} columns"))
-    if t.shape[1] <= 1 or t.shape[0] == 0:
-        return max(t.stride(0), t.shape[1]) if rows > 1 else t.shape[1]
-    _need(t.stride(1) == 1 and (rows <= 1 or t.stride(0) >= t.shape[1]), f"{name} must be row-major")
-    return t.stride(0) if rows > 1 else t.shape[1]
+def _mat(name, t, dtype, rows, cols, dev):
+    """Row stride, in elements, of a row-major matrix on the device (cols None: any)."""
+    if t.dtype is not dtype or t.dim() != 2 or t.get_device() != dev:
+        _bad(f"{name} must be a {dtype} matrix on cuda:{dev}, not {t.dtype} {tuple(t.shape)} on {t.device}")
+    n, m = t.shape
+    if n != rows or (cols is not None and m != cols):
+        _bad(f"{name} must be [{rows}, {'any' if cols is None else cols}], not [{n}, {m}]")
+    ld, inner = t.stride()
+    if n <= 1 or m == 0:
+        ld = m
+    if (inner != 1 and m > 1) or ld < m:
+        _bad(f"{name} must be row-major")
+    return ld
+
+
+def _rows3(name, t, dtype, rows, heads, hd, dev):
+    """Row stride of a [rows, heads, hd] tensor whose rows are contiguous."""
+    if t.dtype is not dtype or tuple(t.shape) != (rows, heads, hd) or t.get_device() != dev:
+        _bad(f"{name} must be a {dtype} [{rows}, {heads}, {hd}] on cuda:{dev}, "
+             f"not {t.dtype} {tuple(t.shape)} on {t.device}")
+    if rows == 0:
+        return heads * hd
+    ld, between, inner = t.stride()
+    if inner != 1 or (heads > 1 and between != hd):
+        _bad(f"{name}: the heads of a row must be contiguous")
+    return ld if rows > 1 else heads * hd
 
 
 def _call(fn, args, dev):
-    stream = torch.cuda.current_stream(dev).cuda_stream
-    if torch.cuda.current_device() == dev.index:
-        st = fn(ctypes.byref(args), stream)
+    if torch.cuda.current_device() == dev:
+        st = fn(args, _raw_stream(dev))
     else:
         with torch.cuda.device(dev):
-            st = fn(ctypes.byref(args), stream)
+            st = fn(args, _raw_stream(dev))
     if st != DFLASH_OK:
         raise DFlashError(st, dflash_last_error(None))
 
@@ -117,60 +139,56 @@ def kv_tables(kv_lens, new_lens, table, free_pages=None, used=None, *, rows: Opt
     maps (default: that of ``row_seq`` / ``row_pos`` / ``slots``).  Missing outputs are allocated;
     ``table_out=table`` and ``used_out=used`` work in place.  ``status`` stays on the device: 0, or a
     sum of 1 (pool short), 2 (table too narrow), 4 (more new rows than ``rows``), 8 (negative length)."""
-    batch = kv_lens.shape[0] if kv_lens.dim() == 1 else 0
-    _need(1 <= batch <= OPS_MAX_BATCH, f"kv_lens must be a vector of 1 to {OPS_MAX_BATCH} lengths")
-    dev = _same_device(kv_lens, (("new_lens", new_lens), ("table", table), ("free_pages", free_pages), ("used", used),
-                                 ("table_out", table_out), ("used_out", used_out), ("q_start", q_start),
-                                 ("row_seq", row_seq), ("row_pos", row_pos), ("slots", slots), ("status", status)))
-    i32 = torch.int32
-    _vec("kv_lens", kv_lens, i32, batch)
-    _vec("new_lens", new_lens, i32, batch)
-    ld = _mat("table", table, i32, batch)
+    dev = _device(kv_lens)
+    batch = kv_lens.numel()
+    if not 1 <= batch <= OPS_MAX_BATCH:
+        _bad(f"kv_lens must hold 1 to {OPS_MAX_BATCH} lengths")
+    p_kv, p_new = _flat("kv_lens", kv_lens, _I32T, batch, dev), _flat("new_lens", new_lens, _I32T, batch, dev)
+    ld = ld_out = _mat("table", table, _I32T, batch, None, dev)
     width = table.shape[1]
-    for t in (row_seq, row_pos, slots):
-        if t is not None:
-            _need(rows is None or rows == t.shape[0], "row_seq, row_pos and slots must have `rows` entries")
-            rows = t.shape[0]
-    _need(rows is not None and rows >= 0, "rows is needed when no row map is given")
-    new = lambda n, dt=i32: torch.empty(n, dtype=dt, device=dev)  # noqa: E731
-    q_start = new(batch + 1) if q_start is None else q_start
-    row_seq = new(rows) if row_seq is None else row_seq
-    row_pos = new(rows) if row_pos is None else row_pos
-    slots = new(rows, torch.int64) if slots is None else slots
-    status = new(1) if status is None else status
-    for name, t, dt, n in (("q_start", q_start, i32, batch + 1), ("row_seq", row_seq, i32, rows),
-                           ("row_pos", row_pos, i32, rows), ("slots", slots, torch.int64, rows),
-                           ("status", status, i32, 1)):
-        _vec(name, t, dt, n)
-    ld_out, n_free = ld, 0
+    if rows is None:
+        for t in (row_seq, row_pos, slots):
+            if t is not None:
+                rows = t.numel()
+        if rows is None:
+            _bad("rows is needed when no row map is given")
+    elif rows < 0:
+        _bad("rows must not be negative")
+    if q_start is None:
+        q_start = torch.empty(batch + 1, dtype=_I32T, device=kv_lens.device)
+    if row_seq is None:
+        row_seq = torch.empty(rows, dtype=_I32T, device=kv_lens.device)
+    if row_pos is None:
+        row_pos = torch.empty(rows, dtype=_I32T, device=kv_lens.device)
+    if slots is None:
+        slots = torch.empty(rows, dtype=_I64T, device=kv_lens.device)
+    if status is None:
+        status = torch.empty(1, dtype=_I32T, device=kv_lens.device)
+    p_status = _flat("status", status, _I32T, 1, dev)
+    n_free = p_free = p_used = p_out = p_uo = 0
     if free_pages is not None:
-        n_free = free_pages.shape[0] if free_pages.dim() == 1 else -1
-        _need(used is not None, "free_pages needs used")
-        _vec("free_pages", free_pages, i32, n_free)
-        _vec("used", used, i32, 1)
-        table_out = torch.empty((batch, width), dtype=i32, device=dev) if table_out is None else table_out
-        used_out = new(1) if used_out is None else used_out
-        _vec("used_out", used_out, i32, 1)
-    else:
-        _need(used is None and used_out is None, "used and used_out need free_pages")
+        if used is None:
+            _bad("free_pages needs used")
+        n_free = free_pages.numel()
+        # (an empty list still has to be told from none at all)
+        p_free = _flat("free_pages", free_pages, _I32T, n_free, dev) or p_status
+        p_used = _flat("used", used, _I32T, 1, dev)
+        if table_out is None:
+            table_out = torch.empty((batch, width), dtype=_I32T, device=kv_lens.device)
+        if used_out is None:
+            used_out = torch.empty(1, dtype=_I32T, device=kv_lens.device)
+        p_uo = _flat("used_out", used_out, _I32T, 1, dev)
+    elif used is not None or used_out is not None:
+        _bad("used and used_out need free_pages")
     if table_out is not None:
-        ld_out = _mat("table_out", table_out, i32, batch, width)
-    # an empty free list still has to be told from none at all
-    free = None if free_pages is None else (free_pages.data_ptr() or status.data_ptr())
-    args = dflash_kv_tables_args(batch, width, rows, n_free, base_pos, scratch_page, ld, ld_out, kv_lens.data_ptr(),
-                                 new_lens.data_ptr(), _ptr(table), free, _ptr(used), _ptr(table_out), _ptr(used_out),
-                                 q_start.data_ptr(), _ptr(row_seq), _ptr(row_pos), _ptr(slots), status.data_ptr())
-    _call(load().dflash_kv_tables, args, dev)
+        ld_out = _mat("table_out", table_out, _I32T, batch, width, dev)
+        p_out = table_out.data_ptr()
+    _call(load().dflash_kv_tables,
+          _TABLES.pack(batch, width, rows, n_free, base_pos, scratch_page, ld, ld_out, p_kv, p_new, table.data_ptr(), p_free,
+                       p_used, p_out, p_uo, _flat("q_start", q_start, _I32T, batch + 1, dev),
+                       _flat("row_seq", row_seq, _I32T, rows, dev), _flat("row_pos", row_pos, _I32T, rows, dev),
+                       _flat("slots", slots, _I64T, rows, dev), p_status), dev)
     return KVTables(table_out, used_out, q_start, row_seq, row_pos, slots, status)
-
-
-def _rows3(name, t, rows, heads, hd):
-    """Row stride of a [rows, heads, hd] tensor whose rows are contiguous."""
-    _need(t.dim() == 3 and tuple(t.shape) == (rows, heads, hd), f"{name} must be [{rows}, {heads}, {hd}]")
-    if rows == 0:
-        return heads * hd
-    _need(t.stride(2) == 1 and (heads == 1 or t.stride(1) == hd), f"{name}: the heads of a row must be contiguous")
-    return t.stride(0) if rows > 1 else heads * hd
 
 
 def shared_prefix_attention(q, k_cache, v_cache, prefix_pages, prefix_len: int, table, kv_lens, q_start, *,
@@ -182,49 +200,57 @@ def shared_prefix_attention(q, k_cache, v_cache, prefix_pages, prefix_len: int, 
     prefix's pages (None for an empty prefix); table: int32 [batch, width], each sequence's own pages;
     kv_lens: int32 [batch], its own keys; q_start: int32 [batch + 1], its rows.  ``scale`` defaults to
     hd ** -0.5.  Returns (out, lse); rows outside q_start keep what ``out`` and ``lse`` held (0 where they
-    are allocated here)."""
-    _need(q.dim() == 3 and k_cache.dim() == 4, "q must be [rows, H, hd] and the caches [pages, H_kv, 64, hd]")
+    are allocated here).  ``workspace``: uint8, at least ``shared_prefix_workspace`` bytes (allocated when
+    None); calls that may run at the same time need one each."""
+    if q.dim() != 3 or k_cache.dim() != 4:
+        _bad("q must be [rows, H, hd] and the caches [pages, H_kv, 64, hd]")
+    dev = _device(q, q, k_cache, v_cache)
     rows, h, hd = q.shape
-    pages, hkv = k_cache.shape[0], k_cache.shape[1]
-    dev = _same_device(q, (("q", q), ("k_cache", k_cache), ("v_cache", v_cache), ("prefix_pages", prefix_pages),
-                           ("table", table), ("kv_lens", kv_lens), ("q_start", q_start), ("out", out), ("lse", lse),
-                           ("workspace", workspace)))
-    dt = _DTYPES.get(q.dtype)
-    _need(dt is not None, f"q must be float32 or bfloat16, not {q.dtype}")
-    for name, c in (("k_cache", k_cache), ("v_cache", v_cache)):
-        _need(c.dtype == q.dtype and tuple(c.shape) == (pages, hkv, PAGE_TOKENS, hd) and c.is_contiguous(),
-              f"{name} must be a contiguous {q.dtype} [pages, H_kv, {PAGE_TOKENS}, {hd}]")
-    batch = kv_lens.shape[0] if kv_lens.dim() == 1 else 0
-    _need(1 <= batch <= OPS_MAX_BATCH, f"kv_lens must be a vector of 1 to {OPS_MAX_BATCH} lengths")
-    _vec("kv_lens", kv_lens, torch.int32, batch)
-    _vec("q_start", q_start, torch.int32, batch + 1)
-    prefix_len = int(prefix_len)
-    n_pre = (prefix_len + PAGE_TOKENS - 1) // PAGE_TOKENS
+    pages, hkv = k_cache.shape[:2]
+    dtype = q.dtype
+    dt = _DTYPES.get(dtype)
+    if dt is None:
+        _bad(f"q must be float32 or bfloat16, not {dtype}")
+    n_kv = pages * hkv * PAGE_TOKENS * hd
+    if k_cache.shape[2] != PAGE_TOKENS or k_cache.shape[3] != hd or v_cache.shape != k_cache.shape:
+        _bad(f"k_cache and v_cache must be [pages, H_kv, {PAGE_TOKENS}, {hd}]")
+    p_k, p_v = _flat("k_cache", k_cache, dtype, n_kv, dev), _flat("v_cache", v_cache, dtype, n_kv, dev)
+    batch = kv_lens.numel()
+    if not 1 <= batch <= OPS_MAX_BATCH:
+        _bad(f"kv_lens must hold 1 to {OPS_MAX_BATCH} lengths")
+    p_kv, p_start = _flat("kv_lens", kv_lens, _I32T, batch, dev), _flat("q_start", q_start, _I32T, batch + 1, dev)
+    p_pre = 0
     if prefix_pages is not None:
-        _need(prefix_pages.dtype == torch.int32 and prefix_pages.dim() == 1 and prefix_pages.is_contiguous()
-              and prefix_pages.shape[0] >= n_pre, f"prefix_pages must be a contiguous int32 tensor of at least {n_pre}")
-    else:
-        _need(prefix_len == 0, "prefix_pages is needed for a prefix")
-    ld_table = _mat("table", table, torch.int32, batch)
-    ld_q = _rows3("q", q, rows, h, hd)
-    out = torch.zeros((rows, h, hd), dtype=q.dtype, device=dev) if out is None else out
-    _need(out.dtype == q.dtype, f"out must be {q.dtype}")
-    ld_out = _rows3("out", out, rows, h, hd)
-    lse = torch.zeros((rows, h), dtype=torch.float32, device=dev) if lse is None else lse
-    _need(lse.dtype == torch.float32 and tuple(lse.shape) == (rows, h) and lse.is_contiguous(),
-          f"lse must be a contiguous float32 [{rows}, {h}]")
+        n_pre = prefix_pages.numel()
+        p_pre = _flat("prefix_pages", prefix_pages, _I32T, n_pre, dev)
+        if n_pre * PAGE_TOKENS < prefix_len:
+            _bad(f"prefix_pages holds {n_pre} pages, too few for {prefix_len} tokens")
+    elif prefix_len != 0:
+        _bad("prefix_pages is needed for a prefix")
+    ld_table = _mat("table", table, _I32T, batch, None, dev)
+    ld_q = _rows3("q", q, dtype, rows, h, hd, dev)
+    if out is None:
+        out = torch.zeros((rows, h, hd), dtype=dtype, device=q.device)
+    ld_out = _rows3("out", out, dtype, rows, h, hd, dev)
+    if lse is None:
+        lse = torch.zeros((rows, h), dtype=_F32T, device=q.device)
     lib = load()
     if workspace is None:
         workspace = torch.empty(lib.dflash_shared_prefix_workspace(dt, h, hkv, hd, batch, rows), dtype=torch.uint8,
-                                device=dev)
-    _need(workspace.is_contiguous(), "workspace must be contiguous")
-    args = dflash_shared_prefix_args(dt, h, hkv, hd, batch, rows, pages, prefix_len, table.shape[1], bool(causal),
-                                     hd ** -0.5 if scale is None else scale, 0, ld_q, ld_out, ld_table, q.data_ptr(),
-                                     k_cache.data_ptr(), v_cache.data_ptr(), _ptr(prefix_pages), table.data_ptr(),
-                                     kv_lens.data_ptr(), q_start.data_ptr(), out.data_ptr(), lse.data_ptr(),
-                                     workspace.data_ptr(), workspace.numel() * workspace.element_size())
-    _call(lib.dflash_shared_prefix_attention, args, dev)
+                                device=q.device)
+    n_ws = workspace.numel() * workspace.element_size()
+    _call(lib.dflash_shared_prefix_attention,
+          _ATTN.pack(dt, h, hkv, hd, batch, rows, pages, prefix_len, table.shape[1], bool(causal),
+                     hd ** -0.5 if scale is None else scale, 0, ld_q, ld_out, ld_table, q.data_ptr(), p_k, p_v, p_pre,
+                     table.data_ptr(), p_kv, p_start, out.data_ptr(), _flat("lse", lse, _F32T, rows * h, dev),
+                     _flat("workspace", workspace, workspace.dtype, workspace.numel(), dev), n_ws), dev)
     return out, lse
+
+
+def shared_prefix_workspace(q, k_cache, batch: int) -> int:
+    """Bytes of workspace that a call of ``shared_prefix_attention`` with these tensors needs."""
+    return load().dflash_shared_prefix_workspace(_DTYPES[q.dtype], q.shape[1], k_cache.shape[1], q.shape[2], batch,
+                                                 q.shape[0])
 
 
 def process_logits(logits, *, rows_per_seq: int = 1, history=None, hist_lens=None, prompt_lens=None, drafts=None,
@@ -238,61 +264,64 @@ def process_logits(logits, *, rows_per_seq: int = 1, history=None, hist_lens=Non
     fp32 [batch]; bias_ids / bias_values: [batch, n] (id -1: unused; the last entry of an id counts);
     masks: int32 bit sets [n_masks, >= ceil(vocab / 32)] with mask_index int32 [rows] (-1: none).
     Returns ``out`` (allocated when None; ``out=logits`` works in place)."""
-    _need(logits.dim() == 2, "logits must be [rows, vocab]")
+    if logits.dim() != 2:
+        _bad("logits must be [rows, vocab]")
+    dev = _device(logits, logits, repetition, presence, frequency, bias_values)
     n, vocab = logits.shape
-    _need(1 <= rows_per_seq <= 32 and n % rows_per_seq == 0, "rows_per_seq must be in [1, 32] and divide the rows")
+    dtype = logits.dtype
+    dt = _DTYPES.get(dtype)
+    if dt is None:
+        _bad(f"logits must be float32 or bfloat16, not {dtype}")
+    if not 1 <= rows_per_seq <= 32 or n % rows_per_seq:
+        _bad("rows_per_seq must be in [1, 32] and divide the rows")
     batch = n // rows_per_seq
-    _need(1 <= batch <= OPS_MAX_BATCH, f"1 to {OPS_MAX_BATCH} sequences")
-    dev = _same_device(logits, (("logits", logits), ("history", history), ("hist_lens", hist_lens),
-                                ("prompt_lens", prompt_lens), ("drafts", drafts), ("repetition", repetition),
-                                ("presence", presence), ("frequency", frequency), ("bias_ids", bias_ids),
-                                ("bias_values", bias_values), ("masks", masks), ("mask_index", mask_index),
-                                ("out", out)))
-    dt = _DTYPES.get(logits.dtype)
-    _need(dt is not None, f"logits must be float32 or bfloat16, not {logits.dtype}")
-    out = torch.empty((n, vocab), dtype=logits.dtype, device=dev) if out is None else out
-    ld = _mat("logits", logits, logits.dtype, n)
-    ld_out = _mat("out", out, logits.dtype, n, vocab)
-    i32, f32 = torch.int32, torch.float32
+    if not 1 <= batch <= OPS_MAX_BATCH:
+        _bad(f"1 to {OPS_MAX_BATCH} sequences")
+    if out is None:
+        out = torch.empty((n, vocab), dtype=dtype, device=logits.device)
+    ld, ld_out = _mat("logits", logits, dtype, n, vocab, dev), _mat("out", out, dtype, n, vocab, dev)
     hist_width = bias_width = n_masks = ld_hist = ld_mask = 0
+    p_hist = p_len = p_prompt = p_draft = p_rep = p_pres = p_freq = p_ids = p_val = p_mask = p_idx = 0
     if history is not None:
-        _need(hist_lens is not None and prompt_lens is not None, "history needs hist_lens and prompt_lens")
-        ld_hist = _mat("history", history, i32, batch)
+        if hist_lens is None or prompt_lens is None:
+            _bad("history needs hist_lens and prompt_lens")
+        ld_hist = _mat("history", history, _I32T, batch, None, dev)
         hist_width = history.shape[1]
-        _vec("hist_lens", hist_lens, i32, batch)
-        _vec("prompt_lens", prompt_lens, i32, batch)
-        for name, t in (("repetition", repetition), ("presence", presence), ("frequency", frequency)):
-            if t is not None:
-                _vec(name, t, f32, batch)
+        p_len, p_prompt = _flat("hist_lens", hist_lens, _I32T, batch, dev), _flat("prompt_lens", prompt_lens, _I32T, batch, dev)
+        p_hist = history.data_ptr() or p_len  # (an empty history still has to be told from none at all)
+        if repetition is not None:
+            p_rep = _flat("repetition", repetition, _F32T, batch, dev)
+        if presence is not None:
+            p_pres = _flat("presence", presence, _F32T, batch, dev)
+        if frequency is not None:
+            p_freq = _flat("frequency", frequency, _F32T, batch, dev)
         if drafts is not None:
-            _need(rows_per_seq > 1, "drafts need more than one row a sequence")
-            _mat("drafts", drafts, i32, batch, rows_per_seq - 1)
-            _need(drafts.is_contiguous(), "drafts must be contiguous")
-    else:
-        _need(hist_lens is None and prompt_lens is None and drafts is None and repetition is None and presence is None
-              and frequency is None, "penalties and drafts need a history")
+            if rows_per_seq == 1:
+                _bad("drafts need more than one row a sequence")
+            p_draft = _flat("drafts", drafts, _I32T, batch * (rows_per_seq - 1), dev)
+    elif any(t is not None for t in (hist_lens, prompt_lens, drafts, repetition, presence, frequency)):
+        _bad("penalties and drafts need a history")
     if bias_ids is not None:
-        _need(bias_values is not None, "bias_ids needs bias_values")
-        bias_width = bias_ids.shape[1] if bias_ids.dim() == 2 else 0
-        _mat("bias_ids", bias_ids, i32, batch, bias_width)
-        _mat("bias_values", bias_values, f32, batch, bias_width)
-        _need(bias_ids.is_contiguous() and bias_values.is_contiguous(), "bias_ids and bias_values must be contiguous")
-    else:
-        _need(bias_values is None, "bias_values needs bias_ids")
+        if bias_values is None:
+            _bad("bias_ids needs bias_values")
+        bias_width = bias_ids.numel() // batch
+        p_ids = _flat("bias_ids", bias_ids, _I32T, batch * bias_width, dev)
+        p_val = _flat("bias_values", bias_values, _F32T, batch * bias_width, dev)
+    elif bias_values is not None:
+        _bad("bias_values needs bias_ids")
     if masks is not None:
-        _need(mask_index is not None, "masks need mask_index")
+        if mask_index is None:
+            _bad("masks need mask_index")
         n_masks = masks.shape[0]
-        ld_mask = _mat("masks", masks, i32, n_masks)
-        _need(masks.shape[1] * 32 >= vocab, "a mask must hold a bit for every token")
-        _vec("mask_index", mask_index, i32, n)
-    else:
-        _need(mask_index is None, "mask_index needs masks")
-    # an empty list (no column, no mask) leaves its group out
-    args = dflash_logits_args(dt, batch, rows_per_seq, vocab, hist_width, bias_width, n_masks, 0, ld, ld_out, ld_hist,
-                              ld_mask, logits.data_ptr(), out.data_ptr(),
-                              None if history is None else (history.data_ptr() or hist_lens.data_ptr()), _ptr(hist_lens),
-                              _ptr(prompt_lens), _ptr(drafts), _ptr(repetition), _ptr(presence), _ptr(frequency),
-                              _ptr(bias_ids) if bias_width else None, _ptr(bias_values),
-                              _ptr(masks) if n_masks else None, _ptr(mask_index))
-    _call(load().dflash_process_logits, args, dev)
+        ld_mask = _mat("masks", masks, _I32T, n_masks, None, dev)
+        if masks.shape[1] * 32 < vocab:
+            _bad("a mask must hold a bit for every token")
+        ld_mask = max(ld_mask, masks.shape[1])
+        p_mask, p_idx = masks.data_ptr(), _flat("mask_index", mask_index, _I32T, n, dev)
+    elif mask_index is not None:
+        _bad("mask_index needs masks")
+    _call(load().dflash_process_logits,
+          _LOGITS.pack(dt, batch, rows_per_seq, vocab, hist_width, bias_width, n_masks, 0, ld, ld_out, ld_hist, ld_mask,
+                       logits.data_ptr(), out.data_ptr(), p_hist, p_len, p_prompt, p_draft, p_rep, p_pres, p_freq,
+                       p_ids if bias_width else 0, p_val, p_mask if n_masks else 0, p_idx), dev)
     return out

@@ -31,6 +31,8 @@ def test_struct_layouts_match_the_header(tmp_path):
     got = [int(x) for x in subprocess.run([str(exe)], capture_output=True, text=True, check=True).stdout.split()]
     want = [ctypes.sizeof(s) for s in structs] + [getattr(s, f[0]).offset for s in structs for f in s._fields_]
     assert got == want
+    # the packed form that the calls pass
+    assert [ops._TABLES.size, ops._ATTN.size, ops._LOGITS.size] == want[:3]
 
 
 P = 4096  # stands for a device pointer (never read: every call here is refused)
