@@ -6,13 +6,15 @@
 // free_pages[used + A_s + j] and its rows start at Q_s.  Bytes: the table read and
 // written, 16 B a row; at the largest session (1024 requests) that is 1.6 MB, far
 // below a launch's latency, so the kernel is bound by its chain of dependent
-// steps: lengths -> scan -> entries.  Hence one launch: one cluster of 1..8 CTAs,
-// every CTA scans the whole batch itself (at most 2048 lengths, from L2) and then
-// writes its share of the table and the rows; a second launch or a grid-wide
-// exchange of the scan would each cost more than the repeated scan.  The cluster's
-// only exchange is a barrier before `used` is overwritten (it may be in place).
+// steps: lengths -> scan -> entries.  Hence one launch in which every CTA scans the
+// whole batch itself (at most 2048 lengths, from L2) and then writes its share of
+// the table (a warp per request) and of the rows: an exchange of the scan between
+// CTAs, or a second launch, would cost more than the repeated scan.  In place
+// (used_out is used) the count may change only when every CTA has read it: small
+// calls run in one CTA, larger ones leave it to a second launch of one CTA.
+#include <algorithm>
+
 #include "ops.h"
-#include "tcgen05.cuh"
 
 namespace dfl {
 
@@ -20,17 +22,19 @@ namespace {
 
 constexpr int NT = 512;
 constexpr int PER = DFLASH_OPS_MAX_BATCH / NT;  // requests per thread of the scan
-constexpr int MAXC = 8;                         // portable cluster size
+constexpr int CTAS = 152;
 
-__global__ void __launch_bounds__(NT) kv_tables_kernel(dflash_kv_tables_args a, int ctas) {
+enum Part { ALL, ENTRIES, COUNT };  // what a launch writes: everything, all but used_out, used_out alone
+
+__global__ void __launch_bounds__(NT) kv_tables_kernel(dflash_kv_tables_args a, Part what) {
     pdl_wait();
     pdl_trigger();
     __shared__ int qs[DFLASH_OPS_MAX_BATCH + 1];  // first row of each request
-    __shared__ int pa[DFLASH_OPS_MAX_BATCH];      // pages taken before each request
+    __shared__ int pa[DFLASH_OPS_MAX_BATCH + 1];  // pages taken before each request
+    __shared__ int kv_s[DFLASH_OPS_MAX_BATCH];
     __shared__ int2 wsum[NT / 32];
     __shared__ int bad_s;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int rank = blockIdx.x;
     if (tid == 0) bad_s = 0;
     __syncthreads();
 
@@ -44,6 +48,7 @@ __global__ void __launch_bounds__(NT) kv_tables_kernel(dflash_kv_tables_args a, 
         nw[i] = ad[i] = 0;
         if (i < per && s0 + i < a.batch) {
             const int kv = a.kv_lens[s0 + i], n = a.new_lens[s0 + i];
+            kv_s[s0 + i] = kv;
             if (kv < 0 || n < 0) {
                 bad |= 8;
             } else {
@@ -88,26 +93,32 @@ __global__ void __launch_bounds__(NT) kv_tables_kernel(dflash_kv_tables_args a, 
             pa[s0 + i] = ex.y;
             ex = make_int2(add(ex.x, nw[i]), add(ex.y, ad[i]));
         }
-    if (tid == 0) qs[a.batch] = total.x;
+    if (tid == 0) {
+        qs[a.batch] = total.x;
+        pa[a.batch] = total.y;
+    }
     int status = bad_s;
     if (a.free_pages && (long long)max(used, 0) + total.y > a.n_free) status |= 1;
     if (total.x > a.rows) status |= 4;
     __syncthreads();
     const bool ok = status == 0;
 
-    const int gt = rank * NT + tid, gn = ctas * NT;
-    // table: old entries copied (unless in place), the request's new pages, then scratch
+    if (blockIdx.x == 0 && tid == 0 && what != ENTRIES && a.used_out)
+        *a.used_out = ok ? used + (a.free_pages ? total.y : 0) : used;
+    if (what == COUNT) return;
+    if (blockIdx.x == 0 && tid == 0) *a.status = status;
+
+    const int gt = blockIdx.x * NT + tid, gn = gridDim.x * NT;
+    // table: the old entries copied (unless in place), the request's new pages, then scratch
     if (ok && a.table_out) {
-        const long long cells = (long long)a.batch * a.width;
-        for (long long i = gt; i < cells; i += gn) {
-            const int s = (int)(i / a.width), j = (int)(i - (long long)s * a.width);
-            const int kv = a.kv_lens[s];
-            const int old = (int)(((long long)kv + 63) >> 6);
-            const int need = (int)(((long long)kv + a.new_lens[s] + 63) >> 6);
-            int page = a.scratch_page;
-            if (j < old || (!a.free_pages && j < need)) page = a.table[(long long)s * a.ld_table + j];
-            else if (j < need) page = a.free_pages[used + pa[s] + j - old];
-            a.table_out[(long long)s * a.ld_out + j] = page;
+        const bool copy = a.table_out != a.table;
+        for (int s = gt >> 5; s < a.batch; s += gn >> 5) {
+            const int old = (kv_s[s] + 63) >> 6, taken = pa[s + 1] - pa[s];
+            const int* src = a.table + (long long)s * a.ld_table;
+            const int* fresh = a.free_pages ? a.free_pages + used + pa[s] - old : src;
+            int* dst = a.table_out + (long long)s * a.ld_out;
+            for (int j = (copy ? 0 : old & ~31) + lane; j < a.width; j += 32)
+                if (copy || j >= old) dst[j] = j < old ? src[j] : j < old + taken ? fresh[j] : a.scratch_page;
         }
     }
     // rows: the request of row r is the last s with qs[s] <= r (requests without rows share
@@ -123,9 +134,9 @@ __global__ void __launch_bounds__(NT) kv_tables_kernel(dflash_kv_tables_args a, 
                 else hi = mid;
             }
             seq = lo;
-            const int kv = a.kv_lens[seq], i = kv + r - qs[seq];
+            const int kv = kv_s[seq], i = kv + r - qs[seq];
             pos = a.base_pos + i;
-            const int j = i >> 6, old = (int)(((long long)kv + 63) >> 6);
+            const int j = i >> 6, old = (kv + 63) >> 6;
             const int page = (j < old || !a.free_pages) ? a.table[(long long)seq * a.ld_table + j]
                                                         : a.free_pages[used + pa[seq] + j - old];
             slot = (long long)page * 64 + (i & 63);
@@ -135,12 +146,6 @@ __global__ void __launch_bounds__(NT) kv_tables_kernel(dflash_kv_tables_args a, 
         if (a.slots) a.slots[r] = slot;
     }
     for (int s = gt; s <= a.batch; s += gn) a.q_start[s] = ok ? qs[s] : 0;
-    if (ctas > 1) tc::cluster_sync();  // every CTA has read `used`
-    else __syncthreads();
-    if (rank == 0 && tid == 0) {
-        *a.status = status;
-        if (a.used_out) *a.used_out = ok ? used + (a.free_pages ? total.y : 0) : used;
-    }
 }
 
 dflash_status fail(const char* msg) {
@@ -151,30 +156,17 @@ dflash_status fail(const char* msg) {
 }  // namespace
 
 void kv_tables(const Launch& L, const dflash_kv_tables_args& a) {
-    // One CTA per 4096 table entries and rows, 1..8 in one cluster
-    const long long work = (long long)a.batch * a.width + a.rows;
-    int c = 1;
-    while (c < MAXC && work > (long long)c * 4096) c *= 2;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(c);
-    cfg.blockDim = dim3(NT);
-    cfg.stream = L.stream;
-    cudaLaunchAttribute attr[2];
-    int n = 0;
-    if (L.pdl) {
-        attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-        attr[n++].val.programmaticStreamSerializationAllowed = 1;
+    // a warp per request, a thread per row; one CTA up to 2048 entries and rows
+    const long long rows = (a.rows + NT - 1) / NT, reqs = (a.batch + NT / 32 - 1) / (NT / 32);
+    int c = (int)std::min<long long>(CTAS, std::max(rows, reqs));
+    if ((long long)a.batch * a.width + a.rows <= 2048) c = 1;
+    const bool split = c > 1 && a.used_out && a.used_out == a.used;
+    launch_k(L, kv_tables_kernel, dim3(c), dim3(NT), 0, 1, a, split ? ENTRIES : ALL);
+    if (split) {
+        Launch after = L;
+        after.pdl = true;
+        launch_k(after, kv_tables_kernel, dim3(1), dim3(NT), 0, 1, a, COUNT);
     }
-    if (c > 1) {
-        attr[n].id = cudaLaunchAttributeClusterDimension;
-        attr[n].val.clusterDim.x = c;
-        attr[n].val.clusterDim.y = attr[n].val.clusterDim.z = 1;
-        ++n;
-    }
-    cfg.attrs = attr;
-    cfg.numAttrs = n;
-    if (cudaLaunchKernelEx(&cfg, kv_tables_kernel, a, c) != cudaSuccess) L.fail();
-    L.bump();
 }
 
 }  // namespace dfl

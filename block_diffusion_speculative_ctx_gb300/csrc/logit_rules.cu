@@ -4,16 +4,23 @@
 // Per row this is one read and one write of the logits (HBM bound: 2 * vocab *
 // element bytes a row, 622 MB for a 512-row verify pass at the Qwen3 vocabulary);
 // the difficulty is that the history is a list of ids while the logits stream by
-// vocabulary.  A CTA owns one chunk of the vocabulary for one sequence: it first
-// turns the sequence's history, drafts and biases into per-token words for its
-// chunk in shared memory (counts by integer atomics, so the order is immaterial),
-// then streams its chunk of every row of the sequence.  The history is read once
-// per (sequence, chunk) instead of once per row, from L2.  Drafts are kept as one
-// bit per draft position and token, so that row j counts the drafts before it
-// (popc of the bits below j) without a barrier between rows.  A flag byte per
-// group of four tokens says whether any rule but a mask touches the group: nearly
-// all groups take the short path (mask only).
+// vocabulary.  A CTA owns one chunk of the vocabulary for (a group of rows of) one
+// sequence.  It first turns the sequence's history and biases into one or two
+// words per token of its chunk in shared memory (counts by integer atomics, so the
+// order is immaterial): the history is read once per chunk instead of once per
+// row, from L2.  Then
+//   - the stream: 16-byte vectors without a touched token are copied under the
+//     row's mask, a row ahead of the stores; the mask words of the row after that
+//     are under way, so no load waits for another.  A vector that its mask closes
+//     entirely is not read;
+//   - the touched vectors, collected in a list, a thread per token: they are few,
+//     but sit together (frequent ids), so spreading them over the CTA keeps one
+//     warp from doing them all, and the rule's code exists once.
+// Drafts stay a list of at most 31 ids: a token that is a draft carries a bit, and
+// only such tokens count the drafts before their row.
 #include <math.h>
+
+#include <algorithm>
 
 #include "ops.h"
 
@@ -22,173 +29,235 @@ namespace dfl {
 namespace {
 
 constexpr int NT = 256;
-constexpr uint32_t IN_PROMPT = 0x80000000u;
+constexpr uint32_t IN_PROMPT = 0x80000000u, IS_DRAFT = 0x40000000u, COUNT = 0x3FFFFFFFu;
 
-template <typename T>
-struct Vec4;
-template <>
-struct Vec4<float> {
-    float4 v;
-    __device__ __forceinline__ void get(float (&x)[4]) const { x[0] = v.x; x[1] = v.y; x[2] = v.z; x[3] = v.w; }
-    __device__ __forceinline__ void set(const float (&x)[4]) { v = make_float4(x[0], x[1], x[2], x[3]); }
-};
-template <>
-struct Vec4<bf16> {
-    uint2 v;
-    __device__ __forceinline__ void get(float (&x)[4]) const {
-        x[0] = __uint_as_float(v.x << 16);
-        x[1] = __uint_as_float(v.x & 0xFFFF0000u);
-        x[2] = __uint_as_float(v.y << 16);
-        x[3] = __uint_as_float(v.y & 0xFFFF0000u);
-    }
-    __device__ __forceinline__ void set(const float (&x)[4]) {
-        const __nv_bfloat162 a = __floats2bfloat162_rn(x[0], x[1]), b = __floats2bfloat162_rn(x[2], x[3]);
-        v = make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
-    }
+struct Plan {
+    int chunk;   // tokens per CTA
+    int rows;    // rows per CTA
+    int groups;  // row groups per sequence
 };
 
-struct Rules {
-    float rep, pres, freq;
-};
-
-// One token's rule: `word` its count after the prompt with IN_PROMPT, `extra` the drafts of it
-// before this row.
-__device__ __forceinline__ float apply(float x, uint32_t word, int extra, const Rules& r) {
-    const uint32_t count = (word & ~IN_PROMPT) + (uint32_t)extra;
-    if (count || (word & IN_PROMPT)) x = x > 0.f ? x / r.rep : x * r.rep;
-    x -= r.freq * (float)count;
-    if (count) x -= r.pres;
-    return x;
-}
-
-// VEC: base pointers and row strides allow 4-token vectors.
-template <typename T, bool VEC>
-__global__ void __launch_bounds__(NT) logit_rules_kernel(dflash_logits_args a, int chunk) {
+// T logits; NV vectors per thread and row (chunk = NT * NV * 16 / sizeof(T) tokens); VEC: base pointers and
+// row strides are multiples of 16 bytes (else the stream moves single elements).
+template <typename T, int NV, bool VEC>
+__global__ void __launch_bounds__(NT) logit_rules_kernel(dflash_logits_args a, Plan pl) {
+    constexpr int G = 16 / (int)sizeof(T);  // tokens of a vector
+    constexpr int CH = NT * NV * G;
+    __shared__ __align__(16) uint32_t count[CH];       // occurrences after the prompt | IN_PROMPT | IS_DRAFT
+    __shared__ __align__(16) uint32_t flag4[CH / G / 4];  // a byte per vector: a rule touches it
+    __shared__ uint16_t list[CH / G];                  // the touched vectors
+    __shared__ int n_list, draft[32], midx[32];
+    extern __shared__ __align__(16) int bias[];        // [CH] 1 + last bias entry of the token, 0: none (bias_ids given)
+    uint8_t* flag = reinterpret_cast<uint8_t*>(flag4);
+    const int tid = threadIdx.x;
+    const int c0 = blockIdx.x * CH, s = blockIdx.y / pl.groups, j0 = (blockIdx.y - s * pl.groups) * pl.rows;
+    const int rows = min(pl.rows, a.rows_per_seq - j0);
+    const long long row0 = (long long)s * a.rows_per_seq + j0;
+    const int n = min(CH, a.vocab - c0);
+    const bool inplace = a.out == a.logits, rules = a.history || a.bias_ids;
+    const T* X = reinterpret_cast<const T*>(a.logits) + row0 * a.ld_logits + c0;
+    T* Y = reinterpret_cast<T*>(a.out) + row0 * a.ld_out + c0;
     pdl_wait();
     pdl_trigger();
-    extern __shared__ uint32_t sm[];
-    uint32_t* count = sm;                    // [chunk] occurrences after the prompt | IN_PROMPT
-    uint32_t* draft = count + chunk;         // [chunk] bit i: draft i is this token
-    int* bias = (int*)(draft + chunk);       // [chunk] 1 + last bias entry of this token (0: none)
-    uint32_t* flag32 = (uint32_t*)(bias + chunk);
-    uint8_t* flag = (uint8_t*)flag32;        // [chunk / 4]: a rule touches one of the four tokens
-    const int tid = threadIdx.x;
-    const int c0 = blockIdx.x * chunk, s = blockIdx.y;
-    const int n = min(chunk, a.vocab - c0);
-    const bool inplace = a.out == a.logits;
 
-    for (int i = tid; i < 3 * chunk + chunk / 16; i += NT) sm[i] = 0u;
+    // ---- the chunk's words
+    if (tid < rows) {
+        const int m = a.masks ? a.mask_index[row0 + tid] : -1;
+        midx[tid] = m < a.n_masks ? m : -1;
+    }
+    if (tid == 0) n_list = 0;
+    if (rules) {
+        uint4* z = reinterpret_cast<uint4*>(count);
+#pragma unroll
+        for (int i = 0; i < CH / 4 / NT; ++i) z[tid + i * NT] = make_uint4(0u, 0u, 0u, 0u);
+        if (a.bias_ids) {
+            z = reinterpret_cast<uint4*>(bias);
+#pragma unroll
+            for (int i = 0; i < CH / 4 / NT; ++i) z[tid + i * NT] = make_uint4(0u, 0u, 0u, 0u);
+        }
+    }
+    for (int i = tid; i < CH / G / 4; i += NT) flag4[i] = 0u;
     __syncthreads();
-    Rules rule{1.f, 0.f, 0.f};
+    float rep = 1.f, pres = 0.f, freq = 0.f;
     if (a.history) {
-        if (a.repetition) rule.rep = a.repetition[s];
-        if (a.presence) rule.pres = a.presence[s];
-        if (a.frequency) rule.freq = a.frequency[s];
+        if (a.repetition) rep = a.repetition[s];
+        if (a.presence) pres = a.presence[s];
+        if (a.frequency) freq = a.frequency[s];
         const int len = min(max(a.hist_lens[s], 0), a.hist_width);
         const int prompt = min(max(a.prompt_lens[s], 0), len);
         const int* h = a.history + (long long)s * a.ld_hist;
-        for (int i = tid; i < len; i += NT) {
-            const unsigned t = (unsigned)(h[i] - c0);
-            if (h[i] >= 0 && t < (unsigned)n) {
+        auto mark = [&](int id, int i) {
+            const unsigned t = (unsigned)id - (unsigned)c0;
+            if (id >= 0 && t < (unsigned)n) {
                 if (i < prompt) atomicOr(&count[t], IN_PROMPT);
                 else atomicAdd(&count[t], 1u);
-                flag[t >> 2] = 1;
+                flag[t / G] = 1;
             }
+        };
+        const int lead = min(len, (int)((16 - ((uintptr_t)h & 15)) & 15) / 4), quads = (len - lead) / 4;
+        if (tid < lead) mark(h[tid], tid);
+#pragma unroll 2
+        for (int q = tid; q < quads; q += NT) {
+            const int4 v = *reinterpret_cast<const int4*>(h + lead + 4 * q);
+            const int i = lead + 4 * q;
+            mark(v.x, i);
+            mark(v.y, i + 1);
+            mark(v.z, i + 2);
+            mark(v.w, i + 3);
         }
-        if (a.drafts && tid < a.rows_per_seq - 1) {
-            const int id = a.drafts[(long long)s * (a.rows_per_seq - 1) + tid];
-            const unsigned t = (unsigned)(id - c0);
-            if (id >= 0 && t < (unsigned)n) {
-                atomicOr(&draft[t], 1u << tid);
-                flag[t >> 2] = 1;
+        const int rest = lead + 4 * quads + tid;
+        if (rest < len) mark(h[rest], rest);
+        if (tid < 32) {
+            int t = -1;
+            if (a.drafts && tid < a.rows_per_seq - 1) {
+                const int id = a.drafts[(long long)s * (a.rows_per_seq - 1) + tid];
+                if (id >= c0 && id - c0 < n) {
+                    t = id - c0;
+                    atomicOr(&count[t], IS_DRAFT);
+                    flag[t / G] = 1;
+                }
             }
+            draft[tid] = t;
         }
     }
-    if (a.bias_ids) {
+    if (a.bias_ids)
         for (int i = tid; i < a.bias_width; i += NT) {
             const int id = a.bias_ids[(long long)s * a.bias_width + i];
-            const unsigned t = (unsigned)(id - c0);
-            if (id >= 0 && t < (unsigned)n) {
-                atomicMax(&bias[t], i + 1);
-                flag[t >> 2] = 1;
+            if (id >= c0 && id - c0 < n) {
+                atomicMax(&bias[id - c0], i + 1);
+                flag[(id - c0) / G] = 1;
             }
         }
-    }
     __syncthreads();
+    if (rules) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+            if (flag[tid + i * NT]) list[atomicAdd(&n_list, 1)] = (uint16_t)(tid + i * NT);
+        __syncthreads();
+    }
 
-    const float* bv = a.bias_values + (long long)s * a.bias_width;
-    for (int j = 0; j < a.rows_per_seq; ++j) {
-        const long long row = (long long)s * a.rows_per_seq + j;
-        const T* x = reinterpret_cast<const T*>(a.logits) + row * a.ld_logits + c0;
-        T* y = reinterpret_cast<T*>(a.out) + row * a.ld_out + c0;
-        const uint32_t* mask = nullptr;
-        if (a.masks) {
-            const int m = a.mask_index[row];
-            if (m >= 0 && m < a.n_masks) mask = a.masks + (long long)m * a.ld_mask + (c0 >> 5);
-        }
-        const uint32_t before = (1u << j) - 1u;  // drafts 0 .. j-1
-        if (VEC) {
-#pragma unroll 4
-            for (int g = tid; g < n / 4; g += NT) {
-                const int t = 4 * g;
-                const uint32_t bits = mask ? (mask[t >> 5] >> (t & 31)) & 15u : 15u;
-                const bool touched = flag[g] != 0;
-                if (inplace && !touched && bits == 15u) continue;
-                float v[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-                Vec4<T> io;
-                if (bits) {
-                    io = *reinterpret_cast<const Vec4<T>*>(x + t);
-                    if (bits != 15u || touched) {
-                        float l[4];
-                        io.get(l);
+    // ---- the stream: vectors without a touched token
+    const int nvec = VEC ? n / G : 0;
+    if (VEC) {
+        constexpr uint32_t ALL = (1u << G) - 1u;
+        auto mask_of = [&](int j) -> const uint32_t* {
+            return j < rows && midx[j] >= 0 ? a.masks + (long long)midx[j] * a.ld_mask + (c0 >> 5) : nullptr;
+        };
+        uint32_t bits[NV], next[NV];  // mask bits of the row whose logits are loaded next, and of the row after
+        uint4 x[NV];
+        auto load_mask = [&](int j, uint32_t (&b)[NV]) {
+            const uint32_t* m = mask_of(j);
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                const int t = (tid + i * NT) * G;
+                b[i] = m && t < n ? m[t >> 5] >> (t & 31) & ALL : ALL;
+            }
+        };
+        // in place, only vectors that the mask changes are touched
+        auto live = [&](int i, uint32_t b) {
+            const int v = tid + i * NT;
+            return v < nvec && !flag[v] && !(inplace && b == ALL);
+        };
+        auto load = [&](int j, const uint32_t (&b)[NV]) {
+#pragma unroll
+            for (int i = 0; i < NV; ++i)
+                if (live(i, b[i]) && b[i]) x[i] = *reinterpret_cast<const uint4*>(X + j * a.ld_logits + (tid + i * NT) * G);
+        };
+        load_mask(0, bits);
+        load_mask(1, next);
+        load(0, bits);
+#pragma unroll 1
+        for (int j = 0; j < rows; ++j) {
+            uint4 y[NV];
+            uint32_t b[NV];
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                y[i] = x[i];
+                b[i] = bits[i];
+                bits[i] = next[i];
+            }
+            load_mask(j + 2, next);
+            if (j + 1 < rows) load(j + 1, bits);
+#pragma unroll
+            for (int i = 0; i < NV; ++i)
+                if (live(i, b[i])) {
+                    uint32_t w[4] = {y[i].x, y[i].y, y[i].z, y[i].w};
+                    if (b[i] != ALL) {
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
-                            if (touched) {
-                                l[e] = apply(l[e], count[t + e], __popc(draft[t + e] & before), rule);
-                                if (bias[t + e]) l[e] += bv[bias[t + e] - 1];
+                            if (sizeof(T) == 4) {
+                                if (!(b[i] >> e & 1u)) w[e] = 0xFF800000u;
+                            } else {
+                                if (!(b[i] >> (2 * e) & 1u)) w[e] = (w[e] & 0xFFFF0000u) | 0xFF80u;
+                                if (!(b[i] >> (2 * e + 1) & 1u)) w[e] = (w[e] & 0xFFFFu) | 0xFF800000u;
                             }
-                            if ((bits >> e) & 1u) v[e] = l[e];
                         }
-                        io.set(v);
                     }
-                } else {
-                    io.set(v);
+                    *reinterpret_cast<uint4*>(Y + j * a.ld_out + (tid + i * NT) * G) = make_uint4(w[0], w[1], w[2], w[3]);
                 }
-                *reinterpret_cast<Vec4<T>*>(y + t) = io;
+        }
+    }
+
+    // ---- single tokens: the touched vectors, and what the stream's vectors do not cover (the last vocab % G
+    // tokens, or everything when rows are not aligned)
+    const float* bv = a.bias_values + (long long)s * a.bias_width;
+    auto token = [&](int j, int t, bool touched) {
+        const int m = midx[j];
+        const bool on = m < 0 || (a.masks[(long long)m * a.ld_mask + ((c0 + t) >> 5)] >> ((c0 + t) & 31) & 1u);
+        if (inplace && on && !touched) return;
+        float l = -INFINITY;
+        if (on) {
+            l = to_f32(X[j * a.ld_logits + t]);
+            if (touched) {
+                const uint32_t w = count[t];
+                uint32_t c = w & COUNT;
+                if (w & IS_DRAFT)
+#pragma unroll 1
+                    for (int i = 0; i < j0 + j; ++i) c += draft[i] == t;
+                if (c || (w & IN_PROMPT)) l = l > 0.f ? l / rep : l * rep;
+                l -= freq * (float)c;
+                if (c) l -= pres;
+                if (a.bias_ids && bias[t]) l += bv[bias[t] - 1];
             }
         }
-        // scalar: rows that are not aligned, and the last vocab % 4 tokens
-        for (int t = (VEC ? (n & ~3) : 0) + tid; t < n; t += NT) {
-            const bool on = mask ? (mask[t >> 5] >> (t & 31)) & 1u : true;
-            const bool touched = flag[t >> 2] != 0;
-            if (inplace && !touched && on) continue;
-            float l = -INFINITY;
-            if (on) {
-                l = to_f32(x[t]);
-                if (touched) {
-                    l = apply(l, count[t], __popc(draft[t] & before), rule);
-                    if (bias[t]) l += bv[bias[t] - 1];
-                }
-            }
-            y[t] = from_f32<T>(l);
-        }
+        Y[j * a.ld_out + t] = from_f32<T>(l);
+    };
+    const int per = rules ? n_list * G : 0, total = per * rows;
+#pragma unroll 2
+    for (int i = tid; i < total; i += NT) {
+        const int j = i / per, k = i - j * per, t = list[k / G] * G + k % G;
+        if (t < n) token(j, t, true);
+    }
+    const int from = nvec * G, left = (n - from) * rows;
+#pragma unroll 4
+    for (int i = tid; i < left; i += NT) {
+        const int j = i / (n - from), t = from + i - j * (n - from);
+        if (!(rules && flag[t / G])) token(j, t, false);
     }
 }
 
+template <typename T, int NV>
+void run(const Launch& L, const dflash_logits_args& a) {
+    Plan pl;
+    pl.chunk = NT * NV * 16 / (int)sizeof(T);
+    const int chunks = (a.vocab + pl.chunk - 1) / pl.chunk;
+    // few CTAs (short batch): the rows of a sequence go to several, each of which reads the history again
+    pl.groups = (int)std::min<long long>(a.rows_per_seq, std::max(1ll, 608ll / ((long long)chunks * a.batch)));
+    pl.rows = (a.rows_per_seq + pl.groups - 1) / pl.groups;
+    pl.groups = (a.rows_per_seq + pl.rows - 1) / pl.rows;
+    const bool vec = (((uintptr_t)a.logits | (uintptr_t)a.out) % 16) == 0 && a.ld_logits % (16 / (int)sizeof(T)) == 0 &&
+                     a.ld_out % (16 / (int)sizeof(T)) == 0;
+    const size_t smem = a.bias_ids ? (size_t)pl.chunk * 4 : 0;
+    launch_k(L, vec ? logit_rules_kernel<T, NV, true> : logit_rules_kernel<T, NV, false>,
+             dim3(chunks, (unsigned)(a.batch * pl.groups)), dim3(NT), smem, 1, a, pl);
+}
+
+// Vectors per thread: two, unless that leaves fewer than two CTAs an SM.
 template <typename T>
 void run(const Launch& L, const dflash_logits_args& a) {
-    // chunk: the largest of 4096 .. 1024 tokens that still gives about two CTAs an SM
-    int chunk = 4096;
-    while (chunk > 1024 && (long long)a.batch * ((a.vocab + chunk - 1) / chunk) < 2 * 152) chunk /= 2;
-    const size_t smem = (size_t)chunk * 12 + chunk / 4;
-    const size_t al = 4 * sizeof(T);
-    const bool vec = (((uintptr_t)a.logits | (uintptr_t)a.out) % al) == 0 && a.ld_logits % 4 == 0 && a.ld_out % 4 == 0;
-    const dim3 grid((a.vocab + chunk - 1) / chunk, a.batch);
-    auto k = vec ? logit_rules_kernel<T, true> : logit_rules_kernel<T, false>;
-    if (smem > 48 * 1024 &&
-        cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
-        L.fail();
-    launch_k(L, k, grid, dim3(NT), smem, 1, a, chunk);
+    const int chunk2 = NT * 2 * 16 / (int)sizeof(T);
+    if ((long long)a.batch * ((a.vocab + chunk2 - 1) / chunk2) >= 304) run<T, 2>(L, a);
+    else run<T, 1>(L, a);
 }
 
 }  // namespace
