@@ -8,14 +8,12 @@
 // sequence.  It first turns the sequence's history and biases into one or two
 // words per token of its chunk in shared memory (counts by integer atomics, so the
 // order is immaterial): the history is read once per chunk instead of once per
-// row, from L2.  Then
-//   - the stream: 16-byte vectors without a touched token are copied under the
-//     row's mask, a row ahead of the stores; the mask words of the row after that
-//     are under way, so no load waits for another.  A vector that its mask closes
-//     entirely is not read;
-//   - the touched vectors, collected in a list, a thread per token: they are few,
-//     but sit together (frequent ids), so spreading them over the CTA keeps one
-//     warp from doing them all, and the rule's code exists once.
+// row, from L2.  Then 16-byte vectors stream by, a row ahead of the stores, with
+// the mask words of the row after that under way, so no load waits for another; a
+// vector that its mask closes entirely is not read, and a flag byte per vector says
+// whether its words are looked up at all.  (Collecting the touched tokens in a list
+// for a pass of their own took 147 us where this takes 110 us at 512 rows of 151936: frequent ids sit
+// together, so the CTAs of the first chunk had nearly all of that pass to do.)
 // Drafts stay a list of at most 31 ids: a token that is a draft carries a bit, and
 // only such tokens count the drafts before their row.
 #include <math.h>
@@ -31,6 +29,24 @@ namespace {
 constexpr int NT = 256;
 constexpr uint32_t IN_PROMPT = 0x80000000u, IS_DRAFT = 0x40000000u, COUNT = 0x3FFFFFFFu;
 
+// A sequence's penalties; x / repetition is x times the reciprocal (one rounding more).
+struct Rules {
+    float rep, inv, pres, freq;
+    const float* bias;  // the sequence's bias_values
+    const int* draft;   // [31] tokens of the chunk, -1: none there
+};
+// The rule of token t (word w, bias entry b - 1) in the j-th row of the sequence.
+__device__ __forceinline__ float apply(float x, uint32_t w, int b, int t, int j, const Rules& r) {
+    uint32_t c = w & COUNT;
+    if (w & IS_DRAFT)
+#pragma unroll 1
+        for (int i = 0; i < j; ++i) c += r.draft[i] == t;
+    if (c || (w & IN_PROMPT)) x *= x > 0.f ? r.inv : r.rep;
+    if (c) x = x - r.freq * (float)c - r.pres;
+    if (b) x += r.bias[b - 1];
+    return x;
+}
+
 struct Plan {
     int chunk;   // tokens per CTA
     int rows;    // rows per CTA
@@ -45,8 +61,7 @@ __global__ void __launch_bounds__(NT) logit_rules_kernel(dflash_logits_args a, P
     constexpr int CH = NT * NV * G;
     __shared__ __align__(16) uint32_t count[CH];       // occurrences after the prompt | IN_PROMPT | IS_DRAFT
     __shared__ __align__(16) uint32_t flag4[CH / G / 4];  // a byte per vector: a rule touches it
-    __shared__ uint16_t list[CH / G];                  // the touched vectors
-    __shared__ int n_list, draft[32], midx[32];
+    __shared__ int draft[32], midx[32];
     extern __shared__ __align__(16) int bias[];        // [CH] 1 + last bias entry of the token, 0: none (bias_ids given)
     uint8_t* flag = reinterpret_cast<uint8_t*>(flag4);
     const int tid = threadIdx.x;
@@ -60,12 +75,52 @@ __global__ void __launch_bounds__(NT) logit_rules_kernel(dflash_logits_args a, P
     pdl_wait();
     pdl_trigger();
 
-    // ---- the chunk's words
+    // ---- the first row's mask words and vectors, under way while the words are made
+    constexpr uint32_t ALL = (1u << G) - 1u;
+    const int nvec = VEC ? n / G : 0;
+    uint32_t bits[NV], next[NV];  // mask bits of the row whose logits are loaded next, and of the row after
+    uint4 x[NV];
+    auto mask_bits = [&](int m, uint32_t (&b)[NV]) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int t = (tid + i * NT) * G;
+            b[i] = m >= 0 && t < n ? a.masks[(long long)m * a.ld_mask + ((c0 + t) >> 5)] >> (t & 31) & ALL : ALL;
+        }
+    };
+    auto load_mask = [&](int j, uint32_t (&b)[NV]) { mask_bits(j < rows ? midx[j] : -1, b); };
+    // in place, only vectors that a rule or the mask changes are touched
+    auto live = [&](int i, uint32_t b) {
+        const int v = tid + i * NT;
+        return v < nvec && (!inplace || b != ALL || flag[v]);
+    };
+    auto load = [&](int j, const uint32_t (&b)[NV]) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+            if (live(i, b[i]) && b[i]) x[i] = *reinterpret_cast<const uint4*>(X + j * a.ld_logits + (tid + i * NT) * G);
+    };
+    if (VEC) {
+        const int m = a.masks ? a.mask_index[row0] : -1;
+        mask_bits(m < a.n_masks ? m : -1, bits);
+        if (!inplace) load(0, bits);
+    }
+
+    // ---- the chunk's words: the first reads of the lists go out before the barrier
+    int len = 0, prompt = 0, lead = 0, quads = 0, bias_id = -1;
+    const int* h = nullptr;
+    int4 first = make_int4(-1, -1, -1, -1);
+    if (a.history) {
+        len = min(max(a.hist_lens[s], 0), a.hist_width);
+        prompt = min(max(a.prompt_lens[s], 0), len);
+        h = a.history + (long long)s * a.ld_hist;
+        lead = min(len, (int)((16 - ((uintptr_t)h & 15)) & 15) / 4);
+        quads = (len - lead) / 4;
+        if (tid < quads) first = *reinterpret_cast<const int4*>(h + lead + 4 * tid);
+    }
+    if (a.bias_ids && tid < a.bias_width) bias_id = a.bias_ids[(long long)s * a.bias_width + tid];
     if (tid < rows) {
         const int m = a.masks ? a.mask_index[row0 + tid] : -1;
         midx[tid] = m < a.n_masks ? m : -1;
     }
-    if (tid == 0) n_list = 0;
     if (rules) {
         uint4* z = reinterpret_cast<uint4*>(count);
 #pragma unroll
@@ -78,14 +133,12 @@ __global__ void __launch_bounds__(NT) logit_rules_kernel(dflash_logits_args a, P
     }
     for (int i = tid; i < CH / G / 4; i += NT) flag4[i] = 0u;
     __syncthreads();
-    float rep = 1.f, pres = 0.f, freq = 0.f;
+    Rules rule = {1.f, 1.f, 0.f, 0.f, a.bias_values + (long long)s * a.bias_width, draft};
     if (a.history) {
-        if (a.repetition) rep = a.repetition[s];
-        if (a.presence) pres = a.presence[s];
-        if (a.frequency) freq = a.frequency[s];
-        const int len = min(max(a.hist_lens[s], 0), a.hist_width);
-        const int prompt = min(max(a.prompt_lens[s], 0), len);
-        const int* h = a.history + (long long)s * a.ld_hist;
+        if (a.repetition) rule.rep = a.repetition[s];
+        if (a.presence) rule.pres = a.presence[s];
+        if (a.frequency) rule.freq = a.frequency[s];
+        rule.inv = 1.f / rule.rep;
         auto mark = [&](int id, int i) {
             const unsigned t = (unsigned)id - (unsigned)c0;
             if (id >= 0 && t < (unsigned)n) {
@@ -94,11 +147,11 @@ __global__ void __launch_bounds__(NT) logit_rules_kernel(dflash_logits_args a, P
                 flag[t / G] = 1;
             }
         };
-        const int lead = min(len, (int)((16 - ((uintptr_t)h & 15)) & 15) / 4), quads = (len - lead) / 4;
         if (tid < lead) mark(h[tid], tid);
-#pragma unroll 2
+#pragma unroll 1
         for (int q = tid; q < quads; q += NT) {
-            const int4 v = *reinterpret_cast<const int4*>(h + lead + 4 * q);
+            const int4 v = first;
+            if (q + NT < quads) first = *reinterpret_cast<const int4*>(h + lead + 4 * (q + NT));
             const int i = lead + 4 * q;
             mark(v.x, i);
             mark(v.y, i + 1);
@@ -122,50 +175,18 @@ __global__ void __launch_bounds__(NT) logit_rules_kernel(dflash_logits_args a, P
     }
     if (a.bias_ids)
         for (int i = tid; i < a.bias_width; i += NT) {
-            const int id = a.bias_ids[(long long)s * a.bias_width + i];
+            const int id = i == tid ? bias_id : a.bias_ids[(long long)s * a.bias_width + i];
             if (id >= c0 && id - c0 < n) {
                 atomicMax(&bias[id - c0], i + 1);
                 flag[(id - c0) / G] = 1;
             }
         }
     __syncthreads();
-    if (rules) {
-#pragma unroll
-        for (int i = 0; i < NV; ++i)
-            if (flag[tid + i * NT]) list[atomicAdd(&n_list, 1)] = (uint16_t)(tid + i * NT);
-        __syncthreads();
-    }
 
-    // ---- the stream: vectors without a touched token
-    const int nvec = VEC ? n / G : 0;
+    // ---- the stream
     if (VEC) {
-        constexpr uint32_t ALL = (1u << G) - 1u;
-        auto mask_of = [&](int j) -> const uint32_t* {
-            return j < rows && midx[j] >= 0 ? a.masks + (long long)midx[j] * a.ld_mask + (c0 >> 5) : nullptr;
-        };
-        uint32_t bits[NV], next[NV];  // mask bits of the row whose logits are loaded next, and of the row after
-        uint4 x[NV];
-        auto load_mask = [&](int j, uint32_t (&b)[NV]) {
-            const uint32_t* m = mask_of(j);
-#pragma unroll
-            for (int i = 0; i < NV; ++i) {
-                const int t = (tid + i * NT) * G;
-                b[i] = m && t < n ? m[t >> 5] >> (t & 31) & ALL : ALL;
-            }
-        };
-        // in place, only vectors that the mask changes are touched
-        auto live = [&](int i, uint32_t b) {
-            const int v = tid + i * NT;
-            return v < nvec && !flag[v] && !(inplace && b == ALL);
-        };
-        auto load = [&](int j, const uint32_t (&b)[NV]) {
-#pragma unroll
-            for (int i = 0; i < NV; ++i)
-                if (live(i, b[i]) && b[i]) x[i] = *reinterpret_cast<const uint4*>(X + j * a.ld_logits + (tid + i * NT) * G);
-        };
-        load_mask(0, bits);
         load_mask(1, next);
-        load(0, bits);
+        if (inplace) load(0, bits);  // (which vectors change is known only now)
 #pragma unroll 1
         for (int j = 0; j < rows; ++j) {
             uint4 y[NV];
@@ -182,6 +203,32 @@ __global__ void __launch_bounds__(NT) logit_rules_kernel(dflash_logits_args a, P
             for (int i = 0; i < NV; ++i)
                 if (live(i, b[i])) {
                     uint32_t w[4] = {y[i].x, y[i].y, y[i].z, y[i].w};
+                    const int v = tid + i * NT;
+                    if (b[i] && flag[v]) {
+#pragma unroll
+                        for (int q = 0; q < G / 4; ++q) {  // four tokens at a time
+                            const uint4 cw = *reinterpret_cast<const uint4*>(count + v * G + 4 * q);
+                            int4 bw = make_int4(0, 0, 0, 0);
+                            if (a.bias_ids) bw = *reinterpret_cast<const int4*>(bias + v * G + 4 * q);
+                            const uint32_t c4[4] = {cw.x, cw.y, cw.z, cw.w};
+                            const int b4[4] = {bw.x, bw.y, bw.z, bw.w};
+                            float l[4];
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                if (sizeof(T) == 4) l[e] = __uint_as_float(w[e]);
+                                else l[e] = __uint_as_float(e & 1 ? w[2 * q + e / 2] & 0xFFFF0000u : w[2 * q + e / 2] << 16);
+                                l[e] = apply(l[e], c4[e], b4[e], v * G + 4 * q + e, j0 + j, rule);
+                            }
+                            if (sizeof(T) == 4) {
+#pragma unroll
+                                for (int e = 0; e < 4; ++e) w[e] = __float_as_uint(l[e]);
+                            } else {
+                                const __nv_bfloat162 p0 = __floats2bfloat162_rn(l[0], l[1]), p1 = __floats2bfloat162_rn(l[2], l[3]);
+                                w[(2 * q) & 3] = *reinterpret_cast<const uint32_t*>(&p0);
+                                w[(2 * q + 1) & 3] = *reinterpret_cast<const uint32_t*>(&p1);
+                            }
+                        }
+                    }
                     if (b[i] != ALL) {
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
@@ -198,41 +245,21 @@ __global__ void __launch_bounds__(NT) logit_rules_kernel(dflash_logits_args a, P
         }
     }
 
-    // ---- single tokens: the touched vectors, and what the stream's vectors do not cover (the last vocab % G
-    // tokens, or everything when rows are not aligned)
-    const float* bv = a.bias_values + (long long)s * a.bias_width;
-    auto token = [&](int j, int t, bool touched) {
-        const int m = midx[j];
-        const bool on = m < 0 || (a.masks[(long long)m * a.ld_mask + ((c0 + t) >> 5)] >> ((c0 + t) & 31) & 1u);
-        if (inplace && on && !touched) return;
-        float l = -INFINITY;
-        if (on) {
-            l = to_f32(X[j * a.ld_logits + t]);
-            if (touched) {
-                const uint32_t w = count[t];
-                uint32_t c = w & COUNT;
-                if (w & IS_DRAFT)
-#pragma unroll 1
-                    for (int i = 0; i < j0 + j; ++i) c += draft[i] == t;
-                if (c || (w & IN_PROMPT)) l = l > 0.f ? l / rep : l * rep;
-                l -= freq * (float)c;
-                if (c) l -= pres;
-                if (a.bias_ids && bias[t]) l += bv[bias[t] - 1];
-            }
-        }
-        Y[j * a.ld_out + t] = from_f32<T>(l);
-    };
-    const int per = rules ? n_list * G : 0, total = per * rows;
-#pragma unroll 2
-    for (int i = tid; i < total; i += NT) {
-        const int j = i / per, k = i - j * per, t = list[k / G] * G + k % G;
-        if (t < n) token(j, t, true);
-    }
+    // ---- single tokens: the last vocab % G of them, or everything when rows are not aligned
     const int from = nvec * G, left = (n - from) * rows;
 #pragma unroll 4
     for (int i = tid; i < left; i += NT) {
         const int j = i / (n - from), t = from + i - j * (n - from);
-        if (!(rules && flag[t / G])) token(j, t, false);
+        const int m = midx[j];
+        const bool on = m < 0 || (a.masks[(long long)m * a.ld_mask + ((c0 + t) >> 5)] >> ((c0 + t) & 31) & 1u);
+        const bool touched = rules && flag[t / G];
+        if (inplace && on && !touched) continue;
+        float l = -INFINITY;
+        if (on) {
+            l = to_f32(X[j * a.ld_logits + t]);
+            if (touched) l = apply(l, count[t], a.bias_ids ? bias[t] : 0, t, j0 + j, rule);
+        }
+        Y[j * a.ld_out + t] = from_f32<T>(l);
     }
 }
 
