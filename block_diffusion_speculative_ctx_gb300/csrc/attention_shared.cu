@@ -1,9 +1,12 @@
 // Attention of a batch that shares a prefix (dflash_shared_prefix_attention in
-// include/dflash.h).
+// include/dflash.h): the entry, its checks, and the merge of the partial results
+// that the main kernels (attention_shared_tc.cu for bf16, attention_shared_f32.cu)
+// leave per segment of the plan (shared_plan.cuh).
 //
-// Simplest form: one warp per (row, query head) walks the row's keys, prefix
-// then own, with an online softmax in fp32 (base 2); lane l holds head
-// dimensions l, l + 32, ...  Every key is read once per query vector.
+// What a call cannot do without: the prefix's keys and values once per call (not
+// once per sequence: 2 * H_kv * hd * prefix_len elements), each sequence's own
+// keys and values once, q and out once, and 4 * hd operations per query vector
+// and key.
 #include <math.h>
 
 #include <algorithm>
@@ -14,69 +17,6 @@
 namespace dfl {
 
 namespace {
-
-template <typename T, int HD>
-__global__ void __launch_bounds__(128) shared_simple_kernel(dflash_shared_prefix_args a) {
-    pdl_wait();
-    pdl_trigger();
-    constexpr int PER = HD / 32;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int r = blockIdx.x, h = blockIdx.y * 4 + warp;
-    if (h >= a.n_heads) return;
-    // the row's sequence: the last s with q_start[s] <= r
-    int lo = 0, hi = a.batch;
-    if (r < a.q_start[0] || r >= a.q_start[a.batch]) return;
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (a.q_start[mid] <= r) lo = mid;
-        else hi = mid;
-    }
-    const int s = lo, start = a.q_start[s], m = a.q_start[s + 1] - start;
-    const int own = a.kv_lens[s];
-    bool bad = start < 0 || m <= 0 || start + m > a.rows || own < 0 || (long long)own > 64ll * a.width;
-    const int lim = bad ? 0 : (a.causal ? max(own - m + (r - start) + 1, 0) : own);
-    const int kvh = h / (a.n_heads / a.n_kv_heads);
-    const T* q = reinterpret_cast<const T*>(a.q) + (long long)r * a.ld_q + (long long)h * HD;
-    float qv[PER], o[PER];
-#pragma unroll
-    for (int i = 0; i < PER; ++i) {
-        qv[i] = to_f32(q[lane + 32 * i]);
-        o[i] = 0.f;
-    }
-    const float sl = a.scale * 1.4426950408889634f;
-    float mx = -INFINITY, l = 0.f;
-    auto walk = [&](const int* pages, int n) {
-        for (int k = 0; k < n; ++k) {
-            const int page = pages[k >> 6];
-            if (page < 0 || page >= a.n_pages) {
-                bad = true;
-                return;
-            }
-            const long long off = (((long long)page * a.n_kv_heads + kvh) * 64 + (k & 63)) * HD;
-            const T* K = reinterpret_cast<const T*>(a.k_cache) + off;
-            const T* V = reinterpret_cast<const T*>(a.v_cache) + off;
-            float d = 0.f;
-#pragma unroll
-            for (int i = 0; i < PER; ++i) d += qv[i] * to_f32(K[lane + 32 * i]);
-            d = warp_sum(d) * sl;
-            const float mn = fmaxf(mx, d);
-            const float al = mx == -INFINITY ? 0.f : exp2f(mx - mn), p = exp2f(d - mn);
-            l = l * al + p;
-#pragma unroll
-            for (int i = 0; i < PER; ++i) o[i] = o[i] * al + p * to_f32(V[lane + 32 * i]);
-            mx = mn;
-        }
-    };
-    if (!bad) walk(a.prefix_pages, a.prefix_len);
-    if (!bad) walk(a.table + (long long)s * a.ld_table, lim);
-    const float inv = bad ? NAN : l > 0.f ? 1.f / l : 0.f;
-    T* out = reinterpret_cast<T*>(a.out) + (long long)r * a.ld_out + (long long)h * HD;
-#pragma unroll
-    for (int i = 0; i < PER; ++i) out[lane + 32 * i] = from_f32<T>(bad ? NAN : o[i] * inv);
-    if (a.lse && lane == 0)
-        a.lse[(long long)r * a.n_heads + h] = bad ? NAN : l > 0.f ? (mx + log2f(l)) * 0.6931471805599453f : -INFINITY;
-}
-
 
 // Merge of the partial results: out = sum_i 2^(m_i - M) o_i / sum_i 2^(m_i - M) l_i over the segments that
 // hold the row's query vectors, prefix and own, in plan order (one fixed order: the same bits every run).
@@ -236,42 +176,52 @@ __global__ void __launch_bounds__(32 * MWARPS, 4) merge_kernel(MergeArgs a) {
 }  // namespace
 
 bool shared_attention_tc(const Launch& L, const sp::Shape& P, const sp::Work& W, const dflash_shared_prefix_args& a);
+bool shared_attention_f32(const Launch& L, const sp::Shape& P, const sp::Work& W, const dflash_shared_prefix_args& a);
 
 namespace {
 
 constexpr int CTAS = 152;  // one per SM
 
 // The sizes alone (what the workspace depends on).
-sp::Shape sizes_of(int H, int Hkv, int hd, int batch, int rows) {
+sp::Shape sizes_of(bool f32, int H, int Hkv, int hd, int batch, int rows) {
     sp::Shape P = {};
     P.H = H;
-    P.Hkv = Hkv;
+    P.VT = f32 ? 32 : 128;
     P.g = H / Hkv;
+    P.parts = 1;
+    while (P.g % P.parts || P.g / P.parts > P.VT) ++P.parts;
+    P.Hkv = Hkv * P.parts;
+    P.g /= P.parts;
     P.hd = hd;
-    P.VT = 128;
     P.RH = P.VT / P.g;
-    P.KT = 64;
+    P.KT = f32 ? 32 : 64;
+    P.one_line = f32;
     P.batch = batch;
     P.rows = rows;
     P.n_cta = CTAS;
     // an item's fixed cost: two tiles on line 0, three on line 1
     P.lead[0] = 2;
-    P.lead[1] = 3;
+    P.lead[1] = f32 ? 1 : 3;
     return P;
+}
+
+template <typename T>
+void merge(const Launch& L, const MergeArgs& m) {
+    // the merge starts as the main kernel's CTAs leave
+    Launch after = L;
+    after.pdl = true;
+    // rows of one stream: the prefix is split over nearly every worker of its line, else over a few
+    if (m.P.rows <= m.P.RH) launch_k(after, merge_kernel<T, MWARPS>, dim3(m.P.rows, m.P.Hkv), dim3(32 * MWARPS), 0, 1, m);
+    else launch_k(after, merge_kernel<T, 1>, dim3((m.P.rows + MWARPS - 1) / MWARPS, m.P.Hkv), dim3(32 * MWARPS), 0, 1, m);
 }
 
 }  // namespace
 
 bool shared_prefix_attention(const Launch& L, const dflash_shared_prefix_args& a) {
-    if (a.dtype == DFLASH_DTYPE_F32) {
-        const dim3 grid(a.rows, (a.n_heads + 3) / 4);
-        if (a.head_dim == 128) launch_k(L, shared_simple_kernel<float, 128>, grid, dim3(128), 0, 1, a);
-        else launch_k(L, shared_simple_kernel<float, 64>, grid, dim3(128), 0, 1, a);
-        return true;
-    }
+    const bool f32 = a.dtype == DFLASH_DTYPE_F32;
     MergeArgs m;
     sp::Shape& P = m.P;
-    P = sizes_of(a.n_heads, a.n_kv_heads, a.head_dim, a.batch, a.rows);
+    P = sizes_of(f32, a.n_heads, a.n_kv_heads, a.head_dim, a.batch, a.rows);
     P.width = a.width;
     P.prefix_len = a.prefix_len;
     P.causal = a.causal != 0;
@@ -286,13 +236,9 @@ bool shared_prefix_attention(const Launch& L, const dflash_shared_prefix_args& a
     m.out = a.out;
     m.lse = a.lse;
     m.ld_out = a.ld_out;
-    if (!shared_attention_tc(L, P, m.W, a)) return false;
-    // the merge starts as the main kernel's CTAs leave
-    Launch after = L;
-    after.pdl = true;
-    // rows of one stream: the prefix is split over nearly every worker of its line, else over a few
-    if (a.rows <= P.RH) launch_k(after, merge_kernel<bf16, MWARPS>, dim3(a.rows, a.n_kv_heads), dim3(32 * MWARPS), 0, 1, m);
-    else launch_k(after, merge_kernel<bf16, 1>, dim3((a.rows + MWARPS - 1) / MWARPS, a.n_kv_heads), dim3(32 * MWARPS), 0, 1, m);
+    if (!(f32 ? shared_attention_f32(L, P, m.W, a) : shared_attention_tc(L, P, m.W, a))) return false;
+    if (f32) merge<float>(L, m);
+    else merge<bf16>(L, m);
     return true;
 }
 
@@ -341,7 +287,7 @@ extern "C" size_t dflash_shared_prefix_workspace(int32_t dtype, int32_t n_heads,
         batch > DFLASH_OPS_MAX_BATCH || rows < 0 || rows > (1 << 20) || (head_dim != 64 && head_dim != 128) ||
         (dtype != DFLASH_DTYPE_F32 && dtype != DFLASH_DTYPE_BF16))
         return 0;
-    return sp::layout(nullptr, sizes_of(n_heads, n_kv_heads, head_dim, batch, rows), nullptr);
+    return sp::layout(nullptr, sizes_of(dtype == DFLASH_DTYPE_F32, n_heads, n_kv_heads, head_dim, batch, rows), nullptr);
 }
 
 extern "C" dflash_status dflash_shared_prefix_attention(const dflash_shared_prefix_args* p, void* cuda_stream) {

@@ -248,19 +248,8 @@ __global__ void __launch_bounds__(NTHR, 1)
     make_plan<NTHR>(P, base, ibase, &bars->plan, h);  // (its barriers order the setup above)
     fence_after();
     const uint32_t tmem = bars->tmem;
-    // for the merge kernel: the head, and a warp per sequence its record and its rows' map
     if (cta == 0 && tid == 0) *a.W.head = h;
-    if (!h.bad)
-#pragma unroll 1
-        for (int q = warp * P.n_cta + cta; q < P.batch; q += P.n_cta * (NTHR / 32)) {
-            const int start = P.q_start[q], m = P.q_start[q + 1] - start;
-            if (lane == 0) {
-                Rec r = {start, m, P.kv_lens[q], base[(m > P.RH ? 0 : MAX_BATCH) + q], ibase[q], {0u, 0u, 0u}};
-                a.W.rec[q] = r;
-            }
-#pragma unroll 1
-            for (int i = lane; i < m; i += 32) a.W.row_seq[start + i] = q;
-        }
+    if (!h.bad) write_records(P, a.W, base, ibase, cta, P.n_cta, warp, NTHR / 32, lane);
     uint32_t* err = &a.W.err[cta];
     Waiter wait{err, &bars->fail};
 

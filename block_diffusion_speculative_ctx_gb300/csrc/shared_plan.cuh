@@ -34,6 +34,8 @@ struct Shape {
     int npt;       // prefix tiles
     int n_cta;
     int lead[2];   // an item's fixed cost in tiles (per line)
+    int one_line;  // every item on line 1, row tiles of one stream
+    int parts;     // KV heads here per KV head of the caches (more query heads than VT are split)
     long long ld_table;
     const int *prefix_pages, *table, *kv_lens, *q_start;
     __host__ __device__ int row_tile(int line) const { return line == 0 ? 2 * RH : RH; }
@@ -72,10 +74,10 @@ struct Work {
 
 // Blocks: line 0 takes two per (item, worker), line 1 one.
 inline long long max_blocks(const Shape& P) {
-    const long long RT = 2 * P.RH;
+    const long long RT = P.row_tile(P.one_line);
     // prefix row tiles; own items: every sequence adds at most one partial row tile to the full ones
     const long long items = P.Hkv * ((P.rows + RT - 1) / RT + P.rows / RT + (P.batch < P.rows ? P.batch : P.rows));
-    return 2 * (items + P.n_cta) + 2 * P.n_cta;
+    return (P.one_line ? items + 2 * P.n_cta : 2 * (items + P.n_cta)) + 2 * P.n_cta;
 }
 
 inline size_t layout(char* p, const Shape& P, Work* w) {
@@ -112,7 +114,7 @@ __device__ __forceinline__ Seq seq_of(const Shape& P, int start, int end, int kv
     Seq q;
     q.m = end - start;
     q.kv = kv;
-    q.line = q.m > P.RH ? 0 : 1;
+    q.line = q.m > P.RH && !P.one_line ? 0 : 1;
     const bool ok = q.m > 0 && kv > 0 && kv <= (long long)64 * P.width;
     q.tiles = ok ? cdiv(kv, P.KT) : 0;
     q.groups = q.tiles ? cdiv(q.m, P.row_tile(q.line)) : 0;
@@ -224,7 +226,7 @@ __device__ __forceinline__ void make_plan(const Shape& P, uint32_t* base, uint32
         h.r_begin = h.r_end = 0;
     }
     const int live = h.r_end - h.r_begin;
-    h.pl = live > P.RH ? 0 : 1;
+    h.pl = live > P.RH && !P.one_line ? 0 : 1;
     h.nqt = cdiv(live, P.row_tile(h.pl));
     h.n_prefix = P.npt ? h.nqt * P.Hkv : 0;
     const unsigned long long cp = (unsigned long long)h.n_prefix * (unsigned)(P.lead[h.pl] + P.npt);
@@ -287,6 +289,21 @@ __device__ __forceinline__ void make_plan(const Shape& P, uint32_t* base, uint32
         h.part[l] = max(1u, (h.W[l] + P.workers(l) - 1) / P.workers(l));
     }
     h.items0 = carry[2] + (h.pl == 0 ? (uint32_t)h.n_prefix : 0u);
+}
+
+// For the merge kernel: a warp per sequence writes its record and its rows' map.
+__device__ __forceinline__ void write_records(const Shape& P, const Work& W, const uint32_t* base, const uint32_t* ibase,
+                                              int cta, int ctas, int warp, int warps, int lane) {
+#pragma unroll 1
+    for (int q = warp * ctas + cta; q < P.batch; q += ctas * warps) {
+        const int start = P.q_start[q], m = P.q_start[q + 1] - start;
+        if (lane == 0) {
+            const Rec r = {start, m, P.kv_lens[q], base[(m > P.RH && !P.one_line ? 0 : MAX_BATCH) + q], ibase[q], {0u, 0u, 0u}};
+            W.rec[q] = r;
+        }
+#pragma unroll 1
+        for (int i = lane; i < m; i += 32) W.row_seq[start + i] = q;
+    }
 }
 
 }  // namespace sp
