@@ -8,7 +8,8 @@ calls raise.
 
 The functions carry the C names:
 
-    dflash_init, dflash_prefill, dflash_set_block_size, dflash_block_size, dflash_set_sampling_filter,
+    dflash_init, dflash_prefill, dflash_prefill_shared, dflash_set_logit_rules, dflash_set_token_masks,
+    dflash_set_block_size, dflash_block_size, dflash_set_sampling_filter,
     dflash_draft_block, dflash_verify,
     dflash_draft_block_sampled, dflash_verify_sampled, dflash_train_forward,
     dflash_generate, dflash_inspect, dflash_destroy, dflash_last_error
@@ -83,11 +84,16 @@ class dflash_profile_entry(ctypes.Structure):
                 ("flops", ctypes.c_double)]
 
 
+class dflash_logit_rules(ctypes.Structure):
+    _fields_ = [("repetition", ctypes.c_void_p), ("presence", ctypes.c_void_p), ("frequency", ctypes.c_void_p),
+                ("bias_width", ctypes.c_int32), ("bias_ids", ctypes.c_void_p), ("bias_values", ctypes.c_void_p)]
+
+
 EXPORTS = ("dflash_init", "dflash_prefill", "dflash_set_block_size", "dflash_block_size", "dflash_draft_block", "dflash_verify", "dflash_draft_block_sampled",
            "dflash_verify_sampled", "dflash_set_sampling_filter", "dflash_train_forward", "dflash_generate",
            "dflash_inspect", "dflash_set_profiling", "dflash_destroy", "dflash_last_error",
            "dflash_kv_tables", "dflash_shared_prefix_attention", "dflash_shared_prefix_workspace",
-           "dflash_process_logits")
+           "dflash_process_logits", "dflash_prefill_shared", "dflash_set_logit_rules", "dflash_set_token_masks")
 
 _lib = None
 
@@ -110,6 +116,9 @@ def load(build_if_missing: bool = False):
     lib.dflash_init.argtypes = [ctypes.POINTER(dflash_config), ctypes.POINTER(dflash_weights), P,
                                 ctypes.POINTER(P)]
     lib.dflash_prefill.argtypes = [P, I32, P, P, P]
+    lib.dflash_prefill_shared.argtypes = [P, I32, I32, P, P, P, P]
+    lib.dflash_set_logit_rules.argtypes = [P, ctypes.POINTER(dflash_logit_rules)]
+    lib.dflash_set_token_masks.argtypes = [P, I32, P, I32, P]
     lib.dflash_draft_block.argtypes = [P, P]
     lib.dflash_verify.argtypes = [P, P, P, P]
     lib.dflash_draft_block_sampled.argtypes = [P, ctypes.c_float, P, P]
@@ -127,7 +136,8 @@ def load(build_if_missing: bool = False):
     lib.dflash_last_error.restype = ctypes.c_char_p
     for f in ("dflash_init", "dflash_prefill", "dflash_draft_block", "dflash_verify", "dflash_draft_block_sampled",
               "dflash_verify_sampled", "dflash_set_sampling_filter", "dflash_train_forward", "dflash_generate",
-              "dflash_inspect", "dflash_set_profiling", "dflash_set_block_size"):
+              "dflash_inspect", "dflash_set_profiling", "dflash_set_block_size", "dflash_prefill_shared",
+              "dflash_set_logit_rules", "dflash_set_token_masks"):
         getattr(lib, f).restype = ctypes.c_int
     lib.dflash_destroy.restype = None
     for f in ("dflash_kv_tables", "dflash_shared_prefix_attention", "dflash_process_logits"):

@@ -21,6 +21,7 @@
 #include "launch.h"
 #include "page_pool.h"
 #include "loss.h"
+#include "ops.h"
 
 using namespace dfl;
 
@@ -143,6 +144,33 @@ struct dflash_ctx {
     float* keep_draft = nullptr;
     float* keep_verify = nullptr;
     float* keep_hidden = nullptr;
+
+    // a batch behind one shared prefix (dflash_prefill_shared): whole pages of slot 0 that every slot's
+    // table begins with; the rounds' attention reads their keys once for the batch
+    int shared_pages = 0;
+    int* own_lens = nullptr;    // [max_batch] keys of each sequence behind the shared pages
+    int* own_start = nullptr;   // [max_batch + 1] first row of each sequence in the pass
+    int* tab_in = nullptr;      // [2][max_batch] own lengths before / new rows of a suffix chunk
+    int* tab_status = nullptr;
+    void* shared_ws = nullptr;
+    size_t shared_ws_bytes = 0;
+
+    // logit rules (dflash_set_logit_rules) and token masks (dflash_set_token_masks) of the target's logits
+    bool rules_next = false, rules_on = false;  // from the next prefill on / for the current batch
+    int bias_width = 0, bias_width_next = 0;
+    std::vector<float> rep_h, pres_h, freq_h, bias_h;
+    std::vector<int> bias_id_h;
+    float *rep = nullptr, *pres = nullptr, *freq = nullptr, *bias_val = nullptr;
+    int* bias_id = nullptr;
+    size_t bias_cap = 0;
+    int* history = nullptr;     // [max_batch][max_seq] committed tokens and the anchor
+    int* hist_len = nullptr;    // [max_batch]
+    int* prompt_len = nullptr;  // [max_batch]
+    bool masks_on = false;      // for the next target pass
+    int mask_rows = 0;
+    uint32_t* masks = nullptr;  // [max_batch * Bmax][mask_words]
+    int mask_words = 0;
+    int* mask_index = nullptr;  // [max_batch * Bmax]
 
     int batch = 0;
     int state = ST_EMPTY;
@@ -356,7 +384,9 @@ dflash_status check_device(dflash_ctx* c) {
         }
         return c->fail(DFLASH_E_DEVICE_CHECK, "device-side check failed (code %u%s%s)", e,
                        (e & ERR_TOKEN_RANGE) ? ": token id outside [0, vocab)" : "",
-                       (e & ERR_POSITION_RANGE) ? ": position beyond max_seq_len" : "");
+                       (e & ERR_NO_TOKEN)       ? ": the rules leave a row without a token"
+                       : (e & ERR_POSITION_RANGE) ? ": position beyond max_seq_len"
+                                                  : "");
     }
     return DFLASH_OK;
 }
@@ -509,8 +539,11 @@ struct Pass {
     // Decoder layers over `rows` rows whose metadata is (row_seq, row_pos).
     // target: causal attention over the target cache, capture of context layers
     // into stage; draft: bidirectional attention over [context ; block].
+    // `shared`: the rows are those of own_start, every sequence begins with the shared pages, and
+    // own_lens holds the keys behind them (these rows' own included).
     void layers(bool target, int rows, const int* row_seq, const int* row_pos, int group_rows, int max_keys,
-                bool capture, double keys_total, int rows_per_seq = 0, const int* stable_len = nullptr) {
+                bool capture, double keys_total, int rows_per_seq = 0, const int* stable_len = nullptr,
+                bool shared = false) {
         Launch L = c->L();
         const int nl = target ? c->Lt : c->Ld;
         const double R = rows, d = c->d, es = c->esz;
@@ -571,8 +604,15 @@ struct Pass {
             // the draft's attention reads this layer's context K/V, appended on the side stream
             if (!target && c->append_forked && cudaStreamWaitEvent(c->stream, c->ctx_ev[l], 0) != cudaSuccess)
                 c->launch_failed = true;
-            timed(c, DFLASH_K_ATTENTION, keys_total * 2 * c->kvd * es + 2 * R * c->qd * es,
-                  4.0 * R * c->H * c->hd * (keys_total / std::max(1.0, (double)c->batch)), [&] { attention<T>(L, ap); });
+            // (with shared pages keys_total counts them once, and a row still sees all of them)
+            const double common = shared ? 64.0 * c->shared_pages : 0.0;
+            const double seen = shared ? common + (keys_total - common) / std::max(1.0, (double)c->batch)
+                                       : keys_total / std::max(1.0, (double)c->batch);
+            timed(c, DFLASH_K_ATTENTION, keys_total * 2 * c->kvd * es + 2 * R * c->qd * es, 4.0 * R * c->H * c->hd * seen,
+                  [&] {
+                      if (!shared) attention<T>(L, ap);
+                      else if (!shared_prefix_attention(L, shared_args(rows, Kc, Vc, target))) L.fail();
+                  });
             residual_gemm(DFLASH_K_GEMM_O, rows, (const T*)c->att, c->qd, (const T*)w.wo, c->qd);
             if (is_bf16) {
                 // gate/up GEMM with the fused norm and the SwiGLU epilogue -> hmid (bf16)
@@ -590,6 +630,75 @@ struct Pass {
                     capture_rows<T>(L, c->x, c->d, rows, (T*)c->stage, c->k * c->d, c->ctx_slot[l] * c->d);
                 });
         }
+    }
+
+    dflash_shared_prefix_args shared_args(int rows, const void* Kc, const void* Vc, bool causal) const {
+        dflash_shared_prefix_args a = {};
+        a.dtype = c->cfg.dtype;
+        a.n_heads = c->H;
+        a.n_kv_heads = c->Hkv;
+        a.head_dim = c->hd;
+        a.batch = c->batch;
+        a.rows = rows;
+        a.n_pages = c->pool_pages;
+        a.prefix_len = c->shared_pages * PAGE_TOKENS;
+        a.width = c->kv.pages_per_seq - c->shared_pages;
+        a.causal = causal ? 1 : 0;
+        a.scale = 1.f / sqrtf((float)c->hd);
+        a.ld_q = a.ld_out = c->qd;
+        a.ld_table = c->kv.pages_per_seq;
+        a.q = c->q;
+        a.k_cache = Kc;
+        a.v_cache = Vc;
+        a.prefix_pages = c->page_table;  // slot 0's first entries
+        a.table = c->page_table + c->shared_pages;
+        a.kv_lens = c->own_lens;
+        a.q_start = c->own_start;
+        a.out = c->att;
+        a.workspace = c->shared_ws;
+        a.workspace_bytes = c->shared_ws_bytes;
+        return a;
+    }
+
+    // Rules and masks on `rows` logit rows per sequence of slots s0 .. s0 + seqs - 1 in c->logits, in place;
+    // the history's lengths are in hist_len.  Then out[row] = the row's argmax.
+    void rule_logits(int s0, int seqs, int rows, const int* drafts, int* out) {
+        Launch L = c->L();
+        dflash_logits_args a = {};
+        a.dtype = DFLASH_DTYPE_F32;
+        a.batch = seqs;
+        a.rows_per_seq = rows;
+        a.vocab = c->V;
+        a.ld_logits = a.ld_out = c->V;
+        a.logits = a.out = c->logits;
+        if (c->rules_on) {
+            a.history = c->history + (size_t)s0 * c->max_seq;
+            a.hist_width = c->max_seq;
+            a.ld_hist = c->max_seq;
+            a.hist_lens = c->hist_len + s0;
+            a.prompt_lens = c->prompt_len + s0;
+            a.drafts = drafts;
+            a.repetition = c->rep + s0;
+            a.presence = c->pres + s0;
+            a.frequency = c->freq + s0;
+            if (c->bias_width) {
+                a.bias_width = c->bias_width;
+                a.bias_ids = c->bias_id + (size_t)s0 * c->bias_width;
+                a.bias_values = c->bias_val + (size_t)s0 * c->bias_width;
+            }
+        }
+        if (c->masks_on) {
+            a.masks = c->masks;
+            a.n_masks = c->cfg.max_batch * c->Bmax;
+            a.ld_mask = c->mask_words;
+            a.mask_index = c->mask_index + (size_t)s0 * rows;
+        }
+        const int n = seqs * rows;
+        timed(c, DFLASH_K_SAMPLING, (double)n * c->V * 8, 0, [&] { process_logits(L, a); });
+        timed(c, DFLASH_K_ARGMAX, (double)n * c->V * 4, 0, [&] {
+            argmax_rows(L, c->logits, c->V, n, c->V, out);
+            check_rows(L, c->logits, c->V, n, out, c->errw);
+        });
     }
 
     // Context feature rms(W_c stage) and its K/V in every draft layer, stored
@@ -692,34 +801,116 @@ struct Pass {
         if (keep) cudaMemcpyAsync(keep, lg, (size_t)rows * c->V * 4, cudaMemcpyDeviceToDevice, c->stream);
     }
 
-    dflash_status prefill(int batch, const int* lens, const int* toks, int* first) {
+    // Rows [r0, r0 + rows) of slot s's prompt (a chunk): the target's layers and the context append.
+    dflash_status prefill_chunk(int s, const int* toks, int r0, int rows) {
         Launch L = c->L();
         const int g = c->H / c->Hkv;
+        CUDA_TRY(c, cudaMemcpyAsync(c->tokens, toks, (size_t)rows * 4, cudaMemcpyHostToDevice, c->stream));
+        fill_prefill_rows(L, s, r0, rows, c->row_seq, c->row_pos);
+        embed_rows<T>(L, c->tokens, (const T*)c->embed, c->V, c->d, rows, c->x, c->errw, c->ss_x, c->R);
+        // bf16, head_dim 128: query groups of 128 vectors for the tcgen05 prefill attention
+        const int gr = (is_bf16 && c->hd == 128 && 128 % g == 0) ? 128 / g : 64 / g;
+        layers(true, rows, c->row_seq, c->row_pos, gr, r0 + rows, true, (double)(r0 + rows));
+        append_context(rows, c->row_seq, c->row_pos);
+        return DFLASH_OK;
+    }
+
+    // First tokens of slots s0 .. s0 + n - 1 from rows [row0, row0 + n) of x.
+    void first_tokens(int row0, int s0, int n, bool fusable) {
+        const bool ruled = c->rules_on || c->masks_on;
+        head(row0, n, c->final_norm, c->anchor + s0, c->keep_prefill ? c->keep_prefill + (size_t)s0 * c->V : nullptr, 0,
+             ruled ? c->logits : nullptr, fusable);
+        if (ruled) rule_logits(s0, n, 1, nullptr, c->anchor + s0);
+    }
+
+    // Lengths, the anchors' place in the history, and the first tokens' way back.
+    dflash_status prefill_end(int batch, const int* lens, int* first) {
+        dflash_status ls = launch_check(c);
+        if (ls != DFLASH_OK) return ls;
+        std::vector<int> nh(lens, lens + batch);
+        CUDA_TRY(c, cudaMemcpyAsync(c->n, nh.data(), (size_t)batch * 4, cudaMemcpyHostToDevice, c->stream));
+        if (c->rules_on) {
+            Launch L = c->L();
+            history_append(L, batch, c->B, c->max_seq, c->n, c->anchor, nullptr, nullptr, c->history);
+        }
+        CUDA_TRY(c, cudaMemcpyAsync(first, c->anchor, (size_t)batch * 4, cudaMemcpyDeviceToHost, c->stream));
+        return check_device(c);
+    }
+
+    dflash_status prefill(int batch, const int* lens, const int* toks, int* first) {
         size_t off = 0;
         for (int s = 0; s < batch; ++s) {
             const int P = lens[s];
             for (int r0 = 0; r0 < P; r0 += PREFILL_CHUNK) {
                 const int rows = std::min(PREFILL_CHUNK, P - r0);
-                CUDA_TRY(c, cudaMemcpyAsync(c->tokens, toks + off + r0, (size_t)rows * 4, cudaMemcpyHostToDevice,
-                                            c->stream));
-                fill_prefill_rows(L, s, r0, rows, c->row_seq, c->row_pos);
-                embed_rows<T>(L, c->tokens, (const T*)c->embed, c->V, c->d, rows, c->x, c->errw, c->ss_x, c->R);
-                // bf16, head_dim 128: query groups of 128 vectors for the tcgen05 prefill attention
-                const int gr = (is_bf16 && c->hd == 128 && 128 % g == 0) ? 128 / g : 64 / g;
-                layers(true, rows, c->row_seq, c->row_pos, gr, r0 + rows, true, (double)(r0 + rows));
-                append_context(rows, c->row_seq, c->row_pos);
-                if (r0 + rows == P)
-                    head(rows - 1, 1, c->final_norm, c->anchor + s,
-                         c->keep_prefill ? c->keep_prefill + (size_t)s * c->V : nullptr, 0, nullptr, rows <= 256);
+                const dflash_status st = prefill_chunk(s, toks + off + r0, r0, rows);
+                if (st != DFLASH_OK) return st;
+                if (r0 + rows == P) first_tokens(rows - 1, s, 1, rows <= 256);
             }
             off += P;
         }
-        dflash_status ls = launch_check(c);
-        if (ls != DFLASH_OK) return ls;
-        std::vector<int> nh(lens, lens + batch);
-        CUDA_TRY(c, cudaMemcpyAsync(c->n, nh.data(), (size_t)batch * 4, cudaMemcpyHostToDevice, c->stream));
-        CUDA_TRY(c, cudaMemcpyAsync(first, c->anchor, (size_t)batch * 4, cudaMemcpyDeviceToHost, c->stream));
-        return check_device(c);
+        return prefill_end(batch, lens, first);
+    }
+
+    // Prefill behind shared pages that slot 0 holds already: the prompts' own tokens (`own`, concatenated,
+    // own_n[s] of slot s), all sequences' rows in one ragged pass per chunk.
+    dflash_status prefill_suffixes(int batch, const std::vector<int>& own_n, const int* own) {
+        Launch L = c->L();
+        const int base = c->shared_pages * PAGE_TOKENS;
+        std::vector<int> done(batch, 0), add(batch), both(2 * batch);
+        size_t off = 0;
+        for (int s = 0; s < batch;) {
+            // the next rows in sequence order, up to a chunk: sequences s .. e - 1, the last maybe in part
+            int rows = 0, e = s, fin = s;
+            std::fill(add.begin(), add.end(), 0);
+            for (; e < batch && rows < PREFILL_CHUNK; ++e) {
+                add[e] = std::min(own_n[e] - done[e], PREFILL_CHUNK - rows);
+                rows += add[e];
+                if (done[e] + add[e] < own_n[e]) {
+                    ++e;
+                    break;
+                }
+                fin = e + 1;
+            }
+            for (int i = 0; i < batch; ++i) {
+                both[i] = done[i];
+                both[batch + i] = add[i];
+            }
+            CUDA_TRY(c, cudaMemcpyAsync(c->tokens, own + off, (size_t)rows * 4, cudaMemcpyHostToDevice, c->stream));
+            CUDA_TRY(c, cudaMemcpyAsync(c->tab_in, both.data(), both.size() * 4, cudaMemcpyHostToDevice, c->stream));
+            // row maps from the lengths; the host pool has backed every page of the table
+            dflash_kv_tables_args t = {};
+            t.batch = batch;
+            t.width = c->kv.pages_per_seq - c->shared_pages;
+            t.rows = rows;
+            t.base_pos = base;
+            t.ld_table = c->kv.pages_per_seq;
+            t.kv_lens = c->tab_in;
+            t.new_lens = c->tab_in + batch;
+            t.table = c->page_table + c->shared_pages;
+            t.q_start = c->own_start;
+            t.row_seq = c->row_seq;
+            t.row_pos = c->row_pos;
+            t.status = c->tab_status;
+            kv_tables(L, t);
+            own_lengths(L, batch, c->tab_in, c->tab_in + batch, 0, c->own_lens, nullptr, nullptr);
+            embed_rows<T>(L, c->tokens, (const T*)c->embed, c->V, c->d, rows, c->x, c->errw, c->ss_x, c->R);
+            double keys = base;
+            for (int i = s; i < e; ++i) keys += done[i] + add[i];
+            layers(true, rows, c->row_seq, c->row_pos, 1, c->max_seq, true, keys, 0, nullptr, true);
+            append_context(rows, c->row_seq, c->row_pos);
+            // the sequences that end here: their last rows gathered, then one head pass
+            if (fin > s) {
+                gather_last_rows(L, c->x, c->d, c->own_start, s, fin - s, c->fcout);
+                CUDA_TRY(c, cudaMemcpyAsync(c->x, c->fcout, (size_t)(fin - s) * c->d * 4, cudaMemcpyDeviceToDevice, c->stream));
+                first_tokens(0, s, fin - s, false);
+            }
+            // (`both` and the token list are pageable: each copy has been staged when it returns)
+            off += rows;
+            for (int i = s; i < e; ++i) done[i] += add[i];
+            s = fin;
+        }
+        return DFLASH_OK;
     }
 
     // Draft pass; `sampled`: proposals drawn from softmax(draft logits / T) (T in device memory).
@@ -757,7 +948,8 @@ struct Pass {
         double keys = 0;
         for (int s = 0; s < b; ++s) keys += c->n_upper[s] + B;
         // (the n committed context entries are complete before each layer's attention starts)
-        layers(false, b * B, c->row_seq, c->row_pos, attn_group_rows(B, g), c->max_seq, false, keys, B, c->n);
+        const bool shared = round_lengths(keys);
+        layers(false, b * B, c->row_seq, c->row_pos, attn_group_rows(B, g), c->max_seq, false, keys, B, c->n, shared);
         join_append();  // (already joined by the last layer's attention; kept for clarity)
         // drafts[s][j] = argmax of row s*B + 1 + j
         head(0, b * B, c->draft_norm, c->drafts, c->keep_draft, B,
@@ -766,6 +958,16 @@ struct Pass {
             timed(c, DFLASH_K_SAMPLING, (double)b * (B - 1) * c->V * 4, 0, [&] {
                 draft_sample(L, c->dlogits, c->V, b, B, c->prm_dev, c->u_draft, c->dstat, c->drafts);
             });
+    }
+
+    // Behind shared pages: the rounds' rows and own lengths for the shared-prefix attention (false: the
+    // sequences are attended one by one).  `keys` then counts the shared keys once.
+    bool round_lengths(double& keys) {
+        if (!c->shared_pages) return false;
+        keys -= 64.0 * c->shared_pages * (c->batch - 1);
+        Launch L = c->L();
+        own_lengths(L, c->batch, c->n, nullptr, c->B - c->shared_pages * PAGE_TOKENS, c->own_lens, c->own_start, &c->B);
+        return true;
     }
 
     // The pass's stream waits for the whole forked append (its last event).
@@ -786,10 +988,17 @@ struct Pass {
         });
         double keys = 0;
         for (int s = 0; s < b; ++s) keys += c->n_upper[s] + B;
-        layers(true, b * B, c->row_seq, c->row_pos, attn_group_rows(B, g), c->max_seq, true, keys, B, c->n);
+        const bool shared = round_lengths(keys);
+        layers(true, b * B, c->row_seq, c->row_pos, attn_group_rows(B, g), c->max_seq, true, keys, B, c->n, shared);
         if (c->keep_hidden)
             cudaMemcpyAsync(c->keep_hidden, c->x, (size_t)b * B * c->d * 4, cudaMemcpyDeviceToDevice, c->stream);
-        head(0, b * B, c->final_norm, c->posterior, c->keep_verify, 0, sampled ? c->logits : nullptr);
+        const bool ruled = c->rules_on || c->masks_on;
+        head(0, b * B, c->final_norm, c->posterior, c->keep_verify, 0, sampled || ruled ? c->logits : nullptr);
+        if (ruled) {
+            // row j continues the history (committed tokens and the anchor) and the first j drafts
+            if (c->rules_on) own_lengths(L, b, c->n, nullptr, 1, c->hist_len, nullptr, nullptr);
+            rule_logits(0, b, B, B > 1 ? c->proposal : nullptr, c->posterior);
+        }
         if (sampled) {
             timed(c, DFLASH_K_SAMPLING, (double)b * (B + 2) * c->V * 4, 0, [&] {
                 verify_sample(L, c->logits, c->dlogits, c->V, b, B, c->prm_dev, c->proposal, c->u_verify, c->tstat,
@@ -801,6 +1010,8 @@ struct Pass {
                        c->ctx_row_pos);
             });
         }
+        if (c->rules_on)
+            history_append(L, b, B, c->max_seq, c->n, c->anchor, c->accepted, c->proposal, c->history);
         c->pending_append = true;
         c->append_B = B;
     }
@@ -894,7 +1105,8 @@ dflash_status run_pass(dflash_ctx* c, dflash_ctx::GraphSlot& g, F&& pass) {
         pass();
         return launch_check(c);
     }
-    const long long key = ((long long)c->batch << 16) | (c->B << 8) | (c->pending_append ? c->append_B : 0);
+    const long long key = ((long long)c->batch << 16) | (c->B << 8) | (c->pending_append ? c->append_B : 0) |
+                          ((long long)c->shared_pages << 32) | (c->rules_on ? 1ll << 60 : 0) | (c->masks_on ? 1ll << 61 : 0);
     if (g.exec && g.key == key) {
         CUDA_TRY(c, cudaGraphLaunch(g.exec, c->stream));
         c->launches += g.kernels;
@@ -939,6 +1151,7 @@ dflash_status run_pass(dflash_ctx* c, dflash_ctx::GraphSlot& g, F&& pass) {
 }
 
 dflash_status do_draft(dflash_ctx* c, bool sampled = false) {
+    c->masks_on = false;  // (masks set before a draft were for a prefill)
     const int with_append = c->pending_append ? 1 : 0;
     dflash_status s = run_pass(c, sampled ? c->g_draft_s[with_append] : c->g_draft[with_append], [&] {
         if (c->cfg.dtype == DFLASH_DTYPE_BF16) Pass<bf16>{c}.draft(sampled);
@@ -953,10 +1166,120 @@ dflash_status do_verify(dflash_ctx* c, bool sampled = false) {
         if (c->cfg.dtype == DFLASH_DTYPE_BF16) Pass<bf16>{c}.verify(sampled);
         else Pass<float>{c}.verify(sampled);
     });
+    c->masks_on = false;  // masks are for one pass
     if (s != DFLASH_OK) return s;
     c->pending_append = true;
     c->append_B = c->B;
     for (int i = 0; i < c->batch; ++i) c->n_upper[i] += c->B;
+    return DFLASH_OK;
+}
+
+// The rules set before this prefill take effect: values and prompts to the device.
+dflash_status start_rules(dflash_ctx* c, int batch) {
+    c->rules_on = c->rules_next;
+    if (!c->rules_on) return DFLASH_OK;
+    const size_t mb = c->cfg.max_batch;
+    if (!c->history) {
+        c->history = (int*)dev_alloc(c, mb * c->max_seq * 4);
+        c->hist_len = (int*)dev_alloc(c, mb * 4);
+        c->prompt_len = (int*)dev_alloc(c, mb * 4);
+        c->rep = (float*)dev_alloc(c, mb * 4);
+        c->pres = (float*)dev_alloc(c, mb * 4);
+        c->freq = (float*)dev_alloc(c, mb * 4);
+        if (!c->history || !c->hist_len || !c->prompt_len || !c->rep || !c->pres || !c->freq) {
+            c->history = nullptr;
+            return c->fail(DFLASH_E_NOMEM, "allocation of the token history failed");
+        }
+    }
+    if (c->bias_width != c->bias_width_next) {
+        // captured passes hold the old width
+        reset_graph(c->g_verify);
+        reset_graph(c->g_verify_s);
+        c->bias_width = c->bias_width_next;
+    }
+    const size_t nb = mb * c->bias_width;
+    if (nb > c->bias_cap) {
+        c->bias_id = (int*)dev_alloc(c, nb * 4);
+        c->bias_val = (float*)dev_alloc(c, nb * 4);
+        c->bias_cap = 0;
+        if (!c->bias_id || !c->bias_val) return c->fail(DFLASH_E_NOMEM, "allocation of the bias lists failed");
+        c->bias_cap = nb;
+        // captured passes hold the old buffers
+        reset_graph(c->g_verify);
+        reset_graph(c->g_verify_s);
+    }
+    CUDA_TRY(c, cudaMemcpyAsync(c->rep, c->rep_h.data(), mb * 4, cudaMemcpyHostToDevice, c->stream));
+    CUDA_TRY(c, cudaMemcpyAsync(c->pres, c->pres_h.data(), mb * 4, cudaMemcpyHostToDevice, c->stream));
+    CUDA_TRY(c, cudaMemcpyAsync(c->freq, c->freq_h.data(), mb * 4, cudaMemcpyHostToDevice, c->stream));
+    if (nb) {
+        CUDA_TRY(c, cudaMemcpyAsync(c->bias_id, c->bias_id_h.data(), nb * 4, cudaMemcpyHostToDevice, c->stream));
+        CUDA_TRY(c, cudaMemcpyAsync(c->bias_val, c->bias_h.data(), nb * 4, cudaMemcpyHostToDevice, c->stream));
+    }
+    (void)batch;
+    return DFLASH_OK;
+}
+
+// Slot s's prompt (two pieces) into the history.
+dflash_status history_prompt(dflash_ctx* c, int s, const int* a, int na, const int* b, int nb) {
+    int* h = c->history + (size_t)s * c->max_seq;
+    const int n = na + nb;
+    if (na) CUDA_TRY(c, cudaMemcpyAsync(h, a, (size_t)na * 4, cudaMemcpyHostToDevice, c->stream));
+    if (nb) CUDA_TRY(c, cudaMemcpyAsync(h + na, b, (size_t)nb * 4, cudaMemcpyHostToDevice, c->stream));
+    CUDA_TRY(c, cudaMemcpyAsync(c->prompt_len + s, &n, 4, cudaMemcpyHostToDevice, c->stream));
+    CUDA_TRY(c, cudaMemcpyAsync(c->hist_len + s, &n, 4, cudaMemcpyHostToDevice, c->stream));
+    return DFLASH_OK;
+}
+
+// Checks that every prefill makes: batch, lengths (behind `prefix` tokens) and token ids.
+dflash_status check_prompts(dflash_ctx* c, int batch, int prefix, const int32_t* lens, const int32_t* toks, size_t* total) {
+    if (batch < 1 || batch > c->cfg.max_batch) return c->fail(DFLASH_E_INVAL, "batch %d outside [1, %d]", batch, c->cfg.max_batch);
+    *total = 0;
+    for (int s = 0; s < batch; ++s) {
+        if (lens[s] < 1) return c->fail(DFLASH_E_INVAL, "prompt %d has length %d", s, lens[s]);
+        if ((long long)prefix + lens[s] + c->B > c->cfg.max_seq_len)
+            return c->fail(DFLASH_E_CAPACITY, "prompt %d: length %lld + block %d exceeds max_seq_len %d", s,
+                           (long long)prefix + lens[s], c->B, c->cfg.max_seq_len);
+        *total += lens[s];
+    }
+    for (size_t i = 0; i < *total; ++i)
+        if (toks[i] < 0 || toks[i] >= c->V) return c->fail(DFLASH_E_INVAL, "prompt token %zu = %d outside [0, %d)", i, toks[i], c->V);
+    if (c->masks_on && c->mask_rows != batch)
+        return c->fail(DFLASH_E_INVAL, "token masks were set for %d rows, the prefill has %d", c->mask_rows, batch);
+    return DFLASH_OK;
+}
+
+// Pages for a new batch: `shared` whole pages of slot 0 at the head of every slot's table, then each
+// prompt's own (+ one block).  On failure every page returns to the pool and the session is empty.
+dflash_status pool_prompts(dflash_ctx* c, int batch, int shared, int prefix, const int32_t* lens) {
+    pool_reset(c);
+    for (int s = 0; s < batch; ++s) {
+        if (s && shared) c->pool.share(s, 0, shared);
+        if (!pool_ensure(c, s, (long long)prefix + lens[s] + c->B)) {
+            const dflash_status st = pool_full(c, s, (long long)prefix + lens[s] + c->B);
+            pool_reset(c);
+            c->batch = 0;
+            c->state = ST_EMPTY;
+            const dflash_status up = pool_upload(c);
+            return up ? up : st;
+        }
+    }
+    return pool_upload(c);
+}
+
+template <class F>
+dflash_status timed_prefill(dflash_ctx* c, F&& run) {
+    if (c->events) cudaEventRecord(c->ev[0], c->stream);
+    dflash_status s = run();
+    c->masks_on = false;
+    if (s != DFLASH_OK) return s;
+    if (c->events) {
+        cudaEventRecord(c->ev[1], c->stream);
+        cudaEventSynchronize(c->ev[1]);
+        float ms = 0.f;
+        cudaEventElapsedTime(&ms, c->ev[0], c->ev[1]);
+        c->stats.prefill_ms += ms;
+    }
+    c->state = ST_READY;
     return DFLASH_OK;
 }
 
@@ -1253,46 +1576,162 @@ dflash_status dflash_prefill(dflash_ctx* c, int32_t batch, const int32_t* lens, 
     if (batch < 1 || batch > c->cfg.max_batch) return c->fail(DFLASH_E_INVAL, "batch %d outside [1, %d]", batch, c->cfg.max_batch);
     if (!lens || !toks || !first) return c->fail(DFLASH_E_INVAL, "NULL argument");
     size_t total = 0;
-    for (int s = 0; s < batch; ++s) {
-        if (lens[s] < 1) return c->fail(DFLASH_E_INVAL, "prompt %d has length %d", s, lens[s]);
-        if (lens[s] + c->B > c->cfg.max_seq_len)
-            return c->fail(DFLASH_E_CAPACITY, "prompt %d: length %d + block %d exceeds max_seq_len %d", s, lens[s],
-                           c->B, c->cfg.max_seq_len);
-        total += lens[s];
-    }
-    for (size_t i = 0; i < total; ++i)
-        if (toks[i] < 0 || toks[i] >= c->V) return c->fail(DFLASH_E_INVAL, "prompt token %zu = %d outside [0, %d)", i, toks[i], c->V);
+    dflash_status s;
+    if ((s = check_prompts(c, batch, 0, lens, toks, &total))) return s;
     // a new batch: every page returns to the pool, then each prompt (+ one block) takes its own
-    pool_reset(c);
-    for (int s = 0; s < batch; ++s)
-        if (!pool_ensure(c, s, (long long)lens[s] + c->B)) {
-            const dflash_status st = pool_full(c, s, (long long)lens[s] + c->B);
-            pool_reset(c);
-            c->batch = 0;
-            c->state = ST_EMPTY;
-            const dflash_status up = pool_upload(c);
-            return up ? up : st;
-        }
-    {
-        dflash_status st = pool_upload(c);
-        if (st) return st;
-    }
+    if ((s = pool_prompts(c, batch, 0, 0, lens))) return s;
     c->batch = batch;
     c->state = ST_EMPTY;
     c->pending_append = false;
+    c->shared_pages = 0;
     c->n_upper.assign(lens, lens + batch);
-    if (c->events) cudaEventRecord(c->ev[0], c->stream);
-    dflash_status s = c->cfg.dtype == DFLASH_DTYPE_BF16 ? Pass<bf16>{c}.prefill(batch, lens, toks, first)
-                                                        : Pass<float>{c}.prefill(batch, lens, toks, first);
-    if (s != DFLASH_OK) return s;
-    if (c->events) {
-        cudaEventRecord(c->ev[1], c->stream);
-        cudaEventSynchronize(c->ev[1]);
-        float ms = 0.f;
-        cudaEventElapsedTime(&ms, c->ev[0], c->ev[1]);
-        c->stats.prefill_ms += ms;
+    if ((s = start_rules(c, batch))) return s;
+    if (c->rules_on) {
+        size_t off = 0;
+        for (int i = 0; i < batch; ++i) {
+            if ((s = history_prompt(c, i, toks + off, lens[i], nullptr, 0))) return s;
+            off += lens[i];
+        }
     }
-    c->state = ST_READY;
+    return timed_prefill(c, [&] {
+        return c->cfg.dtype == DFLASH_DTYPE_BF16 ? Pass<bf16>{c}.prefill(batch, lens, toks, first)
+                                                 : Pass<float>{c}.prefill(batch, lens, toks, first);
+    });
+}
+
+dflash_status dflash_prefill_shared(dflash_ctx* c, int32_t batch, int32_t prefix_len, const int32_t* prefix,
+                                    const int32_t* lens, const int32_t* toks, int32_t* first) {
+    if (!c) return DFLASH_E_INVAL;
+    if (prefix_len < 0 || (prefix_len > 0 && !prefix) || !lens || !toks || !first)
+        return c->fail(DFLASH_E_INVAL, "NULL argument or a negative prefix length");
+    if (batch < 1 || batch > c->cfg.max_batch) return c->fail(DFLASH_E_INVAL, "batch %d outside [1, %d]", batch, c->cfg.max_batch);
+    size_t total = 0;
+    dflash_status s;
+    if ((s = check_prompts(c, batch, prefix_len, lens, toks, &total))) return s;
+    for (int i = 0; i < prefix_len; ++i)
+        if (prefix[i] < 0 || prefix[i] >= c->V) return c->fail(DFLASH_E_INVAL, "prefix token %d = %d outside [0, %d)", i, prefix[i], c->V);
+    // whole pages are shared; the prefix's last tokens (fewer than a page) go with each prompt's own.  (The
+    // exception handling of a session call: nothing below may throw across the C boundary.)
+    try {
+        const int pages = prefix_len / PAGE_TOKENS, base = pages * PAGE_TOKENS, tail = prefix_len - base;
+        std::vector<int> own_n(batch), own, full(batch);
+        own.reserve(total + (size_t)batch * tail);
+        size_t off = 0;
+        for (int i = 0; i < batch; ++i) {
+            own.insert(own.end(), prefix + base, prefix + prefix_len);
+            own.insert(own.end(), toks + off, toks + off + lens[i]);
+            own_n[i] = tail + lens[i];
+            full[i] = prefix_len + lens[i];
+            off += lens[i];
+        }
+        if (pages == 0) return dflash_prefill(c, batch, full.data(), own.data(), first);
+        if (!c->own_lens) {
+            const size_t mb = c->cfg.max_batch;
+            const size_t ws = dflash_shared_prefix_workspace(c->cfg.dtype, c->H, c->Hkv, c->hd, c->cfg.max_batch, c->R);
+            int* lens_d = (int*)dev_alloc(c, mb * 4);
+            int* start_d = (int*)dev_alloc(c, (mb + 1) * 4);
+            int* tab_d = (int*)dev_alloc(c, 2 * mb * 4);
+            int* st_d = (int*)dev_alloc(c, 16);
+            void* ws_d = dev_alloc(c, ws);
+            if (!ws || !lens_d || !start_d || !tab_d || !st_d || !ws_d)
+                return c->fail(DFLASH_E_NOMEM, "allocation of %zu bytes for the shared-prefix attention failed", ws);
+            c->own_lens = lens_d;
+            c->own_start = start_d;
+            c->tab_in = tab_d;
+            c->tab_status = st_d;
+            c->shared_ws = ws_d;
+            c->shared_ws_bytes = ws;
+        }
+        if ((s = pool_prompts(c, batch, pages, prefix_len, lens))) return s;
+        c->batch = batch;
+        c->state = ST_EMPTY;
+        c->pending_append = false;
+        c->shared_pages = pages;
+        c->n_upper.assign(full.begin(), full.end());
+        if ((s = start_rules(c, batch))) return s;
+        if (c->rules_on) {
+            off = 0;
+            for (int i = 0; i < batch; ++i) {
+                if ((s = history_prompt(c, i, prefix, prefix_len, toks + off, lens[i]))) return s;
+                off += lens[i];
+            }
+        }
+        auto run = [&](auto pass) {
+            for (int r0 = 0; r0 < base; r0 += PREFILL_CHUNK) {
+                const dflash_status st = pass.prefill_chunk(0, prefix + r0, r0, std::min(PREFILL_CHUNK, base - r0));
+                if (st != DFLASH_OK) return st;
+            }
+            const dflash_status st = pass.prefill_suffixes(batch, own_n, own.data());
+            return st != DFLASH_OK ? st : pass.prefill_end(batch, full.data(), first);
+        };
+        return timed_prefill(c, [&] { return c->cfg.dtype == DFLASH_DTYPE_BF16 ? run(Pass<bf16>{c}) : run(Pass<float>{c}); });
+    } catch (const std::bad_alloc&) {
+        return c->fail(DFLASH_E_NOMEM, "out of host memory");
+    }
+}
+
+dflash_status dflash_set_logit_rules(dflash_ctx* c, const dflash_logit_rules* r) {
+    if (!c) return DFLASH_E_INVAL;
+    if (!r) {
+        c->rules_next = false;
+        return DFLASH_OK;
+    }
+    if (r->bias_width < 0 || r->bias_width > 4096 || (r->bias_width > 0 && (!r->bias_ids || !r->bias_values)))
+        return c->fail(DFLASH_E_INVAL, "bias_width outside [0, 4096], or a NULL bias list");
+    const size_t mb = c->cfg.max_batch, nb = mb * r->bias_width;
+    for (size_t i = 0; i < mb; ++i) {
+        const float a = r->repetition ? r->repetition[i] : 1.f, b = r->presence ? r->presence[i] : 0.f,
+                    f = r->frequency ? r->frequency[i] : 0.f;
+        if (!(a > 0.f) || !std::isfinite(a) || !std::isfinite(b) || !std::isfinite(f))
+            return c->fail(DFLASH_E_INVAL, "sequence %zu: repetition %g must be positive, presence %g and frequency %g finite", i, a, b, f);
+    }
+    for (size_t i = 0; i < nb; ++i)
+        if (r->bias_ids[i] >= c->V || std::isnan(r->bias_values[i]) || r->bias_values[i] == INFINITY)
+            return c->fail(DFLASH_E_INVAL, "bias entry %zu: id %d outside the vocabulary, or its value is NaN or +inf", i, r->bias_ids[i]);
+    try {
+        auto take = [&](std::vector<float>& v, const float* p, float none) {
+            if (p) v.assign(p, p + mb);
+            else v.assign(mb, none);
+        };
+        take(c->rep_h, r->repetition, 1.f);
+        take(c->pres_h, r->presence, 0.f);
+        take(c->freq_h, r->frequency, 0.f);
+        c->bias_width_next = r->bias_width;
+        c->bias_id_h.assign(r->bias_ids, r->bias_ids + nb);
+        c->bias_h.assign(r->bias_values, r->bias_values + nb);
+    } catch (const std::bad_alloc&) {
+        return c->fail(DFLASH_E_NOMEM, "out of host memory");
+    }
+    c->rules_next = true;
+    return DFLASH_OK;
+}
+
+dflash_status dflash_set_token_masks(dflash_ctx* c, int32_t n_masks, const uint32_t* masks, int32_t rows,
+                                     const int32_t* mask_index) {
+    if (!c) return DFLASH_E_INVAL;
+    c->masks_on = false;
+    if (n_masks == 0) return DFLASH_OK;
+    const int most = c->cfg.max_batch * c->Bmax;
+    if (n_masks < 0 || n_masks > most || !masks || !mask_index)
+        return c->fail(DFLASH_E_INVAL, "n_masks %d outside [0, %d], or a NULL argument", n_masks, most);
+    const int need = c->state == ST_DRAFTED ? c->batch * c->B : rows;
+    if (rows != need || rows < 1 || rows > most)
+        return c->fail(DFLASH_E_INVAL, "%d mask indices: the next verify has %d rows", rows, need);
+    c->mask_words = (c->V + 31) / 32;
+    if (!c->masks) {
+        uint32_t* m = (uint32_t*)dev_alloc(c, (size_t)most * c->mask_words * 4);
+        int* i = (int*)dev_alloc(c, (size_t)most * 4);
+        if (!m || !i) return c->fail(DFLASH_E_NOMEM, "allocation of the token masks failed");
+        c->masks = m;
+        c->mask_index = i;
+    }
+    if (!is_device_ptr(mask_index))
+        for (int i = 0; i < rows; ++i)
+            if (mask_index[i] >= n_masks) return c->fail(DFLASH_E_INVAL, "mask index %d = %d, with %d masks", i, mask_index[i], n_masks);
+    CUDA_TRY(c, cudaMemcpyAsync(c->masks, masks, (size_t)n_masks * c->mask_words * 4, cudaMemcpyDefault, c->stream));
+    CUDA_TRY(c, cudaMemcpyAsync(c->mask_index, mask_index, (size_t)rows * 4, cudaMemcpyDefault, c->stream));
+    c->masks_on = true;
+    c->mask_rows = rows;
     return DFLASH_OK;
 }
 

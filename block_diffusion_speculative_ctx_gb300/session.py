@@ -14,7 +14,7 @@ from . import (ALLOC_FN, DFLASH_DTYPE_BF16, DFLASH_DTYPE_F32, DFLASH_FLAG_KEEP_L
                INSPECT_LOGITS_DRAFT, INSPECT_LOGITS_PREFILL, INSPECT_LOGITS_VERIFY, INSPECT_POSTERIOR,
                INSPECT_STATS, INSPECT_TARGET_K, INSPECT_TARGET_V, INSPECT_PROFILE, INSPECT_PROFILE_RESET,
                KERNEL_CLASSES, DFlashError, _check, _ptr, dflash_config, dflash_profile_entry,
-               dflash_destroy, dflash_init, dflash_layer_weights, dflash_stats, dflash_weights, load)
+               dflash_destroy, dflash_init, dflash_layer_weights, dflash_logit_rules, dflash_stats, dflash_weights, load)
 
 
 def config_from_workload(w, max_batch: int, max_seq_len: int, keep_logits: bool = False) -> dflash_config:
@@ -137,6 +137,57 @@ class Session:
         _check(self.ctx, self.lib.dflash_prefill(self.ctx, len(lens), _ptr(lens), _ptr(toks), _ptr(first)))
         self.batch = len(prompts)
         return first
+
+    def prefill_shared(self, prefix, prompts: Sequence[np.ndarray]) -> np.ndarray:
+        """Prefill of prompts prefix + prompts[i], the prefix computed and stored once; the following
+        rounds attend to its keys once for the batch."""
+        pre = np.ascontiguousarray(np.asarray(prefix, dtype=np.int32))
+        lens = np.array([len(p) for p in prompts], dtype=np.int32)
+        toks = np.ascontiguousarray(np.concatenate([np.asarray(p, dtype=np.int32) for p in prompts]))
+        first = np.zeros(len(prompts), dtype=np.int32)
+        _check(self.ctx, self.lib.dflash_prefill_shared(self.ctx, len(lens), len(pre), _ptr(pre), _ptr(lens), _ptr(toks),
+                                                        _ptr(first)))
+        self.batch = len(prompts)
+        return first
+
+    def set_logit_rules(self, repetition=None, presence=None, frequency=None, bias=None):
+        """Penalties and biases of the target's logits from the next prefill on.  Each a value for every
+        sequence or a list of max_batch; ``bias``: one {token: value} for every sequence or a list of
+        max_batch of them.  No argument: off."""
+        if repetition is None and presence is None and frequency is None and bias is None:
+            _check(self.ctx, self.lib.dflash_set_logit_rules(self.ctx, None))
+            return
+        n = self.max_batch
+        vals = [np.ascontiguousarray(np.broadcast_to(np.asarray(none if v is None else v, np.float32), (n,)))
+                for v, none in ((repetition, 1.0), (presence, 0.0), (frequency, 0.0))]
+        maps = [bias or {}] * n if bias is None or isinstance(bias, dict) else list(bias)
+        if len(maps) != n:
+            raise ValueError(f"bias must be one mapping or a list of {n}")
+        width = max(len(m) for m in maps)
+        ids, add = np.full((n, max(width, 1)), -1, np.int32), np.zeros((n, max(width, 1)), np.float32)
+        for i, m in enumerate(maps):
+            ids[i, :len(m)], add[i, :len(m)] = list(m.keys()), list(m.values())
+        r = dflash_logit_rules(*(_ptr(v) for v in vals), width, _ptr(ids), _ptr(add))
+        _check(self.ctx, self.lib.dflash_set_logit_rules(self.ctx, ctypes.byref(r)))
+
+    def set_token_masks(self, masks=None, mask_index=None):
+        """Token masks of the next verify (after a draft: one index per block row, sequence-major) or of the
+        next prefill's first tokens.  masks: 32-bit words [n, ceil(V / 32)], numpy or a device tensor;
+        mask_index < 0: no mask.  No argument: none."""
+        if masks is None:
+            _check(self.ctx, self.lib.dflash_set_token_masks(self.ctx, 0, None, 0, None))
+            return
+        if isinstance(masks, np.ndarray):
+            masks = np.ascontiguousarray(masks).view(np.uint32)
+        if isinstance(mask_index, (np.ndarray, list, tuple)):
+            mask_index = np.ascontiguousarray(np.asarray(mask_index, dtype=np.int32)).reshape(-1)
+        words = (self.w.vocab + 31) // 32
+        if len(masks.shape) != 2 or masks.shape[1] != words:
+            raise ValueError(f"masks must be [n, {words}]")
+        if not isinstance(masks, np.ndarray) and not (masks.is_contiguous() and masks.element_size() == 4):
+            raise ValueError("masks must be contiguous 32-bit words")
+        n = mask_index.size if isinstance(mask_index, np.ndarray) else mask_index.numel()
+        _check(self.ctx, self.lib.dflash_set_token_masks(self.ctx, masks.shape[0], _ptr(masks), int(n), _ptr(mask_index)))
 
     def set_block_size(self, B: int):
         """Block size of the following rounds, 1 <= B <= the configured one."""

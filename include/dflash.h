@@ -202,6 +202,22 @@ dflash_status dflash_init(const dflash_config* cfg, const dflash_weights* w, voi
 dflash_status dflash_prefill(dflash_ctx* ctx, int32_t batch, const int32_t* prompt_lens,
                              const int32_t* prompt_tokens, int32_t* first_tokens);
 
+/* Prefill of a batch whose prompts begin with the same prefix_len tokens (a
+ * system prompt): dflash_prefill on prompts prefix + own tokens, with the
+ * prefix computed and stored once.  The whole 64-token pages of the prefix are
+ * shared by every sequence's page table (its remaining tokens are prefilled
+ * with each prompt), the prompts' own tokens run in ragged batched passes, and
+ * the following rounds attend to the shared keys once for the batch
+ * (dflash_shared_prefix_attention) until the next prefill.
+ * prefix: host [prefix_len]; prompt_lens: host [batch], each >= 1, without the
+ * prefix; prompt_tokens: host, concatenated; first_tokens: host [batch] output.
+ * The first call allocates the attention's workspace (kept until
+ * dflash_destroy).  Errors: as dflash_prefill, with lengths prefix_len +
+ * prompt_lens[i]; E_INVAL (prefix_len < 0, a prefix token outside [0, V)),
+ * E_NOMEM. */
+dflash_status dflash_prefill_shared(dflash_ctx* ctx, int32_t batch, int32_t prefix_len, const int32_t* prefix,
+                                    const int32_t* prompt_lens, const int32_t* prompt_tokens, int32_t* first_tokens);
+
 /* Set the block size B of the following rounds to block_size, between 1 and
  * the configured block size (the drafter's training block).  A drafter trained
  * at one block size still drafts well at a smaller one, and a smaller block
@@ -291,6 +307,41 @@ dflash_status dflash_verify(dflash_ctx* ctx, const int32_t* draft_tokens, int32_
  * Errors: E_INVAL (ctx NULL, top_k < 0, top_p outside (0, 1]), E_STATE
  * (between a draft and its verify), E_CUDA. */
 dflash_status dflash_set_sampling_filter(dflash_ctx* ctx, int32_t top_k, float top_p);
+
+/* Penalties and biases of the target's logits (the rule of
+ * dflash_process_logits), per sequence slot: host arrays of max_batch values
+ * (bias lists [max_batch][bias_width], id < 0: unused), copied.  NULL arrays
+ * are 1 / 0 / 0 and no bias; rules NULL turns them off.  They apply from the
+ * next prefill on: to the first token and to every verified row, greedy and
+ * sampled, where row j of a block follows the committed tokens, the anchor and
+ * the first j drafts; so the emitted stream is that of decoding token by token
+ * under the same rules.  The drafter's laws are not changed (a proposal may
+ * come from any law).  The temperature and the filter act on the result.
+ * Logits kept for dflash_inspect are those before the rules.
+ * Errors: E_INVAL (repetition not positive, a value not finite (a bias may be
+ * -inf), an id >= V, bias_width outside [0, 4096]), E_NOMEM. */
+typedef struct {
+    const float* repetition;
+    const float* presence;
+    const float* frequency;
+    int32_t bias_width;
+    const int32_t* bias_ids;
+    const float* bias_values;
+} dflash_logit_rules;
+dflash_status dflash_set_logit_rules(dflash_ctx* ctx, const dflash_logit_rules* rules);
+
+/* Token masks (grammar states) of the next target pass alone: between a draft
+ * and its verify, of that verify (rows = batch * B, row j of a block masks the
+ * token after its first j drafts); otherwise of the next prefill's first
+ * tokens (rows = its batch; a draft drops them).  masks: [n_masks][ceil(V / 32)] bit sets, host or
+ * device, copied (bit v % 32 of word v / 32: token v is allowed); mask_index:
+ * [rows], host or device, < 0: no mask.  n_masks 0 drops the masks.  A row that
+ * the masks and biases leave without a token is E_DEVICE_CHECK at the next
+ * synchronising call.
+ * Errors: E_INVAL (sizes, NULL, n_masks above max_batch * block_size, a host
+ * index >= n_masks), E_NOMEM, E_CUDA. */
+dflash_status dflash_set_token_masks(dflash_ctx* ctx, int32_t n_masks, const uint32_t* masks, int32_t rows,
+                                     const int32_t* mask_index);
 
 dflash_status dflash_draft_block_sampled(dflash_ctx* ctx, float temperature, const float* u_draft,
                                         int32_t* draft_tokens);

@@ -1,0 +1,360 @@
+"""Sessions behind one shared prefix (dflash_prefill_shared), with logit rules
+(dflash_set_logit_rules) and with token masks (dflash_set_token_masks), against
+the fp64 oracle on the whole prompts / the rules applied token by token."""
+import numpy as np
+import pytest
+
+import synth
+from synth import configs
+from oracle import model as om, serving, spec
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    from block_diffusion_speculative_ctx_gb300 import build
+    build.build()
+
+
+def _session(w, **kw):
+    from block_diffusion_speculative_ctx_gb300 import Session
+    return Session(w, **kw)
+
+
+def _prompts(w, prefix_len, lens, seed):
+    toks = synth.uniform_ints(seed, 0x70, prefix_len + sum(lens), w.vocab).astype(np.int32)
+    own, at = [], prefix_len
+    for n in lens:
+        own.append(toks[at:at + n])
+        at += n
+    return toks[:prefix_len], own
+
+
+def _rel(a, b):
+    return float(np.linalg.norm(a - b) / max(np.linalg.norm(b), 1e-30))
+
+
+# The bounds are those of the parity tests: fp32 logits 1e-3 and caches 1e-5; bf16 logits 5e-2 (tokens equal
+# but where the oracle's top two lie closer), caches 2e-2.
+@pytest.mark.parametrize("name,prefix_len,lens,schedule", [
+    ("tiny_f32_b3", 64, (7, 1, 30), None),            # a prefix of exactly one page
+    ("tiny_f32_b3", 150, (5, 60, 12), (4, 2, 1, 3)),  # two pages and 22 tokens, changing block sizes
+    ("small_f32", 300, (37, 100), None),
+    ("small_bf16", 130, (37, 100), None),
+    ("small_bf16", 1000, (3, 400), (16, 8)),
+    ("small_bf16_llama", 200, (64, 5, 130, 33), None),
+])
+def test_prefill_shared_and_rounds(name, prefix_len, lens, schedule):
+    w = configs.get(name)
+    w = w.with_(batch=len(lens), prompt_lens=tuple(prefix_len + n for n in lens))
+    bf16 = w.dtype == "bf16"
+    tol = 5e-2 if bf16 else 1e-3
+    m = om.Model(w)
+    prefix, own = _prompts(w, prefix_len, lens, 31)
+    states = [spec.prefill(m, np.concatenate([prefix, p])) for p in own]
+    rounds = 4
+    sess = _session(w, keep_logits=True, max_seq_len=max(w.prompt_lens) + (rounds + 2) * w.block_size + 8)
+    try:
+        first = sess.prefill_shared(prefix, own)
+        plog = sess.logits("prefill")
+        alive = [True] * len(states)
+        for s, st in enumerate(states):
+            assert np.abs(plog[s] - st.first_logits).max() <= tol
+            if int(first[s]) != st.anchor:
+                assert bf16 and spec.top2_margin(st.first_logits[None])[0] < tol
+                alive[s] = False
+            for l in range(w.draft_layers):
+                assert _rel(sess.cache("draft", "k", s, l), st.dcache.k[l]) < (2e-2 if bf16 else 1e-5)
+                assert _rel(sess.cache("draft", "v", s, l), st.dcache.v[l]) < (2e-2 if bf16 else 1e-5)
+        compared = 0
+        for r in range(rounds):
+            B = schedule[r % len(schedule)] if schedule else w.block_size
+            mr = spec.at_block_size(m, B) if schedule else m
+            if schedule:
+                sess.set_block_size(B)
+            sess.draft_block()
+            dlog = sess.logits("draft") if B > 1 else None
+            props = []
+            for s, st in enumerate(states):
+                if not alive[s]:
+                    props.append(np.zeros(B - 1, np.int64))
+                    continue
+                d, odl = spec.draft(mr, st)
+                if B > 1:
+                    assert np.abs(dlog[s] - odl).max() <= tol, f"round {r} sequence {s}"
+                props.append(np.asarray(d))
+            prop = np.stack(props).astype(np.int32) if B > 1 else np.zeros((len(states), 1), np.int32)
+            acc, bonus = sess.verify(prop)
+            vlog = sess.logits("verify")
+            for s, st in enumerate(states):
+                if not alive[s]:
+                    continue
+                rd = spec.verify(mr, st, prop[s][:B - 1].astype(np.int64), keep_logits=True)
+                assert np.abs(vlog[s] - rd.verify_logits).max() <= tol, f"round {r} sequence {s}"
+                if (int(acc[s]), int(bonus[s])) != (rd.accepted, rd.bonus):
+                    assert bf16 and spec.top2_margin(rd.verify_logits).min() < tol
+                    alive[s] = False
+                    continue
+                assert int(sess.lengths()[s]) == st.committed
+                compared += 1
+        assert compared >= 2
+    finally:
+        sess.close()
+
+
+def test_prefill_shared_runs_in_several_chunks():
+    """A prefix longer than one prefill chunk and more suffix rows than one (a sequence split over two), against a
+    plain prefill of the whole prompts by the same library; then graph replays equal eager rounds bit for bit."""
+    w = configs.get("small_bf16")
+    lens = (700, 3, 900, 1200, 64)
+    w = w.with_(batch=len(lens), prompt_lens=tuple(2200 + n for n in lens), target_layers=2, ctx_layer_ids=(0, 1), draft_layers=1)
+    prefix, own = _prompts(w, 2200, lens, 5)
+    out = {}
+    for mode in ("plain", "shared", "eager"):
+        sess = _session(w, keep_logits=True, max_seq_len=max(w.prompt_lens) + 200, graphs=mode != "eager")
+        try:
+            if mode == "plain":
+                sess.prefill([np.concatenate([prefix, p]) for p in own])
+            else:
+                sess.prefill_shared(prefix, own)
+            pl = sess.logits("prefill")
+            v = []
+            for r in range(4):
+                sess.draft_block()
+                prop = synth.uniform_ints(r, 0x7A, len(lens) * (w.block_size - 1), w.vocab).reshape(len(lens), -1).astype(np.int32)
+                sess.verify(prop)
+                v.append(sess.logits("verify"))
+            out[mode] = (pl, v)
+        finally:
+            sess.close()
+    # bf16 storage on both sides, sums in another order: the parity tests' bound, each side's
+    assert np.abs(out["plain"][0] - out["shared"][0]).max() <= 2 * 5e-2
+    assert np.abs(out["plain"][1][0] - out["shared"][1][0]).max() <= 2 * 5e-2
+    np.testing.assert_array_equal(out["shared"][0], out["eager"][0])
+    for a, b in zip(out["shared"][1], out["eager"][1]):
+        np.testing.assert_array_equal(a, b)
+
+
+def test_prefill_shared_pages_are_shared_and_errors():
+    from block_diffusion_speculative_ctx_gb300 import DFLASH_E_CAPACITY, DFLASH_E_INVAL, DFlashError
+    w = configs.get("tiny_f32_b3")
+    prefix, own = _prompts(w, 640, (10, 20, 30), 3)
+    w = w.with_(prompt_lens=tuple(640 + len(p) for p in own))
+    # ten shared pages and one own page each: 13 pages hold what 33 would without sharing
+    sess = _session(w, max_seq_len=760, kv_pool_tokens=13 * 64)
+    try:
+        with pytest.raises(DFlashError) as e:
+            sess.prefill([np.concatenate([prefix, p]) for p in own])
+        assert e.value.status == DFLASH_E_CAPACITY
+        first = sess.prefill_shared(prefix, own)
+        sess.verify(sess.draft_block())
+        with pytest.raises(DFlashError) as e:
+            sess.prefill_shared(prefix, [np.concatenate([p, prefix[:100]]) for p in own])
+        assert e.value.status == DFLASH_E_CAPACITY
+        bad = prefix.copy()
+        bad[3] = w.vocab
+        with pytest.raises(DFlashError) as e:
+            sess.prefill_shared(bad, own)
+        assert e.value.status == DFLASH_E_INVAL
+        with pytest.raises(DFlashError):
+            sess.prefill_shared(prefix, [own[0], own[1][:0], own[2]])
+        # a prefix below one page is a plain prefill; an empty one too; and the session is reusable
+        np.testing.assert_array_equal(sess.prefill_shared(prefix[:20], own), sess.prefill([np.concatenate([prefix[:20], p]) for p in own]))
+        np.testing.assert_array_equal(sess.prefill_shared(prefix[:0], own), sess.prefill(own))
+        np.testing.assert_array_equal(sess.prefill_shared(prefix, own), first)
+    finally:
+        sess.close()
+
+
+# ---------------------------------------------------------------------------------------------- logit rules
+RULES = dict(repetition=[1.3, 1.0, 2.0], presence=[0.5, 0.0, -0.25], frequency=[0.2, 0.4, 0.0],
+             bias=[{5: 3.0, 900: -1e9, 7: 2.5}, {}, {11: 4.0}])
+
+
+def _ruled(lg, history, prompt_len, s):
+    bias = RULES["bias"][s]
+    ids, vals = np.array([list(bias.keys()) or [-1]]), np.array([list(bias.values()) or [0.0]])
+    f = lambda k: np.float32([RULES[k][s]])  # noqa: E731
+    return serving.process_logits(lg[None], 1, history=np.array([history]), hist_lens=[len(history)], prompt_lens=[prompt_len],
+                                  repetition=f("repetition"), presence=f("presence"), frequency=f("frequency"),
+                                  bias_ids=ids, bias_values=vals.astype(np.float32))[0]
+
+
+def _ruled_stream(m, prompt, n, s, mask=None):
+    """Token by token under the rules: (tokens, their top-two margins)."""
+    st = spec.prefill(m, prompt)
+    cache = st.tcache.copy()
+    hist, out, margins = [int(t) for t in prompt], [], []
+    lg = st.first_logits
+    while len(out) < n:
+        z = _ruled(lg, hist, len(prompt), s)
+        if mask is not None:
+            z = np.where(mask(len(out)), z, -np.inf)
+        t = int(np.argmax(z))
+        margins.append(float(np.diff(np.sort(z[np.isfinite(z)])[-2:])[0]))
+        out.append(t)
+        hist.append(t)
+        lg = m.target_forward([t], cache)[0][0]
+    return np.array(out), np.array(margins)
+
+
+def _same_stream(got, stream, n):
+    """Equal up to the first difference, which may only be at a near-tie (both sides' logits agree to 1e-3, so the
+    top two of the oracle lie within 2e-3); returns how many tokens were compared."""
+    toks, margins = stream
+    for i in range(n):
+        if got[i] != toks[i]:
+            assert margins[i] < 2e-3, (i, got[i], toks[i], margins[i])
+            return i
+    return n
+
+
+@pytest.mark.parametrize("shared", [False, True])
+@pytest.mark.parametrize("planted", [False, True])
+def test_ruled_rounds_emit_the_token_by_token_stream(shared, planted):
+    """fp32: the speculative stream under penalties and biases equals decoding token by token under them, with the
+    drafter's own proposals and with planted ones (accepted drafts, which later rows must count)."""
+    w = configs.get("tiny_f32_b3")
+    m = om.Model(w)
+    prefix, own = _prompts(w, 70, (20, 7, 19), 9)
+    prompts = [np.concatenate([prefix, p]) for p in own]
+    n = 26
+    streams = [_ruled_stream(m, p, n + w.block_size, s) for s, p in enumerate(prompts)]
+    assert any(len(set(streams[s][0].tolist())) < n for s in range(3))   # tokens do repeat
+    w = w.with_(prompt_lens=tuple(len(p) for p in prompts))
+    sess = _session(w, max_seq_len=max(w.prompt_lens) + n + 4 * w.block_size)
+    try:
+        sess.set_logit_rules(**RULES)
+        first = sess.prefill_shared(prefix, own) if shared else sess.prefill(prompts)
+        got = [[int(first[s])] for s in range(3)]
+        rounds = 0
+        while min(len(g) for g in got) < n:
+            drafts = sess.draft_block()
+            if planted:   # true tokens, then a wrong one, 0..B-1 of them right
+                for s in range(3):
+                    right = (rounds + s) % w.block_size
+                    nxt = streams[s][0][len(got[s]):len(got[s]) + w.block_size - 1]
+                    drafts[s] = (streams[s][0][0] + 1) % w.vocab
+                    drafts[s][:min(right, len(nxt))] = nxt[:right]
+            acc, bonus = sess.verify(drafts)
+            for s in range(3):
+                got[s] += [int(t) for t in drafts[s][:acc[s]]] + [int(bonus[s])]
+            rounds += 1
+        assert sum(_same_stream(got[s], streams[s], n) for s in range(3)) >= 2 * n
+        if planted:
+            assert rounds < n - 1   # drafts were accepted
+        # off again: the plain greedy stream
+        sess.set_logit_rules()
+        first = sess.prefill(prompts)
+        for s in range(3):
+            assert int(first[s]) == spec.prefill(m, prompts[s]).anchor
+    finally:
+        sess.close()
+
+
+def test_ruled_sampled_round_at_top_1_is_the_greedy_one():
+    """top-k 1 keeps one token of each ruled law: the sampled round emits the ruled greedy stream."""
+    w = configs.get("tiny_f32_b3")
+    m = om.Model(w)
+    prompts = synth.prompts(w)
+    n = 14
+    streams = [_ruled_stream(m, p, n + w.block_size, s) for s, p in enumerate(prompts)]
+    sess = _session(w, max_seq_len=max(w.prompt_lens) + n + 4 * w.block_size)
+    rng = np.random.default_rng(0)
+    try:
+        sess.set_logit_rules(**RULES)
+        sess.set_sampling_filter(top_k=1)
+        first = sess.prefill(prompts)
+        got = [[int(first[s])] for s in range(3)]
+        while min(len(g) for g in got) < n:
+            d = sess.draft_block_sampled(1.3, rng.random((3, w.block_size - 1)).astype(np.float32))
+            acc, emit = sess.verify_sampled(1.3, d, rng.random((3, w.block_size)).astype(np.float32))
+            for s in range(3):
+                got[s] += [int(t) for t in d[s][:acc[s]]] + [int(emit[s])]
+        assert sum(_same_stream(got[s], streams[s], n) for s in range(3)) >= 2 * n
+    finally:
+        sess.close()
+
+
+def _pack(allowed):
+    V = allowed.shape[-1]
+    pad = np.zeros((allowed.shape[0], (V + 31) // 32 * 32), np.uint64)
+    pad[:, :V] = allowed
+    return (pad.reshape(allowed.shape[0], -1, 32) << np.arange(32, dtype=np.uint64)).sum(-1).astype(np.uint32)
+
+
+@pytest.mark.parametrize("device", [False, True])
+def test_masked_rounds_emit_the_masked_stream(device):
+    """A grammar by position: token k of a sequence must be k modulo 3.  With masks (one per state) on the first
+    tokens and on every verify, the emitted stream is the masked token-by-token one."""
+    import torch
+    w = configs.get("tiny_f32_b3")
+    m = om.Model(w)
+    prompts = synth.prompts(w)
+    V, n, B = w.vocab, 12, w.block_size
+    states = np.stack([np.arange(V) % 3 == k for k in range(3)])
+    saved = {k: RULES[k] for k in RULES}
+    streams = [_ruled_stream(m, p, n + B, s, mask=lambda k: states[k % 3]) for s, p in enumerate(prompts)]
+    assert RULES == saved
+    masks = _pack(states)
+    if device:
+        masks = torch.from_numpy(masks.view(np.int32)).cuda()
+    put = lambda i: torch.as_tensor(np.asarray(i), dtype=torch.int32).cuda() if device else np.asarray(i, np.int32)  # noqa: E731
+    sess = _session(w, max_seq_len=max(w.prompt_lens) + 6 * n + 4 * B)
+    try:
+        sess.set_logit_rules(**RULES)
+        sess.set_token_masks(masks, put([0, 0, 0]))
+        first = sess.prefill(prompts)
+        got = [[int(first[s])] for s in range(3)]
+        while min(len(g) for g in got) < n:
+            drafts = sess.draft_block()
+            for s in range(3):
+                nxt = streams[s][0][len(got[s]):len(got[s]) + B - 1]
+                drafts[s][:len(nxt)] = nxt
+                drafts[s][s:] = 0   # some right, the rest wrong or right by chance
+            sess.set_token_masks(masks, put([[(len(got[s]) + j) % 3 for j in range(B)] for s in range(3)]).reshape(-1))
+            acc, bonus = sess.verify(drafts)
+            for s in range(3):
+                got[s] += [int(t) for t in drafts[s][:acc[s]]] + [int(bonus[s])]
+        assert sum(_same_stream(got[s], streams[s], n) for s in range(3)) >= 2 * n
+    finally:
+        sess.close()
+
+
+def test_masks_that_leave_nothing_and_bad_masks():
+    from block_diffusion_speculative_ctx_gb300 import DFLASH_E_DEVICE_CHECK, DFLASH_E_INVAL, DFlashError
+    w = configs.get("tiny_f32_b3")
+    prompts = synth.prompts(w)
+    words = (w.vocab + 31) // 32
+    none, some = np.zeros((1, words), np.uint32), np.full((1, words), 3, np.uint32)
+    B = w.block_size
+    sess = _session(w)
+    try:
+        sess.set_token_masks(none, [-1, 0, -1])
+        with pytest.raises(DFlashError) as e:
+            sess.prefill(prompts)
+        assert e.value.status == DFLASH_E_DEVICE_CHECK and "without a token" in str(e.value)
+        sess.set_token_masks(some, [0, 0])
+        with pytest.raises(DFlashError) as e:   # set for two rows, the prefill has three
+            sess.prefill(prompts)
+        assert e.value.status == DFLASH_E_INVAL
+        sess.set_token_masks()
+        plain = sess.prefill(prompts)
+        for bad in ((none, [0] * 3), (none, [1] * (3 * B)), (np.zeros((1 + 3 * B, words), np.uint32), [0] * (3 * B))):
+            d = sess.draft_block() if sess.lengths()[0] == len(prompts[0]) and bad[1] == [0] * 3 else d
+            with pytest.raises(DFlashError) as e:
+                sess.set_token_masks(*bad)
+            assert e.value.status == DFLASH_E_INVAL
+        sess.set_token_masks(none, [-1] * (3 * B - 1) + [0])
+        with pytest.raises(DFlashError) as e:
+            sess.verify(d)
+        assert e.value.status == DFLASH_E_DEVICE_CHECK
+        np.testing.assert_array_equal(sess.prefill(prompts), plain)   # masks are for one pass; the session goes on
+        for kw in (dict(repetition=0.0), dict(repetition=float("nan")), dict(presence=float("inf")), dict(bias={w.vocab: 1.0}),
+                   dict(bias={1: float("nan")})):
+            with pytest.raises(DFlashError) as e:
+                sess.set_logit_rules(**kw)
+            assert e.value.status == DFLASH_E_INVAL
+    finally:
+        sess.close()
