@@ -20,11 +20,11 @@ namespace {
 
 // Merge of the partial results: out = sum_i 2^(m_i - M) o_i / sum_i 2^(m_i - M) l_i over the segments that
 // hold the row's query vectors, prefix and own, in plan order (one fixed order: the same bits every run).
-// A warp takes one row and one KV head: lanes find the row's sequence and work out the workers of its items
-// (a segment a lane), then take 8 head dimensions of one query vector each (whole 32-byte sectors) and
-// stream the segments through, four in flight.  NW > 1: the warps of a CTA share one (row, KV head), each
-// taking every NW-th segment, for calls of few rows (whose prefix is split the most).  Bytes: 4 hd + 8 per
-// vector and segment, from L2; a row's chain of dependent loads is what a small call waits for.
+// A warp takes one row and one KV head, whose blocks the main kernel has written down (Dir); lanes take 8
+// head dimensions of one query vector each (whole 32-byte sectors) and stream the segments through, two in
+// flight.  NW > 1: the warps of a CTA share one (row, KV head), each taking every NW-th segment, for calls of
+// few rows (whose prefix is split the most).  Bytes: 4 hd + 8 per vector and segment, from L2; a small call
+// waits for its chain of loads and, as much, for the code itself to come from L2 (hence rolled loops).
 struct MergeArgs {
     sp::Shape P;
     sp::Work W;
@@ -62,22 +62,6 @@ struct Part {
     }
 };
 
-// A row's item on its line: the blocks of its segments (first, step, count) and the row's first vector in
-// its stream.
-struct Item {
-    int block = 0, step = 1, count = 0, v = 0;
-};
-__device__ __forceinline__ Item item_of(const sp::Shape& P, const sp::Head& h, int line, uint32_t at, int id, int n_eff, int rl) {
-    Item i;
-    const uint32_t part = h.part[line], t0 = at + (uint32_t)P.lead[line];
-    const int c0 = (int)(t0 / part), x = rl >= P.RH ? 1 : 0;
-    i.count = (int)((t0 + (uint32_t)n_eff - 1u) / part) - c0 + 1;
-    i.step = line == 0 ? 2 : 1;
-    i.block = (int)sp::block_of(P, h, line, id, c0) + x;
-    i.v = (rl - x * P.RH) * P.g;
-    return i;
-}
-
 template <typename T, int NW>
 __global__ void __launch_bounds__(32 * MWARPS, 4) merge_kernel(MergeArgs a) {
     using namespace sp;
@@ -85,35 +69,17 @@ __global__ void __launch_bounds__(32 * MWARPS, 4) merge_kernel(MergeArgs a) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int r = NW > 1 ? blockIdx.x : blockIdx.x * MWARPS + warp, kvh = blockIdx.y;
     __shared__ Part part_s[NW > 1 ? NW : 1][32];
+    if (r >= P.rows) return;  // (NW > 1: the whole CTA)
     pdl_wait();
     pdl_trigger();
-    if (r >= P.rows) return;  // (NW > 1: the whole CTA)
-    const Head h = *a.W.head;
+    const Dir d = a.W.dir[(size_t)r * P.Hkv + kvh];
     uint32_t err = 0;
 #pragma unroll
     for (int i = 0; i < 5; ++i)
         if (lane + 32 * i < P.n_cta) err |= a.W.err[lane + 32 * i];
-    const bool live = r >= h.r_begin && r < h.r_end;
-    bool bad = __any_sync(0xffffffffu, h.bad || err != 0);
-    if (!bad && !live) return;  // a row of no sequence
-    Item pre, own;
-    if (!bad) {
-        const Rec rec = a.W.rec[a.W.row_seq[r]];
-        const Seq q = seq_of(P, rec.start, rec.start + rec.m, rec.kv);
-        bad = rec.kv < 0 || rec.kv > (long long)64 * P.width;
-        if (P.npt) {
-            const int RT = P.row_tile(h.pl), rt = (r - h.r_begin) / RT, id = kvh * h.nqt + rt;
-            pre = item_of(P, h, h.pl, (uint32_t)id * (uint32_t)(P.lead[h.pl] + P.npt), id, P.npt, r - h.r_begin - rt * RT);
-        }
-        if (q.tiles) {
-            const int RT = P.row_tile(q.line), j = r - rec.start, gi = j / RT, k = kvh * q.groups + gi;
-            const int n_eff = seen_tiles(P, q, min(q.m, (gi + 1) * RT));
-            if (n_eff)
-                own = item_of(P, h, q.line, rec.base + (uint32_t)k * (uint32_t)(P.lead[q.line] + q.tiles),
-                              (h.pl == q.line ? h.n_prefix : 0) + (int)rec.ibase + k, n_eff, j - gi * RT);
-        }
-    }
-    const int count = pre.count + own.count;
+    if (d.pre_count == -1) return;  // a row of no sequence
+    const bool bad = __any_sync(0xffffffffu, err != 0) || d.pre_count == -2;
+    const int count = bad ? 0 : d.pre_count + d.own_count;
     const int w0 = NW > 1 ? warp : 0;
     const int chunks = P.hd / 8, elems = P.g * chunks;
 #pragma unroll 1
@@ -131,9 +97,9 @@ __global__ void __launch_bounds__(32 * MWARPS, 4) merge_kernel(MergeArgs a) {
                 ml[i] = make_float2(-INFINITY, 0.f);
                 x[i] = y[i] = make_float4(0.f, 0.f, 0.f, 0.f);
                 if (k < count) {
-                    const bool p = k < pre.count;
-                    const size_t blk = p ? pre.block + k * pre.step : own.block + (k - pre.count) * own.step;
-                    const int v = (p ? pre.v : own.v) + hh;
+                    const bool p = k < d.pre_count;
+                    const size_t blk = p ? d.pre_block + k * d.pre_step : d.own_block + (k - d.pre_count) * d.own_step;
+                    const int v = (p ? d.pre_v : d.own_v) + hh;
                     ml[i] = a.W.ml[blk * P.VT + v];
                     const float* src = a.W.o + ((blk * chunks + c8) * P.VT + v) * 8;
                     x[i] = *reinterpret_cast<const float4*>(src);

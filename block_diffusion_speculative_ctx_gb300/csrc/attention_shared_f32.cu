@@ -57,12 +57,10 @@ __global__ void __launch_bounds__(NT) shared_f32_kernel(F32Args a) {
     const int tid = threadIdx.x, lane = tid & 31, cta = blockIdx.x;
     const int tv = tid >> 3, td = tid & 7;  // vectors 2 tv, 2 tv + 1; keys td + 8 i, dimensions 4 td + 32 i
     pdl_wait();
-    pdl_trigger();
     Head h;
     make_plan<NT>(P, S.base, S.ibase, &S.plan, h);
-    if (cta == 0 && tid == 0) *a.W.head = h;
     if (cta < P.n_cta && tid == 0) a.W.err[cta] = 0u;
-    if (!h.bad) write_records(P, a.W, S.base, S.ibase, cta, gridDim.x, tid >> 5, NT / 32, lane);
+    write_dir(P, h, a.W, S.base, S.ibase, (tid >> 5) * gridDim.x + cta, gridDim.x * (NT / 32), lane);
 
     Walk walk(P, h, 1, cta);
     Seg s;
@@ -191,6 +189,7 @@ __global__ void __launch_bounds__(NT) shared_f32_kernel(F32Args a) {
         }
         __syncthreads();  // Q, K, V and P are free for the next segment
     }
+    pdl_trigger();
 }
 
 template <int HD>

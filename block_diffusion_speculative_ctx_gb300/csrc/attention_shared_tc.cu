@@ -241,15 +241,14 @@ __global__ void __launch_bounds__(NTHR, 1)
         prefetch_tmap(&mv);
     }
     pdl_wait();
-    pdl_trigger();
     if (tid == 0) a.W.err[cta] = 0u;
     Head h;
     fence_before();
     make_plan<NTHR>(P, base, ibase, &bars->plan, h);  // (its barriers order the setup above)
     fence_after();
     const uint32_t tmem = bars->tmem;
-    if (cta == 0 && tid == 0) *a.W.head = h;
-    if (!h.bad) write_records(P, a.W, base, ibase, cta, P.n_cta, warp, NTHR / 32, lane);
+    // for the merge kernel, by the warps that have nothing to do until the first scores
+    if (warp < 8) write_dir(P, h, a.W, base, ibase, warp * P.n_cta + cta, 8 * P.n_cta, lane);
     uint32_t* err = &a.W.err[cta];
     Waiter wait{err, &bars->fail};
 
@@ -564,6 +563,8 @@ __global__ void __launch_bounds__(NTHR, 1)
         }
         __syncwarp();
     }
+    // (not earlier: the merge's CTAs would gather on the SMs that are free first)
+    pdl_trigger();
     fence_before();
     __syncthreads();
     if (warp == 8) {

@@ -42,7 +42,7 @@ struct Shape {
     __host__ __device__ int workers(int line) const { return line == 0 ? n_cta : 2 * n_cta; }
 };
 
-// Cut of the lines, written by CTA 0 for the merge kernel.
+// Cut of the lines.
 struct Head {
     uint32_t W[2];     // length
     uint32_t part[2];  // length of a worker's part: ceil(W / workers)
@@ -52,21 +52,20 @@ struct Head {
     int n_prefix;      // prefix items
     int r_begin, r_end;
     int nqt;           // row tiles of the batch on line pl
+    int max_m;         // rows of the longest sequence
     int bad;           // q_start is not a list of rows, or a line is too long
 };
 
-// A sequence as the merge kernel reads it: its rows, keys, and its own items' first unit and number on
-// their line.
-struct Rec {
-    int start, m, kv;
-    uint32_t base, ibase, pad[3];
+// Where the partial results of one row and KV head lie: blocks (first, count, step) and the row's first
+// vector in them, of its prefix item and its own.  pre_count -1: a row of no sequence; -2: NaN.
+struct Dir {
+    int pre_block, pre_count, own_block, own_count;
+    int pre_v, own_v, pre_step, own_step;
 };
 
 struct Work {
-    Head* head;
     uint32_t* err;        // [n_cta]: a bounded wait ran out
-    Rec* rec;             // [batch]
-    int* row_seq;         // [rows]: of the rows in [r_begin, r_end)
+    Dir* dir;             // [rows][Hkv]
     uint32_t* block_bad;  // [blocks]: a page of the segment lies outside the cache
     float2* ml;           // [blocks][VT]
     float* o;             // [blocks][hd / 8][VT][8]
@@ -89,10 +88,8 @@ inline size_t layout(char* p, const Shape& P, Work* w) {
     };
     const size_t blocks = (size_t)max_blocks(P);
     Work x;
-    x.head = (Head*)take(sizeof(Head));
     x.err = (uint32_t*)take((size_t)P.n_cta * 4);
-    x.rec = (Rec*)take((size_t)P.batch * sizeof(Rec));
-    x.row_seq = (int*)take((size_t)P.rows * 4);
+    x.dir = (Dir*)take((size_t)P.rows * P.Hkv * sizeof(Dir));
     x.block_bad = (uint32_t*)take(blocks * 4);
     x.ml = (float2*)take(blocks * P.VT * 8);
     x.o = (float*)take(blocks * P.VT * P.hd * 4);
@@ -209,13 +206,13 @@ template <int NTHR>
 struct PlanMem {
     uint32_t ws[NTHR / 32][4];
     unsigned long long sum[2];  // in 64 bits: a line of 2^31 units or more is refused
-    int bad;
+    int bad, max_m;
 };
 template <int NTHR>
 __device__ __forceinline__ void make_plan(const Shape& P, uint32_t* base, uint32_t* ibase, PlanMem<NTHR>* m, Head& h) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     if (tid == 0) {
-        m->bad = 0;
+        m->bad = m->max_m = 0;
         m->sum[0] = m->sum[1] = 0;
     }
     h.r_begin = P.q_start[0];
@@ -248,6 +245,7 @@ __device__ __forceinline__ void make_plan(const Shape& P, uint32_t* base, uint32
                 line = q.line;
                 const uint32_t items = (uint32_t)(q.groups * P.Hkv), per = (uint32_t)(P.lead[line] + q.tiles);
                 if (items) atomicAdd(&m->sum[line], (unsigned long long)items * per);
+                atomicMax(&m->max_m, q.m);
                 v[line] = items * per;
                 v[2 + line] = items;
             }
@@ -283,6 +281,7 @@ __device__ __forceinline__ void make_plan(const Shape& P, uint32_t* base, uint32
     if (bad) m->bad = 1;
     __syncthreads();
     h.bad = m->bad || m->sum[0] >> 31 || m->sum[1] >> 31;
+    h.max_m = m->max_m;
 #pragma unroll
     for (int l = 0; l < 2; ++l) {
         h.W[l] = h.bad ? 0u : carry[l];
@@ -291,18 +290,56 @@ __device__ __forceinline__ void make_plan(const Shape& P, uint32_t* base, uint32
     h.items0 = carry[2] + (h.pl == 0 ? (uint32_t)h.n_prefix : 0u);
 }
 
-// For the merge kernel: a warp per sequence writes its record and its rows' map.
-__device__ __forceinline__ void write_records(const Shape& P, const Work& W, const uint32_t* base, const uint32_t* ibase,
-                                              int cta, int ctas, int warp, int warps, int lane) {
+// The blocks of a row's item on its line: first unit `at`, number `id`, n_eff tiles seen, place rl in it.
+__device__ __forceinline__ void dir_item(const Shape& P, const Head& h, int line, uint32_t at, int id, int n_eff, int rl,
+                                         int& block, int& count, int& v, int& step) {
+    const uint32_t part = h.part[line], t0 = at + (uint32_t)P.lead[line];
+    const int c0 = (int)(t0 / part), x = rl >= P.RH ? 1 : 0;
+    count = (int)((t0 + (uint32_t)n_eff - 1u) / part) - c0 + 1;
+    step = line == 0 ? 2 : 1;
+    block = (int)block_of(P, h, line, id, c0) + x;
+    v = (rl - x * P.RH) * P.g;
+}
+
+// The directory for the merge kernel, by `warps` warps of which this is number `w`: a warp takes 32 (row, KV
+// head) pairs of one sequence at a time.
+__device__ __forceinline__ void write_dir(const Shape& P, const Head& h, const Work& W, const uint32_t* base,
+                                          const uint32_t* ibase, int w, int warps, int lane) {
+    // rows of no sequence, or of a call that went wrong
+    const int none = h.bad ? P.rows : P.rows - (h.r_end - h.r_begin);
 #pragma unroll 1
-    for (int q = warp * ctas + cta; q < P.batch; q += ctas * warps) {
-        const int start = P.q_start[q], m = P.q_start[q + 1] - start;
-        if (lane == 0) {
-            const Rec r = {start, m, P.kv_lens[q], base[(m > P.RH && !P.one_line ? 0 : MAX_BATCH) + q], ibase[q], {0u, 0u, 0u}};
-            W.rec[q] = r;
+    for (int i = w * 32 + lane; i < none * P.Hkv; i += warps * 32) {
+        const int k = i / P.Hkv, r = h.bad || k < h.r_begin ? k : k + (h.r_end - h.r_begin);
+        W.dir[(size_t)r * P.Hkv + (i - k * P.Hkv)].pre_count = h.bad ? -2 : -1;
+    }
+    if (h.bad) return;
+    const int chunks = cdiv(h.max_m * P.Hkv, 32);
+#pragma unroll 1
+    for (int u = w; u < P.batch * chunks; u += warps) {
+        const int s = u / chunks, i = (u - s * chunks) * 32 + lane;
+        const int start = P.q_start[s], m = P.q_start[s + 1] - start;
+        if (i >= m * P.Hkv) continue;
+        const Seq q = seq_of(P, start, start + m, P.kv_lens[s]);
+        const int j = i / P.Hkv, kvh = i - j * P.Hkv, r = start + j;
+        Dir d = {0, 0, 0, 0, 0, 0, 1, 1};
+        if (q.kv < 0 || q.kv > (long long)64 * P.width) {
+            d.pre_count = -2;
+        } else {
+            if (P.npt) {
+                const int RT = P.row_tile(h.pl), rt = (r - h.r_begin) / RT, id = kvh * h.nqt + rt;
+                dir_item(P, h, h.pl, (uint32_t)id * (uint32_t)(P.lead[h.pl] + P.npt), id, P.npt, r - h.r_begin - rt * RT,
+                         d.pre_block, d.pre_count, d.pre_v, d.pre_step);
+            }
+            if (q.tiles) {
+                const int RT = P.row_tile(q.line), gi = j / RT, k = kvh * q.groups + gi;
+                const int n_eff = seen_tiles(P, q, min(m, (gi + 1) * RT));
+                if (n_eff)
+                    dir_item(P, h, q.line, base[q.line * MAX_BATCH + s] + (uint32_t)k * (uint32_t)(P.lead[q.line] + q.tiles),
+                             (h.pl == q.line ? h.n_prefix : 0) + (int)ibase[s] + k, n_eff, j - gi * RT, d.own_block, d.own_count,
+                             d.own_v, d.own_step);
+            }
         }
-#pragma unroll 1
-        for (int i = lane; i < m; i += 32) W.row_seq[start + i] = q;
+        W.dir[(size_t)r * P.Hkv + kvh] = d;
     }
 }
 
