@@ -21,7 +21,7 @@ namespace {
 // Merge of the partial results: out = sum_i 2^(m_i - M) o_i / sum_i 2^(m_i - M) l_i over the segments that
 // hold the row's query vectors, prefix and own, in plan order (one fixed order: the same bits every run).
 // A warp takes one row and one KV head, whose blocks the main kernel has written down (Dir); lanes take 8
-// head dimensions of one query vector each (whole 32-byte sectors) and stream the segments through, two in
+// head dimensions of one query vector each (whole 32-byte sectors) and stream the segments through, four in
 // flight.  NW > 1: the warps of a CTA share one (row, KV head), each taking every NW-th segment, for calls of
 // few rows (whose prefix is split the most).  Bytes: 4 hd + 8 per vector and segment, from L2; a small call
 // waits for its chain of loads and, as much, for the code itself to come from L2 (hence rolled loops).
@@ -63,7 +63,7 @@ struct Part {
 };
 
 template <typename T, int NW>
-__global__ void __launch_bounds__(32 * MWARPS, 4) merge_kernel(MergeArgs a) {
+__global__ void __launch_bounds__(32 * MWARPS, 3) merge_kernel(MergeArgs a) {
     using namespace sp;
     const Shape& P = a.P;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -88,11 +88,11 @@ __global__ void __launch_bounds__(32 * MWARPS, 4) merge_kernel(MergeArgs a) {
         Part acc;
         uint32_t bb = 0;
 #pragma unroll 1
-        for (int k0 = w0; k0 < count; k0 += 2 * NW) {
-            float2 ml[2];
-            float4 x[2], y[2];
+        for (int k0 = w0; k0 < count; k0 += 4 * NW) {
+            float2 ml[4];
+            float4 x[4], y[4];
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
+            for (int i = 0; i < 4; ++i) {
                 const int k = k0 + i * NW;
                 ml[i] = make_float2(-INFINITY, 0.f);
                 x[i] = y[i] = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -108,7 +108,7 @@ __global__ void __launch_bounds__(32 * MWARPS, 4) merge_kernel(MergeArgs a) {
                 }
             }
 #pragma unroll
-            for (int i = 0; i < 2; ++i) acc.join(ml[i].x, ml[i].y, x[i], y[i]);
+            for (int i = 0; i < 4; ++i) acc.join(ml[i].x, ml[i].y, x[i], y[i]);
         }
         if (bb) acc.M = NAN;  // (a NaN maximum makes the whole row NaN below)
         if (NW > 1) {

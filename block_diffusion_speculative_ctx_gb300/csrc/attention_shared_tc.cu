@@ -54,18 +54,18 @@ struct Cfg {
     static constexpr int Q_REG = VT * 128, Q_TILE = HALVES * Q_REG;
     static constexpr int KV_REG = KT * 128, TILE = HALVES * KV_REG;
     static constexpr int STAGES = HD == 128 ? 8 : 16;  // 128 KB
-    static constexpr int LOG_STAGES = HD == 128 ? 3 : 4;
     static constexpr int RING_AT = 2 * Q_TILE;
     static constexpr int SMEM_TILES = RING_AT + STAGES * TILE;
 };
 
 constexpr int SEGS = 4;
+constexpr int STAGGER = 700;  // cycles
 // A wait for batch i must not begin once batch i + DONE can have completed (the barrier's parity would be
 // that of before i).  The load warps wait the latest: a stage comes round after at most 16 ring positions, and
 // the shortest segments (one tile: two positions, three batches) put 24 batches on those.
 constexpr int DONE = 32;
 struct LineBars {
-    uint64_t kv_full[16];
+    uint64_t kv_full[2][DONE];  // per load warp: V and K of its i-th batch have landed, on barrier i % DONE
     uint64_t q_full[2], q_empty[2];
     uint64_t p_full[2][2];     // per stream and S buffer
     uint64_t done[2][DONE];    // per stream: its i-th batch of products, on barrier i % DONE
@@ -184,8 +184,8 @@ struct Waiter {
         return ok;
     }
     // about a second
-    static __device__ __noinline__ bool late(uint64_t* bar, uint32_t parity) {
-        for (uint32_t i = 0; i < (1u << 23); ++i) {
+    static __device__ __noinline__ bool late(uint64_t* bar, uint32_t parity, uint32_t limit = 1u << 23) {
+        for (uint32_t i = 0; i < limit; ++i) {
             if (mbar_try_wait(bar, parity)) return true;
             if (i >= 1024) __nanosleep(128);
         }
@@ -218,12 +218,14 @@ __global__ void __launch_bounds__(NTHR, 1)
     if (tid == 0) {
         for (int line = 0; line < 2; ++line) {
             LineBars* B = &bars->line[line];
-            for (int i = 0; i < C::STAGES; ++i) mbar_init(&B->kv_full[i], 1);
             for (int x = 0; x < 2; ++x) {
                 mbar_init(&B->q_full[x], 1);
                 mbar_init(&B->q_empty[x], 1);
                 for (int b = 0; b < 2; ++b) mbar_init(&B->p_full[x][b], 4);
-                for (int b = 0; b < DONE; ++b) mbar_init(&B->done[x][b], 1);
+                for (int b = 0; b < DONE; ++b) {
+                    mbar_init(&B->done[x][b], 1);
+                    mbar_init(&B->kv_full[x][b], 1);
+                }
                 mbar_init(&B->o_empty[x], 4);
                 mbar_init(&B->drain[x], 1);
                 for (int i = 0; i < SEGS; ++i) {
@@ -260,9 +262,10 @@ __global__ void __launch_bounds__(NTHR, 1)
         if (turn == 1) __syncthreads();  // every role of the first line has ended: the ring and TMEM are free
         if (h.W[line] == 0 || bars->fail) continue;
         // ring of a stream: all stages, in step with the other stream (line 0), or half of them (line 1)
-        const uint32_t depth = pair ? C::STAGES : C::STAGES / 2, dshift = pair ? C::LOG_STAGES : C::LOG_STAGES - 1;
+        const uint32_t depth = pair ? C::STAGES : C::STAGES / 2;
         auto stage_of = [&](uint32_t pos) { return pos & (depth - 1); };
-        auto phase_of = [&](uint32_t pos) { return (pos >> dshift) & 1u; };
+        // the tiles of the i-th batch of stream x have landed
+        auto landed = [&](int x, uint32_t i) { return wait(&B->kv_full[pair ? 0 : x][i % DONE], (i / DONE) & 1); };
         // the i-th batch of stream x has completed (i counts through the line)
         auto batch_done = [&](int x, uint32_t i) { return wait(&B->done[x][i % DONE], (i / DONE) & 1); };
         auto worker = [&](int x) { return pair ? cta : 2 * cta + x; };
@@ -284,7 +287,7 @@ __global__ void __launch_bounds__(NTHR, 1)
             const int x = warp - 10;
             if (!pair || x == 0) {
                 Walk walk(P, h, line, worker(x));
-                uint32_t nseg = 0, issued = 0, nb = 0;  // nb: batches before this segment
+                uint32_t nseg = 0, armed = 0, nb = 0;  // nb: batches before this segment
                 int kvh, row0, seq;
                 Seg s;
 #pragma unroll 1
@@ -323,34 +326,37 @@ __global__ void __launch_bounds__(NTHR, 1)
                             const int row = p < 0 ? oob : (p * P.Hkv + kvh) * 64;
                             const uint32_t pos = ring + (kv ? v_seq(j, n) : k_seq(j)), st = first_stage(x) + stage_of(pos);
                             if (pos < depth || (batch_done(x, bars->rel[st]) && (!pair || batch_done(1, bars->rel[st])))) {
-                                bars->rel[st] = nb + j + 2 * kv;
-                                mbar_arrive_expect_tx(&B->kv_full[st], C::TILE);
+                                const uint32_t i = nb + j + 2 * kv;
+                                bars->rel[st] = i;
 #pragma unroll
                                 for (int c = 0; c < C::HALVES; ++c)
-                                    tma_load_2d_u(ring_at + st * C::TILE + c * C::KV_REG, kv ? &mv : &mk, &B->kv_full[st],
-                                                  64 * c, row);
-                                issued = pos + 1;
+                                    tma_load_2d_u(ring_at + st * C::TILE + c * C::KV_REG, kv ? &mv : &mk,
+                                                  &B->kv_full[x][i % DONE], 64 * c, row);
                             }
                         }
                     };
 #pragma unroll 1
-                    for (int j = -1; j < n; ++j) {
-                        if (j >= 0) tile(1, j);
-                        if (j < 0 || j + 1 < n) {
-                            if (j < 0) {
-                                tile(0, 0);
-                                // the queries: behind the first tile, whose stage waits for the segment before alone
-                                if (lane == 0)
-                                    for (int y = x; y < (pair ? 2 : x + 1); ++y) {
-                                        if (!wait(&B->q_empty[y], (nseg & 1) ^ 1)) break;
-                                        mbar_arrive_expect_tx(&B->q_full[y], C::HALVES * 128 * P.g * P.RH);
+                    for (int j = -2; j < n; ++j) {
+                        // batch: V of tile j, K of tile j + 2
+                        const bool has_v = j >= 0, has_k = j + 2 < n;
+                        if (lane == 0) {
+                            uint64_t* bar = &B->kv_full[x][(nb + j + 2) % DONE];
+                            if (has_v || has_k) mbar_arrive_expect_tx(bar, (has_v + has_k) * C::TILE);
+                            else mbar_arrive(bar);  // (an empty batch has its phase too)
+                        }
+                        if (has_v) tile(1, j);
+                        if (has_k) tile(0, j + 2);
+                        armed = nb + j + 3;
+                        if (j == -2 && lane == 0) {
+                            // the queries: behind the first tile, whose stage waits for the segment before alone
+                            for (int y = x; y < (pair ? 2 : x + 1); ++y) {
+                                if (!wait(&B->q_empty[y], (nseg & 1) ^ 1)) break;
+                                mbar_arrive_expect_tx(&B->q_full[y], C::HALVES * 128 * P.g * P.RH);
 #pragma unroll
-                                        for (int c = 0; c < C::HALVES; ++c)
-                                            tma_load_3d(q_at + y * C::Q_TILE + c * C::Q_REG, &mq, &B->q_full[y], 64 * c,
-                                                        kvh * P.g, row0 + (pair ? y * P.RH : 0));
-                                    }
+                                for (int c = 0; c < C::HALVES; ++c)
+                                    tma_load_3d(q_at + y * C::Q_TILE + c * C::Q_REG, &mq, &B->q_full[y], 64 * c, kvh * P.g,
+                                                row0 + (pair ? y * P.RH : 0));
                             }
-                            if (j + 2 < n) tile(0, j + 2);
                         }
                         wait.ok = __shfl_sync(0xffffffffu, (int)wait.ok, 0);
                         if (!wait.ok) break;
@@ -374,8 +380,8 @@ __global__ void __launch_bounds__(NTHR, 1)
                 }
                 // a wait ran out: the copies in flight must land before the CTA leaves its shared memory
                 if (lane == 0 && !wait.ok) {
-                    for (uint32_t pos = issued > depth ? issued - depth : 0; pos < issued; ++pos)
-                        Waiter::late(&B->kv_full[first_stage(x) + stage_of(pos)], phase_of(pos));
+                    for (uint32_t i = armed > DONE ? armed - DONE : 0; i < armed; ++i)
+                        Waiter::late(&B->kv_full[x][i % DONE], (i / DONE) & 1, 1u << 16);
                     for (int y = x; y < (pair ? 2 : x + 1); ++y)
                         if (nseg) Waiter::late(&B->q_full[y], (nseg - 1) & 1);
                 }
@@ -397,14 +403,18 @@ __global__ void __launch_bounds__(NTHR, 1)
 #pragma unroll 1
                     for (int j = -2; j < n; ++j) {
                         // batch: P V of tile j, S of tile j + 2
-                        const uint32_t vpos = ring + v_seq(max(j, 0), n), vst = first_stage(x) + stage_of(vpos);
-                        const uint32_t kpos = ring + k_seq(j + 2), kst = first_stage(x) + stage_of(kpos);
+                        const uint32_t vst = first_stage(x) + stage_of(ring + v_seq(max(j, 0), n));
+                        const uint32_t kst = first_stage(x) + stage_of(ring + k_seq(j + 2));
                         const uint32_t d = tS + 64 * ((nt + j) & 1);  // S buffer of both tiles
-                        if (j + 2 < n) wait(&B->kv_full[kst], phase_of(kpos));
+                        if (j >= 0 || j + 2 < n) landed(x, nb + j + 2);
                         if (j >= 0) {
-                            wait(&B->kv_full[vst], phase_of(vpos));
                             if (j == 0) wait(&B->o_empty[x], (nseg & 1) ^ 1);  // the segment before has been read out
                             wait(&B->p_full[x][(nt + j) & 1], ((nt + j) >> 1) & 1);
+                        } else if (pair && x == 1 && nb + j == (uint32_t)-2) {
+                            // the streams half a tile apart: in step, both would wait for their softmax while the
+                            // tensor cores idle
+                            for (const long long t = clock64(); clock64() - t < STAGGER;) {
+                            }
                         }
                         if (!wait.ok) break;
                         fence_after();
@@ -464,8 +474,8 @@ __global__ void __launch_bounds__(NTHR, 1)
                     if (k0 + KT > s.keys) {
                         // the list ends inside this tile: zero the rows of V behind it (a page's unused slots may
                         // hold anything, and 0 * NaN is NaN); on line 0 both streams do, each before its own P V
-                        const uint32_t pos = ring + v_seq(j, n), st = first_stage(x) + stage_of(pos);
-                        if (!wait(&B->kv_full[st], phase_of(pos))) break;
+                        const uint32_t st = first_stage(x) + stage_of(ring + v_seq(j, n));
+                        if (!landed(x, nb + j + 2)) break;
                         uint8_t* V = sm + C::RING_AT + st * C::TILE;
                         for (int i = (s.keys - k0) * 8 + v; i < KT * 8; i += 128)
 #pragma unroll
