@@ -17,7 +17,10 @@
 // Odd CTAs walk line 1 first, so that the bytes of one line stream while the
 // other line's products run on the neighbours.
 // Roles (warps): 0-3 softmax of A, 4-7 softmax of B (a thread is one query
-// vector), 8 and 9 issue the tcgen05.mma of A and of B, 10 and 11 load.
+// vector), 8 and 9 issue the tcgen05.mma of A and of B, 10 and 11 load (on line 0
+// K and V, on line 1 the tiles of A and of B: a wait costs some 190 cycles even
+// when its phase is long over, and one warp with four of them a tile was what
+// bounded line 0).
 //   TMEM: per stream two S buffers of 64 columns (P overwrites its S as bf16 and
 //   is the A operand of P V from there) and O.  S of tile j + 1 is there before
 //   the softmax of tile j ends, so the softmax never waits for a product chain.
@@ -76,7 +79,7 @@ struct LineBars {
 struct Bars {
     LineBars line[2];
     Seg seg[2][SEGS];  // segments handed from a load warp to the other roles
-    uint32_t rel[16];  // batch that frees a stage (the load warps' own)
+    uint32_t rel[2][16];  // per load warp: the batch that frees a stage
     uint32_t tmem;
     int fail;
     PlanMem<NTHR> plan;
@@ -94,12 +97,6 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map
         "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(
             dst),
         "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2)
-        : "memory");
-}
-__device__ __forceinline__ void tma_load_2d_u(uint32_t dst, const CUtensorMap* map, uint64_t* bar, int c0, int c1) {
-    asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2];" ::"r"(dst),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(c0), "r"(c1)
         : "memory");
 }
 // D (TMEM) (+)= A (TMEM, bf16 pairs) . B (smem)
@@ -224,7 +221,7 @@ __global__ void __launch_bounds__(NTHR, 1)
                 for (int b = 0; b < 2; ++b) mbar_init(&B->p_full[x][b], 4);
                 for (int b = 0; b < DONE; ++b) {
                     mbar_init(&B->done[x][b], 1);
-                    mbar_init(&B->kv_full[x][b], 1);
+                    mbar_init(&B->kv_full[x][b], line == 0 ? 2 : 1);  // load warps that fill the batch
                 }
                 mbar_init(&B->o_empty[x], 4);
                 mbar_init(&B->drain[x], 1);
@@ -284,107 +281,108 @@ __global__ void __launch_bounds__(NTHR, 1)
 
         if (warp >= 10) {
             // ------------------------------------------------------------ loads
-            const int x = warp - 10;
-            if (!pair || x == 0) {
-                Walk walk(P, h, line, worker(x));
-                uint32_t nseg = 0, armed = 0, nb = 0;  // nb: batches before this segment
-                int kvh, row0, seq;
-                Seg s;
+            // line 0: warp 10 (x = 0) hands out the segments and loads Q and K, warp 11 V; line 1: stream x's all
+            const int x = warp - 10, rx = pair ? 0 : x;
+            Walk walk(P, h, line, worker(x));
+            uint32_t nseg = 0, armed = 0, nb = 0;  // nb: batches before this segment
+            uint32_t* rel = bars->rel[x];
+            int kvh, row0, seq;
+            Seg s;
 #pragma unroll 1
-                while (wait.ok) {
-                    if (!walk.next(P, h, base, ibase, s, kvh, row0, seq)) s.n = 0;
-                    if (lane == 0) {
-                        const int slot = nseg % SEGS;
-                        if (wait(&B->seg_empty[x][slot], ((nseg / SEGS) & 1) ^ 1)) {
-                            bars->seg[x][slot] = s;
-                            mbar_arrive(&B->seg_full[x][slot]);
+            while (wait.ok) {
+                if (!walk.next(P, h, base, ibase, s, kvh, row0, seq)) s.n = 0;
+                if (lane == 0 && rx == x) {
+                    const int slot = nseg % SEGS;
+                    if (wait(&B->seg_empty[x][slot], ((nseg / SEGS) & 1) ^ 1)) {
+                        bars->seg[x][slot] = s;
+                        mbar_arrive(&B->seg_full[x][slot]);
+                    }
+                }
+                const int n = s.n;
+                if (n == 0) break;
+                const int* pages = seq < 0 ? P.prefix_pages : P.table + (long long)seq * P.ld_table;
+                const int n_pages = (s.keys + 63) >> 6;  // valid entries of `pages`
+                const int oob = P.n_pages * P.Hkv * 64;  // a row behind the cache: reads as zeros
+                // page numbers 32 at a time, one a lane (K tiles run up to two ahead of V tiles: a window each); past
+                // the list and outside the cache: zeros
+                int bad = 0, w0[2] = {-64, -64}, pg[2] = {0, 0};
+                auto tile = [&](int kv, int j, uint32_t i) {
+                    const int first = s.t0 + j;
+                    if (first >= w0[kv] + 32) {
+                        w0[kv] = first;
+                        pg[kv] = -1;
+                        if (first + lane < n_pages) {
+                            pg[kv] = pages[first + lane];
+                            if (pg[kv] < 0 || pg[kv] >= P.n_pages) {
+                                pg[kv] = -1;
+                                bad |= first + lane < s.t0 + n;
+                            }
                         }
                     }
-                    const int n = s.n;
-                    if (n == 0) break;
-                    const int* pages = seq < 0 ? P.prefix_pages : P.table + (long long)seq * P.ld_table;
-                    const int n_pages = (s.keys + 63) >> 6;  // valid entries of `pages`
-                    const int oob = P.n_pages * P.Hkv * 64;  // a row behind the cache: reads as zeros
-                    // page numbers 32 at a time, one a lane (K tiles run up to two ahead of V tiles: a window
-                    // each); past the list and outside the cache: zeros
-                    int bad = 0, w0[2] = {-64, -64}, pg[2] = {0, 0};
-                    auto tile = [&](int kv, int j) {
-                        const int first = s.t0 + j;
-                        if (first >= w0[kv] + 32) {
-                            w0[kv] = first;
-                            pg[kv] = -1;
-                            if (first + lane < n_pages) {
-                                pg[kv] = pages[first + lane];
-                                if (pg[kv] < 0 || pg[kv] >= P.n_pages) {
-                                    pg[kv] = -1;
-                                    bad |= first + lane < s.t0 + n;
-                                }
-                            }
-                        }
-                        const int p = __shfl_sync(0xffffffffu, pg[kv], first - w0[kv]);
-                        if (lane == 0) {
-                            const int row = p < 0 ? oob : (p * P.Hkv + kvh) * 64;
-                            const uint32_t pos = ring + (kv ? v_seq(j, n) : k_seq(j)), st = first_stage(x) + stage_of(pos);
-                            if (pos < depth || (batch_done(x, bars->rel[st]) && (!pair || batch_done(1, bars->rel[st])))) {
-                                const uint32_t i = nb + j + 2 * kv;
-                                bars->rel[st] = i;
-#pragma unroll
-                                for (int c = 0; c < C::HALVES; ++c)
-                                    tma_load_2d_u(ring_at + st * C::TILE + c * C::KV_REG, kv ? &mv : &mk,
-                                                  &B->kv_full[x][i % DONE], 64 * c, row);
-                            }
-                        }
-                    };
+                    const int p = __shfl_sync(0xffffffffu, pg[kv], first - w0[kv]);
+                    if (lane == 0) {
+                        const uint32_t pos = ring + (kv ? v_seq(j, n) : k_seq(j)), st = first_stage(x) + stage_of(pos);
+                        if (pos < depth || (batch_done(rx, rel[st]) && (!pair || batch_done(1, rel[st]))))
+                            tma_load_3d(ring_at + st * C::TILE, kv ? &mv : &mk, &B->kv_full[rx][i % DONE], 0,
+                                        p < 0 ? oob : (p * P.Hkv + kvh) * 64, 0);
+                    }
+                };
 #pragma unroll 1
-                    for (int j = -2; j < n; ++j) {
-                        // batch: V of tile j, K of tile j + 2
-                        const bool has_v = j >= 0, has_k = j + 2 < n;
-                        if (lane == 0) {
-                            uint64_t* bar = &B->kv_full[x][(nb + j + 2) % DONE];
-                            if (has_v || has_k) mbar_arrive_expect_tx(bar, (has_v + has_k) * C::TILE);
-                            else mbar_arrive(bar);  // (an empty batch has its phase too)
-                        }
-                        if (has_v) tile(1, j);
-                        if (has_k) tile(0, j + 2);
-                        armed = nb + j + 3;
-                        if (j == -2 && lane == 0) {
-                            // the queries: behind the first tile, whose stage waits for the segment before alone
-                            for (int y = x; y < (pair ? 2 : x + 1); ++y) {
-                                if (!wait(&B->q_empty[y], (nseg & 1) ^ 1)) break;
-                                mbar_arrive_expect_tx(&B->q_full[y], C::HALVES * 128 * P.g * P.RH);
-#pragma unroll
-                                for (int c = 0; c < C::HALVES; ++c)
-                                    tma_load_3d(q_at + y * C::Q_TILE + c * C::Q_REG, &mq, &B->q_full[y], 64 * c, kvh * P.g,
-                                                row0 + (pair ? y * P.RH : 0));
-                            }
-                        }
-                        wait.ok = __shfl_sync(0xffffffffu, (int)wait.ok, 0);
-                        if (!wait.ok) break;
-                    }
-                    ++nseg;
-                    bad = __any_sync(0xffffffffu, bad);
+                for (int j = -2; j < n; ++j) {
+                    // batch: V of tile j, K of tile j + 2
+                    const uint32_t i = nb + j + 2;
+                    const bool has_v = j >= 0, has_k = j + 2 < n;
+                    const bool my_v = has_v && (!pair || x == 1), my_k = has_k && (!pair || x == 0);
                     if (lane == 0) {
-                        a.W.block_bad[s.block] = bad;
-                        if (pair) a.W.block_bad[s.block + 1] = bad;
+                        uint64_t* bar = &B->kv_full[rx][i % DONE];
+                        if (my_v || my_k) mbar_arrive_expect_tx(bar, (my_v + my_k) * C::TILE);
+                        else mbar_arrive(bar);  // (a batch without my tiles has its phase too)
                     }
-                    ring += 2 * n;
-                    nb += n + 2;
-                }
-                if (lane == 0 && wait.ok) {
-                    // the last commits have arrived: nothing is under way to this line's barriers any more
-                    for (int y = x; y < (pair ? 2 : x + 1); ++y)
-                        if (nseg) {
-                            for (uint32_t i = nb > DONE ? nb - DONE : 0; i < nb; ++i) batch_done(y, i);
-                            wait(&B->q_empty[y], (nseg - 1) & 1);
+                    if (my_v) tile(1, j, i);
+                    if (my_k) tile(0, j + 2, i);
+                    if (lane == 0) {
+                        if (has_v) rel[first_stage(x) + stage_of(ring + v_seq(j, n))] = i;
+                        if (has_k) rel[first_stage(x) + stage_of(ring + k_seq(j + 2))] = i;
+                    }
+                    armed = i + 1;
+                    if (j == -2 && lane == 0 && rx == x) {
+                        // the queries: behind the first tile, whose stage waits for the segment before alone
+                        for (int y = x; y < (pair ? 2 : x + 1); ++y) {
+                            if (!wait(&B->q_empty[y], (nseg & 1) ^ 1)) break;
+                            mbar_arrive_expect_tx(&B->q_full[y], C::HALVES * 128 * P.g * P.RH);
+#pragma unroll
+                            for (int c = 0; c < C::HALVES; ++c)
+                                tma_load_3d(q_at + y * C::Q_TILE + c * C::Q_REG, &mq, &B->q_full[y], 64 * c, kvh * P.g,
+                                            row0 + (pair ? y * P.RH : 0));
                         }
+                    }
+                    wait.ok = __shfl_sync(0xffffffffu, (int)wait.ok, 0);
+                    if (!wait.ok) break;
                 }
-                // a wait ran out: the copies in flight must land before the CTA leaves its shared memory
-                if (lane == 0 && !wait.ok) {
-                    for (uint32_t i = armed > DONE ? armed - DONE : 0; i < armed; ++i)
-                        Waiter::late(&B->kv_full[x][i % DONE], (i / DONE) & 1, 1u << 16);
-                    for (int y = x; y < (pair ? 2 : x + 1); ++y)
-                        if (nseg) Waiter::late(&B->q_full[y], (nseg - 1) & 1);
+                ++nseg;
+                bad = __any_sync(0xffffffffu, bad);
+                if (lane == 0) {
+                    // (on line 0 warp 10's K tiles speak for the pages)
+                    if (rx == x) a.W.block_bad[s.block] = bad;
+                    if (pair && rx == x) a.W.block_bad[s.block + 1] = bad;
                 }
+                ring += 2 * n;
+                nb += n + 2;
+            }
+            if (lane == 0 && wait.ok && rx == x) {
+                // the last commits have arrived: nothing is under way to this line's barriers any more
+                for (int y = x; y < (pair ? 2 : x + 1); ++y)
+                    if (nseg) {
+                        for (uint32_t i = nb > DONE ? nb - DONE : 0; i < nb; ++i) batch_done(y, i);
+                        wait(&B->q_empty[y], (nseg - 1) & 1);
+                    }
+            }
+            // a wait ran out: the copies in flight must land before the CTA leaves its shared memory
+            if (lane == 0 && !wait.ok) {
+                for (uint32_t i = armed > DONE ? armed - DONE : 0; i < armed; ++i)
+                    Waiter::late(&B->kv_full[rx][i % DONE], (i / DONE) & 1, 1u << 16);
+                for (int y = x; y < (pair ? 2 : x + 1); ++y)
+                    if (nseg) Waiter::late(&B->q_full[y], (nseg - 1) & 1, 1u << 16);
             }
         } else if (warp >= 8) {
             // ------------------------------------------------------------ MMA
@@ -623,10 +621,11 @@ bool run(const Launch& L, const Shape& P, const Work& W, const dflash_shared_pre
         if (!encode(&mq, 3, a.q, dims, strides, box)) return false;
     }
     {
-        const cuuint64_t dims[2] = {(cuuint64_t)HD, (cuuint64_t)P.n_pages * P.Hkv * 64};
-        const cuuint64_t strides[1] = {(cuuint64_t)HD * 2};
-        const cuuint32_t box[2] = {64, 64};
-        if (!encode(&mk, 2, a.k_cache, dims, strides, box) || !encode(&mv, 2, a.v_cache, dims, strides, box)) return false;
+        // the caches as [halves of a row][rows][64]: one copy brings a page's keys of one KV head as 64-dim halves
+        const cuuint64_t dims[3] = {64, (cuuint64_t)P.n_pages * P.Hkv * 64, (cuuint64_t)HD / 64};
+        const cuuint64_t strides[2] = {(cuuint64_t)HD * 2, 128};
+        const cuuint32_t box[3] = {64, 64, (cuuint32_t)HD / 64};
+        if (!encode(&mk, 3, a.k_cache, dims, strides, box) || !encode(&mv, 3, a.v_cache, dims, strides, box)) return false;
     }
     const size_t smem = C::SMEM_TILES + sizeof(Bars) + 3 * MAX_BATCH * 4 + 1024;
     if (cudaFuncSetAttribute(shared_tc_kernel<HD>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
