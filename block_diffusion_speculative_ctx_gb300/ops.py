@@ -63,7 +63,9 @@ class KVTables(NamedTuple):
 # small calls are as long as their host side) and passes the bytes.
 _TABLES, _ATTN, _LOGITS = struct.Struct("6i2q12Q"), struct.Struct("10ifi3q11Q"), struct.Struct("8i4q13Q")
 _I32T, _I64T, _F32T = torch.int32, torch.int64, torch.float32
-_raw_stream = torch._C._cuda_getCurrentRawStream
+_U8T = torch.uint8
+_WORKSPACE = {}  # bytes by (dtype, H, H_kv, hd, batch, rows)
+_raw_stream, _current_device = torch._C._cuda_getCurrentRawStream, torch.cuda.current_device
 
 
 def _bad(msg):
@@ -97,6 +99,8 @@ def _mat(name, t, dtype, rows, cols, dev):
     n, m = t.shape
     if n != rows or (cols is not None and m != cols):
         _bad(f"{name} must be [{rows}, {'any' if cols is None else cols}], not [{n}, {m}]")
+    if t.is_contiguous():
+        return m
     ld, inner = t.stride()
     if n <= 1 or m == 0:
         ld = m
@@ -107,10 +111,10 @@ def _mat(name, t, dtype, rows, cols, dev):
 
 def _rows3(name, t, dtype, rows, heads, hd, dev):
     """Row stride of a [rows, heads, hd] tensor whose rows are contiguous."""
-    if t.dtype is not dtype or tuple(t.shape) != (rows, heads, hd) or t.get_device() != dev:
+    if t.dtype is not dtype or t.shape != (rows, heads, hd) or t.get_device() != dev:
         _bad(f"{name} must be a {dtype} [{rows}, {heads}, {hd}] on cuda:{dev}, "
              f"not {t.dtype} {tuple(t.shape)} on {t.device}")
-    if rows == 0:
+    if t.is_contiguous():
         return heads * hd
     ld, between, inner = t.stride()
     if inner != 1 or (heads > 1 and between != hd):
@@ -119,7 +123,7 @@ def _rows3(name, t, dtype, rows, heads, hd, dev):
 
 
 def _call(fn, args, dev):
-    if torch.cuda.current_device() == dev:
+    if _current_device() == dev:
         st = fn(args, _raw_stream(dev))
     else:
         with torch.cuda.device(dev):
@@ -206,13 +210,14 @@ def shared_prefix_attention(q, k_cache, v_cache, prefix_pages, prefix_len: int, 
         _bad("q must be [rows, H, hd] and the caches [pages, H_kv, 64, hd]")
     dev = _device(q, q, k_cache, v_cache)
     rows, h, hd = q.shape
-    pages, hkv = k_cache.shape[:2]
+    kv_shape = k_cache.shape
+    pages, hkv, page_tokens, kv_hd = kv_shape
     dtype = q.dtype
     dt = _DTYPES.get(dtype)
     if dt is None:
         _bad(f"q must be float32 or bfloat16, not {dtype}")
     n_kv = pages * hkv * PAGE_TOKENS * hd
-    if k_cache.shape[2] != PAGE_TOKENS or k_cache.shape[3] != hd or v_cache.shape != k_cache.shape:
+    if page_tokens != PAGE_TOKENS or kv_hd != hd or v_cache.shape != kv_shape:
         _bad(f"k_cache and v_cache must be [pages, H_kv, {PAGE_TOKENS}, {hd}]")
     p_k, p_v = _flat("k_cache", k_cache, dtype, n_kv, dev), _flat("v_cache", v_cache, dtype, n_kv, dev)
     batch = kv_lens.numel()
@@ -234,16 +239,23 @@ def shared_prefix_attention(q, k_cache, v_cache, prefix_pages, prefix_len: int, 
     ld_out = _rows3("out", out, dtype, rows, h, hd, dev)
     if lse is None:
         lse = torch.zeros((rows, h), dtype=_F32T, device=q.device)
-    lib = load()
     if workspace is None:
-        workspace = torch.empty(lib.dflash_shared_prefix_workspace(dt, h, hkv, hd, batch, rows), dtype=torch.uint8,
-                                device=q.device)
-    n_ws = workspace.numel() * workspace.element_size()
-    _call(lib.dflash_shared_prefix_attention,
+        sizes = (dt, h, hkv, hd, batch, rows)
+        n_ws = _WORKSPACE.get(sizes)
+        if n_ws is None:
+            if len(_WORKSPACE) > 4096:
+                _WORKSPACE.clear()
+            n_ws = _WORKSPACE[sizes] = load().dflash_shared_prefix_workspace(*sizes)
+        workspace = torch.empty(n_ws, dtype=_U8T, device=q.device)
+        p_ws = workspace.data_ptr()
+    else:
+        n_ws = workspace.numel() * workspace.element_size()
+        p_ws = _flat("workspace", workspace, workspace.dtype, workspace.numel(), dev)
+    _call(load().dflash_shared_prefix_attention,
           _ATTN.pack(dt, h, hkv, hd, batch, rows, pages, prefix_len, table.shape[1], bool(causal),
                      hd ** -0.5 if scale is None else scale, 0, ld_q, ld_out, ld_table, q.data_ptr(), p_k, p_v, p_pre,
-                     table.data_ptr(), p_kv, p_start, out.data_ptr(), _flat("lse", lse, _F32T, rows * h, dev),
-                     _flat("workspace", workspace, workspace.dtype, workspace.numel(), dev), n_ws), dev)
+                     table.data_ptr(), p_kv, p_start, out.data_ptr(), _flat("lse", lse, _F32T, rows * h, dev), p_ws, n_ws),
+          dev)
     return out, lse
 
 
