@@ -18,9 +18,8 @@
 // other line's products run on the neighbours.
 // Roles (warps): 0-3 softmax of A, 4-7 softmax of B (a thread is one query
 // vector), 8 and 9 issue the tcgen05.mma of A and of B, 10 and 11 load (on line 0
-// K and V, on line 1 the tiles of A and of B: a wait costs some 190 cycles even
-// when its phase is long over, and one warp with four of them a tile was what
-// bounded line 0).
+// K and V, on line 1 the tiles of A and of B; a wait costs some 190 cycles even
+// when its phase is long over, so two warps share them).
 //   TMEM: per stream two S buffers of 64 columns (P overwrites its S as bf16 and
 //   is the A operand of P V from there) and O.  S of tile j + 1 is there before
 //   the softmax of tile j ends, so the softmax never waits for a product chain.
@@ -36,7 +35,6 @@
 // Every wait is bounded; one that runs out sets the CTA's error word (the merge
 // writes NaN), every role leaves, copies in flight are awaited (bounded).
 #include <math.h>
-#include <stdio.h>
 
 #include "shared_plan.cuh"
 #include "tcgen05.cuh"
@@ -62,7 +60,6 @@ struct Cfg {
 };
 
 constexpr int SEGS = 4;
-constexpr int STAGGER = 700;  // cycles
 // A wait for batch i must not begin once batch i + DONE can have completed (the barrier's parity would be
 // that of before i).  The load warps wait the latest: a stage comes round after at most 16 ring positions, and
 // the shortest segments (one tile: two positions, three batches) put 24 batches on those.
@@ -408,11 +405,6 @@ __global__ void __launch_bounds__(NTHR, 1)
                         if (j >= 0) {
                             if (j == 0) wait(&B->o_empty[x], (nseg & 1) ^ 1);  // the segment before has been read out
                             wait(&B->p_full[x][(nt + j) & 1], ((nt + j) >> 1) & 1);
-                        } else if (pair && x == 1 && nb + j == (uint32_t)-2) {
-                            // the streams half a tile apart: in step, both would wait for their softmax while the
-                            // tensor cores idle
-                            for (const long long t = clock64(); clock64() - t < STAGGER;) {
-                            }
                         }
                         if (!wait.ok) break;
                         fence_after();
