@@ -44,6 +44,8 @@ def _rel(a, b):
     ("small_bf16", 130, (37, 100), None),
     ("small_bf16", 1000, (3, 400), (16, 8)),
     ("small_bf16_llama", 200, (64, 5, 130, 33), None),
+    ("tiny_f32_b3", 4130, (5, 60, 12), (4, 2, 1, 3)),  # 64 shared pages: the rounds attend to them once
+    ("small_bf16_long8k", 4130, (3, 40), None),
 ])
 def test_prefill_shared_and_rounds(name, prefix_len, lens, schedule):
     w = configs.get(name)
@@ -103,13 +105,14 @@ def test_prefill_shared_and_rounds(name, prefix_len, lens, schedule):
         sess.close()
 
 
-def test_prefill_shared_runs_in_several_chunks():
+@pytest.mark.parametrize("prefix_len", [2200, 4200])  # rounds sequence by sequence; rounds on the shared keys
+def test_prefill_shared_runs_in_several_chunks(prefix_len):
     """A prefix longer than one prefill chunk and more suffix rows than one (a sequence split over two), against a
     plain prefill of the whole prompts by the same library; then graph replays equal eager rounds bit for bit."""
     w = configs.get("small_bf16")
     lens = (700, 3, 900, 1200, 64)
-    w = w.with_(batch=len(lens), prompt_lens=tuple(2200 + n for n in lens), target_layers=2, ctx_layer_ids=(0, 1), draft_layers=1)
-    prefix, own = _prompts(w, 2200, lens, 5)
+    w = w.with_(batch=len(lens), prompt_lens=tuple(prefix_len + n for n in lens), target_layers=2, ctx_layer_ids=(0, 1), draft_layers=1)
+    prefix, own = _prompts(w, prefix_len, lens, 5)
     out = {}
     for mode in ("plain", "shared", "eager"):
         sess = _session(w, keep_logits=True, max_seq_len=max(w.prompt_lens) + 200, graphs=mode != "eager")
