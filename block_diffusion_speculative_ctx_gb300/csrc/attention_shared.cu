@@ -31,6 +31,7 @@ struct MergeArgs {
     void* out;
     float* lse;
     long long ld_out;
+    uint32_t* report;  // the session's error word, or null
 };
 
 constexpr int MWARPS = 8;
@@ -78,7 +79,8 @@ __global__ void __launch_bounds__(32 * MWARPS, 3) merge_kernel(MergeArgs a) {
     for (int i = 0; i < 5; ++i)
         if (lane + 32 * i < P.n_cta) err |= a.W.err[lane + 32 * i];
     if (d.pre_count == -1) return;  // a row of no sequence
-    const bool bad = __any_sync(0xffffffffu, err != 0) || d.pre_count == -2;
+    const bool late = __any_sync(0xffffffffu, err != 0), bad = late || d.pre_count == -2;
+    if (late && a.report && lane == 0) atomicOr(a.report, ERR_TIMEOUT);
     const int count = bad ? 0 : d.pre_count + d.own_count;
     const int w0 = NW > 1 ? warp : 0;
     const int chunks = P.hd / 8, elems = P.g * chunks;
@@ -202,6 +204,7 @@ bool shared_prefix_attention(const Launch& L, const dflash_shared_prefix_args& a
     m.out = a.out;
     m.lse = a.lse;
     m.ld_out = a.ld_out;
+    m.report = L.err;
     if (!(f32 ? shared_attention_f32(L, P, m.W, a) : shared_attention_tc(L, P, m.W, a))) return false;
     if (f32) merge<float>(L, m);
     else merge<bf16>(L, m);

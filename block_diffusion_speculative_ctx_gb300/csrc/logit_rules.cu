@@ -310,6 +310,8 @@ dflash_status check_logits(const dflash_logits_args& a, const char** why) {
     if (a.out == a.logits && a.ld_out != a.ld_logits) return bad("process_logits: in place needs one row stride");
     if (a.history && (!a.hist_lens || !a.prompt_lens || a.hist_width < 0 || a.ld_hist < a.hist_width))
         return bad("process_logits: history needs hist_lens, prompt_lens and a row stride of at least hist_width");
+    if (a.hist_width > (1 << 29) || a.bias_width > (1 << 29))
+        return bad("process_logits: hist_width or bias_width above 2^29");
     if (!a.history && (a.drafts || a.repetition || a.presence || a.frequency))
         return bad("process_logits: penalties and drafts need a history");
     if (a.bias_ids && (!a.bias_values || a.bias_width < 0)) return bad("process_logits: bias_ids needs bias_values");

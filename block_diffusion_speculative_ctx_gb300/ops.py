@@ -122,7 +122,11 @@ def _rows3(name, t, dtype, rows, heads, hd, dev):
     return ld if rows > 1 else heads * hd
 
 
-def _call(fn, args, dev):
+def _call(fn, pack, values, dev):
+    try:
+        args = pack(*values)
+    except struct.error as e:
+        raise ValueError(f"an integer argument is out of its range or no integer: {e}") from None
     if _current_device() == dev:
         st = fn(args, _raw_stream(dev))
     else:
@@ -188,7 +192,7 @@ def kv_tables(kv_lens, new_lens, table, free_pages=None, used=None, *, rows: Opt
         ld_out = _mat("table_out", table_out, _I32T, batch, width, dev)
         p_out = table_out.data_ptr()
     _call(load().dflash_kv_tables,
-          _TABLES.pack(batch, width, rows, n_free, base_pos, scratch_page, ld, ld_out, p_kv, p_new, table.data_ptr(), p_free,
+          _TABLES.pack, (batch, width, rows, n_free, base_pos, scratch_page, ld, ld_out, p_kv, p_new, table.data_ptr(), p_free,
                        p_used, p_out, p_uo, _flat("q_start", q_start, _I32T, batch + 1, dev),
                        _flat("row_seq", row_seq, _I32T, rows, dev), _flat("row_pos", row_pos, _I32T, rows, dev),
                        _flat("slots", slots, _I64T, rows, dev), p_status), dev)
@@ -252,7 +256,7 @@ def shared_prefix_attention(q, k_cache, v_cache, prefix_pages, prefix_len: int, 
         n_ws = workspace.numel() * workspace.element_size()
         p_ws = _flat("workspace", workspace, workspace.dtype, workspace.numel(), dev)
     _call(load().dflash_shared_prefix_attention,
-          _ATTN.pack(dt, h, hkv, hd, batch, rows, pages, prefix_len, table.shape[1], bool(causal),
+          _ATTN.pack, (dt, h, hkv, hd, batch, rows, pages, prefix_len, table.shape[1], bool(causal),
                      hd ** -0.5 if scale is None else scale, 0, ld_q, ld_out, ld_table, q.data_ptr(), p_k, p_v, p_pre,
                      table.data_ptr(), p_kv, p_start, out.data_ptr(), _flat("lse", lse, _F32T, rows * h, dev), p_ws, n_ws),
           dev)
@@ -333,7 +337,7 @@ def process_logits(logits, *, rows_per_seq: int = 1, history=None, hist_lens=Non
     elif mask_index is not None:
         _bad("mask_index needs masks")
     _call(load().dflash_process_logits,
-          _LOGITS.pack(dt, batch, rows_per_seq, vocab, hist_width, bias_width, n_masks, 0, ld, ld_out, ld_hist, ld_mask,
+          _LOGITS.pack, (dt, batch, rows_per_seq, vocab, hist_width, bias_width, n_masks, 0, ld, ld_out, ld_hist, ld_mask,
                        logits.data_ptr(), out.data_ptr(), p_hist, p_len, p_prompt, p_draft, p_rep, p_pres, p_freq,
                        p_ids if bias_width else 0, p_val, p_mask if n_masks else 0, p_idx), dev)
     return out

@@ -492,9 +492,9 @@ enum { DFLASH_OPS_MAX_BATCH = 2048 };
  * free_pages NULL: the caller's table already holds every page; nothing is
  * taken and table_out may be NULL.
  * status (device): 0, or a sum of 1 (the pool has too few pages), 2 (a request
- * needs more than width pages), 4 (T > rows), 8 (a negative length or *used).  When it is
- * not 0 nothing is taken: table_out is not written, used_out = *used, q_start
- * is all 0 and every row is -1.
+ * needs more than width pages), 4 (T > rows), 8 (a negative length or *used).
+ * When it is not 0 nothing is taken: table_out is not written, used_out =
+ * *used, q_start is all 0 and every row is -1.
  * table_out may be table and used_out may be used (in place); no other overlap.
  * Rows of table and table_out are ld_table / ld_out entries apart.
  * Errors: E_INVAL (sizes, NULL), E_CUDA. */
@@ -535,12 +535,13 @@ dflash_status dflash_kv_tables(const dflash_kv_tables_args* args, void* cuda_str
  * past the last valid token may hold anything; keys and values of valid
  * tokens must be finite.
  * Device-side checks: a sequence with a page outside [0, n_pages) among its
- * keys, kv_lens[s] outside [0, 64 * width], or q_start decreasing or leaving
- * [0, rows] gets NaN in its rows' out and lse (every row, for a bad prefix
- * page or a bounded device wait that ran out); nothing is read or written out
- * of range.
- * dtype F32 or BF16 (q, caches and out); head_dim 64 or 128; H / H_kv at most
- * 64; q, k_cache and v_cache 16-byte aligned, ld_q a multiple of 16 bytes.
+ * keys or with kv_lens[s] outside [0, 64 * width] gets NaN in its rows' out and
+ * lse; every row of q does behind a bad prefix page, a q_start that decreases
+ * or leaves [0, rows], work beyond 2^31 tiles of 64 keys, or a bounded device
+ * wait that ran out.  Nothing is read or written out of range.
+ * dtype F32 or BF16 (q, caches and out); head_dim 64 or 128; H at most 1024 and
+ * at most 64 times H_kv; q, the caches and out 16-byte aligned, ld_q and ld_out
+ * multiples of 16 bytes.  out may be q (in place, with one row stride).
  * The scores, the softmax and the accumulation are fp32; in BF16 each softmax
  * weight is rounded to bf16 for the product with v.
  * workspace: 16-byte aligned device memory of at least
@@ -606,8 +607,8 @@ typedef struct {
     int32_t batch;
     int32_t rows_per_seq;      /* 1 .. 32 */
     int32_t vocab;
-    int32_t hist_width;        /* columns of history */
-    int32_t bias_width;        /* columns of bias_ids and bias_values */
+    int32_t hist_width;        /* columns of history, at most 2^29 */
+    int32_t bias_width;        /* columns of bias_ids and bias_values, at most 2^29 */
     int32_t n_masks;
     int32_t reserved;          /* 0 */
     int64_t ld_logits;

@@ -94,7 +94,7 @@ def test_shared_prefix_workspace_sizes(lib):
     dict(dtype=2), dict(batch=0), dict(batch=2049), dict(rows_per_seq=0), dict(rows_per_seq=33), dict(vocab=0),
     dict(logits=None), dict(out=None), dict(logits=P + 2), dict(ld_logits=999), dict(ld_out=999), dict(ld_out=1004),
     dict(hist_lens=None), dict(prompt_lens=None), dict(ld_hist=7), dict(history=None), dict(bias_values=None),
-    dict(mask_index=None), dict(ld_mask=31)])
+    dict(mask_index=None), dict(ld_mask=31), dict(hist_width=(1 << 29) + 1, ld_hist=1 << 30), dict(bias_width=(1 << 29) + 1)])
 def test_process_logits_refuses(lib, kw):
     assert lib.dflash_process_logits(ctypes.byref(rules(**kw)), None) == dfl.DFLASH_E_INVAL
     assert "process_logits" in dfl.dflash_last_error(None)

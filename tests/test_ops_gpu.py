@@ -289,6 +289,16 @@ def test_shared_prefix_attention_equals_itself(dtype):
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_shared_prefix_attention_in_place(dtype):
+    """out is q: the queries have all been read before the first result is written."""
+    c = attn_case(dtype, (32, 8, 128), 700, [400, 33, 90], [16, 1, 50], seed=33)
+    x = attn_inputs(c)
+    want = dfl().shared_prefix_attention(*x)
+    got = dfl().shared_prefix_attention(*x, out=x[0])
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("fault", ["table", "table_negative", "prefix", "kv_len", "kv_negative", "q_start"])
 def test_shared_prefix_attention_reports_bad_metadata(dtype, fault):
     """A page, length or row start out of range: NaN in the rows it concerns, the others as they should be."""
@@ -307,11 +317,9 @@ def test_shared_prefix_attention_reports_bad_metadata(dtype, fault):
     out = torch.zeros_like(x[0])
     lse = torch.zeros(x[0].shape[:2], device="cuda")
     dfl().shared_prefix_attention(*x, out=out, lse=lse)
-    if fault == "prefix":
+    if fault in ("prefix", "q_start"):  # every row's keys, or whose rows they are, cannot be told
         assert out.isnan().all() and lse.isnan().all()
         return
-    if fault == "q_start":
-        return  # only that nothing faults: which rows are whose is not defined any more
     assert out[2:4].isnan().all() and lse[2:4].isnan().all()
     # the other rows as without the fault, within the bounds (not bit for bit: how the keys are split
     # depends on every sequence's length, and each split adds its partial sums in another order)
@@ -524,6 +532,11 @@ def test_the_bindings_refuse():
         m.kv_tables(i32([1]), i32([1]), i32([[0]]))
     with pytest.raises(ValueError):
         m.kv_tables(i32([1]), i32([1]), i32([[0]]), i32([1]), rows=1)
+    for bad in (dict(base_pos=1 << 40), dict(scratch_page=0.5)):
+        with pytest.raises(ValueError, match="integer"):
+            m.kv_tables(i32([1]), i32([1]), i32([[0]]), rows=1, **bad)
+    with pytest.raises(ValueError, match="integer"):
+        m.shared_prefix_attention(*x[:4], 5.0, *x[5:])
 
 
 def test_an_empty_batch_of_rows():
