@@ -197,7 +197,7 @@ bool run(const Launch& L, const F32Args& f) {
     const size_t smem = sizeof(Smem<HD>);
     if (cudaFuncSetAttribute(shared_f32_kernel<HD>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
         return false;
-    launch_k(L, shared_f32_kernel<HD>, dim3(f.P.workers(1)), dim3(NT), smem, 1, f);
+    launch_k(L, shared_f32_kernel<HD>, dim3(2 * f.P.n_cta), dim3(NT), smem, 1, f);
     return true;
 }
 

@@ -9,13 +9,14 @@
 // takes the unrounded ones).
 //
 // One CTA per SM holds two streams A, B of 128 query vectors each (TMEM lanes)
-// and walks its part of both lines of the plan (shared_plan.cuh):
+// and walks its part of one of the two lines of the plan (shared_plan.cuh):
 //   line 0: A and B hold different rows of one item and share every K/V tile,
 //           which halves the shared-memory fill per product (tensor-bound);
 //   line 1: A and B walk segments of their own with half of the ring each
 //           (few query vectors, so bound by the K/V bytes).
-// Odd CTAs walk line 1 first, so that the bytes of one line stream while the
-// other line's products run on the neighbours.
+// The CTAs of the two lines run side by side, so the bytes of one line stream
+// while the other line's products run on the neighbours, and each CTA has one
+// start-up.
 // Roles (warps): 0-3 softmax of A, 4-7 softmax of B (a thread is one query
 // vector), 8 and 9 issue the tcgen05.mma of A and of B, 10 and 11 load (on line 0
 // K and V, on line 1 the tiles of A and of B; a wait costs some 190 cycles even
@@ -78,7 +79,6 @@ struct Bars {
     Seg seg[2][SEGS];  // segments handed from a load warp to the other roles
     uint32_t rel[2][16];  // per load warp: the batch that frees a stage
     uint32_t tmem;
-    int fail;
     PlanMem<NTHR> plan;
 };
 
@@ -167,13 +167,11 @@ __device__ __forceinline__ uint32_t v_seq(int j, int n) { return (uint32_t)(j + 
 // The bounded waits of one thread: after one has run out, the later ones return at once.
 struct Waiter {
     uint32_t* err;
-    int* fail;
     bool ok = true;
     __device__ __forceinline__ bool operator()(uint64_t* bar, uint32_t parity) {
         if (!mbar_try_wait(bar, parity) && ok && !late(bar, parity)) {
             ok = false;
             atomicOr(err, ERR_TIMEOUT);
-            *(volatile int*)fail = 1;
         }
         return ok;
     }
@@ -229,7 +227,6 @@ __global__ void __launch_bounds__(NTHR, 1)
             }
         }
         mbar_fence_init();
-        bars->fail = 0;
     }
     if (tid == 32 * 10) {
         prefetch_tmap(&mq);
@@ -246,323 +243,319 @@ __global__ void __launch_bounds__(NTHR, 1)
     // for the merge kernel, by the warps that have nothing to do until the first scores
     if (warp < 8) write_dir(P, h, a.W, base, ibase, warp * P.n_cta + cta, 8 * P.n_cta, lane);
     uint32_t* err = &a.W.err[cta];
-    Waiter wait{err, &bars->fail};
+    Waiter wait{err};
 
-#pragma unroll 1
-    for (int turn = 0; turn < 2; ++turn) {
-        const int line = (cta + turn) & 1;
-        const bool pair = line == 0;
-        LineBars* B = &bars->line[line];
-        if (turn == 1) __syncthreads();  // every role of the first line has ended: the ring and TMEM are free
-        if (h.W[line] == 0 || bars->fail) continue;
-        // ring of a stream: all stages, in step with the other stream (line 0), or half of them (line 1)
-        const uint32_t depth = pair ? C::STAGES : C::STAGES / 2;
-        auto stage_of = [&](uint32_t pos) { return pos & (depth - 1); };
-        // the tiles of the i-th batch of stream x have landed
-        auto landed = [&](int x, uint32_t i) { return wait(&B->kv_full[pair ? 0 : x][i % DONE], (i / DONE) & 1); };
-        // the i-th batch of stream x has completed (i counts through the line)
-        auto batch_done = [&](int x, uint32_t i) { return wait(&B->done[x][i % DONE], (i / DONE) & 1); };
-        auto worker = [&](int x) { return pair ? cta : 2 * cta + x; };
-        auto first_stage = [&](int x) { return pair ? 0u : (uint32_t)x * (C::STAGES / 2); };
-        uint32_t ring = 0;  // ring position of the segment's first tile
-        // the i-th segment, read by a whole warp (or its one issuing lane)
-        auto take = [&](int x, uint32_t i, bool all, Seg& s) {
-            const int rx = pair ? 0 : x, slot = i % SEGS;
-            s.n = 0;
-            if (!wait(&B->seg_full[rx][slot], (i / SEGS) & 1)) return false;
-            s = bars->seg[rx][slot];
-            if (all) __syncwarp();
-            if (!all || lane == 0) mbar_arrive(&B->seg_empty[rx][slot]);
-            return s.n > 0;
-        };
+    // line 1's CTAs are spread evenly between line 0's
+    const int before = cta * h.n1 / P.n_cta, line = (cta + 1) * h.n1 / P.n_cta - before;
+    const bool pair = line == 0;
+    LineBars* B = &bars->line[line];
+    // ring of a stream: all stages, in step with the other stream (line 0), or half of them (line 1)
+    const uint32_t depth = pair ? C::STAGES : C::STAGES / 2;
+    auto stage_of = [&](uint32_t pos) { return pos & (depth - 1); };
+    // the tiles of the i-th batch of stream x have landed
+    auto landed = [&](int x, uint32_t i) { return wait(&B->kv_full[pair ? 0 : x][i % DONE], (i / DONE) & 1); };
+    // the i-th batch of stream x has completed (i counts through the line)
+    auto batch_done = [&](int x, uint32_t i) { return wait(&B->done[x][i % DONE], (i / DONE) & 1); };
+    auto worker = [&](int x) { return pair ? cta - before : 2 * before + x; };
+    auto first_stage = [&](int x) { return pair ? 0u : (uint32_t)x * (C::STAGES / 2); };
+    uint32_t ring = 0;  // ring position of the segment's first tile
+    // the i-th segment, read by a whole warp (or its one issuing lane)
+    auto take = [&](int x, uint32_t i, bool all, Seg& s) {
+        const int rx = pair ? 0 : x, slot = i % SEGS;
+        s.n = 0;
+        if (!wait(&B->seg_full[rx][slot], (i / SEGS) & 1)) return false;
+        s = bars->seg[rx][slot];
+        if (all) __syncwarp();
+        if (!all || lane == 0) mbar_arrive(&B->seg_empty[rx][slot]);
+        return s.n > 0;
+    };
 
-        if (warp >= 10) {
-            // ------------------------------------------------------------ loads
-            // line 0: warp 10 (x = 0) hands out the segments and loads Q and K, warp 11 V; line 1: stream x's all
-            const int x = warp - 10, rx = pair ? 0 : x;
-            Walk walk(P, h, line, worker(x));
-            uint32_t nseg = 0, armed = 0, nb = 0;  // nb: batches before this segment
-            uint32_t* rel = bars->rel[x];
-            int kvh, row0, seq;
-            Seg s;
+    if (warp >= 10) {
+        // ------------------------------------------------------------ loads
+        // line 0: warp 10 (x = 0) hands out the segments and loads Q and K, warp 11 V; line 1: stream x's all
+        const int x = warp - 10, rx = pair ? 0 : x;
+        Walk walk(P, h, line, worker(x));
+        uint32_t nseg = 0, armed = 0, nb = 0;  // nb: batches before this segment
+        uint32_t* rel = bars->rel[x];
+        int kvh, row0, seq;
+        Seg s;
 #pragma unroll 1
-            while (wait.ok) {
-                if (!walk.next(P, h, base, ibase, s, kvh, row0, seq)) s.n = 0;
-                if (lane == 0 && rx == x) {
-                    const int slot = nseg % SEGS;
-                    if (wait(&B->seg_empty[x][slot], ((nseg / SEGS) & 1) ^ 1)) {
-                        bars->seg[x][slot] = s;
-                        mbar_arrive(&B->seg_full[x][slot]);
-                    }
+        while (wait.ok) {
+            if (!walk.next(P, h, base, ibase, s, kvh, row0, seq)) s.n = 0;
+            if (lane == 0 && rx == x) {
+                const int slot = nseg % SEGS;
+                if (wait(&B->seg_empty[x][slot], ((nseg / SEGS) & 1) ^ 1)) {
+                    bars->seg[x][slot] = s;
+                    mbar_arrive(&B->seg_full[x][slot]);
                 }
-                const int n = s.n;
-                if (n == 0) break;
-                const int* pages = seq < 0 ? P.prefix_pages : P.table + (long long)seq * P.ld_table;
-                const int n_pages = (s.keys + 63) >> 6;  // valid entries of `pages`
-                const int oob = P.n_pages * P.Hkv * 64;  // a row behind the cache: reads as zeros
-                // page numbers 32 at a time, one a lane (K tiles run up to two ahead of V tiles: a window each); past
-                // the list and outside the cache: zeros
-                int bad = 0, w0[2] = {-64, -64}, pg[2] = {0, 0};
-                auto tile = [&](int kv, int j, uint32_t i) {
-                    const int first = s.t0 + j;
-                    if (first >= w0[kv] + 32) {
-                        w0[kv] = first;
-                        pg[kv] = -1;
-                        if (first + lane < n_pages) {
-                            pg[kv] = pages[first + lane];
-                            if (pg[kv] < 0 || pg[kv] >= P.n_pages) {
-                                pg[kv] = -1;
-                                bad |= first + lane < s.t0 + n;
-                            }
+            }
+            const int n = s.n;
+            if (n == 0) break;
+            const int* pages = seq < 0 ? P.prefix_pages : P.table + (long long)seq * P.ld_table;
+            const int n_pages = (s.keys + 63) >> 6;  // valid entries of `pages`
+            const int oob = P.n_pages * P.Hkv * 64;  // a row behind the cache: reads as zeros
+            // page numbers 32 at a time, one a lane (K tiles run up to two ahead of V tiles: a window each); past
+            // the list and outside the cache: zeros
+            int bad = 0, w0[2] = {-64, -64}, pg[2] = {0, 0};
+            auto tile = [&](int kv, int j, uint32_t i) {
+                const int first = s.t0 + j;
+                if (first >= w0[kv] + 32) {
+                    w0[kv] = first;
+                    pg[kv] = -1;
+                    if (first + lane < n_pages) {
+                        pg[kv] = pages[first + lane];
+                        if (pg[kv] < 0 || pg[kv] >= P.n_pages) {
+                            pg[kv] = -1;
+                            bad |= first + lane < s.t0 + n;
                         }
                     }
-                    const int p = __shfl_sync(0xffffffffu, pg[kv], first - w0[kv]);
-                    if (lane == 0) {
-                        const uint32_t pos = ring + (kv ? v_seq(j, n) : k_seq(j)), st = first_stage(x) + stage_of(pos);
-                        if (pos < depth || (batch_done(rx, rel[st]) && (!pair || batch_done(1, rel[st]))))
-                            tma_load_3d(ring_at + st * C::TILE, kv ? &mv : &mk, &B->kv_full[rx][i % DONE], 0,
-                                        p < 0 ? oob : (p * P.Hkv + kvh) * 64, 0);
+                }
+                const int p = __shfl_sync(0xffffffffu, pg[kv], first - w0[kv]);
+                if (lane == 0) {
+                    const uint32_t pos = ring + (kv ? v_seq(j, n) : k_seq(j)), st = first_stage(x) + stage_of(pos);
+                    if (pos < depth || (batch_done(rx, rel[st]) && (!pair || batch_done(1, rel[st]))))
+                        tma_load_3d(ring_at + st * C::TILE, kv ? &mv : &mk, &B->kv_full[rx][i % DONE], 0,
+                                    p < 0 ? oob : (p * P.Hkv + kvh) * 64, 0);
+                }
+            };
+#pragma unroll 1
+            for (int j = -2; j < n; ++j) {
+                // batch: V of tile j, K of tile j + 2
+                const uint32_t i = nb + j + 2;
+                const bool has_v = j >= 0, has_k = j + 2 < n;
+                const bool my_v = has_v && (!pair || x == 1), my_k = has_k && (!pair || x == 0);
+                if (lane == 0) {
+                    uint64_t* bar = &B->kv_full[rx][i % DONE];
+                    if (my_v || my_k) mbar_arrive_expect_tx(bar, (my_v + my_k) * C::TILE);
+                    else mbar_arrive(bar);  // (a batch without my tiles has its phase too)
+                }
+                if (my_v) tile(1, j, i);
+                if (my_k) tile(0, j + 2, i);
+                if (lane == 0) {
+                    if (has_v) rel[first_stage(x) + stage_of(ring + v_seq(j, n))] = i;
+                    if (has_k) rel[first_stage(x) + stage_of(ring + k_seq(j + 2))] = i;
+                }
+                armed = i + 1;
+                if (j == -2 && lane == 0 && rx == x) {
+                    // the queries: behind the first tile, whose stage waits for the segment before alone
+                    for (int y = x; y < (pair ? 2 : x + 1); ++y) {
+                        if (!wait(&B->q_empty[y], (nseg & 1) ^ 1)) break;
+                        mbar_arrive_expect_tx(&B->q_full[y], C::HALVES * 128 * P.g * P.RH);
+#pragma unroll
+                        for (int c = 0; c < C::HALVES; ++c)
+                            tma_load_3d(q_at + y * C::Q_TILE + c * C::Q_REG, &mq, &B->q_full[y], 64 * c, kvh * P.g,
+                                        row0 + (pair ? y * P.RH : 0));
                     }
-                };
+                }
+                wait.ok = __shfl_sync(0xffffffffu, (int)wait.ok, 0);
+                if (!wait.ok) break;
+            }
+            ++nseg;
+            bad = __any_sync(0xffffffffu, bad);
+            if (lane == 0) {
+                // (on line 0 warp 10's K tiles speak for the pages)
+                if (rx == x) a.W.block_bad[s.block] = bad;
+                if (pair && rx == x) a.W.block_bad[s.block + 1] = bad;
+            }
+            ring += 2 * n;
+            nb += n + 2;
+        }
+        if (lane == 0 && wait.ok && rx == x) {
+            // the last commits have arrived: nothing is under way to this line's barriers any more
+            for (int y = x; y < (pair ? 2 : x + 1); ++y)
+                if (nseg) {
+                    for (uint32_t i = nb > DONE ? nb - DONE : 0; i < nb; ++i) batch_done(y, i);
+                    wait(&B->q_empty[y], (nseg - 1) & 1);
+                }
+        }
+        // a wait ran out: the copies in flight must land before the CTA leaves its shared memory
+        if (lane == 0 && !wait.ok) {
+            for (uint32_t i = armed > DONE ? armed - DONE : 0; i < armed; ++i)
+                Waiter::late(&B->kv_full[rx][i % DONE], (i / DONE) & 1, 1u << 16);
+            for (int y = x; y < (pair ? 2 : x + 1); ++y)
+                if (nseg) Waiter::late(&B->q_full[y], (nseg - 1) & 1, 1u << 16);
+        }
+    } else if (warp >= 8) {
+        // ------------------------------------------------------------ MMA
+        const int x = warp - 8;
+        if (lane == 0) {
+            constexpr uint32_t ID_S = idesc_bf16(VT, KT), ID_O = idesc_bf16(VT, HD, true);
+            const uint32_t tS = tmem + 128 * x, tO = tmem + 256 + HD * x;
+            const uint64_t q_desc = sw128_desc(q_at + x * C::Q_TILE);
+            const uint64_t k_desc = sw128_desc(ring_at), v_desc = sw128_desc(ring_at, C::KV_REG, 1024);
+            uint32_t nseg = 0, nt = 0, nb = 0;  // segments, tiles and batches before this one
+            Seg s;
+#pragma unroll 1
+            while (take(x, nseg, false, s)) {
+                const int n = s.n;
+                if (!wait(&B->q_full[x], nseg & 1)) break;
 #pragma unroll 1
                 for (int j = -2; j < n; ++j) {
-                    // batch: V of tile j, K of tile j + 2
-                    const uint32_t i = nb + j + 2;
-                    const bool has_v = j >= 0, has_k = j + 2 < n;
-                    const bool my_v = has_v && (!pair || x == 1), my_k = has_k && (!pair || x == 0);
-                    if (lane == 0) {
-                        uint64_t* bar = &B->kv_full[rx][i % DONE];
-                        if (my_v || my_k) mbar_arrive_expect_tx(bar, (my_v + my_k) * C::TILE);
-                        else mbar_arrive(bar);  // (a batch without my tiles has its phase too)
+                    // batch: P V of tile j, S of tile j + 2
+                    const uint32_t vst = first_stage(x) + stage_of(ring + v_seq(max(j, 0), n));
+                    const uint32_t kst = first_stage(x) + stage_of(ring + k_seq(j + 2));
+                    const uint32_t d = tS + 64 * ((nt + j) & 1);  // S buffer of both tiles
+                    if (j >= 0 || j + 2 < n) landed(x, nb + j + 2);
+                    if (j >= 0) {
+                        if (j == 0) wait(&B->o_empty[x], (nseg & 1) ^ 1);  // the segment before has been read out
+                        wait(&B->p_full[x][(nt + j) & 1], ((nt + j) >> 1) & 1);
                     }
-                    if (my_v) tile(1, j, i);
-                    if (my_k) tile(0, j + 2, i);
-                    if (lane == 0) {
-                        if (has_v) rel[first_stage(x) + stage_of(ring + v_seq(j, n))] = i;
-                        if (has_k) rel[first_stage(x) + stage_of(ring + k_seq(j + 2))] = i;
-                    }
-                    armed = i + 1;
-                    if (j == -2 && lane == 0 && rx == x) {
-                        // the queries: behind the first tile, whose stage waits for the segment before alone
-                        for (int y = x; y < (pair ? 2 : x + 1); ++y) {
-                            if (!wait(&B->q_empty[y], (nseg & 1) ^ 1)) break;
-                            mbar_arrive_expect_tx(&B->q_full[y], C::HALVES * 128 * P.g * P.RH);
-#pragma unroll
-                            for (int c = 0; c < C::HALVES; ++c)
-                                tma_load_3d(q_at + y * C::Q_TILE + c * C::Q_REG, &mq, &B->q_full[y], 64 * c, kvh * P.g,
-                                            row0 + (pair ? y * P.RH : 0));
-                        }
-                    }
-                    wait.ok = __shfl_sync(0xffffffffu, (int)wait.ok, 0);
                     if (!wait.ok) break;
-                }
-                ++nseg;
-                bad = __any_sync(0xffffffffu, bad);
-                if (lane == 0) {
-                    // (on line 0 warp 10's K tiles speak for the pages)
-                    if (rx == x) a.W.block_bad[s.block] = bad;
-                    if (pair && rx == x) a.W.block_bad[s.block + 1] = bad;
-                }
-                ring += 2 * n;
-                nb += n + 2;
-            }
-            if (lane == 0 && wait.ok && rx == x) {
-                // the last commits have arrived: nothing is under way to this line's barriers any more
-                for (int y = x; y < (pair ? 2 : x + 1); ++y)
-                    if (nseg) {
-                        for (uint32_t i = nb > DONE ? nb - DONE : 0; i < nb; ++i) batch_done(y, i);
-                        wait(&B->q_empty[y], (nseg - 1) & 1);
-                    }
-            }
-            // a wait ran out: the copies in flight must land before the CTA leaves its shared memory
-            if (lane == 0 && !wait.ok) {
-                for (uint32_t i = armed > DONE ? armed - DONE : 0; i < armed; ++i)
-                    Waiter::late(&B->kv_full[rx][i % DONE], (i / DONE) & 1, 1u << 16);
-                for (int y = x; y < (pair ? 2 : x + 1); ++y)
-                    if (nseg) Waiter::late(&B->q_full[y], (nseg - 1) & 1, 1u << 16);
-            }
-        } else if (warp >= 8) {
-            // ------------------------------------------------------------ MMA
-            const int x = warp - 8;
-            if (lane == 0) {
-                constexpr uint32_t ID_S = idesc_bf16(VT, KT), ID_O = idesc_bf16(VT, HD, true);
-                const uint32_t tS = tmem + 128 * x, tO = tmem + 256 + HD * x;
-                const uint64_t q_desc = sw128_desc(q_at + x * C::Q_TILE);
-                const uint64_t k_desc = sw128_desc(ring_at), v_desc = sw128_desc(ring_at, C::KV_REG, 1024);
-                uint32_t nseg = 0, nt = 0, nb = 0;  // segments, tiles and batches before this one
-                Seg s;
-#pragma unroll 1
-                while (take(x, nseg, false, s)) {
-                    const int n = s.n;
-                    if (!wait(&B->q_full[x], nseg & 1)) break;
-#pragma unroll 1
-                    for (int j = -2; j < n; ++j) {
-                        // batch: P V of tile j, S of tile j + 2
-                        const uint32_t vst = first_stage(x) + stage_of(ring + v_seq(max(j, 0), n));
-                        const uint32_t kst = first_stage(x) + stage_of(ring + k_seq(j + 2));
-                        const uint32_t d = tS + 64 * ((nt + j) & 1);  // S buffer of both tiles
-                        if (j >= 0 || j + 2 < n) landed(x, nb + j + 2);
-                        if (j >= 0) {
-                            if (j == 0) wait(&B->o_empty[x], (nseg & 1) ^ 1);  // the segment before has been read out
-                            wait(&B->p_full[x][(nt + j) & 1], ((nt + j) >> 1) & 1);
-                        }
-                        if (!wait.ok) break;
-                        fence_after();
-                        if (j >= 0) {
-                            const uint64_t vd = v_desc + vst * (C::TILE >> 4);
-#pragma unroll
-                            for (int kk = 0; kk < KT / 16; ++kk)
-                                umma_bf16_ts(tO, d + 8 * kk, vd + ((kk * 2048) >> 4), ID_O, (j > 0 || kk > 0) ? 1u : 0u);
-                        }
-                        if (j + 2 < n) {
-                            const uint64_t kd = k_desc + kst * (C::TILE >> 4);
-#pragma unroll
-                            for (int kk = 0; kk < HD / 16; ++kk)
-                                umma_bf16(d, q_desc + (((kk >> 2) * C::Q_REG + (kk & 3) * 32) >> 4),
-                                          kd + (((kk >> 2) * C::KV_REG + (kk & 3) * 32) >> 4), ID_S, kk > 0 ? 1u : 0u);
-                        }
-                        umma_commit(&B->done[x][(nb + j + 2) % DONE]);
-                        if (j + 3 == n) umma_commit(&B->q_empty[x]);
-                    }
-                    nb += n + 2;
-                    ++nseg;
-                    nt += n;
-                    ring += 2 * n;
-                }
-                if (!wait.ok) {  // products that were issued must have ended before their accumulators are freed
-                    umma_commit(&B->drain[x]);
-                    Waiter::late(&B->drain[x], 0);
-                }
-            }
-            __syncwarp();
-        } else {
-            // ------------------------------------------------------------ softmax
-            const int x = warp >> 2, v = tid & 127, quad = warp & 3;
-            const uint32_t tl = tmem + ((uint32_t)(32 * quad) << 16);
-            const uint32_t tO = tl + 256 + HD * x;
-            const uint64_t scale2 = pack2(a.scale_log2, a.scale_log2);
-            uint32_t nt = 0, nb = 0;  // tiles and batches before this segment
-            uint32_t nseg = 0;
-            Seg s;
-#pragma unroll 1
-            while (take(x, nseg, true, s)) {
-                ++nseg;
-                const int n = s.n;
-                const int r0 = pair ? x * P.RH : 0;  // this stream's rows of the item
-                const int nv = min(P.RH, s.nrows - r0) * P.g;
-                int lim = 0;
-                if (v < nv) lim = max(s.lim0 + s.step * (r0 + v / P.g), 0);
-                const bool live_warp = 32 * quad < nv;
-                float m_run = -INFINITY, l_run = 0.f;
-#pragma unroll 1
-                for (int j = 0; j < n; ++j) {
-                    const int k0 = (s.t0 + j) * KT;
-                    const uint32_t buf = (nt + j) & 1;
-                    const uint32_t tS = tl + 128 * x + 64 * buf;
-                    if (!batch_done(x, nb + j)) break;
                     fence_after();
-                    if (k0 + KT > s.keys) {
-                        // the list ends inside this tile: zero the rows of V behind it (a page's unused slots may
-                        // hold anything, and 0 * NaN is NaN); on line 0 both streams do, each before its own P V
-                        const uint32_t st = first_stage(x) + stage_of(ring + v_seq(j, n));
-                        if (!landed(x, nb + j + 2)) break;
-                        uint8_t* V = sm + C::RING_AT + st * C::TILE;
-                        for (int i = (s.keys - k0) * 8 + v; i < KT * 8; i += 128)
+                    if (j >= 0) {
+                        const uint64_t vd = v_desc + vst * (C::TILE >> 4);
 #pragma unroll
-                            for (int c = 0; c < C::HALVES; ++c)
-                                *reinterpret_cast<uint4*>(V + c * C::KV_REG + i * 16) = make_uint4(0u, 0u, 0u, 0u);
-                        fence_proxy_async();
+                        for (int kk = 0; kk < KT / 16; ++kk)
+                            umma_bf16_ts(tO, d + 8 * kk, vd + ((kk * 2048) >> 4), ID_O, (j > 0 || kk > 0) ? 1u : 0u);
                     }
-                    if (live_warp) {
-                        uint32_t sr[KT];
-                        tmem_ld32_issue(tS, sr);
-                        tmem_ld32_issue(tS + 32, sr + 32);
-                        tmem_ld32_wait(sr);
-                        tmem_ld32_wait(sr + 32);
-                        if (__any_sync(0xffffffffu, k0 + KT > lim)) {
-                            const int left = lim - k0;
+                    if (j + 2 < n) {
+                        const uint64_t kd = k_desc + kst * (C::TILE >> 4);
 #pragma unroll
-                            for (int c = 0; c < KT; ++c)
-                                if (c >= left) sr[c] = 0xFF800000u;  // -inf
-                        }
-                        float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-                        for (int c = 0; c < KT; c += 2)
-                            mx4[(c >> 1) & 3] =
-                                fmaxf(fmaxf(mx4[(c >> 1) & 3], __uint_as_float(sr[c])), __uint_as_float(sr[c + 1]));
-                        const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * a.scale_log2;
-                        const float m_new = mx > m_run + 8.f ? mx : m_run;
-                        if (j > 0 && __any_sync(0xffffffffu, m_new != m_run)) {
-                            // O holds the tiles before this one once the product of the last of them has completed
-                            if (!batch_done(x, nb + j + 1)) break;
-                            fence_after();
-                            const float alpha = m_run == -INFINITY ? 0.f : ex2(m_run - m_new);
-                            l_run *= alpha;
-#pragma unroll 1
-                            for (int c = 0; c < HD; c += 32) {
-                                uint32_t o[32];
-                                tmem_ld32_issue(tO + c, o);
-                                tmem_ld32_wait(o);
-#pragma unroll
-                                for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
-                                tmem_st32(tO + c, o);
-                            }
-                        }
-                        m_run = m_new;
-                        const float neg = m_run == -INFINITY ? 0.f : -m_run;
-                        const uint64_t neg2 = pack2(neg, neg);
-                        uint64_t sum2[2] = {0ull, 0ull};
-                        uint32_t pk[KT / 2];
-#pragma unroll
-                        for (int e = 0; e < KT / 2; ++e) {
-                            float x0, x1;
-                            unpack2(fma2(pack2(__uint_as_float(sr[2 * e]), __uint_as_float(sr[2 * e + 1])), scale2, neg2), x0, x1);
-                            x0 = ex2(x0);
-                            x1 = ex2(x1);
-                            sum2[e & 1] = add2(sum2[e & 1], pack2(x0, x1));
-                            pk[e] = pack2_bf16(x0, x1);
-                        }
-                        tmem_st32(tS, pk);
-                        float s0, s1;
-                        unpack2(add2(sum2[0], sum2[1]), s0, s1);
-                        l_run += s0 + s1;
-                        tmem_st_wait();
+                        for (int kk = 0; kk < HD / 16; ++kk)
+                            umma_bf16(d, q_desc + (((kk >> 2) * C::Q_REG + (kk & 3) * 32) >> 4),
+                                      kd + (((kk >> 2) * C::KV_REG + (kk & 3) * 32) >> 4), ID_S, kk > 0 ? 1u : 0u);
                     }
-                    fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&B->p_full[x][buf]);
+                    umma_commit(&B->done[x][(nb + j + 2) % DONE]);
+                    if (j + 3 == n) umma_commit(&B->q_empty[x]);
                 }
-                if (!batch_done(x, nb + n + 1)) break;
-                fence_after();
-                if (live_warp) {
-                    const size_t blk = s.block + (pair ? x : 0);
-                    if (v < nv) a.W.ml[blk * VT + v] = make_float2(m_run, l_run);
-                    float* o = a.W.o + blk * VT * HD + (size_t)v * 8;
-#pragma unroll 1
-                    for (int c = 0; c < HD; c += 32) {
-                        uint32_t r[32];
-                        tmem_ld32_issue(tO + c, r);
-                        tmem_ld32_wait(r);
-                        if (v < nv)
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                float* d = o + (size_t)(c / 8 + e) * VT * 8;
-                                *reinterpret_cast<uint4*>(d) = make_uint4(r[8 * e], r[8 * e + 1], r[8 * e + 2], r[8 * e + 3]);
-                                *reinterpret_cast<uint4*>(d + 4) =
-                                    make_uint4(r[8 * e + 4], r[8 * e + 5], r[8 * e + 6], r[8 * e + 7]);
-                            }
-                    }
-                }
-                fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&B->o_empty[x]);
-                nt += n;
                 nb += n + 2;
+                ++nseg;
+                nt += n;
                 ring += 2 * n;
+            }
+            if (!wait.ok) {  // products that were issued must have ended before their accumulators are freed
+                umma_commit(&B->drain[x]);
+                Waiter::late(&B->drain[x], 0);
             }
         }
         __syncwarp();
+    } else {
+        // ------------------------------------------------------------ softmax
+        const int x = warp >> 2, v = tid & 127, quad = warp & 3;
+        const uint32_t tl = tmem + ((uint32_t)(32 * quad) << 16);
+        const uint32_t tO = tl + 256 + HD * x;
+        const uint64_t scale2 = pack2(a.scale_log2, a.scale_log2);
+        uint32_t nt = 0, nb = 0;  // tiles and batches before this segment
+        uint32_t nseg = 0;
+        Seg s;
+#pragma unroll 1
+        while (take(x, nseg, true, s)) {
+            ++nseg;
+            const int n = s.n;
+            const int r0 = pair ? x * P.RH : 0;  // this stream's rows of the item
+            const int nv = min(P.RH, s.nrows - r0) * P.g;
+            int lim = 0;
+            if (v < nv) lim = max(s.lim0 + s.step * (r0 + v / P.g), 0);
+            const bool live_warp = 32 * quad < nv;
+            float m_run = -INFINITY, l_run = 0.f;
+#pragma unroll 1
+            for (int j = 0; j < n; ++j) {
+                const int k0 = (s.t0 + j) * KT;
+                const uint32_t buf = (nt + j) & 1;
+                const uint32_t tS = tl + 128 * x + 64 * buf;
+                if (!batch_done(x, nb + j)) break;
+                fence_after();
+                if (k0 + KT > s.keys) {
+                    // the list ends inside this tile: zero the rows of V behind it (a page's unused slots may
+                    // hold anything, and 0 * NaN is NaN); on line 0 both streams do, each before its own P V
+                    const uint32_t st = first_stage(x) + stage_of(ring + v_seq(j, n));
+                    if (!landed(x, nb + j + 2)) break;
+                    uint8_t* V = sm + C::RING_AT + st * C::TILE;
+                    for (int i = (s.keys - k0) * 8 + v; i < KT * 8; i += 128)
+#pragma unroll
+                        for (int c = 0; c < C::HALVES; ++c)
+                            *reinterpret_cast<uint4*>(V + c * C::KV_REG + i * 16) = make_uint4(0u, 0u, 0u, 0u);
+                    fence_proxy_async();
+                }
+                if (live_warp) {
+                    uint32_t sr[KT];
+                    tmem_ld32_issue(tS, sr);
+                    tmem_ld32_issue(tS + 32, sr + 32);
+                    tmem_ld32_wait(sr);
+                    tmem_ld32_wait(sr + 32);
+                    if (__any_sync(0xffffffffu, k0 + KT > lim)) {
+                        const int left = lim - k0;
+#pragma unroll
+                        for (int c = 0; c < KT; ++c)
+                            if (c >= left) sr[c] = 0xFF800000u;  // -inf
+                    }
+                    float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                    for (int c = 0; c < KT; c += 2)
+                        mx4[(c >> 1) & 3] =
+                            fmaxf(fmaxf(mx4[(c >> 1) & 3], __uint_as_float(sr[c])), __uint_as_float(sr[c + 1]));
+                    const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * a.scale_log2;
+                    const float m_new = mx > m_run + 8.f ? mx : m_run;
+                    if (j > 0 && __any_sync(0xffffffffu, m_new != m_run)) {
+                        // O holds the tiles before this one once the product of the last of them has completed
+                        if (!batch_done(x, nb + j + 1)) break;
+                        fence_after();
+                        const float alpha = m_run == -INFINITY ? 0.f : ex2(m_run - m_new);
+                        l_run *= alpha;
+#pragma unroll 1
+                        for (int c = 0; c < HD; c += 32) {
+                            uint32_t o[32];
+                            tmem_ld32_issue(tO + c, o);
+                            tmem_ld32_wait(o);
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+                            tmem_st32(tO + c, o);
+                        }
+                    }
+                    m_run = m_new;
+                    const float neg = m_run == -INFINITY ? 0.f : -m_run;
+                    const uint64_t neg2 = pack2(neg, neg);
+                    uint64_t sum2[2] = {0ull, 0ull};
+                    uint32_t pk[KT / 2];
+#pragma unroll
+                    for (int e = 0; e < KT / 2; ++e) {
+                        float x0, x1;
+                        unpack2(fma2(pack2(__uint_as_float(sr[2 * e]), __uint_as_float(sr[2 * e + 1])), scale2, neg2), x0, x1);
+                        x0 = ex2(x0);
+                        x1 = ex2(x1);
+                        sum2[e & 1] = add2(sum2[e & 1], pack2(x0, x1));
+                        pk[e] = pack2_bf16(x0, x1);
+                    }
+                    tmem_st32(tS, pk);
+                    float s0, s1;
+                    unpack2(add2(sum2[0], sum2[1]), s0, s1);
+                    l_run += s0 + s1;
+                    tmem_st_wait();
+                }
+                fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&B->p_full[x][buf]);
+            }
+            if (!batch_done(x, nb + n + 1)) break;
+            fence_after();
+            if (live_warp) {
+                const size_t blk = s.block + (pair ? x : 0);
+                if (v < nv) a.W.ml[blk * VT + v] = make_float2(m_run, l_run);
+                float* o = a.W.o + blk * VT * HD + (size_t)v * 8;
+#pragma unroll 1
+                for (int c = 0; c < HD; c += 32) {
+                    uint32_t r[32];
+                    tmem_ld32_issue(tO + c, r);
+                    tmem_ld32_wait(r);
+                    if (v < nv)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            float* d = o + (size_t)(c / 8 + e) * VT * 8;
+                            *reinterpret_cast<uint4*>(d) = make_uint4(r[8 * e], r[8 * e + 1], r[8 * e + 2], r[8 * e + 3]);
+                            *reinterpret_cast<uint4*>(d + 4) =
+                                make_uint4(r[8 * e + 4], r[8 * e + 5], r[8 * e + 6], r[8 * e + 7]);
+                        }
+                }
+            }
+            fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&B->o_empty[x]);
+            nt += n;
+            nb += n + 2;
+            ring += 2 * n;
+        }
     }
+    __syncwarp();
     // (not earlier: the merge's CTAs would gather on the SMs that are free first)
     pdl_trigger();
     fence_before();

@@ -39,13 +39,13 @@ struct Shape {
     long long ld_table;
     const int *prefix_pages, *table, *kv_lens, *q_start;
     __host__ __device__ int row_tile(int line) const { return line == 0 ? 2 * RH : RH; }
-    __host__ __device__ int workers(int line) const { return line == 0 ? n_cta : 2 * n_cta; }
 };
 
 // Cut of the lines.
 struct Head {
     uint32_t W[2];     // length
     uint32_t part[2];  // length of a worker's part: ceil(W / workers)
+    int n1;            // CTAs on line 1 (two workers each); the others are on line 0
     uint32_t CP;       // length of the prefix items, at the start of line pl
     uint32_t items0;   // items on line 0
     int pl;            // line of the prefix items
@@ -282,11 +282,15 @@ __device__ __forceinline__ void make_plan(const Shape& P, uint32_t* base, uint32
     __syncthreads();
     h.bad = m->bad || m->sum[0] >> 31 || m->sum[1] >> 31;
     h.max_m = m->max_m;
-#pragma unroll
-    for (int l = 0; l < 2; ++l) {
-        h.W[l] = h.bad ? 0u : carry[l];
-        h.part[l] = max(1u, (h.W[l] + P.workers(l) - 1) / P.workers(l));
-    }
+    h.W[0] = h.bad ? 0u : carry[0];
+    h.W[1] = h.bad ? 0u : carry[1];
+    // CTAs by the lines' work: a tile of line 1 takes a CTA 0.55 of the time of one of line 0 (at 0.48 / 0.55 / 0.62 the
+    // verify blocks of 32 x 16 rows behind 8192 keys take 109 / 101 / 103 us; with every CTA on both lines in turn 116)
+    const long long c0 = 100ll * h.W[0], c1 = 55ll * h.W[1];
+    h.n1 = c0 == 0 ? P.n_cta : c1 == 0 ? 0 : min(max((int)((P.n_cta * c1 + (c0 + c1) / 2) / (c0 + c1)), 1), P.n_cta - 1);
+    const uint32_t w0 = max(P.n_cta - h.n1, 1), w1 = max(2 * h.n1, 1);
+    h.part[0] = max(1u, (h.W[0] + w0 - 1) / w0);
+    h.part[1] = max(1u, (h.W[1] + w1 - 1) / w1);
     h.items0 = carry[2] + (h.pl == 0 ? (uint32_t)h.n_prefix : 0u);
 }
 
