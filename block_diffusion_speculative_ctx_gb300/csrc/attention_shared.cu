@@ -86,7 +86,7 @@ __global__ void __launch_bounds__(32 * MWARPS, 3) merge_kernel(MergeArgs a) {
     const int chunks = P.hd / 8, elems = P.g * chunks;
 #pragma unroll 1
     for (int e0 = 0; e0 < elems; e0 += 32) {
-        const int e = min(e0 + lane, elems - 1), hh = e / chunks, c8 = e - hh * chunks;
+        const int e = min(e0 + lane, elems - 1), c8 = e / P.g, hh = e - c8 * P.g;
         Part acc;
         uint32_t bb = 0;
 #pragma unroll 1
