@@ -167,8 +167,8 @@ sp::Shape sizes_of(bool f32, int H, int Hkv, int hd, int batch, int rows) {
     P.batch = batch;
     P.rows = rows;
     P.n_cta = CTAS;
-    // an item's fixed cost: four tiles on line 0, three on line 1 (32 prompts of 5 .. 130 rows behind 2100 keys: 154 us
-    // with two and three, 134 with three and three, 127 with these, 126 with five and four)
+    // an item's fixed cost: four tiles on line 0, three on line 1 (32 prompts of 5 .. 130 rows behind 2100 keys: 114 us
+    // with these, 130 with two on line 1, 112 with three on line 0, where blocks of 16 then take 22.6 instead of 21.5 us)
     P.lead[0] = 4;
     P.lead[1] = f32 ? 1 : 3;
     return P;
