@@ -963,16 +963,16 @@ struct Pass {
     // Behind shared pages: the rounds' rows and own lengths for the shared-prefix attention (false: the
     // sequences are attended one by one).  `keys` then counts the shared keys once.
     // The rule, from a verify pass of three layers at Qwen3-8B's shapes with 100 own keys, blocks of 16 (one by
-    // one -> shared): the shared form pays two launches and a merge, and saves the prefix's keys of all sequences
-    // but one.  Batch 2: 1024 keys 0.550 -> 0.548 ms, 4096 0.602 -> 0.568.  Batch 4: 2048 0.685 -> 0.703, 4096 0.744
-    // -> 0.722.  Batch 8: 1024 0.820 -> 0.839, 2048 0.856 -> 0.851, 8192 1.055 -> 0.886.  Batch 16: 512 1.029 ->
-    // 1.037, 1024 1.064 -> 1.051.  Batch 32: 512 1.157 -> 1.172, 1024 1.216 -> 1.190, 8192 2.132 -> 1.333.
+    // one -> shared): the shared form pays a launch and a merge, and saves the prefix's keys of all sequences but
+    // one.  512 shared keys: batch 2 0.527 -> 0.522 ms, 8 0.788 -> 0.787 (a draft layer 0.475 -> 0.482), 32 1.158 ->
+    // 1.156.  1024: 2 0.538 -> 0.527, 4 0.651 -> 0.643, 8 0.813 -> 0.801, 32 1.223 -> 1.167.  8192: 2 0.668 ->
+    // 0.569, 8 1.045 -> 0.865, 32 2.136 -> 1.305.
     bool round_lengths(double& keys) {
-        const long long common = 64ll * c->shared_pages;
-        if (common < 1024 || (common < 4096 && common * c->batch < 16384)) return false;
-        keys -= 64.0 * c->shared_pages * (c->batch - 1);
+        const int common = c->shared_pages * PAGE_TOKENS;
+        if (common < 1024) return false;
+        keys -= (double)common * (c->batch - 1);
         Launch L = c->L();
-        own_lengths(L, c->batch, c->n, nullptr, c->B - c->shared_pages * PAGE_TOKENS, c->own_lens, c->own_start, &c->B);
+        own_lengths(L, c->batch, c->n, nullptr, c->B - common, c->own_lens, c->own_start, &c->B);
         return true;
     }
 

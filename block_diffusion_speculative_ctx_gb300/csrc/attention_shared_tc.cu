@@ -452,9 +452,10 @@ __global__ void __launch_bounds__(NTHR, 1)
             const int n = s.n;
             const int r0 = pair ? x * P.RH : 0;  // this stream's rows of the item
             const int nv = min(P.RH, s.nrows - r0) * P.g;
-            int lim = 0;
+            int lim = 0x7fffffff;  // (a lane of no query vector: anything)
             if (v < nv) lim = max(s.lim0 + s.step * (r0 + v / P.g), 0);
             const bool live_warp = 32 * quad < nv;
+            const int lim_warp = __reduce_min_sync(0xffffffffu, lim);
             float m_run = -INFINITY, l_run = 0.f;
 #pragma unroll 1
             for (int j = 0; j < n; ++j) {
@@ -481,7 +482,7 @@ __global__ void __launch_bounds__(NTHR, 1)
                     tmem_ld32_issue(tS + 32, sr + 32);
                     tmem_ld32_wait(sr);
                     tmem_ld32_wait(sr + 32);
-                    if (__any_sync(0xffffffffu, k0 + KT > lim)) {
+                    if (k0 + KT > lim_warp) {
                         const int left = lim - k0;
 #pragma unroll
                         for (int c = 0; c < KT; ++c)
@@ -493,7 +494,7 @@ __global__ void __launch_bounds__(NTHR, 1)
                         mx4[(c >> 1) & 3] =
                             fmaxf(fmaxf(mx4[(c >> 1) & 3], __uint_as_float(sr[c])), __uint_as_float(sr[c + 1]));
                     const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * a.scale_log2;
-                    const float m_new = mx > m_run + 8.f ? mx : m_run;
+                    const float m_new = v < nv && mx > m_run + 8.f ? mx : m_run;
                     if (j > 0 && __any_sync(0xffffffffu, m_new != m_run)) {
                         // O holds the tiles before this one once the product of the last of them has completed
                         if (!batch_done(x, nb + j + 1)) break;

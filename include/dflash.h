@@ -208,8 +208,8 @@ dflash_status dflash_prefill(dflash_ctx* ctx, int32_t batch, const int32_t* prom
  * shared by every sequence's page table (its remaining tokens are prefilled
  * with each prompt), the prompts' own tokens run in ragged batched passes, and
  * until the next prefill the rounds attend to the shared keys once for the
- * batch (dflash_shared_prefix_attention) where that pays: behind 4096 shared
- * keys or more, or 1024 or more with shared keys * batch >= 16384.
+ * batch (dflash_shared_prefix_attention) where that pays: behind 1024 shared
+ * keys or more.
  * prefix: host [prefix_len]; prompt_lens: host [batch], each >= 1, without the
  * prefix; prompt_tokens: host, concatenated; first_tokens: host [batch] output.
  * The first call allocates the attention's workspace (kept until

@@ -44,8 +44,8 @@ def _rel(a, b):
     ("small_bf16", 130, (37, 100), None),
     ("small_bf16", 1000, (3, 400), (16, 8)),
     ("small_bf16_llama", 200, (64, 5, 130, 33), None),
-    ("tiny_f32_b3", 4130, (5, 60, 12), (4, 2, 1, 3)),  # 64 shared pages: the rounds attend to them once
-    ("small_bf16_long8k", 4130, (3, 40), None),
+    ("tiny_f32_b3", 1100, (5, 60, 12), (4, 2, 1, 3)),  # 17 shared pages: the rounds attend to them once
+    ("small_bf16_long8k", 1100, (3, 40), None),
 ])
 def test_prefill_shared_and_rounds(name, prefix_len, lens, schedule):
     w = configs.get(name)
@@ -105,7 +105,7 @@ def test_prefill_shared_and_rounds(name, prefix_len, lens, schedule):
         sess.close()
 
 
-@pytest.mark.parametrize("prefix_len", [2200, 4200])  # rounds sequence by sequence; rounds on the shared keys
+@pytest.mark.parametrize("prefix_len", [900, 2200])  # rounds sequence by sequence; rounds on the shared keys
 def test_prefill_shared_runs_in_several_chunks(prefix_len):
     """A prefix longer than one prefill chunk and more suffix rows than one (a sequence split over two), against a
     plain prefill of the whole prompts by the same library; then graph replays equal eager rounds bit for bit."""
