@@ -288,6 +288,25 @@ def test_shared_prefix_attention_equals_itself(dtype):
     assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
 
 
+def test_shared_prefix_attention_workspaces_of_its_own():
+    """No workspace given: calls of growing and shrinking sizes on the default stream (which share one) while others
+    run on a side stream (one each) give what calls with a workspace of their own give, bit for bit."""
+    cases = [attn_inputs(attn_case("bf16", (8, 2, 128), p, kv, q, seed=71 + p)) for p, kv, q in
+             ((100, [70, 3], [2, 3]), (3000, [400, 90, 65, 10], [90, 1, 64, 17]), (500, [20], [20]))]
+    own = [torch.empty(dfl().shared_prefix_workspace(x[0], x[1], x[6].numel()), dtype=torch.uint8, device="cuda") for x in cases]
+    want = [[t.clone() for t in dfl().shared_prefix_attention(*x, workspace=w)] for x, w in zip(cases, own)]
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    got = []
+    for i in range(12):
+        got.append((i % 3, dfl().shared_prefix_attention(*cases[i % 3])))
+        with torch.cuda.stream(side):
+            got.append(((i + 1) % 3, dfl().shared_prefix_attention(*cases[(i + 1) % 3])))
+    torch.cuda.synchronize()
+    for i, (out, lse) in got:
+        assert torch.equal(out, want[i][0]) and torch.equal(lse, want[i][1])
+
+
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 def test_shared_prefix_attention_in_place(dtype):
     """out is q: the queries have all been read before the first result is written."""
