@@ -269,6 +269,7 @@ extern "C" dflash_status dflash_shared_prefix_attention(const dflash_shared_pref
     if (p->rows == 0) return DFLASH_OK;
     bool failed = false;
     Launch L{(cudaStream_t)cuda_stream, nullptr};
+    L.pdl = true;  // (each kernel waits for what runs before it ahead of its first read)
     L.failed = &failed;
     const bool ok = shared_prefix_attention(L, *p);
     const cudaError_t e = cudaGetLastError();

@@ -191,6 +191,7 @@ extern "C" dflash_status dflash_kv_tables(const dflash_kv_tables_args* p, void* 
         return fail("kv_tables: in place needs one row stride");
     bool failed = false;
     Launch L{(cudaStream_t)cuda_stream, nullptr};
+    L.pdl = true;  // (each kernel waits for what runs before it ahead of its first read)
     L.failed = &failed;
     kv_tables(L, a);
     const cudaError_t e = cudaGetLastError();

@@ -332,6 +332,7 @@ extern "C" dflash_status dflash_process_logits(const dflash_logits_args* p, void
     }
     bool failed = false;
     Launch L{(cudaStream_t)cuda_stream, nullptr};
+    L.pdl = true;  // (each kernel waits for what runs before it ahead of its first read)
     L.failed = &failed;
     process_logits(L, *p);
     const cudaError_t e = cudaGetLastError();
