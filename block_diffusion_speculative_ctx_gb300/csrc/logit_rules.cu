@@ -16,6 +16,9 @@
 // together, so the CTAs of the first chunk had nearly all of that pass to do.)
 // Drafts stay a list of at most 31 ids: a token that is a draft carries a bit, and
 // only such tokens count the drafts before their row.
+// Measured (graph replay): 109 us for 512 rows of 151936 in fp32 (5.7 TB/s of the bytes above, 84 % of a measured copy);
+// 20 us for 64 bf16 rows of 128256 and 9.4 us for 16 rows of one sequence behind up to 8448 tokens, where
+// the lists' chain of loads counts; 3.3 us for a single row.
 #include <math.h>
 
 #include <algorithm>
@@ -268,7 +271,8 @@ void run(const Launch& L, const dflash_logits_args& a) {
     Plan pl;
     pl.chunk = NT * NV * 16 / (int)sizeof(T);
     const int chunks = (a.vocab + pl.chunk - 1) / pl.chunk;
-    // few CTAs (short batch): the rows of a sequence go to several, each of which reads the history again
+    // few CTAs (short batch): the rows of a sequence go to several, each of which reads the history again; 608 CTAs, four
+    // an SM (16 rows of 151936 behind up to 8448 tokens: 11.3 us with 304, 10.3 with 608, 11.5 with 1216)
     pl.groups = (int)std::min<long long>(a.rows_per_seq, std::max(1ll, 608ll / ((long long)chunks * a.batch)));
     pl.rows = (a.rows_per_seq + pl.groups - 1) / pl.groups;
     pl.groups = (a.rows_per_seq + pl.rows - 1) / pl.rows;
@@ -279,11 +283,12 @@ void run(const Launch& L, const dflash_logits_args& a) {
              dim3(chunks, (unsigned)(a.batch * pl.groups)), dim3(NT), smem, 1, a, pl);
 }
 
-// Vectors per thread: two, unless that leaves fewer than two CTAs an SM.
+// Vectors per thread: two (512 rows of 151936: 109 us, with one 123; 64 bf16 rows of 128256: 20 and 27 us), unless the
+// rows, split one a CTA, would leave fewer than two CTAs an SM (one row of 151936: 3.6 us with two, 3.3 with one).
 template <typename T>
 void run(const Launch& L, const dflash_logits_args& a) {
     const int chunk2 = NT * 2 * 16 / (int)sizeof(T);
-    if ((long long)a.batch * ((a.vocab + chunk2 - 1) / chunk2) >= 304) run<T, 2>(L, a);
+    if ((long long)a.batch * a.rows_per_seq * ((a.vocab + chunk2 - 1) / chunk2) >= 304) run<T, 2>(L, a);
     else run<T, 1>(L, a);
 }
 
