@@ -16,9 +16,9 @@
 // together, so the CTAs of the first chunk had nearly all of that pass to do.)
 // Drafts stay a list of at most 31 ids: a token that is a draft carries a bit, and
 // only such tokens count the drafts before their row.
-// Measured (graph replay): 109 us for 512 rows of 151936 in fp32 (5.7 TB/s of the bytes above, 84 % of a measured copy);
-// 20 us for 64 bf16 rows of 128256 and 9.4 us for 16 rows of one sequence behind up to 8448 tokens, where
-// the lists' chain of loads counts; 3.3 us for a single row.
+// Measured (graph replay): 111 us for 512 rows of 151936 in fp32 (5.6 TB/s of the bytes above, 82 % of a measured copy;
+// 125 us for rows of 151937, 261 us token by token); 20 us for 64 bf16 rows of 128256 and 8.5 us for 16 rows of one
+// sequence behind up to 8448 tokens, where the lists' chain of loads counts; 3.4 us for a single row.
 #include <math.h>
 
 #include <algorithm>
@@ -56,9 +56,13 @@ struct Plan {
     int groups;  // row groups per sequence
 };
 
-// T logits; NV vectors per thread and row (chunk = NT * NV * 16 / sizeof(T) tokens); VEC: base pointers and
-// row strides are multiples of 16 bytes (else the stream moves single elements).
-template <typename T, int NV, bool VEC>
+// How rows lie: every row starts on 16 bytes; a row starts anywhere, in logits and out alike (its vectors begin with
+// its first aligned token, the few before and behind them go one by one); logits and out lie differently (single
+// tokens throughout).
+enum Lie { ALIGNED, SHIFTED, SINGLE };
+
+// T logits; NV vectors per thread and row (chunk = NT * NV * 16 / sizeof(T) tokens).
+template <typename T, int NV, Lie LIE>
 __global__ void __launch_bounds__(NT) logit_rules_kernel(dflash_logits_args a, Plan pl) {
     constexpr int G = 16 / (int)sizeof(T);  // tokens of a vector
     constexpr int CH = NT * NV * G;
@@ -80,30 +84,43 @@ __global__ void __launch_bounds__(NT) logit_rules_kernel(dflash_logits_args a, P
 
     // ---- the first row's mask words and vectors, under way while the words are made
     constexpr uint32_t ALL = (1u << G) - 1u;
-    const int nvec = VEC ? n / G : 0;
+    // tokens of row j before its first vector, and its vectors
+    const int mis0 = (int)((uintptr_t)X / sizeof(T)) & (G - 1), mis_ld = (int)a.ld_logits & (G - 1);
+    auto head = [&](int j) { return LIE == SHIFTED ? -(mis0 + j * mis_ld) & (G - 1) : 0; };
+    auto vecs = [&](int j) { return LIE == SINGLE ? 0 : max(n - head(j), 0) / G; };
     uint32_t bits[NV], next[NV];  // mask bits of the row whose logits are loaded next, and of the row after
     uint4 x[NV];
-    auto mask_bits = [&](int m, uint32_t (&b)[NV]) {
+    auto mask_bits = [&](int j, int m, uint32_t (&b)[NV]) {
+        const int h = head(j);
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            const int t = (tid + i * NT) * G;
-            b[i] = m >= 0 && t < n ? a.masks[(long long)m * a.ld_mask + ((c0 + t) >> 5)] >> (t & 31) & ALL : ALL;
+            const int t = h + (tid + i * NT) * G;
+            b[i] = ALL;
+            if (m >= 0 && t < n) {
+                const uint32_t* w = a.masks + (long long)m * a.ld_mask + ((c0 + t) >> 5);
+                b[i] = w[0] >> (t & 31);
+                if (LIE == SHIFTED && (t & 31) > 32 - G && ((c0 + t) | 31) + 1 < a.vocab) b[i] |= w[1] << (32 - (t & 31));
+                b[i] &= ALL;
+            }
         }
     };
-    auto load_mask = [&](int j, uint32_t (&b)[NV]) { mask_bits(j < rows ? midx[j] : -1, b); };
+    auto load_mask = [&](int j, uint32_t (&b)[NV]) { mask_bits(j, j < rows ? midx[j] : -1, b); };
+    // (a shifted vector lies in two groups of G tokens)
+    auto touched_vec = [&](int v, int h) { return flag[v] || (h && flag[v + 1]); };
     // in place, only vectors that a rule or the mask changes are touched
-    auto live = [&](int i, uint32_t b) {
+    auto live = [&](int i, uint32_t b, int j) {
         const int v = tid + i * NT;
-        return v < nvec && (!inplace || b != ALL || flag[v]);
+        return v < vecs(j) && (!inplace || b != ALL || touched_vec(v, head(j)));
     };
     auto load = [&](int j, const uint32_t (&b)[NV]) {
 #pragma unroll
         for (int i = 0; i < NV; ++i)
-            if (live(i, b[i]) && b[i]) x[i] = *reinterpret_cast<const uint4*>(X + j * a.ld_logits + (tid + i * NT) * G);
+            if (live(i, b[i], j) && b[i])
+                x[i] = *reinterpret_cast<const uint4*>(X + j * a.ld_logits + head(j) + (tid + i * NT) * G);
     };
-    if (VEC) {
+    if (LIE != SINGLE) {
         const int m = a.masks ? a.mask_index[row0] : -1;
-        mask_bits(m < a.n_masks ? m : -1, bits);
+        mask_bits(0, m < a.n_masks ? m : -1, bits);
         if (!inplace) load(0, bits);
     }
 
@@ -187,7 +204,7 @@ __global__ void __launch_bounds__(NT) logit_rules_kernel(dflash_logits_args a, P
     __syncthreads();
 
     // ---- the stream
-    if (VEC) {
+    if (LIE != SINGLE) {
         load_mask(1, next);
         if (inplace) load(0, bits);  // (which vectors change is known only now)
 #pragma unroll 1
@@ -204,23 +221,32 @@ __global__ void __launch_bounds__(NT) logit_rules_kernel(dflash_logits_args a, P
             if (j + 1 < rows) load(j + 1, bits);
 #pragma unroll
             for (int i = 0; i < NV; ++i)
-                if (live(i, b[i])) {
+                if (live(i, b[i], j)) {
+                    const int h = head(j);
                     uint32_t w[4] = {y[i].x, y[i].y, y[i].z, y[i].w};
                     const int v = tid + i * NT;
-                    if (b[i] && flag[v]) {
+                    if (b[i] && touched_vec(v, h)) {
 #pragma unroll
                         for (int q = 0; q < G / 4; ++q) {  // four tokens at a time
-                            const uint4 cw = *reinterpret_cast<const uint4*>(count + v * G + 4 * q);
-                            int4 bw = make_int4(0, 0, 0, 0);
-                            if (a.bias_ids) bw = *reinterpret_cast<const int4*>(bias + v * G + 4 * q);
-                            const uint32_t c4[4] = {cw.x, cw.y, cw.z, cw.w};
-                            const int b4[4] = {bw.x, bw.y, bw.z, bw.w};
+                            const int t = h + v * G + 4 * q;
+                            alignas(16) uint32_t c4[4];
+                            alignas(16) int b4[4] = {0, 0, 0, 0};
+                            if (LIE == ALIGNED) {
+                                *reinterpret_cast<uint4*>(c4) = *reinterpret_cast<const uint4*>(count + t);
+                                if (a.bias_ids) *reinterpret_cast<int4*>(b4) = *reinterpret_cast<const int4*>(bias + t);
+                            } else {
+#pragma unroll
+                                for (int e = 0; e < 4; ++e) {
+                                    c4[e] = count[t + e];
+                                    if (a.bias_ids) b4[e] = bias[t + e];
+                                }
+                            }
                             float l[4];
 #pragma unroll
                             for (int e = 0; e < 4; ++e) {
                                 if (sizeof(T) == 4) l[e] = __uint_as_float(w[e]);
                                 else l[e] = __uint_as_float(e & 1 ? w[2 * q + e / 2] & 0xFFFF0000u : w[2 * q + e / 2] << 16);
-                                l[e] = apply(l[e], c4[e], b4[e], v * G + 4 * q + e, j0 + j, rule);
+                                l[e] = apply(l[e], c4[e], b4[e], t + e, j0 + j, rule);
                             }
                             if (sizeof(T) == 4) {
 #pragma unroll
@@ -243,16 +269,18 @@ __global__ void __launch_bounds__(NT) logit_rules_kernel(dflash_logits_args a, P
                             }
                         }
                     }
-                    *reinterpret_cast<uint4*>(Y + j * a.ld_out + (tid + i * NT) * G) = make_uint4(w[0], w[1], w[2], w[3]);
+                    *reinterpret_cast<uint4*>(Y + j * a.ld_out + h + (tid + i * NT) * G) = make_uint4(w[0], w[1], w[2], w[3]);
                 }
         }
     }
 
-    // ---- single tokens: the last vocab % G of them, or everything when rows are not aligned
-    const int from = nvec * G, left = (n - from) * rows;
-#pragma unroll 4
+    // ---- single tokens: those of a row before its first vector and behind its last (SINGLE: all)
+    const int slots = LIE == ALIGNED ? n % G : LIE == SHIFTED ? 2 * G : n, left = slots * rows;
+#pragma unroll (LIE == SINGLE ? 4 : 1)
     for (int i = tid; i < left; i += NT) {
-        const int j = i / (n - from), t = from + i - j * (n - from);
+        const int j = i / slots, k = i - j * slots, h = head(j);
+        const int t = k < h ? k : k + vecs(j) * G;
+        if (t >= n) continue;
         const int m = midx[j];
         const bool on = m < 0 || (a.masks[(long long)m * a.ld_mask + ((c0 + t) >> 5)] >> ((c0 + t) & 31) & 1u);
         const bool touched = rules && flag[t / G];
@@ -272,19 +300,20 @@ void run(const Launch& L, const dflash_logits_args& a) {
     pl.chunk = NT * NV * 16 / (int)sizeof(T);
     const int chunks = (a.vocab + pl.chunk - 1) / pl.chunk;
     // few CTAs (short batch): the rows of a sequence go to several, each of which reads the history again; 608 CTAs, four
-    // an SM (16 rows of 151936 behind up to 8448 tokens: 11.3 us with 304, 10.3 with 608, 11.5 with 1216)
+    // an SM (16 rows of 151936 behind up to 8448 tokens: 11.3 us with 304, 10.3 with 608, 11.5 with 1216, one vector a thread)
     pl.groups = (int)std::min<long long>(a.rows_per_seq, std::max(1ll, 608ll / ((long long)chunks * a.batch)));
     pl.rows = (a.rows_per_seq + pl.groups - 1) / pl.groups;
     pl.groups = (a.rows_per_seq + pl.rows - 1) / pl.rows;
-    const bool vec = (((uintptr_t)a.logits | (uintptr_t)a.out) % 16) == 0 && a.ld_logits % (16 / (int)sizeof(T)) == 0 &&
-                     a.ld_out % (16 / (int)sizeof(T)) == 0;
+    const long long g = 16 / (int)sizeof(T);
+    const bool base = ((uintptr_t)a.logits - (uintptr_t)a.out) % 16 == 0 && (a.ld_logits - a.ld_out) % g == 0;
+    const Lie lie = base && (uintptr_t)a.logits % 16 == 0 && a.ld_logits % g == 0 ? ALIGNED : base ? SHIFTED : SINGLE;
     const size_t smem = a.bias_ids ? (size_t)pl.chunk * 4 : 0;
-    launch_k(L, vec ? logit_rules_kernel<T, NV, true> : logit_rules_kernel<T, NV, false>,
+    launch_k(L, lie == ALIGNED ? logit_rules_kernel<T, NV, ALIGNED> : lie == SHIFTED ? logit_rules_kernel<T, NV, SHIFTED> : logit_rules_kernel<T, NV, SINGLE>,
              dim3(chunks, (unsigned)(a.batch * pl.groups)), dim3(NT), smem, 1, a, pl);
 }
 
-// Vectors per thread: two (512 rows of 151936: 109 us, with one 123; 64 bf16 rows of 128256: 20 and 27 us), unless the
-// rows, split one a CTA, would leave fewer than two CTAs an SM (one row of 151936: 3.6 us with two, 3.3 with one).
+// Vectors per thread: two (512 rows of 151936: 111 us, with one 123; 64 bf16 rows of 128256: 20 and 23 us), unless the
+// rows, split one a CTA, would leave fewer than two CTAs an SM (one row of 151936: 3.6 us with two, 3.4 with one).
 template <typename T>
 void run(const Launch& L, const dflash_logits_args& a) {
     const int chunk2 = NT * 2 * 16 / (int)sizeof(T);

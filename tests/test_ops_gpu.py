@@ -478,6 +478,30 @@ def test_process_logits_strides(dtype):
     assert torch.equal(src[:, 1003:].cpu(), x[:, 1003:])
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("at,to,ld,ld_out", [(0, 0, 6151, 6151), (1, 1, 6152, 6152), (3, 3, 6157, 6165), (5, 5, 6150, 6150),
+                                             (2, 0, 6152, 6152), (0, 0, 6151, 6153), (7, 7, 6145, 6145)])
+def test_process_logits_wherever_rows_begin(dtype, at, to, ld, ld_out):
+    """Logits and out begin `at` and `to` elements behind a 16-byte boundary, with any row stride; everything around
+    the rows is left alone, and a row in place only where the rules change it."""
+    rows, vocab = 4, 6145
+    x, kw = rules_case(dtype, 2, rows, vocab, seed=at + ld, hist=60, n_bias=30, n_masks=3)
+    buf = torch.full((8 * max(ld, ld_out) + 16,), 7.0, dtype=x.dtype, device="cuda")
+    src = buf[at:at + 8 * ld].view(8, ld)[:, :vocab]
+    src.copy_(x)
+    dst_buf = torch.full_like(buf, 3.0)
+    dst = dst_buf[to:to + 8 * ld_out].view(8, ld_out)[:, :vocab]
+    d = rules_dev(kw)
+    rules_check(dtype, x, kw, rows, dfl().process_logits(src, rows_per_seq=rows, out=dst, **d))
+    around = torch.ones_like(dst_buf, dtype=torch.bool)
+    around[to:to + 8 * ld_out].view(8, ld_out)[:, :vocab] = False
+    assert (dst_buf[around] == 3.0).all()
+    rules_check(dtype, x, kw, rows, dfl().process_logits(src, rows_per_seq=rows, out=src, **d))
+    around[:] = True
+    around[at:at + 8 * ld].view(8, ld)[:, :vocab] = False
+    assert (buf[around] == 7.0).all()
+
+
 def test_process_logits_special_values():
     """Infinities and NaN pass through the rules as IEEE arithmetic has it; a mask covers them."""
     x = torch.tensor([[float("nan"), float("inf"), float("-inf"), float("nan"), float("inf"), -0.0, 0.0, 1.0]])
