@@ -229,6 +229,16 @@ __global__ void __launch_bounds__(NTHR, 1)
         tmem_alloc(&bars->tmem, 512);
         tmem_relinquish();
     }
+    if (warp == 9) {  // (a barrier of each ring per lane)
+#pragma unroll 1
+        for (int i = 0; i < 4; ++i) {
+            LineBars* B = &bars->line[i >> 1];
+            mbar_init(&B->done[i & 1][lane], 1);
+            mbar_init(&B->kv_full[i & 1][lane], i < 2 ? 2 : 1);  // load warps that fill the batch
+        }
+        mbar_fence_init();
+    }
+    static_assert(DONE == 32, "a lane each");
     if (tid == 0) {
         for (int line = 0; line < 2; ++line) {
             LineBars* B = &bars->line[line];
@@ -236,10 +246,6 @@ __global__ void __launch_bounds__(NTHR, 1)
                 mbar_init(&B->q_full[x], 1);
                 mbar_init(&B->q_empty[x], 1);
                 for (int b = 0; b < 2; ++b) mbar_init(&B->p_full[x][b], 4);
-                for (int b = 0; b < DONE; ++b) {
-                    mbar_init(&B->done[x][b], 1);
-                    mbar_init(&B->kv_full[x][b], line == 0 ? 2 : 1);  // load warps that fill the batch
-                }
                 mbar_init(&B->o_empty[x], 4);
                 mbar_init(&B->drain[x], 1);
                 for (int i = 0; i < SEGS; ++i) {
@@ -340,6 +346,18 @@ __global__ void __launch_bounds__(NTHR, 1)
                                     p < 0 ? oob : (p * P.Hkv + kvh) * 64, 0);
                 }
             };
+            auto load_q = [&]() {
+                if (lane || rx != x) return;
+#pragma unroll 1
+                for (int y = x; y < (pair ? 2 : x + 1); ++y) {
+                    if (!wait(&B->q_empty[y], (nseg & 1) ^ 1)) break;
+                    mbar_arrive_expect_tx(&B->q_full[y], C::HALVES * 128 * P.g * P.RH);
+#pragma unroll
+                    for (int c = 0; c < C::HALVES; ++c)
+                        tma_load_3d(q_at + y * C::Q_TILE + c * C::Q_REG, &mq, &B->q_full[y], 64 * c, kvh * P.g,
+                                    row0 + (pair ? y * P.RH : 0));
+                }
+            };
 #pragma unroll 1
             for (int j = -2; j < n; ++j) {
                 // batch: V of tile j, K of tile j + 2
@@ -351,6 +369,7 @@ __global__ void __launch_bounds__(NTHR, 1)
                     if (my_v || my_k) mbar_arrive_expect_tx(bar, (my_v + my_k) * C::TILE);
                     else mbar_arrive(bar);  // (a batch without my tiles has its phase too)
                 }
+                if (j == -2 && nseg == 0) load_q();  // (nothing before them: while the page numbers come)
                 if (my_v) tile(1, j, i);
                 if (my_k) tile(0, j + 2, i);
                 if (lane == 0) {
@@ -358,17 +377,8 @@ __global__ void __launch_bounds__(NTHR, 1)
                     if (has_k) rel[first_stage(x) + stage_of(ring + k_seq(j + 2))] = i;
                 }
                 armed = i + 1;
-                if (j == -2 && lane == 0 && rx == x) {
-                    // the queries: behind the first tile, whose stage waits for the segment before alone
-                    for (int y = x; y < (pair ? 2 : x + 1); ++y) {
-                        if (!wait(&B->q_empty[y], (nseg & 1) ^ 1)) break;
-                        mbar_arrive_expect_tx(&B->q_full[y], C::HALVES * 128 * P.g * P.RH);
-#pragma unroll
-                        for (int c = 0; c < C::HALVES; ++c)
-                            tma_load_3d(q_at + y * C::Q_TILE + c * C::Q_REG, &mq, &B->q_full[y], 64 * c, kvh * P.g,
-                                        row0 + (pair ? y * P.RH : 0));
-                    }
-                }
+                // (behind the first tile, whose stage waits for the segment before alone)
+                if (j == -2 && nseg > 0) load_q();
                 wait.ok = __shfl_sync(0xffffffffu, (int)wait.ok, 0);
                 if (!wait.ok) break;
             }

@@ -201,7 +201,8 @@ struct Walk {
 
 // Scan of the batch by every thread of the CTA (NTHR threads, all call it): fills base ([2][MAX_BATCH]:
 // per line, the exclusive sums of the own items' lengths, from the prefix items' end), ibase ([batch]: of
-// the counts on the sequence's line) and the head.  Ends with a barrier.
+// the counts on the sequence's line) and the head.  Ends with a barrier.  (Up to 32 sequences without one in
+// between: the plan is 2 us of a small call's chain, most of it code that comes from L2.)
 template <int NTHR>
 struct PlanMem {
     uint32_t ws[NTHR / 32][4];
@@ -211,46 +212,53 @@ struct PlanMem {
 template <int NTHR>
 __device__ __forceinline__ void make_plan(const Shape& P, uint32_t* base, uint32_t* ibase, PlanMem<NTHR>* m, Head& h) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    if (tid == 0) {
-        m->bad = m->max_m = 0;
-        m->sum[0] = m->sum[1] = 0;
-    }
-    h.r_begin = P.q_start[0];
-    h.r_end = P.q_start[P.batch];
     int bad = 0;
-    if (h.r_begin < 0 || h.r_end < h.r_begin || h.r_end > P.rows) {
-        bad = 1;
-        h.r_begin = h.r_end = 0;
-    }
-    const int live = h.r_end - h.r_begin;
-    h.pl = live > P.RH && !P.one_line ? 0 : 1;
-    h.nqt = cdiv(live, P.row_tile(h.pl));
-    h.n_prefix = P.npt ? h.nqt * P.Hkv : 0;
-    const unsigned long long cp = (unsigned long long)h.n_prefix * (unsigned)(P.lead[h.pl] + P.npt);
-    h.CP = (uint32_t)cp;
-    uint32_t carry[4] = {h.pl == 0 ? h.CP : 0u, h.pl == 1 ? h.CP : 0u, 0u, 0u};  // lengths, item counts
-    __syncthreads();
-    if (tid == 0) atomicAdd(&m->sum[h.pl], cp);
-#pragma unroll 1
-    for (int s0 = 0; s0 < P.batch; s0 += NTHR) {
-        const int s = s0 + tid;
-        uint32_t v[4] = {0u, 0u, 0u, 0u};
-        int line = 0;
-        if (s < P.batch) {
-            const int a = P.q_start[s], b = P.q_start[s + 1];
-            if (a < 0 || b < a || b > P.rows) {
-                bad = 1;
-            } else {
-                const Seq q = seq_of(P, a, b, P.kv_lens[s]);
-                line = q.line;
-                const uint32_t items = (uint32_t)(q.groups * P.Hkv), per = (uint32_t)(P.lead[line] + q.tiles);
-                if (items) atomicAdd(&m->sum[line], (unsigned long long)items * per);
-                atomicMax(&m->max_m, q.m);
-                v[line] = items * per;
-                v[2 + line] = items;
-            }
+    auto rows_ok = [&](int a, int b) { return a >= 0 && b >= a && b <= P.rows; };
+    auto prefix = [&]() -> unsigned long long {  // the prefix items, from r_begin and r_end
+        if (!rows_ok(h.r_begin, h.r_end)) {
+            bad = 1;
+            h.r_begin = h.r_end = 0;
         }
-        uint32_t own[4] = {v[0], v[1], v[2], v[3]};
+        const int live = h.r_end - h.r_begin;
+        h.pl = live > P.RH && !P.one_line ? 0 : 1;
+        h.nqt = cdiv(live, P.row_tile(h.pl));
+        h.n_prefix = P.npt ? h.nqt * P.Hkv : 0;
+        const unsigned long long cp = (unsigned long long)h.n_prefix * (unsigned)(P.lead[h.pl] + P.npt);
+        h.CP = (uint32_t)cp;
+        return cp;
+    };
+    // a sequence's own items: their line, number and length
+    auto own_items = [&](int a, int b, int kv, int& line, uint32_t& items) -> unsigned long long {
+        const Seq q = seq_of(P, a, b, kv);
+        line = q.line;
+        items = (uint32_t)(q.groups * P.Hkv);
+        return (unsigned long long)items * (uint32_t)(P.lead[line] + q.tiles);
+    };
+    uint32_t total[4];  // per line: length, own items
+    if (P.batch <= 32) {
+        // every warp scans the whole batch, a sequence a lane: one round of loads and one barrier
+        const int a = P.q_start[min(lane, P.batch)], b = P.q_start[min(lane + 1, P.batch)];
+        const int kv = lane < P.batch ? P.kv_lens[lane] : 0;
+        h.r_begin = __shfl_sync(0xffffffffu, a, 0);
+        h.r_end = __shfl_sync(0xffffffffu, b, 31);
+        const unsigned long long cp = prefix();
+        int line = 0, len31 = cp >> 31 != 0, m_own = 0;
+        uint32_t items = 0, len = 0;
+        if (rows_ok(a, b)) {
+            const unsigned long long l = own_items(a, b, kv, line, items);
+            len31 |= l >> 31 != 0;
+            len = (uint32_t)l;
+            m_own = b - a;
+        } else {
+            bad = 1;
+        }
+        // (per line, in units of 256: 2^31 is past what is left of 32 bits)
+        const uint32_t sum0 = __reduce_add_sync(0xffffffffu, (line == 0 ? len >> 8 : 0u) + (lane == 0 && h.pl == 0 ? h.CP >> 8 : 0u));
+        const uint32_t sum1 = __reduce_add_sync(0xffffffffu, (line == 1 ? len >> 8 : 0u) + (lane == 0 && h.pl == 1 ? h.CP >> 8 : 0u));
+        h.bad = __any_sync(0xffffffffu, bad | len31) || sum0 >> 23 || sum1 >> 23;
+        h.max_m = __reduce_max_sync(0xffffffffu, m_own);
+        uint32_t v[4] = {line ? 0u : len, line ? len : 0u, line ? 0u : items, line ? items : 0u};
+        const uint32_t own[4] = {v[0], v[1], v[2], v[3]};
 #pragma unroll 1
         for (int o = 1; o < 32; o <<= 1)
 #pragma unroll
@@ -258,40 +266,97 @@ __device__ __forceinline__ void make_plan(const Shape& P, uint32_t* base, uint32
                 const uint32_t y = __shfl_up_sync(0xffffffffu, v[i], o);
                 if (lane >= o) v[i] += y;
             }
-        if (lane == 31)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) m->ws[warp][i] = v[i];
-        __syncthreads();
-#pragma unroll
-        for (int i = 0; i < 4; ++i) v[i] -= own[i];
-#pragma unroll 1
-        for (int w = 0; w < NTHR / 32; ++w)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                if (w == warp) v[i] += carry[i];
-                carry[i] += m->ws[w][i];
-            }
-        if (s < P.batch) {
-            base[s] = v[0];
-            base[MAX_BATCH + s] = v[1];
-            ibase[s] = v[2 + line];
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t before = i == h.pl ? h.CP : 0u;
+            total[i] = __shfl_sync(0xffffffffu, v[i], 31) + before;
+            v[i] += before - own[i];
         }
+        if (warp == 0 && lane < P.batch) {
+            base[lane] = v[0];
+            base[MAX_BATCH + lane] = v[1];
+            ibase[lane] = line ? v[3] : v[2];
+        }
+    } else {
+        if (tid == 0) {
+            m->bad = m->max_m = 0;
+            m->sum[0] = m->sum[1] = 0;
+        }
+        h.r_begin = P.q_start[0];
+        h.r_end = P.q_start[P.batch];
+        const unsigned long long cp = prefix();
+        total[0] = h.pl == 0 ? h.CP : 0u;
+        total[1] = h.pl == 1 ? h.CP : 0u;
+        total[2] = total[3] = 0u;
         __syncthreads();
+        if (tid == 0) atomicAdd(&m->sum[h.pl], cp);
+#pragma unroll 1
+        for (int s0 = 0; s0 < P.batch; s0 += NTHR) {
+            const int s = s0 + tid;
+            uint32_t v[4] = {0u, 0u, 0u, 0u};
+            int line = 0;
+            if (s < P.batch) {
+                const int a = P.q_start[s], b = P.q_start[s + 1];
+                if (!rows_ok(a, b)) {
+                    bad = 1;
+                } else {
+                    uint32_t items;
+                    const unsigned long long l = own_items(a, b, P.kv_lens[s], line, items);
+                    if (items) atomicAdd(&m->sum[line], l);
+                    atomicMax(&m->max_m, b - a);
+                    if (line) {
+                        v[1] = (uint32_t)l;
+                        v[3] = items;
+                    } else {
+                        v[0] = (uint32_t)l;
+                        v[2] = items;
+                    }
+                }
+            }
+            uint32_t own[4] = {v[0], v[1], v[2], v[3]};
+#pragma unroll 1
+            for (int o = 1; o < 32; o <<= 1)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const uint32_t y = __shfl_up_sync(0xffffffffu, v[i], o);
+                    if (lane >= o) v[i] += y;
+                }
+            if (lane == 31)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) m->ws[warp][i] = v[i];
+            __syncthreads();
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[i] -= own[i];
+#pragma unroll 1
+            for (int w = 0; w < NTHR / 32; ++w)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    if (w == warp) v[i] += total[i];
+                    total[i] += m->ws[w][i];
+                }
+            if (s < P.batch) {
+                base[s] = v[0];
+                base[MAX_BATCH + s] = v[1];
+                ibase[s] = line ? v[3] : v[2];
+            }
+            __syncthreads();
+        }
+        if (bad) m->bad = 1;
+        __syncthreads();
+        h.bad = m->bad || m->sum[0] >> 31 || m->sum[1] >> 31;
+        h.max_m = m->max_m;
     }
-    if (bad) m->bad = 1;
-    __syncthreads();
-    h.bad = m->bad || m->sum[0] >> 31 || m->sum[1] >> 31;
-    h.max_m = m->max_m;
-    h.W[0] = h.bad ? 0u : carry[0];
-    h.W[1] = h.bad ? 0u : carry[1];
+    h.W[0] = h.bad ? 0u : total[0];
+    h.W[1] = h.bad ? 0u : total[1];
+    h.items0 = total[2] + (h.pl == 0 ? (uint32_t)h.n_prefix : 0u);
     // CTAs by the lines' work: a tile of line 1 takes a CTA 0.55 of the time of one of line 0 (at 0.48 / 0.55 / 0.62 the
     // verify blocks of 32 x 16 rows behind 8192 keys take 109 / 101 / 103 us; with every CTA on both lines in turn 116)
-    const long long c0 = 100ll * h.W[0], c1 = 55ll * h.W[1];
-    h.n1 = c0 == 0 ? P.n_cta : c1 == 0 ? 0 : min(max((int)((P.n_cta * c1 + (c0 + c1) / 2) / (c0 + c1)), 1), P.n_cta - 1);
+    const float c0 = (float)h.W[0], c1 = 0.55f * (float)h.W[1];
+    h.n1 = h.W[0] == 0 ? P.n_cta : h.W[1] == 0 ? 0 : min(max(__float2int_rn(P.n_cta * (c1 / (c0 + c1))), 1), P.n_cta - 1);
     const uint32_t w0 = max(P.n_cta - h.n1, 1), w1 = max(2 * h.n1, 1);
     h.part[0] = max(1u, (h.W[0] + w0 - 1) / w0);
     h.part[1] = max(1u, (h.W[1] + w1 - 1) / w1);
-    h.items0 = carry[2] + (h.pl == 0 ? (uint32_t)h.n_prefix : 0u);
+    __syncthreads();
 }
 
 // The blocks of a row's item on its line: first unit `at`, number `id`, n_eff tiles seen, place rl in it.
