@@ -22,8 +22,8 @@ namespace {
 // hold the row's query vectors, prefix and own, in plan order (one fixed order: the same bits every run).
 // A warp takes one row and one KV head, whose blocks the main kernel has written down (Dir); lanes take 8
 // head dimensions of one query vector each (whole 32-byte sectors) and stream the segments through, four in
-// flight.  NW > 1: the warps of a CTA share one (row, KV head), each taking every NW-th segment, for calls of
-// few rows (whose prefix is split the most).  Bytes: 4 hd + 8 per vector and segment, from L2; a small call
+// flight.  NW > 1: the warps of a CTA share one (row, KV head), by elements and by segments, for calls of few rows
+// (whose prefix is split the most).  Bytes: 4 hd + 8 per vector and segment, from L2; a small call
 // waits for its chain of loads and, as much, for the code itself to come from L2 (hence rolled loops).  Consecutive
 // lanes take the heads of a row, then the next 8 dimensions: a load of 32 lanes then takes whole 128-byte lines of
 // the partials (32 prompts of 5 .. 130 rows: the call 127 -> 121 us).  Measured under a profiler: 12 us for 512 rows of
@@ -85,20 +85,23 @@ __global__ void __launch_bounds__(32 * MWARPS, 3) merge_kernel(MergeArgs a) {
     const bool late = __any_sync(0xffffffffu, err != 0), bad = late || d.pre_count == -2;
     if (late && a.report && lane == 0) atomicOr(a.report, ERR_TIMEOUT);
     const int count = bad ? 0 : d.pre_count + d.own_count;
-    const int w0 = NW > 1 ? warp : 0;
     const int chunks = P.hd / 8, elems = P.g * chunks;
+    // NW > 1: warp = (w0, we) takes every `splits`-th segment, from w0 on, of one 32-lane share of the elements
+    const int shares = NW > 1 ? min(cdiv(elems, 32), NW) : 1, splits = NW > 1 ? NW / shares : 1;
+    const int w0 = NW > 1 ? warp / shares : 0, we = NW > 1 ? warp - w0 * shares : 0;
 #pragma unroll 1
-    for (int e0 = 0; e0 < elems; e0 += 32) {
+    for (int eb = 0; eb < elems; eb += 32 * shares) {
+        const int e0 = eb + 32 * we;
         const int e = min(e0 + lane, elems - 1), c8 = e / P.g, hh = e - c8 * P.g;
         Part acc;
         uint32_t bb = 0;
 #pragma unroll 1
-        for (int k0 = w0; k0 < count; k0 += 4 * NW) {
+        for (int k0 = w0; k0 < (w0 < splits ? count : 0); k0 += 4 * splits) {
             float2 ml[4];
             float4 x[4], y[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const int k = k0 + i * NW;
+                const int k = k0 + i * splits;
                 ml[i] = make_float2(-INFINITY, 0.f);
                 x[i] = y[i] = make_float4(0.f, 0.f, 0.f, 0.f);
                 if (k < count) {
@@ -117,12 +120,12 @@ __global__ void __launch_bounds__(32 * MWARPS, 3) merge_kernel(MergeArgs a) {
         }
         if (bb) acc.M = NAN;  // (a NaN maximum makes the whole row NaN below)
         if (NW > 1) {
-            part_s[w0][lane] = acc;
+            part_s[warp][lane] = acc;
             __syncthreads();
             if (w0 == 0)
 #pragma unroll 1
-                for (int q = 1; q < NW; ++q) {
-                    const Part p = part_s[q][lane];
+                for (int q = 1; q < splits; ++q) {
+                    const Part p = part_s[warp + q * shares][lane];
                     if (isnan(p.M) || isnan(acc.M)) acc.M = NAN;
                     else
                         acc.join(p.M, p.l, make_float4(p.o[0], p.o[1], p.o[2], p.o[3]),
