@@ -20,9 +20,9 @@ namespace {
 
 // Merge of the partial results: out = sum_i 2^(m_i - M) o_i / sum_i 2^(m_i - M) l_i over the segments that
 // hold the row's query vectors, prefix and own, in plan order (one fixed order: the same bits every run).
-// A warp takes one row and one KV head, whose blocks the main kernel has written down (Dir); lanes take 8
-// head dimensions of one query vector each (whole 32-byte sectors) and stream the segments through, four in
-// flight.  NW > 1: the warps of a CTA share one (row, KV head), by elements and by segments, for calls of few rows
+// A warp takes one row and one KV head (or 32 elements of them), whose blocks the main kernel has written down
+// (Dir); lanes take 8 head dimensions of one query vector each (whole 32-byte sectors) and stream the segments through,
+// four in flight.  NW > 1: the warps of a CTA share one (row, KV head), by elements and by segments, for calls of few rows
 // (whose prefix is split the most).  Bytes: 4 hd + 8 per vector and segment, from L2; a small call
 // waits for its chain of loads and, as much, for the code itself to come from L2 (hence rolled loops).  Consecutive
 // lanes take the heads of a row, then the next 8 dimensions: a load of 32 lanes then takes whole 128-byte lines of
@@ -35,6 +35,7 @@ struct MergeArgs {
     float* lse;
     long long ld_out;
     uint32_t* report;  // the session's error word, or null
+    int warps;         // NW == 1: warps per (row, KV head), by elements
 };
 
 constexpr int MWARPS = 8;
@@ -71,7 +72,8 @@ __global__ void __launch_bounds__(32 * MWARPS, 3) merge_kernel(MergeArgs a) {
     using namespace sp;
     const Shape& P = a.P;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int r = NW > 1 ? blockIdx.x : blockIdx.x * MWARPS + warp, kvh = blockIdx.y;
+    const int unit = blockIdx.x * MWARPS + warp;
+    const int r = NW > 1 ? blockIdx.x : unit / a.warps, kvh = blockIdx.y;
     __shared__ Part part_s[NW > 1 ? NW : 1][32];
     if (r >= P.rows) return;  // (NW > 1: the whole CTA)
     pdl_wait();
@@ -86,12 +88,14 @@ __global__ void __launch_bounds__(32 * MWARPS, 3) merge_kernel(MergeArgs a) {
     if (late && a.report && lane == 0) atomicOr(a.report, ERR_TIMEOUT);
     const int count = bad ? 0 : d.pre_count + d.own_count;
     const int chunks = P.hd / 8, elems = P.g * chunks;
-    // NW > 1: warp = (w0, we) takes every `splits`-th segment, from w0 on, of one 32-lane share of the elements
-    const int shares = NW > 1 ? min(cdiv(elems, 32), NW) : 1, splits = NW > 1 ? NW / shares : 1;
-    const int w0 = NW > 1 ? warp / shares : 0, we = NW > 1 ? warp - w0 * shares : 0;
+    // Warp we of `shares` takes every shares-th 32 elements; NW > 1: of the CTA's warps, warp w0 of each such group every
+    // splits-th segment from w0 on.
+    const int shares = NW > 1 ? min(cdiv(elems, 32), NW) : a.warps, splits = NW > 1 ? NW / shares : 1;
+    const int w0 = NW > 1 ? warp / shares : 0, we = NW > 1 ? warp - w0 * shares : unit - r * a.warps;
 #pragma unroll 1
     for (int eb = 0; eb < elems; eb += 32 * shares) {
         const int e0 = eb + 32 * we;
+        if (NW == 1 && e0 >= elems) break;
         const int e = min(e0 + lane, elems - 1), c8 = e / P.g, hh = e - c8 * P.g;
         Part acc;
         uint32_t bb = 0;
@@ -186,9 +190,19 @@ void merge(const Launch& L, const MergeArgs& m) {
     Launch after = L;
     after.pdl = true;
     // Rows of one stream: the prefix is split over nearly every worker of its line, else over a few.  (One token of four
-    // sequences behind 512 keys: 13.2 us with eight warps, 15.1 with one; verify blocks 32 x 16: 128 and 98 us.)
-    if (m.P.rows <= m.P.RH) launch_k(after, merge_kernel<T, MWARPS>, dim3(m.P.rows, m.P.Hkv), dim3(32 * MWARPS), 0, 1, m);
-    else launch_k(after, merge_kernel<T, 1>, dim3((m.P.rows + MWARPS - 1) / MWARPS, m.P.Hkv), dim3(32 * MWARPS), 0, 1, m);
+    // sequences behind 512 keys: 10.3 us with eight warps, 11.0 with a warp per 32 elements, fp32 blocks of four 9.8 and
+    // 12.0; verify blocks 32 x 16: 110 and 95 us.)
+    if (m.P.rows <= m.P.RH) {
+        launch_k(after, merge_kernel<T, MWARPS>, dim3(m.P.rows, m.P.Hkv), dim3(32 * MWARPS), 0, 1, m);
+        return;
+    }
+    // A warp per 32 elements while that is at most seven CTAs an SM, else one per (row, KV head).  (Blocks of 16 of 8
+    // sequences behind 1000 keys: 17.0 and 19.4 us; 32 prompts of 5 .. 130 rows behind 2100: 114.4 and 111.0.)
+    MergeArgs a = m;
+    const int shares = (m.P.g * m.P.hd / 8 + 31) / 32;
+    auto ctas = [&](int w) { return (int)(((long long)m.P.rows * w + MWARPS - 1) / MWARPS); };
+    if ((long long)ctas(shares) * m.P.Hkv <= 7 * CTAS) a.warps = shares;
+    launch_k(after, merge_kernel<T, 1>, dim3(ctas(a.warps), m.P.Hkv), dim3(32 * MWARPS), 0, 1, a);
 }
 
 }  // namespace
@@ -213,6 +227,7 @@ bool shared_prefix_attention(const Launch& L, const dflash_shared_prefix_args& a
     m.lse = a.lse;
     m.ld_out = a.ld_out;
     m.report = L.err;
+    m.warps = 1;
     if (!(f32 ? shared_attention_f32(L, P, m.W, a) : shared_attention_tc(L, P, m.W, a))) return false;
     if (f32) merge<float>(L, m);
     else merge<bf16>(L, m);
