@@ -35,17 +35,18 @@
 //
 // What bounds it.  Tensor cores: 64 keys of both streams are 1260 cycles (S is fed
 // from shared memory at 48 cycles an M128 N64 K16 product, P V takes 64).  Measured
-// on line 0: 1780 cycles, 1190 TFLOP/s (32 x 16 rows of 32 heads against 32768 keys:
-// 230 us with the merge).  That is the chain of a softmax warp, which has one tile at
+// on line 0: 1780 cycles, 1200 TFLOP/s (32 x 16 rows of 32 heads against 32768 keys:
+// 228 us with the merge).  That is the chain of a softmax warp, which has one tile at
 // a time: wait 190 cycles, scores out of TMEM 310, maximum 270, exponentials 660 (two
 // warps share a scheduler's unit), P into TMEM 185, hand-over 140, loop.  Measured and
 // not kept: two warps per 32 rows, half of the keys each (279 us where this took 241);
 // the streams' products in turn, half a tile apart (288: one stream's products alone
 // wait for their own accumulator, 69 cycles each); the next scores loaded while P is
 // stored (267); hand-over by a flag in shared memory (243).
-// Line 1 is bound by bytes: 5.9 TB/s of K and V on 8192 own keys of 32 sequences.  The
-// small calls are a chain: lengths, plan, pages, first tile, partial result, merge
-// (13.2 us for one token of four sequences behind 512 keys).
+// Line 1 is bound by bytes: 6.3 TB/s of K and V on 8192 own keys of 32 sequences.  The
+// small calls are a chain: lengths, plan (2200 cycles), pages, first tile (4500), its
+// softmax and product (1900), partial result, merge (10.3 us for one token of four
+// sequences behind 512 keys).
 //
 // Every wait is bounded; one that runs out sets the CTA's error word (the merge
 // writes NaN), every role leaves, copies in flight are awaited (bounded).

@@ -8,17 +8,18 @@
 // sequence.  It first turns the sequence's history and biases into one or two
 // words per token of its chunk in shared memory (counts by integer atomics, so the
 // order is immaterial): the history is read once per chunk instead of once per
-// row, from L2.  Then 16-byte vectors stream by, a row ahead of the stores, with
-// the mask words of the row after that under way, so no load waits for another; a
-// vector that its mask closes entirely is not read, and a flag byte per vector says
-// whether its words are looked up at all.  (Collecting the touched tokens in a list
+// row, from L2.  Then 16-byte vectors stream by, a row ahead of the stores (copied
+// asynchronously into shared memory, each thread its own), with the mask words of
+// the row after that under way, so no load waits for another; a vector that its
+// mask closes entirely is not read, and a flag byte per vector says whether its
+// words are looked up at all.  (Collecting the touched tokens in a list
 // for a pass of their own took 147 us where this takes 110 us at 512 rows of 151936: frequent ids sit
 // together, so the CTAs of the first chunk had nearly all of that pass to do.)
 // Drafts stay a list of at most 31 ids: a token that is a draft carries a bit, and
 // only such tokens count the drafts before their row.
-// Measured (graph replay): 111 us for 512 rows of 151936 in fp32 (5.6 TB/s of the bytes above, 82 % of a measured copy;
-// 125 us for rows of 151937, 261 us token by token); 20 us for 64 bf16 rows of 128256 and 8.5 us for 16 rows of one
-// sequence behind up to 8448 tokens, where the lists' chain of loads counts; 3.4 us for a single row.
+// Measured (graph replay): 107 us for 512 rows of 151936 in fp32 (5.8 TB/s of the bytes above, 86 % of a measured copy;
+// 122 us for rows of 151937, 261 us token by token); 18 us for 64 bf16 rows of 128256 and 9.6 us for 16 rows of one
+// sequence behind up to 8448 tokens, where the lists' chain of loads counts; 3.5 us for a single row.
 #include <math.h>
 
 #include <algorithm>
@@ -29,7 +30,7 @@ namespace dfl {
 
 namespace {
 
-constexpr int NT = 256;
+constexpr int NT = 256, DEPTH = 2;
 constexpr uint32_t IN_PROMPT = 0x80000000u, IS_DRAFT = 0x40000000u, COUNT = 0x3FFFFFFFu;
 
 // A sequence's penalties; x / repetition is x times the reciprocal (one rounding more).
@@ -48,6 +49,10 @@ __device__ __forceinline__ float apply(float x, uint32_t w, int b, int t, int j,
     if (c) x = x - r.freq * (float)c - r.pres;
     if (b) x += r.bias[b - 1];
     return x;
+}
+
+__device__ __forceinline__ void cp16(void* dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(src) : "memory");
 }
 
 struct Plan {
@@ -88,8 +93,10 @@ __global__ void __launch_bounds__(NT) logit_rules_kernel(dflash_logits_args a, P
     const int mis0 = (int)((uintptr_t)X / sizeof(T)) & (G - 1), mis_ld = (int)a.ld_logits & (G - 1);
     auto head = [&](int j) { return LIE == SHIFTED ? -(mis0 + j * mis_ld) & (G - 1) : 0; };
     auto vecs = [&](int j) { return LIE == SINGLE ? 0 : max(n - head(j), 0) / G; };
-    uint32_t bits[NV], next[NV];  // mask bits of the row whose logits are loaded next, and of the row after
-    uint4 x[NV];
+    // Rows on their way: each thread's vectors of DEPTH rows in shared memory, its own alone (no barrier).  512 rows of
+    // 151936: 107 us with two rows, 112 with four, 166 with eight (fewer CTAs an SM); 112 with the row ahead in registers.
+    uint4* ring = reinterpret_cast<uint4*>(bias + (a.bias_ids ? CH : 0)) + tid;
+    uint32_t bits[DEPTH - 1][NV], next[NV];  // mask bits of the rows on their way, and of the row after them
     auto mask_bits = [&](int j, int m, uint32_t (&b)[NV]) {
         const int h = head(j);
 #pragma unroll
@@ -113,15 +120,22 @@ __global__ void __launch_bounds__(NT) logit_rules_kernel(dflash_logits_args a, P
         return v < vecs(j) && (!inplace || b != ALL || touched_vec(v, head(j)));
     };
     auto load = [&](int j, const uint32_t (&b)[NV]) {
+        if (j < rows)
 #pragma unroll
-        for (int i = 0; i < NV; ++i)
-            if (live(i, b[i], j) && b[i])
-                x[i] = *reinterpret_cast<const uint4*>(X + j * a.ld_logits + head(j) + (tid + i * NT) * G);
+            for (int i = 0; i < NV; ++i)
+                if (live(i, b[i], j) && b[i])
+                    cp16(ring + ((j & (DEPTH - 1)) * NV + i) * NT, X + j * a.ld_logits + head(j) + (tid + i * NT) * G);
+        asm volatile("cp.async.commit_group;" ::: "memory");
     };
     if (LIE != SINGLE) {
-        const int m = a.masks ? a.mask_index[row0] : -1;
-        mask_bits(0, m < a.n_masks ? m : -1, bits);
-        if (!inplace) load(0, bits);
+#pragma unroll
+        for (int r = 0; r < DEPTH - 1; ++r) {
+            const int m = a.masks && r < rows ? a.mask_index[row0 + r] : -1;
+            mask_bits(r, m < a.n_masks ? m : -1, bits[r]);
+        }
+        if (!inplace)
+#pragma unroll
+            for (int r = 0; r < DEPTH - 1; ++r) load(r, bits[r]);
     }
 
     // ---- the chunk's words: the first reads of the lists go out before the barrier
@@ -205,25 +219,29 @@ __global__ void __launch_bounds__(NT) logit_rules_kernel(dflash_logits_args a, P
 
     // ---- the stream
     if (LIE != SINGLE) {
-        load_mask(1, next);
-        if (inplace) load(0, bits);  // (which vectors change is known only now)
+        load_mask(DEPTH - 1, next);
+        if (inplace)  // (which vectors change is known only now)
+#pragma unroll
+            for (int r = 0; r < DEPTH - 1; ++r) load(r, bits[r]);
 #pragma unroll 1
         for (int j = 0; j < rows; ++j) {
-            uint4 y[NV];
+            load(j + DEPTH - 1, next);
             uint32_t b[NV];
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
-                y[i] = x[i];
-                b[i] = bits[i];
-                bits[i] = next[i];
+                b[i] = bits[0][i];
+#pragma unroll
+                for (int r = 0; r < DEPTH - 2; ++r) bits[r][i] = bits[r + 1][i];
+                bits[DEPTH - 2][i] = next[i];
             }
-            load_mask(j + 2, next);
-            if (j + 1 < rows) load(j + 1, bits);
+            load_mask(j + DEPTH, next);
+            asm volatile("cp.async.wait_group %0;" ::"n"(DEPTH - 1) : "memory");
 #pragma unroll
             for (int i = 0; i < NV; ++i)
                 if (live(i, b[i], j)) {
                     const int h = head(j);
-                    uint32_t w[4] = {y[i].x, y[i].y, y[i].z, y[i].w};
+                    const uint4 y = ring[((j & (DEPTH - 1)) * NV + i) * NT];
+                    uint32_t w[4] = {y.x, y.y, y.z, y.w};
                     const int v = tid + i * NT;
                     if (b[i] && touched_vec(v, h)) {
 #pragma unroll
@@ -307,13 +325,22 @@ void run(const Launch& L, const dflash_logits_args& a) {
     const long long g = 16 / (int)sizeof(T);
     const bool base = ((uintptr_t)a.logits - (uintptr_t)a.out) % 16 == 0 && (a.ld_logits - a.ld_out) % g == 0;
     const Lie lie = base && (uintptr_t)a.logits % 16 == 0 && a.ld_logits % g == 0 ? ALIGNED : base ? SHIFTED : SINGLE;
-    const size_t smem = a.bias_ids ? (size_t)pl.chunk * 4 : 0;
-    launch_k(L, lie == ALIGNED ? logit_rules_kernel<T, NV, ALIGNED> : lie == SHIFTED ? logit_rules_kernel<T, NV, SHIFTED> : logit_rules_kernel<T, NV, SINGLE>,
-             dim3(chunks, (unsigned)(a.batch * pl.groups)), dim3(NT), smem, 1, a, pl);
+    const size_t smem = (a.bias_ids ? (size_t)pl.chunk * 4 : 0) +
+                        (lie == SINGLE ? 0 : (size_t)std::min(pl.rows, DEPTH) * NV * NT * 16);
+    auto* k = lie == ALIGNED   ? logit_rules_kernel<T, NV, ALIGNED>
+              : lie == SHIFTED ? logit_rules_kernel<T, NV, SHIFTED>
+                               : logit_rules_kernel<T, NV, SINGLE>;
+    // (static shared memory: at most 17.2 KB of the 48 that need no leave)
+    if (smem > 30u << 10 && cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess) {
+        L.fail();
+        return;
+    }
+    launch_k(L, k, dim3(chunks, (unsigned)(a.batch * pl.groups)), dim3(NT), smem, 1, a, pl);
 }
 
-// Vectors per thread: two (512 rows of 151936: 111 us, with one 123; 64 bf16 rows of 128256: 20 and 23 us), unless the
-// rows, split one a CTA, would leave fewer than two CTAs an SM (one row of 151936: 3.6 us with two, 3.4 with one).
+// Vectors per thread: two (with a row ahead in registers, 512 rows of 151936 took 111 us, with one vector 123; 64 bf16
+// rows of 128256 20 and 23 us), unless the rows, split one a CTA, would leave fewer than two CTAs an SM (one row of
+// 151936: 3.6 us with two, 3.4 with one).
 template <typename T>
 void run(const Launch& L, const dflash_logits_args& a) {
     const int chunk2 = NT * 2 * 16 / (int)sizeof(T);
