@@ -2,18 +2,21 @@
 // dflash_shared_prefix_attention for F32; attention_shared.cu merges).
 //
 // The same plan as the bf16 kernel with one line of work (shared_plan.cuh): a
-// worker is a CTA of 128 threads with 32 query vectors, an item one KV head's
-// vectors of 32 / g rows, a tile 32 keys (half a page).  Per tile
-//   S = Q K^T   a thread has 2 vectors x 4 keys, 32 FMAs per 6 vector loads from
-//               shared memory;
+// worker is a CTA of 128 threads with 32 or 64 query vectors, an item one KV
+// head's vectors of that many / g rows, a tile 32 keys (half a page).  Per tile
+//   S = Q K^T   a thread has 2 or 4 vectors x 4 keys: 32 or 64 FMAs per 6 or 8
+//               vector loads from shared memory;
 //   softmax     online in fp32 (base 2); a vector's 32 scores lie in 8 lanes;
-//   O += P V    a thread has 2 vectors x hd / 8 dimensions.
+//   O += P V    a thread has 2 or 4 vectors x hd / 8 dimensions.
 // K and V of the next tile land (cp.async, double-buffered) meanwhile; keys behind
 // the list's end are filled with zeros, so what a page's unused slots hold never
 // matters.  Bound by the FMA pipes and shared memory for long work, by the chain
 // lengths -> pages -> tile for the short calls that fp32 models make: 9.8 us (merge
 // included, graph replay) for 3 blocks of 4 rows behind 500 keys, whose bytes take
-// 0.1 us; the tiles of a plain fp32 kernel without the plan took 184 us.
+// 0.1 us; the tiles of a plain fp32 kernel without the plan took 184 us.  64 vectors
+// a worker where the call has more than 32 per KV head: 16 rows of 8 sequences
+// behind 4096 keys take 226 us (39 TFLOP/s) at 32 heads of 128 and 68 us at 16 heads
+// of 64, with 32 vectors 339 and 116 us; a call that fits 32 would compute twice.
 #include <math.h>
 
 #include "shared_plan.cuh"
@@ -24,17 +27,17 @@ namespace {
 
 using namespace sp;
 
-constexpr int NT = 128, VT = 32, KT = 32;
+constexpr int NT = 128, KT = 32;
 
-template <int HD>
+template <int HD, int VT>
 struct Smem {
     static constexpr int LD = HD + 4;  // rows 16 bytes apart in the banks
     float q[VT][LD];
     float k[2][KT][LD];
     float v[2][KT][LD];
     float p[VT][KT + 4];
-    uint32_t base[2 * MAX_BATCH], ibase[MAX_BATCH];
     PlanMem<NT> plan;
+    uint32_t base[1];  // [2][batch], then ibase [batch]
 };
 
 struct F32Args {
@@ -50,25 +53,28 @@ __device__ __forceinline__ void cp16(float* dst, const float* src, bool full) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(d), "l"(src), "r"(full ? 16 : 0) : "memory");
 }
 
-template <int HD>
-__global__ void __launch_bounds__(NT) shared_f32_kernel(F32Args a) {
+// UV query vectors a thread.
+template <int HD, int UV>
+__global__ void __launch_bounds__(NT, 2) shared_f32_kernel(F32Args a) {
     extern __shared__ __align__(16) uint8_t raw[];
-    Smem<HD>& S = *reinterpret_cast<Smem<HD>*>(raw);
+    constexpr int VT = 16 * UV;
+    Smem<HD, VT>& S = *reinterpret_cast<Smem<HD, VT>*>(raw);
     constexpr int C4 = HD / 4, DPT = HD / 32;  // float4 per row; float4 of O per thread and vector
     const Shape& P = a.P;
     const int tid = threadIdx.x, lane = tid & 31, cta = blockIdx.x;
-    const int tv = tid >> 3, td = tid & 7;  // vectors 2 tv, 2 tv + 1; keys td + 8 i, dimensions 4 td + 32 i
+    const int tv = tid >> 3, td = tid & 7;  // vectors UV tv ..; keys td + 8 i, dimensions 4 td + 32 i
     pdl_wait();
     Head h;
-    make_plan<NT>(P, S.base, S.ibase, &S.plan, h);
+    uint32_t *base = S.base, *ibase = base + 2 * P.batch;
+    make_plan<NT>(P, base, ibase, &S.plan, h);
     if (cta < P.n_cta && tid == 0) a.W.err[cta] = 0u;
-    write_dir(P, h, a.W, S.base, S.ibase, (tid >> 5) * gridDim.x + cta, gridDim.x * (NT / 32), lane);
+    write_dir(P, h, a.W, base, ibase, (tid >> 5) * gridDim.x + cta, gridDim.x * (NT / 32), lane);
 
     Walk walk(P, h, 1, cta);
     Seg s;
     int kvh, row0, seq;
 #pragma unroll 1
-    while (walk.next(P, h, S.base, S.ibase, s, kvh, row0, seq)) {
+    while (walk.next(P, h, base, ibase, s, kvh, row0, seq)) {
         const int* pages = seq < 0 ? P.prefix_pages : P.table + (long long)seq * P.ld_table;
         const int nv = s.nrows * P.g;
         int bad = 0;
@@ -96,12 +102,14 @@ __global__ void __launch_bounds__(NT) shared_f32_kernel(F32Args a) {
             }
             *reinterpret_cast<float4*>(&S.q[v][4 * c]) = x;
         }
-        int lim[2];
-        float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
-        float4 o[2][DPT];
+        int lim[UV];
+        float m[UV], l[UV];
+        float4 o[UV][DPT];
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-            const int v = 2 * tv + u;
+        for (int u = 0; u < UV; ++u) {
+            const int v = UV * tv + u;
+            m[u] = -INFINITY;
+            l[u] = 0.f;
             lim[u] = v < nv ? max(s.lim0 + s.step * (v / P.g), 0) : 0;
 #pragma unroll
             for (int i = 0; i < DPT; ++i) o[u][i] = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -112,20 +120,26 @@ __global__ void __launch_bounds__(NT) shared_f32_kernel(F32Args a) {
             __syncthreads();  // the tile has come; the other buffer and P are free
             if (j + 1 < s.n) load(j + 1);
             const int b = j & 1, k0 = (s.t0 + j) * KT;
-            float sc[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+            float sc[UV][4];
+#pragma unroll
+            for (int u = 0; u < UV; ++u)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) sc[u][i] = 0.f;
 #pragma unroll 4
             for (int c = 0; c < HD; c += 4) {
-                const float4 q0 = *reinterpret_cast<const float4*>(&S.q[2 * tv][c]);
-                const float4 q1 = *reinterpret_cast<const float4*>(&S.q[2 * tv + 1][c]);
+                float4 q[UV];
+#pragma unroll
+                for (int u = 0; u < UV; ++u) q[u] = *reinterpret_cast<const float4*>(&S.q[UV * tv + u][c]);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const float4 k = *reinterpret_cast<const float4*>(&S.k[b][td + 8 * i][c]);
-                    sc[0][i] = fmaf(q0.w, k.w, fmaf(q0.z, k.z, fmaf(q0.y, k.y, fmaf(q0.x, k.x, sc[0][i]))));
-                    sc[1][i] = fmaf(q1.w, k.w, fmaf(q1.z, k.z, fmaf(q1.y, k.y, fmaf(q1.x, k.x, sc[1][i]))));
+#pragma unroll
+                    for (int u = 0; u < UV; ++u)
+                        sc[u][i] = fmaf(q[u].w, k.w, fmaf(q[u].z, k.z, fmaf(q[u].y, k.y, fmaf(q[u].x, k.x, sc[u][i]))));
                 }
             }
 #pragma unroll
-            for (int u = 0; u < 2; ++u) {
+            for (int u = 0; u < UV; ++u) {
                 float mx = -INFINITY;
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
@@ -142,7 +156,7 @@ __global__ void __launch_bounds__(NT) shared_f32_kernel(F32Args a) {
                 for (int i = 0; i < 4; ++i) {
                     sc[u][i] = exp2f(sc[u][i] - ref);
                     sum += sc[u][i];
-                    S.p[2 * tv + u][td + 8 * i] = sc[u][i];
+                    S.p[UV * tv + u][td + 8 * i] = sc[u][i];
                 }
 #pragma unroll
                 for (int x = 1; x < 8; x <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
@@ -158,29 +172,34 @@ __global__ void __launch_bounds__(NT) shared_f32_kernel(F32Args a) {
             __syncwarp();  // a vector's weights were written by its own eight lanes
 #pragma unroll 2
             for (int k = 0; k < KT; k += 4) {
-                const float4 p0 = *reinterpret_cast<const float4*>(&S.p[2 * tv][k]);
-                const float4 p1 = *reinterpret_cast<const float4*>(&S.p[2 * tv + 1][k]);
-                const float pa[4] = {p0.x, p0.y, p0.z, p0.w}, pb[4] = {p1.x, p1.y, p1.z, p1.w};
+                float p[UV][4];
+#pragma unroll
+                for (int u = 0; u < UV; ++u) {
+                    const float4 x = *reinterpret_cast<const float4*>(&S.p[UV * tv + u][k]);
+                    p[u][0] = x.x;
+                    p[u][1] = x.y;
+                    p[u][2] = x.z;
+                    p[u][3] = x.w;
+                }
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
 #pragma unroll
                     for (int i = 0; i < DPT; ++i) {
                         const float4 x = *reinterpret_cast<const float4*>(&S.v[b][k + e][4 * td + 32 * i]);
-                        o[0][i].x = fmaf(pa[e], x.x, o[0][i].x);
-                        o[0][i].y = fmaf(pa[e], x.y, o[0][i].y);
-                        o[0][i].z = fmaf(pa[e], x.z, o[0][i].z);
-                        o[0][i].w = fmaf(pa[e], x.w, o[0][i].w);
-                        o[1][i].x = fmaf(pb[e], x.x, o[1][i].x);
-                        o[1][i].y = fmaf(pb[e], x.y, o[1][i].y);
-                        o[1][i].z = fmaf(pb[e], x.z, o[1][i].z);
-                        o[1][i].w = fmaf(pb[e], x.w, o[1][i].w);
+#pragma unroll
+                        for (int u = 0; u < UV; ++u) {
+                            o[u][i].x = fmaf(p[u][e], x.x, o[u][i].x);
+                            o[u][i].y = fmaf(p[u][e], x.y, o[u][i].y);
+                            o[u][i].z = fmaf(p[u][e], x.z, o[u][i].z);
+                            o[u][i].w = fmaf(p[u][e], x.w, o[u][i].w);
+                        }
                     }
             }
         }
         if (tid == 0) a.W.block_bad[s.block] = bad;
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-            const int v = 2 * tv + u;
+        for (int u = 0; u < UV; ++u) {
+            const int v = UV * tv + u;
             if (v >= nv) continue;
             if (td == 0) a.W.ml[(size_t)s.block * VT + v] = make_float2(m[u], l[u]);
 #pragma unroll
@@ -194,12 +213,12 @@ __global__ void __launch_bounds__(NT) shared_f32_kernel(F32Args a) {
     pdl_trigger();
 }
 
-template <int HD>
+template <int HD, int UV>
 bool run(const Launch& L, const F32Args& f) {
-    const size_t smem = sizeof(Smem<HD>);
-    if (cudaFuncSetAttribute(shared_f32_kernel<HD>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
+    const size_t smem = sizeof(Smem<HD, 16 * UV>) + 3 * f.P.batch * 4;
+    if (cudaFuncSetAttribute(shared_f32_kernel<HD, UV>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
         return false;
-    launch_k(L, shared_f32_kernel<HD>, dim3(2 * f.P.n_cta), dim3(NT), smem, 1, f);
+    launch_k(L, shared_f32_kernel<HD, UV>, dim3(2 * f.P.n_cta), dim3(NT), smem, 1, f);
     return true;
 }
 
@@ -214,7 +233,8 @@ bool shared_attention_f32(const Launch& L, const sp::Shape& P, const sp::Work& W
     f.v = (const float*)a.v_cache;
     f.ld_q = a.ld_q;
     f.scale_log2 = (float)((double)a.scale * 1.4426950408889634);
-    return P.hd == 128 ? run<128>(L, f) : run<64>(L, f);
+    if (P.VT == 64) return P.hd == 128 ? run<128, 4>(L, f) : run<64, 4>(L, f);
+    return P.hd == 128 ? run<128, 2>(L, f) : run<64, 2>(L, f);
 }
 
 }  // namespace dfl

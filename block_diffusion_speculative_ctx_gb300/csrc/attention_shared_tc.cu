@@ -219,8 +219,8 @@ __global__ void __launch_bounds__(NTHR, 1)
     const uint32_t sb = smem_u32(sm);
     const uint32_t q_at = sb, ring_at = sb + C::RING_AT;
     Bars* bars = reinterpret_cast<Bars*>(sm + C::SMEM_TILES);
-    uint32_t* base = reinterpret_cast<uint32_t*>(bars + 1);  // [2][MAX_BATCH]
-    uint32_t* ibase = base + 2 * MAX_BATCH;
+    uint32_t* base = reinterpret_cast<uint32_t*>(bars + 1);  // [2][batch], then [batch]
+    uint32_t* ibase = base + 2 * a.P.batch;
 
     const Shape& P = a.P;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -641,7 +641,7 @@ bool run(const Launch& L, const Shape& P, const Work& W, const dflash_shared_pre
         const cuuint32_t box[3] = {64, 64, (cuuint32_t)HD / 64};
         if (!encode(&mk, 3, a.k_cache, dims, strides, box) || !encode(&mv, 3, a.v_cache, dims, strides, box)) return false;
     }
-    const size_t smem = C::SMEM_TILES + sizeof(Bars) + 3 * MAX_BATCH * 4 + 1024;
+    const size_t smem = C::SMEM_TILES + sizeof(Bars) + 3 * P.batch * 4 + 1024;
     if (cudaFuncSetAttribute(shared_tc_kernel<HD>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
         return false;
     launch_k(L, shared_tc_kernel<HD>, dim3(P.n_cta), dim3(NTHR), smem, 1, t, mq, mk, mv);

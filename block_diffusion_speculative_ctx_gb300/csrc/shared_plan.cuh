@@ -23,8 +23,6 @@
 namespace dfl {
 namespace sp {
 
-constexpr int MAX_BATCH = DFLASH_OPS_MAX_BATCH;
-
 struct Shape {
     int H, Hkv, g, hd;
     int VT;        // query vectors per stream
@@ -145,7 +143,7 @@ struct Walk {
                                          int& kvh, int& row0, int& seq) {
         const uint32_t lead = P.lead[line];
         const int RT = P.row_tile(line);
-        base += line * MAX_BATCH;
+        base += line * P.batch;
 #pragma unroll 1
         while (p < p1) {
             uint32_t b;
@@ -199,7 +197,7 @@ struct Walk {
     }
 };
 
-// Scan of the batch by every thread of the CTA (NTHR threads, all call it): fills base ([2][MAX_BATCH]:
+// Scan of the batch by every thread of the CTA (NTHR threads, all call it): fills base ([2][batch]:
 // per line, the exclusive sums of the own items' lengths, from the prefix items' end), ibase ([batch]: of
 // the counts on the sequence's line) and the head.  Ends with a barrier.  (Up to 32 sequences without one in
 // between: the plan is 2 us of a small call's chain, most of it code that comes from L2.)
@@ -274,7 +272,7 @@ __device__ __forceinline__ void make_plan(const Shape& P, uint32_t* base, uint32
         }
         if (warp == 0 && lane < P.batch) {
             base[lane] = v[0];
-            base[MAX_BATCH + lane] = v[1];
+            base[P.batch + lane] = v[1];
             ibase[lane] = line ? v[3] : v[2];
         }
     } else {
@@ -336,7 +334,7 @@ __device__ __forceinline__ void make_plan(const Shape& P, uint32_t* base, uint32
                 }
             if (s < P.batch) {
                 base[s] = v[0];
-                base[MAX_BATCH + s] = v[1];
+                base[P.batch + s] = v[1];
                 ibase[s] = line ? v[3] : v[2];
             }
             __syncthreads();
@@ -403,7 +401,7 @@ __device__ __forceinline__ void write_dir(const Shape& P, const Head& h, const W
                 const int RT = P.row_tile(q.line), gi = j / RT, k = kvh * q.groups + gi;
                 const int n_eff = seen_tiles(P, q, min(m, (gi + 1) * RT));
                 if (n_eff)
-                    dir_item(P, h, q.line, base[q.line * MAX_BATCH + s] + (uint32_t)k * (uint32_t)(P.lead[q.line] + q.tiles),
+                    dir_item(P, h, q.line, base[q.line * P.batch + s] + (uint32_t)k * (uint32_t)(P.lead[q.line] + q.tiles),
                              (h.pl == q.line ? h.n_prefix : 0) + (int)ibase[s] + k, n_eff, j - gi * RT, d.own_block, d.own_count,
                              d.own_v, d.own_step);
             }

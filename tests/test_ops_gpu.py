@@ -308,6 +308,23 @@ def test_shared_prefix_attention_workspaces_of_its_own():
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("batch", [31, 32, 33, 65])
+def test_shared_prefix_attention_batches_around_a_warp(dtype, batch):
+    """The plan is made by a warp up to 32 sequences and by the whole CTA beyond; empty sequences first, last and
+    between; then a row start that decreases, in either."""
+    rng = np.random.default_rng(batch)
+    q = rng.integers(0, 4, batch)
+    q[[0, batch // 2, batch - 1]] = 0
+    c = attn_case(dtype, (4, 2, 64), 200, rng.integers(0, 150, batch), q, seed=batch)
+    x = list(attn_inputs(c))
+    attn_check(c, dfl().shared_prefix_attention(*x), True)
+    x[7] = x[7].clone()
+    x[7][batch // 2] = -1
+    out, lse = dfl().shared_prefix_attention(*x)
+    assert out.isnan().all() and lse.isnan().all()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
 def test_shared_prefix_attention_in_place(dtype):
     """out is q: the queries have all been read before the first result is written."""
     c = attn_case(dtype, (32, 8, 128), 700, [400, 33, 90], [16, 1, 50], seed=33)
