@@ -11,11 +11,15 @@ refused while autograd is recording."""
 from __future__ import annotations
 
 import ctypes
+import importlib.machinery
+import importlib.util
+import os
 import struct
 from typing import NamedTuple, Optional
 
 import torch
 
+from . import build as _build_mod
 from . import DFLASH_DTYPE_BF16, DFLASH_DTYPE_F32, DFLASH_OK, DFlashError, dflash_last_error, load
 
 _P, _I32, _I64, _F = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_float
@@ -124,6 +128,28 @@ def _rows3(name, t, dtype, rows, heads, hd, dev):
     if inner != 1 or (heads > 1 and between != hd):
         _bad(f"{name}: the heads of a row must be contiguous")
     return ld if rows > 1 else heads * hd
+
+
+_PYTHON_CHECKS = (_flat, _mat, _rows3)
+
+
+def _use_extension():
+    """The same three checks from csrc/tensor_args.cpp, where it has been built (a small call's host side is
+    shorter by a third)."""
+    global _flat, _mat, _rows3
+    path = _build_mod.tensor_args_path()
+    if path is None or not os.path.exists(path):
+        return
+    try:
+        spec = importlib.util.spec_from_loader("_tensor_args", importlib.machinery.ExtensionFileLoader("_tensor_args", path))
+        m = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(m)
+    except ImportError:
+        return
+    _flat, _mat, _rows3 = m.flat, m.mat, m.rows3
+
+
+_use_extension()
 
 
 def _call(fn, pack, values, dev):

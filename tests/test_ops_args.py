@@ -116,3 +116,32 @@ def test_the_bindings_refuse_cpu_tensors():
     c = torch.zeros(1, 1, 64, 64)
     with pytest.raises(ValueError, match="CUDA"):
         dfl.shared_prefix_attention(torch.zeros(1, 1, 64), c, c, None, 0, i[:1, None], i[:1], i)
+
+
+def test_the_checks_in_python_and_in_the_extension_agree(lib):
+    """The same addresses and strides, and refusals of the same tensors, wherever both forms are there."""
+    import torch
+    if ops._flat is ops._PYTHON_CHECKS[0]:
+        ops._use_extension()
+    if ops._flat is ops._PYTHON_CHECKS[0]:
+        pytest.skip("the extension has not been built")
+    i, x = torch.arange(24, dtype=torch.int32), torch.zeros(4, 6, 8)
+    m = i.view(4, 6)
+    calls = [(0, ("a", t, d, n, dev)) for t in (i, m, i[::2], i[:0], i[3:4], m[:, :2], m.t()) for d in (torch.int32, torch.int64)
+             for n in (t.numel(), 24) for dev in (-1, 0)]
+    calls += [(1, ("a", t, torch.int32, r, c, -1)) for t in (m, m[:, 1:4], m[::2], m.t(), m[:1, :3], m[:0], m[:, :0], m[:, ::2], i,
+                                                             m[:1].expand(4, 6)) for r in (4, 2, 6, 1, 0) for c in (None, 6, 3)]
+    calls += [(2, ("a", t, torch.float32, *s, -1)) for t in (x, x[::2], x[:, :3], x[:, :, :4], x.transpose(0, 1), x[:1], x[:, :1], x[:0], x[:, :, :0], m)
+              for s in ((0, 6, 8), (4, 6, 0), (4, 6, 8), (2, 6, 8), (4, 3, 8), (4, 6, 4), (6, 4, 8), (1, 6, 8), (4, 1, 8))]
+    refused = 0
+    for which, a in calls:
+        got = []
+        for f in (ops._PYTHON_CHECKS[which], (ops._flat, ops._mat, ops._rows3)[which]):
+            try:
+                got.append(f(*a))
+            except ValueError as e:
+                got.append(ValueError)
+                assert str(e).startswith("a")
+        assert got[0] == got[1], (which, a, got)
+        refused += got[0] is ValueError
+    assert 0 < refused < len(calls)
