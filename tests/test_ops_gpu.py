@@ -248,10 +248,11 @@ def test_shared_prefix_attention(i, dtype):
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
-def test_shared_prefix_attention_many_short_sequences(dtype):
+@pytest.mark.parametrize("batch", [300, 2048])
+def test_shared_prefix_attention_many_short_sequences(dtype, batch):
     rng = np.random.default_rng(3)
-    kv = rng.integers(0, 90, 300)
-    c = attn_case(dtype, (2, 1, 64), 130, kv, rng.integers(0, 3, 300), seed=4)
+    kv = rng.integers(0, 90, batch)
+    c = attn_case(dtype, (2, 1, 64), 130, kv, rng.integers(0, 3, batch), seed=4)
     attn_check(c, dfl().shared_prefix_attention(*attn_inputs(c)), True)
 
 
