@@ -165,7 +165,7 @@ sp::Shape sizes_of(bool f32, int H, int Hkv, int hd, int batch, int rows) {
     sp::Shape P = {};
     P.H = H;
     P.g = H / Hkv;
-    P.VT = !f32 ? 128 : (long long)rows * P.g > 32 ? 64 : 32;  // (figures: attention_shared_f32.cu)
+    P.VT = !f32 ? 128 : (long long)rows * P.g > 32ll * batch ? 64 : 32;  // (figures: attention_shared_f32.cu)
     P.parts = 1;
     while (P.g % P.parts || P.g / P.parts > P.VT) ++P.parts;
     P.Hkv = Hkv * P.parts;

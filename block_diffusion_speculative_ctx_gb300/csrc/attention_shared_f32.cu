@@ -14,9 +14,10 @@
 // lengths -> pages -> tile for the short calls that fp32 models make: 9.8 us (merge
 // included, graph replay) for 3 blocks of 4 rows behind 500 keys, whose bytes take
 // 0.1 us; the tiles of a plain fp32 kernel without the plan took 184 us.  64 vectors
-// a worker where the call has more than 32 per KV head: 16 rows of 8 sequences
-// behind 4096 keys take 226 us (39 TFLOP/s) at 32 heads of 128 and 68 us at 16 heads
-// of 64, with 32 vectors 339 and 116 us; a call that fits 32 would compute twice.
+// a worker where a sequence has more than 32 per KV head on average: 16 rows of 8
+// sequences behind 4096 keys take 226 us (39 TFLOP/s) at 32 heads of 128 and 68 us at
+// 16 heads of 64, with 32 vectors 339 and 116 us; sequences that fit 32 would compute
+// in vain on their own keys (16 x 1 row, 2000 own keys: 216 us with 64, 164 with 32).
 #include <math.h>
 
 #include "shared_plan.cuh"
