@@ -160,12 +160,15 @@ namespace {
 
 constexpr int CTAS = 152;  // one per SM
 
+// Query vectors of a worker (fp32: figures in attention_shared_f32.cu).
+int vectors_of(bool f32, int g, int batch, int rows) { return !f32 ? 128 : (long long)rows * g > 32ll * batch ? 64 : 32; }
+
 // The sizes alone (what the workspace depends on).
-sp::Shape sizes_of(bool f32, int H, int Hkv, int hd, int batch, int rows) {
+sp::Shape sizes_of(bool f32, int VT, int H, int Hkv, int hd, int batch, int rows) {
     sp::Shape P = {};
     P.H = H;
     P.g = H / Hkv;
-    P.VT = !f32 ? 128 : (long long)rows * P.g > 32ll * batch ? 64 : 32;  // (figures: attention_shared_f32.cu)
+    P.VT = VT;
     P.parts = 1;
     while (P.g % P.parts || P.g / P.parts > P.VT) ++P.parts;
     P.Hkv = Hkv * P.parts;
@@ -211,7 +214,7 @@ bool shared_prefix_attention(const Launch& L, const dflash_shared_prefix_args& a
     const bool f32 = a.dtype == DFLASH_DTYPE_F32;
     MergeArgs m;
     sp::Shape& P = m.P;
-    P = sizes_of(f32, a.n_heads, a.n_kv_heads, a.head_dim, a.batch, a.rows);
+    P = sizes_of(f32, vectors_of(f32, a.n_heads / a.n_kv_heads, a.batch, a.rows), a.n_heads, a.n_kv_heads, a.head_dim, a.batch, a.rows);
     P.width = a.width;
     P.prefix_len = a.prefix_len;
     P.causal = a.causal != 0;
@@ -279,7 +282,11 @@ extern "C" size_t dflash_shared_prefix_workspace(int32_t dtype, int32_t n_heads,
         batch > DFLASH_OPS_MAX_BATCH || rows < 0 || rows > (1 << 20) || (head_dim != 64 && head_dim != 128) ||
         (dtype != DFLASH_DTYPE_F32 && dtype != DFLASH_DTYPE_BF16))
         return 0;
-    return sp::layout(nullptr, sizes_of(dtype == DFLASH_DTYPE_F32, n_heads, n_kv_heads, head_dim, batch, rows), nullptr);
+    // (the larger of fp32's two forms: no call with fewer rows or sequences needs more)
+    auto bytes = [&](bool f32, int VT) {
+        return sp::layout(nullptr, sizes_of(f32, VT, n_heads, n_kv_heads, head_dim, batch, rows), nullptr);
+    };
+    return dtype == DFLASH_DTYPE_F32 ? std::max(bytes(true, 32), bytes(true, 64)) : bytes(false, 128);
 }
 
 extern "C" dflash_status dflash_shared_prefix_attention(const dflash_shared_prefix_args* p, void* cuda_stream) {

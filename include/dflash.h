@@ -577,8 +577,8 @@ typedef struct {
     size_t workspace_bytes;
 } dflash_shared_prefix_args;
 dflash_status dflash_shared_prefix_attention(const dflash_shared_prefix_args* args, void* cuda_stream);
-/* Bytes of workspace for a call with these sizes (any lengths within them);
- * 0 for sizes that the call refuses. */
+/* Bytes of workspace for a call with these sizes (any lengths within them, and
+ * any smaller batch or rows); 0 for sizes that the call refuses. */
 size_t dflash_shared_prefix_workspace(int32_t dtype, int32_t n_heads, int32_t n_kv_heads, int32_t head_dim,
                                       int32_t batch, int32_t rows);
 

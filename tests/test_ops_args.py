@@ -88,6 +88,13 @@ def test_shared_prefix_workspace_sizes(lib):
     f = lib.dflash_shared_prefix_workspace
     assert f(1, 32, 8, 128, 32, 512) > 0
     assert f(1, 32, 8, 128, 32, 513) >= f(1, 32, 8, 128, 32, 512)
+    # what a larger call needs is enough for a smaller one
+    for dtype in (0, 1):
+        for h, hkv, hd in ((4, 2, 64), (32, 8, 128), (7, 7, 64), (64, 1, 128), (24, 8, 64)):
+            grid = [[f(dtype, h, hkv, hd, b, r) for r in (1, 2, 7, 8, 9, 31, 33, 64, 257, 2048, 4096)] for b in (1, 2, 8, 33, 64, 1024)]
+            assert all(x > 0 for row in grid for x in row)
+            assert all(row == sorted(row) for row in grid)
+            assert all(list(col) == sorted(col) for col in zip(*grid))
 
 
 @pytest.mark.parametrize("kw", [
