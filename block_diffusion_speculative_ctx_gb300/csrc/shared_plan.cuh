@@ -50,7 +50,6 @@ struct Head {
     int n_prefix;      // prefix items
     int r_begin, r_end;
     int nqt;           // row tiles of the batch on line pl
-    int max_m;         // rows of the longest sequence
     int bad;           // q_start is not a list of rows, or a line is too long
 };
 
@@ -205,7 +204,7 @@ template <int NTHR>
 struct PlanMem {
     uint32_t ws[NTHR / 32][4];
     unsigned long long sum[2];  // in 64 bits: a line of 2^31 units or more is refused
-    int bad, max_m;
+    int bad;
 };
 template <int NTHR>
 __device__ __forceinline__ void make_plan(const Shape& P, uint32_t* base, uint32_t* ibase, PlanMem<NTHR>* m, Head& h) {
@@ -240,13 +239,12 @@ __device__ __forceinline__ void make_plan(const Shape& P, uint32_t* base, uint32
         h.r_begin = __shfl_sync(0xffffffffu, a, 0);
         h.r_end = __shfl_sync(0xffffffffu, b, 31);
         const unsigned long long cp = prefix();
-        int line = 0, len31 = cp >> 31 != 0, m_own = 0;
+        int line = 0, len31 = cp >> 31 != 0;
         uint32_t items = 0, len = 0;
         if (rows_ok(a, b)) {
             const unsigned long long l = own_items(a, b, kv, line, items);
             len31 |= l >> 31 != 0;
             len = (uint32_t)l;
-            m_own = b - a;
         } else {
             bad = 1;
         }
@@ -254,7 +252,6 @@ __device__ __forceinline__ void make_plan(const Shape& P, uint32_t* base, uint32
         const uint32_t sum0 = __reduce_add_sync(0xffffffffu, (line == 0 ? len >> 8 : 0u) + (lane == 0 && h.pl == 0 ? h.CP >> 8 : 0u));
         const uint32_t sum1 = __reduce_add_sync(0xffffffffu, (line == 1 ? len >> 8 : 0u) + (lane == 0 && h.pl == 1 ? h.CP >> 8 : 0u));
         h.bad = __any_sync(0xffffffffu, bad | len31) || sum0 >> 23 || sum1 >> 23;
-        h.max_m = __reduce_max_sync(0xffffffffu, m_own);
         uint32_t v[4] = {line ? 0u : len, line ? len : 0u, line ? 0u : items, line ? items : 0u};
         const uint32_t own[4] = {v[0], v[1], v[2], v[3]};
 #pragma unroll 1
@@ -277,7 +274,7 @@ __device__ __forceinline__ void make_plan(const Shape& P, uint32_t* base, uint32
         }
     } else {
         if (tid == 0) {
-            m->bad = m->max_m = 0;
+            m->bad = 0;
             m->sum[0] = m->sum[1] = 0;
         }
         h.r_begin = P.q_start[0];
@@ -301,7 +298,6 @@ __device__ __forceinline__ void make_plan(const Shape& P, uint32_t* base, uint32
                     uint32_t items;
                     const unsigned long long l = own_items(a, b, P.kv_lens[s], line, items);
                     if (items) atomicAdd(&m->sum[line], l);
-                    atomicMax(&m->max_m, b - a);
                     if (line) {
                         v[1] = (uint32_t)l;
                         v[3] = items;
@@ -342,7 +338,6 @@ __device__ __forceinline__ void make_plan(const Shape& P, uint32_t* base, uint32
         if (bad) m->bad = 1;
         __syncthreads();
         h.bad = m->bad || m->sum[0] >> 31 || m->sum[1] >> 31;
-        h.max_m = m->max_m;
     }
     h.W[0] = h.bad ? 0u : total[0];
     h.W[1] = h.bad ? 0u : total[1];
@@ -368,26 +363,28 @@ __device__ __forceinline__ void dir_item(const Shape& P, const Head& h, int line
     v = (rl - x * P.RH) * P.g;
 }
 
-// The directory for the merge kernel, by `warps` warps of which this is number `w`: a warp takes 32 (row, KV
-// head) pairs of one sequence at a time.
+// The directory for the merge kernel, by `warps` warps of which this is number `w`: a lane takes a (row, KV head)
+// pair at a time.  Pairs are numbered through the rows of q (at most 2^20 of them, times 1024 heads), and the row's
+// sequence is searched in the row starts: the work is the rows', whatever the longest sequence is.
 __device__ __forceinline__ void write_dir(const Shape& P, const Head& h, const Work& W, const uint32_t* base,
                                           const uint32_t* ibase, int w, int warps, int lane) {
-    // rows of no sequence, or of a call that went wrong
-    const int none = h.bad ? P.rows : P.rows - (h.r_end - h.r_begin);
+    const int pairs = P.rows * P.Hkv;
 #pragma unroll 1
-    for (int i = w * 32 + lane; i < none * P.Hkv; i += warps * 32) {
-        const int k = i / P.Hkv, r = h.bad || k < h.r_begin ? k : k + (h.r_end - h.r_begin);
-        W.dir[(size_t)r * P.Hkv + (i - k * P.Hkv)].pre_count = h.bad ? -2 : -1;
-    }
-    if (h.bad) return;
-    const int chunks = cdiv(h.max_m * P.Hkv, 32);
+    for (int i = w * 32 + lane; i < pairs; i += warps * 32) {
+        const int r = i / P.Hkv, kvh = i - r * P.Hkv;
+        if (h.bad || r < h.r_begin || r >= h.r_end) {  // a call that went wrong, or a row of no sequence
+            W.dir[i].pre_count = h.bad ? -2 : -1;
+            continue;
+        }
+        int s = 0, hi = P.batch;  // the last sequence that begins at or before r (empty ones share their start with it)
 #pragma unroll 1
-    for (int u = w; u < P.batch * chunks; u += warps) {
-        const int s = u / chunks, i = (u - s * chunks) * 32 + lane;
-        const int start = P.q_start[s], m = P.q_start[s + 1] - start;
-        if (i >= m * P.Hkv) continue;
+        while (hi - s > 1) {
+            const int mid = (s + hi) >> 1;
+            if (P.q_start[mid] <= r) s = mid;
+            else hi = mid;
+        }
+        const int start = P.q_start[s], m = P.q_start[s + 1] - start, j = r - start;
         const Seq q = seq_of(P, start, start + m, P.kv_lens[s]);
-        const int j = i / P.Hkv, kvh = i - j * P.Hkv, r = start + j;
         Dir d = {0, 0, 0, 0, 0, 0, 1, 1};
         if (q.kv < 0 || q.kv > (long long)64 * P.width) {
             d.pre_count = -2;
@@ -406,7 +403,7 @@ __device__ __forceinline__ void write_dir(const Shape& P, const Head& h, const W
                              d.own_v, d.own_step);
             }
         }
-        W.dir[(size_t)r * P.Hkv + kvh] = d;
+        W.dir[i] = d;
     }
 }
 

@@ -381,6 +381,43 @@ def test_shared_prefix_attention_past_32_bit_offsets():
     attn_check(c, dfl().shared_prefix_attention(*x), True)
 
 
+def sampled_case(c, q, rows):
+    """The case with some of its rows alone (their queries in q): each a sequence of its own that sees what the row saw."""
+    start, kv = c["start"], c["kv"]
+    s = np.searchsorted(start, rows, "right") - 1
+    m, j = start[s + 1] - start[s], rows - start[s]
+    return dict(c, q=q, table=c["table"][s], kv=np.maximum(kv[s] - m + j + 1, 0), start=np.arange(len(rows) + 1))
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_shared_prefix_attention_one_long_sequence_of_2048(dtype):
+    """600000 rows of one sequence next to 2047 single ones, 64 KV heads: sequences x the longest one's rows x KV heads
+    passes 2^31, the rows' own number does not."""
+    H, hd, long = 64, 64, 600000
+    kv, q = np.zeros(2048, np.int64), np.ones(2048, np.int64)
+    kv[[0, 699, 700, 701, 2047]], q[700] = [3, 1, 150, 64, 65], long
+    c = attn_case(dtype, (H, H, hd), 70, kv, np.zeros(2048, np.int64), seed=81)
+    x = list(attn_inputs(c))
+    rows = int(q.sum())
+    x[0] = torch.empty((rows, H, hd), dtype=DT[dtype], device="cuda")
+    torch.manual_seed(82)
+    torch.cuda.manual_seed(82)
+    for part in x[0].split(1 << 16):
+        part.normal_()
+    c["start"] = np.concatenate([[0], np.cumsum(q)])
+    x[7] = i32(c["start"])
+    out, lse = dfl().shared_prefix_attention(*x)
+    pick = np.array([0, 1, 699, 700, 701, 700 + 127, 700 + 131072, 700 + 524287, 700 + 599849, 700 + 599850, 700 + 599999,
+                     700 + long, 700 + long + 1, rows - 1])
+    t = torch.from_numpy(pick).cuda()
+    some = sampled_case(c, x[0][t].float().cpu().numpy(), pick)
+    attn_check(some, (out[t], lse[t]), True)
+    for part in lse.split(1 << 16):
+        assert part.isfinite().all()
+    del x, out, lse
+    torch.cuda.empty_cache()
+
+
 def test_shared_prefix_attention_graph_streams_and_workspaces():
     """Captured once, replayed with other lengths, pages and queries in place, while an eager call runs on a
     second stream with a workspace of its own."""
