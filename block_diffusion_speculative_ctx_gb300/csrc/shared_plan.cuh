@@ -76,11 +76,15 @@ inline long long max_blocks(const Shape& P) {
     return (P.one_line ? items + 2 * P.n_cta : 2 * (items + P.n_cta)) + 2 * P.n_cta;
 }
 
+// Its sections begin on multiples of 256 bytes wherever the workspace itself begins (partial results are stored 32 bytes
+// at a time); the size has room for that.
+constexpr size_t ALIGN = 256;
 inline size_t layout(char* p, const Shape& P, Work* w) {
+    p = (char*)(((uintptr_t)p + ALIGN - 1) / ALIGN * ALIGN);
     size_t at = 0;
     auto take = [&](size_t bytes) {
         char* q = p + at;
-        at += (bytes + 255) / 256 * 256;
+        at += (bytes + ALIGN - 1) / ALIGN * ALIGN;
         return q;
     };
     const size_t blocks = (size_t)max_blocks(P);
@@ -91,7 +95,7 @@ inline size_t layout(char* p, const Shape& P, Work* w) {
     x.ml = (float2*)take(blocks * P.VT * 8);
     x.o = (float*)take(blocks * P.VT * P.hd * 4);
     if (w) *w = x;
-    return at;
+    return at + ALIGN;
 }
 
 __device__ __forceinline__ int cdiv(int a, int b) { return (a + b - 1) / b; }

@@ -309,6 +309,20 @@ def test_shared_prefix_attention_workspaces_of_its_own():
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("at", [16, 32, 48, 240, 4080])
+def test_shared_prefix_attention_wherever_its_workspace_begins(dtype, at):
+    """A workspace of exactly the size asked for, on any 16-byte boundary: the same bits, and nothing written beside it."""
+    c = attn_case(dtype, (8, 2, 128), 300, [70, 3, 130], [2, 3, 40], seed=75)
+    x = attn_inputs(c)
+    want = dfl().shared_prefix_attention(*x)
+    n = dfl().shared_prefix_workspace(x[0], x[1], 3)
+    buf = torch.full((4096 + n + 4096,), 0xA5, dtype=torch.uint8, device="cuda")
+    got = dfl().shared_prefix_attention(*x, workspace=buf[at:at + n])
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    assert (buf[:at] == 0xA5).all() and (buf[at + n:] == 0xA5).all()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("batch", [31, 32, 33, 65])
 def test_shared_prefix_attention_batches_around_a_warp(dtype, batch):
     """The plan is made by a warp up to 32 sequences and by the whole CTA beyond; empty sequences first, last and
