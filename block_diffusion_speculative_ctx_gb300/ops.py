@@ -15,6 +15,7 @@ import importlib.machinery
 import importlib.util
 import os
 import struct
+import threading
 from typing import NamedTuple, Optional
 
 import torch
@@ -69,10 +70,14 @@ _TABLES, _ATTN, _LOGITS = struct.Struct("6i2q12Q"), struct.Struct("10ifi3q11Q"),
 _I32T, _I64T, _F32T = torch.int32, torch.int64, torch.float32
 _U8T = torch.uint8
 _WORKSPACE = {}  # bytes by (dtype, H, H_kv, hd, batch, rows)
-# Workspaces of calls on a device's default stream, one a device: (bytes, address, tensor).  Such calls run one after
-# the other (whichever thread makes them) and are never captured, and that stream lives as long as the device; on any
-# other stream each call allocates its own.  An allocation beside a call costs 5 us of the 17 that a small one takes.
+# Workspaces of calls on a device's default stream, one a device: (bytes, address, tensor).  That stream is never
+# captured and lives as long as the device; on any other stream each call allocates its own.  An allocation beside a call
+# costs 5 us of the 17 that a small one takes.  A call queues two kernels, the second of which reads what the first left in
+# the workspace, and the C call runs without the interpreter's lock: so a call that uses a kept workspace holds _KEPT_LOCK
+# from looking it up until both are queued (the stream then runs the calls one after the other, whichever threads made
+# them).  Re-entrant, for a call out of a signal handler or a finalizer.
 _KEPT = {}
+_KEPT_LOCK = threading.RLock()
 _raw_stream, _current_device = torch._C._cuda_getCurrentRawStream, torch.cuda.current_device
 
 
@@ -274,29 +279,30 @@ def shared_prefix_attention(q, k_cache, v_cache, prefix_pages, prefix_len: int, 
     ld_out = _rows3("out", out, dtype, rows, h, hd, dev)
     if lse is None:
         lse = torch.zeros((rows, h), dtype=_F32T, device=q.device)
-    if workspace is None:
-        sizes = (dt, h, hkv, hd, batch, rows)
-        n_ws = _WORKSPACE.get(sizes)
-        if n_ws is None:
-            if len(_WORKSPACE) > 4096:
-                _WORKSPACE.clear()
-            n_ws = _WORKSPACE[sizes] = load().dflash_shared_prefix_workspace(*sizes)
-        default = _raw_stream(dev) == 0
-        kept = _KEPT.get(dev) if default else None
+    fn = load().dflash_shared_prefix_attention
+    args = (dt, h, hkv, hd, batch, rows, pages, prefix_len, table.shape[1], bool(causal), hd ** -0.5 if scale is None else scale, 0,
+            ld_q, ld_out, ld_table, q.data_ptr(), p_k, p_v, p_pre, table.data_ptr(), p_kv, p_start, out.data_ptr(),
+            _flat("lse", lse, _F32T, rows * h, dev))
+    if workspace is not None:
+        n_ws = workspace.numel() * workspace.element_size()
+        _call(fn, _ATTN.pack, (*args, _flat("workspace", workspace, workspace.dtype, workspace.numel(), dev), n_ws), dev)
+        return out, lse
+    sizes = (dt, h, hkv, hd, batch, rows)
+    n_ws = _WORKSPACE.get(sizes)
+    if n_ws is None:
+        if len(_WORKSPACE) > 4096:
+            _WORKSPACE.clear()
+        n_ws = _WORKSPACE[sizes] = load().dflash_shared_prefix_workspace(*sizes)
+    if _raw_stream(dev) != 0:
+        workspace = torch.empty(n_ws, dtype=_U8T, device=q.device)
+        _call(fn, _ATTN.pack, (*args, workspace.data_ptr(), n_ws), dev)
+        return out, lse
+    with _KEPT_LOCK:
+        kept = _KEPT.get(dev)
         if kept is None or kept[0] < n_ws:
             workspace = torch.empty(n_ws, dtype=_U8T, device=q.device)
-            kept = (n_ws, workspace.data_ptr(), workspace)
-            if default:
-                _KEPT[dev] = kept
-        p_ws = kept[1]
-    else:
-        n_ws = workspace.numel() * workspace.element_size()
-        p_ws = _flat("workspace", workspace, workspace.dtype, workspace.numel(), dev)
-    _call(load().dflash_shared_prefix_attention,
-          _ATTN.pack, (dt, h, hkv, hd, batch, rows, pages, prefix_len, table.shape[1], bool(causal),
-                     hd ** -0.5 if scale is None else scale, 0, ld_q, ld_out, ld_table, q.data_ptr(), p_k, p_v, p_pre,
-                     table.data_ptr(), p_kv, p_start, out.data_ptr(), _flat("lse", lse, _F32T, rows * h, dev), p_ws, n_ws),
-          dev)
+            kept = _KEPT[dev] = (n_ws, workspace.data_ptr(), workspace)
+        _call(fn, _ATTN.pack, (*args, kept[1], n_ws), dev)
     return out, lse
 
 

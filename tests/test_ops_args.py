@@ -152,3 +152,45 @@ def test_the_checks_in_python_and_in_the_extension_agree(lib):
         assert got[0] == got[1], (which, a, got)
         refused += got[0] is ValueError
     assert 0 < refused < len(calls)
+
+
+def test_calls_on_a_kept_workspace_queue_one_at_a_time(monkeypatch):
+    """A call queues two kernels with the workspace between them: two host threads on the default stream must not be
+    inside the C call with the same workspace at once.  (The C call is a stand-in: no GPU.)"""
+    import threading
+    import time
+
+    import torch
+    inside, lock, overlaps, calls = {}, threading.Lock(), [], []
+
+    def call(fn, pack, values, dev):
+        ws, size = values[-2:]
+        with lock:
+            overlaps.append(inside.get(ws, 0))
+            inside[ws] = inside.get(ws, 0) + 1
+            calls.append((ws, size))
+        time.sleep(0.002)  # (gives up the interpreter's lock, as the foreign call does)
+        with lock:
+            inside[ws] -= 1
+
+    monkeypatch.setattr(ops, "_call", call)
+    monkeypatch.setattr(ops, "_device", lambda *a: 0)
+    monkeypatch.setattr(ops, "_flat", lambda name, t, *a: t.data_ptr())
+    monkeypatch.setattr(ops, "_mat", lambda *a: 4)
+    monkeypatch.setattr(ops, "_rows3", lambda *a: 256)
+    monkeypatch.setattr(ops, "_raw_stream", lambda dev: 0)
+    monkeypatch.setattr(ops, "_KEPT", {})
+    c = torch.zeros(2, 2, 64, 64)
+
+    def work(rows):
+        i = torch.zeros(rows + 1, dtype=torch.int32)
+        for _ in range(20):
+            ops.shared_prefix_attention(torch.zeros(rows, 4, 64), c, c, None, 0, i[:rows, None], i[:rows], i)
+
+    threads = [threading.Thread(target=work, args=(r,)) for r in (1, 3, 40)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert len(calls) == 60 and not any(overlaps)
+    assert len({n for _, n in calls}) == 3

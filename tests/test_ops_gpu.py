@@ -308,6 +308,30 @@ def test_shared_prefix_attention_workspaces_of_its_own():
         assert torch.equal(out, want[i][0]) and torch.equal(lse, want[i][1])
 
 
+def test_shared_prefix_attention_from_two_threads():
+    """Two host threads with calls of different shapes on the default stream, which share the kept workspace: each
+    result is that of a call with a workspace of its own, bit for bit."""
+    import threading
+    cases = [attn_inputs(attn_case("bf16", heads, p, kv, q, seed=77 + p)) for heads, p, kv, q in
+             (((8, 2, 128), 100, [70, 3], [2, 3]), ((32, 8, 128), 900, [400, 90, 65, 10], [9, 1, 64, 17]))]
+    own = [torch.empty(dfl().shared_prefix_workspace(x[0], x[1], x[6].numel()), dtype=torch.uint8, device="cuda") for x in cases]
+    want = [[t.clone() for t in dfl().shared_prefix_attention(*x, workspace=w)] for x, w in zip(cases, own)]
+    torch.cuda.synchronize()
+    wrong = [0, 0]
+
+    def work(i):
+        for _ in range(20):
+            got = [dfl().shared_prefix_attention(*cases[i]) for _ in range(50)]
+            wrong[i] += sum(not (torch.equal(o, want[i][0]) and torch.equal(l, want[i][1])) for o, l in got)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert wrong == [0, 0]
+
+
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("at", [16, 32, 48, 240, 4080])
 def test_shared_prefix_attention_wherever_its_workspace_begins(dtype, at):
