@@ -1731,11 +1731,17 @@ dflash_status dflash_set_token_masks(dflash_ctx* c, int32_t n_masks, const uint3
         c->masks = m;
         c->mask_index = i;
     }
-    if (!is_device_ptr(mask_index))
+    const bool on_device = is_device_ptr(mask_index);
+    if (!on_device)
         for (int i = 0; i < rows; ++i)
             if (mask_index[i] >= n_masks) return c->fail(DFLASH_E_INVAL, "mask index %d = %d, with %d masks", i, mask_index[i], n_masks);
     CUDA_TRY(c, cudaMemcpyAsync(c->masks, masks, (size_t)n_masks * c->mask_words * 4, cudaMemcpyDefault, c->stream));
     CUDA_TRY(c, cudaMemcpyAsync(c->mask_index, mask_index, (size_t)rows * 4, cudaMemcpyDefault, c->stream));
+    if (on_device) {  // (the passes may be captured with the buffers' capacity: what lies behind these masks is never theirs)
+        drop_indices(c->L(), c->mask_index, rows, n_masks);
+        const dflash_status s = launch_check(c);
+        if (s) return s;
+    }
     c->masks_on = true;
     c->mask_rows = rows;
     return DFLASH_OK;

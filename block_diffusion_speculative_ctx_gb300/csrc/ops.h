@@ -28,6 +28,8 @@ void gather_last_rows(const Launch& L, const float* x, int d, const int* start, 
 // (accepted NULL: the anchor alone).  n is the new committed length.
 void history_append(const Launch& L, int batch, int B, int ld, const int* n, const int* anchor, const int* accepted,
                     const int* proposal, int* history);
+// index[i] >= n becomes -1 (no mask).
+void drop_indices(const Launch& L, int* index, int rows, int n);
 // Rows whose best logit is -inf have no token: the error word says so, and token 0 gets all of the row's
 // mass, so that what follows stays defined.
 void check_rows(const Launch& L, float* logits, long long ld, int rows, const int* best, uint32_t* err);

@@ -38,6 +38,13 @@ __global__ void history_append_kernel(int batch, int B, int ld, const int* __res
     if (threadIdx.x == 0 && len < ld) h[len] = anchor[s];
 }
 
+__global__ void drop_indices_kernel(int* __restrict__ index, int rows, int n) {
+    pdl_wait();
+    pdl_trigger();
+    const int r = blockIdx.x * blockDim.x + threadIdx.x;
+    if (r < rows && index[r] >= n) index[r] = -1;
+}
+
 __global__ void check_rows_kernel(float* __restrict__ logits, long long ld, int rows, const int* __restrict__ best,
                                   uint32_t* __restrict__ err) {
     pdl_wait();
@@ -61,6 +68,10 @@ void gather_last_rows(const Launch& L, const float* x, int d, const int* start, 
 void history_append(const Launch& L, int batch, int B, int ld, const int* n, const int* anchor, const int* accepted,
                     const int* proposal, int* history) {
     launch_k(L, history_append_kernel, dim3(batch), dim3(32), 0, 1, batch, B, ld, n, anchor, accepted, proposal, history);
+}
+
+void drop_indices(const Launch& L, int* index, int rows, int n) {
+    launch_k(L, drop_indices_kernel, dim3((rows + 127) / 128), dim3(128), 0, 1, index, rows, n);
 }
 
 void check_rows(const Launch& L, float* logits, long long ld, int rows, const int* best, uint32_t* err) {

@@ -361,3 +361,37 @@ def test_masks_that_leave_nothing_and_bad_masks():
             assert e.value.status == DFLASH_E_INVAL
     finally:
         sess.close()
+
+
+def test_a_device_mask_index_behind_the_masks_means_no_mask():
+    """Masks of an earlier call still lie in the session's buffer behind a later, shorter list: a device index that
+    points there leaves the row as it is, as does one far outside."""
+    import torch
+    w = configs.get("tiny_f32_b3")
+    prompts = synth.prompts(w)
+    words, B = (w.vocab + 31) // 32, w.block_size
+    only = np.zeros((3, words), np.uint32)   # mask k allows token k alone
+    only[:, 0] = [1, 2, 4]
+    dev = lambda x: torch.from_numpy(np.asarray(x, np.int32)).cuda()  # noqa: E731
+    sess = _session(w, max_seq_len=max(w.prompt_lens) + 8 * B)
+    try:
+        plain = sess.prefill(prompts)
+        sess.set_token_masks(dev(only.view(np.int32)), dev([0, 1, 2]))
+        np.testing.assert_array_equal(sess.prefill(prompts), [0, 1, 2])
+        sess.set_token_masks(dev(only[2:].view(np.int32)), dev([0, 1, 2]))   # one mask: 1 and 2 lie behind it
+        np.testing.assert_array_equal(sess.prefill(prompts), [2, plain[1], plain[2]])
+        sess.set_token_masks(dev(only[2:].view(np.int32)), dev([1 << 30, -(1 << 31), 0]))
+        np.testing.assert_array_equal(sess.prefill(prompts), [plain[0], plain[1], 2])
+        # the same in verified rows
+        d = sess.draft_block()
+        sess.set_token_masks(dev(only[:1].view(np.int32)), dev([0] + [1] * (3 * B - 1)))
+        acc, bonus = sess.verify(d)
+        assert d[0][0] != 0 and (int(acc[0]), int(bonus[0])) == (0, 0)
+        sess.set_token_masks(dev(only[2:].view(np.int32)), dev([1, 1, 0]))
+        sess.prefill(prompts)
+        np.testing.assert_array_equal(sess.draft_block(), d)
+        a2, b2 = sess.verify(d)   # without masks: the rows above that were not masked
+        np.testing.assert_array_equal(a2[1:], acc[1:])
+        np.testing.assert_array_equal(b2[1:], bonus[1:])
+    finally:
+        sess.close()
