@@ -630,7 +630,9 @@ __global__ void __launch_bounds__(LT, 2) verify_sample_kernel(
                 const LawStat ts = tstat[s * B + j], ds = dstat[s * B + j + 1];
                 const float p = law_weight_x(logits[(size_t)(s * B + j) * V + y], y, ts, inv_tv) / ts.s;
                 const float q = law_weight_x(dlogits[(size_t)(s * B + j + 1) * V + y], y, ds, inv_td) / ds.s;
-                const float ratio = q > 0.f ? fminf(1.f, p / q) : 1.f;
+                // (a proposal outside the drafter's law is accepted where the target's law has it at all: a token that a
+                // filter, a mask or a bias closes has p = 0 and is never emitted)
+                const float ratio = q > 0.f ? fminf(1.f, p / q) : p > 0.f ? 1.f : 0.f;
                 ok = clamp_u(u[j]) < ratio;
             }
         }

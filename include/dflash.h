@@ -283,7 +283,8 @@ dflash_status dflash_verify(dflash_ctx* ctx, const int32_t* draft_tokens, int32_
  *
  * dflash_verify_sampled: one causal target pass as dflash_verify; with
  * p_j = softmax(verify logits_j / T), filtered, proposal j (block row j+1) is accepted
- * while u_verify[s*B + j] < min(1, p_j(y)/q_{j+1}(y)); at the first rejection
+ * while u_verify[s*B + j] < min(1, p_j(y)/q_{j+1}(y)) (where q_{j+1}(y) = 0:
+ * always if p_j(y) > 0, else never); at the first rejection
  * the emitted token is drawn from [p_a - q_{a+1}]_+ (normalised), else from
  * p_{B-1}, with u_verify[s*B + B-1].  Caches keep the anchor and the a_i
  * accepted rows (n_i += a_i + 1); the emitted token is the next anchor.

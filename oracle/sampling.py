@@ -92,8 +92,11 @@ def sample_inverse_cdf(weights: np.ndarray, u: float) -> int:
 
 
 def accept_probability(p_y: float, q_y: float) -> float:
-    """eq. 6: min(1, p(y) / q(y))."""
-    return 1.0 if q_y <= 0.0 else min(1.0, p_y / q_y)
+    """eq. 6: min(1, p(y) / q(y)).  A proposal outside the drafter's law (q(y) = 0) is accepted where the target's
+    law has it at all: a token of p(y) = 0 (filtered, masked) is never emitted."""
+    if q_y <= 0.0:
+        return 1.0 if p_y > 0.0 else 0.0
+    return min(1.0, p_y / q_y)
 
 
 def residual(p: np.ndarray, q: np.ndarray):

@@ -395,3 +395,75 @@ def test_a_device_mask_index_behind_the_masks_means_no_mask():
         np.testing.assert_array_equal(b2[1:], bonus[1:])
     finally:
         sess.close()
+
+
+@pytest.mark.parametrize("filtered", [False, True])
+def test_masked_sampled_rounds_emit_open_tokens_alone(filtered):
+    """Masks and -inf biases in sampled rounds, with proposals from any law: no closed token is accepted or emitted,
+    filtered or not."""
+    w = configs.get("tiny_f32_b3")
+    prompts = synth.prompts(w)
+    V, B, n = w.vocab, w.block_size, 10
+    states = np.stack([np.arange(V) % 3 == k for k in range(3)])
+    masks = _pack(states)
+    banned = 9
+    rng = np.random.default_rng(4)
+    sess = _session(w, keep_logits=True, max_seq_len=max(w.prompt_lens) + (n + 2) * B)
+    tested = 0
+    try:
+        sess.set_logit_rules(bias={banned: -np.inf})
+        if filtered:
+            sess.set_sampling_filter(top_k=5)
+        sess.set_token_masks(masks, [0, 1, 2])
+        anchor = sess.prefill(prompts)
+        assert [int(t) % 3 for t in anchor] == [0, 1, 2] and banned not in anchor
+        for r in range(n):
+            u = rng.random((3, B - 1)).astype(np.float32)
+            d = sess.draft_block_sampled(1.0, u)
+            dlog = sess.logits("draft")
+            state = rng.integers(0, 3, (3, B))
+            for s in range(3):
+                # proposals that the drafter's own filtered law does not have (its least likely tokens), open ones and
+                # closed ones in turn
+                for j in range(B - 1):
+                    want = states[state[s, j]] if (r + s + j) % 2 else ~states[state[s, j]]
+                    d[s, j] = np.flatnonzero(want)[np.argmin(dlog[s, j + 1][want])]
+            if r % 3 == 2:
+                d[:, 0], state[:, 0] = banned, 0
+            sess.set_token_masks(masks, state.reshape(-1))
+            acc, emit = sess.verify_sampled(1.0, d, (0.999 * rng.random((3, B))).astype(np.float32))
+            for s in range(3):
+                row = np.arange(int(acc[s]) + 1)
+                out = np.append(d[s][:acc[s]], emit[s])
+                assert (out % 3 == state[s, row]).all() and banned not in out, (r, s, out, state[s])
+                tested += len(out)
+    finally:
+        sess.close()
+    assert tested >= 3 * n
+
+
+def test_a_proposal_outside_the_drafters_law_is_accepted_where_the_target_has_it():
+    """A mask that leaves one token: p is 1 there.  Proposed although the drafter's top-1 law lacks it, it is accepted
+    (and every closed one refused)."""
+    w = configs.get("tiny_f32_b3")
+    V, B = w.vocab, w.block_size
+    sess = _session(w, keep_logits=True, max_seq_len=max(w.prompt_lens) + 4 * B)
+    try:
+        sess.set_sampling_filter(top_k=1)
+        sess.prefill(synth.prompts(w))
+        d = sess.draft_block_sampled(1.0, np.full((3, B - 1), 0.5, np.float32))
+        only = np.zeros((3 * B, V), bool)
+        tok = np.zeros((3, B), np.int64)
+        for s in range(3):
+            for j in range(B):
+                tok[s, j] = (int(d[s, min(j, B - 2)]) + 1 + j) % V   # not the drafter's
+                only[s * B + j, tok[s, j]] = True
+        sess.set_token_masks(_pack(only), np.arange(3 * B))
+        prop = tok[:, :B - 1].astype(np.int32)
+        prop[1, 1] = (prop[1, 1] + 1) % V                            # closed
+        prop[2, 0] = d[2, 0]                                         # the drafter's own, closed
+        acc, emit = sess.verify_sampled(1.0, prop, np.full((3, B), 0.5, np.float32))
+        assert acc.tolist() == [B - 1, 1, 0]
+        assert emit.tolist() == [tok[0, B - 1], tok[1, 1], tok[2, 0]]
+    finally:
+        sess.close()

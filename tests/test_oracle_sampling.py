@@ -181,3 +181,11 @@ def test_all_accepted_emits_the_bonus_from_the_last_block_row():
         assert rd.bonus == draws[B1]
         seen_rows.update(j for j in range(B1) if draws[j] != draws[B1])
     assert seen_rows == set(range(B1))   # every other row's law would have given a different token somewhere
+
+
+def test_a_token_outside_the_target_law_is_never_accepted():
+    """p(y) = 0 (filtered or masked) is a rejection whatever the drafter's law is; outside the drafter's law alone it
+    is an acceptance."""
+    assert sp.accept_probability(0.0, 0.0) == 0.0
+    assert sp.accept_probability(0.0, 0.5) == 0.0
+    assert sp.accept_probability(1e-300, 0.0) == 1.0
