@@ -167,6 +167,7 @@ struct dflash_ctx {
     int* hist_len = nullptr;    // [max_batch]
     int* prompt_len = nullptr;  // [max_batch]
     bool masks_on = false;      // for the next target pass
+    bool masks_verify = false;  // ... which is the verify of the block that was drafted when they were set
     int mask_rows = 0;
     uint32_t* masks = nullptr;  // [max_batch * Bmax][mask_words]
     int mask_words = 0;
@@ -1249,7 +1250,7 @@ dflash_status check_prompts(dflash_ctx* c, int batch, int prefix, const int32_t*
     }
     for (size_t i = 0; i < *total; ++i)
         if (toks[i] < 0 || toks[i] >= c->V) return c->fail(DFLASH_E_INVAL, "prompt token %zu = %d outside [0, %d)", i, toks[i], c->V);
-    if (c->masks_on && c->mask_rows != batch)
+    if (c->masks_on && !c->masks_verify && c->mask_rows != batch)
         return c->fail(DFLASH_E_INVAL, "token masks were set for %d rows, the prefill has %d", c->mask_rows, batch);
     return DFLASH_OK;
 }
@@ -1257,6 +1258,7 @@ dflash_status check_prompts(dflash_ctx* c, int batch, int prefix, const int32_t*
 // Pages for a new batch: `shared` whole pages of slot 0 at the head of every slot's table, then each
 // prompt's own (+ one block).  On failure every page returns to the pool and the session is empty.
 dflash_status pool_prompts(dflash_ctx* c, int batch, int shared, int prefix, const int32_t* lens) {
+    if (c->masks_verify) c->masks_on = false;  // (a verify that this prefill takes the place of)
     pool_reset(c);
     for (int s = 0; s < batch; ++s) {
         if (s && shared) c->pool.share(s, 0, shared);
@@ -1715,8 +1717,10 @@ dflash_status dflash_set_logit_rules(dflash_ctx* c, const dflash_logit_rules* r)
 dflash_status dflash_set_token_masks(dflash_ctx* c, int32_t n_masks, const uint32_t* masks, int32_t rows,
                                      const int32_t* mask_index) {
     if (!c) return DFLASH_E_INVAL;
-    c->masks_on = false;
-    if (n_masks == 0) return DFLASH_OK;
+    if (n_masks == 0) {
+        c->masks_on = false;
+        return DFLASH_OK;
+    }
     const int most = c->cfg.max_batch * c->Bmax;
     if (n_masks < 0 || n_masks > most || !masks || !mask_index)
         return c->fail(DFLASH_E_INVAL, "n_masks %d outside [0, %d], or a NULL argument", n_masks, most);
@@ -1735,6 +1739,7 @@ dflash_status dflash_set_token_masks(dflash_ctx* c, int32_t n_masks, const uint3
     if (!on_device)
         for (int i = 0; i < rows; ++i)
             if (mask_index[i] >= n_masks) return c->fail(DFLASH_E_INVAL, "mask index %d = %d, with %d masks", i, mask_index[i], n_masks);
+    c->masks_on = false;  // (from here on the buffers change: masks set before are gone if a copy fails)
     CUDA_TRY(c, cudaMemcpyAsync(c->masks, masks, (size_t)n_masks * c->mask_words * 4, cudaMemcpyDefault, c->stream));
     CUDA_TRY(c, cudaMemcpyAsync(c->mask_index, mask_index, (size_t)rows * 4, cudaMemcpyDefault, c->stream));
     if (on_device) {  // (the passes may be captured with the buffers' capacity: what lies behind these masks is never theirs)
@@ -1743,6 +1748,7 @@ dflash_status dflash_set_token_masks(dflash_ctx* c, int32_t n_masks, const uint3
         if (s) return s;
     }
     c->masks_on = true;
+    c->masks_verify = c->state == ST_DRAFTED;
     c->mask_rows = rows;
     return DFLASH_OK;
 }

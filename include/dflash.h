@@ -334,13 +334,14 @@ dflash_status dflash_set_logit_rules(dflash_ctx* ctx, const dflash_logit_rules* 
 
 /* Token masks (grammar states) of the next target pass alone: between a draft
  * and its verify, of that verify (rows = batch * B, row j of a block masks the
- * token after its first j drafts); otherwise of the next prefill's first
- * tokens (rows = its batch; a draft drops them).  masks: [n_masks][ceil(V / 32)] bit sets, host or
- * device, copied (bit v % 32 of word v / 32: token v is allowed); mask_index:
- * [rows], host or device, < 0: no mask, as is a device index >= n_masks (a
- * host one is refused).  n_masks 0 drops the masks.  A row that
- * the masks and biases leave without a token is E_DEVICE_CHECK at the next
- * synchronising call.
+ * token after its first j drafts; a prefill in the verify's place drops them);
+ * otherwise of the next prefill's first tokens (rows = its batch; a draft drops
+ * them).  masks: [n_masks][ceil(V / 32)] bit sets, host or device, copied (bit
+ * v % 32 of word v / 32: token v is allowed); mask_index: [rows], host or
+ * device, < 0: no mask, as is a device index >= n_masks (a host one is
+ * refused).  n_masks 0 drops the masks; a refused call leaves those set before.
+ * A row that the masks and biases leave without a token is E_DEVICE_CHECK at
+ * the next synchronising call.
  * Errors: E_INVAL (sizes, NULL, n_masks above max_batch * block_size, a host
  * index >= n_masks), E_NOMEM, E_CUDA. */
 dflash_status dflash_set_token_masks(dflash_ctx* ctx, int32_t n_masks, const uint32_t* masks, int32_t rows,

@@ -467,3 +467,64 @@ def test_a_proposal_outside_the_drafters_law_is_accepted_where_the_target_has_it
         assert emit.tolist() == [tok[0, B - 1], tok[1, 1], tok[2, 0]]
     finally:
         sess.close()
+
+
+def test_refused_masks_leave_those_set_before():
+    """Masks set for a verify or a prefill, then refused ones: the pass runs under the first."""
+    from block_diffusion_speculative_ctx_gb300 import DFLASH_E_INVAL, DFlashError
+    w = configs.get("tiny_f32_b3")
+    prompts = synth.prompts(w)
+    words, B = (w.vocab + 31) // 32, w.block_size
+    only = np.zeros((2, words), np.uint32)
+    only[:, 0] = [1 << 5, 1 << 6]
+
+    def refused(sess, rows):
+        for bad in ((only, [2] + [0] * (rows - 1)), (only, [0] * (rows + 1) if rows != 3 else []),
+                    (np.zeros((3 * B + 1, words), np.uint32), [0] * rows)):
+            with pytest.raises(DFlashError) as e:
+                sess.set_token_masks(*bad)
+            assert e.value.status == DFLASH_E_INVAL
+
+    sess = _session(w, max_seq_len=max(w.prompt_lens) + 8 * B)
+    try:
+        sess.set_token_masks(only, [0, 1, 0])
+        refused(sess, 3)
+        assert sess.prefill(prompts).tolist() == [5, 6, 5]
+        d = np.full_like(sess.draft_block(), 7)
+        sess.set_token_masks(only, [0, 1, 1] * B)
+        refused(sess, 3 * B)
+        with pytest.raises(DFlashError):   # a refused verify keeps them too
+            sess.verify(np.full_like(d, w.vocab))
+        acc, bonus = sess.verify(d)
+        assert acc.tolist() == [0, 0, 0] and bonus.tolist() == [[5, 6, 6][(s * B) % 3] for s in range(3)]
+    finally:
+        sess.close()
+
+
+def test_a_prefill_drops_the_masks_of_the_verify_it_takes_the_place_of():
+    """Masks set after a draft belong to its verify: a prefill instead runs without them, whether or not their number
+    of rows is its batch, and a refused prefill leaves them."""
+    from block_diffusion_speculative_ctx_gb300 import DFlashError
+    w = configs.get("tiny_f32_b3")
+    prompts = synth.prompts(w)
+    words, B = (w.vocab + 31) // 32, w.block_size
+    only = np.zeros((1, words), np.uint32)
+    only[0, 0] = 1 << 5
+    sess = _session(w, max_seq_len=max(w.prompt_lens) + 8 * B)
+    try:
+        plain = sess.prefill(prompts)
+        assert 5 not in plain
+        for block in (B, 1):   # 3 B rows, then 3: as many as the prefill has
+            sess.set_block_size(block)
+            sess.draft_block()
+            sess.set_token_masks(only, [0] * (3 * block))
+            np.testing.assert_array_equal(sess.prefill(prompts), plain)
+            d = sess.draft_block()
+            sess.set_token_masks(only, [0] * (3 * block))
+            with pytest.raises(DFlashError):
+                sess.prefill([prompts[0][:0], prompts[1], prompts[2]])
+            acc, bonus = sess.verify(d)
+            assert acc.tolist() == [0, 0, 0] and bonus.tolist() == [5, 5, 5]
+            np.testing.assert_array_equal(sess.prefill(prompts), plain)
+    finally:
+        sess.close()
