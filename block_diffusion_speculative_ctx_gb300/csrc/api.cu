@@ -266,6 +266,17 @@ bool is_device_ptr(const void* p) {
     return a.type == cudaMemoryTypeDevice || a.type == cudaMemoryTypeManaged;
 }
 
+// Page-locked host memory: an asynchronous copy from it is still reading when the call returns (one from pageable memory
+// has been staged by then).
+bool is_pinned_ptr(const void* p) {
+    cudaPointerAttributes a;
+    if (cudaPointerGetAttributes(&a, p) != cudaSuccess) {
+        cudaGetLastError();
+        return false;
+    }
+    return a.type == cudaMemoryTypeHost;
+}
+
 template <typename T>
 T* elem(void* base, size_t offset_elems) {
     return reinterpret_cast<T*>(base) + offset_elems;
@@ -1742,6 +1753,7 @@ dflash_status dflash_set_token_masks(dflash_ctx* c, int32_t n_masks, const uint3
     c->masks_on = false;  // (from here on the buffers change: masks set before are gone if a copy fails)
     CUDA_TRY(c, cudaMemcpyAsync(c->masks, masks, (size_t)n_masks * c->mask_words * 4, cudaMemcpyDefault, c->stream));
     CUDA_TRY(c, cudaMemcpyAsync(c->mask_index, mask_index, (size_t)rows * 4, cudaMemcpyDefault, c->stream));
+    if (is_pinned_ptr(masks) || is_pinned_ptr(mask_index)) CUDA_TRY(c, cudaStreamSynchronize(c->stream));
     if (on_device) {  // (the passes may be captured with the buffers' capacity: what lies behind these masks is never theirs)
         drop_indices(c->L(), c->mask_index, rows, n_masks);
         const dflash_status s = launch_check(c);

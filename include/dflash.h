@@ -340,6 +340,9 @@ dflash_status dflash_set_logit_rules(dflash_ctx* ctx, const dflash_logit_rules* 
  * v % 32 of word v / 32: token v is allowed); mask_index: [rows], host or
  * device, < 0: no mask, as is a device index >= n_masks (a host one is
  * refused).  n_masks 0 drops the masks; a refused call leaves those set before.
+ * Host arrays are the caller's again when the call returns (from page-locked
+ * memory it waits for the stream); device arrays must stay until the copy, on
+ * the session's stream, has run.
  * A row that the masks and biases leave without a token is E_DEVICE_CHECK at
  * the next synchronising call.
  * Errors: E_INVAL (sizes, NULL, n_masks above max_batch * block_size, a host

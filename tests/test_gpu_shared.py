@@ -528,3 +528,25 @@ def test_a_prefill_drops_the_masks_of_the_verify_it_takes_the_place_of():
             np.testing.assert_array_equal(sess.prefill(prompts), plain)
     finally:
         sess.close()
+
+
+def test_host_masks_are_the_callers_again_after_the_call():
+    """Page-locked masks and indices are overwritten as soon as the call returns, while the session's stream is still
+    busy with what was queued before."""
+    import torch
+    w = configs.get("tiny_f32_b3")
+    prompts = synth.prompts(w)
+    words = (w.vocab + 31) // 32
+    sess = _session(w)
+    try:
+        sess.prefill(prompts)
+        masks = torch.zeros((3, words), dtype=torch.int32).pin_memory()
+        masks[:, 0] = torch.tensor([1 << 5, 1 << 6, 1 << 7])
+        index = torch.tensor([2, 0, 1], dtype=torch.int32).pin_memory()
+        torch.cuda._sleep(50_000_000)
+        sess.set_token_masks(masks, index)
+        masks.fill_(1 << 9)
+        index.fill_(-1)
+        assert sess.prefill(prompts).tolist() == [7, 5, 6]
+    finally:
+        sess.close()
