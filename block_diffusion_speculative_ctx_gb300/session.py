@@ -186,6 +186,8 @@ class Session:
             raise ValueError(f"masks must be [n, {words}]")
         if not isinstance(masks, np.ndarray) and not (masks.is_contiguous() and masks.element_size() == 4):
             raise ValueError("masks must be contiguous 32-bit words")
+        if not isinstance(mask_index, np.ndarray) and not (mask_index.is_contiguous() and str(mask_index.dtype) == "torch.int32"):
+            raise ValueError("mask_index must be contiguous int32")
         n = mask_index.size if isinstance(mask_index, np.ndarray) else mask_index.numel()
         _check(self.ctx, self.lib.dflash_set_token_masks(self.ctx, masks.shape[0], _ptr(masks), int(n), _ptr(mask_index)))
 

@@ -194,3 +194,25 @@ def test_calls_on_a_kept_workspace_queue_one_at_a_time(monkeypatch):
         t.join()
     assert len(calls) == 60 and not any(overlaps)
     assert len({n for _, n in calls}) == 3
+
+
+def test_session_masks_refuse_other_index_types():
+    """A mask index of another type or with gaps would be read as other numbers."""
+    import torch
+    from types import SimpleNamespace
+    calls = []
+    sess = dfl.Session.__new__(dfl.Session)
+    sess.w, sess.ctx = SimpleNamespace(vocab=70), None
+    sess.lib = SimpleNamespace(dflash_set_token_masks=lambda ctx, n, masks, rows, index: calls.append((n, rows)) or 0)
+    masks = torch.zeros(2, 3, dtype=torch.int32)
+    index = torch.zeros(8, dtype=torch.int32)
+    for bad in (index.long(), index.float(), index[::2]):
+        with pytest.raises(ValueError, match="mask_index"):
+            sess.set_token_masks(masks, bad)
+    for bad in (masks.long(), masks[:, :2], masks.t().contiguous().t(), masks[0]):
+        with pytest.raises(ValueError, match="masks"):
+            sess.set_token_masks(bad, index)
+    assert not calls
+    sess.set_token_masks(masks, index)
+    sess.set_token_masks(masks.numpy(), [0, 1, -1])
+    assert calls == [(2, 8), (2, 3)]
