@@ -1701,8 +1701,8 @@ dflash_status dflash_set_logit_rules(dflash_ctx* c, const dflash_logit_rules* r)
     for (size_t i = 0; i < mb; ++i) {
         const float a = r->repetition ? r->repetition[i] : 1.f, b = r->presence ? r->presence[i] : 0.f,
                     f = r->frequency ? r->frequency[i] : 0.f;
-        if (!(a > 0.f) || !std::isfinite(a) || !std::isfinite(b) || !std::isfinite(f))
-            return c->fail(DFLASH_E_INVAL, "sequence %zu: repetition %g must be positive, presence %g and frequency %g finite", i, a, b, f);
+        if (!(a >= 0x1p-126f && a <= 0x1p126f) || !std::isfinite(b) || !std::isfinite(f))
+            return c->fail(DFLASH_E_INVAL, "sequence %zu: repetition %g must lie in [2^-126, 2^126], presence %g and frequency %g finite", i, a, b, f);
     }
     for (size_t i = 0; i < nb; ++i)
         if (r->bias_ids[i] >= c->V || std::isnan(r->bias_values[i]) || r->bias_values[i] == INFINITY)

@@ -33,7 +33,9 @@ namespace {
 constexpr int NT = 256, DEPTH = 2;
 constexpr uint32_t IN_PROMPT = 0x80000000u, IS_DRAFT = 0x40000000u, COUNT = 0x3FFFFFFFu;
 
-// A sequence's penalties; x / repetition is x times the reciprocal (one rounding more).
+// A sequence's penalties; x / repetition is x times the rounded reciprocal (one rounding more, and the reciprocal has to be
+// a normal number).  By an fp32 division a token 64 bf16 rows of 128256 take 22.1 us (so 18.1) and 512 rows of 151936 112 (so
+// 106); the product corrected by its remainder, twice, 19.2 and 110; with a power of two for any penalty 18.7 and 108.5.
 struct Rules {
     float rep, inv, pres, freq;
     const float* bias;  // the sequence's bias_values

@@ -320,8 +320,8 @@ dflash_status dflash_set_sampling_filter(dflash_ctx* ctx, int32_t top_k, float t
  * under the same rules.  The drafter's laws are not changed (a proposal may
  * come from any law).  The temperature and the filter act on the result.
  * Logits kept for dflash_inspect are those before the rules.
- * Errors: E_INVAL (repetition not positive, a value not finite (a bias may be
- * -inf), an id >= V, bias_width outside [0, 4096]), E_NOMEM. */
+ * Errors: E_INVAL (repetition outside [2^-126, 2^126], a value not finite (a
+ * bias may be -inf), an id >= V, bias_width outside [0, 4096]), E_NOMEM. */
 typedef struct {
     const float* repetition;
     const float* presence;
@@ -598,7 +598,10 @@ size_t dflash_shared_prefix_workspace(int32_t dtype, int32_t n_heads, int32_t n_
  *   x = x - frequency * c;   c > 0:  x = x - presence
  *   x = x + bias_values of the last entry of bias_ids[s] that is v
  *   bit v of the row's mask is 0:    x = -inf
- * in fp32, rounded once to the logits' type.  A mask that allows no token
+ * in fp32, rounded once to the logits' type; x / repetition is the product of x
+ * and the penalty's reciprocal, each rounded to fp32, for penalties between
+ * 2^-126 and 2^126 (beyond, the reciprocal overflows or loses bits).  A mask
+ * that allows no token
  * leaves a row of -inf.  Ids outside [0, vocab) in history, drafts and
  * bias_ids are skipped (padding); a mask_index outside [0, n_masks) means no
  * mask; hist_lens is clamped to [0, hist_width], prompt_lens to [0, hist_lens].

@@ -550,3 +550,18 @@ def test_host_masks_are_the_callers_again_after_the_call():
         assert sess.prefill(prompts).tolist() == [7, 5, 6]
     finally:
         sess.close()
+
+
+def test_repetition_penalties_without_a_normal_reciprocal_are_refused():
+    from block_diffusion_speculative_ctx_gb300 import DFLASH_E_INVAL, DFlashError
+    w = configs.get("tiny_f32")
+    sess = _session(w)
+    try:
+        for r in (2.0 ** -127, 2.0 ** -149, 2.0 ** 127, float("inf"), 0.0, -1.0):
+            with pytest.raises(DFlashError) as e:
+                sess.set_logit_rules(repetition=r)
+            assert e.value.status == DFLASH_E_INVAL
+        for r in (2.0 ** -126, 2.0 ** 126):
+            sess.set_logit_rules(repetition=r)
+    finally:
+        sess.close()

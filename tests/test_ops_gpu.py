@@ -606,6 +606,32 @@ def test_process_logits_special_values():
     assert y[5] == -0.5 and y[6] == -0.5 and y[7] == 1.0
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_process_logits_repetition_over_its_range(dtype):
+    """Positive logits over the repetition penalty, others times it.  A quotient has the rounding of a reciprocal, that of a
+    product and that to the type (u = 2^-24: 2 u + u^2, and half a step of the type) and, where it is subnormal, up to a
+    step of the format in place of each; a product is rounded once in fp32, bit for bit."""
+    rep = torch.tensor([1.1, 3.0, 0.7, 2.0 ** -126, 1.3 * 2.0 ** -120, 2.0 ** 126, 1.9 * 2.0 ** 125, 49.0, 1.0, 2.0 ** -64])
+    n = len(rep)
+    g = torch.Generator().manual_seed(6)
+    x = torch.randn((n, 2000), generator=g).to(DT[dtype])
+    x[3:5] *= 2.0 ** -20
+    x[:, 7] = float("inf")
+    hist = torch.arange(2000, dtype=torch.int32).repeat(n, 1)
+    lens = i32([2000] * n)
+    for prompt in (lens, i32([0] * n)):   # seen in the prompt, or after it
+        y = dfl().process_logits(x.cuda(), history=hist.cuda(), hist_lens=lens, prompt_lens=prompt, repetition=rep.cuda()).cpu()
+        pos, f = x.float() > 0, x.float()
+        times = (f * rep[:, None]).to(DT[dtype])
+        assert torch.equal(y[~pos], times[~pos])
+        want = x.double() / rep.double()[:, None]
+        finite = pos & want.isfinite()
+        assert (y[pos & ~finite] == float("inf")).all()
+        half, step = (0.0, 2.0 ** -149) if dtype == "f32" else (2.0 ** -8, 2.0 ** -133)
+        tol = (2 * 2.0 ** -24 + 2.0 ** -48 + half) * want.abs() * (1 + 2.0 ** -8) + 2 * step * (want.abs() < 2.0 ** -126)
+        assert ((y.double() - want).abs()[finite] <= tol[finite]).all()
+
+
 def test_process_logits_duplicates_and_padding():
     """The same id many times in the history, the drafts and the bias list (its last entry counts)."""
     x = torch.zeros(4, 64)
