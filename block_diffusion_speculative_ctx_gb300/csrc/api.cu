@@ -257,6 +257,15 @@ void* dev_alloc(dflash_ctx* c, size_t bytes) {
     return p;
 }
 
+// Gives one of dev_alloc's buffers back (null: nothing); what still uses it must have run.
+void dev_free(dflash_ctx* c, void* p) {
+    const auto i = std::find(c->allocs.begin(), c->allocs.end(), p);
+    if (!p || i == c->allocs.end()) return;
+    c->allocs.erase(i);
+    if (c->cfg.free) c->cfg.free(p, c->cfg.alloc_user);
+    else cudaFree(p);
+}
+
 bool is_device_ptr(const void* p) {
     cudaPointerAttributes a;
     if (cudaPointerGetAttributes(&a, p) != cudaSuccess) {
@@ -1205,6 +1214,8 @@ dflash_status start_rules(dflash_ctx* c, int batch) {
         c->pres = (float*)dev_alloc(c, mb * 4);
         c->freq = (float*)dev_alloc(c, mb * 4);
         if (!c->history || !c->hist_len || !c->prompt_len || !c->rep || !c->pres || !c->freq) {
+            for (void* p : {(void*)c->history, (void*)c->hist_len, (void*)c->prompt_len, (void*)c->rep, (void*)c->pres, (void*)c->freq})
+                dev_free(c, p);
             c->history = nullptr;
             return c->fail(DFLASH_E_NOMEM, "allocation of the token history failed");
         }
@@ -1217,14 +1228,17 @@ dflash_status start_rules(dflash_ctx* c, int batch) {
     }
     const size_t nb = mb * c->bias_width;
     if (nb > c->bias_cap) {
-        c->bias_id = (int*)dev_alloc(c, nb * 4);
-        c->bias_val = (float*)dev_alloc(c, nb * 4);
-        c->bias_cap = 0;
-        if (!c->bias_id || !c->bias_val) return c->fail(DFLASH_E_NOMEM, "allocation of the bias lists failed");
-        c->bias_cap = nb;
         // captured passes hold the old buffers
+        CUDA_TRY(c, cudaStreamSynchronize(c->stream));
         reset_graph(c->g_verify);
         reset_graph(c->g_verify_s);
+        dev_free(c, c->bias_id);
+        dev_free(c, c->bias_val);
+        c->bias_cap = 0;
+        c->bias_id = (int*)dev_alloc(c, nb * 4);
+        c->bias_val = (float*)dev_alloc(c, nb * 4);
+        if (!c->bias_id || !c->bias_val) return c->fail(DFLASH_E_NOMEM, "allocation of the bias lists failed");
+        c->bias_cap = nb;
     }
     CUDA_TRY(c, cudaMemcpyAsync(c->rep, c->rep_h.data(), mb * 4, cudaMemcpyHostToDevice, c->stream));
     CUDA_TRY(c, cudaMemcpyAsync(c->pres, c->pres_h.data(), mb * 4, cudaMemcpyHostToDevice, c->stream));
@@ -1652,8 +1666,10 @@ dflash_status dflash_prefill_shared(dflash_ctx* c, int32_t batch, int32_t prefix
             int* tab_d = (int*)dev_alloc(c, 2 * mb * 4);
             int* st_d = (int*)dev_alloc(c, 16);
             void* ws_d = dev_alloc(c, ws);
-            if (!ws || !lens_d || !start_d || !tab_d || !st_d || !ws_d)
+            if (!ws || !lens_d || !start_d || !tab_d || !st_d || !ws_d) {
+                for (void* p : {(void*)lens_d, (void*)start_d, (void*)tab_d, (void*)st_d, ws_d}) dev_free(c, p);
                 return c->fail(DFLASH_E_NOMEM, "allocation of %zu bytes for the shared-prefix attention failed", ws);
+            }
             c->own_lens = lens_d;
             c->own_start = start_d;
             c->tab_in = tab_d;
@@ -1742,7 +1758,11 @@ dflash_status dflash_set_token_masks(dflash_ctx* c, int32_t n_masks, const uint3
     if (!c->masks) {
         uint32_t* m = (uint32_t*)dev_alloc(c, (size_t)most * c->mask_words * 4);
         int* i = (int*)dev_alloc(c, (size_t)most * 4);
-        if (!m || !i) return c->fail(DFLASH_E_NOMEM, "allocation of the token masks failed");
+        if (!m || !i) {
+            dev_free(c, m);
+            dev_free(c, i);
+            return c->fail(DFLASH_E_NOMEM, "allocation of the token masks failed");
+        }
         c->masks = m;
         c->mask_index = i;
     }

@@ -565,3 +565,71 @@ def test_repetition_penalties_without_a_normal_reciprocal_are_refused():
             sess.set_logit_rules(repetition=r)
     finally:
         sess.close()
+
+
+def test_growing_bias_lists_give_the_old_ones_back():
+    """A bias map that grows token by token: the session holds one pair of lists, and tokens follow the new one (the kept
+    logits are those before the rules)."""
+    w = configs.get("tiny_f32_b3")
+    prompts = synth.prompts(w)
+    sess = _session(w, keep_logits=True, max_seq_len=max(w.prompt_lens) + 8 * w.block_size)
+    bias = np.zeros(w.vocab, np.float32)
+    try:
+        held = []
+        for n in range(1, 30):
+            bias[19 + n] = 50.0 + 19 + n
+            sess.set_logit_rules(bias={t: 50.0 + t for t in range(20, 20 + n)})
+            first = sess.prefill(prompts)
+            np.testing.assert_array_equal(first, (sess.logits("prefill") + bias).argmax(-1))
+            acc, bonus = sess.verify(sess.draft_block())
+            best = (sess.logits("verify") + bias).argmax(-1)
+            assert bonus.tolist() == [best[s, acc[s]] for s in range(3)]
+            assert all(20 <= t < 20 + n for t in (*first, *bonus))
+            held.append(len(sess.alloc.live))
+        assert len(set(held)) == 1, held
+        sess.set_logit_rules(bias={30: 99.0})   # shorter again: the lists stay
+        assert sess.prefill(prompts).tolist() == [30] * 3 and len(sess.alloc.live) == held[0]
+    finally:
+        sess.close()
+        assert not sess.alloc.live
+
+
+def test_a_failed_allocation_leaves_nothing_behind():
+    """The allocator refuses each of the shared prefix's, the rules' and the masks' buffers in turn: E_NOMEM, nothing more
+    held than before, and the call succeeds once it can."""
+    from block_diffusion_speculative_ctx_gb300 import DFLASH_E_NOMEM, DFlashError
+    from block_diffusion_speculative_ctx_gb300 import session as sm
+    left = [1 << 30]
+    real = sm._TorchAllocator
+
+    class Allocator(real):
+        def _alloc(self, nbytes, user):
+            left[0] -= 1
+            return None if left[0] < 0 else super()._alloc(nbytes, user)
+
+    w = configs.get("tiny_f32_b3")
+    prefix, own = _prompts(w, 70, (20, 7, 19), 9)
+    w = w.with_(prompt_lens=tuple(70 + len(p) for p in own))
+    sm._TorchAllocator = Allocator
+    try:
+        sess = _session(w, max_seq_len=max(w.prompt_lens) + 8 * w.block_size)
+    finally:
+        sm._TorchAllocator = real
+    try:
+        masks = np.full((1, (w.vocab + 31) // 32), 0xFFFFFFFF, np.uint32)
+        steps = [lambda: sess.prefill_shared(prefix, own),
+                 lambda: sess.set_logit_rules(repetition=1.1) or sess.prefill(own),
+                 lambda: sess.set_token_masks(masks, [0, 0, 0])]
+        for step, buffers in zip(steps, (5, 6, 2)):
+            before = len(sess.alloc.live)
+            for k in range(buffers):
+                left[0] = k
+                with pytest.raises(DFlashError) as e:
+                    step()
+                assert e.value.status == DFLASH_E_NOMEM and len(sess.alloc.live) == before, k
+            left[0] = 1 << 30
+            step()
+            assert len(sess.alloc.live) == before + buffers
+    finally:
+        left[0] = 1 << 30
+        sess.close()
