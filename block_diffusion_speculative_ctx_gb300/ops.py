@@ -75,7 +75,9 @@ _WORKSPACE = {}  # bytes by (dtype, H, H_kv, hd, batch, rows)
 # costs 5 us of the 17 that a small one takes.  A call queues two kernels, the second of which reads what the first left in
 # the workspace, and the C call runs without the interpreter's lock: so a call that uses a kept workspace holds _KEPT_LOCK
 # from looking it up until both are queued (the stream then runs the calls one after the other, whichever threads made
-# them).  Re-entrant, for a call out of a signal handler or a finalizer.
+# them).  Re-entrant, for a call out of a signal handler or a finalizer.  Kept up to KEPT_MAX bytes (32 verify blocks of 16 rows
+# of 32 heads take 92 MB): calls that need more run for hundreds of microseconds and allocate theirs.
+KEPT_MAX = 256 << 20
 _KEPT = {}
 _KEPT_LOCK = threading.RLock()
 _raw_stream, _current_device = torch._C._cuda_getCurrentRawStream, torch.cuda.current_device
@@ -245,7 +247,7 @@ def shared_prefix_attention(q, k_cache, v_cache, prefix_pages, prefix_len: int, 
     hd ** -0.5.  Returns (out, lse); rows outside q_start keep what ``out`` and ``lse`` held (0 where they
     are allocated here).  ``workspace``: uint8, at least ``shared_prefix_workspace`` bytes; calls that may
     run at the same time need one each.  None: allocated for the call, or on a device's default stream the
-    largest one needed there so far, which is kept."""
+    largest one of up to 256 MB needed there so far, which is kept."""
     if q.dim() != 3 or k_cache.dim() != 4:
         _bad("q must be [rows, H, hd] and the caches [pages, H_kv, 64, hd]")
     dev = _device(q, q, k_cache, v_cache)
@@ -293,7 +295,7 @@ def shared_prefix_attention(q, k_cache, v_cache, prefix_pages, prefix_len: int, 
         if len(_WORKSPACE) > 4096:
             _WORKSPACE.clear()
         n_ws = _WORKSPACE[sizes] = load().dflash_shared_prefix_workspace(*sizes)
-    if _raw_stream(dev) != 0:
+    if n_ws > KEPT_MAX or _raw_stream(dev) != 0:
         workspace = torch.empty(n_ws, dtype=_U8T, device=q.device)
         _call(fn, _ATTN.pack, (*args, workspace.data_ptr(), n_ws), dev)
         return out, lse

@@ -216,3 +216,23 @@ def test_session_masks_refuse_other_index_types():
     sess.set_token_masks(masks, index)
     sess.set_token_masks(masks.numpy(), [0, 1, -1])
     assert calls == [(2, 8), (2, 3)]
+
+
+def test_no_workspace_is_kept_beyond_its_limit(monkeypatch):
+    """A large call on the default stream allocates for itself; what is kept stays within the limit.  (No GPU: the foreign
+    call is a stand-in.)"""
+    import torch
+    calls = []
+    monkeypatch.setattr(ops, "_call", lambda fn, pack, values, dev: calls.append(values[-2:]))
+    monkeypatch.setattr(ops, "_device", lambda *a: 0)
+    monkeypatch.setattr(ops, "_flat", lambda name, t, *a: t.data_ptr())
+    monkeypatch.setattr(ops, "_mat", lambda *a: 4)
+    monkeypatch.setattr(ops, "_rows3", lambda *a: 256)
+    monkeypatch.setattr(ops, "_raw_stream", lambda dev: 0)
+    monkeypatch.setattr(ops, "_KEPT", {})
+    c = torch.zeros(2, 2, 64, 64)
+    for rows in (1, 150000, 8, 150000, 1):
+        i = torch.zeros(2, dtype=torch.int32)
+        ops.shared_prefix_attention(torch.zeros(rows, 4, 64), c, c, None, 0, i[:1, None], i[:1], i)
+    assert [n > ops.KEPT_MAX for _, n in calls] == [False, True, False, True, False]
+    assert calls[2][0] == calls[4][0] == ops._KEPT[0][1] and ops._KEPT[0][0] == calls[2][1] <= ops.KEPT_MAX
