@@ -1,5 +1,5 @@
-// Checks of tensor arguments for the Python operators (ops.py), as a CPython extension: type, size, device and layout of a
-// tensor are read from the tensor itself instead of attribute by attribute through Python (some 0.4 us a tensor; a call
+// Checks of tensor arguments for the Python operators (ops.py), and the versions of the tensors that they write, as a CPython
+// extension: type, size, device and layout of a tensor are read from the tensor itself instead of attribute by attribute through Python (some 0.4 us a tensor; a call
 // takes up to twelve, and a small call is as long as its host side).
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
@@ -103,9 +103,24 @@ PyObject* rows3(PyObject*, PyObject* const* a, Py_ssize_t na) {
     });
 }
 
+// written(t, ...): the tensors (or None) have been written to: their versions rise, so that a backward pass that saved one of
+// them says so
+PyObject* written(PyObject*, PyObject* const* a, Py_ssize_t na) {
+    return guarded([&]() -> PyObject* {
+        for (Py_ssize_t i = 0; i < na; ++i) {
+            if (a[i] == Py_None) continue;
+            const at::Tensor* t = tensor(a[i]);
+            if (!t) return nullptr;
+            if (!t->is_inference()) t->unsafeGetTensorImpl()->bump_version();
+        }
+        Py_RETURN_NONE;
+    });
+}
+
 PyMethodDef methods[] = {{"flat", (PyCFunction)(void (*)(void))flat, METH_FASTCALL, nullptr},
                          {"mat", (PyCFunction)(void (*)(void))mat, METH_FASTCALL, nullptr},
                          {"rows3", (PyCFunction)(void (*)(void))rows3, METH_FASTCALL, nullptr},
+                         {"written", (PyCFunction)(void (*)(void))written, METH_FASTCALL, nullptr},
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_tensor_args", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 

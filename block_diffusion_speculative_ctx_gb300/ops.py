@@ -6,8 +6,10 @@ stateless calls of the C ABI (include/dflash.h, "serving operators").
     process_logits           penalties for repeated tokens, biases and grammar masks on logits
 
 Every call queues its kernels on torch's current stream of the tensors' device and
-returns without synchronising.  None has a gradient: tensors that require one are
-refused while autograd is recording."""
+returns without synchronising.  None has a gradient: tensors that require one, outputs
+among them, are refused while autograd is recording, and so are tensors with a
+forward-mode tangent.  Outputs of the caller's count as written in place (their versions
+rise)."""
 from __future__ import annotations
 
 import ctypes
@@ -19,6 +21,7 @@ import threading
 from typing import NamedTuple, Optional
 
 import torch
+from torch.autograd import forward_ad as _forward_ad
 
 from . import build as _build_mod
 from . import DFLASH_DTYPE_BF16, DFLASH_DTYPE_F32, DFLASH_OK, DFlashError, dflash_last_error, load
@@ -96,6 +99,10 @@ def _device(first, *floats):
         for t in floats:
             if t is not None and t.requires_grad:
                 _bad("a tensor requires a gradient, which these operators do not have")
+    if _forward_ad._current_level >= 0:
+        for t in floats:
+            if t is not None and _forward_ad.unpack_dual(t).tangent is not None:
+                _bad("a tensor carries a forward-mode tangent, which these operators do not have")
     return dev
 
 
@@ -137,13 +144,21 @@ def _rows3(name, t, dtype, rows, heads, hd, dev):
     return ld if rows > 1 else heads * hd
 
 
+def _written(*tensors):
+    """The tensors (or None) have been written to: their versions rise."""
+    for t in tensors:
+        if t is not None and not t.is_inference():
+            torch.autograd.graph.increment_version(t)
+
+
 _PYTHON_CHECKS = (_flat, _mat, _rows3)
+_PYTHON_WRITTEN = _written
 
 
 def _use_extension():
-    """The same three checks from csrc/tensor_args.cpp, where it has been built (a small call's host side is
+    """The same three checks (and _written) from csrc/tensor_args.cpp, where it has been built (a small call's host side is
     shorter by a third)."""
-    global _flat, _mat, _rows3
+    global _flat, _mat, _rows3, _written
     path = _build_mod.tensor_args_path()
     if path is None or not os.path.exists(path):
         return
@@ -151,9 +166,9 @@ def _use_extension():
         spec = importlib.util.spec_from_loader("_tensor_args", importlib.machinery.ExtensionFileLoader("_tensor_args", path))
         m = importlib.util.module_from_spec(spec)
         spec.loader.exec_module(m)
-    except ImportError:
+        _flat, _mat, _rows3, _written = m.flat, m.mat, m.rows3, m.written
+    except (ImportError, AttributeError):  # (AttributeError: built from an older source)
         return
-    _flat, _mat, _rows3 = m.flat, m.mat, m.rows3
 
 
 _use_extension()
@@ -233,6 +248,7 @@ def kv_tables(kv_lens, new_lens, table, free_pages=None, used=None, *, rows: Opt
                        p_used, p_out, p_uo, _flat("q_start", q_start, _I32T, batch + 1, dev),
                        _flat("row_seq", row_seq, _I32T, rows, dev), _flat("row_pos", row_pos, _I32T, rows, dev),
                        _flat("slots", slots, _I64T, rows, dev), p_status), dev)
+    _written(table_out, used_out, q_start, row_seq, row_pos, slots, status)
     return KVTables(table_out, used_out, q_start, row_seq, row_pos, slots, status)
 
 
@@ -250,7 +266,7 @@ def shared_prefix_attention(q, k_cache, v_cache, prefix_pages, prefix_len: int, 
     largest one of up to 256 MB needed there so far, which is kept."""
     if q.dim() != 3 or k_cache.dim() != 4:
         _bad("q must be [rows, H, hd] and the caches [pages, H_kv, 64, hd]")
-    dev = _device(q, q, k_cache, v_cache)
+    dev = _device(q, q, k_cache, v_cache, out, lse)
     rows, h, hd = q.shape
     kv_shape = k_cache.shape
     pages, hkv, page_tokens, kv_hd = kv_shape
@@ -288,23 +304,24 @@ def shared_prefix_attention(q, k_cache, v_cache, prefix_pages, prefix_len: int, 
     if workspace is not None:
         n_ws = workspace.numel() * workspace.element_size()
         _call(fn, _ATTN.pack, (*args, _flat("workspace", workspace, workspace.dtype, workspace.numel(), dev), n_ws), dev)
-        return out, lse
-    sizes = (dt, h, hkv, hd, batch, rows)
-    n_ws = _WORKSPACE.get(sizes)
-    if n_ws is None:
-        if len(_WORKSPACE) > 4096:
-            _WORKSPACE.clear()
-        n_ws = _WORKSPACE[sizes] = load().dflash_shared_prefix_workspace(*sizes)
-    if n_ws > KEPT_MAX or _raw_stream(dev) != 0:
-        workspace = torch.empty(n_ws, dtype=_U8T, device=q.device)
-        _call(fn, _ATTN.pack, (*args, workspace.data_ptr(), n_ws), dev)
-        return out, lse
-    with _KEPT_LOCK:
-        kept = _KEPT.get(dev)
-        if kept is None or kept[0] < n_ws:
+    else:
+        sizes = (dt, h, hkv, hd, batch, rows)
+        n_ws = _WORKSPACE.get(sizes)
+        if n_ws is None:
+            if len(_WORKSPACE) > 4096:
+                _WORKSPACE.clear()
+            n_ws = _WORKSPACE[sizes] = load().dflash_shared_prefix_workspace(*sizes)
+        if n_ws > KEPT_MAX or _raw_stream(dev) != 0:
             workspace = torch.empty(n_ws, dtype=_U8T, device=q.device)
-            kept = _KEPT[dev] = (n_ws, workspace.data_ptr(), workspace)
-        _call(fn, _ATTN.pack, (*args, kept[1], n_ws), dev)
+            _call(fn, _ATTN.pack, (*args, workspace.data_ptr(), n_ws), dev)
+        else:
+            with _KEPT_LOCK:
+                kept = _KEPT.get(dev)
+                if kept is None or kept[0] < n_ws:
+                    workspace = torch.empty(n_ws, dtype=_U8T, device=q.device)
+                    kept = _KEPT[dev] = (n_ws, workspace.data_ptr(), workspace)
+                _call(fn, _ATTN.pack, (*args, kept[1], n_ws), dev)
+    _written(out, lse)
     return out, lse
 
 
@@ -327,7 +344,7 @@ def process_logits(logits, *, rows_per_seq: int = 1, history=None, hist_lens=Non
     Returns ``out`` (allocated when None; ``out=logits`` works in place)."""
     if logits.dim() != 2:
         _bad("logits must be [rows, vocab]")
-    dev = _device(logits, logits, repetition, presence, frequency, bias_values)
+    dev = _device(logits, logits, repetition, presence, frequency, bias_values, out)
     n, vocab = logits.shape
     dtype = logits.dtype
     dt = _DTYPES.get(dtype)
@@ -385,4 +402,5 @@ def process_logits(logits, *, rows_per_seq: int = 1, history=None, hist_lens=Non
           _LOGITS.pack, (dt, batch, rows_per_seq, vocab, hist_width, bias_width, n_masks, 0, ld, ld_out, ld_hist, ld_mask,
                        logits.data_ptr(), out.data_ptr(), p_hist, p_len, p_prompt, p_draft, p_rep, p_pres, p_freq,
                        p_ids if bias_width else 0, p_val, p_mask if n_masks else 0, p_idx), dev)
+    _written(out)
     return out

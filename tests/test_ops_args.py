@@ -236,3 +236,43 @@ def test_no_workspace_is_kept_beyond_its_limit(monkeypatch):
         ops.shared_prefix_attention(torch.zeros(rows, 4, 64), c, c, None, 0, i[:1, None], i[:1], i)
     assert [n > ops.KEPT_MAX for _, n in calls] == [False, True, False, True, False]
     assert calls[2][0] == calls[4][0] == ops._KEPT[0][1] and ops._KEPT[0][0] == calls[2][1] <= ops.KEPT_MAX
+
+
+def test_versions_of_written_tensors_rise(lib):
+    """In either form of the binding's helper, views of a tensor included; inference tensors have no version."""
+    import torch
+    forms = [ops._PYTHON_WRITTEN]
+    if ops._written is ops._PYTHON_WRITTEN:
+        ops._use_extension()
+    if ops._written is not ops._PYTHON_WRITTEN:
+        forms.append(ops._written)
+    for f in forms:
+        t, i = torch.zeros(4, 4), torch.zeros(3, dtype=torch.int32)
+        f(t, None, i)
+        assert t._version == 1 and i._version == 1
+        f(t[1:])
+        assert t._version == 2
+        with torch.inference_mode():
+            z = torch.zeros(2)
+        f(z)
+
+
+def test_gradients_are_refused_in_both_modes():
+    import torch
+    from torch.autograd import forward_ad
+    from types import SimpleNamespace
+    first = SimpleNamespace(get_device=lambda: 0)
+    x = torch.zeros(3)
+    assert ops._device(first, x, None) == 0
+    with pytest.raises(ValueError, match="gradient"):
+        ops._device(first, x, x.clone().requires_grad_())
+    with torch.no_grad():
+        ops._device(first, x.clone().requires_grad_())
+    with forward_ad.dual_level():
+        ops._device(first, x, None)
+        dual = forward_ad.make_dual(x.clone(), torch.ones(3))
+        with pytest.raises(ValueError, match="tangent"):
+            ops._device(first, x, dual)
+        with torch.no_grad():
+            with pytest.raises(ValueError, match="tangent"):
+                ops._device(first, dual)

@@ -701,6 +701,49 @@ def test_the_bindings_refuse():
         m.shared_prefix_attention(*x[:4], 5.0, *x[5:])
 
 
+def test_autograd_sees_what_the_operators_write():
+    """Outputs that require a gradient and inputs with a tangent are refused; a tensor that autograd has saved and that a
+    call then writes over stops the backward pass, as any other write in place does."""
+    m = dfl()
+    c = attn_case("f32", (8, 2, 128), 64, [5], [1], seed=1)
+    x = attn_inputs(c)
+    out, lse = torch.zeros_like(x[0]), torch.zeros(1, 8, device="cuda")
+    for kw in (dict(out=out.clone().requires_grad_()), dict(out=out, lse=lse.clone().requires_grad_())):
+        with pytest.raises(ValueError, match="gradient"):
+            m.shared_prefix_attention(*x, **kw)
+        with torch.no_grad():
+            m.shared_prefix_attention(*x, **kw)
+    z = torch.zeros(2, 50, device="cuda")
+    with pytest.raises(ValueError, match="gradient"):
+        m.process_logits(z, out=z.clone().requires_grad_())
+    with torch.autograd.forward_ad.dual_level():
+        with pytest.raises(ValueError, match="tangent"):
+            m.process_logits(torch.autograd.forward_ad.make_dual(z, torch.ones_like(z)))
+
+    w = torch.ones(2, 50, device="cuda", requires_grad=True)
+    table = i32([[7, 7]])
+
+    def process(t):
+        m.process_logits(t, bias_ids=i32([[3], [4]]), bias_values=torch.ones(2, 1, device="cuda"), out=t)
+
+    def attend(t):
+        m.shared_prefix_attention(*x, out=t)
+
+    for write, t in ((process, z.clone()), (attend, out.clone())):
+        y = (t * torch.ones_like(t, requires_grad=True)).sum()   # saves t
+        write(t)
+        with pytest.raises(RuntimeError, match="inplace"):
+            y.backward()
+    y = w.index_select(1, table[0]).sum()   # saves the indices
+    m.kv_tables(i32([3]), i32([1]), table, i32([9]), i32([0]), rows=1, table_out=table)
+    with pytest.raises(RuntimeError, match="inplace"):
+        y.backward()
+    with torch.inference_mode():
+        t = torch.zeros(2, 50, device="cuda")
+        process(t)
+    process(t)
+
+
 def test_an_empty_batch_of_rows():
     c = attn_case("bf16", (8, 2, 128), 64, [5], [0], seed=1)
     out, lse = dfl().shared_prefix_attention(*attn_inputs(c))
