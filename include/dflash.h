@@ -540,11 +540,13 @@ dflash_status dflash_kv_tables(const dflash_kv_tables_args* args, void* cuda_str
  * [q_start[0], q_start[batch]) are left as they were.  The slots of a page
  * past the last valid token may hold anything; keys and values of valid
  * tokens must be finite.
- * Device-side checks: a sequence with a page outside [0, n_pages) among its
- * keys or with kv_lens[s] outside [0, 64 * width] gets NaN in its rows' out and
- * lse; every row of q does behind a bad prefix page, a q_start that decreases
- * or leaves [0, rows], work beyond 2^31 tiles of 64 keys, or a bounded device
- * wait that ran out.  Nothing is read or written out of range.
+ * Device-side checks: a sequence with kv_lens[s] outside [0, 64 * width] gets
+ * NaN in its rows' out and lse, one with a page outside [0, n_pages) among its
+ * keys in every row that sees the page (rows of the sequence before those may
+ * get NaN or their result).  Every row of every sequence gets NaN behind a bad
+ * prefix page or a bounded device wait that ran out, every row of q behind a
+ * q_start that decreases or leaves [0, rows] or work beyond 2^31 tiles of 64
+ * keys.  Nothing is read or written out of range.
  * dtype F32 or BF16 (q, caches and out); head_dim 64 or 128; H at most 1024 and
  * at most 64 times H_kv; q, the caches and out 16-byte aligned, ld_q and ld_out
  * multiples of 16 bytes.  out may be q (in place, with one row stride).

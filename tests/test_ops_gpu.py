@@ -403,6 +403,29 @@ def test_shared_prefix_attention_reports_bad_metadata(dtype, fault):
     attn_check(c, (out, lse), True)
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("page", [0, 2, 3])
+def test_shared_prefix_attention_bad_page_of_many_rows(dtype, page):
+    """A sequence of several row tiles: every row that sees the bad page is NaN, a row before it NaN or right, and the other
+    sequence and the rows of none are as they should be."""
+    c = attn_case(dtype, (8, 2, 128), 100, [200, 70], [200, 70], seed=43)
+    x = list(attn_inputs(c))
+    good = dfl().shared_prefix_attention(*x)
+    x[5][0, page] = -7
+    x[7] = x[7] + 2
+    out, lse = torch.full((274, 8, 128), 5.0, dtype=x[0].dtype, device="cuda"), torch.full((274, 8), 5.0, device="cuda")
+    q = torch.zeros_like(out)
+    q[2:272] = x[0]
+    dfl().shared_prefix_attention(q, *x[1:], out=out, lse=lse)
+    assert (out[[0, 1, 272, 273]] == 5.0).all() and (lse[[0, 1, 272, 273]] == 5.0).all()
+    out, lse = out[2:272], lse[2:272]
+    assert out[64 * page:200].isnan().all() and lse[64 * page:200].isnan().all()
+    assert not lse[200:].isnan().any()
+    nan = lse.isnan()
+    assert torch.equal(out.isnan(), nan[..., None].expand_as(out))
+    attn_check(c, (torch.where(nan[..., None], good[0], out), torch.where(nan, good[1], lse)), True)
+
+
 def test_shared_prefix_attention_past_32_bit_offsets():
     """Pages whose element offset passes 2^31 (and whose byte offset passes 2^32)."""
     hkv, hd = 8, 128
