@@ -666,6 +666,7 @@ struct Pass {
         a.width = c->kv.pages_per_seq - c->shared_pages;
         a.causal = causal ? 1 : 0;
         a.scale = 1.f / sqrtf((float)c->hd);
+        a.flags = DFLASH_ATTENTION_WEIGHT_PAIRS;  // (as the session's other attention holds its weights)
         a.ld_q = a.ld_out = c->qd;
         a.ld_table = c->kv.pages_per_seq;
         a.q = c->q;
@@ -985,9 +986,9 @@ struct Pass {
     // sequences are attended one by one).  `keys` then counts the shared keys once.
     // The rule, from a verify pass of three layers at Qwen3-8B's shapes with 100 own keys, blocks of 16 (one by
     // one -> shared): the shared form pays a launch and a merge, and saves the prefix's keys of all sequences but
-    // one.  512 shared keys: batch 2 0.527 -> 0.522 ms, 8 0.788 -> 0.787 (a draft layer 0.475 -> 0.482), 32 1.158 ->
-    // 1.156.  1024: 2 0.538 -> 0.527, 4 0.651 -> 0.643, 8 0.813 -> 0.801, 32 1.223 -> 1.167.  8192: 2 0.668 ->
-    // 0.569, 8 1.045 -> 0.865, 32 2.136 -> 1.305.
+    // one.  512 shared keys: batch 2 0.537 -> 0.522 ms, 4 0.643 -> 0.639 (a draft layer 0.380 -> 0.380), 8 0.794 -> 0.789,
+    // 32 1.147 -> 1.141.  1024: 2 0.551 -> 0.534, 4 0.663 -> 0.655, 8 0.817 -> 0.802, 32 1.210 -> 1.161.  8192: 2 0.675 ->
+    // 0.570, 4 0.80 -> 0.706, 8 1.052 -> 0.867, 32 2.125 -> 1.350.
     bool round_lengths(double& keys) {
         const int common = c->shared_pages * PAGE_TOKENS;
         if (common < 1024) return false;

@@ -6,7 +6,8 @@
 // score exceeds it by more than 8, so that weights stay below 2^8), running sum
 // l = sum 2^(s - m) and O = sum 2^(s - m) v, one pass over the keys; fp32
 // throughout, the weights rounded once to bf16 for the product with V (the sum
-// takes the unrounded ones).
+// takes the unrounded ones), or held as bf16 pairs (PAIR: hi, and lo = what hi's
+// rounding left, in the other half of the S buffer; O += hi V + lo V).
 //
 // One CTA per SM holds two streams A, B of 128 query vectors each (TMEM lanes)
 // and walks its part of one of the two lines of the plan (shared_plan.cuh):
@@ -47,6 +48,12 @@
 // small calls are a chain: lengths, plan (2200 cycles), pages, first tile (4500), its
 // softmax and product (1900), partial result, merge (10.3 us for one token of four
 // sequences behind 512 keys).
+//
+// Pairs cost 5 % where bytes or the chain of a small call bound it (32 single rows
+// behind 8192 keys 43.4 -> 46.9 us) and a fifth to a quarter where the softmax does
+// (32 x 16 rows behind 8192 96 -> 119 us).  Sessions take them: their other attention
+// holds its weights so, and a bf16 model's verify logits behind 1024 shared keys are
+// 20 % farther from 64 bits without them (rms 5.1e-3 instead of 4.2e-3).
 //
 // Every wait is bounded; one that runs out sets the CTA's error word (the merge
 // writes NaN), every role leaves, copies in flight are awaited (bounded).
@@ -208,7 +215,8 @@ struct Waiter {
     }
 };
 
-template <int HD>
+// PAIR: the weights of P V as bf16 pairs.
+template <int HD, bool PAIR>
 __global__ void __launch_bounds__(NTHR, 1)
     shared_tc_kernel(const __grid_constant__ TcArgs a, const __grid_constant__ CUtensorMap mq,
                      const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv) {
@@ -440,6 +448,10 @@ __global__ void __launch_bounds__(NTHR, 1)
 #pragma unroll
                         for (int kk = 0; kk < KT / 16; ++kk)
                             umma_bf16_ts(tO, d + 8 * kk, vd + ((kk * 2048) >> 4), ID_O, (j > 0 || kk > 0) ? 1u : 0u);
+                        if constexpr (PAIR)
+#pragma unroll
+                            for (int kk = 0; kk < KT / 16; ++kk)
+                                umma_bf16_ts(tO, d + 32 + 8 * kk, vd + ((kk * 2048) >> 4), ID_O, 1u);
                     }
                     if (j + 2 < n) {
                         const uint64_t kd = k_desc + kst * (C::TILE >> 4);
@@ -540,7 +552,7 @@ __global__ void __launch_bounds__(NTHR, 1)
                     const float neg = m_run == -INFINITY ? 0.f : -m_run;
                     const uint64_t neg2 = pack2(neg, neg);
                     uint64_t sum2[2] = {0ull, 0ull};
-                    uint32_t pk[KT / 2];
+                    uint32_t pk[KT / 2], pl[PAIR ? KT / 2 : 1];  // weights, and what their rounding left
 #pragma unroll
                     for (int e = 0; e < KT / 2; ++e) {
                         float x0, x1;
@@ -549,8 +561,11 @@ __global__ void __launch_bounds__(NTHR, 1)
                         x1 = ex2(x1);
                         sum2[e & 1] = add2(sum2[e & 1], pack2(x0, x1));
                         pk[e] = pack2_bf16(x0, x1);
+                        if constexpr (PAIR)
+                            pl[e] = pack2_bf16(x0 - __uint_as_float(pk[e] << 16), x1 - __uint_as_float(pk[e] & 0xFFFF0000u));
                     }
                     tmem_st32(tS, pk);
+                    if constexpr (PAIR) tmem_st32(tS + 32, pl);
                     float s0, s1;
                     unpack2(add2(sum2[0], sum2[1]), s0, s1);
                     l_run += s0 + s1;
@@ -620,7 +635,7 @@ bool encode(CUtensorMap* m, int rank, const void* ptr, const cuuint64_t* dims, c
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int HD>
+template <int HD, bool PAIR>
 bool run(const Launch& L, const Shape& P, const Work& W, const dflash_shared_prefix_args& a) {
     using C = Cfg<HD>;
     TcArgs t;
@@ -642,16 +657,17 @@ bool run(const Launch& L, const Shape& P, const Work& W, const dflash_shared_pre
         if (!encode(&mk, 3, a.k_cache, dims, strides, box) || !encode(&mv, 3, a.v_cache, dims, strides, box)) return false;
     }
     const size_t smem = C::SMEM_TILES + sizeof(Bars) + 3 * P.batch * 4 + 1024;
-    if (cudaFuncSetAttribute(shared_tc_kernel<HD>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
+    if (cudaFuncSetAttribute(shared_tc_kernel<HD, PAIR>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
         return false;
-    launch_k(L, shared_tc_kernel<HD>, dim3(P.n_cta), dim3(NTHR), smem, 1, t, mq, mk, mv);
+    launch_k(L, shared_tc_kernel<HD, PAIR>, dim3(P.n_cta), dim3(NTHR), smem, 1, t, mq, mk, mv);
     return true;
 }
 
 }  // namespace
 
 bool shared_attention_tc(const Launch& L, const sp::Shape& P, const sp::Work& W, const dflash_shared_prefix_args& a) {
-    return P.hd == 128 ? run<128>(L, P, W, a) : run<64>(L, P, W, a);
+    if (a.flags & DFLASH_ATTENTION_WEIGHT_PAIRS) return P.hd == 128 ? run<128, true>(L, P, W, a) : run<64, true>(L, P, W, a);
+    return P.hd == 128 ? run<128, false>(L, P, W, a) : run<64, false>(L, P, W, a);
 }
 
 }  // namespace dfl

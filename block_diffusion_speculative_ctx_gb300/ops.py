@@ -254,7 +254,7 @@ def kv_tables(kv_lens, new_lens, table, free_pages=None, used=None, *, rows: Opt
 
 def shared_prefix_attention(q, k_cache, v_cache, prefix_pages, prefix_len: int, table, kv_lens, q_start, *,
                             causal: bool = True, scale: Optional[float] = None, out=None, lse=None,
-                            workspace=None):
+                            workspace=None, weight_pairs: bool = False):
     """Attention of a batch whose sequences share a prefix (``dflash_shared_prefix_attention``).
 
     q: [rows, H, hd] (fp32 or bf16); k_cache, v_cache: [pages, H_kv, 64, hd]; prefix_pages: int32, the
@@ -263,7 +263,8 @@ def shared_prefix_attention(q, k_cache, v_cache, prefix_pages, prefix_len: int, 
     hd ** -0.5.  Returns (out, lse); rows outside q_start keep what ``out`` and ``lse`` held (0 where they
     are allocated here).  ``workspace``: uint8, at least ``shared_prefix_workspace`` bytes; calls that may
     run at the same time need one each.  None: allocated for the call, or on a device's default stream the
-    largest one of up to 256 MB needed there so far, which is kept."""
+    largest one of up to 256 MB needed there so far, which is kept.  ``weight_pairs``: bf16 calls hold each
+    softmax weight as a bf16 pair (16 bits) instead of one bf16 (8 bits) for the product with v."""
     if q.dim() != 3 or k_cache.dim() != 4:
         _bad("q must be [rows, H, hd] and the caches [pages, H_kv, 64, hd]")
     dev = _device(q, q, k_cache, v_cache, out, lse)
@@ -298,7 +299,8 @@ def shared_prefix_attention(q, k_cache, v_cache, prefix_pages, prefix_len: int, 
     if lse is None:
         lse = torch.zeros((rows, h), dtype=_F32T, device=q.device)
     fn = load().dflash_shared_prefix_attention
-    args = (dt, h, hkv, hd, batch, rows, pages, prefix_len, table.shape[1], bool(causal), hd ** -0.5 if scale is None else scale, 0,
+    args = (dt, h, hkv, hd, batch, rows, pages, prefix_len, table.shape[1], bool(causal), hd ** -0.5 if scale is None else scale,
+            1 if weight_pairs else 0,
             ld_q, ld_out, ld_table, q.data_ptr(), p_k, p_v, p_pre, table.data_ptr(), p_kv, p_start, out.data_ptr(),
             _flat("lse", lse, _F32T, rows * h, dev))
     if workspace is not None:

@@ -551,11 +551,14 @@ dflash_status dflash_kv_tables(const dflash_kv_tables_args* args, void* cuda_str
  * at most 64 times H_kv; q, the caches and out 16-byte aligned, ld_q and ld_out
  * multiples of 16 bytes.  out may be q (in place, with one row stride).
  * The scores, the softmax and the accumulation are fp32; in BF16 each softmax
- * weight is rounded to bf16 for the product with v.
+ * weight is rounded to bf16 for the product with v, or with the flag
+ * DFLASH_ATTENTION_WEIGHT_PAIRS held as a sum of two bf16 values (16 bits), as
+ * the sessions hold it; F32 calls round none and ignore the flag.
  * workspace: 16-byte aligned device memory of at least
  * dflash_shared_prefix_workspace() bytes, used by this call only until it has
  * finished: calls that may overlap need workspaces of their own.
  * Errors: E_INVAL, E_CUDA. */
+enum { DFLASH_ATTENTION_WEIGHT_PAIRS = 1 };
 typedef struct {
     int32_t dtype;
     int32_t n_heads;
@@ -568,7 +571,10 @@ typedef struct {
     int32_t width;             /* table entries per sequence */
     int32_t causal;
     float scale;               /* > 0 */
-    int32_t reserved;          /* 0 */
+    union {
+        int32_t flags;         /* 0, or DFLASH_ATTENTION_WEIGHT_PAIRS */
+        int32_t reserved;
+    };
     int64_t ld_q;              /* elements between rows of q (H * hd when contiguous) */
     int64_t ld_out;            /* elements between rows of out */
     int64_t ld_table;

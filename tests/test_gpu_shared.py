@@ -633,3 +633,33 @@ def test_a_failed_allocation_leaves_nothing_behind():
     finally:
         left[0] = 1 << 30
         sess.close()
+
+
+@pytest.mark.parametrize("prefix_len", [960, 1024, 2048])   # rounds sequence by sequence; rounds on the shared keys
+def test_bf16_rounds_behind_shared_keys_are_as_exact_as_others(prefix_len):
+    """The rms error of a bf16 session's logits against 64 bits, behind a shared prefix and on the same prompts without
+    sharing.  Both make the same kinds of roundings, in another order: over 2 x 16 rows of logits the two rms values agree to
+    some percent (their spread is 1 / sqrt(2 n) of n independent errors).  A weight rounded to one bf16 would add a rounding of
+    the size of the attention output's own, a fifth more in all; the bound lies half way."""
+    w = configs.get("small_bf16")
+    lens = (37, 100)
+    w = w.with_(batch=2, prompt_lens=tuple(prefix_len + n for n in lens))
+    m = om.Model(w)
+    prefix, own = _prompts(w, prefix_len, lens, 31)
+    prompts = [np.concatenate([prefix, p]) for p in own]
+    states = [spec.prefill(m, p) for p in prompts]
+    prop = synth.uniform_ints(3, 4, 2 * (w.block_size - 1), w.vocab).reshape(2, -1).astype(np.int32)
+    want = [m.target_forward(np.concatenate([[st.anchor], p.astype(np.int64)]), st.tcache.copy())[0] for st, p in zip(states, prop)]
+    rms = {}
+    for shared in (False, True):
+        sess = _session(w, keep_logits=True, max_seq_len=prefix_len + 300)
+        try:
+            first = sess.prefill_shared(prefix, own) if shared else sess.prefill(prompts)
+            assert [int(t) for t in first] == [st.anchor for st in states]
+            sess.draft_block()
+            sess.verify(prop)
+            err = sess.logits("verify") - np.stack(want)
+            rms[shared] = float(np.sqrt((err ** 2).mean()))
+        finally:
+            sess.close()
+    assert rms[True] <= 1.1 * rms[False], rms

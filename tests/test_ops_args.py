@@ -276,3 +276,9 @@ def test_gradients_are_refused_in_both_modes():
         with torch.no_grad():
             with pytest.raises(ValueError, match="tangent"):
                 ops._device(first, dual)
+
+
+@pytest.mark.parametrize("flags", [2, 3, -1, 1 << 30])
+def test_unknown_attention_flags_are_refused(lib, flags):
+    assert lib.dflash_shared_prefix_attention(ctypes.byref(attn(reserved=flags)), None) == dfl.DFLASH_E_INVAL
+    assert "flags" in dfl.dflash_last_error(None)

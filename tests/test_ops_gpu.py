@@ -247,6 +247,34 @@ def test_shared_prefix_attention(i, dtype):
     attn_check(c, dfl().shared_prefix_attention(*attn_inputs(c), causal=causal), causal)
 
 
+@pytest.mark.parametrize("i", range(len(ATTN)))
+def test_shared_prefix_attention_weight_pairs(i):
+    """bf16 with each weight as a pair: what the second value leaves of a weight is half a step of half a step (2^-16) where
+    attn_check has half a step; the other terms are its.  lse is that of the plain call, bit for bit."""
+    heads, prefix, kv, q, causal = ATTN[i]
+    c = attn_case("bf16", heads, prefix, kv, q, seed=100 + i)
+    x = attn_inputs(c)
+    got = dfl().shared_prefix_attention(*x, causal=causal, weight_pairs=True)
+    attn_check(c, got, causal)
+    assert torch.equal(got[1], dfl().shared_prefix_attention(*x, causal=causal)[1])
+    scale, u = c["hd"] ** -0.5, 2.0 ** -24
+    out, _, weight = serving.shared_prefix_attention(c["q"], c["k"], c["v"], c["pre"], c["prefix"], c["table"], c["kv"],
+                                                     c["start"], causal, scale)
+    n = c["prefix"] + int(c["kv"].max())
+    qk = scale * float(np.abs(c["q"]).max()) * np.nanmax(np.abs(np.where(np.isfinite(c["k"]), c["k"], 0)).sum(-1))
+    delta = 2 * c["hd"] * u * qk + 4 * qk * u + 2.0 ** -22 + (n + 64) * u
+    tol = HALF["bf16"] * np.abs(out) + (delta + 2.0 ** -16) * weight + 1e-30
+    err = np.abs(got[0].float().cpu().numpy() - out)
+    assert (err <= tol).all(), float((err / tol).max())
+
+
+def test_shared_prefix_attention_weight_pairs_in_fp32_change_nothing():
+    c = attn_case("f32", (8, 2, 128), 300, [70, 3], [2, 3], seed=5)
+    x = attn_inputs(c)
+    a, b = dfl().shared_prefix_attention(*x), dfl().shared_prefix_attention(*x, weight_pairs=True)
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("batch", [300, 2048])
 def test_shared_prefix_attention_many_short_sequences(dtype, batch):
