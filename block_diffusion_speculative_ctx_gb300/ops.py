@@ -177,8 +177,6 @@ _use_extension()
 def _call(fn, pack, values, dev):
     try:
         args = pack(*values)
-    except OverflowError as e:
-        raise ValueError(f"a floating-point argument is out of the range of fp32: {e}") from None
     except struct.error as e:
         raise ValueError(f"an integer argument is out of its range or no integer: {e}") from None
     if _current_device() == dev:
