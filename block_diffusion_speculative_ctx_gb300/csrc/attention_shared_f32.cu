@@ -11,7 +11,7 @@
 // K and V of the next tile land (cp.async, double-buffered) meanwhile; keys behind
 // the list's end are filled with zeros, so what a page's unused slots hold never
 // matters.  Bound by the FMA pipes and shared memory for long work, by the chain
-// lengths -> pages -> tile for the short calls that fp32 models make: 9.8 us (merge
+// lengths -> pages -> tile for the short calls that fp32 models make: 8.7 us (merge
 // included, graph replay) for 3 blocks of 4 rows behind 500 keys, whose bytes take
 // 0.1 us; the tiles of a plain fp32 kernel without the plan took 184 us.  64 vectors
 // a worker where a sequence has more than 32 per KV head on average: 16 rows of 8

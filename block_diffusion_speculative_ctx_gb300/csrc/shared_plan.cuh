@@ -369,7 +369,9 @@ __device__ __forceinline__ void dir_item(const Shape& P, const Head& h, int line
 
 // The directory for the merge kernel, by `warps` warps of which this is number `w`: a lane takes a (row, KV head)
 // pair at a time.  Pairs are numbered through the rows of q (at most 2^20 of them, times 1024 heads), and the row's
-// sequence is searched in the row starts: the work is the rows', whatever the longest sequence is.
+// sequence is searched in the row starts: the work is the rows', whatever the longest sequence is.  (Chunks of 32 pairs of one
+// sequence, as many for each as the longest one needs: 1024 sequences, one of 1024 rows and the others of one, 304 us instead
+// of 235; fp32 blocks of four 9.7 instead of 8.7.)
 __device__ __forceinline__ void write_dir(const Shape& P, const Head& h, const Work& W, const uint32_t* base,
                                           const uint32_t* ibase, int w, int warps, int lane) {
     const int pairs = P.rows * P.Hkv;
