@@ -193,7 +193,7 @@ def prepare(case, seed):
                     k=noise(layers, n_pages, hkv, PAGE, hd).to(dt), v=noise(layers, n_pages, hkv, PAGE, hd).to(dt),
                     masks=torch.empty((rows, _ceil(int(m.max()), 32)), **i32), depth=torch.empty(rows, **i32),
                     row_pos=torch.empty(rows, **i32), path=torch.empty((b, DEPTH), **i32), accepted=torch.empty(b, **i32),
-                    bonus=torch.empty(b, **i32), kv_out=torch.empty(b, **i32), status=torch.empty(3, **i32))
+                    bonus=torch.empty(b, **i32), kv_out=torch.empty(b, **i32), status=torch.empty((3, b), **i32))
     if op == "pages":
         g, kv, _ = _lengths(case, seed)
         b, kids, hkv, hd, layers = case["batch"], case["kids"], case["kv_heads"], case["hd"], case["layers"]
@@ -291,11 +291,11 @@ def _step(s):
     if own:
         import block_diffusion_speculative_ctx_gb300 as dfl
         t = dfl.tree_masks(s["parents"], s["q_start"], kv_lens=s["kv"], masks=s["masks"], depth=s["depth"],
-                           row_pos=s["row_pos"], status=s["status"][:1])
+                           row_pos=s["row_pos"], status=s["status"][0])
         a = dfl.tree_accept(s["parents"], s["tokens"], s["posterior"], s["q_start"], path=s["path"], accepted=s["accepted"],
-                            bonus=s["bonus"], status=s["status"][1:2])
+                            bonus=s["bonus"], status=s["status"][1])
         c = dfl.kv_compact(s["k"], s["v"], s["table"], s["kv"], s["q_start"], a.path, a.accepted, kv_out=s["kv_out"],
-                           status=s["status"][2:])
+                           status=s["status"][2])
         return [t.masks, t.depth, t.row_pos, a.path, a.accepted, a.bonus, c.kv_lens, s["status"], s["k"], s["v"]]
     start, kv, wide = s["q_start"].long(), s["kv"].long(), s["max_m"]
     rows, b = s["parents"].numel(), kv.numel()
