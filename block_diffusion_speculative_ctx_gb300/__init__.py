@@ -15,12 +15,15 @@ The functions carry the C names:
     dflash_generate, dflash_inspect, dflash_destroy, dflash_last_error
 
 ``Session`` wraps them for tests and the benchmark.  ``kv_tables``,
-``shared_prefix_attention`` and ``process_logits`` (ops.py) are the stateless
-serving operators over torch tensors.
+``shared_prefix_attention`` and ``process_logits`` (ops.py), ``tree_masks``,
+``tree_attention``, ``tree_accept``, ``kv_compact``, ``kv_fork`` and ``kv_release``
+(ops_tree.py) and ``token_logprobs`` with its gradient (ops_logprobs.py) are the
+stateless operators over torch tensors.
 """
 from __future__ import annotations
 
 import ctypes
+import importlib
 import os
 from typing import Optional
 
@@ -93,7 +96,9 @@ EXPORTS = ("dflash_init", "dflash_prefill", "dflash_set_block_size", "dflash_blo
            "dflash_verify_sampled", "dflash_set_sampling_filter", "dflash_train_forward", "dflash_generate",
            "dflash_inspect", "dflash_set_profiling", "dflash_destroy", "dflash_last_error",
            "dflash_kv_tables", "dflash_shared_prefix_attention", "dflash_shared_prefix_workspace",
-           "dflash_process_logits", "dflash_prefill_shared", "dflash_set_logit_rules", "dflash_set_token_masks")
+           "dflash_process_logits", "dflash_prefill_shared", "dflash_set_logit_rules", "dflash_set_token_masks",
+           "dflash_tree_masks", "dflash_tree_attention", "dflash_tree_accept", "dflash_kv_compact", "dflash_kv_fork",
+           "dflash_kv_release", "dflash_token_logprobs", "dflash_token_logprobs_grad")
 
 _lib = None
 
@@ -140,7 +145,9 @@ def load(build_if_missing: bool = False):
               "dflash_set_logit_rules", "dflash_set_token_masks"):
         getattr(lib, f).restype = ctypes.c_int
     lib.dflash_destroy.restype = None
-    for f in ("dflash_kv_tables", "dflash_shared_prefix_attention", "dflash_process_logits"):
+    for f in ("dflash_kv_tables", "dflash_shared_prefix_attention", "dflash_process_logits", "dflash_tree_masks",
+              "dflash_tree_attention", "dflash_tree_accept", "dflash_kv_compact", "dflash_kv_fork", "dflash_kv_release",
+              "dflash_token_logprobs", "dflash_token_logprobs_grad"):
         getattr(lib, f).argtypes = [P, P]
         getattr(lib, f).restype = ctypes.c_int
     lib.dflash_shared_prefix_workspace.argtypes = [I32] * 6
@@ -226,10 +233,18 @@ def dflash_destroy(ctx):
 from .session import Session, config_from_workload  # noqa: E402,F401
 
 
+_OPERATORS = {
+    "ops": ("kv_tables", "shared_prefix_attention", "shared_prefix_workspace", "process_logits", "KVTables"),
+    "ops_tree": ("tree_masks", "tree_attention", "tree_accept", "kv_compact", "kv_fork", "kv_release", "TreeMasks",
+                 "TreeAccept", "KVCompact", "KVFork", "KVRelease"),
+    "ops_logprobs": ("token_logprobs", "token_logprobs_grad", "TokenLogprobs"),
+}
+
+
 def __getattr__(name):
-    # the serving operators (ops.py) need torch, which this module itself does not import
-    if name in ("kv_tables", "shared_prefix_attention", "shared_prefix_workspace", "process_logits", "KVTables"):
-        from . import ops
-        globals()[name] = getattr(ops, name)
-        return globals()[name]
+    # the serving operators need torch, which this module itself does not import
+    for module, names in _OPERATORS.items():
+        if name in names:
+            globals()[name] = getattr(importlib.import_module("." + module, __name__), name)
+            return globals()[name]
     raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

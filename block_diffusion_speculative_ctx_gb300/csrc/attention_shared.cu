@@ -1,5 +1,6 @@
 // Attention of a batch that shares a prefix (dflash_shared_prefix_attention in
-// include/dflash.h): the entry, its checks, and the merge of the partial results
+// include/dflash.h) and of trees of drafted tokens (dflash_tree_attention): the
+// entries, their checks, and the merge of the partial results
 // that the main kernels (attention_shared_tc.cu for bf16, attention_shared_f32.cu)
 // leave per segment of the plan (shared_plan.cuh).
 //
@@ -8,6 +9,8 @@
 // keys and values once, q and out once, and 4 * hd operations per query vector
 // and key.
 #include <math.h>
+#include <stdio.h>
+#include <string.h>
 
 #include <algorithm>
 
@@ -210,14 +213,14 @@ void merge(const Launch& L, const MergeArgs& m) {
 
 }  // namespace
 
-bool shared_prefix_attention(const Launch& L, const dflash_shared_prefix_args& a) {
+bool shared_prefix_attention(const Launch& L, const dflash_shared_prefix_args& a, const TreeMasks* tree) {
     const bool f32 = a.dtype == DFLASH_DTYPE_F32;
     MergeArgs m;
     sp::Shape& P = m.P;
     P = sizes_of(f32, vectors_of(f32, a.n_heads / a.n_kv_heads, a.batch, a.rows), a.n_heads, a.n_kv_heads, a.head_dim, a.batch, a.rows);
     P.width = a.width;
     P.prefix_len = a.prefix_len;
-    P.causal = a.causal != 0;
+    P.causal = a.causal != 0 && !tree;
     P.n_pages = a.n_pages;
     P.npt = (a.prefix_len + P.KT - 1) / P.KT;
     P.ld_table = a.ld_table;
@@ -225,6 +228,11 @@ bool shared_prefix_attention(const Launch& L, const dflash_shared_prefix_args& a
     P.table = a.table;
     P.kv_lens = a.kv_lens;
     P.q_start = a.q_start;
+    if (tree) {
+        P.masks = tree->masks;
+        P.ld_mask = tree->ld_mask;
+        P.words = tree->words;
+    }
     sp::layout((char*)a.workspace, P, &m.W);
     m.out = a.out;
     m.lse = a.lse;
@@ -290,23 +298,50 @@ extern "C" size_t dflash_shared_prefix_workspace(int32_t dtype, int32_t n_heads,
     return dtype == DFLASH_DTYPE_F32 ? std::max(bytes(true, 32), bytes(true, 64)) : bytes(false, 128);
 }
 
-extern "C" dflash_status dflash_shared_prefix_attention(const dflash_shared_prefix_args* p, void* cuda_stream) {
-    const char* why = "shared_prefix_attention: args is NULL";
-    if (!p || check_shared_prefix(*p, &why) != DFLASH_OK) {
-        set_global_error(why);
-        return DFLASH_E_INVAL;
-    }
-    if (p->rows == 0) return DFLASH_OK;
+namespace {
+
+dflash_status queue(const dflash_shared_prefix_args& a, const TreeMasks* tree, void* cuda_stream, const char* unprepared) {
+    if (a.rows == 0) return DFLASH_OK;
     bool failed = false;
     Launch L{(cudaStream_t)cuda_stream, nullptr};
     L.pdl = true;  // (each kernel waits for what runs before it ahead of its first read)
     L.failed = &failed;
-    const bool ok = shared_prefix_attention(L, *p);
+    const bool ok = shared_prefix_attention(L, a, tree);
     const cudaError_t e = cudaGetLastError();
     if (!ok || failed || e != cudaSuccess) {
-        set_global_error(e != cudaSuccess ? cudaGetErrorString(e)
-                                          : "shared_prefix_attention: a kernel could not be prepared");
+        set_global_error(e != cudaSuccess ? cudaGetErrorString(e) : unprepared);
         return DFLASH_E_CUDA;
     }
     return DFLASH_OK;
+}
+
+dflash_status refuse(const char* why) {
+    set_global_error(why);
+    return DFLASH_E_INVAL;
+}
+
+}  // namespace
+
+extern "C" dflash_status dflash_shared_prefix_attention(const dflash_shared_prefix_args* p, void* cuda_stream) {
+    const char* why = "shared_prefix_attention: args is NULL";
+    if (!p || check_shared_prefix(*p, &why) != DFLASH_OK) return refuse(why);
+    return queue(*p, nullptr, cuda_stream, "shared_prefix_attention: a kernel could not be prepared");
+}
+
+extern "C" dflash_status dflash_tree_attention(const dflash_tree_attention_args* p, void* cuda_stream) {
+    if (!p) return refuse("tree_attention: args is NULL");
+    const char* why = "";
+    if (check_shared_prefix(p->attn, &why) != DFLASH_OK) {
+        // the same checks, in this call's name
+        char text[256];
+        const char* at = strchr(why, ':');
+        snprintf(text, sizeof text, "tree_attention%s", at ? at : "");
+        return refuse(text);
+    }
+    if (p->words < 1 || p->words > (1 << 20)) return refuse("tree_attention: words outside [1, 2^20]");
+    if (p->reserved != 0) return refuse("tree_attention: reserved must be 0");
+    if (p->attn.rows > 0 && !p->masks) return refuse("tree_attention: masks is NULL");
+    if (p->ld_mask < p->words) return refuse("tree_attention: ld_mask is smaller than words");
+    const TreeMasks tree = {p->masks, p->ld_mask, p->words};
+    return queue(p->attn, &tree, cuda_stream, "tree_attention: a kernel could not be prepared");
 }

@@ -54,8 +54,9 @@ __device__ __forceinline__ void cp16(float* dst, const float* src, bool full) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(d), "l"(src), "r"(full ? 16 : 0) : "memory");
 }
 
-// UV query vectors a thread.
-template <int HD, int UV>
+// UV query vectors a thread.  TREE: rows see the own keys that their masks name; keys that no row of the item sees are filled
+// with zeros like those behind the list's end.
+template <int HD, int UV, bool TREE>
 __global__ void __launch_bounds__(NT, 2) shared_f32_kernel(F32Args a) {
     extern __shared__ __align__(16) uint8_t raw[];
     constexpr int VT = 16 * UV;
@@ -75,7 +76,7 @@ __global__ void __launch_bounds__(NT, 2) shared_f32_kernel(F32Args a) {
     Seg s;
     int kvh, row0, seq;
 #pragma unroll 1
-    while (walk.next(P, h, base, ibase, s, kvh, row0, seq)) {
+    while (walk.next<TREE>(P, h, base, ibase, s, kvh, row0, seq)) {
         const int* pages = seq < 0 ? P.prefix_pages : P.table + (long long)seq * P.ld_table;
         const int nv = s.nrows * P.g;
         int bad = 0;
@@ -83,11 +84,17 @@ __global__ void __launch_bounds__(NT, 2) shared_f32_kernel(F32Args a) {
             const int k0 = (s.t0 + j) * KT, page = pages[k0 >> 6];
             const bool in = page >= 0 && page < P.n_pages;
             bad |= !in;
+            uint32_t seen = ~0u;
+            if (TREE && k0 + KT > s.lim0) {
+                seen = 0u;
+                for (int r = lane; r < s.nrows; r += 32) seen |= tree_sees32(P, s, row0 + r, k0);
+                seen = __reduce_or_sync(0xffffffffu, seen);
+            }
             const long long off = (((long long)(in ? page : 0) * (P.Hkv / P.parts) + kvh / P.parts) * 64 + (k0 & 63)) * HD;
 #pragma unroll 4
             for (int i = tid; i < KT * C4; i += NT) {
                 const int r = i / C4, c = i - r * C4;
-                const bool full = in && k0 + r < s.keys;
+                const bool full = in && (TREE && k0 + KT > s.lim0 ? seen >> r & 1u : k0 + r < s.keys);
                 cp16(&S.k[j & 1][r][4 * c], a.k + off + r * HD + 4 * c, full);
                 cp16(&S.v[j & 1][r][4 * c], a.v + off + r * HD + 4 * c, full);
             }
@@ -111,7 +118,7 @@ __global__ void __launch_bounds__(NT, 2) shared_f32_kernel(F32Args a) {
             const int v = UV * tv + u;
             m[u] = -INFINITY;
             l[u] = 0.f;
-            lim[u] = v < nv ? max(s.lim0 + s.step * (v / P.g), 0) : 0;
+            lim[u] = v < nv ? (TREE ? v / P.g : max(s.lim0 + s.step * (v / P.g), 0)) : TREE ? -1 : 0;  // (TREE: the row)
 #pragma unroll
             for (int i = 0; i < DPT; ++i) o[u][i] = make_float4(0.f, 0.f, 0.f, 0.f);
         }
@@ -142,9 +149,12 @@ __global__ void __launch_bounds__(NT, 2) shared_f32_kernel(F32Args a) {
 #pragma unroll
             for (int u = 0; u < UV; ++u) {
                 float mx = -INFINITY;
+                uint32_t sees = ~0u;
+                if (TREE && k0 + KT > s.lim0) sees = lim[u] < 0 ? 0u : tree_sees32(P, s, row0 + lim[u], k0);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    sc[u][i] = k0 + td + 8 * i < lim[u] ? sc[u][i] * a.scale_log2 : -INFINITY;
+                    const bool on = TREE ? sees >> (td + 8 * i) & 1u : k0 + td + 8 * i < lim[u];
+                    sc[u][i] = on ? sc[u][i] * a.scale_log2 : -INFINITY;
                     mx = fmaxf(mx, sc[u][i]);
                 }
 #pragma unroll
@@ -214,13 +224,19 @@ __global__ void __launch_bounds__(NT, 2) shared_f32_kernel(F32Args a) {
     pdl_trigger();
 }
 
-template <int HD, int UV>
+template <int HD, int UV, bool TREE>
 bool run(const Launch& L, const F32Args& f) {
     const size_t smem = sizeof(Smem<HD, 16 * UV>) + 3 * f.P.batch * 4;
-    if (cudaFuncSetAttribute(shared_f32_kernel<HD, UV>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
+    if (cudaFuncSetAttribute(shared_f32_kernel<HD, UV, TREE>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
         return false;
-    launch_k(L, shared_f32_kernel<HD, UV>, dim3(2 * f.P.n_cta), dim3(NT), smem, 1, f);
+    launch_k(L, shared_f32_kernel<HD, UV, TREE>, dim3(2 * f.P.n_cta), dim3(NT), smem, 1, f);
     return true;
+}
+
+template <bool TREE>
+bool pick(const Launch& L, const Shape& P, const F32Args& f) {
+    if (P.VT == 64) return P.hd == 128 ? run<128, 4, TREE>(L, f) : run<64, 4, TREE>(L, f);
+    return P.hd == 128 ? run<128, 2, TREE>(L, f) : run<64, 2, TREE>(L, f);
 }
 
 }  // namespace
@@ -234,8 +250,8 @@ bool shared_attention_f32(const Launch& L, const sp::Shape& P, const sp::Work& W
     f.v = (const float*)a.v_cache;
     f.ld_q = a.ld_q;
     f.scale_log2 = (float)((double)a.scale * 1.4426950408889634);
-    if (P.VT == 64) return P.hd == 128 ? run<128, 4>(L, f) : run<64, 4>(L, f);
-    return P.hd == 128 ? run<128, 2>(L, f) : run<64, 2>(L, f);
+    if (P.masks) return pick<true>(L, P, f);
+    return pick<false>(L, P, f);
 }
 
 }  // namespace dfl

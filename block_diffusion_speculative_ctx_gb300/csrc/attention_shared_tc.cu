@@ -215,8 +215,10 @@ struct Waiter {
     }
 };
 
-// PAIR: the weights of P V as bf16 pairs.
-template <int HD, bool PAIR>
+// PAIR: the weights of P V as bf16 pairs.  TREE: rows see the own keys that their masks name; the tiles that hold nodes of
+// the tree take 64 mask bits a row (two to three words from L2, asked for before the scores are waited for) and zero the rows
+// of V that no row of the item sees.
+template <int HD, bool PAIR, bool TREE>
 __global__ void __launch_bounds__(NTHR, 1)
     shared_tc_kernel(const __grid_constant__ TcArgs a, const __grid_constant__ CUtensorMap mq,
                      const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv) {
@@ -318,7 +320,7 @@ __global__ void __launch_bounds__(NTHR, 1)
         Seg s;
 #pragma unroll 1
         while (wait.ok) {
-            if (!walk.next(P, h, base, ibase, s, kvh, row0, seq)) s.n = 0;
+            if (!walk.next<TREE>(P, h, base, ibase, s, kvh, row0, seq)) s.n = 0;
             if (lane == 0 && rx == x) {
                 const int slot = nseg % SEGS;
                 if (wait(&B->seg_empty[x][slot], ((nseg / SEGS) & 1) ^ 1)) {
@@ -490,7 +492,7 @@ __global__ void __launch_bounds__(NTHR, 1)
             const int r0 = pair ? x * P.RH : 0;  // this stream's rows of the item
             const int nv = min(P.RH, s.nrows - r0) * P.g;
             int lim = 0x7fffffff;  // (a lane of no query vector: anything)
-            if (v < nv) lim = max(s.lim0 + s.step * (r0 + v / P.g), 0);
+            if (!TREE && v < nv) lim = max(s.lim0 + s.step * (r0 + v / P.g), 0);
             const bool live_warp = 32 * quad < nv;
             const int lim_warp = __reduce_min_sync(0xffffffffu, lim);
             float m_run = -INFINITY, l_run = 0.f;
@@ -499,15 +501,25 @@ __global__ void __launch_bounds__(NTHR, 1)
                 const int k0 = (s.t0 + j) * KT;
                 const uint32_t buf = (nt + j) & 1;
                 const uint32_t tS = tl + 128 * x + 64 * buf;
+                const bool tree_tile = TREE && k0 + KT > s.lim0;
+                uint64_t sees = ~0ull, seen = ~0ull;  // keys that this vector's row sees, that some row of the item sees
+                if (TREE && tree_tile) {
+                    if (v < nv) sees = tree_sees64(P, s, s.row0 + r0 + v / P.g, k0);
+                    uint64_t any = 0;
+                    for (int r = lane; r < s.nrows; r += 32) any |= tree_sees64(P, s, s.row0 + r, k0);
+                    seen = (uint64_t)__reduce_or_sync(0xffffffffu, (uint32_t)(any >> 32)) << 32 |
+                           __reduce_or_sync(0xffffffffu, (uint32_t)any);
+                }
                 if (!batch_done(x, nb + j)) break;
                 fence_after();
-                if (k0 + KT > s.keys) {
+                if (TREE ? seen != ~0ull : k0 + KT > s.keys) {
                     // the list ends inside this tile: zero the rows of V behind it (a page's unused slots may
                     // hold anything, and 0 * NaN is NaN); on line 0 both streams do, each before its own P V
                     const uint32_t st = first_stage(x) + stage_of(ring + v_seq(j, n));
                     if (!landed(x, nb + j + 2)) break;
                     uint8_t* V = sm + C::RING_AT + st * C::TILE;
-                    for (int i = (s.keys - k0) * 8 + v; i < KT * 8; i += 128)
+                    for (int i = (TREE ? 0 : (s.keys - k0) * 8) + v; i < KT * 8; i += 128)
+                        if (!TREE || !(seen >> (i >> 3) & 1u))
 #pragma unroll
                         for (int c = 0; c < C::HALVES; ++c)
                             *reinterpret_cast<uint4*>(V + c * C::KV_REG + i * 16) = make_uint4(0u, 0u, 0u, 0u);
@@ -519,7 +531,14 @@ __global__ void __launch_bounds__(NTHR, 1)
                     tmem_ld32_issue(tS + 32, sr + 32);
                     tmem_ld32_wait(sr);
                     tmem_ld32_wait(sr + 32);
-                    if (k0 + KT > lim_warp) {
+                    if (TREE) {
+                        if (tree_tile) {
+                            const uint32_t w[2] = {(uint32_t)sees, (uint32_t)(sees >> 32)};
+#pragma unroll
+                            for (int c = 0; c < KT; ++c)
+                                if (!(w[c >> 5] >> (c & 31) & 1u)) sr[c] = 0xFF800000u;
+                        }
+                    } else if (k0 + KT > lim_warp) {
                         const int left = lim - k0;
 #pragma unroll
                         for (int c = 0; c < KT; ++c)
@@ -635,7 +654,7 @@ bool encode(CUtensorMap* m, int rank, const void* ptr, const cuuint64_t* dims, c
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int HD, bool PAIR>
+template <int HD, bool PAIR, bool TREE>
 bool run(const Launch& L, const Shape& P, const Work& W, const dflash_shared_prefix_args& a) {
     using C = Cfg<HD>;
     TcArgs t;
@@ -657,17 +676,27 @@ bool run(const Launch& L, const Shape& P, const Work& W, const dflash_shared_pre
         if (!encode(&mk, 3, a.k_cache, dims, strides, box) || !encode(&mv, 3, a.v_cache, dims, strides, box)) return false;
     }
     const size_t smem = C::SMEM_TILES + sizeof(Bars) + 3 * P.batch * 4 + 1024;
-    if (cudaFuncSetAttribute(shared_tc_kernel<HD, PAIR>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
+    if (cudaFuncSetAttribute(shared_tc_kernel<HD, PAIR, TREE>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
         return false;
-    launch_k(L, shared_tc_kernel<HD, PAIR>, dim3(P.n_cta), dim3(NTHR), smem, 1, t, mq, mk, mv);
+    launch_k(L, shared_tc_kernel<HD, PAIR, TREE>, dim3(P.n_cta), dim3(NTHR), smem, 1, t, mq, mk, mv);
     return true;
 }
 
 }  // namespace
 
+namespace {
+
+template <bool TREE>
+bool pick(const Launch& L, const sp::Shape& P, const sp::Work& W, const dflash_shared_prefix_args& a) {
+    if (a.flags & DFLASH_ATTENTION_WEIGHT_PAIRS)
+        return P.hd == 128 ? run<128, true, TREE>(L, P, W, a) : run<64, true, TREE>(L, P, W, a);
+    return P.hd == 128 ? run<128, false, TREE>(L, P, W, a) : run<64, false, TREE>(L, P, W, a);
+}
+
+}  // namespace
+
 bool shared_attention_tc(const Launch& L, const sp::Shape& P, const sp::Work& W, const dflash_shared_prefix_args& a) {
-    if (a.flags & DFLASH_ATTENTION_WEIGHT_PAIRS) return P.hd == 128 ? run<128, true>(L, P, W, a) : run<64, true>(L, P, W, a);
-    return P.hd == 128 ? run<128, false>(L, P, W, a) : run<64, false>(L, P, W, a);
+    return P.masks ? pick<true>(L, P, W, a) : pick<false>(L, P, W, a);
 }
 
 }  // namespace dfl

@@ -11,8 +11,14 @@ namespace dfl {
 // kv_tables.cu
 void kv_tables(const Launch& L, const dflash_kv_tables_args& a);
 
-// attention_shared.cu: false when a kernel could not be prepared (nothing queued).
-bool shared_prefix_attention(const Launch& L, const dflash_shared_prefix_args& a);
+// attention_shared.cu: false when a kernel could not be prepared (nothing queued).  With `tree`, rows see the own keys that
+// their masks name instead of the causal ones.
+struct TreeMasks {
+    const uint32_t* masks;
+    long long ld_mask;
+    int words;
+};
+bool shared_prefix_attention(const Launch& L, const dflash_shared_prefix_args& a, const TreeMasks* tree = nullptr);
 
 // logit_rules.cu
 void process_logits(const Launch& L, const dflash_logits_args& a);
@@ -33,6 +39,23 @@ void drop_indices(const Launch& L, int* index, int rows, int n);
 // Rows whose best logit is -inf have no token: the error word says so, and token 0 gets all of the row's
 // mass, so that what follows stays defined.
 void check_rows(const Launch& L, float* logits, long long ld, int rows, const int* best, uint32_t* err);
+
+// The caches [layers][n_pages][n_kv_heads][64][head_dim] of a call: NULL, or which of the texts says what is wrong.
+template <typename A>
+const char* bad_caches(const A& a, const char* dtype, const char* layers, const char* sizes, const char* lie) {
+    if (a.dtype != DFLASH_DTYPE_F32 && a.dtype != DFLASH_DTYPE_BF16) return dtype;
+    if (a.layers < 1 || a.layers > 1024) return layers;
+    const long long es = a.dtype == DFLASH_DTYPE_BF16 ? 2 : 4;
+    // (token slots 64 * page + token are 32-bit)
+    if (a.n_pages < 1 || a.n_pages > (1 << 24) || a.n_kv_heads < 1 || a.n_kv_heads > 1024 || a.head_dim < 1 ||
+        a.head_dim > 4096 || a.head_dim * es % 16)
+        return sizes;
+    const long long layer = (long long)a.n_pages * a.n_kv_heads * 64 * a.head_dim;
+    if (!a.k_cache || !a.v_cache || (((uintptr_t)a.k_cache | (uintptr_t)a.v_cache) & 15u) || a.ld_layer * es % 16 ||
+        (a.layers > 1 && a.ld_layer < layer))
+        return lie;
+    return nullptr;
+}
 
 // The entries' argument checks: DFLASH_OK, or E_INVAL with the reason in *why.
 dflash_status check_shared_prefix(const dflash_shared_prefix_args& a, const char** why);

@@ -36,6 +36,11 @@ struct Shape {
     int parts;     // KV heads here per KV head of the caches (more query heads than VT are split)
     long long ld_table;
     const int *prefix_pages, *table, *kv_lens, *q_start;
+    // trees (masks given): row r sees its sequence's committed keys, those before the last m, and of these m the ones whose
+    // bit is set in its `words` words
+    const uint32_t* masks;
+    long long ld_mask;
+    int words;
     __host__ __device__ int row_tile(int line) const { return line == 0 ? 2 * RH : RH; }
 };
 
@@ -131,8 +136,28 @@ struct Seg {
     int lim0;         // keys seen by the item's first row
     int step;         // and by each row more (causal own keys: 1, else 0)
     int nrows;        // rows of the item
+    int row0;         // the first of them (trees alone)
     uint32_t block;
 };
+
+// Which of the keys k0 .. k0 + 31 (or + 63) row `row` of a tree's item sees: bit c for key k0 + c.  The keys before the
+// committed ones' end lim0 are seen by all, node i of the tree is key lim0 + i, and behind the last key nothing is.
+__device__ __forceinline__ uint32_t tree_word(const Shape& P, const uint32_t* mask, int i) {
+    return i >= 0 && i < P.words ? mask[i] : 0u;
+}
+__device__ __forceinline__ uint32_t tree_sees32(const Shape& P, const Seg& s, int row, int k0) {
+    const int at = k0 - s.lim0, left = s.keys - k0;  // node of key k0
+    if (left <= 0) return 0u;
+    const uint32_t live = left < 32 ? (1u << left) - 1u : ~0u;
+    if (at <= -32) return live;
+    const uint32_t* mask = P.masks + (long long)row * P.ld_mask;
+    const int w = at >> 5;  // (-1: committed keys first)
+    const uint32_t lo = w < 0 ? ~0u : tree_word(P, mask, w);
+    return __funnelshift_r(lo, tree_word(P, mask, w + 1), at & 31) & live;
+}
+__device__ __forceinline__ uint64_t tree_sees64(const Shape& P, const Seg& s, int row, int k0) {
+    return (uint64_t)tree_sees32(P, s, row, k0 + 32) << 32 | tree_sees32(P, s, row, k0);
+}
 
 // Walks the segments of worker `c` on a line.  base / ibase: see make_plan.
 struct Walk {
@@ -142,6 +167,7 @@ struct Walk {
         : p(min(h.W[ln], (uint32_t)worker * h.part[ln])), p1(min(h.W[ln], p + h.part[ln])), line(ln), c(worker) {}
 
     // The next segment, its KV head, first row of q and sequence (-1: prefix).
+    template <bool TREE = false>
     __device__ __forceinline__ bool next(const Shape& P, const Head& h, const uint32_t* base, const uint32_t* ibase, Seg& s,
                                          int& kvh, int& row0, int& seq) {
         const uint32_t lead = P.lead[line];
@@ -187,8 +213,10 @@ struct Walk {
                     s.lim0 = q.kv - q.m + r + 1;
                     s.step = 1;
                 }
+                if (TREE) s.lim0 = q.kv - q.m;  // (the committed keys; the masks say the rest)
                 n_eff = seen_tiles(P, q, r + s.nrows);
             }
+            if (TREE) s.row0 = row0;
             // tile t is unit b + lead + t
             s.t0 = max((int)(p - b) - (int)lead, 0);
             s.n = min(n_eff, (int)min(p1 - b, lead + (uint32_t)n) - (int)lead) - s.t0;

@@ -5,6 +5,9 @@ stateless calls of the C ABI (include/dflash.h, "serving operators").
     shared_prefix_attention  attention of a batch whose sequences share a prefix
     process_logits           penalties for repeated tokens, biases and grammar masks on logits
 
+ops_tree.py has those of trees of drafted tokens and of pages that several sequences hold,
+ops_logprobs.py the log probabilities of tokens and their gradient.
+
 Every call queues its kernels on torch's current stream of the tensors' device and
 returns without synchronising.  None has a gradient: tensors that require one, outputs
 among them, are refused while autograd is recording, and so are tensors with a
@@ -252,6 +255,29 @@ def kv_tables(kv_lens, new_lens, table, free_pages=None, used=None, *, rows: Opt
     return KVTables(table_out, used_out, q_start, row_seq, row_pos, slots, status)
 
 
+def _attend(fn, pack, args, more, sizes, workspace, dev, device):
+    """The attention call fn of args, a workspace (the caller's, the kept one or the call's own) and more."""
+    if workspace is not None:
+        n_ws = workspace.numel() * workspace.element_size()
+        _call(fn, pack, (*args, _flat("workspace", workspace, workspace.dtype, workspace.numel(), dev), n_ws, *more), dev)
+        return
+    n_ws = _WORKSPACE.get(sizes)
+    if n_ws is None:
+        if len(_WORKSPACE) > 4096:
+            _WORKSPACE.clear()
+        n_ws = _WORKSPACE[sizes] = load().dflash_shared_prefix_workspace(*sizes)
+    if n_ws > KEPT_MAX or _raw_stream(dev) != 0:
+        workspace = torch.empty(n_ws, dtype=_U8T, device=device)
+        _call(fn, pack, (*args, workspace.data_ptr(), n_ws, *more), dev)
+        return
+    with _KEPT_LOCK:
+        kept = _KEPT.get(dev)
+        if kept is None or kept[0] < n_ws:
+            workspace = torch.empty(n_ws, dtype=_U8T, device=device)
+            kept = _KEPT[dev] = (n_ws, workspace.data_ptr(), workspace)
+        _call(fn, pack, (*args, kept[1], n_ws, *more), dev)
+
+
 def shared_prefix_attention(q, k_cache, v_cache, prefix_pages, prefix_len: int, table, kv_lens, q_start, *,
                             causal: bool = True, scale: Optional[float] = None, out=None, lse=None,
                             workspace=None, weight_pairs: bool = False):
@@ -303,26 +329,7 @@ def shared_prefix_attention(q, k_cache, v_cache, prefix_pages, prefix_len: int, 
             1 if weight_pairs else 0,
             ld_q, ld_out, ld_table, q.data_ptr(), p_k, p_v, p_pre, table.data_ptr(), p_kv, p_start, out.data_ptr(),
             _flat("lse", lse, _F32T, rows * h, dev))
-    if workspace is not None:
-        n_ws = workspace.numel() * workspace.element_size()
-        _call(fn, _ATTN.pack, (*args, _flat("workspace", workspace, workspace.dtype, workspace.numel(), dev), n_ws), dev)
-    else:
-        sizes = (dt, h, hkv, hd, batch, rows)
-        n_ws = _WORKSPACE.get(sizes)
-        if n_ws is None:
-            if len(_WORKSPACE) > 4096:
-                _WORKSPACE.clear()
-            n_ws = _WORKSPACE[sizes] = load().dflash_shared_prefix_workspace(*sizes)
-        if n_ws > KEPT_MAX or _raw_stream(dev) != 0:
-            workspace = torch.empty(n_ws, dtype=_U8T, device=q.device)
-            _call(fn, _ATTN.pack, (*args, workspace.data_ptr(), n_ws), dev)
-        else:
-            with _KEPT_LOCK:
-                kept = _KEPT.get(dev)
-                if kept is None or kept[0] < n_ws:
-                    workspace = torch.empty(n_ws, dtype=_U8T, device=q.device)
-                    kept = _KEPT[dev] = (n_ws, workspace.data_ptr(), workspace)
-                _call(fn, _ATTN.pack, (*args, kept[1], n_ws), dev)
+    _attend(fn, _ATTN.pack, args, (), (dt, h, hkv, hd, batch, rows), workspace, dev, q.device)
     _written(out, lse)
     return out, lse
 

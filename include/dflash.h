@@ -648,6 +648,274 @@ typedef struct {
 } dflash_logits_args;
 dflash_status dflash_process_logits(const dflash_logits_args* args, void* cuda_stream);
 
+/* ------------------------------------------------------ trees of drafted tokens
+ * A sequence's rows q_start[s] .. q_start[s+1]-1 (m of them) are the nodes of
+ * a tree in drafting order: node 0 is the root (the anchor, committed whatever
+ * the target says), a node's parent comes before it.  kv_lens[s] counts the
+ * sequence's own keys, those of the m nodes, its last, among them: node i is
+ * own key kv_lens[s] - m + i.  At most DFLASH_TREE_MAX_NODES nodes a tree. */
+enum { DFLASH_TREE_MAX_NODES = 1024 };
+
+/* Masks, depths and positions of trees from their nodes' parents.
+ *   masks[r]   = bit i % 32 of word i / 32 set for node r itself and each of
+ *                its ancestors i, `words` words; the others 0
+ *   depth[r]   = links between node r and its root
+ *   row_pos[r] = base_pos + kv_lens[s] - m + depth[r]
+ * parents[r] is the parent's number in its tree or -1 (a root).
+ * status[s] (device): 0, or a sum of 1 (a parent that does not come before its
+ * child, or below -1), 2 (more nodes than 32 * words or than
+ * DFLASH_TREE_MAX_NODES), 4 (q_start decreases or leaves [0, rows]).  With 1 or
+ * 2 the sequence's rows get masks 0, depth -1 and row_pos -1, with 4 nothing
+ * of it is written.  Rows of no sequence are left as they were.
+ * Errors: E_INVAL (sizes, NULL), E_CUDA. */
+typedef struct {
+    int32_t batch;             /* 1 .. DFLASH_OPS_MAX_BATCH */
+    int32_t rows;              /* rows of parents, masks, depth and row_pos, at most 2^20 */
+    int32_t words;             /* words a mask, at least 1 */
+    int32_t base_pos;          /* position of a sequence's first own key (a shared prefix before it) */
+    int64_t ld_mask;           /* words between masks */
+    const int32_t* parents;    /* [rows] */
+    const int32_t* q_start;    /* [batch + 1] */
+    const int32_t* kv_lens;    /* [batch]; NULL when row_pos is */
+    uint32_t* masks;           /* [rows][ld_mask] */
+    int32_t* depth;            /* [rows] or NULL */
+    int32_t* row_pos;          /* [rows] or NULL */
+    int32_t* status;           /* [batch] */
+} dflash_tree_masks_args;
+dflash_status dflash_tree_masks(const dflash_tree_masks_args* args, void* cuda_stream);
+
+/* Attention of trees: dflash_shared_prefix_attention (all that it says holds,
+ * workspace, flags and an empty prefix included; attn.causal is ignored), but
+ * row r of sequence s sees, behind the prefix, its committed keys
+ * i < kv_lens[s] - m and of the m nodes' keys those whose bit is set in
+ * masks[r] (bit i % 32 of word i / 32 for node i; nodes behind the last word
+ * are not seen).  Masks are any sets: dflash_tree_masks makes those of trees.  A
+ * row that sees no key gets out = 0 and lse = -inf.  What a node's key and value
+ * hold does not matter to a row if no row of its sequence sees the node; the
+ * values of nodes that some row sees must be finite, like all valid tokens'.
+ * Errors: E_INVAL, E_CUDA. */
+typedef struct {
+    dflash_shared_prefix_args attn;
+    const uint32_t* masks;     /* [attn.rows][ld_mask] */
+    int64_t ld_mask;           /* words between masks */
+    int32_t words;             /* words a mask, 1 .. 2^20 */
+    int32_t reserved;          /* 0 */
+} dflash_tree_attention_args;
+dflash_status dflash_tree_attention(const dflash_tree_attention_args* args, void* cuda_stream);
+
+/* Greedy acceptance of a verified tree: from the root on, the child that holds
+ * the target's choice, the lowest where several do, until none does.
+ *   path[s][0 .. accepted[s]] = the nodes kept, root first; behind them -1
+ *   accepted[s] = drafts accepted (nodes kept but the root), at most width - 1
+ *   bonus[s]    = posterior of the last node kept: the next anchor
+ * parents, tokens, posterior: per row, the parent's number in the tree (-1: a
+ * root), the drafted token, the target's choice behind the row.  A sequence
+ * without rows gets accepted = bonus = -1 and a path of -1.
+ * status[s] (device): as dflash_tree_masks (2: more than
+ * DFLASH_TREE_MAX_NODES nodes); when not 0, accepted = bonus = -1, path -1.
+ * Errors: E_INVAL (sizes, NULL), E_CUDA. */
+typedef struct {
+    int32_t batch;
+    int32_t rows;
+    int32_t width;             /* entries of a path, 1 .. DFLASH_TREE_MAX_NODES */
+    int32_t reserved;          /* 0 */
+    const int32_t* parents;    /* [rows] */
+    const int32_t* tokens;     /* [rows] */
+    const int32_t* posterior;  /* [rows] */
+    const int32_t* q_start;    /* [batch + 1] */
+    int32_t* path;             /* [batch][width] */
+    int32_t* accepted;         /* [batch] */
+    int32_t* bonus;            /* [batch] */
+    int32_t* status;           /* [batch] */
+} dflash_tree_accept_args;
+dflash_status dflash_tree_accept(const dflash_tree_accept_args* args, void* cuda_stream);
+
+/* Keeps the accepted nodes of a cache: in every layer, of keys and values
+ * alike, the token of node path[s][j] moves to node j's place, j <=
+ * accepted[s], and kv_out[s] = kv_lens[s] - m + accepted[s] + 1.  The places
+ * behind hold what they held, to be overwritten.  path must rise strictly, as
+ * dflash_tree_accept's does (any other rule of acceptance may fill it).
+ * A layer's cache is [n_pages][H_kv][64][hd], layers are ld_layer elements apart.
+ * status[s] (device): 0, or a sum of 1 (accepted outside [-1, width), or a path
+ * that does not rise within [0, m)), 4 (q_start decreases or is negative), 8
+ * (kv_lens outside [m, 64 * width_table]), 16 (a page of a moved token outside
+ * [0, n_pages)).  When not 0, nothing of the sequence moves and kv_out =
+ * kv_lens.  No two sequences may hold the same page among their nodes'.
+ * kv_out may not be kv_lens.  Errors: E_INVAL (sizes, NULL), E_CUDA. */
+typedef struct {
+    int32_t dtype;             /* F32 or BF16 */
+    int32_t batch;
+    int32_t layers;            /* 1 .. 1024 */
+    int32_t n_pages;
+    int32_t n_kv_heads;
+    int32_t head_dim;          /* a row of a head is a multiple of 16 bytes */
+    int32_t width;             /* entries of a path, 1 .. DFLASH_TREE_MAX_NODES */
+    int32_t width_table;       /* table entries per sequence */
+    int64_t ld_layer;          /* elements between layers (a multiple of 16 bytes) */
+    int64_t ld_table;
+    void* k_cache;             /* [layers][n_pages][H_kv][64][hd], 16-byte aligned */
+    void* v_cache;
+    const int32_t* table;      /* [batch][width_table] */
+    const int32_t* kv_lens;    /* [batch] */
+    const int32_t* q_start;    /* [batch + 1] */
+    const int32_t* path;       /* [batch][width] */
+    const int32_t* accepted;   /* [batch] */
+    int32_t* kv_out;           /* [batch] */
+    int32_t* status;           /* [batch] */
+} dflash_kv_compact_args;
+dflash_status dflash_kv_compact(const dflash_kv_compact_args* args, void* cuda_stream);
+
+/* ------------------------------------------------------ pages held by several
+ * refs[p] counts the holders of page p beyond its first: 0 for a free page and
+ * for one that a single sequence holds, so pages that dflash_kv_tables hands
+ * out need nothing.  The free list is dflash_kv_tables': entries 0 .. *used - 1
+ * are taken. */
+
+/* Sequences that continue others.  Child c continues sequence parents[c] (any
+ * number of children a parent) with n = kv_lens[parents[c]] tokens:
+ *   table_out[c][j] = the parent's page for j < n / 64, shared (its refs rise
+ *                     by one); for n % 64 > 0 entry n / 64 is the next page of
+ *                     free_pages (children in order) with the parent's last
+ *                     n % 64 tokens copied, keys and values of every layer;
+ *                     scratch_page behind
+ *   lens_out[c] = n, used_out = *used + pages taken
+ * A shared page is full, so neither side writes to it again.
+ * status (device): 0, or a sum of 1 (the pool has too few pages), 2 (a parent
+ * holds more than width pages), 8 (a negative length or *used, or a parent
+ * outside [0, batch)): nothing is taken, table_out, refs and the caches are as
+ * they were, lens_out is 0 and used_out = *used; and 16 (a page outside
+ * [0, n_pages)) alone: such an entry is copied as it is, counted and copied to
+ * or from nowhere, and the rest is done.
+ * used_out may be used; table_out may be rows of the same matrix behind table's.
+ * No other overlap.  Errors: E_INVAL (sizes, NULL), E_CUDA. */
+typedef struct {
+    int32_t dtype;
+    int32_t batch;             /* sequences of table and kv_lens: 1 .. DFLASH_OPS_MAX_BATCH */
+    int32_t children;          /* 1 .. DFLASH_OPS_MAX_BATCH */
+    int32_t width;             /* table entries per sequence, parents and children alike */
+    int32_t n_free;
+    int32_t scratch_page;
+    int32_t layers;            /* 1 .. 1024 */
+    int32_t n_pages;
+    int32_t n_kv_heads;
+    int32_t head_dim;
+    int64_t ld_layer;
+    int64_t ld_table;
+    int64_t ld_out;
+    void* k_cache;             /* as dflash_kv_compact */
+    void* v_cache;
+    const int32_t* parents;    /* [children] */
+    const int32_t* kv_lens;    /* [batch] */
+    const int32_t* table;      /* [batch][width] */
+    const int32_t* free_pages; /* [n_free] */
+    const int32_t* used;       /* [1] */
+    int32_t* refs;             /* [n_pages] */
+    int32_t* table_out;        /* [children][width] */
+    int32_t* lens_out;         /* [children] */
+    int32_t* used_out;         /* [1] */
+    int32_t* status;           /* [1] */
+} dflash_kv_fork_args;
+dflash_status dflash_kv_fork(const dflash_kv_fork_args* args, void* cuda_stream);
+
+/* Gives back the pages of sequences that have ended: each of the
+ * ceil(kv_lens[s] / 64) pages of the sequences seqs[0 .. n) loses a holder, and a
+ * page without one returns to the free list.  Returned pages lie in
+ * free_pages[used_out .. *used - 1] in the order of their first mention (seqs in
+ * order, then table entries): a release right behind the call that took the pages
+ * restores the list.  The tables and lengths of the sequences are the caller's to
+ * forget.
+ * status (device): 0, or a sum of 1 (more pages return than were taken), 2 (a
+ * length above 64 * width), 8 (a negative length, a *used outside [0, n_free], or
+ * a sequence outside [0, batch) or named twice), 16 (a page outside [0, n_pages)
+ * or with negative refs), 32 (a page returned by more sequences than hold it).
+ * When not 0, nothing changes and used_out = *used.
+ * used_out may be used.  Errors: E_INVAL (sizes, NULL), E_CUDA. */
+typedef struct {
+    int32_t batch;             /* sequences of table and kv_lens: 1 .. DFLASH_OPS_MAX_BATCH */
+    int32_t n;                 /* sequences that end: 1 .. DFLASH_OPS_MAX_BATCH */
+    int32_t width;             /* table entries per sequence, at most 2^18 */
+    int32_t n_free;
+    int32_t n_pages;
+    int32_t reserved;          /* 0 */
+    int64_t ld_table;
+    const int32_t* seqs;       /* [n] */
+    const int32_t* kv_lens;    /* [batch] */
+    const int32_t* table;      /* [batch][width] */
+    int32_t* free_pages;       /* [n_free] */
+    const int32_t* used;       /* [1] */
+    int32_t* refs;             /* [n_pages] */
+    int32_t* used_out;         /* [1] */
+    int32_t* status;           /* [1] */
+} dflash_kv_release_args;
+dflash_status dflash_kv_release(const dflash_kv_release_args* args, void* cuda_stream);
+
+/* ------------------------------------------------------ log probabilities
+ * Of each row of logits, x = logits * inv_temperature (the product rounded to
+ * fp32; so is all that follows):
+ *   lse          = ln sum_v exp(x_v)
+ *   logprobs[i]  = x_t - lse for the row's i-th token t; 0 for a t outside
+ *                  [0, vocab) (padding)
+ *   ranks[i]     = tokens ahead of t: of a larger logit, or an equal one and a
+ *                  lower id; -1 for padding
+ *   entropy      = -sum_v p_v ln p_v, p = exp(x - lse)
+ *   top_ids, top_logprobs = the k likeliest tokens, likeliest first, the lower id
+ *                  first among equal logits
+ * Tokens at -inf have probability 0; they are no alternatives: where fewer than k
+ * tokens are left, the list ends in id -1 and -inf.  A row of -inf alone has lse =
+ * logprobs = -inf and entropy 0.  A row that holds NaN or +inf gets NaN
+ * everywhere (but padding's 0), ranks and top_ids -1.
+ * Any of the outputs may be NULL.  Rows are ld_logits elements apart.
+ * Errors: E_INVAL, E_CUDA. */
+enum { DFLASH_LOGPROBS_MAX_TOKENS = 32, DFLASH_LOGPROBS_MAX_TOP = 32 };
+typedef struct {
+    int32_t dtype;             /* of logits: F32 or BF16 */
+    int32_t rows;
+    int32_t vocab;
+    int32_t n;                 /* tokens a row, 0 .. DFLASH_LOGPROBS_MAX_TOKENS */
+    int32_t k;                 /* alternatives a row, 0 .. DFLASH_LOGPROBS_MAX_TOP */
+    float inv_temperature;     /* > 0, finite */
+    int64_t ld_logits;
+    const void* logits;        /* [rows][vocab] */
+    const int32_t* tokens;     /* [rows][n]; NULL when n is 0 */
+    float* logprobs;           /* [rows][n] or NULL */
+    int32_t* ranks;            /* [rows][n] or NULL */
+    float* entropy;            /* [rows] or NULL */
+    float* lse;                /* [rows] or NULL */
+    int32_t* top_ids;          /* [rows][k] or NULL */
+    float* top_logprobs;       /* [rows][k] or NULL */
+} dflash_logprobs_args;
+dflash_status dflash_token_logprobs(const dflash_logprobs_args* args, void* cuda_stream);
+
+/* Gradient of a loss of those log probabilities and entropies by the logits,
+ * with p_v = exp(x_v - lse), g_i = grad_logprobs[i] (0 for padding) and h =
+ * grad_entropy:
+ *   out_v = inv_temperature * (sum_{i: t_i = v} g_i - p_v sum_i g_i
+ *                              - h p_v (ln p_v + entropy))
+ * in fp32, rounded once to the logits' type.  lse and entropy are what
+ * dflash_token_logprobs gave (both entropy and grad_entropy, or neither).  A row
+ * whose g and h are all 0 gets zeros, whatever it holds; one of -inf alone the
+ * g at its tokens.  out may be logits, with one row
+ * stride; no other overlap.
+ * Errors: E_INVAL, E_CUDA. */
+typedef struct {
+    int32_t dtype;             /* of logits and out */
+    int32_t rows;
+    int32_t vocab;
+    int32_t n;                 /* 0 .. DFLASH_LOGPROBS_MAX_TOKENS */
+    float inv_temperature;
+    int32_t reserved;          /* 0 */
+    int64_t ld_logits;
+    int64_t ld_out;
+    const void* logits;
+    const int32_t* tokens;     /* [rows][n]; NULL when n is 0 */
+    const float* lse;          /* [rows] */
+    const float* grad_logprobs; /* [rows][n]; NULL when n is 0 */
+    const float* entropy;      /* [rows] or NULL */
+    const float* grad_entropy; /* [rows] or NULL */
+    void* out;                 /* [rows][vocab] */
+} dflash_logprobs_grad_args;
+dflash_status dflash_token_logprobs_grad(const dflash_logprobs_grad_args* args, void* cuda_stream);
+
 /* Release every library-owned buffer.  NULL is a no-op. */
 void dflash_destroy(dflash_ctx* ctx);
 
