@@ -41,6 +41,30 @@ __device__ __forceinline__ float max_nan(float x, float y) {
     asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(x), "f"(y));
     return r;
 }
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ uint64_t pack2(float lo, float hi) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ void unpack2(uint64_t v, float& lo, float& hi) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
 // The G elements of a 16-byte vector.
 template <typename T>
 __device__ __forceinline__ void widen(const uint4& r, float* x) {
@@ -57,54 +81,130 @@ __device__ __forceinline__ void widen(const uint4& r, float* x) {
 }
 
 // ------------------------------------------------------------------------------ forward
-constexpr int NT = 256, WARPS = NT / 32, E = 16;  // threads; elements of a thread in a tile
+constexpr int E = 16;  // elements of a thread in a tile
 constexpr int MAXC = 8;
-constexpr int CAP = 4096;      // candidates in the list
-constexpr int MANY = 128;      // threads of a tile that may add to it
-constexpr int GROUPS = 64;
+constexpr int LIST = 512;            // candidates of the list
 constexpr int NOWHERE = 0x60000000;  // id of an element that is none
 constexpr uint64_t ABOVE_NOTHING = 0x0080000000000000ull;  // the smallest key of a token above -inf
+constexpr int CAP = 4096;  // of the list of a slice that overflows the short one: candidates,
+constexpr int MANY = 128;  // threads of a tile that may add to it
 
-struct Part {  // of a CTA, read by the cluster's first
-    float m, l, t;
+struct Part {  // what a CTA hands to the cluster's first
+    float3 sums;  // m, l, t
     int ahead[MAXT];
     uint64_t best[MAXK];
 };
+template <int NT>
 struct Shared {
-    Part part;
+    Part part, in[MAXC];
     float xt[MAXT];
     int id[MAXT];
-    float red[3][WARPS];
+    float3 red[NT / 32];
     int n_cand, n_keep, below;
+    float tau_v;
     uint64_t tau;
-    uint64_t group[GROUPS];
-    uint64_t all[MAXC * MAXK];
+    alignas(16) uint64_t group[NT / 4];
+    uint64_t keep[MAXK];
 };
+constexpr size_t LIST_BYTES = (CAP + 8) * 8;  // dynamic shared memory of the kernels with alternatives
 
 __device__ __forceinline__ uint64_t key_of(float x, int id) { return argmax_key(x + 0.f, (uint32_t)id); }  // (-0 is 0)
 __device__ __forceinline__ float key_value(uint64_t k) {
     const uint32_t u = (uint32_t)(k >> 32);
     return __uint_as_float(u & 0x80000000u ? u & 0x7FFFFFFFu : ~u);
 }
-template <typename V>
-__device__ __forceinline__ V ld_part(const V* local, int rank, int parts) {
-    if (parts == 1) return *local;
-    uint32_t remote;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(tc::smem_u32(local)), "r"(rank));
-    V v;
-    if constexpr (sizeof(V) == 8) {
-        asm volatile("ld.shared::cluster.b64 %0, [%1];" : "=l"(v) : "r"(remote) : "memory");
-    } else {
-        uint32_t w;
-        asm volatile("ld.shared::cluster.b32 %0, [%1];" : "=r"(w) : "r"(remote) : "memory");
-        v = *reinterpret_cast<V*>(&w);
+template <int N>
+struct Int {
+    static constexpr int value = N;
+};
+// The next value above x of T's (-0 is 0; NaN above +inf).
+template <typename T>
+__device__ __forceinline__ float next_above(float x) {
+    constexpr int STEP = sizeof(T) == 4 ? 1 : 1 << 16;
+    const int u = __float_as_int(x + 0.f);
+    return __int_as_float(u >= 0 ? u + STEP : u - STEP);
+}
+__device__ __forceinline__ void add_if_ge(int& n, float x, float y) {
+    asm("{\n .reg .pred p;\n setp.ge.f32 p, %1, %2;\n @p add.s32 %0, %0, 1;\n}" : "+r"(n) : "f"(x), "f"(y));
+}
+// Keys of list[0 .. n) above `mine`; list is 16-byte aligned and list[n] is 0 where n is odd.
+__device__ __forceinline__ int count_above(const uint64_t* list, int n, uint64_t mine) {
+    int c = 0;
+#pragma unroll 4
+    for (int j = 0; j < n; j += 2) {
+        const ulonglong2 y = *reinterpret_cast<const ulonglong2*>(list + j);
+        c += (y.x > mine) + (y.y > mine);
     }
-    return v;
+    return c;
+}
+// The same by four neighbouring threads, to each of them; list[n .. n + 8) is 0.
+__device__ __forceinline__ int count_above4(const uint64_t* list, int n, uint64_t mine) {
+    int c = 0;
+#pragma unroll 2
+    for (int j = 2 * (threadIdx.x & 3); j < n; j += 8) {
+        const ulonglong2 y = *reinterpret_cast<const ulonglong2*>(list + j);
+        c += (y.x > mine) + (y.y > mine);
+    }
+    c += __shfl_xor_sync(0xffffffffu, c, 1);
+    return c + __shfl_xor_sync(0xffffffffu, c, 2);
+}
+__device__ __forceinline__ void st_first(uint32_t* local, uint32_t v) {  // to the same place in the cluster's first CTA
+    uint32_t remote;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(remote) : "r"(tc::smem_u32(local)));
+    asm volatile("st.shared::cluster.b32 [%0], %1;" ::"r"(remote), "r"(v) : "memory");
 }
 
+// A CTA's part of a row: tokens before the first aligned vector and behind the last one are an extra tile of the last CTA's.
+template <typename T, int NT>
+struct Slice {
+    static constexpr int G = 16 / (int)sizeof(T), NV = E / G;
+    const T* X;
+    int head, vecs, left, v0, v1, whole, full, tiles;
+    __device__ __forceinline__ Slice(const T* row, int vocab, int rank, int parts) : X(row) {
+        head = min(vocab, (int)((16 - ((uintptr_t)X & 15)) & 15) / (int)sizeof(T));
+        vecs = (vocab - head) / G;
+        left = vocab - vecs * G;
+        const int per = (vecs + parts - 1) / parts;
+        v0 = min(vecs, rank * per);
+        v1 = min(vecs, v0 + per);
+        whole = (v1 - v0) / (NT * NV);
+        full = (v1 - v0 + NT * NV - 1) / (NT * NV);
+        tiles = full + (rank == parts - 1 && left > 0);
+    }
+    // this thread's elements of tile `it` (-inf where there are none)
+    __device__ __forceinline__ void load(int it, uint4 (&r)[NV]) const {
+        const int tid = threadIdx.x, at = v0 + it * NV * NT + tid;
+        const uint4* p = reinterpret_cast<const uint4*>(X + head) + at;
+        if (it < whole) {
+#pragma unroll
+            for (int i = 0; i < NV; ++i) r[i] = __ldcs(p + i * NT);
+            return;
+        }
+        const uint32_t NONE = sizeof(T) == 4 ? 0xFF800000u : 0xFF80FF80u;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            r[i] = make_uint4(NONE, NONE, NONE, NONE);
+            if (it < full && at + i * NT < v1) r[i] = __ldcs(p + i * NT);
+        }
+        if (it == full && it < tiles && tid < left) {
+            const T x = X[tid < head ? tid : tid + vecs * G];
+            if constexpr (sizeof(T) == 4) r[0].x = __float_as_uint(to_f32(x));
+            else r[0].x = 0xFF800000u | __float_as_uint(to_f32(x)) >> 16;
+        }
+    }
+    __device__ __forceinline__ int first_id(int it) const { return head + (v0 + it * NV * NT) * G; }
+    // id of element e of tile `it`
+    __device__ __forceinline__ int id(int it, int e) const {
+        const int tid = threadIdx.x;
+        if (it == full) return e == 0 && tid < left ? (tid < head ? tid : tid + vecs * G) : NOWHERE;
+        return first_id(it) + ((e / G) * NT + tid) * G + e % G;
+    }
+};
+
 // The list's k best keys alone (n > k of them are in it), its k-th best as the new tau.  By all threads; the k-th key is
-// found bit by bit.  Lists that need it come from rows whose logits rise along the vocabulary.
-__device__ __noinline__ void keep_best(Shared& S, uint64_t* cand, int n, int k) {
+// found bit by bit.
+template <int NT>
+__device__ __noinline__ void keep_best(Shared<NT>& S, uint64_t* cand, int n, int k) {
     const int tid = threadIdx.x;
     uint64_t kth = 0;
 #pragma unroll 1
@@ -123,9 +223,9 @@ __device__ __noinline__ void keep_best(Shared& S, uint64_t* cand, int n, int k) 
     if (tid == 0) S.n_keep = 0;
     __syncthreads();
     for (int i = tid; i < n; i += NT)
-        if (cand[i] >= kth) S.all[atomicAdd(&S.n_keep, 1)] = cand[i];
+        if (cand[i] >= kth) S.keep[atomicAdd(&S.n_keep, 1)] = cand[i];
     __syncthreads();
-    if (tid < k) cand[tid] = S.all[tid];
+    if (tid < k) cand[tid] = S.keep[tid];
     if (tid == 0) {
         S.n_cand = k;
         S.tau = kth;
@@ -133,47 +233,115 @@ __device__ __noinline__ void keep_best(Shared& S, uint64_t* cand, int n, int k) 
     __syncthreads();
 }
 
-template <typename T, bool TOP>
-__global__ void __launch_bounds__(NT) logprobs_kernel(dflash_logprobs_args a, int parts) {
-    constexpr int G = 16 / (int)sizeof(T), NV = E / G;
-    __shared__ Shared S;
-    extern __shared__ __align__(16) uint64_t cand[];  // [CAP] (TOP)
+// The candidates of a slice that has overflowed the short list, from its beginning, into the long one: its k best keys (or
+// all that it has), S.n_cand of them.  Before a tile could fill the list tau, now a key, is raised (where more than MANY threads
+// of a tile reach it: to the k-th largest of the maxima of groups of four threads, which at most 4 k threads reach) and the list
+// cut to the k best; keys are all different, so rows in any order and of any ties fit.  For rows whose logits rise along the
+// vocabulary, or are all alike.
+template <typename T, int NT>
+__device__ __noinline__ void candidates_again(Shared<NT>& S, uint64_t* cand, const Slice<T, NT>& sl, int k) {
+    const int tid = threadIdx.x;
+    __syncthreads();
+    if (tid == 0) {
+        S.n_cand = 0;
+        S.tau = ABOVE_NOTHING;
+    }
+    __syncthreads();
+    uint64_t tau = ABOVE_NOTHING;
+    float tau_v = key_value(tau);
+    int room = CAP;  // entries that are surely free
+#pragma unroll 1
+    for (int it = 0; it < sl.tiles; ++it) {
+        uint4 r[Slice<T, NT>::NV];
+        float x[E];
+        sl.load(it, r);
+#pragma unroll
+        for (int i = 0; i < Slice<T, NT>::NV; ++i) widen<T>(r[i], x + i * Slice<T, NT>::G);
+        float tm = x[0];
+#pragma unroll
+        for (int e = 1; e < E; ++e) tm = fmaxf(tm, x[e]);
+        int n = __syncthreads_count(tm >= tau_v);
+        if (n > MANY) {
+            uint64_t key = 0;
+            if (tm >= tau_v) {
+                int at = 0;
+#pragma unroll
+                for (int e = E - 1; e >= 0; --e)
+                    if (x[e] == tm) at = e;
+                key = key_of(tm, sl.id(it, at));
+            }
+#pragma unroll
+            for (int o = 1; o < 4; o <<= 1) {
+                const uint64_t y = __shfl_xor_sync(0xffffffffu, key, o);
+                key = y > key ? y : key;
+            }
+            if (tid % 4 == 0) S.group[tid / 4] = key;
+            __syncthreads();
+            if (tid < NT / 4) {
+                const uint64_t mine = S.group[tid];
+                if (mine > tau && count_above(S.group, NT / 4, mine) == k - 1) S.tau = mine;
+            }
+            __syncthreads();
+            tau = S.tau;
+            tau_v = key_value(tau);
+            n = MANY;
+        }
+        if (tm >= tau_v) {
+#pragma unroll
+            for (int e = 0; e < E; ++e)
+                if (x[e] >= tau_v) {
+                    const uint64_t key = key_of(x[e], sl.id(it, e));
+                    if (key >= tau) {
+                        const int at = atomicAdd(&S.n_cand, 1);
+                        if (at < CAP) cand[at] = key;
+                    }
+                }
+        }
+        room -= E * n;
+        if (room < E * MANY) {
+            __syncthreads();
+            const int have = min(S.n_cand, CAP);
+            __syncthreads();
+            room = CAP - have;
+            if (room < CAP / 2) {
+                keep_best<NT>(S, cand, have, k);
+                tau = S.tau;
+                tau_v = key_value(tau);
+                room = CAP - k;
+            }
+        }
+    }
+    __syncthreads();
+    const int have = min(S.n_cand, CAP);
+    __syncthreads();
+    if (have > k) keep_best<NT>(S, cand, have, k);
+}
+
+template <typename T, bool TOP, int NT>
+__global__ void __launch_bounds__(NT, 1024 / NT) logprobs_kernel(dflash_logprobs_args a, int parts) {
+    constexpr int G = 16 / (int)sizeof(T), NV = E / G, WARPS = NT / 32, GROUPS = NT / 4;
+    __shared__ Shared<NT> S;
+    extern __shared__ __align__(16) uint64_t list[];  // (TOP) keys of the list,
+    int* ids = reinterpret_cast<int*>(list + LIST + 8);  // and their ids
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const long long row = blockIdx.x;
     const int rank = parts > 1 ? (int)tc::cluster_rank() : 0;
-    const T* X = reinterpret_cast<const T*>(a.logits) + row * a.ld_logits;
+    // (its end: the first CTA's shared memory is there to be written to)
+    if (parts > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+    const Slice<T, NT> sl(reinterpret_cast<const T*>(a.logits) + row * a.ld_logits, a.vocab, rank, parts);
     pdl_wait();
     pdl_trigger();
-
-    // tokens before the first aligned vector and behind the last one go to an extra tile of the last CTA
-    const int head = min(a.vocab, (int)((16 - ((uintptr_t)X & 15)) & 15) / (int)sizeof(T));
-    const int vecs = (a.vocab - head) / G, left = a.vocab - vecs * G;
-    const int per = (vecs + parts - 1) / parts, v0 = min(vecs, rank * per), v1 = min(vecs, v0 + per);
-    const int full = (v1 - v0 + NT * NV - 1) / (NT * NV), tiles = full + (rank == parts - 1 && left > 0);
-    const uint32_t NONE = sizeof(T) == 4 ? 0xFF800000u : 0xFF80FF80u;  // -inf
-    auto load = [&](int it, uint4 (&r)[NV]) {
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            r[i] = make_uint4(NONE, NONE, NONE, NONE);
-            const int v = v0 + (it * NV + i) * NT + tid;
-            if (it < full && v < v1) r[i] = __ldcs(reinterpret_cast<const uint4*>(X + head) + v);
-        }
-        if (it == full && it < tiles && tid < left) {
-            const T x = X[tid < head ? tid : tid + vecs * G];
-            if constexpr (sizeof(T) == 4) r[0].x = __float_as_uint(to_f32(x));
-            else r[0].x = 0xFF800000u | __float_as_uint(to_f32(x)) >> 16;
-        }
-    };
     uint4 next[NV];
-    load(0, next);
+    sl.load(0, next);
 
+    // (seen by all behind the first tile's barrier)
     if (tid < MAXT) {
         int t = -1;
         float x = 0.f;
         if (tid < a.n) {
             t = a.tokens[row * a.n + tid];
             if (t < 0 || t >= a.vocab) t = -1;
-            else x = to_f32(X[t]);
+            else x = to_f32(sl.X[t]);
         }
         S.id[tid] = t;
         S.xt[tid] = x;
@@ -183,243 +351,336 @@ __global__ void __launch_bounds__(NT) logprobs_kernel(dflash_logprobs_args a, in
     static_assert(MAXT == MAXK, "one thread for both");
     if (tid == 0) {
         S.n_cand = 0;
-        S.tau = ABOVE_NOTHING;
+        S.tau_v = -INFINITY;
     }
-    __syncthreads();
 
     const float c = a.inv_temperature * LOG2E;
+    const uint64_t c2 = pack2(c, c);
     float m = -INFINITY, l = 0.f, t = 0.f;
-    uint64_t tau = ABOVE_NOTHING;
-    float tau_v = key_value(tau);
-    int room = CAP;  // entries that are surely free
+    int my_id = -1;  // lane's token and its logit
+    float my_xt = 0.f;
+    float tau_v = -INFINITY;  // candidates are as large (-inf: not known yet)
+    int refresh = 2;
+    // f(its key, the keys above it) for each of the list's n keys, by all threads, four a key; ends without a barrier
+    auto rank_list = [&](int n, auto&& f) {
+        for (int i0 = 0; i0 < n; i0 += NT / 4) {
+            const uint64_t mine = list[min(i0 + tid / 4, n)];
+            const int above = count_above4(list, n, mine);
+            if (mine && (tid & 3) == 0) f(mine, above);
+        }
+    };
+    int keyed = 0;  // of the list, keys; from there on, ids
+    auto make_keys = [&](int n) {
+        for (int i = keyed + tid; i < n; i += NT) list[i] = key_of(to_f32(sl.X[ids[i]]), ids[i]);
+        if (tid < 8) list[n + tid] = 0;
+        keyed = n;
+    };
 #pragma unroll 1
-    for (int it = 0; it < tiles; ++it) {
+    for (int it = 0; it < sl.tiles; ++it) {
         float x[E];
-#pragma unroll
-        for (int i = 0; i < NV; ++i) widen<T>(next[i], x + i * G);
-        load(it + 1, next);
-        const bool single = it == full;  // (one element a thread)
-        int id[NV];
+        uint4 raw[NV];
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            const int v = v0 + (it * NV + i) * NT + tid;
-            id[i] = v < v1 ? head + v * G : NOWHERE;
+            raw[i] = next[i];
+            widen<T>(next[i], x + i * G);
         }
-        if (single) id[0] = tid < left ? (tid < head ? tid : tid + vecs * G) : NOWHERE;
+        sl.load(it + 1, next);
 
         // ---- statistics
         float tm = fmaxf(x[0], x[1]);
 #pragma unroll
-        for (int e = 2; e < E; e += 2) tm = fmaxf(tm, fmaxf(x[e], x[e + 1]));
+        for (int e = 2; e < E; e += 2) tm = fmaxf(fmaxf(tm, x[e]), x[e + 1]);
         if (tm > m) {
             const float d = (m - tm) * c, al = ex2(d);
             t = m == -INFINITY ? 0.f : al * fmaf(l, max_nan(d, -1000.f), t);
             l *= al;
             m = tm;
         }
-        const float ref = m == -INFINITY ? 0.f : m;
-        if (a.entropy) {
+        const float ref = m == -INFINITY ? 0.f : -m;
+        const uint64_t ref2 = pack2(ref, ref);
+        {
+            uint64_t l2[2] = {0ull, 0ull}, t2[2] = {0ull, 0ull};
 #pragma unroll
-            for (int e = 0; e < E; ++e) {
-                const float y = max_nan((x[e] - ref) * c, -1000.f), p = ex2(y);
-                l += p;
-                t = fmaf(p, y, t);
+            for (int e = 0; e < E; e += 2) {
+                float y0, y1;
+                unpack2(mul2(add2(pack2(x[e], x[e + 1]), ref2), c2), y0, y1);
+                y0 = max_nan(y0, -1000.f);  // (2^y y = 0 for a token at -inf)
+                y1 = max_nan(y1, -1000.f);
+                const uint64_t p2 = pack2(ex2(y0), ex2(y1));
+                l2[(e >> 1) & 1] = add2(l2[(e >> 1) & 1], p2);
+                t2[(e >> 1) & 1] = fma2(p2, pack2(y0, y1), t2[(e >> 1) & 1]);
             }
-        } else {
-#pragma unroll
-            for (int e = 0; e < E; ++e) l += ex2((x[e] - ref) * c);
+            float s0, s1;
+            unpack2(add2(l2[0], l2[1]), s0, s1);
+            l += s0 + s1;
+            unpack2(add2(t2[0], t2[1]), s0, s1);
+            t += s0 + s1;
         }
 
-        // ---- ranks
-        if (a.ranks)
+        // ---- a first tau, from the first tile that holds enough tokens (tau_v is the CTA's): among the maxima of the groups of
+        // four threads the k-th largest, which k elements reach
+        if (TOP && tau_v == -INFINITY) {
+            float* group = reinterpret_cast<float*>(S.group);
+            float g = fmaxf(tm, __shfl_xor_sync(0xffffffffu, tm, 1));
+            g = fmaxf(g, __shfl_xor_sync(0xffffffffu, g, 2));
+            if (tid % 4 == 0) group[tid / 4] = g;
+            __syncthreads();
+            int n = 0;  // groups above, and 2^16 times those as large
+#pragma unroll 4
+            for (int j = 4 * (tid & 3); j < GROUPS; j += 16) {
+                const float4 y = *reinterpret_cast<const float4*>(group + j);
+                n += (y.x > g) + (y.y > g) + (y.z > g) + (y.w > g);
+                n += ((y.x == g) + (y.y == g) + (y.z == g) + (y.w == g)) << 16;
+            }
+            n += __shfl_xor_sync(0xffffffffu, n, 1);
+            n += __shfl_xor_sync(0xffffffffu, n, 2);
+            const int above = n & 0xFFFF;
+            if (tid % 4 == 0 && above < a.k && above + (n >> 16) >= a.k) S.tau_v = g;  // (the same value from each that writes)
+            __syncthreads();
+            tau_v = S.tau_v;
+        } else if (!TOP && it == 0) {
+            __syncthreads();
+        }
+
+        // ---- ranks: of the ids behind the token's those of a larger logit count, of the ids before it also those of the same
+        if (a.ranks) {
+            const int first = sl.first_id(it), end = it == sl.full ? 0 : first + NT * E;
+            if (it == 0 && lane < a.n) {
+                my_id = S.id[lane];
+                my_xt = S.xt[lane];
+            }
+            const bool before = my_id >= end && end > 0;  // lane's token lies behind the tile
+            const float my_least = before ? my_xt : next_above<T>(my_xt);
+            // tokens q .. q + Q - 1: a warp's counts to shared memory
+            auto count = [&](int q, auto Qc) {
+                constexpr int Q = decltype(Qc)::value;
+                uint32_t n[(Q + 1) / 2];  // two tokens' counts each
+#pragma unroll
+                for (int i = 0; i < (Q + 1) / 2; ++i) n[i] = 0;
+#pragma unroll
+                for (int i = 0; i < Q; ++i) {
+                    const float least = __shfl_sync(0xffffffffu, my_least, q + i);
+                    int mine;
+                    if constexpr (sizeof(T) == 4) {
+                        int n0 = 0, n1 = 0;
+#pragma unroll
+                        for (int e = 0; e < E; e += 2) {
+                            add_if_ge(n0, x[e], least);
+                            add_if_ge(n1, x[e + 1], least);
+                        }
+                        mine = n0 + n1;
+                    } else {
+                        // (0 or 1 in bf16: sums up to 256 are exact)
+                        const __nv_bfloat162 l2 = __float2bfloat162_rn(least);
+                        __nv_bfloat162 n2[2] = {__float2bfloat162_rn(0.f), __float2bfloat162_rn(0.f)};
+#pragma unroll
+                        for (int j = 0; j < NV; ++j) {
+                            const uint32_t w[4] = {raw[j].x, raw[j].y, raw[j].z, raw[j].w};
+#pragma unroll
+                            for (int k = 0; k < 4; ++k)
+                                n2[k & 1] = __hadd2(n2[k & 1], __hge2(*reinterpret_cast<const __nv_bfloat162*>(&w[k]), l2));
+                        }
+                        n2[0] = __hadd2(n2[0], n2[1]);
+                        mine = __float2int_rn(__low2float(n2[0]) + __high2float(n2[0]));
+                    }
+                    n[i / 2] += (uint32_t)mine << 16 * (i & 1);
+                }
+#pragma unroll
+                for (int i = 0; i < (Q + 1) / 2; ++i) n[i] = __reduce_add_sync(0xffffffffu, n[i]);
+                uint32_t v = n[0];
+#pragma unroll
+                for (int i = 1; i < (Q + 1) / 2; ++i)
+                    if (lane / 2 == i) v = n[i];
+                v = v >> 16 * (lane & 1) & 0xFFFFu;
+                if (lane < Q && v) atomicAdd(&S.part.ahead[q + lane], (int)v);
+            };
+            int q = 0;
 #pragma unroll 1
-            for (int q = 0; q < a.n; ++q) {
-                const float xt = S.xt[q];
-                const int at = S.id[q];
-                if (at < 0 || !__any_sync(0xffffffffu, tm >= xt)) continue;
-                int ahead = 0;
+            for (; q + 4 <= a.n; q += 4) count(q, Int<4>());
+#pragma unroll 1
+            for (; q < a.n; ++q) count(q, Int<1>());
+            // the tile that holds a token has ids on both sides of it: those before it of the same logit; and elements that are
+            // none, which are -inf, have been counted as large as a token at -inf behind them
+            const bool here = my_id >= 0 && (it == sl.full || (my_id >= first && my_id < end)),
+                       extra = before && it >= sl.whole && my_xt == -INFINITY;
+            for (uint32_t w = __ballot_sync(0xffffffffu, here || extra); w; w &= w - 1) {
+                const int i = __ffs(w) - 1, at = __shfl_sync(0xffffffffu, my_id, i);
+                const float xt = __shfl_sync(0xffffffffu, my_xt, i);
+                int n = 0;
 #pragma unroll
-                for (int i = 0; i < NV; ++i) {
-                    if (single) {
-                        if (i == 0) ahead += x[0] > xt || (x[0] == xt && id[0] < at);
-                    } else if (id[i] > at) {
-#pragma unroll
-                        for (int e = 0; e < G; ++e) ahead += x[i * G + e] > xt;
+                for (int j = 0; j < NV; ++j) {
+                    const int id = it < sl.full && sl.v0 + (it * NV + j) * NT + tid >= sl.v1 ? NOWHERE : sl.id(it, j * G);
+                    if (at >= end && end > 0) {
+                        if (id == NOWHERE) n -= G;
                     } else {
 #pragma unroll
-                        for (int e = 0; e < G; ++e) ahead += x[i * G + e] > xt || (x[i * G + e] == xt && id[i] + e < at);
+                        for (int e = 0; e < G; ++e) n += x[j * G + e] == xt && id + e < at && (e == 0 || it < sl.full);
                     }
                 }
-                ahead = __reduce_add_sync(0xffffffffu, ahead);
-                if (lane == 0 && ahead) atomicAdd(&S.part.ahead[q], ahead);
+                n = __reduce_add_sync(0xffffffffu, n);
+                if (lane == 0 && n) atomicAdd(&S.part.ahead[i], n);
             }
+        }
 
-        // ---- candidates
+        // ---- candidates; tau becomes the k-th best of the list now and then
         if (TOP) {
-            bool may = tm >= tau_v;
-            int n = __syncthreads_count(may);
-            if (n > MANY) {
-                uint64_t key = 0;
-                if (may) {
-#pragma unroll
-                    for (int e = E - 1; e >= 0; --e)
-                        if (x[e] == tm) key = key_of(tm, id[e / G] + e % G);
-                }
-#pragma unroll
-                for (int o = 1; o < NT / GROUPS; o <<= 1) {
-                    const uint64_t y = __shfl_xor_sync(0xffffffffu, key, o);
-                    key = y > key ? y : key;
-                }
-                if (tid % (NT / GROUPS) == 0) S.group[tid / (NT / GROUPS)] = key;
-                __syncthreads();
-                if (tid < GROUPS) {
-                    const uint64_t mine = S.group[tid];
-                    int above = 0;
-#pragma unroll 8
-                    for (int j = 0; j < GROUPS; ++j) above += S.group[j] > mine;
-                    if (above == a.k - 1 && mine > tau) S.tau = mine;
-                }
-                __syncthreads();
-                tau = S.tau;
-                tau_v = key_value(tau);
-                may = tm >= tau_v;
-                n = MANY;
-            }
-            if (may) {
+            const float least_v = fmaxf(tau_v, -3.402823466e38f);  // (-inf is none)
+            if (tm >= least_v) {
+                uint32_t on = 0;
 #pragma unroll
                 for (int e = 0; e < E; ++e)
-                    if (x[e] >= tau_v) {
-                        const uint64_t key = key_of(x[e], id[e / G] + e % G);
-                        if (key >= tau) {
-                            const int at = atomicAdd(&S.n_cand, 1);
-                            if (at < CAP) cand[at] = key;
-                        }
-                    }
-            }
-            room -= E * n;
-            if (room < E * MANY) {
-                __syncthreads();
-                const int have = min(S.n_cand, CAP);
-                __syncthreads();
-                room = CAP - have;
-                if (room < CAP / 2) {
-                    keep_best(S, cand, have, a.k);
-                    tau = S.tau;
-                    tau_v = key_value(tau);
-                    room = CAP - a.k;
+                    if (x[e] >= least_v) on |= 1u << e;
+                int at = atomicAdd(&S.n_cand, __popc(on));
+                for (; on; on &= on - 1, ++at) {
+                    if (at < LIST) ids[at] = sl.id(it, __ffs(on) - 1);
                 }
+            }
+            if (it == refresh && it + 2 < sl.tiles) {  // (behind 3, 9, 33 .. tiles)
+                refresh *= 4;
+                __syncthreads();
+                const int n = S.n_cand;
+                if (n >= a.k && n <= LIST) {
+                    make_keys(n);
+                    __syncthreads();
+                    rank_list(n, [&](uint64_t key, int above) {
+                        if (above == a.k - 1) S.tau_v = key_value(key);
+                    });
+                }
+                __syncthreads();
+                tau_v = S.tau_v;
             }
         }
     }
 
-    // ---- the CTA's results
+    // ---- the CTA's results (the list's logits come while the warps join their sums)
+    int n = 0;
+    if (TOP) {
+        __syncthreads();
+        n = S.n_cand;
+        if (n <= LIST) make_keys(n);
+    }
     {
-        float M = warp_max(m);
+        const float M = warp_max(m);
         const float al = m == -INFINITY ? 0.f : ex2((m - M) * c);
         t = m == -INFINITY ? 0.f : al * fmaf(l, max_nan((m - M) * c, -1000.f), t);
         l = warp_sum(l * al);
         t = warp_sum(t);
-        if (lane == 0) {
-            S.red[0][warp] = M;
-            S.red[1][warp] = l;
-            S.red[2][warp] = t;
-        }
+        if (lane == 0) S.red[warp] = make_float3(M, l, t);
     }
     __syncthreads();
-    if (TOP) {
-        int n = min(S.n_cand, CAP);
-        if (n > 512) {
-            __syncthreads();
-            keep_best(S, cand, n, a.k);
-            n = a.k;
+    // sums of `count` places, the same in every thread
+    auto join = [&](int count, auto&& at) {
+        float3 y[MAXC];
+        float M = -INFINITY, L = 0.f, Z = 0.f;
+#pragma unroll
+        for (int i0 = 0; i0 < NT / 32; i0 += MAXC) {
+            if (i0 >= count) break;
+            const float before = M;
+#pragma unroll
+            for (int i = 0; i < MAXC; ++i) {
+                y[i] = i0 + i < count ? at(i0 + i) : make_float3(-INFINITY, 0.f, 0.f);
+                M = fmaxf(M, y[i].x);
+            }
+            auto add = [&](float m0, float l0, float t0) {
+                const float d = (m0 - M) * c, al = m0 == -INFINITY ? 0.f : ex2(d);
+                L = fmaf(l0, al, L);
+                if (m0 != -INFINITY) Z = fmaf(al, fmaf(l0, max_nan(d, -1000.f), t0), Z);
+            };
+            const float l0 = L, z0 = Z;
+            L = Z = 0.f;
+            add(before, l0, z0);
+#pragma unroll
+            for (int i = 0; i < MAXC; ++i) add(y[i].x, y[i].y, y[i].z);
         }
-        for (int i = tid; i < n; i += NT) {
-            const uint64_t mine = cand[i];
-            int above = 0;
-            for (int j = 0; j < n; ++j) above += cand[j] > mine;
-            if (above < a.k) S.part.best[above] = mine;
-        }
-    }
-    // (M, l, t) of lanes 0 .. n-1 joined in all of them
-    auto join = [&](int n) {
-        const float M = warp_max(lane < n ? m : -INFINITY);
-        const float al = m == -INFINITY ? 0.f : ex2((m - M) * c);
-        t = lane >= n || m == -INFINITY ? 0.f : al * fmaf(l, max_nan((m - M) * c, -1000.f), t);
-        l = warp_sum(lane < n ? l * al : 0.f);
-        t = warp_sum(t);
-        m = M;
+        return make_float3(M, L, Z);
     };
-    if (warp == 0) {
-        if (lane < WARPS) {
-            m = S.red[0][lane];
-            l = S.red[1][lane];
-            t = S.red[2][lane];
-        }
-        join(WARPS);
-        if (lane == 0) {
-            S.part.m = m;
-            S.part.l = l;
-            S.part.t = t;
-        }
-    }
-    __syncwarp();
-    if (parts > 1) tc::cluster_sync();
-    else __syncthreads();
-    if (rank == 0) {
-        // ---- the row's: every warp joins the parts
-        const int r = min(lane, parts - 1);
-        m = ld_part(&S.part.m, r, parts);
-        l = ld_part(&S.part.l, r, parts);
-        t = ld_part(&S.part.t, r, parts);
-        join(parts);
-        const bool bad = isnan(l) || m == INFINITY, none = l == 0.f;
-        const float ln_l = logf(l);
-        auto logprob = [&](float x) { return bad ? NAN : x == -INFINITY ? -INFINITY : (x - m) * a.inv_temperature - ln_l; };
-        if (tid == 0) {
-            if (a.lse) a.lse[row] = bad ? NAN : none ? -INFINITY : fmaf(m, a.inv_temperature, ln_l);
-            if (a.entropy) a.entropy[row] = bad ? NAN : none ? 0.f : ln_l - LN2 * (t / l);
-        }
-        if (tid < a.n) {
-            const int at = S.id[tid];
-            int ahead = 0;
-            for (int q = 0; q < parts; ++q) ahead += ld_part(&S.part.ahead[tid], q, parts);
-            if (a.logprobs) a.logprobs[row * a.n + tid] = at < 0 ? 0.f : logprob(S.xt[tid]);
-            if (a.ranks) a.ranks[row * a.n + tid] = at < 0 || bad ? -1 : ahead;
-        }
-        if (TOP) {
-            const int q = tid / MAXK, i = tid % MAXK;
-            const uint64_t mine = q < parts ? ld_part(&S.part.best[i], q, parts) : 0;
-            if (q < parts) S.all[tid] = mine;
-            if (tid < a.k) {  // (what a row of few tokens leaves)
-                if (a.top_ids) a.top_ids[row * a.k + tid] = -1;
-                if (a.top_logprobs) a.top_logprobs[row * a.k + tid] = bad ? NAN : -INFINITY;
-            }
+    if (tid == NT - 1) S.part.sums = join(WARPS, [&](int i) { return S.red[i]; });
+    if (TOP) {
+        if (n > LIST) {
+            candidates_again<T, NT>(S, list, sl, a.k);
+            n = S.n_cand;
+            if (tid < 8) list[n + tid] = 0;
             __syncthreads();
-            if (mine && !bad) {
-                int above = 0;
-                for (int s = 0; s < parts; ++s)
-                    for (int j = 0; j < a.k; ++j) above += S.all[s * MAXK + j] > mine;
-                if (above < a.k) {
-                    if (a.top_ids) a.top_ids[row * a.k + above] = (int)argmax_key_index(mine);
-                    if (a.top_logprobs) a.top_logprobs[row * a.k + above] = logprob(key_value(mine));
-                }
+        }
+        rank_list(n, [&](uint64_t key, int above) {
+            if (above < a.k) S.part.best[above] = key;
+        });
+    }
+    __syncthreads();
+    constexpr int WORDS = sizeof(Part) / 4;
+    static_assert(WORDS <= NT, "a thread a word");
+    if (parts > 1) {
+        asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
+        if (tid < WORDS) st_first(reinterpret_cast<uint32_t*>(&S.in[rank]) + tid, reinterpret_cast<const uint32_t*>(&S.part)[tid]);
+        __syncwarp();
+        tc::cluster_sync();
+        if (rank != 0) return;
+    }
+    const Part* in = parts > 1 ? S.in : &S.part;
+
+    // ---- the row's
+    const float3 sums = join(parts, [&](int i) { return in[i].sums; });
+    m = sums.x;
+    const bool bad = isnan(sums.y) || m == INFINITY, none = sums.y == 0.f;
+    const float ln_l = logf(sums.y);
+    auto logprob = [&](float x) { return bad ? NAN : x == -INFINITY ? -INFINITY : (x - m) * a.inv_temperature - ln_l; };
+    if (tid == NT - 1) {
+        if (a.lse) a.lse[row] = bad ? NAN : none ? -INFINITY : fmaf(m, a.inv_temperature, ln_l);
+        if (a.entropy) a.entropy[row] = bad ? NAN : none ? 0.f : ln_l - LN2 * (sums.z / sums.y);
+    }
+    if (tid < a.n) {
+        const int at = S.id[tid];
+        int ahead = 0;
+        for (int q = 0; q < parts; ++q) ahead += in[q].ahead[tid];
+        if (a.logprobs) a.logprobs[row * a.n + tid] = at < 0 ? 0.f : logprob(S.xt[tid]);
+        if (a.ranks) a.ranks[row * a.n + tid] = at < 0 || bad ? -1 : ahead;
+    }
+    if (TOP) {
+        // The lists are sorted (0 behind): an alternative's place is the number of keys above it in each of them.
+        const int q = tid / MAXK, i = tid % MAXK;
+        const uint64_t mine = q < parts && i < a.k ? in[q].best[i] : 0;
+        int found = 0;  // alternatives of the row (k or more, or, where it has fewer tokens, all)
+        for (int s = 0; s < parts; ++s) found += __popc(__ballot_sync(0xffffffffu, in[s].best[lane] != 0));
+        if (tid < a.k && (bad || tid >= found)) {
+            if (a.top_ids) a.top_ids[row * a.k + tid] = -1;
+            if (a.top_logprobs) a.top_logprobs[row * a.k + tid] = bad ? NAN : -INFINITY;
+        }
+        if (mine && !bad) {
+            int above = 0;
+#pragma unroll
+            for (int s = 0; s < MAXC; ++s) {
+                const uint64_t* y = in[min(s, parts - 1)].best;
+                int at = 0;
+#pragma unroll
+                for (int step = MAXK / 2; step; step >>= 1) at += y[at + step - 1] > mine ? step : 0;
+                at += y[at] > mine;
+                above += s < parts ? at : 0;
+            }
+            if (above < a.k) {
+                if (a.top_ids) a.top_ids[row * a.k + above] = (int)argmax_key_index(mine);
+                if (a.top_logprobs) a.top_logprobs[row * a.k + above] = logprob(key_value(mine));
             }
         }
     }
-    __syncwarp();
-    if (parts > 1) tc::cluster_sync();  // (no CTA leaves while its results are read)
 }
-static_assert(MAXC * MAXK == NT, "a thread for every part's every alternative");
 
+template <typename T, int NT>
+void forward(const Launch& L, const dflash_logprobs_args& a, int parts) {
+    static_assert(MAXC * MAXK <= NT, "a thread for every part's every alternative");
+    const bool top = a.k > 0 && (a.top_ids || a.top_logprobs);
+    if (top) launch_k(L, logprobs_kernel<T, true, NT>, dim3(a.rows, 1, parts), dim3(NT), LIST_BYTES, parts, a, parts);
+    else launch_k(L, logprobs_kernel<T, false, NT>, dim3(a.rows, 1, parts), dim3(NT), 0, parts, a, parts);
+}
+// A row goes to so many CTAs that there are four an SM, if its tiles last (512 rows of 151936 in one, two and four parts: 66, 63
+// and 75 us; 64 bf16 rows of 128256 in two, four and eight: 25, 19 and 19), and to wider ones where every CTA has an SM
+// of its own (one row: 9.6 us, with 256 threads 11.7).
 template <typename T>
 void forward(const Launch& L, const dflash_logprobs_args& a) {
-    const int G = 16 / (int)sizeof(T);
-    const long long tiles = ((long long)a.vocab / G + NT * (E / G) - 1) / (NT * (E / G));
+    const long long tiles = ((long long)a.vocab + 256 * E - 1) / (256 * E);
     int parts = 1;
-    while (parts < MAXC && 2 * parts <= tiles && (long long)a.rows * parts < 152 * 16) parts *= 2;
-    const bool top = a.k > 0 && (a.top_ids || a.top_logprobs);
-    if (top) launch_k(L, logprobs_kernel<T, true>, dim3(a.rows, 1, parts), dim3(NT), CAP * 8, parts, a, parts);
-    else launch_k(L, logprobs_kernel<T, false>, dim3(a.rows, 1, parts), dim3(NT), 0, parts, a, parts);
+    while (parts < MAXC && 2 * parts <= tiles && (long long)a.rows * parts < 608) parts *= 2;
+    if ((long long)a.rows * parts <= 152 && tiles >= 2 * parts) forward<T, 512>(L, a, parts);
+    else forward<T, 256>(L, a, parts);
 }
 
 // ----------------------------------------------------------------------------- backward
