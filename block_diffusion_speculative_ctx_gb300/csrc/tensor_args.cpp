@@ -103,6 +103,70 @@ PyObject* rows3(PyObject*, PyObject* const* a, Py_ssize_t na) {
     });
 }
 
+// ints(dev, name, t, n, name, t, n, ...): addresses of contiguous int32 tensors of n elements each
+PyObject* ints(PyObject*, PyObject* const* a, Py_ssize_t na) {
+    if (na < 1 || na % 3 != 1) return PyErr_Format(PyExc_TypeError, "a device, and a name, a tensor and a number each");
+    return guarded([&]() -> PyObject* {
+        const long dev = PyLong_AsLong(a[0]);
+        if (PyErr_Occurred()) return nullptr;
+        PyObject* out = PyTuple_New(na / 3);
+        if (!out) return nullptr;
+        for (Py_ssize_t i = 0; i < na / 3; ++i) {
+            PyObject *name = a[3 * i + 1], *o = a[3 * i + 2];
+            const at::Tensor* t = tensor(o);
+            const long long n = PyLong_AsLongLong(a[3 * i + 3]);
+            if (!t || PyErr_Occurred()) {
+                Py_DECREF(out);
+                return nullptr;
+            }
+            if (t->scalar_type() != at::kInt || t->numel() != n || t->get_device() != dev || !t->is_contiguous()) {
+                Py_DECREF(out);
+                return refuse(name, PyUnicode_FromFormat("a contiguous torch.int32 tensor of %lld elements", n), dev, o);
+            }
+            PyObject* address = PyLong_FromVoidPtr(t->data_ptr());
+            if (!address) {
+                Py_DECREF(out);
+                return nullptr;
+            }
+            PyTuple_SET_ITEM(out, i, address);
+        }
+        return out;
+    });
+}
+
+// caches(k, v, dev): (dtype code, layers, pages, heads, hd, elements between layers) of two caches of pages of 64 tokens
+PyObject* caches(PyObject*, PyObject* const* a, Py_ssize_t na) {
+    if (!args(na, 3)) return nullptr;
+    return guarded([&]() -> PyObject* {
+        const at::Tensor *k = tensor(a[0]), *v = k ? tensor(a[1]) : nullptr;
+        const long dev = PyLong_AsLong(a[2]);
+        if (!v || PyErr_Occurred()) return nullptr;
+        auto bad = [](const char* m) -> PyObject* {
+            PyErr_SetString(PyExc_ValueError, m);
+            return nullptr;
+        };
+        const bool bf16 = k->scalar_type() == at::kBFloat16;
+        if (!bf16 && k->scalar_type() != at::kFloat) return bad("k_cache must be float32 or bfloat16");
+        const int64_t d = k->dim();
+        if (v->scalar_type() != k->scalar_type() || v->sizes() != k->sizes() || (d != 4 && d != 5) || k->size(d - 2) != 64)
+            return bad("k_cache and v_cache must be alike, [pages, H_kv, 64, hd] or [layers, pages, H_kv, 64, hd]");
+        if (k->get_device() != dev || v->get_device() != dev) return bad("k_cache and v_cache must be on the other tensors' device");
+        const int64_t pages = k->size(d - 4), heads = k->size(d - 3), hd = k->size(d - 1), layer = pages * heads * 64 * hd;
+        for (const at::Tensor* t : {k, v}) {  // a layer is contiguous
+            int64_t want = 1;
+            for (int64_t i = d - 1; i >= d - 4; --i) {
+                if (t->size(i) != 1 && t->stride(i) != want) return bad("a layer of k_cache and v_cache must be contiguous");
+                want *= t->size(i);
+            }
+        }
+        const int64_t layers = d == 5 ? k->size(0) : 1;
+        if (layers < 1) return bad("k_cache and v_cache must hold a layer");
+        if (layers > 1 && k->stride(0) != v->stride(0)) return bad("k_cache and v_cache must have one stride between layers");
+        return Py_BuildValue("iLLLLL", bf16 ? 1 : 0, (long long)layers, (long long)pages, (long long)heads, (long long)hd,
+                             layers > 1 ? (long long)k->stride(0) : (long long)layer);
+    });
+}
+
 // written(t, ...): the tensors (or None) have been written to: their versions rise, so that a backward pass that saved one of
 // them says so
 PyObject* written(PyObject*, PyObject* const* a, Py_ssize_t na) {
@@ -120,6 +184,8 @@ PyObject* written(PyObject*, PyObject* const* a, Py_ssize_t na) {
 PyMethodDef methods[] = {{"flat", (PyCFunction)(void (*)(void))flat, METH_FASTCALL, nullptr},
                          {"mat", (PyCFunction)(void (*)(void))mat, METH_FASTCALL, nullptr},
                          {"rows3", (PyCFunction)(void (*)(void))rows3, METH_FASTCALL, nullptr},
+                         {"ints", (PyCFunction)(void (*)(void))ints, METH_FASTCALL, nullptr},
+                         {"caches", (PyCFunction)(void (*)(void))caches, METH_FASTCALL, nullptr},
                          {"written", (PyCFunction)(void (*)(void))written, METH_FASTCALL, nullptr},
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_tensor_args", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};

@@ -147,6 +147,37 @@ def _rows3(name, t, dtype, rows, heads, hd, dev):
     return ld if rows > 1 else heads * hd
 
 
+def _ints(dev, *named):
+    """Addresses of contiguous int32 tensors, each given as its name, itself and its number of elements."""
+    return tuple(_flat(named[i], named[i + 1], _I32T, named[i + 2], dev) for i in range(0, len(named), 3))
+
+
+def _caches(k, v, dev):
+    """(dtype code, layers, pages, heads, hd, elements between layers) of two caches [layers, pages, H_kv, 64, hd], or of one
+    layer's without the first dimension."""
+    dt = _DTYPES.get(k.dtype)
+    if dt is None:
+        _bad("k_cache must be float32 or bfloat16")
+    d = k.dim()
+    if v.dtype is not k.dtype or v.shape != k.shape or d not in (4, 5) or k.shape[-2] != PAGE_TOKENS:
+        _bad(f"k_cache and v_cache must be alike, [pages, H_kv, {PAGE_TOKENS}, hd] or [layers, pages, H_kv, {PAGE_TOKENS}, hd]")
+    if k.get_device() != dev or v.get_device() != dev:
+        _bad("k_cache and v_cache must be on the other tensors' device")
+    pages, heads, tokens, hd = k.shape[-4:]
+    for t in (k, v):
+        want = 1
+        for size, stride in zip(reversed(t.shape[-4:]), reversed(t.stride()[-4:])):
+            if size != 1 and stride != want:
+                _bad("a layer of k_cache and v_cache must be contiguous")
+            want *= size
+    layers = k.shape[0] if d == 5 else 1
+    if layers < 1:
+        _bad("k_cache and v_cache must hold a layer")
+    if layers > 1 and k.stride(0) != v.stride(0):
+        _bad("k_cache and v_cache must have one stride between layers")
+    return dt, layers, pages, heads, hd, k.stride(0) if layers > 1 else pages * heads * tokens * hd
+
+
 def _written(*tensors):
     """The tensors (or None) have been written to: their versions rise."""
     for t in tensors:
@@ -156,12 +187,13 @@ def _written(*tensors):
 
 _PYTHON_CHECKS = (_flat, _mat, _rows3)
 _PYTHON_WRITTEN = _written
+_PYTHON_GROUPS = (_ints, _caches)
 
 
 def _use_extension():
-    """The same three checks (and _written) from csrc/tensor_args.cpp, where it has been built (a small call's host side is
+    """The same checks (and _written) from csrc/tensor_args.cpp, where it has been built (a small call's host side is
     shorter by a third)."""
-    global _flat, _mat, _rows3, _written
+    global _flat, _mat, _rows3, _written, _ints, _caches
     path = _build_mod.tensor_args_path()
     if path is None or not os.path.exists(path):
         return
@@ -169,7 +201,7 @@ def _use_extension():
         spec = importlib.util.spec_from_loader("_tensor_args", importlib.machinery.ExtensionFileLoader("_tensor_args", path))
         m = importlib.util.module_from_spec(spec)
         spec.loader.exec_module(m)
-        _flat, _mat, _rows3, _written = m.flat, m.mat, m.rows3, m.written
+        _flat, _mat, _rows3, _written, _ints, _caches = m.flat, m.mat, m.rows3, m.written, m.ints, m.caches
     except (ImportError, AttributeError):  # (AttributeError: built from an older source)
         return
 

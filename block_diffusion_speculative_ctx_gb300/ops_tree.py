@@ -97,40 +97,11 @@ class KVRelease(NamedTuple):
     status: torch.Tensor
 
 
-def _int(name, t, n, dev):
-    return _ops._flat(name, t, _I32T, n, dev)
-
-
 def _batch(name, t, extra=0):
     n = t.numel() - extra
     if not 1 <= n <= OPS_MAX_BATCH:
         _bad(f"{name} must hold {1 + extra} to {OPS_MAX_BATCH + extra} entries")
     return n
-
-
-def _caches(k, v, dev):
-    """(dtype, layers, pages, heads, hd, elements between layers) of two caches [layers, pages, H_kv, 64, hd], or of one
-    layer's without the first dimension."""
-    dt = _DTYPES.get(k.dtype)
-    if dt is None:
-        _bad(f"k_cache must be float32 or bfloat16, not {k.dtype}")
-    shape = k.shape
-    if v.dtype is not k.dtype or v.shape != shape or len(shape) not in (4, 5) or shape[-2] != PAGE_TOKENS:
-        _bad(f"k_cache and v_cache must be alike, [pages, H_kv, {PAGE_TOKENS}, hd] or [layers, pages, H_kv, {PAGE_TOKENS}, hd]")
-    if k.get_device() != dev or v.get_device() != dev:
-        _bad(f"k_cache and v_cache must be on cuda:{dev}")
-    if len(shape) == 4:
-        if not (k.is_contiguous() and v.is_contiguous()):
-            _bad("k_cache and v_cache must be contiguous")
-        return dt, 1, shape[0], shape[1], shape[3], k.numel()
-    layer = shape[1] * shape[2] * PAGE_TOKENS * shape[4]
-    if shape[0] < 1 or not (k[0].is_contiguous() and v[0].is_contiguous()):
-        _bad("a layer of k_cache and v_cache must be contiguous")
-    if shape[0] == 1:
-        return dt, 1, shape[1], shape[2], shape[4], layer
-    if k.stride(0) != v.stride(0):
-        _bad("k_cache and v_cache must have one stride between layers")
-    return dt, shape[0], shape[1], shape[2], shape[4], k.stride(0)
 
 
 def tree_masks(parents, q_start, *, kv_lens=None, base_pos: int = 0, words: Optional[int] = None, masks=None, depth=None,
@@ -146,7 +117,6 @@ def tree_masks(parents, q_start, *, kv_lens=None, base_pos: int = 0, words: Opti
     1 (a parent not before its child), 2 (too many nodes), 4 (bad q_start)."""
     dev = _device(parents)
     rows, batch = parents.numel(), _batch("q_start", q_start, 1)
-    p_par, p_start = _int("parents", parents, rows, dev), _int("q_start", q_start, batch + 1, dev)
     if masks is None:
         if words is None:
             words = max(1, -(-min(rows, TREE_MAX_NODES) // 32))
@@ -156,19 +126,19 @@ def tree_masks(parents, q_start, *, kv_lens=None, base_pos: int = 0, words: Opti
     ld = max(_ops._mat("masks", masks, _I32T, rows, words, dev), words)
     if depth is None:
         depth = torch.zeros(rows, dtype=_I32T, device=parents.device)
-    p_kv = p_pos = 0
-    if kv_lens is not None:
-        p_kv = _int("kv_lens", kv_lens, batch, dev)
-        if row_pos is None:
-            row_pos = torch.zeros(rows, dtype=_I32T, device=parents.device)
-        p_pos = _int("row_pos", row_pos, rows, dev)
-    elif row_pos is not None:
-        _bad("row_pos needs kv_lens")
     if status is None:
         status = torch.empty(batch, dtype=_I32T, device=parents.device)
+    p_par, p_start, p_depth, p_status = _ops._ints(dev, "parents", parents, rows, "q_start", q_start, batch + 1, "depth", depth,
+                                                   rows, "status", status, batch)
+    p_kv = p_pos = 0
+    if kv_lens is not None:
+        if row_pos is None:
+            row_pos = torch.zeros(rows, dtype=_I32T, device=parents.device)
+        p_kv, p_pos = _ops._ints(dev, "kv_lens", kv_lens, batch, "row_pos", row_pos, rows)
+    elif row_pos is not None:
+        _bad("row_pos needs kv_lens")
     _call(load().dflash_tree_masks, _MASKS.pack,
-          (batch, rows, words, base_pos, ld, p_par, p_start, p_kv, masks.data_ptr(), _int("depth", depth, rows, dev), p_pos,
-           _int("status", status, batch, dev)), dev)
+          (batch, rows, words, base_pos, ld, p_par, p_start, p_kv, masks.data_ptr(), p_depth, p_pos, p_status), dev)
     _ops._written(masks, depth, row_pos, status)
     return TreeMasks(masks, depth, row_pos, status)
 
@@ -196,11 +166,11 @@ def tree_attention(q, k_cache, v_cache, table, kv_lens, q_start, masks, *, prefi
     n_kv = pages * hkv * PAGE_TOKENS * hd
     p_k, p_v = _ops._flat("k_cache", k_cache, dtype, n_kv, dev), _ops._flat("v_cache", v_cache, dtype, n_kv, dev)
     batch = _batch("kv_lens", kv_lens)
-    p_kv, p_start = _int("kv_lens", kv_lens, batch, dev), _int("q_start", q_start, batch + 1, dev)
+    p_kv, p_start = _ops._ints(dev, "kv_lens", kv_lens, batch, "q_start", q_start, batch + 1)
     p_pre = 0
     if prefix_pages is not None:
         n_pre = prefix_pages.numel()
-        p_pre = _int("prefix_pages", prefix_pages, n_pre, dev)
+        p_pre = _ops._flat("prefix_pages", prefix_pages, _I32T, n_pre, dev)
         if n_pre * PAGE_TOKENS < prefix_len:
             _bad(f"prefix_pages holds {n_pre} pages, too few for {prefix_len} tokens")
     elif prefix_len != 0:
@@ -234,7 +204,6 @@ def tree_accept(parents, tokens, posterior, q_start, *, width: Optional[int] = N
     ``tree_masks``."""
     dev = _device(parents)
     rows, batch = parents.numel(), _batch("q_start", q_start, 1)
-    p = [_int(n, t, rows, dev) for n, t in (("parents", parents), ("tokens", tokens), ("posterior", posterior))]
     if path is None:
         if width is None:
             _bad("width is needed when no path is given")
@@ -249,8 +218,10 @@ def tree_accept(parents, tokens, posterior, q_start, *, width: Optional[int] = N
     if status is None:
         status = torch.empty(batch, dtype=_I32T, device=parents.device)
     _call(load().dflash_tree_accept, _ACCEPT.pack,
-          (batch, rows, width, 0, *p, _int("q_start", q_start, batch + 1, dev), _int("path", path, batch * width, dev),
-           _int("accepted", accepted, batch, dev), _int("bonus", bonus, batch, dev), _int("status", status, batch, dev)), dev)
+          (batch, rows, width, 0,
+           *_ops._ints(dev, "parents", parents, rows, "tokens", tokens, rows, "posterior", posterior, rows, "q_start", q_start,
+                       batch + 1, "path", path, batch * width, "accepted", accepted, batch, "bonus", bonus, batch, "status",
+                       status, batch)), dev)
     _ops._written(path, accepted, bonus, status)
     return TreeAccept(path, accepted, bonus, status)
 
@@ -265,7 +236,7 @@ def kv_compact(k_cache, v_cache, table, kv_lens, q_start, path, accepted, *, kv_
     within the tree), 4 (bad q_start), 8 (bad length), 16 (bad page): nothing of the sequence has moved."""
     dev = _device(kv_lens, k_cache, v_cache)
     batch = _batch("kv_lens", kv_lens)
-    dt, layers, pages, hkv, hd, ld_layer = _caches(k_cache, v_cache, dev)
+    dt, layers, pages, hkv, hd, ld_layer = _ops._caches(k_cache, v_cache, dev)
     ld_table = _ops._mat("table", table, _I32T, batch, None, dev)
     if path.dim() != 2:
         _bad("path must be [batch, width]")
@@ -276,9 +247,9 @@ def kv_compact(k_cache, v_cache, table, kv_lens, q_start, path, accepted, *, kv_
         status = torch.empty(batch, dtype=_I32T, device=kv_lens.device)
     _call(load().dflash_kv_compact, _COMPACT.pack,
           (dt, batch, layers, pages, hkv, hd, width, table.shape[1], ld_layer, ld_table, k_cache.data_ptr(), v_cache.data_ptr(),
-           table.data_ptr(), _int("kv_lens", kv_lens, batch, dev), _int("q_start", q_start, batch + 1, dev),
-           _int("path", path, batch * width, dev), _int("accepted", accepted, batch, dev), _int("kv_out", kv_out, batch, dev),
-           _int("status", status, batch, dev)), dev)
+           table.data_ptr(),
+           *_ops._ints(dev, "kv_lens", kv_lens, batch, "q_start", q_start, batch + 1, "path", path, batch * width, "accepted",
+                       accepted, batch, "kv_out", kv_out, batch, "status", status, batch)), dev)
     _ops._written(k_cache, v_cache, kv_out, status)
     return KVCompact(kv_out, status)
 
@@ -295,7 +266,7 @@ def kv_fork(parents, kv_lens, table, free_pages, used, refs, k_cache, v_cache, *
     1 (pool short), 2 (table too narrow), 8 (a bad length or parent), and 16 (a bad page, which is left out)."""
     dev = _device(parents, k_cache, v_cache)
     n, batch = _batch("parents", parents), _batch("kv_lens", kv_lens)
-    dt, layers, pages, hkv, hd, ld_layer = _caches(k_cache, v_cache, dev)
+    dt, layers, pages, hkv, hd, ld_layer = _ops._caches(k_cache, v_cache, dev)
     ld_table, width = _ops._mat("table", table, _I32T, batch, None, dev), table.shape[1]
     if table_out is None:
         table_out = torch.empty((n, width), dtype=_I32T, device=table.device)
@@ -305,14 +276,15 @@ def kv_fork(parents, kv_lens, table, free_pages, used, refs, k_cache, v_cache, *
         used_out = torch.empty(1, dtype=_I32T, device=table.device)
     if status is None:
         status = torch.empty(1, dtype=_I32T, device=table.device)
-    p_status, n_free = _int("status", status, 1, dev), free_pages.numel()
+    n_free = free_pages.numel()
+    p_par, p_kv, p_free, p_used, p_refs, p_lens, p_uo, p_status = _ops._ints(
+        dev, "parents", parents, n, "kv_lens", kv_lens, batch, "free_pages", free_pages, n_free, "used", used, 1, "refs", refs,
+        pages, "lens_out", lens_out, n, "used_out", used_out, 1, "status", status, 1)
+    # (an empty list still has to be told from none at all)
     _call(load().dflash_kv_fork, _FORK.pack,
           (dt, batch, n, width, n_free, scratch_page, layers, pages, hkv, hd, ld_layer, ld_table,
            _ops._mat("table_out", table_out, _I32T, n, width, dev), k_cache.data_ptr(), v_cache.data_ptr(),
-           _int("parents", parents, n, dev), _int("kv_lens", kv_lens, batch, dev), table.data_ptr(),
-           _int("free_pages", free_pages, n_free, dev) or p_status, _int("used", used, 1, dev),
-           _int("refs", refs, pages, dev), table_out.data_ptr(), _int("lens_out", lens_out, n, dev),
-           _int("used_out", used_out, 1, dev), p_status), dev)
+           p_par, p_kv, table.data_ptr(), p_free or p_status, p_used, p_refs, table_out.data_ptr(), p_lens, p_uo, p_status), dev)
     _ops._written(refs, k_cache, v_cache, table_out, lens_out, used_out, status)
     return KVFork(table_out, lens_out, used_out, status)
 
@@ -332,10 +304,12 @@ def kv_release(seqs, kv_lens, table, free_pages, used, refs, *, used_out=None, s
         used_out = torch.empty(1, dtype=_I32T, device=table.device)
     if status is None:
         status = torch.empty(1, dtype=_I32T, device=table.device)
-    p_status, n_free, pages = _int("status", status, 1, dev), free_pages.numel(), refs.numel()
+    n_free, pages = free_pages.numel(), refs.numel()
+    p_seqs, p_kv, p_free, p_used, p_refs, p_uo, p_status = _ops._ints(
+        dev, "seqs", seqs, n, "kv_lens", kv_lens, batch, "free_pages", free_pages, n_free, "used", used, 1, "refs", refs, pages,
+        "used_out", used_out, 1, "status", status, 1)
     _call(load().dflash_kv_release, _RELEASE.pack,
-          (batch, n, table.shape[1], n_free, pages, 0, ld_table, _int("seqs", seqs, n, dev), _int("kv_lens", kv_lens, batch, dev),
-           table.data_ptr(), _int("free_pages", free_pages, n_free, dev) or p_status, _int("used", used, 1, dev),
-           _int("refs", refs, pages, dev), _int("used_out", used_out, 1, dev), p_status), dev)
+          (batch, n, table.shape[1], n_free, pages, 0, ld_table, p_seqs, p_kv, table.data_ptr(), p_free or p_status, p_used,
+           p_refs, p_uo, p_status), dev)
     _ops._written(free_pages, refs, used_out, status)
     return KVRelease(used_out, status)

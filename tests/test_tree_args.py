@@ -148,6 +148,32 @@ def test_the_bindings_refuse_cpu_tensors():
             f()
 
 
+def test_the_grouped_checks_in_python_and_in_the_extension_agree(lib):
+    """Addresses, layouts and refusals of the same tensors, wherever both forms are there."""
+    if ops._ints is ops._PYTHON_GROUPS[0]:
+        ops._use_extension()
+    if ops._ints is ops._PYTHON_GROUPS[0]:
+        pytest.skip("the extension has not been built")
+    i, x = torch.arange(24, dtype=torch.int32), torch.zeros(3, 4, 2, 64, 8)
+    calls = [(0, (d, "a", t, n, "b", i, 24)) for t in (i, i[:0], i[::2], i[3:4], i.view(4, 6).t(), i.long()) for n in (t.numel(), 24) for d in (-1, 0)]
+    calls += [(0, (-1,)), (0, (-1, "a", i[:5], 5)), (0, (-1, "a", i, 24, "b", i[1:], 24))]
+    wide = torch.zeros(3, 9, 2, 64, 8)
+    views = [x, x[0], x[:1], x[:0], x[1:], x[:, :2], wide[:, :4], wide[:, 2:6], x[:, :, :1], x[..., :4], x.bfloat16(), x.half(), x.transpose(0, 1),
+             x[:, :, :, :32], x[0, 0], x.expand(3, 4, 2, 64, 8)[:, :1]]
+    calls += [(1, (k, v, d)) for k in views for v in views for d in (-1, 0)]
+    refused = 0
+    for which, a in calls:
+        got = []
+        for f in (ops._PYTHON_GROUPS[which], (ops._ints, ops._caches)[which]):
+            try:
+                got.append(f(*a))
+            except ValueError:
+                got.append(ValueError)
+        assert got[0] == got[1], (which, [y.shape if hasattr(y, "shape") else y for y in a])
+        refused += got[0] is ValueError
+    assert 0 < refused < len(calls)
+
+
 # ---------------------------------------------------------------------------------------------- the oracles' pins
 def test_oracle_chain_is_the_causal_attention():
     rng = np.random.default_rng(0)
