@@ -4,6 +4,7 @@
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 
+#include <c10/core/GradMode.h>
 #include <torch/csrc/Dtype.h>
 #include <torch/csrc/autograd/python_variable.h>
 
@@ -103,25 +104,29 @@ PyObject* rows3(PyObject*, PyObject* const* a, Py_ssize_t na) {
     });
 }
 
-// ints(dev, name, t, n, name, t, n, ...): addresses of contiguous int32 tensors of n elements each
-PyObject* ints(PyObject*, PyObject* const* a, Py_ssize_t na) {
-    if (na < 1 || na % 3 != 1) return PyErr_Format(PyExc_TypeError, "a device, and a name, a tensor and a number each");
+// A tuple of the addresses of contiguous tensors of n elements each, from `each` arguments a tensor: its name, itself, its type
+// (int32 where each is three) and n.
+PyObject* addresses(PyObject* const* a, Py_ssize_t na, int each) {
+    if (na < 1 || na % each != 1) return PyErr_Format(PyExc_TypeError, "a device, and %d arguments for each tensor", each);
     return guarded([&]() -> PyObject* {
         const long dev = PyLong_AsLong(a[0]);
         if (PyErr_Occurred()) return nullptr;
-        PyObject* out = PyTuple_New(na / 3);
+        PyObject* out = PyTuple_New(na / each);
         if (!out) return nullptr;
-        for (Py_ssize_t i = 0; i < na / 3; ++i) {
-            PyObject *name = a[3 * i + 1], *o = a[3 * i + 2];
-            const at::Tensor* t = tensor(o);
-            const long long n = PyLong_AsLongLong(a[3 * i + 3]);
+        for (Py_ssize_t i = 0; i < na / each; ++i) {
+            PyObject* const* e = a + 1 + each * i;
+            const at::Tensor* t = tensor(e[1]);
+            const long long n = PyLong_AsLongLong(e[each - 1]);
             if (!t || PyErr_Occurred()) {
                 Py_DECREF(out);
                 return nullptr;
             }
-            if (t->scalar_type() != at::kInt || t->numel() != n || t->get_device() != dev || !t->is_contiguous()) {
+            if (!(each == 3 ? t->scalar_type() == at::kInt : of_type(*t, e[2])) || t->numel() != n || t->get_device() != dev ||
+                !t->is_contiguous()) {
                 Py_DECREF(out);
-                return refuse(name, PyUnicode_FromFormat("a contiguous torch.int32 tensor of %lld elements", n), dev, o);
+                return refuse(e[0], each == 3 ? PyUnicode_FromFormat("a contiguous torch.int32 tensor of %lld elements", n)
+                                              : PyUnicode_FromFormat("a contiguous %S tensor of %lld elements", e[2], n),
+                              dev, e[1]);
             }
             PyObject* address = PyLong_FromVoidPtr(t->data_ptr());
             if (!address) {
@@ -131,6 +136,23 @@ PyObject* ints(PyObject*, PyObject* const* a, Py_ssize_t na) {
             PyTuple_SET_ITEM(out, i, address);
         }
         return out;
+    });
+}
+// ints(dev, name, t, n, ...), flats(dev, name, t, dtype, n, ...)
+PyObject* ints(PyObject*, PyObject* const* a, Py_ssize_t na) { return addresses(a, na, 3); }
+PyObject* flats(PyObject*, PyObject* const* a, Py_ssize_t na) { return addresses(a, na, 4); }
+
+// free_of_grad(t, ...): whether none of the tensors (or None) would record a gradient
+PyObject* free_of_grad(PyObject*, PyObject* const* a, Py_ssize_t na) {
+    return guarded([&]() -> PyObject* {
+        if (c10::GradMode::is_enabled())
+            for (Py_ssize_t i = 0; i < na; ++i) {
+                if (a[i] == Py_None) continue;
+                const at::Tensor* t = tensor(a[i]);
+                if (!t) return nullptr;
+                if (t->requires_grad()) Py_RETURN_FALSE;
+            }
+        Py_RETURN_TRUE;
     });
 }
 
@@ -185,6 +207,8 @@ PyMethodDef methods[] = {{"flat", (PyCFunction)(void (*)(void))flat, METH_FASTCA
                          {"mat", (PyCFunction)(void (*)(void))mat, METH_FASTCALL, nullptr},
                          {"rows3", (PyCFunction)(void (*)(void))rows3, METH_FASTCALL, nullptr},
                          {"ints", (PyCFunction)(void (*)(void))ints, METH_FASTCALL, nullptr},
+                         {"flats", (PyCFunction)(void (*)(void))flats, METH_FASTCALL, nullptr},
+                         {"free_of_grad", (PyCFunction)(void (*)(void))free_of_grad, METH_FASTCALL, nullptr},
                          {"caches", (PyCFunction)(void (*)(void))caches, METH_FASTCALL, nullptr},
                          {"written", (PyCFunction)(void (*)(void))written, METH_FASTCALL, nullptr},
                          {nullptr, nullptr, 0, nullptr}};

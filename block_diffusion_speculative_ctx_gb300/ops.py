@@ -93,15 +93,18 @@ def _bad(msg):
     raise ValueError(msg)
 
 
+def _free_of_grad(*floats):
+    """Whether none of the tensors (or None) would record a gradient."""
+    return not torch.is_grad_enabled() or not any(t is not None and t.requires_grad for t in floats)
+
+
 def _device(first, *floats):
     """Index of the one CUDA device of the call; floating tensors that record a gradient are refused."""
     dev = first.get_device()
     if dev < 0:
         _bad("the operators run on CUDA tensors only")
-    if torch.is_grad_enabled():
-        for t in floats:
-            if t is not None and t.requires_grad:
-                _bad("a tensor requires a gradient, which these operators do not have")
+    if floats and not _free_of_grad(*floats):
+        _bad("a tensor requires a gradient, which these operators do not have")
     if _forward_ad._current_level >= 0:
         for t in floats:
             if t is not None and _forward_ad.unpack_dual(t).tangent is not None:
@@ -152,6 +155,11 @@ def _ints(dev, *named):
     return tuple(_flat(named[i], named[i + 1], _I32T, named[i + 2], dev) for i in range(0, len(named), 3))
 
 
+def _flats(dev, *named):
+    """Addresses of contiguous tensors, each given as its name, itself, its type and its number of elements."""
+    return tuple(_flat(*named[i:i + 4], dev) for i in range(0, len(named), 4))
+
+
 def _caches(k, v, dev):
     """(dtype code, layers, pages, heads, hd, elements between layers) of two caches [layers, pages, H_kv, 64, hd], or of one
     layer's without the first dimension."""
@@ -187,13 +195,13 @@ def _written(*tensors):
 
 _PYTHON_CHECKS = (_flat, _mat, _rows3)
 _PYTHON_WRITTEN = _written
-_PYTHON_GROUPS = (_ints, _caches)
+_PYTHON_GROUPS = (_ints, _caches, _flats, _free_of_grad)
 
 
 def _use_extension():
     """The same checks (and _written) from csrc/tensor_args.cpp, where it has been built (a small call's host side is
     shorter by a third)."""
-    global _flat, _mat, _rows3, _written, _ints, _caches
+    global _flat, _mat, _rows3, _written, _ints, _caches, _flats, _free_of_grad
     path = _build_mod.tensor_args_path()
     if path is None or not os.path.exists(path):
         return
@@ -201,7 +209,8 @@ def _use_extension():
         spec = importlib.util.spec_from_loader("_tensor_args", importlib.machinery.ExtensionFileLoader("_tensor_args", path))
         m = importlib.util.module_from_spec(spec)
         spec.loader.exec_module(m)
-        _flat, _mat, _rows3, _written, _ints, _caches = m.flat, m.mat, m.rows3, m.written, m.ints, m.caches
+        _flat, _mat, _rows3, _written, _ints, _caches, _flats, _free_of_grad = (
+            m.flat, m.mat, m.rows3, m.written, m.ints, m.caches, m.flats, m.free_of_grad)
     except (ImportError, AttributeError):  # (AttributeError: built from an older source)
         return
 

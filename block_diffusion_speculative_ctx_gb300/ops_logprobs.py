@@ -54,14 +54,14 @@ def _logits(name, t, dev):
     return dt, rows, vocab, max(_ops._mat(name, t, t.dtype, rows, vocab, dev), vocab)
 
 
-def _tokens(t, rows, dev):
-    """Tokens a row, and the address, of tokens [rows] or [rows, n]."""
+def _tokens(t, rows):
+    """Tokens a row of tokens [rows] or [rows, n]."""
     if t.dim() not in (1, 2) or t.shape[0] != rows:
         _bad(f"tokens must be [{rows}] or [{rows}, n]")
     n = 1 if t.dim() == 1 else t.shape[1]
     if n > LOGPROBS_MAX_TOKENS:
         _bad(f"at most {LOGPROBS_MAX_TOKENS} tokens a row")
-    return n, _ops._flat("tokens", t, _I32T, rows * n, dev)
+    return n
 
 
 def _inverse(temperature):
@@ -70,13 +70,13 @@ def _inverse(temperature):
     return 1.0 / temperature
 
 
-def _alike(name, t, like, dtype, dev):
-    """An output of the shape `like` (allocated when None), and its address."""
+def _alike(name, t, like, dtype, device):
+    """An output of the shape `like`, allocated when None."""
     if t is None:
-        t = torch.empty(like, dtype=dtype, device=f"cuda:{dev}")
-    elif t.shape != like:
+        return torch.empty(like, dtype=dtype, device=device)
+    if t.shape != like:
         _bad(f"{name} must be {list(like)}, not {list(t.shape)}")
-    return t, _ops._flat(name, t, dtype, t.numel(), dev)
+    return t
 
 
 def token_logprobs(logits, tokens, *, top: int = 0, temperature: float = 1.0, logprobs=None, ranks=None, entropy=None,
@@ -90,22 +90,23 @@ def token_logprobs(logits, tokens, *, top: int = 0, temperature: float = 1.0, lo
     -1 and -inf where fewer tokens are above -inf).  All fp32; missing outputs are allocated."""
     dev = _device(logits, logits, logprobs, entropy, lse, top_logprobs)
     dt, rows, vocab, ld = _logits("logits", logits, dev)
-    n, p_tok = _tokens(tokens, rows, dev)
+    n = _tokens(tokens, rows)
     if not 0 <= top <= LOGPROBS_MAX_TOP:
         _bad(f"top must be in [0, {LOGPROBS_MAX_TOP}]")
-    logprobs, p_lp = _alike("logprobs", logprobs, tokens.shape, _F32T, dev)
-    ranks, p_rank = _alike("ranks", ranks, tokens.shape, _I32T, dev)
-    entropy, p_ent = _alike("entropy", entropy, (rows,), _F32T, dev)
-    lse, p_lse = _alike("lse", lse, (rows,), _F32T, dev)
-    p_ids = p_top = 0
+    like, device = tokens.shape, logits.device
+    logprobs, ranks = _alike("logprobs", logprobs, like, _F32T, device), _alike("ranks", ranks, like, _I32T, device)
+    entropy, lse = _alike("entropy", entropy, (rows,), _F32T, device), _alike("lse", lse, (rows,), _F32T, device)
+    p = _ops._flats(dev, "tokens", tokens, _I32T, rows * n, "logprobs", logprobs, _F32T, rows * n, "ranks", ranks, _I32T,
+                    rows * n, "entropy", entropy, _F32T, rows, "lse", lse, _F32T, rows)
+    p_top = (0, 0)
     if top:
-        top_ids, p_ids = _alike("top_ids", top_ids, (rows, top), _I32T, dev)
-        top_logprobs, p_top = _alike("top_logprobs", top_logprobs, (rows, top), _F32T, dev)
+        top_ids = _alike("top_ids", top_ids, (rows, top), _I32T, device)
+        top_logprobs = _alike("top_logprobs", top_logprobs, (rows, top), _F32T, device)
+        p_top = _ops._flats(dev, "top_ids", top_ids, _I32T, rows * top, "top_logprobs", top_logprobs, _F32T, rows * top)
     elif top_ids is not None or top_logprobs is not None:
         _bad("top_ids and top_logprobs need top")
     _call(load().dflash_token_logprobs, _LOGPROBS.pack,
-          (dt, rows, vocab, n, top, _inverse(temperature), ld, logits.data_ptr(), p_tok, p_lp, p_rank, p_ent, p_lse, p_ids,
-           p_top), dev)
+          (dt, rows, vocab, n, top, _inverse(temperature), ld, logits.data_ptr(), *p, *p_top), dev)
     _ops._written(logprobs, ranks, entropy, lse, top_ids, top_logprobs)
     return TokenLogprobs(logprobs, ranks, entropy, lse, top_ids, top_logprobs)
 
@@ -120,16 +121,16 @@ def token_logprobs_grad(logits, tokens, lse, grad_logprobs, *, entropy=None, gra
     For alternatives' log probabilities, name their ids among the tokens."""
     dev = _device(logits, logits, lse, grad_logprobs, entropy, grad_entropy, out)
     dt, rows, vocab, ld = _logits("logits", logits, dev)
-    n, p_tok = _tokens(tokens, rows, dev)
-    if grad_logprobs is None:
-        _bad("grad_logprobs is needed")
-    p_g = _alike("grad_logprobs", grad_logprobs, tokens.shape, _F32T, dev)[1]
-    p_lse = _ops._flat("lse", lse, _F32T, rows, dev)
+    n = _tokens(tokens, rows)
+    if grad_logprobs is None or grad_logprobs.shape != tokens.shape:
+        _bad("grad_logprobs must have the shape of tokens")
+    p_tok, p_lse, p_g = _ops._flats(dev, "tokens", tokens, _I32T, rows * n, "lse", lse, _F32T, rows, "grad_logprobs",
+                                    grad_logprobs, _F32T, rows * n)
     p_ent = p_h = 0
     if grad_entropy is not None:
         if entropy is None:
             _bad("grad_entropy needs entropy")
-        p_ent, p_h = _ops._flat("entropy", entropy, _F32T, rows, dev), _ops._flat("grad_entropy", grad_entropy, _F32T, rows, dev)
+        p_ent, p_h = _ops._flats(dev, "entropy", entropy, _F32T, rows, "grad_entropy", grad_entropy, _F32T, rows)
     if out is None:
         out = torch.empty((rows, vocab), dtype=logits.dtype, device=logits.device)
     ld_out = max(_ops._mat("out", out, logits.dtype, rows, vocab, dev), vocab)

@@ -20,7 +20,7 @@ import torch
 
 from . import load
 from . import ops as _ops
-from .ops import (_DTYPES, _F32T, _I32, _I32T, _I64, _P, OPS_MAX_BATCH, PAGE_TOKENS, _attend, _bad, _call, _device,
+from .ops import (_F32T, _I32, _I32T, _I64, _P, OPS_MAX_BATCH, PAGE_TOKENS, _attend, _bad, _call, _device,
                   dflash_shared_prefix_args)
 
 TREE_MAX_NODES = 1024
@@ -151,22 +151,21 @@ def tree_attention(q, k_cache, v_cache, table, kv_lens, q_start, masks, *, prefi
     q_start), but of the sequence's own kv_lens keys row r sees the committed ones, those before its m last,
     and of these m the nodes whose bit is set in masks[r] (int32 [rows, words], as ``tree_masks`` makes them, or
     any others).  A row that sees nothing gives 0 and an lse of -inf.  Returns (out, lse)."""
+    dev = _device(q, q, k_cache, v_cache, out, lse)
     if q.dim() != 3 or k_cache.dim() != 4:
         _bad("q must be [rows, H, hd] and the caches [pages, H_kv, 64, hd]")
-    dev = _device(q, q, k_cache, v_cache, out, lse)
     rows, h, hd = q.shape
-    kv_shape = k_cache.shape
-    pages, hkv, page_tokens, kv_hd = kv_shape
     dtype = q.dtype
-    dt = _DTYPES.get(dtype)
-    if dt is None:
-        _bad(f"q must be float32 or bfloat16, not {dtype}")
-    if page_tokens != PAGE_TOKENS or kv_hd != hd or v_cache.shape != kv_shape:
-        _bad(f"k_cache and v_cache must be [pages, H_kv, {PAGE_TOKENS}, {hd}]")
-    n_kv = pages * hkv * PAGE_TOKENS * hd
-    p_k, p_v = _ops._flat("k_cache", k_cache, dtype, n_kv, dev), _ops._flat("v_cache", v_cache, dtype, n_kv, dev)
+    dt, _, pages, hkv, kv_hd, _ = _ops._caches(k_cache, v_cache, dev)
+    if k_cache.dtype is not dtype or kv_hd != hd:
+        _bad(f"k_cache and v_cache must be {dtype} [pages, H_kv, {PAGE_TOKENS}, {hd}]")
     batch = _batch("kv_lens", kv_lens)
-    p_kv, p_start = _ops._ints(dev, "kv_lens", kv_lens, batch, "q_start", q_start, batch + 1)
+    if out is None:
+        out = torch.zeros((rows, h, hd), dtype=dtype, device=q.device)
+    if lse is None:
+        lse = torch.zeros((rows, h), dtype=_F32T, device=q.device)
+    p_kv, p_start, p_lse = _ops._flats(dev, "kv_lens", kv_lens, _I32T, batch, "q_start", q_start, _I32T, batch + 1,
+                                       "lse", lse, _F32T, rows * h)
     p_pre = 0
     if prefix_pages is not None:
         n_pre = prefix_pages.numel()
@@ -179,14 +178,10 @@ def tree_attention(q, k_cache, v_cache, table, kv_lens, q_start, masks, *, prefi
     ld_mask = _ops._mat("masks", masks, _I32T, rows, None, dev)
     words = masks.shape[1]
     ld_q = _ops._rows3("q", q, dtype, rows, h, hd, dev)
-    if out is None:
-        out = torch.zeros((rows, h, hd), dtype=dtype, device=q.device)
     ld_out = _ops._rows3("out", out, dtype, rows, h, hd, dev)
-    if lse is None:
-        lse = torch.zeros((rows, h), dtype=_F32T, device=q.device)
     args = (dt, h, hkv, hd, batch, rows, pages, prefix_len, table.shape[1], 0, hd ** -0.5 if scale is None else scale,
-            1 if weight_pairs else 0, ld_q, ld_out, ld_table, q.data_ptr(), p_k, p_v, p_pre, table.data_ptr(), p_kv, p_start,
-            out.data_ptr(), _ops._flat("lse", lse, _F32T, rows * h, dev))
+            1 if weight_pairs else 0, ld_q, ld_out, ld_table, q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), p_pre,
+            table.data_ptr(), p_kv, p_start, out.data_ptr(), p_lse)
     _attend(load().dflash_tree_attention, _TREE.pack, args, (masks.data_ptr(), max(ld_mask, words), words, 0),
             (dt, h, hkv, hd, batch, rows), workspace, dev, q.device)
     _ops._written(out, lse)

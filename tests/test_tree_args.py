@@ -161,15 +161,19 @@ def test_the_grouped_checks_in_python_and_in_the_extension_agree(lib):
     views = [x, x[0], x[:1], x[:0], x[1:], x[:, :2], wide[:, :4], wide[:, 2:6], x[:, :, :1], x[..., :4], x.bfloat16(), x.half(), x.transpose(0, 1),
              x[:, :, :, :32], x[0, 0], x.expand(3, 4, 2, 64, 8)[:, :1]]
     calls += [(1, (k, v, d)) for k in views for v in views for d in (-1, 0)]
+    calls += [(2, (d, "a", t, dt, n, "b", x, torch.float32, x.numel())) for t in (i, i[::2], x, x[:, :1], x.bfloat16())
+              for dt in (torch.int32, torch.float32) for n in (t.numel(), 7) for d in (-1, 0)]
+    leaf = torch.zeros(3, requires_grad=True)
+    calls += [(3, a) for a in ((), (None, x), (x, leaf, None), (leaf.detach(),), (leaf,))]
     refused = 0
     for which, a in calls:
         got = []
-        for f in (ops._PYTHON_GROUPS[which], (ops._ints, ops._caches)[which]):
+        for f in (ops._PYTHON_GROUPS[which], (ops._ints, ops._caches, ops._flats, ops._free_of_grad)[which]):
             try:
                 got.append(f(*a))
             except ValueError:
                 got.append(ValueError)
-        assert got[0] == got[1], (which, [y.shape if hasattr(y, "shape") else y for y in a])
+        assert got[0] == got[1] and type(got[0]) is type(got[1]), (which, [y.shape if hasattr(y, "shape") else y for y in a])
         refused += got[0] is ValueError
     assert 0 < refused < len(calls)
 
