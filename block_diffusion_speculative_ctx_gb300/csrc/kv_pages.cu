@@ -12,7 +12,8 @@
 //   2  its count falls by one for each mention: a page without a holder ends at -1
 //      (below: it was returned too often, and the counts go back);
 //   3  of a page's mentions the first takes it: an atomic minimum over the
-//      mentions' numbers, kept in the count itself as INT_MIN + number;
+//      mentions' numbers, kept in the count itself as INT_MIN + number (left out
+//      where no page named had a second holder);
 //   4  each warp counts the pages that its mentions took; with the counts of the
 //      warps before it, it knows their places in the free list.
 // Mentions are numbered (place in seqs, table entry) and a warp owns consecutive
@@ -277,15 +278,16 @@ __global__ void __launch_bounds__(NR) kv_release_kernel(dflash_kv_release_args a
         if (n_cta > 1) tc::cluster_sync();
         else __syncthreads();
     };
-    // the cluster's barrier; true when some CTA called it with a flag
+    // the cluster's barrier, and the flags that some thread called it with
     int round = 0;
-    auto any = [&](bool x) {
-        if (__syncthreads_or(x) && tid == 0) flag_s[round & 1] = 1;
+    auto any = [&](int x) {
+        x = __reduce_or_sync(0xffffffffu, x);
+        if (lane == 0 && x) atomicOr(&flag_s[round & 1], x);
         meet();
         int on = 0;
         for (int r = 0; r < n_cta; ++r) on |= n_cta > 1 ? ld_peer_int(&flag_s[round & 1], r) : flag_s[round & 1];
         ++round;
-        return on != 0;
+        return on;
     };
 
     int freed = 0;
@@ -295,22 +297,33 @@ __global__ void __launch_bounds__(NR) kv_release_kernel(dflash_kv_release_args a
         if (any(out)) status = BAD_PAGE;
     }
     if (status == 0) {
+        enum { OVER = 1, SHARED = 2 };  // a count below what its page had; a page that several mentions free
+        int seen = 0;
         mentions([&](int page, int, bool live) {
-            if (live) atomicSub(&a.refs[page], 1);
+            if (!live) return;
+            const int before = atomicSub(&a.refs[page], 1);
+            if (before < 0) seen |= OVER;
+            if (before > 0) seen |= SHARED;  // (it may yet be freed by others)
         });
-        meet();
-        bool over = false;
-        mentions([&](int page, int, bool live) { over |= live && ld_count(&a.refs[page]) < -1; });
-        if (any(over)) {
+        seen = any(seen);
+        if (seen & OVER) {
             status = BAD_COUNT;
         } else {
-            mentions([&](int page, int number, bool live) {
-                if (live && ld_count(&a.refs[page]) < 0) atomicMin(&a.refs[page], INT32_MIN + number);
-            });
-            meet();
+            // which of a page's mentions takes it (a page that had no other holder has one)
+            if (seen & SHARED) {
+                mentions([&](int page, int number, bool live) {
+                    if (live && ld_count(&a.refs[page]) < 0) atomicMin(&a.refs[page], INT32_MIN + number);
+                });
+                meet();
+            }
+            auto takes = [&](int page, int number, bool live) {
+                if (!live) return false;
+                const int c = ld_count(&a.refs[page]);
+                return seen & SHARED ? c == INT32_MIN + number : c < 0;
+            };
             int mine_taken = 0;
             mentions([&](int page, int number, bool live) {
-                mine_taken += __popc(__ballot_sync(0xffffffffu, live && ld_count(&a.refs[page]) == INT32_MIN + number));
+                mine_taken += __popc(__ballot_sync(0xffffffffu, takes(page, number, live)));
             });
             if (lane == 0) counts[warp] = mine_taken;
             meet();
@@ -325,9 +338,9 @@ __global__ void __launch_bounds__(NR) kv_release_kernel(dflash_kv_release_args a
             if (freed > used) status = SHORT_POOL;
             int at = used - freed + ahead;
             mentions([&](int page, int number, bool live) {
-                const bool takes = live && ld_count(&a.refs[page]) == INT32_MIN + number;
-                const uint32_t took = __ballot_sync(0xffffffffu, takes);
-                if (takes) {
+                const bool mine = takes(page, number, live);
+                const uint32_t took = __ballot_sync(0xffffffffu, mine);
+                if (mine) {
                     if (status == 0) a.free_pages[at + __popc(took & ((1u << lane) - 1u))] = page;
                     atomicExch(&a.refs[page], status == 0 ? 0 : -1);
                 }

@@ -357,7 +357,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) logprobs_kernel(dflash_logprobs
     const float c = a.inv_temperature * LOG2E;
     const uint64_t c2 = pack2(c, c);
     float m = -INFINITY, l = 0.f, t = 0.f;
-    int my_id = -1;  // lane's token and its logit
+    int my_id = -1, my_ahead = 0;  // lane's token, the warp's elements ahead of it, and its logit
     float my_xt = 0.f;
     float tau_v = -INFINITY;  // candidates are as large (-inf: not known yet)
     int refresh = 2;
@@ -444,14 +444,16 @@ __global__ void __launch_bounds__(NT, 1024 / NT) logprobs_kernel(dflash_logprobs
 
         // ---- ranks: of the ids behind the token's those of a larger logit count, of the ids before it also those of the same
         if (a.ranks) {
-            const int first = sl.first_id(it), end = it == sl.full ? 0 : first + NT * E;
             if (it == 0 && lane < a.n) {
                 my_id = S.id[lane];
                 my_xt = S.xt[lane];
             }
-            const bool before = my_id >= end && end > 0;  // lane's token lies behind the tile
+            // (the extra tile of single tokens has ids on both sides of any token)
+            const bool single = it == sl.full;
+            const int first = sl.first_id(it);
+            const bool before = !single && my_id >= first + NT * E;  // lane's token lies behind the tile
             const float my_least = before ? my_xt : next_above<T>(my_xt);
-            // tokens q .. q + Q - 1: a warp's counts to shared memory
+            // tokens q .. q + Q - 1: the warp's counts to their lanes
             auto count = [&](int q, auto Qc) {
                 constexpr int Q = decltype(Qc)::value;
                 uint32_t n[(Q + 1) / 2];  // two tokens' counts each
@@ -487,12 +489,9 @@ __global__ void __launch_bounds__(NT, 1024 / NT) logprobs_kernel(dflash_logprobs
                 }
 #pragma unroll
                 for (int i = 0; i < (Q + 1) / 2; ++i) n[i] = __reduce_add_sync(0xffffffffu, n[i]);
-                uint32_t v = n[0];
 #pragma unroll
-                for (int i = 1; i < (Q + 1) / 2; ++i)
-                    if (lane / 2 == i) v = n[i];
-                v = v >> 16 * (lane & 1) & 0xFFFFu;
-                if (lane < Q && v) atomicAdd(&S.part.ahead[q + lane], (int)v);
+                for (int i = 0; i < Q; ++i)
+                    if (lane == q + i) my_ahead += (int)(n[i / 2] >> 16 * (i & 1) & 0xFFFFu);
             };
             int q = 0;
 #pragma unroll 1
@@ -501,7 +500,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) logprobs_kernel(dflash_logprobs
             for (; q < a.n; ++q) count(q, Int<1>());
             // the tile that holds a token has ids on both sides of it: those before it of the same logit; and elements that are
             // none, which are -inf, have been counted as large as a token at -inf behind them
-            const bool here = my_id >= 0 && (it == sl.full || (my_id >= first && my_id < end)),
+            const bool here = single ? my_id >= 0 : (unsigned)(my_id - first) < (unsigned)(NT * E),
                        extra = before && it >= sl.whole && my_xt == -INFINITY;
             for (uint32_t w = __ballot_sync(0xffffffffu, here || extra); w; w &= w - 1) {
                 const int i = __ffs(w) - 1, at = __shfl_sync(0xffffffffu, my_id, i);
@@ -509,16 +508,16 @@ __global__ void __launch_bounds__(NT, 1024 / NT) logprobs_kernel(dflash_logprobs
                 int n = 0;
 #pragma unroll
                 for (int j = 0; j < NV; ++j) {
-                    const int id = it < sl.full && sl.v0 + (it * NV + j) * NT + tid >= sl.v1 ? NOWHERE : sl.id(it, j * G);
-                    if (at >= end && end > 0) {
+                    const int id = !single && sl.v0 + (it * NV + j) * NT + tid >= sl.v1 ? NOWHERE : sl.id(it, j * G);
+                    if (!single && at >= first + NT * E) {
                         if (id == NOWHERE) n -= G;
                     } else {
 #pragma unroll
-                        for (int e = 0; e < G; ++e) n += x[j * G + e] == xt && id + e < at && (e == 0 || it < sl.full);
+                        for (int e = 0; e < G; ++e) n += x[j * G + e] == xt && id + e < at && (e == 0 || !single);
                     }
                 }
                 n = __reduce_add_sync(0xffffffffu, n);
-                if (lane == 0 && n) atomicAdd(&S.part.ahead[i], n);
+                if (lane == i) my_ahead += n;
             }
         }
 
@@ -551,6 +550,8 @@ __global__ void __launch_bounds__(NT, 1024 / NT) logprobs_kernel(dflash_logprobs
             }
         }
     }
+
+    if (a.ranks && my_ahead) atomicAdd(&S.part.ahead[lane], my_ahead);
 
     // ---- the CTA's results (the list's logits come while the warps join their sums)
     int n = 0;
