@@ -144,25 +144,18 @@ __global__ void __launch_bounds__(NT_COPY) fork_copy_kernel(dflash_kv_fork_args 
     const int run = tail * vecs, page = 64 * vecs;  // vectors of a head that are copied, and that it has in a page
     const uint4* src = cache + (long long)from * a.n_kv_heads * page;
     uint4* dst = cache + (long long)to * a.n_kv_heads * page;
-    const int all = run * a.n_kv_heads;
-    int h = tid / run, in_run = tid - h * run;
-    for (int i0 = tid; i0 < all; i0 += DEEP * NT_COPY) {
+    // a warp takes DEEP vectors a lane of one head's run at a time
+    constexpr int PIECE = 32 * DEEP;
+    const int lane = tid & 31, pieces = (run + PIECE - 1) / PIECE;
+    for (int u = tid >> 5; u < pieces * a.n_kv_heads; u += NT_COPY / 32) {
+        const int h = u / pieces, i0 = (u - h * pieces) * PIECE + lane, at = h * page + i0, left = run - i0;
         uint4 x[DEEP];
-        int at[DEEP];
-#pragma unroll
-        for (int i = 0; i < DEEP; ++i) {
-            at[i] = h * page + in_run;
-            if (i0 + i * NT_COPY < all) x[i] = src[at[i]];
-            in_run += NT_COPY;
-            if (in_run >= run) {
-                const int q = in_run / run;
-                h += q;
-                in_run -= q * run;
-            }
-        }
 #pragma unroll
         for (int i = 0; i < DEEP; ++i)
-            if (i0 + i * NT_COPY < all) dst[at[i]] = x[i];
+            if (32 * i < left) x[i] = src[at + 32 * i];
+#pragma unroll
+        for (int i = 0; i < DEEP; ++i)
+            if (32 * i < left) dst[at + 32 * i] = x[i];
     }
 }
 
@@ -232,12 +225,9 @@ __global__ void __launch_bounds__(NR) kv_release_kernel(dflash_kv_release_args a
     if (lane == 31) wsum[warp] = inc;
     int status = __syncthreads_or(bad & BAD_LENGTH) ? BAD_LENGTH : 0;
     status |= __syncthreads_or(bad & BAD_WIDTH) ? BAD_WIDTH : 0;
-    int before = 0, total = 0;
-#pragma unroll 1
-    for (int w = 0; w < WARPS; ++w) {
-        if (w == warp) before = total;
-        total += wsum[w];
-    }
+    const int sums = wsum[lane];  // (a lane a warp)
+    const int total = __reduce_add_sync(0xffffffffu, sums);
+    int before = __reduce_add_sync(0xffffffffu, lane < warp ? sums : 0);
     before += inc - both;
     if (2 * tid < a.n) units_s[2 * tid] = before;
     if (2 * tid + 1 < a.n) units_s[2 * tid + 1] = before + mine[0];
@@ -248,17 +238,18 @@ __global__ void __launch_bounds__(NR) kv_release_kernel(dflash_kv_release_args a
     // sequence's last page are not live
     const int warps = n_cta * WARPS, share = (total + warps - 1) / warps;
     const int u0 = min(total, (rank * WARPS + warp) * share), u1 = min(total, u0 + share);
+    int k0 = 0;  // the first unit's sequence: units_s[k0] <= u0 < units_s[k0 + 1]
+    if (u0 < u1) {
+        int hi = a.n;
+        while (hi - k0 > 1) {
+            const int mid = (k0 + hi) >> 1;
+            if (units_s[mid] <= u0) k0 = mid;
+            else hi = mid;
+        }
+    }
     auto mentions = [&](auto&& f) {
-        int k = 0;
+        int k = k0;
         for (int u = u0; u < u1; ++u) {
-            if (u == u0) {
-                int hi = a.n;  // units_s[k] <= u < units_s[hi]
-                while (hi - k > 1) {
-                    const int mid = (k + hi) >> 1;
-                    if (units_s[mid] <= u) k = mid;
-                    else hi = mid;
-                }
-            }
             while (units_s[k + 1] <= u) ++k;
             const int* row = a.table + (long long)seq_s[k] * a.ld_table;
             const int j0 = (u - units_s[k]) * UNIT;
