@@ -28,6 +28,7 @@ namespace dfl {
 namespace {
 
 constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
+constexpr float MIN_INVERSE = 1.f / (1 << 20), MAX_INVERSE = 1 << 20;  // of a temperature
 constexpr int MAXT = DFLASH_LOGPROBS_MAX_TOKENS, MAXK = DFLASH_LOGPROBS_MAX_TOP;
 
 __device__ __forceinline__ float ex2(float x) {
@@ -812,8 +813,8 @@ extern "C" dflash_status dflash_token_logprobs(const dflash_logprobs_args* p, vo
     if (a.vocab < 1 || a.vocab > (1 << 30)) return fail("token_logprobs: vocab outside [1, 2^30]");
     if (a.n < 0 || a.n > MAXT) return fail("token_logprobs: n outside [0, 32]");
     if (a.k < 0 || a.k > MAXK) return fail("token_logprobs: k outside [0, 32]");
-    if (!(a.inv_temperature > 0.f) || a.inv_temperature > 3e38f)
-        return fail("token_logprobs: inv_temperature must be positive and finite");
+    if (!(a.inv_temperature >= MIN_INVERSE && a.inv_temperature <= MAX_INVERSE))
+        return fail("token_logprobs: inv_temperature outside [2^-20, 2^20]");
     if ((a.rows > 0 && !a.logits) || (a.rows > 0 && a.n > 0 && !a.tokens)) return fail("token_logprobs: NULL argument");
     if ((uintptr_t)a.logits % (a.dtype == DFLASH_DTYPE_BF16 ? 2 : 4)) return fail("token_logprobs: logits is not aligned to its type");
     if (a.ld_logits < a.vocab) return fail("token_logprobs: the row stride is smaller than vocab");
@@ -832,8 +833,8 @@ extern "C" dflash_status dflash_token_logprobs_grad(const dflash_logprobs_grad_a
     if (a.rows < 0 || a.rows > (1 << 20)) return fail("token_logprobs_grad: rows outside [0, 2^20]");
     if (a.vocab < 1 || a.vocab > (1 << 30)) return fail("token_logprobs_grad: vocab outside [1, 2^30]");
     if (a.n < 0 || a.n > MAXT) return fail("token_logprobs_grad: n outside [0, 32]");
-    if (!(a.inv_temperature > 0.f) || a.inv_temperature > 3e38f)
-        return fail("token_logprobs_grad: inv_temperature must be positive and finite");
+    if (!(a.inv_temperature >= MIN_INVERSE && a.inv_temperature <= MAX_INVERSE))
+        return fail("token_logprobs_grad: inv_temperature outside [2^-20, 2^20]");
     if (a.reserved != 0) return fail("token_logprobs_grad: reserved must be 0");
     if (a.rows > 0 && (!a.logits || !a.out || !a.lse || (a.n > 0 && (!a.tokens || !a.grad_logprobs)) || (a.grad_entropy && !a.entropy)))
         return fail("token_logprobs_grad: NULL argument");

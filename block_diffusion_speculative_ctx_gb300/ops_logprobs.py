@@ -65,8 +65,8 @@ def _tokens(t, rows):
 
 
 def _inverse(temperature):
-    if not temperature > 0 or temperature == float("inf"):
-        _bad("temperature must be positive and finite")
+    if not 2.0 ** -20 <= temperature <= 2.0 ** 20:
+        _bad("temperature must be in [2^-20, 2^20]")
     return 1.0 / temperature
 
 

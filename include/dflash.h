@@ -653,7 +653,9 @@ dflash_status dflash_process_logits(const dflash_logits_args* args, void* cuda_s
  * a tree in drafting order: node 0 is the root (the anchor, committed whatever
  * the target says), a node's parent comes before it.  kv_lens[s] counts the
  * sequence's own keys, those of the m nodes, its last, among them: node i is
- * own key kv_lens[s] - m + i.  At most DFLASH_TREE_MAX_NODES nodes a tree. */
+ * own key kv_lens[s] - m + i.  At most DFLASH_TREE_MAX_NODES nodes a tree.
+ * Outputs of these calls, of the page calls and of the log probabilities
+ * overlap neither one another nor an input, but where a call says so. */
 enum { DFLASH_TREE_MAX_NODES = 1024 };
 
 /* Masks, depths and positions of trees from their nodes' parents.
@@ -873,7 +875,7 @@ typedef struct {
     int32_t vocab;
     int32_t n;                 /* tokens a row, 0 .. DFLASH_LOGPROBS_MAX_TOKENS */
     int32_t k;                 /* alternatives a row, 0 .. DFLASH_LOGPROBS_MAX_TOP */
-    float inv_temperature;     /* > 0, finite */
+    float inv_temperature;     /* 2^-20 .. 2^20 */
     int64_t ld_logits;
     const void* logits;        /* [rows][vocab] */
     const int32_t* tokens;     /* [rows][n]; NULL when n is 0 */

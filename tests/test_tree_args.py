@@ -107,10 +107,11 @@ REFUSED = {
                    + [{n: None} for n in ("seqs", "kv_lens", "table", "free_pages", "used", "refs", "used_out", "status")]),
     "token_logprobs": (logprobs, [dict(dtype=2), dict(rows=-1), dict(rows=(1 << 20) + 1), dict(vocab=0), dict(vocab=(1 << 30) + 1, ld_logits=1 << 31),
                                   dict(n=-1), dict(n=33), dict(k=-1), dict(k=33), dict(inv_temperature=0.0), dict(inv_temperature=-1.0),
-                                  dict(inv_temperature=float("nan")), dict(inv_temperature=float("inf")), dict(logits=None), dict(tokens=None),
+                                  dict(inv_temperature=float("nan")), dict(inv_temperature=float("inf")), dict(inv_temperature=2.0 ** 20 * 1.001),
+                                  dict(inv_temperature=2.0 ** -20 * 0.999), dict(logits=None), dict(tokens=None),
                                   dict(logits=P + 2), dict(ld_logits=99)]),
     "token_logprobs_grad": (grad, [dict(dtype=2), dict(rows=-1), dict(rows=(1 << 20) + 1), dict(vocab=0), dict(n=33), dict(inv_temperature=0.0),
-                                   dict(reserved=1), dict(logits=None), dict(out=None), dict(lse=None), dict(tokens=None), dict(grad_logprobs=None),
+                                   dict(inv_temperature=2.0 ** 21), dict(reserved=1), dict(logits=None), dict(out=None), dict(lse=None), dict(tokens=None), dict(grad_logprobs=None),
                                    dict(entropy=None), dict(logits=P + 1), dict(out=P + 2), dict(ld_logits=99), dict(ld_out=99),
                                    dict(out=P, ld_out=101), dict(rows=1 << 20, vocab=1 << 25, ld_logits=1 << 25, ld_out=1 << 25)]),
 }

@@ -556,6 +556,34 @@ def test_kv_release_changes_nothing_when_it_cannot(fault, status, many):
     np.testing.assert_array_equal(host(rf), refs)
 
 
+def test_pages_and_layers_behind_2_31_elements():
+    """Caches of more than 2^31 elements a layer, and layers as far apart: the last page's tokens move, and are copied and read."""
+    hkv, hd = 8, 128
+    pages = (1 << 31) // (hkv * 64 * hd) + 2
+    layer = pages * hkv * 64 * hd
+    store = [torch.zeros(layer + 128 * hkv * 64 * hd, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    k, v = (x.as_strided((2, pages, hkv, 64, hd), (128 * hkv * 64 * hd, hkv * 64 * hd, 64 * hd, hd, 1)) for x in store)
+    with pytest.raises(Exception, match="ld_layer"):  # (layers that overlap)
+        dfl().kv_compact(k, v, i32([[0]]), i32([1]), i32([0, 1]), i32([[0]]), i32([0]))
+    k, v = (x[:layer].view(pages, hkv, 64, hd) for x in store)
+    g = torch.Generator().manual_seed(1)
+    last = pages - 1
+    for x in (k, v):
+        x[last - 1:] = torch.randn((2, hkv, 64, hd), generator=g).to(torch.bfloat16).cuda()
+    table, kv, start = i32([[last - 1, last]]), i32([90]), i32([0, 12])
+    before = k[last].clone()
+    got = dfl().kv_compact(k, v, table, kv, start, i32([[0, 3, 11, -1]]), i32([2]))
+    assert int(got.status) == 0 and int(got.kv_lens) == 81
+    assert torch.equal(k[last, :, 15], before[:, 17]) and torch.equal(k[last, :, 16], before[:, 25])  # nodes 3 and 11, to 79 and 80
+    refs = torch.zeros(pages, dtype=torch.int32, device="cuda")
+    f = dfl().kv_fork(i32([0]), got.kv_lens, table, i32([pages // 2 + 5]), i32([0]), refs, k, v)
+    assert int(f.status) == 0 and torch.equal(k[pages // 2 + 5, :, :17], k[last, :, :17]) and int(refs[last - 1]) == 1
+    c = dict(q=torch.randn((1, 8, hd), generator=g).to(torch.bfloat16).float().numpy(), k=host(k[last - 1:].float()), v=host(v[last - 1:].float()), pre=[],
+             prefix=0, table=np.array([[0, 1]]), kv=np.array([81]), start=np.array([0, 1]), sees=[np.ones((1, 1), bool)], dtype="bf16", hd=hd)
+    q = torch.from_numpy(c["q"]).to(torch.bfloat16).cuda()
+    attn_check(c, dfl().tree_attention(q, k, v, table, got.kv_lens, i32([0, 1]), i32([[1]])))
+
+
 # ------------------------------------------------------------------------------------------ a run of them together
 @pytest.mark.parametrize("graph", [False, True])
 def test_a_verified_tree_from_masks_to_the_next_step(graph):
