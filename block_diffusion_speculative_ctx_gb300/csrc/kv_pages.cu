@@ -4,8 +4,12 @@
 // Fork: two launches.  The first reads the children's lengths in every CTA (at
 // most 2048 from L2, as the page tables do) and shares the work on the tables and
 // the counts, a warp per child; the second copies the pages that end inside, a CTA
-// per child, layer and cache, each head's tokens being one run of the page.  Bytes:
-// twice the copied tokens, nothing for the shared ones.
+// per child, layer and cache, each head's tokens being one run of the page, of which a
+// warp takes 4 KB at a time (by vectors of the whole page in turn: 64 children over
+// 36 layers 66 us instead of 54).  Bytes: the parents' last tokens once (their other
+// children find them in L2) and each child's copy; nothing for the shared pages.
+// Measured (graph replay): 4.9 us for four children over 5 layers; with the release
+// 69 us for 64 children of 8 parents over 36 layers (340 MB: 50 us at a measured copy's rate).
 //
 // Release: one launch of one cluster, whose barriers separate the steps.
 //   1  every page named is looked at (range, count);
@@ -18,7 +22,8 @@
 //      warps before it, it knows their places in the free list.
 // Mentions are numbered (place in seqs, table entry) and a warp owns consecutive
 // ones, so the list's order does not depend on the order of the atomics.  Bound by
-// latency: some ten dependent trips to L2.
+// latency: seven to nine dependent trips to L2 and as many barriers; 6.1 us for four
+// sequences of nine pages.
 #include <algorithm>
 
 #include "ops.h"

@@ -9,10 +9,14 @@
 // Acceptance: with next(p) = the lowest child of p that holds posterior[p] (an
 // atomic minimum a node, whatever the order), the path is next applied from the
 // root on: m independent steps and one chain of as many reads as tokens accepted.
-// Both are bound by latency (a launch, two dependent reads of a few KB).
+// Both are bound by latency (a launch, two dependent reads of a few KB): some 2 us
+// each in a graph.
 // Compaction: path[j] >= j rises, so moves in the order of j never overwrite a row
 // that is still to be read; a thread owns 16 bytes of a row of one head and has
 // eight moves' loads in flight before their stores.  Bytes: twice the moved rows.
+// Measured (graph replay, the three calls together): 6.0 us for one tree of 16 nodes
+// over 5 layers, 10.5 us for 32 trees of up to 64 nodes over 36 layers (35 MB moved,
+// 5.2 us at a measured copy's rate).
 #include "ops.h"
 
 namespace dfl {
