@@ -371,13 +371,13 @@ __global__ void __launch_bounds__(NT, 1024 / NT) logprobs_kernel(dflash_logprobs
     const float c = a.inv_temperature * LOG2E;
     const uint64_t c2 = pack2(c, c);
     float m = -INFINITY, l = 0.f, t = 0.f;
-    int my_id = -1, my_ahead = 0;  // lane's token, the warp's elements ahead of it, and its logit
+    int my_id = -1, my_ahead = 0;  // lane's token, the warp's elements ahead of it (of one token: the lane's), and its logit
     float my_xt = 0.f;
     float tau_v = -INFINITY;  // candidates are as large (-inf: not known yet)
     int refresh = 2;
     // f(its key, the keys above it) for each of the list's n keys, by all threads, four a key; ends without a barrier
     auto rank_list = [&](int n, auto&& f) {
-        for (int i0 = 0; i0 < n; i0 += NT / 4) {
+        for (int i0 = 0; i0 + 8 * warp < n; i0 += NT / 4) {
             const uint64_t mine = list[min(i0 + tid / 4, n)];
             const int above = count_above4(list, n, mine);
             if (mine && (tid & 3) == 0) f(mine, above);
@@ -458,17 +458,31 @@ __global__ void __launch_bounds__(NT, 1024 / NT) logprobs_kernel(dflash_logprobs
 
         // ---- ranks: of the ids behind the token's those of a larger logit count, of the ids before it also those of the same
         if (a.ranks) {
-            if (it == 0 && lane < a.n) {
-                my_id = S.id[lane];
-                my_xt = S.xt[lane];
-            }
             // (the extra tile of single tokens has ids on both sides of any token)
             const bool single = it == sl.full;
             const int first = sl.first_id(it);
-            const bool before = !single && my_id >= first + NT * E;  // lane's token lies behind the tile
-            const float my_least = before ? my_xt : next_above<T>(my_xt);
+            // this thread's elements as large as `least`, added to n
+            auto add_ahead = [&](int& n, float least) {
+                if constexpr (sizeof(T) == 4) {
+#pragma unroll
+                    for (int e = 0; e < E; ++e) add_if_ge(n, x[e], least);
+                } else {
+                    // (0 or 1 in bf16: sums up to 256 are exact)
+                    const __nv_bfloat162 l2 = __float2bfloat162_rn(least);
+                    __nv_bfloat162 n2[2] = {__float2bfloat162_rn(0.f), __float2bfloat162_rn(0.f)};
+#pragma unroll
+                    for (int j = 0; j < NV; ++j) {
+                        const uint32_t w[4] = {raw[j].x, raw[j].y, raw[j].z, raw[j].w};
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            n2[k & 1] = __hadd2(n2[k & 1], __hge2(*reinterpret_cast<const __nv_bfloat162*>(&w[k]), l2));
+                    }
+                    n2[0] = __hadd2(n2[0], n2[1]);
+                    n += __float2int_rn(__low2float(n2[0]) + __high2float(n2[0]));
+                }
+            };
             // tokens q .. q + Q - 1: the warp's counts to their lanes
-            auto count = [&](int q, auto Qc) {
+            auto count = [&](int q, float my_least, auto Qc) {
                 constexpr int Q = decltype(Qc)::value;
                 uint32_t n[(Q + 1) / 2];  // two tokens' counts each
 #pragma unroll
@@ -476,29 +490,8 @@ __global__ void __launch_bounds__(NT, 1024 / NT) logprobs_kernel(dflash_logprobs
 #pragma unroll
                 for (int i = 0; i < Q; ++i) {
                     const float least = __shfl_sync(0xffffffffu, my_least, q + i);
-                    int mine;
-                    if constexpr (sizeof(T) == 4) {
-                        int n0 = 0, n1 = 0;
-#pragma unroll
-                        for (int e = 0; e < E; e += 2) {
-                            add_if_ge(n0, x[e], least);
-                            add_if_ge(n1, x[e + 1], least);
-                        }
-                        mine = n0 + n1;
-                    } else {
-                        // (0 or 1 in bf16: sums up to 256 are exact)
-                        const __nv_bfloat162 l2 = __float2bfloat162_rn(least);
-                        __nv_bfloat162 n2[2] = {__float2bfloat162_rn(0.f), __float2bfloat162_rn(0.f)};
-#pragma unroll
-                        for (int j = 0; j < NV; ++j) {
-                            const uint32_t w[4] = {raw[j].x, raw[j].y, raw[j].z, raw[j].w};
-#pragma unroll
-                            for (int k = 0; k < 4; ++k)
-                                n2[k & 1] = __hadd2(n2[k & 1], __hge2(*reinterpret_cast<const __nv_bfloat162*>(&w[k]), l2));
-                        }
-                        n2[0] = __hadd2(n2[0], n2[1]);
-                        mine = __float2int_rn(__low2float(n2[0]) + __high2float(n2[0]));
-                    }
+                    int mine = 0;
+                    add_ahead(mine, least);
                     n[i / 2] += (uint32_t)mine << 16 * (i & 1);
                 }
 #pragma unroll
@@ -507,18 +500,9 @@ __global__ void __launch_bounds__(NT, 1024 / NT) logprobs_kernel(dflash_logprobs
                 for (int i = 0; i < Q; ++i)
                     if (lane == q + i) my_ahead += (int)(n[i / 2] >> 16 * (i & 1) & 0xFFFFu);
             };
-            int q = 0;
-#pragma unroll 1
-            for (; q + 4 <= a.n; q += 4) count(q, Int<4>());
-#pragma unroll 1
-            for (; q < a.n; ++q) count(q, Int<1>());
-            // the tile that holds a token has ids on both sides of it: those before it of the same logit; and elements that are
-            // none, which are -inf, have been counted as large as a token at -inf behind them
-            const bool here = single ? my_id >= 0 : (unsigned)(my_id - first) < (unsigned)(NT * E),
-                       extra = before && it >= sl.whole && my_xt == -INFINITY;
-            for (uint32_t w = __ballot_sync(0xffffffffu, here || extra); w; w &= w - 1) {
-                const int i = __ffs(w) - 1, at = __shfl_sync(0xffffffffu, my_id, i);
-                const float xt = __shfl_sync(0xffffffffu, my_xt, i);
+            // The tile that holds a token (or single tokens) has ids on both sides of it: those before it of the same logit.  And
+            // elements that are none, which are -inf, have been counted as large as a token at -inf behind them.
+            auto ties = [&](int at, float xt) {
                 int n = 0;
 #pragma unroll
                 for (int j = 0; j < NV; ++j) {
@@ -530,8 +514,31 @@ __global__ void __launch_bounds__(NT, 1024 / NT) logprobs_kernel(dflash_logprobs
                         for (int e = 0; e < G; ++e) n += x[j * G + e] == xt && id + e < at && (e == 0 || !single);
                     }
                 }
-                n = __reduce_add_sync(0xffffffffu, n);
-                if (lane == i) my_ahead += n;
+                return n;
+            };
+            if (it == 0 && (lane < a.n || a.n == 1)) {
+                my_id = S.id[a.n == 1 ? 0 : lane];
+                my_xt = S.xt[a.n == 1 ? 0 : lane];
+            }
+            const bool before = !single && my_id >= first + NT * E;  // lane's token lies behind the tile
+            const bool here = single ? my_id >= 0 : (unsigned)(my_id - first) < (unsigned)(NT * E),
+                       extra = before && it >= sl.whole && my_xt == -INFINITY;
+            const float my_least = before ? my_xt : next_above<T>(my_xt);
+            if (a.n == 1) {
+                // (every lane holds the one token; its counts are joined at the end)
+                add_ahead(my_ahead, my_least);
+                if (here || extra) my_ahead += ties(my_id, my_xt);
+            } else {
+                int q = 0;
+#pragma unroll 1
+                for (; q + 4 <= a.n; q += 4) count(q, my_least, Int<4>());
+#pragma unroll 1
+                for (; q < a.n; ++q) count(q, my_least, Int<1>());
+                for (uint32_t w = __ballot_sync(0xffffffffu, here || extra); w; w &= w - 1) {
+                    const int i = __ffs(w) - 1;
+                    const int n = __reduce_add_sync(0xffffffffu, ties(__shfl_sync(0xffffffffu, my_id, i), __shfl_sync(0xffffffffu, my_xt, i)));
+                    if (lane == i) my_ahead += n;
+                }
             }
         }
 
@@ -565,7 +572,13 @@ __global__ void __launch_bounds__(NT, 1024 / NT) logprobs_kernel(dflash_logprobs
         }
     }
 
-    if (a.ranks && my_ahead) atomicAdd(&S.part.ahead[lane], my_ahead);
+    if (a.ranks) {
+        if (a.n == 1) {
+            my_ahead = __reduce_add_sync(0xffffffffu, my_ahead);
+            if (lane) my_ahead = 0;
+        }
+        if (my_ahead) atomicAdd(&S.part.ahead[lane], my_ahead);
+    }
 
     // ---- the CTA's results (the list's logits come while the warps join their sums)
     int n = 0;
