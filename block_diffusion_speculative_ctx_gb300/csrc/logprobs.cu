@@ -654,6 +654,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) logprobs_kernel(dflash_logprobs
     auto logprob = [&](float x) { return bad ? NAN : x == -INFINITY ? -INFINITY : (x - m) * a.inv_temperature - ln_l; };
     if (tid == NT - 1) {
         if (a.lse) a.lse[row] = bad ? NAN : none ? -INFINITY : fmaf(m, a.inv_temperature, ln_l);
+        if (a.lse_parts) *reinterpret_cast<float2*>(a.lse_parts + 2 * row) = bad ? make_float2(NAN, NAN) : make_float2(m, ln_l);
         if (a.entropy) a.entropy[row] = bad ? NAN : none ? 0.f : ln_l - LN2 * (sums.z / sums.y);
     }
     if (tid < a.n) {
@@ -745,11 +746,18 @@ __global__ void __launch_bounds__(NB) logprobs_grad_kernel(dflash_logprobs_grad_
     const float h = a.grad_entropy ? a.grad_entropy[row] : 0.f, H = a.entropy ? a.entropy[row] : 0.f;
     const float sum = warp_sum(g);
     const bool zero = !__any_sync(0xffffffffu, g != 0.f) && h == 0.f;
-    float lse = a.lse[row];
+    float lse, best = 0.f;  // x / T - lse, or with its two parts (x - best) / T - lse
+    if (a.lse_parts) {
+        const float2 two = *reinterpret_cast<const float2*>(a.lse_parts + 2 * row);
+        best = two.x == -INFINITY ? 0.f : two.x;
+        lse = two.y;
+    } else {
+        lse = a.lse[row];
+    }
     if (lse == -INFINITY) lse = INFINITY;  // (a row of -inf alone: p = 0)
     // -p (G + h (ln p + H)); ln p below any p that is not 0
     auto slope = [&](float x) {
-        const float z = max_nan(fmaf(x, a.inv_temperature, -lse), -1000.f);
+        const float z = max_nan(fmaf(x - best, a.inv_temperature, -lse), -1000.f);
         return -ex2(z * LOG2E) * fmaf(h, z + H, sum);
     };
     if (VECTORS) {
@@ -843,6 +851,7 @@ extern "C" dflash_status dflash_token_logprobs(const dflash_logprobs_args* p, vo
         return fail("token_logprobs: inv_temperature outside [2^-20, 2^20]");
     if ((a.rows > 0 && !a.logits) || (a.rows > 0 && a.n > 0 && !a.tokens)) return fail("token_logprobs: NULL argument");
     if ((uintptr_t)a.logits % (a.dtype == DFLASH_DTYPE_BF16 ? 2 : 4)) return fail("token_logprobs: logits is not aligned to its type");
+    if ((uintptr_t)a.lse_parts % 8) return fail("token_logprobs: lse_parts is not aligned to 8 bytes");
     if (a.ld_logits < a.vocab) return fail("token_logprobs: the row stride is smaller than vocab");
     if (a.rows == 0) return DFLASH_OK;
     return queue(cuda_stream, "token_logprobs: launch failed", [&](const Launch& L) {
@@ -862,10 +871,11 @@ extern "C" dflash_status dflash_token_logprobs_grad(const dflash_logprobs_grad_a
     if (!(a.inv_temperature >= MIN_INVERSE && a.inv_temperature <= MAX_INVERSE))
         return fail("token_logprobs_grad: inv_temperature outside [2^-20, 2^20]");
     if (a.reserved != 0) return fail("token_logprobs_grad: reserved must be 0");
-    if (a.rows > 0 && (!a.logits || !a.out || !a.lse || (a.n > 0 && (!a.tokens || !a.grad_logprobs)) || (a.grad_entropy && !a.entropy)))
+    if (a.rows > 0 && (!a.logits || !a.out || (!a.lse && !a.lse_parts) || (a.n > 0 && (!a.tokens || !a.grad_logprobs)) || (a.grad_entropy && !a.entropy)))
         return fail("token_logprobs_grad: NULL argument");
     const uintptr_t es = a.dtype == DFLASH_DTYPE_BF16 ? 2 : 4;
     if (((uintptr_t)a.logits | (uintptr_t)a.out) % es) return fail("token_logprobs_grad: logits or out is not aligned to its type");
+    if ((uintptr_t)a.lse_parts % 8) return fail("token_logprobs_grad: lse_parts is not aligned to 8 bytes");
     if (a.ld_logits < a.vocab || a.ld_out < a.vocab) return fail("token_logprobs_grad: a row stride is smaller than vocab");
     if (a.out == a.logits && a.ld_out != a.ld_logits && a.rows > 1) return fail("token_logprobs_grad: in place needs one row stride");
     const long long chunk = NB * VB;

@@ -20,17 +20,17 @@ LOGPROBS_MAX_TOKENS = LOGPROBS_MAX_TOP = 32
 
 class dflash_logprobs_args(ctypes.Structure):
     _fields_ = ([(n, _I32) for n in ("dtype", "rows", "vocab", "n", "k")] + [("inv_temperature", _F), ("ld_logits", _I64)]
-                + [(n, _P) for n in ("logits", "tokens", "logprobs", "ranks", "entropy", "lse", "top_ids", "top_logprobs")])
+                + [(n, _P) for n in ("logits", "tokens", "logprobs", "ranks", "entropy", "lse", "top_ids", "top_logprobs", "lse_parts")])
 
 
 class dflash_logprobs_grad_args(ctypes.Structure):
     _fields_ = ([(n, _I32) for n in ("dtype", "rows", "vocab", "n")] + [("inv_temperature", _F), ("reserved", _I32)]
                 + [(n, _I64) for n in ("ld_logits", "ld_out")]
-                + [(n, _P) for n in ("logits", "tokens", "lse", "grad_logprobs", "entropy", "grad_entropy", "out")])
+                + [(n, _P) for n in ("logits", "tokens", "lse", "grad_logprobs", "entropy", "grad_entropy", "out", "lse_parts")])
 
 
 # (packed forms of the structs, as in ops.py)
-_LOGPROBS, _GRAD = struct.Struct("5ifq8Q"), struct.Struct("4ifi2q7Q")
+_LOGPROBS, _GRAD = struct.Struct("5ifq9Q"), struct.Struct("4ifi2q8Q")
 
 
 class TokenLogprobs(NamedTuple):
@@ -80,15 +80,16 @@ def _alike(name, t, like, dtype, device):
 
 
 def token_logprobs(logits, tokens, *, top: int = 0, temperature: float = 1.0, logprobs=None, ranks=None, entropy=None,
-                   lse=None, top_ids=None, top_logprobs=None) -> TokenLogprobs:
+                   lse=None, top_ids=None, top_logprobs=None, lse_parts=None) -> TokenLogprobs:
     """Log probabilities of given tokens (``dflash_token_logprobs``).
 
     logits: [rows, vocab] (fp32 or bf16); tokens: int32 [rows] or [rows, n] (n <= 32; an id outside the vocabulary
     is padding).  The law is softmax(logits / temperature).  Gives ``logprobs`` (of tokens' shape; padding 0),
     ``ranks`` (int32, tokens ahead of each; padding -1), ``entropy`` and ``lse`` [rows], and for top > 0 the
     likeliest tokens' ``top_ids`` and ``top_logprobs`` [rows, top], the lower id first among equals (top <= 32;
-    -1 and -inf where fewer tokens are above -inf).  All fp32; missing outputs are allocated."""
-    dev = _device(logits, logits, logprobs, entropy, lse, top_logprobs)
+    -1 and -inf where fewer tokens are above -inf).  All fp32; missing outputs are allocated, but for ``lse_parts``
+    ([rows, 2], written when given): the largest logit and the rest of lse, for the gradient of rows of any size."""
+    dev = _device(logits, logits, logprobs, entropy, lse, top_logprobs, lse_parts)
     dt, rows, vocab, ld = _logits("logits", logits, dev)
     n = _tokens(tokens, rows)
     if not 0 <= top <= LOGPROBS_MAX_TOP:
@@ -105,9 +106,12 @@ def token_logprobs(logits, tokens, *, top: int = 0, temperature: float = 1.0, lo
         p_top = _ops._flats(dev, "top_ids", top_ids, _I32T, rows * top, "top_logprobs", top_logprobs, _F32T, rows * top)
     elif top_ids is not None or top_logprobs is not None:
         _bad("top_ids and top_logprobs need top")
+    p_parts = 0
+    if lse_parts is not None:
+        p_parts = _ops._flat("lse_parts", _alike("lse_parts", lse_parts, (rows, 2), _F32T, device), _F32T, 2 * rows, dev)
     _call(load().dflash_token_logprobs, _LOGPROBS.pack,
-          (dt, rows, vocab, n, top, _inverse(temperature), ld, logits.data_ptr(), *p, *p_top), dev)
-    _ops._written(logprobs, ranks, entropy, lse, top_ids, top_logprobs)
+          (dt, rows, vocab, n, top, _inverse(temperature), ld, logits.data_ptr(), *p, *p_top, p_parts), dev)
+    _ops._written(logprobs, ranks, entropy, lse, top_ids, top_logprobs, lse_parts)
     return TokenLogprobs(logprobs, ranks, entropy, lse, top_ids, top_logprobs)
 
 
@@ -115,7 +119,9 @@ def token_logprobs_grad(logits, tokens, lse, grad_logprobs, *, entropy=None, gra
                         out=None):
     """Gradient by the logits of a loss of ``token_logprobs``' results (``dflash_token_logprobs_grad``).
 
-    logits, tokens, temperature: as given there; lse, entropy: as it gave them; grad_logprobs: fp32 of tokens' shape,
+    logits, tokens, temperature: as given there; lse, entropy: as it gave them; lse may be its lse_parts [rows, 2], from
+    which the probabilities of rows of any size are exact (lse's own last digit is a factor of exp(2^-24 |lse|), and of a row
+    all of the type's lowest value it says nothing); grad_logprobs: fp32 of tokens' shape,
     the loss's gradient by each log probability (padding's does not count); grad_entropy: fp32 [rows] or None, by the
     entropies (needs entropy).  Returns ``out`` (of logits' type, allocated when None; ``out=logits`` works in place).
     For alternatives' log probabilities, name their ids among the tokens."""
@@ -124,8 +130,11 @@ def token_logprobs_grad(logits, tokens, lse, grad_logprobs, *, entropy=None, gra
     n = _tokens(tokens, rows)
     if grad_logprobs is None or grad_logprobs.shape != tokens.shape:
         _bad("grad_logprobs must have the shape of tokens")
-    p_tok, p_lse, p_g = _ops._flats(dev, "tokens", tokens, _I32T, rows * n, "lse", lse, _F32T, rows, "grad_logprobs",
-                                    grad_logprobs, _F32T, rows * n)
+    parts = lse.dim() == 2
+    if parts and lse.shape != (rows, 2):
+        _bad(f"lse must be [{rows}], or lse_parts [{rows}, 2]")
+    p_tok, p_lse, p_g = _ops._flats(dev, "tokens", tokens, _I32T, rows * n, "lse", lse, _F32T, rows * 2 if parts else rows,
+                                    "grad_logprobs", grad_logprobs, _F32T, rows * n)
     p_ent = p_h = 0
     if grad_entropy is not None:
         if entropy is None:
@@ -135,7 +144,7 @@ def token_logprobs_grad(logits, tokens, lse, grad_logprobs, *, entropy=None, gra
         out = torch.empty((rows, vocab), dtype=logits.dtype, device=logits.device)
     ld_out = max(_ops._mat("out", out, logits.dtype, rows, vocab, dev), vocab)
     _call(load().dflash_token_logprobs_grad, _GRAD.pack,
-          (dt, rows, vocab, n, _inverse(temperature), 0, ld, ld_out, logits.data_ptr(), p_tok, p_lse, p_g, p_ent, p_h,
-           out.data_ptr()), dev)
+          (dt, rows, vocab, n, _inverse(temperature), 0, ld, ld_out, logits.data_ptr(), p_tok,
+           0 if parts else p_lse, p_g, p_ent, p_h, out.data_ptr(), p_lse if parts else 0), dev)
     _ops._written(out)
     return out

@@ -859,12 +859,14 @@ dflash_status dflash_kv_release(const dflash_kv_release_args* args, void* cuda_s
  *                  [0, vocab) (padding)
  *   ranks[i]     = tokens ahead of t: of a larger logit, or an equal one and a
  *                  lower id; -1 for padding
+ *   lse_parts    = the largest logit and ln sum_v exp(x_v - its x): lse =
+ *                  lse_parts[0] * inv_temperature + lse_parts[1]
  *   entropy      = -sum_v p_v ln p_v, p = exp(x - lse)
  *   top_ids, top_logprobs = the k likeliest tokens, likeliest first, the lower id
  *                  first among equal logits
  * Tokens at -inf have probability 0; they are no alternatives: where fewer than k
  * tokens are left, the list ends in id -1 and -inf.  A row of -inf alone has lse =
- * logprobs = -inf and entropy 0.  A row that holds NaN or +inf gets NaN
+ * lse_parts = logprobs = -inf and entropy 0.  A row that holds NaN or +inf gets NaN
  * everywhere (but padding's 0), ranks and top_ids -1.
  * Any of the outputs may be NULL.  Rows are ld_logits elements apart.
  * Errors: E_INVAL, E_CUDA. */
@@ -885,6 +887,7 @@ typedef struct {
     float* lse;                /* [rows] or NULL */
     int32_t* top_ids;          /* [rows][k] or NULL */
     float* top_logprobs;       /* [rows][k] or NULL */
+    float* lse_parts;          /* [rows][2], 8-byte aligned, or NULL */
 } dflash_logprobs_args;
 dflash_status dflash_token_logprobs(const dflash_logprobs_args* args, void* cuda_stream);
 
@@ -894,7 +897,11 @@ dflash_status dflash_token_logprobs(const dflash_logprobs_args* args, void* cuda
  *   out_v = inv_temperature * (sum_{i: t_i = v} g_i - p_v sum_i g_i
  *                              - h p_v (ln p_v + entropy))
  * in fp32, rounded once to the logits' type.  lse and entropy are what
- * dflash_token_logprobs gave (both entropy and grad_entropy, or neither).  A row
+ * dflash_token_logprobs gave (both entropy and grad_entropy, or neither).  p
+ * comes from lse_parts where they are given, as exact for rows of any size;
+ * from lse alone, p is off by the factor exp(+-2^-24 |lse|): a row all of the
+ * type's lowest value, whose lse is that value or below fp32's range, needs
+ * lse_parts.  A row
  * whose g and h are all 0 gets zeros, whatever it holds; one of -inf alone the
  * g at its tokens.  out may be logits, with one row
  * stride; no other overlap.
@@ -910,11 +917,12 @@ typedef struct {
     int64_t ld_out;
     const void* logits;
     const int32_t* tokens;     /* [rows][n]; NULL when n is 0 */
-    const float* lse;          /* [rows] */
+    const float* lse;          /* [rows]; NULL with lse_parts */
     const float* grad_logprobs; /* [rows][n]; NULL when n is 0 */
     const float* entropy;      /* [rows] or NULL */
     const float* grad_entropy; /* [rows] or NULL */
     void* out;                 /* [rows][vocab] */
+    const float* lse_parts;    /* [rows][2], 8-byte aligned, or NULL: lse is read */
 } dflash_logprobs_grad_args;
 dflash_status dflash_token_logprobs_grad(const dflash_logprobs_grad_args* args, void* cuda_stream);
 

@@ -303,3 +303,48 @@ def test_a_loss_and_its_gradient():
     loss = (logp.gather(1, names.long().clamp(min=0)) * (names >= 0) * adv).sum() + 0.01 * -(logp.exp() * logp).sum()
     loss.backward()
     grad_check("f32", x.cpu(), host(names), host(adv), host(bonus), got, host(y.grad))
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("temperature", [0.5, 1.0, 3.0])
+def test_token_logprobs_grad_of_rows_of_any_size(dtype, temperature):
+    """From lse_parts: a row all of the type's lowest value is uniform, and rows far from 0 are as exact as others."""
+    vocab = 5000
+    x = rows_of(dtype, 6, vocab, seed=15).float()
+    x[0] = torch.finfo(DT[dtype]).min
+    x[1] += 1e5 if dtype == "f32" else 500.0
+    x[2] = float("-inf")
+    x[2, 5] = torch.finfo(DT[dtype]).min
+    x[3] = float("-inf")
+    x[4, 9] = float("nan")
+    x = x.to(DT[dtype])
+    t = np.array([[3, 60], [7, -1], [5, 6], [2, vocab - 1], [1, 0], [4, 2]])
+    rng = np.random.default_rng(3)
+    g, h = rng.standard_normal((6, 2)).astype(np.float32), rng.standard_normal(6).astype(np.float32)
+    two = torch.empty((6, 2), device="cuda")
+    f = dfl().token_logprobs(x.cuda(), i32(t), temperature=temperature, lse_parts=two)
+    got = dfl().token_logprobs_grad(x.cuda(), i32(t), two, torch.from_numpy(g).cuda(), entropy=f.entropy, grad_entropy=torch.from_numpy(h).cuda(),
+                                    temperature=temperature)
+    assert torch.isnan(got[4]).all() and torch.isnan(two[4]).all()
+    rows = [0, 1, 2, 3, 5]
+    xs = host(x.float())[rows]
+    best = xs.max(1)
+    np.testing.assert_array_equal(host(two)[rows, 0], best)
+    y = np.where(np.isneginf(xs), -np.inf, xs.astype(np.float64) - np.where(np.isneginf(best), 0, best)[:, None])  # (rows from 0: the same law)
+    want = trees.token_logprobs_grad(y, t[rows], g[rows], h[rows], temperature)
+    grad_check(dtype, torch.from_numpy(np.where(np.isneginf(y), -np.inf, np.maximum(y, -1e30))), t[rows], g[rows], h[rows], got[rows], want, temperature)
+
+
+def test_parts_of_lse_make_lse():
+    x = rows_of("f32", 4, 3001, seed=16)
+    t = tokens_of(x, 1, seed=2)
+    two = torch.empty((4, 2), device="cuda")
+    f = dfl().token_logprobs(x.cuda(), i32(t), temperature=0.7, lse_parts=two)
+    want = host(two).astype(np.float64)
+    want = want[:, 0] * np.float32(1 / 0.7) + want[:, 1]
+    # one rounding
+    np.testing.assert_allclose(host(f.lse), want, rtol=U, atol=0)
+    with pytest.raises(ValueError, match="lse_parts"):
+        dfl().token_logprobs(x.cuda(), i32(t), lse_parts=torch.empty((4, 1), device="cuda"))
+    with pytest.raises(ValueError, match="lse_parts"):
+        dfl().token_logprobs_grad(x.cuda(), i32(t), torch.empty((4, 3), device="cuda"), f.logprobs)
