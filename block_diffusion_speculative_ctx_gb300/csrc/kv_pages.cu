@@ -6,7 +6,7 @@
 // the counts, a warp per child; the second copies the pages that end inside, a CTA
 // per child, layer and cache, each head's tokens being one run of the page, of which a
 // warp takes 4 KB at a time (by vectors of the whole page in turn: 64 children over
-// 36 layers 66 us instead of 54).  Bytes: the parents' last tokens once (their other
+// 36 layers, with their release, 80 us instead of 69).  Bytes: the parents' last tokens once (their other
 // children find them in L2) and each child's copy; nothing for the shared pages.
 // Measured (graph replay): 4.9 us for four children over 5 layers; with the release
 // 69 us for 64 children of 8 parents over 36 layers (340 MB: 50 us at a measured copy's rate).
@@ -184,7 +184,7 @@ __device__ __forceinline__ int ld_peer_int(const int* local, uint32_t rank) {
 
 __global__ void __launch_bounds__(NR) kv_release_kernel(dflash_kv_release_args a, int n_cta) {
     __shared__ int units_s[MAXB + 1];  // units of the sequences before
-    __shared__ int seq_s[MAXB], pages_s[MAXB];
+    __shared__ int seq_s[MAXB], first_s[MAXB], pages_s[MAXB];  // its table entries first_s .. pages_s - 1 are named
     __shared__ uint32_t named[MAXB / 32];
     __shared__ int wsum[WARPS], counts[WARPS];
     __shared__ int flag_s[2];
@@ -204,18 +204,19 @@ __global__ void __launch_bounds__(NR) kv_release_kernel(dflash_kv_release_args a
         mine[i] = 0;
         if (k < a.n) {
             const int s = a.seqs[k];
-            int pages = 0;
+            int pages = 0, first = 0;
             if (s < 0 || s >= a.batch || atomicOr(&named[s >> 5], 1u << (s & 31)) >> (s & 31) & 1u) {
                 bad |= BAD_LENGTH;
             } else {
-                const int kv = a.kv_lens[s];
-                if (kv < 0) bad |= BAD_LENGTH;
+                const int kv = a.kv_lens[s], keep = a.keep_lens ? a.keep_lens[s] : 0;
+                if (kv < 0 || keep < 0 || keep > kv) bad |= BAD_LENGTH;
                 else if (kv > (long long)64 * a.width) bad |= BAD_WIDTH;
-                else pages = (kv + 63) >> 6;
+                else pages = (kv + 63) >> 6, first = (keep + 63) >> 6;
             }
             seq_s[k] = s;
+            first_s[k] = first;
             pages_s[k] = pages;
-            mine[i] = (pages + UNIT - 1) / UNIT;
+            mine[i] = (pages - first + UNIT - 1) / UNIT;
         }
     }
     const int used = *a.used;
@@ -257,7 +258,7 @@ __global__ void __launch_bounds__(NR) kv_release_kernel(dflash_kv_release_args a
         for (int u = u0; u < u1; ++u) {
             while (units_s[k + 1] <= u) ++k;
             const int* row = a.table + (long long)seq_s[k] * a.ld_table;
-            const int j0 = (u - units_s[k]) * UNIT;
+            const int j0 = first_s[k] + (u - units_s[k]) * UNIT;
             int page[UNIT / 32];
 #pragma unroll
             for (int i = 0; i < UNIT / 32; ++i) {

@@ -246,6 +246,7 @@ extern "C" dflash_status dflash_kv_compact(const dflash_kv_compact_args* p, void
     if (!a.kv_lens || !a.q_start || !a.path || !a.accepted || !a.kv_out || !a.status || (a.width_table > 0 && !a.table))
         return fail("kv_compact: NULL argument");
     if (a.kv_out == a.kv_lens) return fail("kv_compact: kv_out may not be kv_lens");
+    if (a.k_cache == a.v_cache) return fail("kv_compact: v_cache may not be k_cache");  // (its tokens would be moved twice)
     const int vecs = a.head_dim * (a.dtype == DFLASH_DTYPE_BF16 ? 2 : 4) / 16;
     return queue(cuda_stream, "kv_compact: launch failed", [&](const Launch& L) {
         launch_k(L, kv_compact_kernel, dim3(a.batch, 2 * a.layers), dim3(NT_MOVE), 0, 1, a, vecs);

@@ -57,13 +57,14 @@ class dflash_kv_fork_args(ctypes.Structure):
 
 class dflash_kv_release_args(ctypes.Structure):
     _fields_ = ([(n, _I32) for n in ("batch", "n", "width", "n_free", "n_pages", "reserved")] + [("ld_table", _I64)]
-                + [(n, _P) for n in ("seqs", "kv_lens", "table", "free_pages", "used", "refs", "used_out", "status")])
+                + [(n, _P) for n in ("seqs", "kv_lens", "table", "free_pages", "used", "refs", "used_out", "status",
+                                     "keep_lens")])
 
 
 # (packed forms of the structs, as in ops.py)
 _MASKS, _TREE = struct.Struct("4iq7Q"), struct.Struct("10ifi3q11QQq2i")
 _ACCEPT, _COMPACT = struct.Struct("4i8Q"), struct.Struct("8i2q9Q")
-_FORK, _RELEASE = struct.Struct("10i3q12Q"), struct.Struct("6iq8Q")
+_FORK, _RELEASE = struct.Struct("10i3q12Q"), struct.Struct("6iq9Q")
 
 
 class TreeMasks(NamedTuple):
@@ -284,11 +285,13 @@ def kv_fork(parents, kv_lens, table, free_pages, used, refs, k_cache, v_cache, *
     return KVFork(table_out, lens_out, used_out, status)
 
 
-def kv_release(seqs, kv_lens, table, free_pages, used, refs, *, used_out=None, status=None) -> KVRelease:
-    """The pages of ended sequences back to the free list (``dflash_kv_release``).
+def kv_release(seqs, kv_lens, table, free_pages, used, refs, *, keep_lens=None, used_out=None, status=None) -> KVRelease:
+    """The pages of ended or shortened sequences back to the free list (``dflash_kv_release``).
 
     seqs: int32 [n], the sequences that end; kv_lens, table: int32 [batch] and [batch, width]; free_pages, used, refs:
-    as ``kv_fork``, free_pages and refs changed in place.  A page returns when its last holder leaves.  ``used_out=used``
+    as ``kv_fork``, free_pages and refs changed in place.  A page returns when its last holder leaves.  With keep_lens
+    (int32 [batch]) the sequences live on with so many tokens and give back the pages behind them: after a step of trees,
+    kv_lens are the lengths with the trees and keep_lens ``kv_compact``'s.  ``used_out=used``
     works in place.  ``status`` stays on the device: 0, or a sum of 1 (more pages return than were taken), 2 (table
     too narrow), 8 (a bad length, used or sequence, or one named twice), 16 (a bad page), 32 (a page returned by
     more sequences than hold it): nothing has changed."""
@@ -305,6 +308,6 @@ def kv_release(seqs, kv_lens, table, free_pages, used, refs, *, used_out=None, s
         "used_out", used_out, 1, "status", status, 1)
     _call(load().dflash_kv_release, _RELEASE.pack,
           (batch, n, table.shape[1], n_free, pages, 0, ld_table, p_seqs, p_kv, table.data_ptr(), p_free or p_status, p_used,
-           p_refs, p_uo, p_status), dev)
+           p_refs, p_uo, p_status, 0 if keep_lens is None else _ops._flat("keep_lens", keep_lens, _I32T, batch, dev)), dev)
     _ops._written(free_pages, refs, used_out, status)
     return KVRelease(used_out, status)

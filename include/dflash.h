@@ -743,7 +743,7 @@ dflash_status dflash_tree_accept(const dflash_tree_accept_args* args, void* cuda
  * (kv_lens outside [m, 64 * width_table]), 16 (a page of a moved token outside
  * [0, n_pages)).  When not 0, nothing of the sequence moves and kv_out =
  * kv_lens.  No two sequences may hold the same page among their nodes'.
- * kv_out may not be kv_lens.  Errors: E_INVAL (sizes, NULL), E_CUDA. */
+ * kv_out may not be kv_lens, nor v_cache k_cache.  Errors: E_INVAL (sizes, NULL), E_CUDA. */
 typedef struct {
     int32_t dtype;             /* F32 or BF16 */
     int32_t batch;
@@ -826,9 +826,16 @@ dflash_status dflash_kv_fork(const dflash_kv_fork_args* args, void* cuda_stream)
  * order, then table entries): a release right behind the call that took the pages
  * restores the list.  The tables and lengths of the sequences are the caller's to
  * forget.
+ * With keep_lens a sequence s lives on with its first keep_lens[s] tokens and
+ * gives back the pages behind them, entries ceil(keep_lens[s] / 64) and on: after
+ * a step whose tree grew past a page and was cut behind it, kv_lens are the
+ * lengths with the tree and keep_lens dflash_kv_compact's kv_out (dflash_kv_tables
+ * takes new pages behind ceil(kv / 64), whatever the table holds there).  The page that
+ * a cut ends in is written to next: it may have no other holder.
  * status (device): 0, or a sum of 1 (more pages return than were taken), 2 (a
- * length above 64 * width), 8 (a negative length, a *used outside [0, n_free], or
- * a sequence outside [0, batch) or named twice), 16 (a page outside [0, n_pages)
+ * length above 64 * width), 8 (a negative length, keep_lens outside [0, kv_lens], a
+ * *used outside [0, n_free], or a
+ * sequence outside [0, batch) or named twice), 16 (a page outside [0, n_pages)
  * or with negative refs), 32 (a page returned by more sequences than hold it).
  * When not 0, nothing changes and used_out = *used.
  * used_out may be used.  Errors: E_INVAL (sizes, NULL), E_CUDA. */
@@ -848,6 +855,7 @@ typedef struct {
     int32_t* refs;             /* [n_pages] */
     int32_t* used_out;         /* [1] */
     int32_t* status;           /* [1] */
+    const int32_t* keep_lens;  /* [batch], or NULL: 0 */
 } dflash_kv_release_args;
 dflash_status dflash_kv_release(const dflash_kv_release_args* args, void* cuda_stream);
 

@@ -101,9 +101,9 @@ def kv_fork(parents, kv_lens, table, free_pages, used, refs, caches, scratch):
     return tables, [int(kv_lens[p]) for p in parents], used, refs, caches
 
 
-def kv_release(seqs, kv_lens, table, free_pages, used, refs):
+def kv_release(seqs, kv_lens, table, free_pages, used, refs, keep=None):
     """(free_pages, used, refs, status)."""
-    names = [int(p) for s in seqs for p in table[s, : -(-int(kv_lens[s]) // PAGE)]]
+    names = [int(p) for s in seqs for p in table[s, -(-int(keep[s]) // PAGE) if keep is not None else 0: -(-int(kv_lens[s]) // PAGE)]]
     gone = [p for p in dict.fromkeys(names) if names.count(p) == refs[p] + 1]
     if any(names.count(p) > refs[p] + 1 for p in names):
         return free_pages, used, refs, 32

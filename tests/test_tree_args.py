@@ -243,3 +243,20 @@ def test_oracle_log_probabilities_and_their_gradient():
     logp = torch.log_softmax(fine / 0.8, 1)
     (0.5 * logp[0, 3] - logp[1, 29] - (torch.tensor(h) * (logp.exp() * logp).sum(1)).sum()).backward()
     np.testing.assert_allclose(trees.token_logprobs_grad(x, t, g, h, 0.8), fine.grad.numpy(), rtol=1e-9, atol=1e-12)
+
+
+def test_compact_refuses_one_cache_for_both(lib):
+    assert lib.dflash_kv_compact(ctypes.byref(compact()), None) == dfl.DFLASH_E_INVAL
+    assert dfl.dflash_last_error(None) == "kv_compact: v_cache may not be k_cache"
+
+
+@pytest.mark.parametrize("name,make", [("token_logprobs", logprobs), ("token_logprobs_grad", grad)])
+def test_parts_of_lse_are_aligned(lib, name, make):
+    assert getattr(lib, "dflash_" + name)(ctypes.byref(make(lse_parts=P + 4)), None) == dfl.DFLASH_E_INVAL
+    assert dfl.dflash_last_error(None) == name + ": lse_parts is not aligned to 8 bytes"
+
+
+def test_oracle_release_behind_a_cut():
+    table, free, refs = np.array([[4, 1, 2], [3, 5, 0]]), np.arange(6), np.zeros(6, int)
+    f, used, refs, status = trees.kv_release([1, 0], [130, 70], table, free, 5, refs, keep=[65, 64])
+    assert (status, used) == (0, 3) and f[3:5].tolist() == [5, 2]

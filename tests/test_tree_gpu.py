@@ -556,6 +556,62 @@ def test_kv_release_changes_nothing_when_it_cannot(fault, status, many):
     np.testing.assert_array_equal(host(rf), refs)
 
 
+@pytest.mark.parametrize("batch,width", [(1, 1), (3, 5), (500, 40)])
+def test_kv_release_behind_a_cut(batch, width):
+    """Sequences that live on with fewer tokens: whole ones, none, and cuts at and inside pages; of one CTA and of a cluster."""
+    rng = np.random.default_rng(batch)
+    kv = rng.integers(0, 64 * width + 1, batch)
+    keep = np.minimum(kv, rng.integers(0, 64 * width + 1, batch))
+    keep[::3] = keep[::3] // 64 * 64
+    keep[-1] = kv[-1]
+    pages = -(-kv // 64)
+    table, perm, at = np.full((batch, width), -5), rng.permutation(int(pages.sum()) + 3), 0
+    for s in range(batch):
+        table[s, :pages[s]] = perm[at:at + pages[s]]
+        at += pages[s]
+    seqs, used = rng.permutation(batch)[:max(1, batch - 1)], at + 1
+    want = trees.kv_release(seqs, kv, table, np.arange(len(perm)), used, np.zeros(len(perm), int), keep)
+    fl, u, refs = i32(np.arange(len(perm))), i32([used]), i32(np.zeros(len(perm)))
+    r = dfl().kv_release(i32(seqs), i32(kv), i32(table), fl, u, refs, keep_lens=i32(keep), used_out=u)
+    assert int(r.status) == want[3] == 0 and int(u) == want[1]
+    np.testing.assert_array_equal(host(fl), want[0])
+    np.testing.assert_array_equal(host(refs), want[2])
+
+
+@pytest.mark.parametrize("cut", [-1, 101])
+def test_kv_release_refuses_a_cut_outside_the_sequence(cut):
+    fl, u, refs = i32([0, 1, 2, 3]), i32([4]), i32([0] * 4)
+    r = dfl().kv_release(i32([1, 0]), i32([100, 100]), i32([[0, 1], [2, 3]]), fl, u, refs, keep_lens=i32([cut, 0]), used_out=u)
+    assert int(r.status) == 8 and int(u) == 4 and (host(refs) == 0).all() and host(fl).tolist() == [0, 1, 2, 3]
+
+
+def test_steps_of_trees_lose_no_page():
+    """Trees that reach past a page and are cut before it, over many steps: the pages taken are the ones that hold tokens."""
+    d = dfl()
+    rng = np.random.default_rng(21)
+    batch, m, n_pages, width = 4, 40, 60, 12
+    k, v = (torch.zeros((n_pages + 1, 1, 64, 8), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    fl, used, refs = i32(rng.permutation(n_pages)), i32([0]), i32(np.zeros(n_pages + 1))
+    lens, table, new = i32(np.zeros(batch)), i32(np.full((batch, width), n_pages)), i32([m] * batch)
+    q_start, seqs = i32(np.arange(batch + 1) * m), i32(np.arange(batch))
+    for it in range(60):
+        t = d.kv_tables(lens, new, table, fl, used, rows=batch * m, scratch_page=n_pages, table_out=table, used_out=used)
+        assert int(t.status) == 0
+        kv = lens + new
+        acc = rng.integers(0, 9, batch)
+        path = np.full((batch, 9), -1)
+        for s in range(batch):
+            path[s, :acc[s] + 1] = np.concatenate([[0], 1 + np.sort(rng.choice(m - 1, acc[s], replace=False))])
+        c = d.kv_compact(k, v, table, kv, q_start, i32(path), i32(acc))
+        r = d.kv_release(seqs, kv, table, fl, used, refs, keep_lens=c.kv_lens, used_out=used)
+        assert (host(c.status) == 0).all() and int(r.status) == 0
+        lens = c.kv_lens
+        held = -(-host(lens) // 64)
+        assert int(used) == held.sum()
+        mine = np.concatenate([host(table)[s, :held[s]] for s in range(batch)])
+        assert sorted(np.concatenate([mine, host(fl)[int(used):]])) == list(range(n_pages))
+
+
 def test_pages_and_layers_behind_2_31_elements():
     """Caches of more than 2^31 elements a layer, and layers as far apart: the last page's tokens move, and are copied and read."""
     hkv, hd = 8, 128
