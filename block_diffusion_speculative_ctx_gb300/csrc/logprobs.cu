@@ -138,8 +138,10 @@ __device__ __forceinline__ float next_above(float x) {
     const int u = __float_as_int(x + 0.f);
     return __int_as_float(u >= 0 ? u + STEP : u - STEP);
 }
-__device__ __forceinline__ void add_if_ge(int& n, float x, float y) {
-    asm("{\n .reg .pred p;\n setp.ge.f32 p, %1, %2;\n @p add.s32 %0, %0, 1;\n}" : "+r"(n) : "f"(x), "f"(y));
+__device__ __forceinline__ int minus_if_ge(float x, float y) {  // x >= y ? -1 : 0
+    int r;
+    asm("set.ge.s32.f32 %0, %1, %2;" : "=r"(r) : "f"(x), "f"(y));
+    return r;
 }
 // Keys of list[0 .. n) above `mine`; list is 16-byte aligned and list[n] is 0 where n is odd.
 __device__ __forceinline__ int count_above(const uint64_t* list, int n, uint64_t mine) {
@@ -372,7 +374,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) logprobs_kernel(dflash_logprobs
     const uint64_t c2 = pack2(c, c);
     float m = -INFINITY, l = 0.f, t = 0.f;
     int my_id = -1, my_ahead = 0;  // lane's token, the warp's elements ahead of it (of one token: the lane's), and its logit
-    float my_xt = 0.f;
+    float my_xt = 0.f, lowest = INFINITY;  // (the lowest of the tokens' logits: a warp's elements below it are ahead of none)
     float tau_v = -INFINITY;  // candidates are as large (-inf: not known yet)
     int refresh = 2;
     // f(its key, the keys above it) for each of the list's n keys, by all threads, four a key; ends without a barrier
@@ -457,7 +459,14 @@ __global__ void __launch_bounds__(NT, 1024 / NT) logprobs_kernel(dflash_logprobs
         }
 
         // ---- ranks: of the ids behind the token's those of a larger logit count, of the ids before it also those of the same
-        if (a.ranks) {
+        if (a.ranks && it == 0) {
+            if (lane < a.n || a.n == 1) {
+                my_id = S.id[a.n == 1 ? 0 : lane];
+                my_xt = S.xt[a.n == 1 ? 0 : lane];
+            }
+            lowest = -warp_max(my_id < 0 ? -INFINITY : -my_xt);
+        }
+        if (a.ranks && __any_sync(0xffffffffu, tm >= lowest)) {
             // (the extra tile of single tokens has ids on both sides of any token)
             const bool single = it == sl.full;
             const int first = sl.first_id(it);
@@ -465,7 +474,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) logprobs_kernel(dflash_logprobs
             auto add_ahead = [&](int& n, float least) {
                 if constexpr (sizeof(T) == 4) {
 #pragma unroll
-                    for (int e = 0; e < E; ++e) add_if_ge(n, x[e], least);
+                    for (int e = 0; e < E; e += 2) n -= minus_if_ge(x[e], least) + minus_if_ge(x[e + 1], least);
                 } else {
                     // (0 or 1 in bf16: sums up to 256 are exact)
                     const __nv_bfloat162 l2 = __float2bfloat162_rn(least);
@@ -516,10 +525,6 @@ __global__ void __launch_bounds__(NT, 1024 / NT) logprobs_kernel(dflash_logprobs
                 }
                 return n;
             };
-            if (it == 0 && (lane < a.n || a.n == 1)) {
-                my_id = S.id[a.n == 1 ? 0 : lane];
-                my_xt = S.xt[a.n == 1 ? 0 : lane];
-            }
             const bool before = !single && my_id >= first + NT * E;  // lane's token lies behind the tile
             const bool here = single ? my_id >= 0 : (unsigned)(my_id - first) < (unsigned)(NT * E),
                        extra = before && it >= sl.whole && my_xt == -INFINITY;
