@@ -218,7 +218,9 @@ struct Waiter {
 // PAIR: the weights of P V as bf16 pairs.  TREE: rows see the own keys that their masks name; the tiles that hold nodes of
 // the tree take 64 mask bits a row (two to three words from L2, asked for before the scores are waited for) and zero the rows
 // of V that no row of the item sees.  Measured (graph replay): 230 us for 32 trees of 33 .. 64 nodes behind 8192 shared keys and
-// 256 .. 2048 own (1030 TFLOP/s over the call, merge 22 us: the chain above); 10.5 us for 16 nodes behind 512 keys.
+// 256 .. 2048 own (1030 TFLOP/s over the call, merge 22 us: the chain above); 10.5 us for 16 nodes behind 512 keys.  Measured and
+// not kept: sixteen softmax warps, two a vector that take its tiles in turn and pass m and l on (264 us, 12.3 for the 16 nodes: each
+// has a score buffer of its own, whose next scores come behind its own product, so its loop is chain and products in a row).
 template <int HD, bool PAIR, bool TREE>
 __global__ void __launch_bounds__(NTHR, 1)
     shared_tc_kernel(const __grid_constant__ TcArgs a, const __grid_constant__ CUtensorMap mq,

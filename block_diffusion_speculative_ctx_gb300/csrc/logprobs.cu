@@ -8,7 +8,10 @@
 // (l, t) into a (l, t + l d), d = (m - m') log2(e) / T, a = 2^d.  The difference comes
 // before the scale, so logits of the type's lowest value stay what they are.
 // Ranks: a token's are counted as the tiles go by (x >= the token's logit for ids
-// before it, x >= the next value above for ids behind it), four tokens at a time.
+// before it, x >= the next value above for ids behind it), four tokens at a time; a
+// warp's tile that lies below all of several tokens is passed over (512 fp32 rows, eight
+// tokens of the 50 likeliest, 5 alternatives: 67 us; eight of the best 64th: 109; with one token
+// the test costs more than it saves, 63 us for 60).
 // Alternatives: elements that reach tau, a lower bound of the k-th best, go to a list
 // of ids in shared memory.  The first tile gives tau: of the maxima of groups of four
 // threads the k-th largest is a bound that k elements reach.  Now and then tau becomes the k-th best of
@@ -17,12 +20,13 @@
 // id), all different.  The tiles go by without a barrier.
 // A row is split over the CTAs of a cluster, which push their results into the shared
 // memory of its first one: no workspace, no second launch.
-// Bound by the issue of instructions: 21 a logit with a rank and alternatives, 11 for
-// the sums alone.  Measured (graph replay): 512 fp32 rows of 151936, one token, 5
-// alternatives 61.7 us (75 % of a measured copy's rate; 50 us without rank and
-// alternatives); one row with 20 alternatives 8.1 us; 64 bf16 rows of 128256 with 8
-// tokens and 8 alternatives 19.5 us (the chain of a CTA's four tiles, bootstrap, list, cluster and
-// join).  Measured and not kept: a barrier and a count of candidates a tile (118 us
+// Bound by the issue of instructions: 19 a logit with a rank and alternatives, 11 for
+// the sums alone.  Measured (calls in a row): 512 fp32 rows of 151936, one token, 5
+// alternatives 59.7 us (77 % of a measured copy's rate; 50.5 us without rank and
+// alternatives); one row with 20 alternatives 8.0 us; 64 bf16 rows of 128256 with 8
+// tokens and 8 alternatives 19.1 us (the chain of a CTA's four tiles, bootstrap, list, cluster and
+// join).  Measured and not kept: ranks counted in integers (comparisons and integer adds share a pipe of half
+// rate: 512 rows with eight tokens 149 us); a barrier and a count of candidates a tile (118 us
 // for 65), a candidate's logit picked from registers (70 with 20 alternatives for
 // 63), sums that clamp only where a tile holds -inf (60 us for the sums alone: registers), three
 // CTAs an SM without spills (69).
@@ -127,10 +131,6 @@ __device__ __forceinline__ float key_value(uint64_t k) {
     const uint32_t u = (uint32_t)(k >> 32);
     return __uint_as_float(u & 0x80000000u ? u & 0x7FFFFFFFu : ~u);
 }
-template <int N>
-struct Int {
-    static constexpr int value = N;
-};
 // The next value above x of T's (-0 is 0; NaN above +inf).
 template <typename T>
 __device__ __forceinline__ float next_above(float x) {
@@ -138,9 +138,9 @@ __device__ __forceinline__ float next_above(float x) {
     const int u = __float_as_int(x + 0.f);
     return __int_as_float(u >= 0 ? u + STEP : u - STEP);
 }
-__device__ __forceinline__ int minus_if_ge(float x, float y) {  // x >= y ? -1 : 0
-    int r;
-    asm("set.ge.s32.f32 %0, %1, %2;" : "=r"(r) : "f"(x), "f"(y));
+__device__ __forceinline__ float one_if_ge(float x, float y) {  // x >= y ? 1 : 0
+    float r;
+    asm("set.ge.f32.f32 %0, %1, %2;" : "=f"(r) : "f"(x), "f"(y));
     return r;
 }
 // Keys of list[0 .. n) above `mine`; list is 16-byte aligned and list[n] is 0 where n is odd.
@@ -466,83 +466,96 @@ __global__ void __launch_bounds__(NT, 1024 / NT) logprobs_kernel(dflash_logprobs
             }
             lowest = -warp_max(my_id < 0 ? -INFINITY : -my_xt);
         }
-        if (a.ranks && __any_sync(0xffffffffu, tm >= lowest)) {
-            // (the extra tile of single tokens has ids on both sides of any token)
-            const bool single = it == sl.full;
+        if (a.ranks && (a.n == 1 || __any_sync(0xffffffffu, tm >= lowest))) {
             const int first = sl.first_id(it);
-            // this thread's elements as large as `least`, added to n
-            auto add_ahead = [&](int& n, float least) {
+            // lane i's count of ahead += the warp's
+            auto credit = [&](int i, int n) { my_ahead += lane == i ? n : 0; };
+            // this thread's elements as large as least(j), j their vector (counted in floating point: comparisons have their pipe to
+            // themselves)
+            auto as_large = [&](auto&& least) {
                 if constexpr (sizeof(T) == 4) {
+                    uint64_t n2[2] = {0ull, 0ull};
 #pragma unroll
-                    for (int e = 0; e < E; e += 2) n -= minus_if_ge(x[e], least) + minus_if_ge(x[e + 1], least);
+                    for (int j = 0; j < NV; ++j) {
+                        const float y = least(j);
+#pragma unroll
+                        for (int e = 0; e < G; e += 2)
+                            n2[e >> 1] = add2(n2[e >> 1], pack2(one_if_ge(x[j * G + e], y), one_if_ge(x[j * G + e + 1], y)));
+                    }
+                    float lo, hi;
+                    unpack2(add2(n2[0], n2[1]), lo, hi);
+                    return __float2int_rn(lo + hi);
                 } else {
                     // (0 or 1 in bf16: sums up to 256 are exact)
-                    const __nv_bfloat162 l2 = __float2bfloat162_rn(least);
                     __nv_bfloat162 n2[2] = {__float2bfloat162_rn(0.f), __float2bfloat162_rn(0.f)};
 #pragma unroll
                     for (int j = 0; j < NV; ++j) {
+                        const __nv_bfloat162 y = __float2bfloat162_rn(least(j));
                         const uint32_t w[4] = {raw[j].x, raw[j].y, raw[j].z, raw[j].w};
 #pragma unroll
                         for (int k = 0; k < 4; ++k)
-                            n2[k & 1] = __hadd2(n2[k & 1], __hge2(*reinterpret_cast<const __nv_bfloat162*>(&w[k]), l2));
+                            n2[k & 1] = __hadd2(n2[k & 1], __hge2(*reinterpret_cast<const __nv_bfloat162*>(&w[k]), y));
                     }
                     n2[0] = __hadd2(n2[0], n2[1]);
-                    n += __float2int_rn(__low2float(n2[0]) + __high2float(n2[0]));
+                    return __float2int_rn(__low2float(n2[0]) + __high2float(n2[0]));
                 }
             };
-            // tokens q .. q + Q - 1: the warp's counts to their lanes
-            auto count = [&](int q, float my_least, auto Qc) {
-                constexpr int Q = decltype(Qc)::value;
-                uint32_t n[(Q + 1) / 2];  // two tokens' counts each
-#pragma unroll
-                for (int i = 0; i < (Q + 1) / 2; ++i) n[i] = 0;
-#pragma unroll
-                for (int i = 0; i < Q; ++i) {
-                    const float least = __shfl_sync(0xffffffffu, my_least, q + i);
-                    int mine = 0;
-                    add_ahead(mine, least);
-                    n[i / 2] += (uint32_t)mine << 16 * (i & 1);
+            if (it == sl.full) {  // single tokens: ids on both sides of any
+                const int id = sl.id(it, 0);
+                for (int i = 0; i < a.n; ++i) {
+                    const float xt = __shfl_sync(0xffffffffu, my_xt, i);
+                    const int at = __shfl_sync(0xffffffffu, my_id, i);
+                    credit(i, __popc(__ballot_sync(0xffffffffu, x[0] > xt || (x[0] == xt && id < at))));
                 }
-#pragma unroll
-                for (int i = 0; i < (Q + 1) / 2; ++i) n[i] = __reduce_add_sync(0xffffffffu, n[i]);
-#pragma unroll
-                for (int i = 0; i < Q; ++i)
-                    if (lane == q + i) my_ahead += (int)(n[i / 2] >> 16 * (i & 1) & 0xFFFFu);
-            };
-            // The tile that holds a token (or single tokens) has ids on both sides of it: those before it of the same logit.  And
-            // elements that are none, which are -inf, have been counted as large as a token at -inf behind them.
-            auto ties = [&](int at, float xt) {
-                int n = 0;
-#pragma unroll
-                for (int j = 0; j < NV; ++j) {
-                    const int id = !single && sl.v0 + (it * NV + j) * NT + tid >= sl.v1 ? NOWHERE : sl.id(it, j * G);
-                    if (!single && at >= first + NT * E) {
-                        if (id == NOWHERE) n -= G;
-                    } else {
-#pragma unroll
-                        for (int e = 0; e < G; ++e) n += x[j * G + e] == xt && id + e < at && (e == 0 || !single);
-                    }
-                }
-                return n;
-            };
-            const bool before = !single && my_id >= first + NT * E;  // lane's token lies behind the tile
-            const bool here = single ? my_id >= 0 : (unsigned)(my_id - first) < (unsigned)(NT * E),
-                       extra = before && it >= sl.whole && my_xt == -INFINITY;
-            const float my_least = before ? my_xt : next_above<T>(my_xt);
-            if (a.n == 1) {
-                // (every lane holds the one token; its counts are joined at the end)
-                add_ahead(my_ahead, my_least);
-                if (here || extra) my_ahead += ties(my_id, my_xt);
             } else {
-                int q = 0;
+                const bool before = my_id >= first + NT * E;  // lane's token lies behind the tile
+                // A token in the tile has ids on both sides; and elements that are none, -inf, are not as large as a token at -inf
+                // behind them.
+                const bool mixed = (unsigned)(my_id - first) < (unsigned)(NT * E) || (before && it >= sl.whole && my_xt == -INFINITY);
+                const float my_least = before ? my_xt : next_above<T>(my_xt);
+                // the same of the token at `at` by vectors: each lies before it, behind it or holds it
+                auto of_mixed = [&](int at, float xt) {
+                    constexpr int STEP = NT * G;  // ids from a thread's vector to its next
+                    const float above = next_above<T>(xt);
+                    const int t = at - first - tid * G;
+                    int n = as_large([&](int j) { return t >= j * STEP + G ? xt : above; });
+                    if ((t & (STEP - 1)) < G && (unsigned)t < NV * STEP) {
+#pragma unroll
+                        for (int j = 0; j < NV; ++j)
+#pragma unroll
+                            for (int e = 0; e < G; ++e) n += t > j * STEP + e && t < j * STEP + G && x[j * G + e] == xt;
+                    }
+                    if (it >= sl.whole && xt == -INFINITY) {
+#pragma unroll
+                        for (int j = 0; j < NV; ++j)
+                            if (t >= j * STEP + G && sl.v0 + (it * NV + j) * NT + tid >= sl.v1) n -= G;
+                    }
+                    return n;
+                };
+                if (a.n == 1) {  // (every lane holds the one token; its counts are joined at the end)
+                    my_ahead += mixed ? of_mixed(my_id, my_xt) : as_large([&](int) { return my_least; });
+                } else {
+                    const uint32_t some = __ballot_sync(0xffffffffu, mixed);
 #pragma unroll 1
-                for (; q + 4 <= a.n; q += 4) count(q, my_least, Int<4>());
-#pragma unroll 1
-                for (; q < a.n; ++q) count(q, my_least, Int<1>());
-                for (uint32_t w = __ballot_sync(0xffffffffu, here || extra); w; w &= w - 1) {
-                    const int i = __ffs(w) - 1;
-                    const int n = __reduce_add_sync(0xffffffffu, ties(__shfl_sync(0xffffffffu, my_id, i), __shfl_sync(0xffffffffu, my_xt, i)));
-                    if (lane == i) my_ahead += n;
+                    for (int q = 0; q < a.n;) {
+                        if (q + 4 > a.n || some >> q & 15u) {
+                            const int n = of_mixed(__shfl_sync(0xffffffffu, my_id, q), __shfl_sync(0xffffffffu, my_xt, q));
+                            credit(q, __reduce_add_sync(0xffffffffu, n));
+                            ++q;
+                            continue;
+                        }
+                        uint32_t n[2] = {0u, 0u};  // two tokens' counts each
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const float least = __shfl_sync(0xffffffffu, my_least, q + i);
+                            n[i / 2] += (uint32_t)as_large([&](int) { return least; }) << 16 * (i & 1);
+                        }
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) n[i] = __reduce_add_sync(0xffffffffu, n[i]);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) credit(q + i, (int)(n[i / 2] >> 16 * (i & 1) & 0xFFFFu));
+                        q += 4;
+                    }
                 }
             }
         }
