@@ -528,7 +528,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) logprobs_kernel(dflash_logprobs
                     if (it >= sl.whole && xt == -INFINITY) {
 #pragma unroll
                         for (int j = 0; j < NV; ++j)
-                            if (t >= j * STEP + G && sl.v0 + (it * NV + j) * NT + tid >= sl.v1) n -= G;
+                            if (sl.v0 + (it * NV + j) * NT + tid >= sl.v1) n -= min(max(t - j * STEP, 0), G);
                     }
                     return n;
                 };

@@ -348,3 +348,26 @@ def test_parts_of_lse_make_lse():
         dfl().token_logprobs(x.cuda(), i32(t), lse_parts=torch.empty((4, 1), device="cuda"))
     with pytest.raises(ValueError, match="lse_parts"):
         dfl().token_logprobs_grad(x.cuda(), i32(t), torch.empty((4, 3), device="cuda"), f.logprobs)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("n", [1, 4, 7])
+@pytest.mark.parametrize("vocab", [30, 157, 4099, 9001])
+def test_ranks_of_masked_tokens_anywhere(dtype, n, vocab):
+    """Tokens at -inf before the first aligned vector, behind the last one and at the ends of the CTAs' slices, behind elements
+    that are none."""
+    for offset in (0, 1, 5):
+        x = torch.full((vocab, vocab + 9), float("-inf"))
+        x[:, :vocab] = rows_of("f32", vocab, vocab, seed=vocab)
+        x[torch.rand(x.shape, generator=torch.Generator().manual_seed(offset)) < 0.9] = float("-inf")
+        x = x[:min(vocab, 200)].to(DT[dtype])
+        rows = len(x)
+        t = np.random.default_rng(n).integers(0, vocab, (rows, n))
+        t[:, 0] = vocab - 1 - np.arange(rows) % min(vocab, 9)
+        t[:, -1] = np.arange(rows) % vocab
+        y = torch.empty(rows * (vocab + 9) + 5, dtype=DT[dtype], device="cuda")[offset:offset + rows * (vocab + 9)].view(rows, vocab + 9)
+        y.copy_(x)
+        got = dfl().token_logprobs(y[:, :vocab], i32(t))
+        z, ids = host(x.float())[:, None, :vocab], np.arange(vocab)
+        xt = np.take_along_axis(z[:, 0], t, 1)[:, :, None]
+        np.testing.assert_array_equal(host(got.ranks), ((z > xt) | ((z == xt) & (ids < t[:, :, None]))).sum(2))
