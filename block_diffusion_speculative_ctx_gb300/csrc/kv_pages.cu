@@ -14,7 +14,8 @@
 // Release: one launch of one cluster, whose barriers separate the steps.
 //   1  every page named is looked at (range, count);
 //   2  its count falls by one for each mention: a page without a holder ends at -1
-//      (below: it was returned too often, and the counts go back);
+//      (below: it was returned too often, and the counts go back); with cuts, the counts
+//      left on the pages that they end in tell whether another holder stays;
 //   3  of a page's mentions the first takes it: an atomic minimum over the
 //      mentions' numbers, kept in the count itself as INT_MIN + number (left out
 //      where no page named had a second holder);
@@ -23,7 +24,7 @@
 // Mentions are numbered (place in seqs, table entry) and a warp owns consecutive
 // ones, so the list's order does not depend on the order of the atomics.  Bound by
 // latency: seven to nine dependent trips to L2 and as many barriers; 6.1 us for four
-// sequences of nine pages.
+// sequences of nine pages (with cuts a barrier and a trip more).
 #include <algorithm>
 
 #include "ops.h"
@@ -34,7 +35,7 @@ namespace dfl {
 namespace {
 
 constexpr int MAXB = DFLASH_OPS_MAX_BATCH;
-enum : int { SHORT_POOL = 1, BAD_WIDTH = 2, BAD_LENGTH = 8, BAD_PAGE = 16, BAD_COUNT = 32 };
+enum : int { SHORT_POOL = 1, BAD_WIDTH = 2, BAD_LENGTH = 8, BAD_PAGE = 16, BAD_COUNT = 32, SHARED_CUT = 64 };
 
 // ------------------------------------------------------------------------------ fork
 constexpr int NT = 512, PER = MAXB / NT;
@@ -197,11 +198,13 @@ __global__ void __launch_bounds__(NR) kv_release_kernel(dflash_kv_release_args a
     __syncthreads();
 
     // ---- the sequences, by every CTA: thread t owns 2 t and 2 t + 1
-    int bad = 0, mine[2];
+    int bad = 0, mine[2], cut[2];  // (cut: the page that a cut ends inside)
+    bool out = false;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
         const int k = 2 * tid + i;
         mine[i] = 0;
+        cut[i] = -1;
         if (k < a.n) {
             const int s = a.seqs[k];
             int pages = 0, first = 0;
@@ -211,7 +214,13 @@ __global__ void __launch_bounds__(NR) kv_release_kernel(dflash_kv_release_args a
                 const int kv = a.kv_lens[s], keep = a.keep_lens ? a.keep_lens[s] : 0;
                 if (kv < 0 || keep < 0 || keep > kv) bad |= BAD_LENGTH;
                 else if (kv > (long long)64 * a.width) bad |= BAD_WIDTH;
-                else pages = (kv + 63) >> 6, first = (keep + 63) >> 6;
+                else {
+                    pages = (kv + 63) >> 6, first = (keep + 63) >> 6;
+                    if (rank == 0 && keep < kv && keep & 63) {
+                        cut[i] = a.table[(long long)s * a.ld_table + (keep >> 6)];
+                        out |= cut[i] < 0 || cut[i] >= a.n_pages || ld_count(&a.refs[cut[i]]) < 0;
+                    }
+                }
             }
             seq_s[k] = s;
             first_s[k] = first;
@@ -289,12 +298,11 @@ __global__ void __launch_bounds__(NR) kv_release_kernel(dflash_kv_release_args a
 
     int freed = 0;
     if (status == 0) {  // (every CTA found the same)
-        bool out = false;
         mentions([&](int page, int, bool live) { out |= live && (page < 0 || page >= a.n_pages || ld_count(&a.refs[page]) < 0); });
         if (any(out)) status = BAD_PAGE;
     }
     if (status == 0) {
-        enum { OVER = 1, SHARED = 2 };  // a count below what its page had; a page that several mentions free
+        enum { OVER = 1, SHARED = 2, CUT = 4 };  // a count below what its page had; a page that several mentions free; a cut's with others
         int seen = 0;
         mentions([&](int page, int, bool live) {
             if (!live) return;
@@ -303,8 +311,17 @@ __global__ void __launch_bounds__(NR) kv_release_kernel(dflash_kv_release_args a
             if (before > 0) seen |= SHARED;  // (it may yet be freed by others)
         });
         seen = any(seen);
-        if (seen & OVER) {
-            status = BAD_COUNT;
+        if (a.keep_lens && !(seen & OVER)) {  // (a cut's own sequence stays, so its page's count may not fall below 0 either)
+            int left = 0;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int c = cut[i] < 0 ? 0 : ld_count(&a.refs[cut[i]]);
+                left |= c < 0 ? OVER : c > 0 ? CUT : 0;
+            }
+            seen |= any(left);
+        }
+        if (seen & (OVER | CUT)) {
+            status = seen & OVER ? BAD_COUNT : SHARED_CUT;
         } else {
             // which of a page's mentions takes it (a page that had no other holder has one)
             if (seen & SHARED) {

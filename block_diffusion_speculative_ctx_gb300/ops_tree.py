@@ -294,7 +294,8 @@ def kv_release(seqs, kv_lens, table, free_pages, used, refs, *, keep_lens=None, 
     kv_lens are the lengths with the trees and keep_lens ``kv_compact``'s.  ``used_out=used``
     works in place.  ``status`` stays on the device: 0, or a sum of 1 (more pages return than were taken), 2 (table
     too narrow), 8 (a bad length, used or sequence, or one named twice), 16 (a bad page), 32 (a page returned by
-    more sequences than hold it): nothing has changed."""
+    more sequences than hold it), 64 (a cut ends inside a page that others hold, which the next token would be written
+    to: fork the sequence at the shorter length instead, and end it): nothing has changed."""
     dev = _device(seqs)
     n, batch = _batch("seqs", seqs), _batch("kv_lens", kv_lens)
     ld_table = _ops._mat("table", table, _I32T, batch, None, dev)

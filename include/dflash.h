@@ -831,12 +831,15 @@ dflash_status dflash_kv_fork(const dflash_kv_fork_args* args, void* cuda_stream)
  * a step whose tree grew past a page and was cut behind it, kv_lens are the
  * lengths with the tree and keep_lens dflash_kv_compact's kv_out (dflash_kv_tables
  * takes new pages behind ceil(kv / 64), whatever the table holds there).  The page that
- * a cut ends in is written to next: it may have no other holder.
+ * a cut ends inside (keep_lens[s] below kv_lens[s] and not a multiple of 64) is written to
+ * next: behind the call it may have no other holder.  A sequence whose cut meets a shared
+ * page can fork itself at the shorter length (dflash_kv_fork copies the page) and end.
  * status (device): 0, or a sum of 1 (more pages return than were taken), 2 (a
  * length above 64 * width), 8 (a negative length, keep_lens outside [0, kv_lens], a
  * *used outside [0, n_free], or a
  * sequence outside [0, batch) or named twice), 16 (a page outside [0, n_pages)
- * or with negative refs), 32 (a page returned by more sequences than hold it).
+ * or with negative refs), 32 (a page returned by more sequences than hold it), 64 (a
+ * cut ends inside a page that others hold).
  * When not 0, nothing changes and used_out = *used.
  * used_out may be used.  Errors: E_INVAL (sizes, NULL), E_CUDA. */
 typedef struct {

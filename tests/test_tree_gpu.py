@@ -743,3 +743,75 @@ def test_the_operators_on_a_side_stream_beside_others():
     torch.cuda.synchronize()
     for i, (o, l) in got:
         assert torch.equal(o, want[i][0]) and torch.equal(l, want[i][1])
+
+
+def cut_case(kind, many):
+    """Pages 0 and 1 hold 128 tokens of sequences 0 and 1, which have a page of their own each behind them; 2 is alone."""
+    kv, keep, seqs = [200, 200, 130], [200, 100, 70], [1]
+    table, refs, status = [[0, 1, 2, 3], [0, 1, 4, 5], [6, 7, 8, 9]], np.zeros(10, int), 64
+    refs[:2] = 1
+    if kind == "last page":         # nothing is given back, and the page is written to all the same
+        kv, keep = [128, 128, 130], [128, 100, 70]
+    elif kind == "both":
+        keep, seqs = [120, 100, 70], [0, 1]
+    elif kind == "first page":
+        keep = [200, 63, 70]
+    elif kind == "whole pages":     # a new page is written to next
+        keep, status = [200, 64, 70], 0
+    elif kind == "nothing left":
+        keep, status = [200, 0, 70], 0
+    elif kind == "no cut":
+        kv, keep, status = [100, 100, 130], [100, 100, 70], 0
+    elif kind == "others end":      # the other holder leaves in the same call
+        keep, seqs, status = [0, 100, 70], [0, 1], 0
+    elif kind == "alone":
+        seqs, status = [2], 0
+    elif kind == "held by fewer":   # page 1 is sequence 1's alone, and another gives it back
+        refs[1], keep, seqs, status = 0, [0, 100, 70], [0, 1], 32
+    elif kind == "bad page":
+        table[2][1], seqs, status = 10, [2], 16
+    elif kind == "bad count":
+        refs[7], seqs, status = -1, [2], 16
+    if many:  # hundreds of others end with it: a cluster of eight CTAs
+        n = 400
+        table += (10 + np.arange(4 * n).reshape(n, 4)).tolist()
+        kv, keep, seqs = kv + [250] * n, keep + [0] * n, list(range(3, 3 + n)) + seqs
+        refs = np.concatenate([refs, np.zeros(4 * n, int)])
+        table = [[p if kind != "bad page" or p != 10 or s != 2 else len(refs) for p in row] for s, row in enumerate(table)]
+    free = np.arange(len(refs), len(refs) + len(refs) + 4)
+    return kv, keep, seqs, np.array(table), refs, free, status
+
+
+@pytest.mark.parametrize("many", [False, True])
+@pytest.mark.parametrize("kind", ["shared", "last page", "both", "first page", "whole pages", "nothing left", "no cut", "others end", "alone",
+                                  "held by fewer", "bad page", "bad count"])
+def test_kv_release_refuses_a_cut_into_a_page_that_others_hold(kind, many):
+    """The page that a cut ends in is written to next: with another holder left the call says so and changes nothing."""
+    kv, keep, seqs, table, refs, free, status = cut_case(kind, many)
+    used = len(refs)
+    fl, u, rf = i32(free), i32([used]), i32(refs)
+    r = dfl().kv_release(i32(seqs), i32(kv), i32(table), fl, u, rf, keep_lens=i32(keep), used_out=u)
+    assert int(r.status) == status
+    if status == 0:
+        free, used, refs, _ = trees.kv_release(seqs, kv, table, free, used, refs, keep)
+    assert int(u) == used
+    np.testing.assert_array_equal(host(fl), free)
+    np.testing.assert_array_equal(host(rf), refs)
+
+
+def test_a_fork_that_is_cut_back_takes_a_page_of_its_own():
+    """What a caller does instead: the sequence forks itself at the shorter length, which copies the page, and ends."""
+    rng = np.random.default_rng(31)
+    f = fork_state(rng, [128])
+    fl, used, refs = i32(f["spare"]), i32([0]), i32(f["refs"])
+    k, v, table = f["k"], f["v"], i32(f["table"])
+    kid = dfl().kv_fork(i32([0]), i32([128]), table, fl, used, refs, k, v, scratch_page=f["scratch"], used_out=used)
+    cut = dfl().kv_release(i32([0]), kid.kv_lens, kid.table, fl, used, refs, keep_lens=i32([100]), used_out=used)
+    assert int(cut.status) == 64 and int(used) == 0
+    short = dfl().kv_fork(i32([0]), i32([100]), kid.table, fl, used, refs, k, v, scratch_page=f["scratch"], used_out=used)
+    end = dfl().kv_release(i32([0]), kid.kv_lens, kid.table, fl, used, refs, used_out=used)
+    assert int(short.status) == int(end.status) == 0 and int(used) == 1
+    pages, parent = host(short.table)[0], f["table"][0]
+    assert pages[0] == parent[0] and pages[1] == f["spare"][0]
+    assert host(refs)[parent[0]] == 1 and host(refs)[parent[1]] == 0 and host(refs)[pages[1]] == 0
+    assert torch.equal(k[:, pages[1], :, :36], k[:, parent[1], :, :36])
