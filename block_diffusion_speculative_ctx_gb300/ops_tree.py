@@ -289,13 +289,14 @@ def kv_release(seqs, kv_lens, table, free_pages, used, refs, *, keep_lens=None, 
     """The pages of ended or shortened sequences back to the free list (``dflash_kv_release``).
 
     seqs: int32 [n], the sequences that end; kv_lens, table: int32 [batch] and [batch, width]; free_pages, used, refs:
-    as ``kv_fork``, free_pages and refs changed in place.  A page returns when its last holder leaves.  With keep_lens
-    (int32 [batch]) the sequences live on with so many tokens and give back the pages behind them: after a step of trees,
-    kv_lens are the lengths with the trees and keep_lens ``kv_compact``'s.  ``used_out=used``
-    works in place.  ``status`` stays on the device: 0, or a sum of 1 (more pages return than were taken), 2 (table
-    too narrow), 8 (a bad length, used or sequence, or one named twice), 16 (a bad page), 32 (a page returned by
-    more sequences than hold it), 64 (a cut ends inside a page that others hold, which the next token would be written
-    to: fork the sequence at the shorter length instead, and end it): nothing has changed."""
+    as ``kv_fork``, free_pages and refs changed in place.  A page returns when its last holder leaves.  A sequence ends
+    once: the counts do not tell free pages from held ones, and a later call that names it again puts its pages into
+    the list twice.  With keep_lens (int32 [batch]) the sequences live on with so many tokens and give back the pages
+    behind them: after a step of trees, kv_lens are the lengths with the trees and keep_lens ``kv_compact``'s.
+    ``used_out=used`` works in place.  ``status`` stays on the device: 0, or a sum of 1 (more pages return than were
+    taken), 2 (table too narrow), 8 (a bad length, used or sequence, or one named twice), 16 (a bad page), 32 (a page
+    returned by more sequences of this call than hold it), 64 (a cut ends inside a page that others hold, which the next
+    token would be written to: fork the sequence at the shorter length instead, and end it): nothing has changed."""
     dev = _device(seqs)
     n, batch = _batch("seqs", seqs), _batch("kv_lens", kv_lens)
     ld_table = _ops._mat("table", table, _I32T, batch, None, dev)

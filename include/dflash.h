@@ -771,7 +771,8 @@ dflash_status dflash_kv_compact(const dflash_kv_compact_args* args, void* cuda_s
  * refs[p] counts the holders of page p beyond its first: 0 for a free page and
  * for one that a single sequence holds, so pages that dflash_kv_tables hands
  * out need nothing.  The free list is dflash_kv_tables': entries 0 .. *used - 1
- * are taken. */
+ * are taken.  The counts do not say whether a page is free: that the sequences named
+ * hold their pages is the caller's to keep. */
 
 /* Sequences that continue others.  Child c continues sequence parents[c] (any
  * number of children a parent) with n = kv_lens[parents[c]] tokens:
@@ -825,7 +826,10 @@ dflash_status dflash_kv_fork(const dflash_kv_fork_args* args, void* cuda_stream)
  * free_pages[used_out .. *used - 1] in the order of their first mention (seqs in
  * order, then table entries): a release right behind the call that took the pages
  * restores the list.  The tables and lengths of the sequences are the caller's to
- * forget.
+ * forget: a sequence ends once.  Of the mentions of one call too many are reported (32),
+ * but a later call that names an ended sequence again is taken at its word, and its pages,
+ * free or another's by then, go into the list a second time (or, where fewer pages
+ * are taken than it returns, status 1).
  * With keep_lens a sequence s lives on with its first keep_lens[s] tokens and
  * gives back the pages behind them, entries ceil(keep_lens[s] / 64) and on: after
  * a step whose tree grew past a page and was cut behind it, kv_lens are the
@@ -838,7 +842,7 @@ dflash_status dflash_kv_fork(const dflash_kv_fork_args* args, void* cuda_stream)
  * length above 64 * width), 8 (a negative length, keep_lens outside [0, kv_lens], a
  * *used outside [0, n_free], or a
  * sequence outside [0, batch) or named twice), 16 (a page outside [0, n_pages)
- * or with negative refs), 32 (a page returned by more sequences than hold it), 64 (a
+ * or with negative refs), 32 (a page returned by more sequences of the call than hold it), 64 (a
  * cut ends inside a page that others hold).
  * When not 0, nothing changes and used_out = *used.
  * used_out may be used.  Errors: E_INVAL (sizes, NULL), E_CUDA. */

@@ -815,3 +815,13 @@ def test_a_fork_that_is_cut_back_takes_a_page_of_its_own():
     assert pages[0] == parent[0] and pages[1] == f["spare"][0]
     assert host(refs)[parent[0]] == 1 and host(refs)[parent[1]] == 0 and host(refs)[pages[1]] == 0
     assert torch.equal(k[:, pages[1], :, :36], k[:, parent[1], :, :36])
+
+
+def test_a_sequence_ends_once():
+    """The counts know holders beyond the first, not whether a page is free: a call after the one that ended a sequence cannot tell
+    that it names the same one, and takes the pages again, or finds more of them than were taken."""
+    table, kv = i32([[0, 1], [2, 3]]), i32([100, 100])
+    fl, used, refs = i32([0, 1, 2, 3]), i32([4]), i32([0] * 4)
+    for status, left, want in ((0, 2, [0, 1, 0, 1]), (0, 0, [0, 1, 0, 1]), (1, 0, [0, 1, 0, 1])):
+        r = dfl().kv_release(i32([0]), kv, table, fl, used, refs, used_out=used)
+        assert int(r.status) == status and int(used) == left and host(fl).tolist() == want and (host(refs) == 0).all()
