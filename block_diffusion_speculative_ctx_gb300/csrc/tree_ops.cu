@@ -52,9 +52,12 @@ __global__ void __launch_bounds__(NT_MASK) tree_masks_kernel(dflash_tree_masks_a
             bad |= p < -1 || p >= j;
         }
     if (__syncthreads_or(bad)) status |= BAD_TREE;
-    if (tid == 0) a.status[s] = status;
+    // the root's position, and the largest that m nodes can have
+    const int kv = a.row_pos ? a.kv_lens[s] : m;
+    const long long base = (long long)a.base_pos + kv - m;
+    const bool placed = kv >= 0 && base >= 0 && base + m <= 1ll << 31;
+    if (tid == 0) a.status[s] = status & BAD_ROWS || placed ? status : status | BAD_LENGTH;
     if (status & BAD_ROWS) return;
-    const int base = a.row_pos ? a.base_pos + a.kv_lens[s] - m : 0;
     for (int j = tid; j < m; j += NT_MASK) {
         uint32_t* out = a.masks + (long long)(start + j) * a.ld_mask;
         int at = a.words - 1, depth = -1;  // word that is written next
@@ -74,7 +77,7 @@ __global__ void __launch_bounds__(NT_MASK) tree_masks_kernel(dflash_tree_masks_a
             w = 0;
         }
         if (a.depth) a.depth[start + j] = depth;
-        if (a.row_pos) a.row_pos[start + j] = depth < 0 ? -1 : base + depth;
+        if (a.row_pos) a.row_pos[start + j] = depth < 0 || !placed ? -1 : (int)(base + depth);
     }
 }
 

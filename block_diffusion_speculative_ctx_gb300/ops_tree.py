@@ -115,7 +115,8 @@ def tree_masks(parents, q_start, *, kv_lens=None, base_pos: int = 0, words: Opti
     the rows of the whole batch need: give the widest tree's ceil(m / 32).  ``depth``: int32 [rows].  With
     kv_lens (int32 [batch], own keys, the tree's among them) ``row_pos`` is base_pos + kv_lens - m + depth.
     Missing outputs are allocated (0 in rows of no tree).  ``status``: int32 [batch] on the device, 0 or a sum of
-    1 (a parent not before its child), 2 (too many nodes), 4 (bad q_start)."""
+    1 (a parent not before its child), 2 (too many nodes), 4 (bad q_start), 8 (a length whose positions are below 0
+    or beyond int32: row_pos is -1, masks and depth are as they should be)."""
     dev = _device(parents)
     rows, batch = parents.numel(), _batch("q_start", q_start, 1)
     if masks is None:
@@ -196,8 +197,8 @@ def tree_accept(parents, tokens, posterior, q_start, *, width: Optional[int] = N
     parents, tokens, posterior: int32 [rows], a node's parent in its tree, its drafted token and the target's
     choice behind it; q_start: int32 [batch + 1].  ``path``: int32 [batch, width], the nodes kept from the root
     on (-1 behind them; at most ``width``); ``accepted``: int32 [batch], the drafts among them (-1 for a sequence
-    without rows); ``bonus``: int32 [batch], the target's choice behind the last.  ``status``: int32 [batch], as
-    ``tree_masks``."""
+    without rows); ``bonus``: int32 [batch], the target's choice behind the last.  ``status``: int32 [batch], 1,
+    2 or 4 as ``tree_masks``: a bad tree has accepted = bonus = -1 and a path of -1."""
     dev = _device(parents)
     rows, batch = parents.numel(), _batch("q_start", q_start, 1)
     if path is None:

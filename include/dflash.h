@@ -663,11 +663,16 @@ enum { DFLASH_TREE_MAX_NODES = 1024 };
  *                its ancestors i, `words` words; the others 0
  *   depth[r]   = links between node r and its root
  *   row_pos[r] = base_pos + kv_lens[s] - m + depth[r]
- * parents[r] is the parent's number in its tree or -1 (a root).
+ * parents[r] is the parent's number in its tree or -1 (a root).  A kv_lens[s] below
+ * m means that the first m - kv_lens[s] nodes lie before the sequence's first own key:
+ * dflash_tree_attention takes such a length (they have no key), and here their positions are
+ * below base_pos, which has to leave room for them.
  * status[s] (device): 0, or a sum of 1 (a parent that does not come before its
  * child, or below -1), 2 (more nodes than 32 * words or than
- * DFLASH_TREE_MAX_NODES), 4 (q_start decreases or leaves [0, rows]).  With 1 or
- * 2 the sequence's rows get masks 0, depth -1 and row_pos -1, with 4 nothing
+ * DFLASH_TREE_MAX_NODES), 4 (q_start decreases or leaves [0, rows]), 8 (with row_pos: a
+ * negative kv_lens[s], base_pos + kv_lens[s] - m < 0 or base_pos + kv_lens[s] > 2^31).
+ * With 1 or 2 the sequence's rows get masks 0, depth -1 and row_pos -1, with 8 alone
+ * a row_pos of -1 beside their masks and depths, with 4 nothing
  * of it is written.  Rows of no sequence are left as they were.
  * Errors: E_INVAL (sizes, NULL), E_CUDA. */
 typedef struct {
@@ -713,8 +718,8 @@ dflash_status dflash_tree_attention(const dflash_tree_attention_args* args, void
  * parents, tokens, posterior: per row, the parent's number in the tree (-1: a
  * root), the drafted token, the target's choice behind the row.  A sequence
  * without rows gets accepted = bonus = -1 and a path of -1.
- * status[s] (device): as dflash_tree_masks (2: more than
- * DFLASH_TREE_MAX_NODES nodes); when not 0, accepted = bonus = -1, path -1.
+ * status[s] (device): 1, 2 (more than DFLASH_TREE_MAX_NODES nodes) or 4, as
+ * dflash_tree_masks; when not 0, accepted = bonus = -1, path -1.
  * Errors: E_INVAL (sizes, NULL), E_CUDA. */
 typedef struct {
     int32_t batch;

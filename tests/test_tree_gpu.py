@@ -825,3 +825,25 @@ def test_a_sequence_ends_once():
     for status, left, want in ((0, 2, [0, 1, 0, 1]), (0, 0, [0, 1, 0, 1]), (1, 0, [0, 1, 0, 1])):
         r = dfl().kv_release(i32([0]), kv, table, fl, used, refs, used_out=used)
         assert int(r.status) == status and int(used) == left and host(fl).tolist() == want and (host(refs) == 0).all()
+
+
+@pytest.mark.parametrize("base,kv,m,status,first", [
+    (0, 3, 5, 8, None), (0, -1, 5, 8, None), (17, -1, 5, 8, None), (17, 3, 5, 0, 15), (2, 3, 5, 0, 0), (1, 3, 5, 8, None),
+    (1 << 30, (1 << 31) - 1, 5, 8, None), (1 << 30, (1 << 30) + 1, 5, 8, None), (1 << 30, 1 << 30, 5, 0, (1 << 31) - 5),
+    (0, (1 << 31) - 1, 1, 0, (1 << 31) - 2), (0, -1, 0, 8, None)])
+def test_tree_masks_of_lengths_below_the_tree_and_beyond_a_position(base, kv, m, status, first):
+    """A length below m counts from behind the cache's begin, as in the attention, where base_pos leaves room; masks and depths
+    do not depend on it."""
+    p = random_tree(np.random.default_rng(m), m, 0.9)
+    t = dfl().tree_masks(i32(np.concatenate([p, [-1, 0]])), i32([0, m, m + 2]), kv_lens=i32([kv, 2]), base_pos=base, words=1)
+    assert host(t.status).tolist() == [status, 0]
+    sees, depth = trees.ancestors(p)
+    np.testing.assert_array_equal(host(t.masks)[:m], trees.words(sees, 1))
+    np.testing.assert_array_equal(host(t.depth)[:m], depth)
+    np.testing.assert_array_equal(host(t.row_pos), np.concatenate([first + depth if status == 0 else np.full(m, -1), [base, base + 1]]))
+
+
+def test_tree_masks_report_a_bad_tree_and_its_bad_length():
+    t = dfl().tree_masks(i32([-1, 1]), i32([0, 2]), kv_lens=i32([-4]), words=1)
+    assert host(t.status).tolist() == [9] and host(t.row_pos).tolist() == host(t.depth).tolist() == [-1, -1]
+    assert (host(t.masks) == 0).all()
