@@ -401,6 +401,8 @@ extern "C" dflash_status dflash_kv_fork(const dflash_kv_fork_args* p, void* cuda
                                      "kv_fork: n_pages, n_kv_heads or head_dim out of range (a head's row is a multiple of 16 bytes)",
                                      "kv_fork: the caches must be 16-byte aligned, ld_layer a multiple of 16 bytes and no smaller than a layer"))
         return fail(why);
+    // (one cache for both is copied twice alike)
+    if (a.k_cache != a.v_cache && caches_overlap(a)) return fail("kv_fork: k_cache and v_cache overlap");
     if (a.batch < 1 || a.batch > MAXB) return fail("kv_fork: batch outside [1, 2048]");
     if (a.children < 1 || a.children > MAXB) return fail("kv_fork: children outside [1, 2048]");
     if (a.width < 1 || a.width > (1 << 22) || a.ld_table < a.width || a.ld_out < a.width)

@@ -57,6 +57,20 @@ const char* bad_caches(const A& a, const char* dtype, const char* layers, const 
     return nullptr;
 }
 
+// Whether two such caches (of good sizes) share memory: layer i of one and layer i + j of the other, which may lie between
+// each other.
+template <typename A>
+bool caches_overlap(const A& a) {
+    const long long es = a.dtype == DFLASH_DTYPE_BF16 ? 2 : 4;
+    const long long layer = (long long)a.n_pages * a.n_kv_heads * 64 * a.head_dim * es, between = a.ld_layer * es;
+    const long long apart = (long long)((uintptr_t)a.v_cache - (uintptr_t)a.k_cache);
+    for (long long j = 1 - a.layers; j < a.layers; ++j) {
+        const long long d = apart + j * between;
+        if (d > -layer && d < layer) return true;
+    }
+    return false;
+}
+
 // The entries' argument checks: DFLASH_OK, or E_INVAL with the reason in *why.
 dflash_status check_shared_prefix(const dflash_shared_prefix_args& a, const char** why);
 dflash_status check_logits(const dflash_logits_args& a, const char** why);

@@ -242,6 +242,9 @@ extern "C" dflash_status dflash_kv_compact(const dflash_kv_compact_args* p, void
                                      "kv_compact: n_pages, n_kv_heads or head_dim out of range (a head's row is a multiple of 16 bytes)",
                                      "kv_compact: the caches must be 16-byte aligned, ld_layer a multiple of 16 bytes and no smaller than a layer"))
         return fail(why);
+    // (their tokens would be moved twice)
+    if (a.k_cache == a.v_cache) return fail("kv_compact: v_cache may not be k_cache");
+    if (caches_overlap(a)) return fail("kv_compact: k_cache and v_cache overlap");
     if (a.batch < 1 || a.batch > DFLASH_OPS_MAX_BATCH) return fail("kv_compact: batch outside [1, 2048]");
     if (a.width < 1 || a.width > MAXN) return fail("kv_compact: width outside [1, 1024]");
     if (a.width_table < 0 || a.width_table > (1 << 22) || a.ld_table < a.width_table)
@@ -249,7 +252,6 @@ extern "C" dflash_status dflash_kv_compact(const dflash_kv_compact_args* p, void
     if (!a.kv_lens || !a.q_start || !a.path || !a.accepted || !a.kv_out || !a.status || (a.width_table > 0 && !a.table))
         return fail("kv_compact: NULL argument");
     if (a.kv_out == a.kv_lens) return fail("kv_compact: kv_out may not be kv_lens");
-    if (a.k_cache == a.v_cache) return fail("kv_compact: v_cache may not be k_cache");  // (its tokens would be moved twice)
     const int vecs = a.head_dim * (a.dtype == DFLASH_DTYPE_BF16 ? 2 : 4) / 16;
     return queue(cuda_stream, "kv_compact: launch failed", [&](const Launch& L) {
         launch_k(L, kv_compact_kernel, dim3(a.batch, 2 * a.layers), dim3(NT_MOVE), 0, 1, a, vecs);

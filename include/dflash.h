@@ -748,7 +748,8 @@ dflash_status dflash_tree_accept(const dflash_tree_accept_args* args, void* cuda
  * (kv_lens outside [m, 64 * width_table]), 16 (a page of a moved token outside
  * [0, n_pages)).  When not 0, nothing of the sequence moves and kv_out =
  * kv_lens.  No two sequences may hold the same page among their nodes'.
- * kv_out may not be kv_lens, nor v_cache k_cache.  Errors: E_INVAL (sizes, NULL), E_CUDA. */
+ * kv_out may not be kv_lens, and the layers of v_cache share no memory with those of k_cache
+ * (they may lie between each other).  Errors: E_INVAL (sizes, NULL, caches that overlap), E_CUDA. */
 typedef struct {
     int32_t dtype;             /* F32 or BF16 */
     int32_t batch;
@@ -810,7 +811,7 @@ typedef struct {
     int64_t ld_layer;
     int64_t ld_table;
     int64_t ld_out;
-    void* k_cache;             /* as dflash_kv_compact */
+    void* k_cache;             /* as dflash_kv_compact, or both the same */
     void* v_cache;
     const int32_t* parents;    /* [children] */
     const int32_t* kv_lens;    /* [batch] */

@@ -260,3 +260,27 @@ def test_oracle_release_behind_a_cut():
     table, free, refs = np.array([[4, 1, 2], [3, 5, 0]]), np.arange(6), np.zeros(6, int)
     f, used, refs, status = trees.kv_release([1, 0], [130, 70], table, free, 5, refs, keep=[65, 64])
     assert (status, used) == (0, 3) and f[3:5].tolist() == [5, 2]
+
+
+LAYER = 9 * 2 * 64 * 64 * 2  # bytes of a layer of compact()'s and fork()'s caches
+
+
+@pytest.mark.parametrize("name,make", [("kv_compact", compact), ("kv_fork", fork)])
+@pytest.mark.parametrize("between,apart", [(LAYER, 16), (LAYER, LAYER - 16), (LAYER, -16), (LAYER, LAYER), (LAYER, 3 * LAYER - 16),
+                                           (2 * LAYER, LAYER - 16), (2 * LAYER, 4 * LAYER), (2 * LAYER, -LAYER - 16), (3 * LAYER, 2 * LAYER + 16),
+                                           (3 * LAYER, -6 * LAYER + 16)])
+def test_caches_that_overlap_are_refused(lib, name, make, between, apart):
+    a = make(k_cache=1 << 40, v_cache=(1 << 40) + apart, ld_layer=between // 2)
+    assert getattr(lib, "dflash_" + name)(ctypes.byref(a), None) == dfl.DFLASH_E_INVAL
+    assert dfl.dflash_last_error(None) == name + ": k_cache and v_cache overlap"
+
+
+@pytest.mark.parametrize("name,make", [("kv_compact", compact), ("kv_fork", fork)])
+@pytest.mark.parametrize("between,apart", [(LAYER, 3 * LAYER), (LAYER, -3 * LAYER), (2 * LAYER, LAYER), (2 * LAYER, -LAYER), (2 * LAYER, 3 * LAYER),
+                                           (2 * LAYER, 5 * LAYER), (2 * LAYER, 5 * LAYER + 16), (3 * LAYER, LAYER + 16), (3 * LAYER, -4 * LAYER),
+                                           (3 * LAYER, -2 * LAYER), (3 * LAYER, 2 * LAYER)])
+def test_caches_beside_each_other_are_not(lib, name, make, between, apart):
+    """(The call is refused for its NULL status, which is looked at behind the caches.)"""
+    a = make(k_cache=1 << 40, v_cache=(1 << 40) + apart, ld_layer=between // 2, status=None)
+    assert getattr(lib, "dflash_" + name)(ctypes.byref(a), None) == dfl.DFLASH_E_INVAL
+    assert dfl.dflash_last_error(None) == name + ": NULL argument"

@@ -847,3 +847,21 @@ def test_tree_masks_report_a_bad_tree_and_its_bad_length():
     t = dfl().tree_masks(i32([-1, 1]), i32([0, 2]), kv_lens=i32([-4]), words=1)
     assert host(t.status).tolist() == [9] and host(t.row_pos).tolist() == host(t.depth).tolist() == [-1, -1]
     assert (host(t.masks) == 0).all()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_kv_compact_and_fork_of_interleaved_caches(dtype):
+    """Keys and values of a layer beside each other in one tensor: views that interleave and do not overlap."""
+    rng = np.random.default_rng(9)
+    kv, layers, hkv, hd = np.array([90, 130]), 3, 2, 64
+    (k, v), table, spare = cache_case(rng, dtype, layers, hkv, hd, kv, slack=4)
+    both = torch.stack([k, v], 1)
+    ki, vi = both[:, 0], both[:, 1]
+    start, path, acc = i32([0, 9, 20]), i32([[0, 3, 8, -1], [0, 1, 10, -1]]), i32([2, 2])
+    got = [dfl().kv_compact(*x, i32(table), i32(kv), start, path, acc) for x in ((k, v), (ki, vi))]
+    assert all((host(g.status) == 0).all() for g in got) and torch.equal(got[0].kv_lens, got[1].kv_lens)
+    assert torch.equal(both, torch.stack([k, v], 1))
+    for x in ((k, v), (ki, vi)):
+        f = dfl().kv_fork(i32([1, 0]), got[0].kv_lens, i32(table), i32(spare), i32([0]), i32(np.zeros(k.shape[1])), *x)
+        assert int(f.status) == 0
+    assert torch.equal(both, torch.stack([k, v], 1))
