@@ -229,7 +229,8 @@ def kv_compact(k_cache, v_cache, table, kv_lens, q_start, path, accepted, *, kv_
     k_cache, v_cache: [pages, H_kv, 64, hd] or [layers, pages, H_kv, 64, hd] (fp32 or bf16), changed in place;
     table: int32 [batch, width]; kv_lens: int32 [batch], own keys, the tree's among them; q_start: int32
     [batch + 1]; path, accepted: as ``tree_accept`` gives them.  The lengths behind it are in ``kv_lens`` of the
-    result (``kv_out``, not kv_lens itself).  ``status``: int32 [batch], 0 or a sum of 1 (a path that does not rise
+    result (``kv_out``, not kv_lens itself).  An ``accepted`` of -1, as a tree gets that ``tree_accept`` refused, keeps no
+    node, the root neither: its length is the one before the step, and status is 0 (``tree_accept``'s is not).  ``status``: int32 [batch], 0 or a sum of 1 (a path that does not rise
     within the tree), 4 (bad q_start), 8 (bad length), 16 (bad page): nothing of the sequence has moved."""
     dev = _device(kv_lens, k_cache, v_cache)
     batch = _batch("kv_lens", kv_lens)

@@ -747,7 +747,10 @@ dflash_status dflash_tree_accept(const dflash_tree_accept_args* args, void* cuda
  * that does not rise within [0, m)), 4 (q_start decreases or is negative), 8
  * (kv_lens outside [m, 64 * width_table]), 16 (a page of a moved token outside
  * [0, n_pages)).  When not 0, nothing of the sequence moves and kv_out =
- * kv_lens.  No two sequences may hold the same page among their nodes'.
+ * kv_lens.  With accepted[s] = -1 none of the m nodes is kept, the root neither: kv_out =
+ * kv_lens - m, with status 0.  That is what a tree gets that dflash_tree_accept refused (its
+ * status says so): the whole step of that sequence is taken back, its anchor's key and value
+ * are still to be made.  No two sequences may hold the same page among their nodes'.
  * kv_out may not be kv_lens, and the layers of v_cache share no memory with those of k_cache
  * (they may lie between each other).  Errors: E_INVAL (sizes, NULL, caches that overlap), E_CUDA. */
 typedef struct {

@@ -865,3 +865,16 @@ def test_kv_compact_and_fork_of_interleaved_caches(dtype):
         f = dfl().kv_fork(i32([1, 0]), got[0].kv_lens, i32(table), i32(spare), i32([0]), i32(np.zeros(k.shape[1])), *x)
         assert int(f.status) == 0
     assert torch.equal(both, torch.stack([k, v], 1))
+
+
+def test_kv_compact_of_a_refused_tree_takes_the_step_back():
+    """tree_accept gives a bad tree accepted = -1, and compaction then keeps none of its nodes, the root neither."""
+    rng = np.random.default_rng(6)
+    kv = np.array([70, 75])
+    (k, v), table, _ = cache_case(rng, "bf16", 2, 2, 64, kv)
+    a = dfl().tree_accept(i32([-1, 0, 0, -1, 2, 0]), i32(np.zeros(6)), i32(np.zeros(6)), i32([0, 3, 6]), width=3)
+    assert host(a.status).tolist() == [0, 1] and host(a.accepted)[1] == -1
+    before = [x[:, table[1, :2]].clone() for x in (k, v)]
+    c = dfl().kv_compact(k, v, i32(table), i32(kv), i32([0, 3, 6]), a.path, a.accepted)
+    assert host(c.status).tolist() == [0, 0] and host(c.kv_lens).tolist() == [69, 72]
+    assert all(torch.equal(x[:, table[1, :2]], b) for x, b in zip((k, v), before))
