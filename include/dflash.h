@@ -876,18 +876,20 @@ typedef struct {
 dflash_status dflash_kv_release(const dflash_kv_release_args* args, void* cuda_stream);
 
 /* ------------------------------------------------------ log probabilities
- * Of each row of logits, x = logits * inv_temperature (the product rounded to
- * fp32; so is all that follows):
- *   lse          = ln sum_v exp(x_v)
- *   logprobs[i]  = x_t - lse for the row's i-th token t; 0 for a t outside
+ * Of each row x of logits, with its largest logit m and
+ * z_v = (x_v - m) * inv_temperature (fp32; the difference comes before the
+ * product, so that rows far from 0 are as exact as others):
+ *   lse_parts    = m and L = ln sum_v exp(z_v)
+ *   lse          = m * inv_temperature + L, rounded once (infinite where that is
+ *                  beyond fp32, while what follows is not)
+ *   logprobs[i]  = z_t - L for the row's i-th token t; 0 for a t outside
  *                  [0, vocab) (padding)
  *   ranks[i]     = tokens ahead of t: of a larger logit, or an equal one and a
- *                  lower id; -1 for padding
- *   lse_parts    = the largest logit and ln sum_v exp(x_v - its x): lse =
- *                  lse_parts[0] * inv_temperature + lse_parts[1]
- *   entropy      = -sum_v p_v ln p_v, p = exp(x - lse)
- *   top_ids, top_logprobs = the k likeliest tokens, likeliest first, the lower id
- *                  first among equal logits
+ *                  lower id; -1 for padding (the logits themselves are compared, without
+ *                  the temperature)
+ *   entropy      = -sum_v p_v ln p_v, ln p_v = z_v - L
+ *   top_ids, top_logprobs = the k likeliest tokens by their logits, likeliest first,
+ *                  the lower id first among equal ones
  * Tokens at -inf have probability 0; they are no alternatives: where fewer than k
  * tokens are left, the list ends in id -1 and -inf.  A row of -inf alone has lse =
  * lse_parts = logprobs = -inf and entropy 0.  A row that holds NaN or +inf gets NaN
@@ -916,16 +918,16 @@ typedef struct {
 dflash_status dflash_token_logprobs(const dflash_logprobs_args* args, void* cuda_stream);
 
 /* Gradient of a loss of those log probabilities and entropies by the logits,
- * with p_v = exp(x_v - lse), g_i = grad_logprobs[i] (0 for padding) and h =
- * grad_entropy:
+ * with p_v = exp(x_v * inv_temperature - lse), from lse_parts exp(z_v - L), g_i =
+ * grad_logprobs[i] (0 for padding) and h = grad_entropy:
  *   out_v = inv_temperature * (sum_{i: t_i = v} g_i - p_v sum_i g_i
  *                              - h p_v (ln p_v + entropy))
  * in fp32, rounded once to the logits' type.  lse and entropy are what
  * dflash_token_logprobs gave (both entropy and grad_entropy, or neither).  p
  * comes from lse_parts where they are given, as exact for rows of any size;
  * from lse alone, p is off by the factor exp(+-2^-24 |lse|): a row all of the
- * type's lowest value, whose lse is that value or below fp32's range, needs
- * lse_parts.  A row
+ * type's lowest value, whose lse is that value or below fp32's range, or one whose lse
+ * is beyond it above, needs lse_parts.  A row
  * whose g and h are all 0 gets zeros, whatever it holds; one of -inf alone the
  * g at its tokens.  out may be logits, with one row
  * stride; no other overlap.

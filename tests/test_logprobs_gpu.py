@@ -371,3 +371,44 @@ def test_ranks_of_masked_tokens_anywhere(dtype, n, vocab):
         z, ids = host(x.float())[:, None, :vocab], np.arange(vocab)
         xt = np.take_along_axis(z[:, 0], t, 1)[:, :, None]
         np.testing.assert_array_equal(host(got.ranks), ((z > xt) | ((z == xt) & (ids < t[:, :, None]))).sum(2))
+
+
+def test_ranks_and_order_are_those_of_the_logits_themselves():
+    """Neighbours of 1e5 that a product with 1 / T rounded to fp32 would make equal, and logits whose product is beyond fp32."""
+    step = 2.0 ** -7  # of fp32 at 1e5
+    x = np.full((2, 6000), 9e4, np.float32)
+    x[0, [10, 4000, 20, 5999]] = 1e5 + step * np.array([0, 1, 2, 3])
+    assert len(set((x[0, [10, 4000, 20, 5999]] * np.float32(1 / 3.0)).tolist())) < 4
+    x[1, :50], x[1, 50:] = 2e38, -2e38
+    t = np.array([[10, 4000, 20], [49, 0, 60]])
+    got = dfl().token_logprobs(torch.from_numpy(x).cuda(), i32(t), top=4, temperature=3.0)
+    assert host(got.ranks).tolist() == [[3, 2, 1], [49, 0, 60]]
+    assert host(got.top_ids).tolist() == [[5999, 20, 4000, 10], [0, 1, 2, 3]]
+    got = dfl().token_logprobs(torch.from_numpy(x[1:]).cuda(), i32(t[1:]), top=4, temperature=0.25)
+    assert np.isposinf(host(got.lse)).all() and abs(float(got.entropy) - np.log(50)) < 1e-5
+    np.testing.assert_allclose(host(got.logprobs)[0, :2], -np.log(50), rtol=1e-6)
+    assert np.isneginf(host(got.logprobs)[0, 2])  # (-4e38 / 0.25 lies beyond fp32)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("temperature", [0.7, 3.0, 2.0 ** -20, 2.0 ** 20])
+def test_log_probabilities_of_rows_far_from_zero(dtype, temperature):
+    """The difference to the largest logit comes before the scale: check()'s bound of logprobs has no term of the logits' size."""
+    x = rows_of("f32", 4, 9001, seed=21)
+    x[1] += 1e5 if dtype == "f32" else 500.0
+    x[2] -= 1e6 if dtype == "f32" else 900.0
+    x[3] *= 1e-3
+    x = x.to(DT[dtype])
+    t = tokens_of(x, 3, seed=22)
+    two = torch.empty((4, 2), device="cuda")
+    f = dfl().token_logprobs(x.cuda(), i32(t), top=6, temperature=temperature, lse_parts=two)
+    check(x, t, 6, f, temperature)
+    np.testing.assert_array_equal(host(two)[:, 0], host(x.float()).max(1))
+    # and the gradient from the parts, whose law is that of the rows from 0
+    rng = np.random.default_rng(5)
+    g, h = rng.standard_normal((4, 3)).astype(np.float32), rng.standard_normal(4).astype(np.float32)
+    got = dfl().token_logprobs_grad(x.cuda(), i32(t), two, torch.from_numpy(g).cuda(), entropy=f.entropy, grad_entropy=torch.from_numpy(h).cuda(),
+                                    temperature=temperature)
+    y = host(x.float()).astype(np.float64)
+    y -= y.max(1, keepdims=True)
+    grad_check(dtype, torch.from_numpy(y), t, g, h, got, trees.token_logprobs_grad(y, t, g, h, temperature), temperature)
