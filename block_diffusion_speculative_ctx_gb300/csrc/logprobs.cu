@@ -573,7 +573,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) logprobs_kernel(dflash_logprobs
                     if (at < LIST) ids[at] = sl.id(it, __ffs(on) - 1);
                 }
             }
-            if (it == refresh && 3 * it < sl.tiles) {  // (behind 3, 9, 33 .. tiles, if twice as many are left)
+            if (it == refresh && 3 * it < sl.tiles) {  // (behind 3, 9, 33 .. tiles of at least 7, 25, 97 ..)
                 refresh *= 4;
                 __syncthreads();
                 const int n = S.n_cand;
