@@ -412,3 +412,50 @@ def test_log_probabilities_of_rows_far_from_zero(dtype, temperature):
     y = host(x.float()).astype(np.float64)
     y -= y.max(1, keepdims=True)
     grad_check(dtype, torch.from_numpy(y), t, g, h, got, trees.token_logprobs_grad(y, t, g, h, temperature), temperature)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("rows,vocab", [(1, 151936), (7, 33003), (300, 4099), (5, 40)])
+@pytest.mark.parametrize("n", [5, 9, 16, 31, 32])
+def test_ranks_of_up_to_32_tokens(dtype, rows, vocab, n):
+    """Likely and unlikely ones, tokens at -inf, the same token twice, padding among them, in every lane."""
+    x = rows_of("f32", rows, vocab, seed=vocab + n)
+    x[::2][torch.rand(x[::2].shape, generator=torch.Generator().manual_seed(n)) < 0.5] = float("-inf")
+    x = x.to(DT[dtype]).cuda()
+    rng = np.random.default_rng(n)
+    t = rng.integers(0, vocab, (rows, n))
+    likely = host(x.float().topk(min(40, vocab), 1)[1])
+    for r in range(rows):
+        some = rng.permutation(n)[:n // 2]
+        t[r, some] = rng.choice(likely[r], len(some))
+    t[:, n // 3], t[::3, n - 1] = t[:, 0], -1
+    t[1::3, n // 2] = vocab
+    got = dfl().token_logprobs(x, i32(t), top=3)
+    z, ids = x.double(), torch.arange(vocab, device="cuda")
+    for i in range(n):
+        real = (t[:, i] >= 0) & (t[:, i] < vocab)
+        at = torch.from_numpy(np.where(real, t[:, i], 0)).cuda()[:, None]
+        xt = z.gather(1, at)
+        want = host(((z > xt) | ((z == xt) & (ids < at))).sum(1))
+        np.testing.assert_array_equal(host(got.ranks)[:, i], np.where(real, want, -1))
+        np.testing.assert_array_equal(host(got.logprobs)[~real, i], 0)
+
+
+def test_rows_that_begin_behind_2_31_elements():
+    rows, vocab, ld = 10, 5000, (1 << 28) + 8
+    store = [torch.empty((rows - 1) * ld + vocab, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    x, out = (s.as_strided((rows, vocab), (ld, 1)) for s in store)
+    y = rows_of("bf16", rows, vocab, seed=30)
+    x.copy_(y)
+    out.fill_(7.0)
+    t = tokens_of(y, 3, seed=31)
+    got = dfl().token_logprobs(x, i32(t), top=5)
+    check(y, t, 5, got)
+    rng = np.random.default_rng(32)
+    g, h = rng.standard_normal((rows, 3)).astype(np.float32), rng.standard_normal(rows).astype(np.float32)
+    want = trees.token_logprobs_grad(host(y.float()), t, g, h)
+    kw = dict(entropy=got.entropy, grad_entropy=torch.from_numpy(h).cuda())
+    dfl().token_logprobs_grad(x, i32(t), got.lse, torch.from_numpy(g).cuda(), out=out, **kw)
+    grad_check("bf16", y, t, g, h, out, want)
+    dfl().token_logprobs_grad(x, i32(t), got.lse, torch.from_numpy(g).cuda(), out=x, **kw)  # in place
+    assert torch.equal(x, out)

@@ -878,3 +878,44 @@ def test_kv_compact_of_a_refused_tree_takes_the_step_back():
     c = dfl().kv_compact(k, v, i32(table), i32(kv), i32([0, 3, 6]), a.path, a.accepted)
     assert host(c.status).tolist() == [0, 0] and host(c.kv_lens).tolist() == [69, 72]
     assert all(torch.equal(x[:, table[1, :2]], b) for x, b in zip((k, v), before))
+
+
+def test_steps_and_pages_on_a_side_stream_beside_others():
+    """Masks, acceptance, compaction, fork and release on two streams at once, each with tensors of its own: what they give alone."""
+    d = dfl()
+    sizes, n = [40, 33, 64, 17], 4
+    kv = np.array([300, 120, 700, 64]) + sizes
+
+    def state(i):
+        rng = np.random.default_rng(50 + i)
+        forest, tokens, posterior = forest_case(rng, sizes, 5)
+        f = fork_state(rng, kv, layers=6, hkv=8, hd=128, free=60)
+        table = np.pad(f["table"], ((0, 0), (0, 2)), constant_values=f["scratch"])
+        return dict(par=i32(np.concatenate(forest)), tok=i32(np.concatenate(tokens)), post=i32(np.concatenate(posterior)), k=f["k"], v=f["v"],
+                    start=i32(starts(sizes)), kv=i32(kv), table=i32(table), fl=i32(f["spare"]), used=i32([2]), refs=i32(f["refs"]),
+                    parents=i32(np.arange(3 * n) % n), kids=i32(np.arange(3 * n)), scratch=f["scratch"])
+
+    def run(s):
+        t = d.tree_masks(s["par"], s["start"], kv_lens=s["kv"], words=2)
+        a = d.tree_accept(s["par"], s["tok"], s["post"], s["start"], width=9)
+        c = d.kv_compact(s["k"], s["v"], s["table"], s["kv"], s["start"], a.path, a.accepted)
+        f = d.kv_fork(s["parents"], c.kv_lens, s["table"], s["fl"], s["used"], s["refs"], s["k"], s["v"], scratch_page=s["scratch"],
+                      used_out=s["used"])
+        held = s["refs"].clone()
+        r = d.kv_release(s["kids"], f.kv_lens, f.table, s["fl"], s["used"], s["refs"], used_out=s["used"])
+        return [*t, *a, *c, f.table, f.kv_lens, f.status, held, r.status, s["fl"], s["used"], s["refs"], s["k"], s["v"]]
+
+    want = [[x.clone() for x in run(state(i))] for i in range(2)]
+    both = [[state(i) for _ in range(4)] for i in range(2)]
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    torch.cuda.synchronize()
+    got = [[], []]
+    for j in range(4):
+        got[0].append(run(both[0][j]))
+        with torch.cuda.stream(side):
+            got[1].append(run(both[1][j]))
+    torch.cuda.synchronize()
+    for i in range(2):
+        for g in got[i]:
+            assert all(torch.equal(x, y) for x, y in zip(g, want[i]))
