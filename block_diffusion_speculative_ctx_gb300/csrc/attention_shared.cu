@@ -300,24 +300,11 @@ extern "C" size_t dflash_shared_prefix_workspace(int32_t dtype, int32_t n_heads,
 
 namespace {
 
-dflash_status queue(const dflash_shared_prefix_args& a, const TreeMasks* tree, void* cuda_stream, const char* unprepared) {
+dflash_status attend(const dflash_shared_prefix_args& a, const TreeMasks* tree, void* cuda_stream, const char* unprepared) {
     if (a.rows == 0) return DFLASH_OK;
-    bool failed = false;
-    Launch L{(cudaStream_t)cuda_stream, nullptr};
-    L.pdl = true;  // (each kernel waits for what runs before it ahead of its first read)
-    L.failed = &failed;
-    const bool ok = shared_prefix_attention(L, a, tree);
-    const cudaError_t e = cudaGetLastError();
-    if (!ok || failed || e != cudaSuccess) {
-        set_global_error(e != cudaSuccess ? cudaGetErrorString(e) : unprepared);
-        return DFLASH_E_CUDA;
-    }
-    return DFLASH_OK;
-}
-
-dflash_status refuse(const char* why) {
-    set_global_error(why);
-    return DFLASH_E_INVAL;
+    return queue(cuda_stream, unprepared, [&](const Launch& L) {
+        if (!shared_prefix_attention(L, a, tree)) L.fail();
+    });
 }
 
 }  // namespace
@@ -325,7 +312,7 @@ dflash_status refuse(const char* why) {
 extern "C" dflash_status dflash_shared_prefix_attention(const dflash_shared_prefix_args* p, void* cuda_stream) {
     const char* why = "shared_prefix_attention: args is NULL";
     if (!p || check_shared_prefix(*p, &why) != DFLASH_OK) return refuse(why);
-    return queue(*p, nullptr, cuda_stream, "shared_prefix_attention: a kernel could not be prepared");
+    return attend(*p, nullptr, cuda_stream, "shared_prefix_attention: a kernel could not be prepared");
 }
 
 extern "C" dflash_status dflash_tree_attention(const dflash_tree_attention_args* p, void* cuda_stream) {
@@ -343,5 +330,5 @@ extern "C" dflash_status dflash_tree_attention(const dflash_tree_attention_args*
     if (p->attn.rows > 0 && !p->masks) return refuse("tree_attention: masks is NULL");
     if (p->ld_mask < p->words) return refuse("tree_attention: ld_mask is smaller than words");
     const TreeMasks tree = {p->masks, p->ld_mask, p->words};
-    return queue(p->attn, &tree, cuda_stream, "tree_attention: a kernel could not be prepared");
+    return attend(p->attn, &tree, cuda_stream, "tree_attention: a kernel could not be prepared");
 }

@@ -374,20 +374,6 @@ __global__ void __launch_bounds__(NR) kv_release_kernel(dflash_kv_release_args a
     meet();  // (no CTA leaves while another may read its flags; every CTA has read *used)
 }
 
-dflash_status fail(const char* msg) {
-    set_global_error(msg);
-    return DFLASH_E_INVAL;
-}
-
-dflash_status done(bool failed, const char* failed_text) {
-    const cudaError_t e = cudaGetLastError();
-    if (failed || e != cudaSuccess) {
-        set_global_error(e != cudaSuccess ? cudaGetErrorString(e) : failed_text);
-        return DFLASH_E_CUDA;
-    }
-    return DFLASH_OK;
-}
-
 }  // namespace
 
 }  // namespace dfl
@@ -395,54 +381,47 @@ dflash_status done(bool failed, const char* failed_text) {
 using namespace dfl;
 
 extern "C" dflash_status dflash_kv_fork(const dflash_kv_fork_args* p, void* cuda_stream) {
-    if (!p) return fail("kv_fork: args is NULL");
+    if (!p) return refuse("kv_fork: args is NULL");
     const dflash_kv_fork_args& a = *p;
     if (const char* why = bad_caches(a, "kv_fork: dtype must be F32 or BF16", "kv_fork: layers outside [1, 1024]",
                                      "kv_fork: n_pages, n_kv_heads or head_dim out of range (a head's row is a multiple of 16 bytes)",
                                      "kv_fork: the caches must be 16-byte aligned, ld_layer a multiple of 16 bytes and no smaller than a layer"))
-        return fail(why);
+        return refuse(why);
     // (one cache for both is copied twice alike)
-    if (a.k_cache != a.v_cache && caches_overlap(a)) return fail("kv_fork: k_cache and v_cache overlap");
-    if (a.batch < 1 || a.batch > MAXB) return fail("kv_fork: batch outside [1, 2048]");
-    if (a.children < 1 || a.children > MAXB) return fail("kv_fork: children outside [1, 2048]");
+    if (a.k_cache != a.v_cache && caches_overlap(a)) return refuse("kv_fork: k_cache and v_cache overlap");
+    if (a.batch < 1 || a.batch > MAXB) return refuse("kv_fork: batch outside [1, 2048]");
+    if (a.children < 1 || a.children > MAXB) return refuse("kv_fork: children outside [1, 2048]");
     if (a.width < 1 || a.width > (1 << 22) || a.ld_table < a.width || a.ld_out < a.width)
-        return fail("kv_fork: width outside [1, 2^22], or a table row stride is smaller");
-    if (a.n_free < 0) return fail("kv_fork: n_free must not be negative");
+        return refuse("kv_fork: width outside [1, 2^22], or a table row stride is smaller");
+    if (a.n_free < 0) return refuse("kv_fork: n_free must not be negative");
     if (!a.parents || !a.kv_lens || !a.table || !a.free_pages || !a.used || !a.refs || !a.table_out || !a.lens_out ||
         !a.used_out || !a.status)
-        return fail("kv_fork: NULL argument");
+        return refuse("kv_fork: NULL argument");
     if (a.table_out == a.table || a.lens_out == a.kv_lens)
-        return fail("kv_fork: the children's tables and lengths may not be the parents'");
-    bool failed = false;
-    Launch L{(cudaStream_t)cuda_stream, nullptr};
-    L.pdl = true;  // (each kernel waits for what runs before it ahead of its first read)
-    L.failed = &failed;
+        return refuse("kv_fork: the children's tables and lengths may not be the parents'");
     const int ctas = std::min(152, (a.children + NT / 32 - 1) / (NT / 32));
-    launch_k(L, fork_tables_kernel, dim3(ctas), dim3(NT), 0, 1, a);
     const int vecs = a.head_dim * (a.dtype == DFLASH_DTYPE_BF16 ? 2 : 4) / 16;
-    launch_k(L, fork_copy_kernel, dim3(a.children, 2 * a.layers), dim3(NT_COPY), 0, 1, a, vecs);
-    return done(failed, "kv_fork: launch failed");
+    return queue(cuda_stream, "kv_fork: launch failed", [&](const Launch& L) {
+        launch_k(L, fork_tables_kernel, dim3(ctas), dim3(NT), 0, 1, a);
+        launch_k(L, fork_copy_kernel, dim3(a.children, 2 * a.layers), dim3(NT_COPY), 0, 1, a, vecs);
+    });
 }
 
 extern "C" dflash_status dflash_kv_release(const dflash_kv_release_args* p, void* cuda_stream) {
-    if (!p) return fail("kv_release: args is NULL");
+    if (!p) return refuse("kv_release: args is NULL");
     const dflash_kv_release_args& a = *p;
-    if (a.batch < 1 || a.batch > MAXB) return fail("kv_release: batch outside [1, 2048]");
-    if (a.n < 1 || a.n > MAXB) return fail("kv_release: n outside [1, 2048]");
+    if (a.batch < 1 || a.batch > MAXB) return refuse("kv_release: batch outside [1, 2048]");
+    if (a.n < 1 || a.n > MAXB) return refuse("kv_release: n outside [1, 2048]");
     if (a.width < 1 || a.width > MAX_WIDTH || a.ld_table < a.width)
-        return fail("kv_release: width outside [1, 2^18], or ld_table smaller");
-    if (a.n_free < 0 || a.n_pages < 1) return fail("kv_release: n_free < 0 or n_pages < 1");
-    if (a.reserved != 0) return fail("kv_release: reserved must be 0");
+        return refuse("kv_release: width outside [1, 2^18], or ld_table smaller");
+    if (a.n_free < 0 || a.n_pages < 1) return refuse("kv_release: n_free < 0 or n_pages < 1");
+    if (a.reserved != 0) return refuse("kv_release: reserved must be 0");
     if (!a.seqs || !a.kv_lens || !a.table || !a.free_pages || !a.used || !a.refs || !a.used_out || !a.status)
-        return fail("kv_release: NULL argument");
-    bool failed = false;
-    Launch L{(cudaStream_t)cuda_stream, nullptr};
-    L.pdl = true;
-    L.failed = &failed;
+        return refuse("kv_release: NULL argument");
     // a warp per unit while they last
     const long long units = (long long)a.n * ((a.width + UNIT - 1) / UNIT);
     int ctas = 1;
     while (ctas < MAXC && units > (long long)ctas * WARPS) ctas *= 2;
-    launch_k(L, kv_release_kernel, dim3(1, 1, ctas), dim3(NR), 0, ctas, a, ctas);
-    return done(failed, "kv_release: launch failed");
+    return queue(cuda_stream, "kv_release: launch failed",
+                 [&](const Launch& L) { launch_k(L, kv_release_kernel, dim3(1, 1, ctas), dim3(NR), 0, ctas, a, ctas); });
 }

@@ -44,43 +44,16 @@ namespace dfl {
 
 namespace {
 
+using tc::add2, tc::ex2, tc::fma2, tc::mul2, tc::pack2, tc::unpack2;
+
 constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
 constexpr float MIN_INVERSE = 1.f / (1 << 20), MAX_INVERSE = 1 << 20;  // of a temperature
 constexpr int MAXT = DFLASH_LOGPROBS_MAX_TOKENS, MAXK = DFLASH_LOGPROBS_MAX_TOP;
 
-__device__ __forceinline__ float ex2(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
 // max(x, y), NaN where one is.
 __device__ __forceinline__ float max_nan(float x, float y) {
     float r;
     asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(x), "f"(y));
-    return r;
-}
-// Two fp32 operations in one instruction.
-__device__ __forceinline__ uint64_t pack2(float lo, float hi) {
-    uint64_t r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
-    return r;
-}
-__device__ __forceinline__ void unpack2(uint64_t v, float& lo, float& hi) {
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
-}
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-    uint64_t r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-    return r;
-}
-__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
-    uint64_t r;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
-    uint64_t r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
     return r;
 }
 // The G elements of a 16-byte vector.
@@ -831,26 +804,6 @@ void backward(const Launch& L, const dflash_logprobs_grad_args& a) {
     else launch_k(L, logprobs_grad_kernel<T, false>, grid, dim3(NB), 0, 1, a, chunks);
 }
 
-dflash_status fail(const char* msg) {
-    set_global_error(msg);
-    return DFLASH_E_INVAL;
-}
-
-template <typename F>
-dflash_status queue(void* cuda_stream, const char* failed_text, F&& f) {
-    bool failed = false;
-    Launch L{(cudaStream_t)cuda_stream, nullptr};
-    L.pdl = true;  // (each kernel waits for what runs before it ahead of its first read)
-    L.failed = &failed;
-    f(L);
-    const cudaError_t e = cudaGetLastError();
-    if (failed || e != cudaSuccess) {
-        set_global_error(e != cudaSuccess ? cudaGetErrorString(e) : failed_text);
-        return DFLASH_E_CUDA;
-    }
-    return DFLASH_OK;
-}
-
 }  // namespace
 
 }  // namespace dfl
@@ -858,19 +811,19 @@ dflash_status queue(void* cuda_stream, const char* failed_text, F&& f) {
 using namespace dfl;
 
 extern "C" dflash_status dflash_token_logprobs(const dflash_logprobs_args* p, void* cuda_stream) {
-    if (!p) return fail("token_logprobs: args is NULL");
+    if (!p) return refuse("token_logprobs: args is NULL");
     const dflash_logprobs_args& a = *p;
-    if (a.dtype != DFLASH_DTYPE_F32 && a.dtype != DFLASH_DTYPE_BF16) return fail("token_logprobs: dtype must be F32 or BF16");
-    if (a.rows < 0 || a.rows > (1 << 20)) return fail("token_logprobs: rows outside [0, 2^20]");
-    if (a.vocab < 1 || a.vocab > (1 << 30)) return fail("token_logprobs: vocab outside [1, 2^30]");
-    if (a.n < 0 || a.n > MAXT) return fail("token_logprobs: n outside [0, 32]");
-    if (a.k < 0 || a.k > MAXK) return fail("token_logprobs: k outside [0, 32]");
+    if (a.dtype != DFLASH_DTYPE_F32 && a.dtype != DFLASH_DTYPE_BF16) return refuse("token_logprobs: dtype must be F32 or BF16");
+    if (a.rows < 0 || a.rows > (1 << 20)) return refuse("token_logprobs: rows outside [0, 2^20]");
+    if (a.vocab < 1 || a.vocab > (1 << 30)) return refuse("token_logprobs: vocab outside [1, 2^30]");
+    if (a.n < 0 || a.n > MAXT) return refuse("token_logprobs: n outside [0, 32]");
+    if (a.k < 0 || a.k > MAXK) return refuse("token_logprobs: k outside [0, 32]");
     if (!(a.inv_temperature >= MIN_INVERSE && a.inv_temperature <= MAX_INVERSE))
-        return fail("token_logprobs: inv_temperature outside [2^-20, 2^20]");
-    if ((a.rows > 0 && !a.logits) || (a.rows > 0 && a.n > 0 && !a.tokens)) return fail("token_logprobs: NULL argument");
-    if ((uintptr_t)a.logits % (a.dtype == DFLASH_DTYPE_BF16 ? 2 : 4)) return fail("token_logprobs: logits is not aligned to its type");
-    if ((uintptr_t)a.lse_parts % 8) return fail("token_logprobs: lse_parts is not aligned to 8 bytes");
-    if (a.ld_logits < a.vocab) return fail("token_logprobs: the row stride is smaller than vocab");
+        return refuse("token_logprobs: inv_temperature outside [2^-20, 2^20]");
+    if ((a.rows > 0 && !a.logits) || (a.rows > 0 && a.n > 0 && !a.tokens)) return refuse("token_logprobs: NULL argument");
+    if ((uintptr_t)a.logits % (a.dtype == DFLASH_DTYPE_BF16 ? 2 : 4)) return refuse("token_logprobs: logits is not aligned to its type");
+    if ((uintptr_t)a.lse_parts % 8) return refuse("token_logprobs: lse_parts is not aligned to 8 bytes");
+    if (a.ld_logits < a.vocab) return refuse("token_logprobs: the row stride is smaller than vocab");
     if (a.rows == 0) return DFLASH_OK;
     return queue(cuda_stream, "token_logprobs: launch failed", [&](const Launch& L) {
         if (a.dtype == DFLASH_DTYPE_BF16) forward<bf16>(L, a);
@@ -879,25 +832,25 @@ extern "C" dflash_status dflash_token_logprobs(const dflash_logprobs_args* p, vo
 }
 
 extern "C" dflash_status dflash_token_logprobs_grad(const dflash_logprobs_grad_args* p, void* cuda_stream) {
-    if (!p) return fail("token_logprobs_grad: args is NULL");
+    if (!p) return refuse("token_logprobs_grad: args is NULL");
     const dflash_logprobs_grad_args& a = *p;
     if (a.dtype != DFLASH_DTYPE_F32 && a.dtype != DFLASH_DTYPE_BF16)
-        return fail("token_logprobs_grad: dtype must be F32 or BF16");
-    if (a.rows < 0 || a.rows > (1 << 20)) return fail("token_logprobs_grad: rows outside [0, 2^20]");
-    if (a.vocab < 1 || a.vocab > (1 << 30)) return fail("token_logprobs_grad: vocab outside [1, 2^30]");
-    if (a.n < 0 || a.n > MAXT) return fail("token_logprobs_grad: n outside [0, 32]");
+        return refuse("token_logprobs_grad: dtype must be F32 or BF16");
+    if (a.rows < 0 || a.rows > (1 << 20)) return refuse("token_logprobs_grad: rows outside [0, 2^20]");
+    if (a.vocab < 1 || a.vocab > (1 << 30)) return refuse("token_logprobs_grad: vocab outside [1, 2^30]");
+    if (a.n < 0 || a.n > MAXT) return refuse("token_logprobs_grad: n outside [0, 32]");
     if (!(a.inv_temperature >= MIN_INVERSE && a.inv_temperature <= MAX_INVERSE))
-        return fail("token_logprobs_grad: inv_temperature outside [2^-20, 2^20]");
-    if (a.reserved != 0) return fail("token_logprobs_grad: reserved must be 0");
+        return refuse("token_logprobs_grad: inv_temperature outside [2^-20, 2^20]");
+    if (a.reserved != 0) return refuse("token_logprobs_grad: reserved must be 0");
     if (a.rows > 0 && (!a.logits || !a.out || (!a.lse && !a.lse_parts) || (a.n > 0 && (!a.tokens || !a.grad_logprobs)) || (a.grad_entropy && !a.entropy)))
-        return fail("token_logprobs_grad: NULL argument");
+        return refuse("token_logprobs_grad: NULL argument");
     const uintptr_t es = a.dtype == DFLASH_DTYPE_BF16 ? 2 : 4;
-    if (((uintptr_t)a.logits | (uintptr_t)a.out) % es) return fail("token_logprobs_grad: logits or out is not aligned to its type");
-    if ((uintptr_t)a.lse_parts % 8) return fail("token_logprobs_grad: lse_parts is not aligned to 8 bytes");
-    if (a.ld_logits < a.vocab || a.ld_out < a.vocab) return fail("token_logprobs_grad: a row stride is smaller than vocab");
-    if (a.out == a.logits && a.ld_out != a.ld_logits && a.rows > 1) return fail("token_logprobs_grad: in place needs one row stride");
+    if (((uintptr_t)a.logits | (uintptr_t)a.out) % es) return refuse("token_logprobs_grad: logits or out is not aligned to its type");
+    if ((uintptr_t)a.lse_parts % 8) return refuse("token_logprobs_grad: lse_parts is not aligned to 8 bytes");
+    if (a.ld_logits < a.vocab || a.ld_out < a.vocab) return refuse("token_logprobs_grad: a row stride is smaller than vocab");
+    if (a.out == a.logits && a.ld_out != a.ld_logits && a.rows > 1) return refuse("token_logprobs_grad: in place needs one row stride");
     const long long chunk = NB * VB;
-    if ((long long)a.rows * ((a.vocab + chunk - 1) / chunk) >= (1ll << 31)) return fail("token_logprobs_grad: rows * vocab is too large");
+    if ((long long)a.rows * ((a.vocab + chunk - 1) / chunk) >= (1ll << 31)) return refuse("token_logprobs_grad: rows * vocab is too large");
     if (a.rows == 0) return DFLASH_OK;
     return queue(cuda_stream, "token_logprobs_grad: launch failed", [&](const Launch& L) {
         if (a.dtype == DFLASH_DTYPE_BF16) backward<bf16>(L, a);

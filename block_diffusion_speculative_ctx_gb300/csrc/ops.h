@@ -71,6 +71,27 @@ bool caches_overlap(const A& a) {
     return false;
 }
 
+// The entries' ends: a refused argument, and what f(L) queues on the caller's stream (failed_text: what to say where no CUDA
+// error does).
+inline dflash_status refuse(const char* why) {
+    set_global_error(why);
+    return DFLASH_E_INVAL;
+}
+template <typename F>
+dflash_status queue(void* cuda_stream, const char* failed_text, F&& f) {
+    bool failed = false;
+    Launch L{(cudaStream_t)cuda_stream, nullptr};
+    L.pdl = true;  // (each kernel waits for what runs before it ahead of its first read)
+    L.failed = &failed;
+    f(L);
+    const cudaError_t e = cudaGetLastError();
+    if (failed || e != cudaSuccess) {
+        set_global_error(e != cudaSuccess ? cudaGetErrorString(e) : failed_text);
+        return DFLASH_E_CUDA;
+    }
+    return DFLASH_OK;
+}
+
 // The entries' argument checks: DFLASH_OK, or E_INVAL with the reason in *why.
 dflash_status check_shared_prefix(const dflash_shared_prefix_args& a, const char** why);
 dflash_status check_logits(const dflash_logits_args& a, const char** why);

@@ -181,26 +181,6 @@ __global__ void __launch_bounds__(NT_MOVE) kv_compact_kernel(dflash_kv_compact_a
     }
 }
 
-dflash_status fail(const char* msg) {
-    set_global_error(msg);
-    return DFLASH_E_INVAL;
-}
-
-template <typename F>
-dflash_status queue(void* cuda_stream, const char* failed_text, F&& f) {
-    bool failed = false;
-    Launch L{(cudaStream_t)cuda_stream, nullptr};
-    L.pdl = true;  // (each kernel waits for what runs before it ahead of its first read)
-    L.failed = &failed;
-    f(L);
-    const cudaError_t e = cudaGetLastError();
-    if (failed || e != cudaSuccess) {
-        set_global_error(e != cudaSuccess ? cudaGetErrorString(e) : failed_text);
-        return DFLASH_E_CUDA;
-    }
-    return DFLASH_OK;
-}
-
 }  // namespace
 
 }  // namespace dfl
@@ -208,50 +188,50 @@ dflash_status queue(void* cuda_stream, const char* failed_text, F&& f) {
 using namespace dfl;
 
 extern "C" dflash_status dflash_tree_masks(const dflash_tree_masks_args* p, void* cuda_stream) {
-    if (!p) return fail("tree_masks: args is NULL");
+    if (!p) return refuse("tree_masks: args is NULL");
     const dflash_tree_masks_args& a = *p;
-    if (a.batch < 1 || a.batch > DFLASH_OPS_MAX_BATCH) return fail("tree_masks: batch outside [1, 2048]");
-    if (a.rows < 0 || a.rows > (1 << 20)) return fail("tree_masks: rows outside [0, 2^20]");
+    if (a.batch < 1 || a.batch > DFLASH_OPS_MAX_BATCH) return refuse("tree_masks: batch outside [1, 2048]");
+    if (a.rows < 0 || a.rows > (1 << 20)) return refuse("tree_masks: rows outside [0, 2^20]");
     if (a.words < 1 || a.words > (1 << 20) || a.ld_mask < a.words)
-        return fail("tree_masks: words outside [1, 2^20], or ld_mask smaller");
-    if (a.base_pos < 0 || a.base_pos > (1 << 30)) return fail("tree_masks: base_pos outside [0, 2^30]");
+        return refuse("tree_masks: words outside [1, 2^20], or ld_mask smaller");
+    if (a.base_pos < 0 || a.base_pos > (1 << 30)) return refuse("tree_masks: base_pos outside [0, 2^30]");
     if (!a.q_start || !a.status || (a.rows > 0 && (!a.parents || !a.masks)) || (a.row_pos && !a.kv_lens))
-        return fail("tree_masks: NULL argument");
+        return refuse("tree_masks: NULL argument");
     return queue(cuda_stream, "tree_masks: launch failed",
                  [&](const Launch& L) { launch_k(L, tree_masks_kernel, dim3(a.batch), dim3(NT_MASK), 0, 1, a); });
 }
 
 extern "C" dflash_status dflash_tree_accept(const dflash_tree_accept_args* p, void* cuda_stream) {
-    if (!p) return fail("tree_accept: args is NULL");
+    if (!p) return refuse("tree_accept: args is NULL");
     const dflash_tree_accept_args& a = *p;
-    if (a.batch < 1 || a.batch > DFLASH_OPS_MAX_BATCH) return fail("tree_accept: batch outside [1, 2048]");
-    if (a.rows < 0 || a.rows > (1 << 20)) return fail("tree_accept: rows outside [0, 2^20]");
-    if (a.width < 1 || a.width > MAXN) return fail("tree_accept: width outside [1, 1024]");
-    if (a.reserved != 0) return fail("tree_accept: reserved must be 0");
+    if (a.batch < 1 || a.batch > DFLASH_OPS_MAX_BATCH) return refuse("tree_accept: batch outside [1, 2048]");
+    if (a.rows < 0 || a.rows > (1 << 20)) return refuse("tree_accept: rows outside [0, 2^20]");
+    if (a.width < 1 || a.width > MAXN) return refuse("tree_accept: width outside [1, 1024]");
+    if (a.reserved != 0) return refuse("tree_accept: reserved must be 0");
     if (!a.q_start || !a.path || !a.accepted || !a.bonus || !a.status ||
         (a.rows > 0 && (!a.parents || !a.tokens || !a.posterior)))
-        return fail("tree_accept: NULL argument");
+        return refuse("tree_accept: NULL argument");
     return queue(cuda_stream, "tree_accept: launch failed",
                  [&](const Launch& L) { launch_k(L, tree_accept_kernel, dim3(a.batch), dim3(NT_MASK), 0, 1, a); });
 }
 
 extern "C" dflash_status dflash_kv_compact(const dflash_kv_compact_args* p, void* cuda_stream) {
-    if (!p) return fail("kv_compact: args is NULL");
+    if (!p) return refuse("kv_compact: args is NULL");
     const dflash_kv_compact_args& a = *p;
     if (const char* why = bad_caches(a, "kv_compact: dtype must be F32 or BF16", "kv_compact: layers outside [1, 1024]",
                                      "kv_compact: n_pages, n_kv_heads or head_dim out of range (a head's row is a multiple of 16 bytes)",
                                      "kv_compact: the caches must be 16-byte aligned, ld_layer a multiple of 16 bytes and no smaller than a layer"))
-        return fail(why);
+        return refuse(why);
     // (their tokens would be moved twice)
-    if (a.k_cache == a.v_cache) return fail("kv_compact: v_cache may not be k_cache");
-    if (caches_overlap(a)) return fail("kv_compact: k_cache and v_cache overlap");
-    if (a.batch < 1 || a.batch > DFLASH_OPS_MAX_BATCH) return fail("kv_compact: batch outside [1, 2048]");
-    if (a.width < 1 || a.width > MAXN) return fail("kv_compact: width outside [1, 1024]");
+    if (a.k_cache == a.v_cache) return refuse("kv_compact: v_cache may not be k_cache");
+    if (caches_overlap(a)) return refuse("kv_compact: k_cache and v_cache overlap");
+    if (a.batch < 1 || a.batch > DFLASH_OPS_MAX_BATCH) return refuse("kv_compact: batch outside [1, 2048]");
+    if (a.width < 1 || a.width > MAXN) return refuse("kv_compact: width outside [1, 1024]");
     if (a.width_table < 0 || a.width_table > (1 << 22) || a.ld_table < a.width_table)
-        return fail("kv_compact: width_table outside [0, 2^22], or ld_table smaller");
+        return refuse("kv_compact: width_table outside [0, 2^22], or ld_table smaller");
     if (!a.kv_lens || !a.q_start || !a.path || !a.accepted || !a.kv_out || !a.status || (a.width_table > 0 && !a.table))
-        return fail("kv_compact: NULL argument");
-    if (a.kv_out == a.kv_lens) return fail("kv_compact: kv_out may not be kv_lens");
+        return refuse("kv_compact: NULL argument");
+    if (a.kv_out == a.kv_lens) return refuse("kv_compact: kv_out may not be kv_lens");
     const int vecs = a.head_dim * (a.dtype == DFLASH_DTYPE_BF16 ? 2 : 4) / 16;
     return queue(cuda_stream, "kv_compact: launch failed", [&](const Launch& L) {
         launch_k(L, kv_compact_kernel, dim3(a.batch, 2 * a.layers), dim3(NT_MOVE), 0, 1, a, vecs);
