@@ -36,11 +36,13 @@
 //
 // What bounds it.  Tensor cores: 64 keys of both streams are 1260 cycles (S is fed
 // from shared memory at 48 cycles an M128 N64 K16 product, P V takes 64).  Measured
-// on line 0: 1780 cycles, 1200 TFLOP/s (32 x 16 rows of 32 heads against 32768 keys:
-// 228 us with the merge).  That is the chain of a softmax warp, which has one tile at
-// a time: wait 190 cycles, scores out of TMEM 310, maximum 270, exponentials 660 (two
-// warps share a scheduler's unit), P into TMEM 185, hand-over 140, loop.  Measured and
-// not kept: two warps per 32 rows, half of the keys each (279 us where this took 241);
+// on line 0: 1750 to 1780 cycles, 1200 TFLOP/s (32 x 16 rows of 32 heads against 32768
+// keys: 229 us with the merge).  That is the chain of a softmax warp, which has one tile
+// at a time; by clocks read between the dependent steps of one warp a stream: wait for the
+// scores 370 cycles, scores out of TMEM 140, maximum and rescue test 315, exponentials with
+// the sum and the rounding 630 (two warps share a scheduler), P into TMEM 65, hand-over 70,
+// loop 160; with PAIR 710, 170, 310, 855, 75, 80, 160 (2350).  Trees differ by the wait
+// alone (480, with PAIR 765: 1800 and 2320 a tile).  Measured and not kept: two warps per 32 rows, half of the keys each (279 us where this took 241);
 // the streams' products in turn, half a tile apart (288: one stream's products alone
 // wait for their own accumulator, 69 cycles each); the next scores loaded while P is
 // stored (267); hand-over by a flag in shared memory (243).
@@ -194,8 +196,10 @@ struct Waiter {
 // PAIR: the weights of P V as bf16 pairs.  TREE: rows see the own keys that their masks name; the tiles that hold nodes of
 // the tree take 64 mask bits a row (two to three words from L2, asked for before the scores are waited for) and zero the rows
 // of V that no row of the item sees.  Measured (graph replay): 230 us for 32 trees of 33 .. 64 nodes behind 8192 shared keys and
-// 256 .. 2048 own (1030 TFLOP/s over the call, merge 22 us: the chain above); 10.5 us for 16 nodes behind 512 keys.  Measured and
-// not kept: sixteen softmax warps, two a vector that take its tiles in turn and pass m and l on (264 us, 12.3 for the 16 nodes: each
+// 256 .. 2048 own (1030 TFLOP/s over the call, merge 22 us: the chain above); 10.6 us for 16 nodes behind 512 keys.  With PAIR 297
+// and 11.2 us.  One bf16 a weight is what a call gets that does not ask for pairs, as in the causal form, whose bits a chain's
+// tree has: its output is 2.1e-3 .. 2.4e-3 (rms, relative) from 64 bits, with pairs 1.7e-3, which the output's own rounding
+// makes.  Measured and not kept: sixteen softmax warps, two a vector that take its tiles in turn and pass m and l on (264 us, 12.3 for the 16 nodes: each
 // has a score buffer of its own, whose next scores come behind its own product, so its loop is chain and products in a row).
 template <int HD, bool PAIR, bool TREE>
 __global__ void __launch_bounds__(NTHR, 1)

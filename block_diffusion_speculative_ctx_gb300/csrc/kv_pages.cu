@@ -9,7 +9,7 @@
 // 36 layers, with their release, 80 us instead of 69).  Bytes: the parents' last tokens once (their other
 // children find them in L2) and each child's copy; nothing for the shared pages.
 // Measured (graph replay): 4.9 us for four children over 5 layers; with the release
-// 69 us for 64 children of 8 parents over 36 layers (340 MB: 50 us at a measured copy's rate).
+// 71 us for 64 children of 8 parents over 36 layers (340 MB: 50 us at a measured copy's rate).
 //
 // Release: one launch of one cluster, whose barriers separate the steps.
 //   1  every page named is looked at (range, count);

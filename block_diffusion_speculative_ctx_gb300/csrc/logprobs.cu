@@ -22,8 +22,8 @@
 // memory of its first one: no workspace, no second launch.
 // Bound by the issue of instructions: 19 a logit with a rank and alternatives, 11 for
 // the sums alone.  Measured (calls in a row): 512 fp32 rows of 151936, one token, 5
-// alternatives 59.7 us (77 % of a measured copy's rate; 50.5 us without rank and
-// alternatives); one row with 20 alternatives 8.0 us; 64 bf16 rows of 128256 with 8
+// alternatives 60.7 us (76 % of a measured copy's rate; 50.5 us without rank and
+// alternatives); one row with 20 alternatives 7.9 us; 64 bf16 rows of 128256 with 8
 // tokens and 8 alternatives 19.1 us (the chain of a CTA's four tiles, bootstrap, list, cluster and
 // join).  Measured and not kept: ranks counted in integers (comparisons and integer adds share a pipe of half
 // rate: 512 rows with eight tokens 149 us); a barrier and a count of candidates a tile (118 us
@@ -691,9 +691,22 @@ void forward(const Launch& L, const dflash_logprobs_args& a, int parts) {
     if (top) launch_k(L, logprobs_kernel<T, true, NT>, dim3(a.rows, 1, parts), dim3(NT), LIST_BYTES, parts, a, parts);
     else launch_k(L, logprobs_kernel<T, false, NT>, dim3(a.rows, 1, parts), dim3(NT), 0, parts, a, parts);
 }
-// A row goes to so many CTAs that there are four an SM, if its tiles last (512 rows of 151936 in one, two and four parts: 66, 63
-// and 75 us; 64 bf16 rows of 128256 in two, four and eight: 25, 19 and 19), and to wider ones where every CTA has an SM
-// of its own (one row: 9.6 us, with 256 threads 11.7).
+// A row goes to so many CTAs that there are four an SM, if its tiles last, and to wider ones where every CTA has an SM of its own
+// (one row with 20 alternatives: 7.8 us, with 256 threads 9.7; without any 5.1 and 5.2).  Measured (graph replay, us; * the rule's),
+// one token and five alternatives of fp32 rows of 151936 but where said, in
+//                       one    two    four   eight parts
+//   one row, 20         30     19.3   13.8   9.7 (wide: 7.8 *)
+//   32 rows             27.6   17.7   11.7   9.5 *
+//   128 rows            28.6   22.1   21.0   25.4 *
+//   256 rows            37.6   34.4   40.2 * 46.8
+//   304 rows            39.7   36.1 * 47.1   54.4
+//   512 rows            57.6   60.7 * 70.2   86.0
+//   512, eight tokens   118    109 *  121    138
+//   1024 rows           111 *  114    129
+//   64 bf16 rows of 128256, eight tokens and alternatives
+//                       40.7   24.6   19.0   19.1 *
+// so four an SM suit few rows and several tokens; where rows * parts comes out just below 608 (128, 256 and 512 rows here) half the
+// parts would take 5 to 17 % less for one token.
 template <typename T>
 void forward(const Launch& L, const dflash_logprobs_args& a) {
     const long long tiles = ((long long)a.vocab + 256 * E - 1) / (256 * E);
